@@ -3,8 +3,8 @@ marshalling only. Tensor arguments may be torch tensors (their data_ptr()
 is passed), plain ints (device addresses) or None (NULL)."""
 from __future__ import annotations
 
-__all__ = ["M2Error", "M2Dims", "M2RowNorm", "M2Lm", "M2LmLayer", "BF16", "F32", "NORM_NONE", "NORM_RMS",
-           "NORM_GATED", "library_path", "load", "dims", "row_norm", "lm_model"]
+__all__ = ["M2Error", "M2Dims", "M2RowNorm", "M2Lm", "M2LmLayer", "M2KvCache", "M2Rope", "BF16", "F32", "NORM_NONE",
+           "NORM_RMS", "NORM_GATED", "library_path", "load", "dims", "row_norm", "lm_model", "kv_cache", "rope"]
 
 import ctypes
 import os
@@ -86,6 +86,40 @@ def lm_model(kinds: str, layers, hidden, mixer: M2Dims, n_heads=0, n_kv_heads=0,
     return m
 
 
+class M2KvCache(ctypes.Structure):
+    _fields_ = [(n, ctypes.c_int) for n in ("n_sessions", "n_kv_heads", "head_dim", "page_size", "n_pages", "max_pages",
+                                            "act")] + \
+               [(n, ctypes.c_void_p) for n in ("page_table", "k_pages", "v_pages", "k_scales", "v_scales", "k_tail",
+                                               "v_tail", "k_tail_out", "v_tail_out")]
+
+
+class M2Rope(ctypes.Structure):
+    _fields_ = [("rot_dim", ctypes.c_int), ("interleaved", ctypes.c_int), ("n_pos", ctypes.c_int),
+                ("cos", ctypes.c_void_p), ("sin", ctypes.c_void_p)]
+
+
+def kv_cache(n_sessions, n_kv_heads, page_size, n_pages, max_pages, page_table, k_pages, v_pages, k_scales, v_scales,
+             k_tail=None, v_tail=None, k_tail_out=None, v_tail_out=None, act="bf16", head_dim=128) -> M2KvCache:
+    """The m2_kv_cache description of a paged 8-bit cache. Tails out that are
+    not given are the tails (updated in place). The structure keeps the
+    tensors behind its addresses alive."""
+    kto = k_tail if k_tail_out is None else k_tail_out
+    vto = v_tail if v_tail_out is None else v_tail_out
+    tensors = (page_table, k_pages, v_pages, k_scales, v_scales, k_tail, v_tail, kto, vto)
+    c = M2KvCache(int(n_sessions), int(n_kv_heads), int(head_dim), int(page_size), int(n_pages), int(max_pages),
+                  _act_code(act), *[_p(t) for t in tensors])
+    c._keep = tensors
+    return c
+
+
+def rope(rot_dim, n_pos, cos, sin, interleaved=False) -> M2Rope:
+    """The m2_rope rotation by cos and sin tables [n_pos, rot_dim / 2] fp32; it
+    keeps them alive."""
+    r = M2Rope(int(rot_dim), int(bool(interleaved)), int(n_pos), _p(cos), _p(sin))
+    r._keep = (cos, sin)
+    return r
+
+
 def library_path() -> str:
     return _LIB_PATH
 
@@ -142,6 +176,13 @@ def load():
         lib.mamba2_lm_step.restype = ip
         lib.mamba2_lm_prefill.argtypes = [mp, ip, ip, vp, vp, ip, vp, sz, vp]
         lib.mamba2_lm_prefill.restype = ip
+        cp = ctypes.POINTER(M2KvCache)
+        lib.mamba2_kv_append.argtypes = [cp, ip] + [vp] * 4 + [lp, ctypes.POINTER(M2Rope), ip, vp, lp, vp, lp, vp]
+        lib.mamba2_kv_append.restype = ip
+        lib.mamba2_attn_paged.argtypes = [cp] + [ip] * 3 + [vp] * 3 + [lp, ctypes.c_float, vp, lp, vp, sz, vp]
+        lib.mamba2_attn_paged.restype = ip
+        lib.mamba2_attn_paged_workspace_bytes.argtypes = [cp, ip, ip]
+        lib.mamba2_attn_paged_workspace_bytes.restype = sz
         lib.mamba2_status_string.argtypes = [ip]
         lib.mamba2_status_string.restype = ctypes.c_char_p
         lib.mamba2_last_cuda_error.argtypes = []
@@ -403,5 +444,36 @@ def mamba2_lm_prefill(m: M2Lm, n_sessions, T, hidden, lengths, chunk, workspace,
     if check and rc:
         raise M2Error(rc, "mamba2_lm_prefill")
     return rc
+
+
+def mamba2_kv_append(c: M2KvCache, T, lengths, n_new, k, v, kv_stride, rope=None, n_heads=0, q=None, q_stride=0,
+                     q_out=None, q_out_stride=0, stream=None, check=True) -> int:
+    """Appends up to T positions a session to a paged 8-bit cache, rotating the
+    keys (and q into q_out) by position (see mamba2_kv_append in
+    include/mamba2.h)."""
+    rc = load().mamba2_kv_append(
+        ctypes.byref(c), int(T), _p(lengths), _p(n_new), _p(k), _p(v), int(kv_stride),
+        None if rope is None else ctypes.byref(rope), int(n_heads), _p(q), int(q_stride), _p(q_out), int(q_out_stride),
+        _stream(stream))
+    if check and rc:
+        raise M2Error(rc, "mamba2_kv_append")
+    return rc
+
+
+def mamba2_attn_paged_workspace_bytes(c: M2KvCache, T, n_heads) -> int:
+    return load().mamba2_attn_paged_workspace_bytes(ctypes.byref(c), int(T), int(n_heads))
+
+
+def mamba2_attn_paged(c: M2KvCache, T, n_heads, causal, lengths, n_new, q, q_stride, scale, out, out_stride, workspace,
+                      workspace_bytes=None, stream=None, check=True) -> int:
+    """Attention of up to T positions a session over a paged 8-bit cache (see
+    mamba2_attn_paged in include/mamba2.h)."""
+    rc = load().mamba2_attn_paged(
+        ctypes.byref(c), int(T), int(n_heads), int(bool(causal)), _p(lengths), _p(n_new), _p(q), int(q_stride),
+        float(scale), _p(out), int(out_stride), _p(workspace), _ws_bytes(workspace, workspace_bytes), _stream(stream))
+    if check and rc:
+        raise M2Error(rc, "mamba2_attn_paged")
+    return rc
+
 
 __all__ += [n for n in list(globals()) if n.startswith("mamba2_")]

@@ -174,7 +174,8 @@ enum : unsigned int {
     ERR_MBAR_TIMEOUT_LOAD = 0x101,
     ERR_MBAR_TIMEOUT_MMA = 0x102,
     ERR_TMEM_ALLOC = 0x103,
-    ERR_ATTN_LENGTH = 0x104,  // a cached length outside [0, max_len)
+    ERR_ATTN_LENGTH = 0x104,  // a cached length outside [0, max_len), or positions past a page table's reach
+    ERR_KV_PAGE = 0x105,      // a page number outside the pool
 };
 
 }  // namespace m2

@@ -1,0 +1,237 @@
+// Appending new keys and values to a paged cache held in e4m3, with the
+// position rotation of keys (and queries) applied on the way.
+//
+// A block of 16 positions of one kv head shares one fp32 scale:
+//     m = max(max |block|, 2^-100), scale = m / 448, code = e4m3(x * (448 / m)),
+// e4m3 by rounding to nearest even, the one rounding that a cached value
+// gets. The positions of the block that is still open are kept in fp32 (the
+// tail, rows [0, length mod 16)), so a block is always quantised from its
+// exact values by its own maximum, and the cache does not depend on how the
+// positions were split over calls: a prefill and single frames leave the same
+// bits. The rotation of dims (a, b) of a pair at position t by the table's
+// cos and sin, each product and sum rounded to fp32 by itself (no fused
+// multiply-add, so that the codes are those of the formula as written):
+//     a' = a cos_t - b sin_t,  b' = a sin_t + b cos_t.
+//
+// Memory-bound: per new position and kv head 2 x 128 activations in and
+// 2 x 128 bytes of codes out; per query head 128 activations in and out. The
+// open block costs up to 15 fp32 rows in and out a call, which is what a
+// single frame mostly moves.
+//
+// One CTA per (block, kv head, session): thread = (row, 8 dims) of the keys
+// and of the values, so that every global access is 8 or 16 bytes wide and
+// the pair (d, d + rot / 2) of the half layout sits in another lane of the
+// same half-warp. The maximum goes through shuffles and shared memory. The
+// queries' rows go to CTAs of their own, 16 rows of 128 dims at a time.
+#include <cuda_fp8.h>
+
+#include "m2_common.cuh"
+#include "m2_paged.h"
+
+namespace m2 {
+
+namespace {
+
+constexpr int kApThreads = 256;  // 16 rows x 16 pieces of 8 dims
+constexpr int kPieces = kKvD / 8;
+
+template <typename TA>
+__device__ __forceinline__ void load8(const void* base, size_t elem, float (&f)[8]) {
+    Act8<TA> x;
+    x.load_rw(base, elem);  // a plain load: q may be rotated in place
+#pragma unroll
+    for (int j = 0; j < 8; ++j) f[j] = x.get(j);
+}
+
+__device__ __forceinline__ void load8_f32(const float* p, float (&f)[8]) {
+    const float4 a = *reinterpret_cast<const float4*>(p), b = *reinterpret_cast<const float4*>(p + 4);
+    f[0] = a.x; f[1] = a.y; f[2] = a.z; f[3] = a.w;
+    f[4] = b.x; f[5] = b.y; f[6] = b.z; f[7] = b.w;
+}
+
+__device__ __forceinline__ void store8_f32(float* p, const float (&f)[8]) {
+    *reinterpret_cast<float4*>(p) = make_float4(f[0], f[1], f[2], f[3]);
+    *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
+}
+
+// Dims [8 piece, 8 piece + 8) of a row at position pos, rotated in place.
+// Every lane of the warp calls it (the half layout exchanges dims between
+// lanes); `turn` false leaves the lane's values.
+__device__ __forceinline__ void rotate8(const KvAppendArgs& a, int piece, int lane, int pos, bool turn, float (&f)[8]) {
+    if (a.rot == 0) return;
+    const int half = a.rot >> 1;
+    if (a.interleaved) {
+        if (!turn || 8 * piece >= a.rot) return;
+        const float4 c = __ldg(reinterpret_cast<const float4*>(a.cos + (size_t)pos * half + 4 * piece));
+        const float4 s = __ldg(reinterpret_cast<const float4*>(a.sin + (size_t)pos * half + 4 * piece));
+        const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
+#pragma unroll
+        for (int j = 0; j < 4; ++j) {
+            const float x = f[2 * j], y = f[2 * j + 1];
+            f[2 * j] = __fsub_rn(__fmul_rn(x, cv[j]), __fmul_rn(y, sv[j]));
+            f[2 * j + 1] = __fadd_rn(__fmul_rn(x, sv[j]), __fmul_rn(y, cv[j]));
+        }
+        return;
+    }
+    const int hp = half >> 3;  // pieces of one half
+    const bool first = piece < hp, in = piece < 2 * hp;
+    const int mate = !in ? lane : first ? lane + hp : lane - hp;
+    float g[8];
+#pragma unroll
+    for (int j = 0; j < 8; ++j) g[j] = __shfl_sync(0xffffffffu, f[j], mate);
+    if (!turn || !in) return;
+    const size_t at = (size_t)pos * half + 8 * (first ? piece : piece - hp);
+    float c[8], s[8];
+    load8_f32(a.cos + at, c);
+    load8_f32(a.sin + at, s);
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        const float u = __fmul_rn(f[j], c[j]), w = __fmul_rn(g[j], s[j]);
+        f[j] = first ? __fsub_rn(u, w) : __fadd_rn(w, u);
+    }
+}
+
+__device__ __forceinline__ uint2 pack_e4m3(const float (&f)[8], float inv) {
+    uint32_t h[4];
+#pragma unroll
+    for (int j = 0; j < 4; ++j)
+        h[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(f[2 * j], inv), __fmul_rn(f[2 * j + 1], inv)), __NV_SATFINITE,
+                                        __NV_E4M3);
+    return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
+}
+
+// grid (blocks of a session x kv heads + CTAs of its queries, sessions)
+template <typename TA>
+__global__ void __launch_bounds__(kApThreads) kv_append_kernel(KvAppendArgs a, int blocks) {
+    __shared__ uint32_t smax[2][kApThreads / 32];
+    const KvCache& c = a.c;
+    const int s = blockIdx.y;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int row = tid / kPieces, piece = tid % kPieces;
+
+    pdl_wait();  // the rows and the cache may come from the previous kernel
+    pdl_trigger();
+    int L, n;
+    const long limit = a.rot ? min(c.capacity(), (long)a.n_pos) : c.capacity();
+    if (!kv_extent(c, s, a.T, a.lens, a.n_new, limit, &L, &n)) {  // the whole session is refused
+        if (blockIdx.x == 0 && tid == 0) atomicOr(c.err, ERR_ATTN_LENGTH);
+        return;
+    }
+    if ((int)blockIdx.x >= blocks * c.Hkv) {
+        // the queries: 16 (position, head) rows
+        const int r = ((int)blockIdx.x - blocks * c.Hkv) * (kApThreads / kPieces) + row;
+        const int t = r / a.Hq, h = r % a.Hq;
+        const bool live = t < n;
+        float f[8] = {};
+        if (live) load8<TA>(a.q, ((size_t)s * a.T + t) * a.q_stride + (size_t)h * kKvD + 8 * piece, f);
+        rotate8(a, piece, lane, L + t, live, f);
+        if (live) {
+            const size_t o = ((size_t)s * a.T + t) * a.qo_stride + (size_t)h * kKvD + 8 * piece;
+            if constexpr (sizeof(TA) == 2) {
+                uint32_t w[4];
+#pragma unroll
+                for (int j = 0; j < 4; ++j)
+                    w[j] = (uint32_t)float_to_bf16_bits(f[2 * j]) | ((uint32_t)float_to_bf16_bits(f[2 * j + 1]) << 16);
+                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.q_out) + o) = make_uint4(w[0], w[1], w[2], w[3]);
+            } else {
+                store8_f32(reinterpret_cast<float*>(a.q_out) + o, f);
+            }
+        }
+        return;
+    }
+    const int b = (int)blockIdx.x / c.Hkv, g = (int)blockIdx.x % c.Hkv;
+    const int end = L + n;
+    const int base = (L & ~(kKvBlock - 1)) + b * kKvBlock;
+    const size_t tail = (((size_t)s * c.Hkv + g) * kKvBlock + row) * kKvD + 8 * piece;
+    if (base >= end && b > 0) return;
+
+    // position `pos` of the session, one of the new ones, in fp32 and rotated
+    auto fresh = [&](int pos, bool live, float (&k)[8], float (&v)[8]) {
+        if (live) {
+            const size_t e = ((size_t)s * a.T + (pos - L)) * a.kv_stride + (size_t)g * kKvD + 8 * piece;
+            load8<TA>(a.k, e, k);
+            load8<TA>(a.v, e, v);
+        }
+        rotate8(a, piece, lane, pos, live, k);
+    };
+    const int pos = base + row;
+    const bool old = pos < L, live = pos < end;
+    float k[8] = {}, v[8] = {};
+    if (old) {
+        load8_f32(c.kt + tail, k);
+        load8_f32(c.vt + tail, v);
+    }
+    {
+        float kn[8] = {}, vn[8] = {};
+        fresh(pos, live && !old, kn, vn);
+        if (live && !old) {
+#pragma unroll
+            for (int j = 0; j < 8; ++j) {
+                k[j] = kn[j];
+                v[j] = vn[j];
+            }
+        }
+    }
+    // the block's maxima, as the bits of |x|: their order is that of the
+    // numbers, and a NaN is above them all
+    uint32_t mk = 0, mv = 0;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        mk = max(mk, __float_as_uint(k[j]) & 0x7FFFFFFFu);
+        mv = max(mv, __float_as_uint(v[j]) & 0x7FFFFFFFu);
+    }
+    mk = __reduce_max_sync(0xffffffffu, mk);
+    mv = __reduce_max_sync(0xffffffffu, mv);
+    if (lane == 0) {
+        smax[0][warp] = mk;
+        smax[1][warp] = mv;
+    }
+    __syncthreads();  // ... and every row of the tail has been read
+#pragma unroll
+    for (int w = 0; w < kApThreads / 32; ++w) {
+        mk = max(mk, smax[0][w]);
+        mv = max(mv, smax[1][w]);
+    }
+    mk = max(mk, __float_as_uint(kKvTiny));
+    mv = max(mv, __float_as_uint(kKvTiny));
+    if (n > 0) {
+        const int page = c.table[(size_t)s * c.max_pages + (base >> c.ps_shift)];
+        if (page < 0 || page >= c.n_pages) {
+            if (tid == 0) atomicOr(c.err, ERR_KV_PAGE);
+        } else {
+            const size_t at = ((size_t)page * c.Hkv + g) * c.ps + (base & (c.ps - 1));  // row of the block's first position
+            if (live) {
+                const size_t o = (at + row) * kKvD + 8 * piece;
+                *reinterpret_cast<uint2*>(c.kp + o) = pack_e4m3(k, __fdiv_rn(kE4m3Max, __uint_as_float(mk)));
+                *reinterpret_cast<uint2*>(c.vp + o) = pack_e4m3(v, __fdiv_rn(kE4m3Max, __uint_as_float(mv)));
+            }
+            if (tid == 0) {
+                c.ks[at / kKvBlock] = __fdiv_rn(__uint_as_float(mk), kE4m3Max);
+                c.vs[at / kKvBlock] = __fdiv_rn(__uint_as_float(mv), kE4m3Max);
+            }
+        }
+    }
+    // the tail of the block that is open afterwards, written by the CTA that
+    // reads the one open before (in place, nobody else may overwrite it)
+    if (b == 0) {
+        const int last = end & ~(kKvBlock - 1);
+        const bool stays = row < (end & (kKvBlock - 1));
+        if (last != base) fresh(last + row, stays, k, v);
+        if (stays) {
+            store8_f32(c.kto + tail, k);
+            store8_f32(c.vto + tail, v);
+        }
+    }
+}
+
+}  // namespace
+
+cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t st) {
+    const long blocks = ((long)kKvBlock - 1 + a.T + kKvBlock - 1) / kKvBlock;  // the most a session touches
+    const long qctas = ((long)a.T * a.Hq + kApThreads / kPieces - 1) / (kApThreads / kPieces);
+    const dim3 grid((unsigned)(blocks * a.c.Hkv + qctas), (unsigned)a.c.S);
+    return a.bf16 ? launch_pdl(kv_append_kernel<bf16_t>, grid, dim3(kApThreads), 0, st, a, (int)blocks)
+                  : launch_pdl(kv_append_kernel<float>, grid, dim3(kApThreads), 0, st, a, (int)blocks);
+}
+
+}  // namespace m2

@@ -20,8 +20,9 @@
  *   mamba2_conv_scan — whole history / prefill, chunked (SSD) evaluation;
  *   mamba2_step      — one frame for a batch of sessions from cached state.
  * Around it: the gated output norm and the 4-bit projections of the Mamba
- * layer, and the cached decode of the model's attention layers
- * (mamba2_gated_norm, mamba2_qlinear, mamba2_attn_decode).
+ * layer, the cached decode of the model's attention layers
+ * (mamba2_gated_norm, mamba2_qlinear, mamba2_attn_decode), and a paged 8-bit
+ * cache for them (mamba2_kv_append, mamba2_attn_paged).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -482,6 +483,140 @@ m2_status mamba2_lm_step(const m2_lm* m, int n_sessions, void* hidden, const int
  * position; the caller advances lengths by T. Errors as mamba2_lm_step. */
 m2_status mamba2_lm_prefill(const m2_lm* m, int n_sessions, int T, void* hidden, const int32_t* lengths, int chunk,
                             void* workspace, size_t workspace_bytes, void* stream);
+
+/* ------------------------------------------------------------------------
+ * A paged key/value cache held in 8 bits, for many sessions of different ages
+ * (the attention KV caches of "docs/nemotron-voicechat.md", section Online
+ * session, at half the bytes a position and with memory that follows each
+ * session's real length). It stands beside mamba2_attn_decode, whose caches
+ * are dense and in the activation dtype.
+ *
+ * Position p of session s lies in page page_table[s][p / page_size], slot
+ * p % page_size. Keys and values are e4m3 with one fp32 scale for each block
+ * of 16 positions (slots 16 i .. 16 i + 15 of a page) and kv head:
+ *     m = max(max |block|, 2^-100), scale = m / 448,
+ *     code = e4m3(x * (448 / m))    to nearest even,  value = scale * code
+ * The positions of the block that is still open are kept in fp32 as well
+ * (the tail: rows [0, length % 16)), so that a block is always quantised from
+ * its exact values: the cache holds the same bits however the positions were
+ * split over calls. A value gets one rounding, to e4m3 (at most 2^-4 of
+ * itself, or 2^-10 of the scale where the code is subnormal).
+ *
+ * k_pages, v_pages [n_pages, n_kv_heads, page_size, head_dim] bytes; k_scales,
+ * v_scales [n_pages, n_kv_heads, page_size / 16] fp32; tails
+ * [n_sessions, n_kv_heads, 16, head_dim] fp32; page_table
+ * [n_sessions, max_pages] int32 (entries past a session's positions are not
+ * read). The tails are used by mamba2_kv_append only; k_tail_out and
+ * v_tail_out may be k_tail and v_tail (the tail updated in place), otherwise
+ * they must not overlap them. `act` is the dtype of the rows that go in and
+ * out (keys, values, queries, outputs).
+ * Sizes: head_dim 128; page_size 16, 32, 64 or 128; max_pages * page_size at
+ *   most 2^30; n_pages * n_kv_heads * page_size below 2^31; n_sessions and
+ *   n_kv_heads at most 65535.
+ * Sharing: sessions may list the same page (a common prefix) as long as no
+ *   call appends to it; a page that positions are appended to belongs to one
+ *   session and is listed once. A length may be set back to a multiple of 16,
+ *   or within the open block; elsewhere the tail holds another block.
+ * A table entry outside [0, n_pages) among those a call needs is seen only on
+ *   the device: the error word reads 0x105 (mamba2_device_error) and nothing
+ *   outside the pool is touched. */
+typedef struct {
+    int n_sessions;   /* S */
+    int n_kv_heads;
+    int head_dim;     /* 128 */
+    int page_size;    /* positions a page */
+    int n_pages;      /* pages in the pool */
+    int max_pages;    /* columns of the page table */
+    m2_dtype act;
+    const int32_t* page_table;
+    uint8_t *k_pages, *v_pages;
+    float *k_scales, *v_scales;
+    const float *k_tail, *v_tail;
+    float *k_tail_out, *v_tail_out;
+} m2_kv_cache;
+
+/* Rotation of the first rot_dim dims of each head by its position p, by
+ * tables cos and sin [n_pos, rot_dim / 2] fp32 (16-byte aligned): for pair i,
+ *     a' = a cos[p][i] - b sin[p][i],  b' = a sin[p][i] + b cos[p][i]
+ * with (a, b) = dims (2 i, 2 i + 1) if interleaved, else (i, rot_dim / 2 + i);
+ * each product and sum rounded to fp32. rot_dim: a multiple of 16, at most
+ * head_dim (0: no rotation). */
+typedef struct {
+    int rot_dim;
+    int interleaved;
+    int n_pos;
+    const float *cos, *sin;
+} m2_rope;
+
+/* Appends up to T new positions to each session: session s with lengths[s]
+ * positions cached gets n_new[s] more (n_new NULL: T for all; values are
+ * clamped to [0, T]), its rows t < n_new[s] of k and v at position
+ * lengths[s] + t, the keys rotated by that position (rope NULL: not). The
+ * caller advances lengths.
+ *
+ * k, v: rows of n_kv_heads * 128 activations, one for each (session,
+ *   position), row s * T + t starting kv_stride * (s * T + t) elements past
+ *   the pointer (so that they may be columns of the q | k | v projection's
+ *   rows); 16-byte aligned, kv_stride times the element size a multiple of 16
+ *   bytes, at least n_kv_heads * 128.
+ * q, q_out (both NULL: none): the new positions' queries, rows of
+ *   n_heads * 128 activations at q_stride and q_out_stride as above, rotated
+ *   like the keys and rounded once; q_out may be q (with the same stride).
+ *   Rows t >= n_new[s] of q_out are left as they were.
+ * lengths, n_new: int32 [S] in device memory, 4-byte aligned.
+ * Written: the codes of the new positions, and of the older ones of the block
+ *   that was open (its scale may grow); the scales of the blocks touched; the
+ *   open rows [0, (lengths[s] + n_new[s]) % 16) of the tails out. Slots past
+ *   the new positions are left as they were. With n_new[s] = 0 only the open
+ *   rows of the tails are copied.
+ * A block that holds an infinity or a NaN gets a scale that is one, and its
+ *   values read as NaN; other blocks are not affected.
+ * Errors: M2_EINVAL, M2_ESHAPE (sizes as m2_kv_cache and m2_rope state;
+ *   n_heads not a multiple of n_kv_heads), M2_EALIGN, M2_EUNSUPPORTED,
+ *   M2_ECUDA. Seen only on the device, in the error word: 0x104, a negative
+ *   length or positions past max_pages * page_size (or, with a rotation,
+ *   n_pos): that session is left as it was; 0x105, a page number outside the
+ *   pool: that block is not written. n_sessions == 0 is a no-op once the
+ *   arguments check out. Asynchronous on `stream`. */
+m2_status mamba2_kv_append(const m2_kv_cache* c, int T, const int32_t* lengths, const int32_t* n_new, const void* k,
+                           const void* v, long kv_stride, const m2_rope* rope, int n_heads, const void* q, long q_stride,
+                           void* q_out, long q_out_stride, void* stream);
+
+/* Grouped-query attention over the paged cache, for single frames, for many
+ * positions at once (a prefill, sessions catching up) and across to another
+ * sequence's states. Query head h reads kv head g = h / (n_heads / n_kv_heads).
+ * For t < n_new[s] (NULL: T; clamped to [0, T]):
+ *     a_p = scale * q[s][t][h] . k[p],  out[s][t][h] = sum_p softmax(a)_p v[p]
+ * over the positions
+ *   causal != 0: p <= lengths[s] + t. lengths[s] counts the positions before
+ *     this call's, as for mamba2_kv_append, whose lengths and n_new it takes;
+ *     the new positions must have been appended;
+ *   causal == 0: p < lengths[s], for every t (cross attention to an encoder's
+ *     states that another cache holds). With lengths[s] = 0 the outputs are
+ *     zeros.
+ * Rows t >= n_new[s] of out are left as they were.
+ *
+ * q, out: rows of n_heads * 128 activations, row s * T + t starting q_stride
+ *   (out_stride) * (s * T + t) elements past the pointer; 16-byte aligned,
+ *   strides times the element size a multiple of 16 bytes, at least
+ *   n_heads * 128. out must not overlap q.
+ * Scores, softmax and sums in fp32, out rounded once.
+ * Scratch: workspace of at least mamba2_attn_paged_workspace_bytes(...) (NULL
+ *   where that is 0), which calls that may overlap on the GPU must not share.
+ * Errors: M2_EINVAL (also a scale that is not finite), M2_ESHAPE, M2_EALIGN,
+ *   M2_EWORKSPACE, M2_EUNSUPPORTED, M2_ECUDA. Seen only on the device, in the
+ *   error word: 0x104, a negative length or positions past max_pages *
+ *   page_size: that session's rows of out are zeros; 0x105, a page number
+ *   outside the pool: what the rows that would read it hold is undefined.
+ *   n_sessions == 0 or T == 0 is a no-op once the arguments check out.
+ *   Asynchronous on `stream`. */
+m2_status mamba2_attn_paged(const m2_kv_cache* c, int T, int n_heads, int causal, const int32_t* lengths,
+                            const int32_t* n_new, const void* q, long q_stride, float scale, void* out, long out_stride,
+                            void* workspace, size_t workspace_bytes, void* stream);
+
+/* Bytes of device scratch that mamba2_attn_paged needs (0: none, or the sizes
+ * are invalid). Only the sizes in `c` are read. */
+size_t mamba2_attn_paged_workspace_bytes(const m2_kv_cache* c, int T, int n_heads);
 
 /* Static description of a status code. */
 const char* mamba2_status_string(m2_status s);
