@@ -6,107 +6,582 @@
 // (cross attention: a cache of other states, the same for every query). ks
 // and vs are the scales of the position's block of 16.
 //
-// One warp per (session, query, head), 32 positions at a time: each lane a
-// position's score, then each lane 4 dims of the weighted values, with the
-// running maximum and sum of an online softmax; fp32 throughout.
-#include <cuda_fp8.h>
+// attn_paged_rows_kernel: few rows (single frames). A kv head's rows are its
+// (query, head) pairs, row = t R + r, taken 8 or 16 at a time. Bound by HBM:
+// every cached key and value is read once for 8 or 16 rows, 256 bytes and
+// 32 scale-bits a position and kv head. One CTA ("walker") takes a run of
+// 64-position chunks of one (session, kv head, row group): a producer warp
+// keeps a ring of TMA copies in flight (a page, or the part of one that lies
+// in the chunk, is one box of 128-byte rows; the scales come by 4-byte
+// asynchronous copies on the same barrier), and each of four warps takes 16
+// positions of every chunk, which is one block of the cache, so that both
+// scales are constants of the warp. The walkers of one (session, kv head, row
+// group) form a thread-block cluster and merge through distributed shared
+// memory, so that one launch does it all.
+//
+// Codes become fp16 exactly (cvt from e4m3), so the products run on fp16
+// matrix instructions with fp32 sums:
+//   q      scaled by a power of two for each row (its largest element to
+//          [2^14, 2^15)): a bf16 row is exact, an fp32 row goes in as two
+//          terms, hi + lo, 22 bits;
+//   weight p = 2^(x - m) goes in times its value's scale, relative to the
+//          running maximum of that product: w = p vs 2^(m - mv + 15), at most
+//          2^15, one fp16 term (2^-11) for bf16 activations, two for fp32.
+//          Blocks whose values are of very different size thus lose nothing
+//          to fp16's range; sums of p (l) stay fp32 and apart.
+//     out = 2^(mv - m - 15) acc / l.
+#include <cuda.h>
+#include <cuda_fp16.h>
+#include <cuda_runtime.h>
+
+#include <mutex>
 
 #include "m2_common.cuh"
 #include "m2_paged.h"
+#include "m2_tc.cuh"
 
 namespace m2 {
 
 namespace {
 
-constexpr int kPaWarps = 4;
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNone = -1e30f;  // a running maximum before any position
 
 __device__ __forceinline__ float ex2_approx(float x) {
     float r;
     asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
     return r;
 }
-
-__device__ __forceinline__ float e4m3_to_float(uint32_t b) {
-    __half_raw h = __nv_cvt_fp8_to_halfraw((__nv_fp8_storage_t)b, __NV_E4M3);
-    return __half2float(__half(h));
+__device__ __forceinline__ float lg2_approx(float x) {
+    float r;
+    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+// two e4m3 codes (the low byte first) as fp16, exactly
+__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
+    return r;
+}
+__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
+    uint32_t r;
+    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
+    return r;
+}
+__device__ __forceinline__ float2 unpack_f16x2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
+__device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+__device__ __forceinline__ void ldsm_x4_trans(uint32_t addr, uint32_t (&r)[4]) {
+    asm volatile("ldmatrix.sync.aligned.m8n8.x4.trans.shared.b16 {%0, %1, %2, %3}, [%4];"
+                 : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
+                 : "r"(addr));
+}
+// d += A B, m16n8k16, fp16 in, fp32 accumulate
+__device__ __forceinline__ void mma_f16(float (&d)[4], uint32_t a0, uint32_t a1, uint32_t a2, uint32_t a3, uint32_t b0,
+                                        uint32_t b1) {
+    asm volatile(
+        "mma.sync.aligned.m16n8k16.row.col.f32.f16.f16.f32 {%0, %1, %2, %3}, {%4, %5, %6, %7}, {%8, %9}, "
+        "{%0, %1, %2, %3};"
+        : "+f"(d[0]), "+f"(d[1]), "+f"(d[2]), "+f"(d[3])
+        : "r"(a0), "r"(a1), "r"(a2), "r"(a3), "r"(b0), "r"(b1));
+}
+// The warp's 8 x 8 matrix of 16-bit elements, transposed, in the same layout.
+__device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
+    uint32_t r;
+    asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
+    return r;
+}
+// 4 bytes global -> shared, completion counted by cp_async_arrive
+__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
+    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
+}
+// One of the barrier's expected arrivals, made when this thread's earlier
+// cp.async copies have landed.
+__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
+    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
 
-template <typename TA>
-__global__ void __launch_bounds__(32 * kPaWarps) attn_paged_simple_kernel(PagedAttnArgs a) {
-    __shared__ float sq[kPaWarps][kKvD];
+// The power of two that takes a row's largest magnitude to [2^14, 2^15) (1
+// for a row of zeros; the exponent is kept below 2^126).
+__device__ __forceinline__ float row_power(float amax) {
+    const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
+    return amax == 0.f ? 1.f : __uint_as_float((uint32_t)(min(14 - ex, 126) + 127) << 23);
+}
+
+constexpr int kRwWarps = 4;                              // warps that compute
+constexpr int kRwThreads = 32 * kRwWarps + 32;           // ... and the producer
+constexpr int kRwTc = 16 * kRwWarps;                     // positions per chunk
+constexpr uint32_t kRwTile = kRwTc * kKvD;               // a chunk's keys (or values)
+constexpr int kRwMaxW = 16;                              // walkers per cluster
+constexpr uint32_t kRwSlotF = kKvD + 4;                  // floats of a merge slot: acc, m, l, mv
+
+// Shared memory of rows groups of 8 NT rows: the ring (keys, then values of
+// each stage), the stages' scales, the slots that an owner receives, barriers.
+template <int NT>
+struct RwSmem {
+    static constexpr int kRows = 8 * NT;
+    static constexpr int kStages = NT == 1 ? 6 : 5;
+    static constexpr int kSlots = kRows + kRwMaxW - 1;  // ceil(rows / W) W, at most
+    static constexpr uint32_t kScales = kStages * 2 * kRwTile;               // float [stage][8]
+    static constexpr uint32_t kRecv = kScales + kStages * 2 * kRwWarps * 4;
+    static constexpr uint32_t kBar = kRecv + kSlots * kRwSlotF * 4;          // full, empty [kStages]
+    static constexpr uint32_t kFlag = kBar + 2 * kStages * 8;
+    static constexpr uint32_t kBytes = kFlag + 16 + 1024;                    // + slack to align to 1024
+    // the warps' merge, over the ring: acc [warp][row][128], then (m, l, mv)
+    static constexpr uint32_t kMl = kRwWarps * kRows * kKvD * 4;
+    static_assert(kMl + kRwWarps * kRows * 4 * 4 <= kScales, "the merge fits in the ring");
+    static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two CTAs an SM");
+};
+
+// grid (W x Hkv x row groups, S), a cluster of W walkers when W > 1.
+// TERMS: fp16 terms of a query and of a weight (2 for fp32 activations).
+template <typename TA, int NT, int TERMS>
+__global__ void __launch_bounds__(kRwThreads, 2)
+    attn_paged_rows_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap tmk,
+                           const __grid_constant__ CUtensorMap tmv, int W) {
+    using L = RwSmem<NT>;
+    constexpr int ST = L::kStages;
+    extern __shared__ uint8_t rw_raw[];
+    uint8_t* sm = rw_raw + ((1024u - (tc::smem_u32(rw_raw) & 1023u)) & 1023u);
+    float* scales = reinterpret_cast<float*>(sm + L::kScales);
+    float* recv = reinterpret_cast<float*>(sm + L::kRecv);
+    uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBar);
+    uint64_t* empty = full + ST;
+    volatile uint32_t* flag = reinterpret_cast<uint32_t*>(sm + L::kFlag);
     const KvCache& c = a.c;
-    const int lane = threadIdx.x & 31, warp = threadIdx.x >> 5, s = blockIdx.y;
-    const long r = (long)blockIdx.x * kPaWarps + warp;
-    const int t = (int)(r / a.Hq), h = (int)(r % a.Hq), g = h / (a.Hq / c.Hkv);
-    pdl_wait();
-    pdl_trigger();
-    int L, n;
-    const bool ok = kv_extent(c, s, a.T, a.lens, a.n_new, c.capacity(), &L, &n);
-    if (!ok) {
-        if (blockIdx.x == 0 && threadIdx.x == 0) atomicOr(c.err, ERR_ATTN_LENGTH);
-        L = 0;
+    const int wk = (int)blockIdx.x % W, pair = (int)blockIdx.x / W, s = blockIdx.y;
+    const int g = pair % c.Hkv, row0 = pair / c.Hkv * L::kRows;
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int R = a.Hq / c.Hkv;
+
+    if (tid == 0) {
+        for (int i = 0; i < ST; ++i) {
+            tc::mbar_init(full + i, 1 + 32);
+            tc::mbar_init(empty + i, kRwWarps);
+        }
+        tc::fence_mbar_init();
+        *flag = 0;
     }
-    if (t >= n) return;
-    const int seen = !ok ? 0 : a.causal ? L + t + 1 : L;
-    const size_t qo = ((size_t)s * a.T + t) * a.q_stride + (size_t)h * kKvD + 4 * lane;
-#pragma unroll
-    for (int j = 0; j < 4; ++j) sq[warp][4 * lane + j] = load_act<TA>(a.q, qo + j);
-    __syncwarp();
-    const float sl2 = a.scale * kLog2e;
-    float m = -INFINITY, l = 0.f, acc[4] = {0.f, 0.f, 0.f, 0.f};
-    bool bad_page = false;
-    for (int p0 = 0; p0 < seen; p0 += 32) {
-        const int p = p0 + lane;
-        float v = -INFINITY, vs = 0.f;
-        size_t at = 0;
-        if (p < seen) {
-            const int page = c.table[(size_t)s * c.max_pages + (p >> c.ps_shift)];
-            if (page < 0 || page >= c.n_pages) {
-                bad_page = true;
-            } else {
-                at = ((size_t)page * c.Hkv + g) * c.ps + (p & (c.ps - 1));
-                float d = 0.f;
-                for (int i = 0; i < kKvD / 16; ++i) {
-                    const uint4 w = *reinterpret_cast<const uint4*>(c.kp + at * kKvD + 16 * i);
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-#pragma unroll
-                    for (int e = 0; e < 16; ++e) d = fmaf(sq[warp][16 * i + e], e4m3_to_float((u[e / 4] >> (8 * (e % 4))) & 0xFFu), d);
+    if (W > 1) tc::cluster_arrive_relaxed();  // waited on before the first remote store: every walker has started
+    pdl_wait();  // the queries and the cache may come from the previous kernel
+    pdl_trigger();
+    int before, n;
+    const bool ok = kv_extent(c, s, a.T, a.lens, a.n_new, a.causal ? c.capacity() : c.capacity() + a.T, &before, &n) &&
+                    before <= c.capacity();
+    if (!ok && blockIdx.x == 0 && tid == 0) atomicOr(c.err, ERR_ATTN_LENGTH);
+    const int rows = min(n * R - row0, (int)L::kRows);
+    if (rows <= 0) return;  // the whole cluster
+    // positions that this group's last row sees, in chunks, and this walker's run of them
+    const int total = !ok ? 0 : a.causal ? before + (row0 + rows - 1) / R + 1 : before;
+    const int nch = (total + kRwTc - 1) / kRwTc, cpw = (nch + W - 1) / W;
+    const int cb = wk * cpw, ce = min(cb + cpw, nch);
+    __syncthreads();  // the barriers are initialised
+
+    if (warp == kRwWarps) {
+        // ---------------------------------------------------------- producer
+        const int* table = c.table + (size_t)s * c.max_pages;
+        const int box = min(c.ps, kRwTc), pieces = kRwTc / box;  // rows a copy, copies a chunk
+        const int last_page = (total - 1) >> c.ps_shift;
+        int held = -32, page_ids = 0;  // this lane's entry of table[held .. held + 31]
+        bool good = true;
+        for (int ch = cb; ch < ce && good; ++ch) {
+            const int st = (ch - cb) % ST;
+            const uint32_t round = (uint32_t)((ch - cb) / ST);
+            if (round > 0 && !tc::mbar_wait(empty + st, (round - 1) & 1)) {
+                if (lane == 0) atomicOr(c.err, ERR_MBAR_TIMEOUT_LOAD);
+                *flag = 1;
+                good = false;
+            }
+            good = __all_sync(0xffffffffu, good);
+            if (!good) break;
+            const int p0 = ch * kRwTc, left = min(kRwTc, total - p0);  // positions to load
+            const int first = p0 >> c.ps_shift;
+            if (first + 4 > held + 32 || held < 0) {  // a chunk lies in at most four pages
+                held = first;
+                page_ids = first + lane <= last_page ? table[first + lane] : 0;
+                if (page_ids < 0 || page_ids >= c.n_pages) {
+                    atomicOr(c.err, ERR_KV_PAGE);
+                    page_ids = 0;  // some page of the pool: what is read is unused or undefined
                 }
-                v = d * (c.ks[at / kKvBlock] * sl2);
-                vs = c.vs[at / kKvBlock];
+                __syncwarp();
+            }
+            uint8_t* dst = sm + st * 2 * kRwTile;
+            const int live = (left + box - 1) / box;
+            if (lane == 0) tc::mbar_arrive_expect_tx(full + st, (uint32_t)(live * box * kKvD * 2));
+            __syncwarp();
+            for (int i = 0; i < pieces; ++i) {
+                const int page = __shfl_sync(0xffffffffu, page_ids, first + i - held);
+                if (i < live && lane == 0) {
+                    const int y = (page * c.Hkv + g) * c.ps + (p0 & (c.ps - 1));  // (0 for pages of at most a chunk)
+                    tc::tma_load_2d(dst + i * box * kKvD, &tmk, 0, y, full + st);
+                    tc::tma_load_2d(dst + kRwTile + i * box * kKvD, &tmv, 0, y, full + st);
+                }
+            }
+            // the chunk's scales: lanes 0 .. 3 the keys' four blocks, 4 .. 7 the values'
+            {
+                const int b = lane & (kRwWarps - 1), p = p0 + b * kKvBlock;
+                const int page = __shfl_sync(0xffffffffu, page_ids, min((p >> c.ps_shift) - held, 31));
+                if (lane < 2 * kRwWarps && p < total) {
+                    const size_t at = (((size_t)page * c.Hkv + g) << (c.ps_shift - 4)) + ((p & (c.ps - 1)) >> 4);
+                    cp_async4(scales + st * 2 * kRwWarps + lane, (lane < kRwWarps ? c.ks : c.vs) + at);
+                }
+                cp_async_arrive(full + st);
             }
         }
-        if (__any_sync(0xffffffffu, bad_page)) {
-            bad_page = true;
-            break;
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    }
+    const int gq = lane >> 2, t = lane & 3;  // fragment row and lane in its quad
+    // per fragment of 8 rows: scores' factor, and the last position seen, of
+    // rows 2t and 2t + 1; running maximum, this lane's part of the sum,
+    // reference of the weights; acc^T: dims 16 u + 2 gq (+ 1) of rows 2t, 2t + 1
+    float m[NT][2], l[NT][2], mv[NT][2], acc[NT][8][4];
+#pragma unroll
+    for (int f = 0; f < NT; ++f) {
+#pragma unroll
+        for (int e = 0; e < 2; ++e) m[f][e] = mv[f][e] = kNone, l[f][e] = 0.f;
+#pragma unroll
+        for (int u = 0; u < 8; ++u)
+#pragma unroll
+            for (int e = 0; e < 4; ++e) acc[f][u][e] = 0.f;
+    }
+    if (warp < kRwWarps) {
+        // Q^T as the B operand (k = dims, n = row gq): the 16 dims of a K-step
+        // are taken in the order of the keys' bytes, lane t its dims 4t .. 4t + 3
+        uint32_t qb[NT][8][TERMS][2];
+        float cs[NT][2];
+        int lim[NT][2];
+#pragma unroll
+        for (int f = 0; f < NT; ++f) {
+            const int row = row0 + min(8 * f + gq, rows - 1);  // (rows past the last read it again)
+            const size_t at = ((size_t)s * a.T + row / R) * a.q_stride + (size_t)(g * R + row % R) * kKvD + 4 * t;
+            float x[8][4], top = 0.f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                if constexpr (sizeof(TA) == 2) {
+                    const uint2 w = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.q) + at + 16 * u));
+                    x[u][0] = __uint_as_float(w.x << 16);
+                    x[u][1] = __uint_as_float(w.x & 0xFFFF0000u);
+                    x[u][2] = __uint_as_float(w.y << 16);
+                    x[u][3] = __uint_as_float(w.y & 0xFFFF0000u);
+                } else {
+                    const float4 w = __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.q) + at + 16 * u));
+                    x[u][0] = w.x, x[u][1] = w.y, x[u][2] = w.z, x[u][3] = w.w;
+                }
+#pragma unroll
+                for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(x[u][e]));
+            }
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
+            top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
+            const float pw = row_power(top), sg = a.scale < 0.f ? -pw : pw;
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const float y0 = x[u][2 * h] * sg, y1 = x[u][2 * h + 1] * sg;
+                    qb[f][u][0][h] = pack_f16x2(y0, y1);
+                    if constexpr (TERMS == 2) {
+                        const float2 hi = unpack_f16x2(qb[f][u][0][h]);
+                        qb[f][u][1][h] = pack_f16x2(y0 - hi.x, y1 - hi.y);
+                    }
+                }
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+                const float p2 = __shfl_sync(0xffffffffu, pw, 4 * (2 * t + e));
+                cs[f][e] = fabsf(a.scale) * kLog2e / p2;
+                const int r = 8 * f + 2 * t + e;
+                lim[f][e] = r >= rows ? -1 : a.causal ? before + (row0 + r) / R : total - 1;
+            }
         }
-        float mx = v;
-        for (int off = 16; off > 0; off >>= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
-        const float mn = fmaxf(m, mx), corr = ex2_approx(m - mn);
-        m = mn;
-        const float pr = ex2_approx(v - mn);
-        l = fmaf(l, corr, pr);
+        bool good = true;
+        for (int ch = cb; ch < ce; ++ch) {
+            const int st = (ch - cb) % ST;
+            if (!tc::mbar_wait(full + st, (uint32_t)((ch - cb) / ST) & 1)) {
+                atomicOr(c.err, ERR_MBAR_TIMEOUT_LOAD);
+                *flag = 1;
+                good = false;
+            }
+            good = __all_sync(0xffffffffu, good);
+            if (!good) break;
+            const int p0 = ch * kRwTc + 16 * warp;  // this warp's block
+            if (p0 < total) {
+                uint8_t* sV = sm + st * 2 * kRwTile + kRwTile + warp * 16 * kKvD;
+                const uint32_t kb = tc::smem_u32(sV - kRwTile), vb = tc::smem_u32(sV);
+                if (p0 + 16 > total) {  // whatever lies behind the last position counts as zero values
+                    for (int e = lane; e < (p0 + 16 - total) * 8; e += 32)
+                        *reinterpret_cast<uint4*>(sV + (total - p0) * kKvD + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    __syncwarp();
+                }
+                const float ks = scales[st * 2 * kRwWarps + warp], vs = scales[st * 2 * kRwWarps + kRwWarps + warp];
+                // S^T (16 positions x 8 rows): lanes 8j .. 8j + 7 address the
+                // 8 x 16-byte piece j: positions + 8 (j & 1), 16-byte unit + (j >> 1)
+                const int fr = (lane & 7) + 8 * ((lane >> 3) & 1), fu = lane >> 4;
+                float sc[NT][4];
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] *= corr;
-        for (int i = 0; i < min(32, seen - p0); ++i) {
-            const float w = __shfl_sync(0xffffffffu, pr * vs, i);
-            const size_t ai = __shfl_sync(0xffffffffu, at, i);
-            const uint32_t u = *reinterpret_cast<const uint32_t*>(c.vp + ai * kKvD + 4 * lane);
+                for (int f = 0; f < NT; ++f)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) acc[j] = fmaf(w, e4m3_to_float((u >> (8 * j)) & 0xFFu), acc[j]);
+                    for (int e = 0; e < 4; ++e) sc[f][e] = 0.f;
+#pragma unroll
+                for (int u = 0; u < 8; u += 2) {
+                    uint32_t w[4];
+                    ldsm_x4(kb + fr * kKvD + (((u + fu) ^ (fr & 7)) << 4), w);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t a0 = e4m3x2_to_f16x2(w[2 * h] & 0xFFFFu), a2 = e4m3x2_to_f16x2(w[2 * h] >> 16);
+                        const uint32_t a1 = e4m3x2_to_f16x2(w[2 * h + 1] & 0xFFFFu), a3 = e4m3x2_to_f16x2(w[2 * h + 1] >> 16);
+#pragma unroll
+                        for (int f = 0; f < NT; ++f)
+#pragma unroll
+                            for (int k = 0; k < TERMS; ++k)
+                                mma_f16(sc[f], a0, a1, a2, a3, qb[f][u + h][k][0], qb[f][u + h][k][1]);
+                    }
+                }
+                const float lvs = lg2_approx(vs);
+                uint32_t pb[NT][TERMS][2];
+#pragma unroll
+                for (int f = 0; f < NT; ++f) {
+                    float x[4], w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        x[e] = p0 + gq + 8 * (e >> 1) <= lim[f][e & 1] ? sc[f][e] * (cs[f][e & 1] * ks) : -INFINITY;
+#pragma unroll
+                    for (int e = 0; e < 2; ++e) {
+                        float mx = fmaxf(x[e], x[e + 2]);
+#pragma unroll
+                        for (int off = 4; off < 32; off <<= 1) mx = fmaxf(mx, __shfl_xor_sync(0xffffffffu, mx, off));
+                        const float mn = fmaxf(m[f][e], mx), vn = fmaxf(mv[f][e], mx + lvs);
+                        const float cl = ex2_approx(m[f][e] - mn), cv = ex2_approx(mv[f][e] - vn);
+                        m[f][e] = mn;
+                        mv[f][e] = vn;
+                        const float pa = ex2_approx(x[e] - mn), pc = ex2_approx(x[e + 2] - mn);  // 0 for -inf
+                        l[f][e] = fmaf(l[f][e], cl, pa + pc);
+                        const float to = vs == 0.f ? 0.f : vs * ex2_approx(mn - vn + 15.f);
+                        w[e] = pa * to;
+                        w[e + 2] = pc * to;
+#pragma unroll
+                        for (int u = 0; u < 8; ++u) {
+                            acc[f][u][e] *= cv;
+                            acc[f][u][e + 2] *= cv;
+                        }
+                    }
+                    // P^T as the B operand (k = positions, n = row gq)
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t hi = pack_f16x2(w[2 * h], w[2 * h + 1]);
+                        pb[f][0][h] = movmatrix_t(hi);
+                        if constexpr (TERMS == 2) {
+                            const float2 back = unpack_f16x2(hi);
+                            pb[f][1][h] = movmatrix_t(pack_f16x2(w[2 * h] - back.x, w[2 * h + 1] - back.y));
+                        }
+                    }
+                }
+                // acc^T += V^T P^T. A transposed 8 x 8 piece gives a lane the
+                // dims (2 gq, 2 gq + 1) of positions 2t, 2t + 1: dim 2 gq goes to
+                // the product's row gq, 2 gq + 1 to row gq + 8
+#pragma unroll
+                for (int u = 0; u < 8; u += 2) {
+                    uint32_t w[4];
+                    ldsm_x4_trans(vb + fr * kKvD + (((u + fu) ^ (fr & 7)) << 4), w);
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        const uint32_t lo = __byte_perm(w[2 * h], 0, 0x3120), hi = __byte_perm(w[2 * h + 1], 0, 0x3120);
+                        const uint32_t a0 = e4m3x2_to_f16x2(lo & 0xFFFFu), a1 = e4m3x2_to_f16x2(lo >> 16);
+                        const uint32_t a2 = e4m3x2_to_f16x2(hi & 0xFFFFu), a3 = e4m3x2_to_f16x2(hi >> 16);
+#pragma unroll
+                        for (int f = 0; f < NT; ++f)
+#pragma unroll
+                            for (int k = 0; k < TERMS; ++k) mma_f16(acc[f][u + h], a0, a1, a2, a3, pb[f][k][0], pb[f][k][1]);
+                    }
+                }
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(empty + st);
         }
     }
-    for (int off = 16; off > 0; off >>= 1) l += __shfl_xor_sync(0xffffffffu, l, off);
-    if (bad_page) {
-        if (lane == 0) atomicOr(c.err, ERR_KV_PAGE);
-        l = 0.f;
+    __syncthreads();  // the ring is free for the merge
+    if (*flag) {
+        // a wait gave up: let the copies still in flight land (bounded) and
+        // contribute nothing (the error word is set)
+        if (tid == 0)
+            for (int i = 0; i < ST; ++i)
+                tc::mbar_wait(full + i, 0, 100000000ull), tc::mbar_wait(full + i, 1, 100000000ull);
+        __syncthreads();
 #pragma unroll
-        for (int j = 0; j < 4; ++j) acc[j] = 0.f;
+        for (int f = 0; f < NT; ++f) {
+#pragma unroll
+            for (int e = 0; e < 2; ++e) m[f][e] = mv[f][e] = kNone, l[f][e] = 0.f;
+#pragma unroll
+            for (int u = 0; u < 8; ++u)
+#pragma unroll
+                for (int e = 0; e < 4; ++e) acc[f][u][e] = 0.f;
+        }
     }
-    const size_t o = ((size_t)s * a.T + t) * a.out_stride + (size_t)h * kKvD + 4 * lane;
+    // the warps' results through shared memory
+    float* sacc = reinterpret_cast<float*>(sm);
+    float4* sml = reinterpret_cast<float4*>(sm + L::kMl);
+    if (warp < kRwWarps) {
 #pragma unroll
-    for (int j = 0; j < 4; ++j) store_act<TA>(a.out, o + j, l == 0.f ? 0.f : acc[j] / l);
+        for (int f = 0; f < NT; ++f)
+#pragma unroll
+            for (int e = 0; e < 2; ++e) {
+#pragma unroll
+                for (int off = 4; off < 32; off <<= 1) l[f][e] += __shfl_xor_sync(0xffffffffu, l[f][e], off);
+                const int r = warp * L::kRows + 8 * f + 2 * t + e;
+                if (gq == 0) sml[r] = make_float4(m[f][e], l[f][e], mv[f][e], 0.f);
+#pragma unroll
+                for (int u = 0; u < 8; ++u)
+                    *reinterpret_cast<float2*>(sacc + r * kKvD + 16 * u + 2 * gq) = make_float2(acc[f][u][e], acc[f][u][e + 2]);
+            }
+    }
+    __syncthreads();
+    if (W > 1) tc::cluster_wait();  // every walker of the cluster has started: its shared memory is there
+    auto write = [&](int r, float o, float lsum, float from) {  // row r of the group, dim tid
+        const int row = row0 + r;
+        const size_t at = ((size_t)s * a.T + row / R) * a.out_stride + (size_t)(g * R + row % R) * kKvD + tid;
+        store_act<TA>(a.out, at, lsum == 0.f ? 0.f : o / lsum * from);  // a row that sees nothing: zeros
+    };
+    // this walker's (acc, m, l, mv) of each row, to the row's owner: slot
+    // (r / W) W + wk of walker r % W
+    if (tid < kKvD) {
+        for (int r = 0; r < rows; ++r) {
+            float M = kNone, V = kNone;
+#pragma unroll
+            for (int w = 0; w < kRwWarps; ++w) {
+                const float4 x = sml[w * L::kRows + r];
+                M = fmaxf(M, x.x);
+                V = fmaxf(V, x.z);
+            }
+            float o = 0.f, sum = 0.f;
+#pragma unroll
+            for (int w = 0; w < kRwWarps; ++w) {
+                const float4 x = sml[w * L::kRows + r];
+                o = fmaf(ex2_approx(x.z - V), sacc[(w * L::kRows + r) * kKvD + tid], o);
+                sum = fmaf(ex2_approx(x.x - M), x.y, sum);
+            }
+            if (W == 1) {
+                write(r, o, sum, ex2_approx(V - M - 15.f));
+            } else {
+                const uint32_t slot = tc::smem_u32(recv + ((r / W) * W + wk) * kRwSlotF), owner = (uint32_t)(r % W);
+                tc::st_cluster_f32(tc::cluster_map(slot + 4u * tid, owner), o);
+                if (tid == 0) {
+                    tc::st_cluster_f32x2(tc::cluster_map(slot + 4u * kKvD, owner), make_float2(M, sum));
+                    tc::st_cluster_f32(tc::cluster_map(slot + 4u * (kKvD + 2), owner), V);
+                }
+            }
+        }
+    }
+    if (W == 1) return;
+    tc::cluster_arrive();  // the stores into the owners' slots are visible ...
+    tc::cluster_wait();    // ... once every walker has made them
+    if (tid < kKvD) {
+        for (int r = wk; r < rows; r += W) {
+            const float* sl = recv + (r / W) * W * kRwSlotF;
+            float M = kNone, V = kNone;
+            for (int w = 0; w < W; ++w) {
+                M = fmaxf(M, sl[w * kRwSlotF + kKvD]);
+                V = fmaxf(V, sl[w * kRwSlotF + kKvD + 2]);
+            }
+            float o = 0.f, sum = 0.f;
+            for (int w = 0; w < W; ++w) {
+                o = fmaf(ex2_approx(sl[w * kRwSlotF + kKvD + 2] - V), sl[w * kRwSlotF + tid], o);
+                sum = fmaf(ex2_approx(sl[w * kRwSlotF + kKvD] - M), sl[w * kRwSlotF + kKvD + 1], sum);
+            }
+            write(r, o, sum, ex2_approx(V - M - 15.f));
+        }
+    }
+}
+
+// Pages as rows of 128 bytes; a box is a page, or 64 rows of a longer one.
+cudaError_t make_page_map(const uint8_t* pages, const KvCache& c, int box_rows, CUtensorMap* map) {
+    tc::EncodeTiledFn enc = tc::encode_tiled();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[2] = {(cuuint64_t)kKvD, (cuuint64_t)c.n_pages * c.Hkv * c.ps};
+    const cuuint64_t strides[1] = {(cuuint64_t)kKvD};
+    const cuuint32_t box[2] = {(cuuint32_t)kKvD, (cuuint32_t)(c.ps < box_rows ? c.ps : box_rows)};
+    const cuuint32_t estr[2] = {1, 1};
+    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(pages), dims, strides, box, estr,
+                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
+// Per device, once: the kernel's shared-memory and cluster attributes, and
+// how many clusters of 2, 4, 8 and 16 walkers the device holds at once.
+struct RwSetup {
+    bool done;
+    int clusters[5];
+};
+
+template <typename TA, int NT, int TERMS>
+cudaError_t rows_setup(const RwSetup** out) {
+    static std::mutex mutex;
+    static RwSetup per_device[64];
+    auto* kernel = attn_paged_rows_kernel<TA, NT, TERMS>;
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mutex);
+    RwSetup& u = per_device[dev & 63];
+    if (!u.done) {
+        e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RwSmem<NT>::kBytes);
+        if (e != cudaSuccess) return e;
+        const bool wide = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
+        u.clusters[0] = 1 << 30;
+        for (int k = 1; k < 5; ++k) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(1u << k);
+            cfg.blockDim = dim3(kRwThreads);
+            cfg.dynamicSmemBytes = RwSmem<NT>::kBytes;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 1u << k;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int held = 0;
+            if ((k == 4 && !wide) || cudaOccupancyMaxActiveClusters(&held, kernel, &cfg) != cudaSuccess) held = 0;
+            u.clusters[k] = held;
+        }
+        (void)cudaGetLastError();  // a refused query leaves no sticky error
+        u.done = true;
+    }
+    *out = &u;
+    return cudaSuccess;
+}
+
+template <typename TA, int NT, int TERMS>
+cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t st) {
+    const RwSetup* setup = nullptr;
+    cudaError_t e = rows_setup<TA, NT, TERMS>(&setup);
+    if (e != cudaSuccess) return e;
+    CUtensorMap tmk, tmv;
+    e = make_page_map(a.c.kp, a.c, kRwTc, &tmk);
+    if (e == cudaSuccess) e = make_page_map(a.c.vp, a.c, kRwTc, &tmv);
+    if (e != cudaSuccess) return e;
+    const int groups = (a.T * (a.Hq / a.c.Hkv) + 8 * NT - 1) / (8 * NT);
+    // The walkers of a group double while all CTAs stay resident at once (two
+    // an SM of the 152) and each may still get a chunk.
+    const long pairs = (long)a.c.S * a.c.Hkv * groups, chunks = (a.c.capacity() + kRwTc - 1) / kRwTc;
+    int W = 1;
+    for (int k = 1; k < 5 && pairs * 2 * W <= 2 * 152 && 2 * W <= chunks && pairs <= setup->clusters[k]; ++k) W *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3(W * groups * a.c.Hkv, a.c.S);
+    cfg.blockDim = dim3(kRwThreads);
+    cfg.dynamicSmemBytes = RwSmem<NT>::kBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = W;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = W > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, attn_paged_rows_kernel<TA, NT, TERMS>, a, tmk, tmv, W);
 }
 
 }  // namespace
@@ -117,10 +592,8 @@ size_t attn_paged_workspace_bytes(const KvCache& c, int T, int Hq, bool bf16) {
 }
 
 cudaError_t launch_attn_paged(const PagedAttnArgs& a, cudaStream_t st) {
-    const long rows = (long)a.T * a.Hq;
-    const dim3 grid((unsigned)((rows + kPaWarps - 1) / kPaWarps), (unsigned)a.c.S);
-    return a.bf16 ? launch_pdl(attn_paged_simple_kernel<bf16_t>, grid, dim3(32 * kPaWarps), 0, st, a)
-                  : launch_pdl(attn_paged_simple_kernel<float>, grid, dim3(32 * kPaWarps), 0, st, a);
+    if (!a.bf16) return launch_rows<float, 1, 2>(a, st);
+    return a.T * (a.Hq / a.c.Hkv) <= 8 ? launch_rows<bf16_t, 1, 1>(a, st) : launch_rows<bf16_t, 2, 1>(a, st);
 }
 
 }  // namespace m2
