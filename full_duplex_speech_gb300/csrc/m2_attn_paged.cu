@@ -30,45 +30,14 @@
 //          Blocks whose values are of very different size thus lose nothing
 //          to fp16's range; sums of p (l) stay fp32 and apart.
 //     out = 2^(mv - m - 15) acc / l.
-#include <cuda.h>
-#include <cuda_fp16.h>
-#include <cuda_runtime.h>
-
 #include <mutex>
 
-#include "m2_common.cuh"
-#include "m2_paged.h"
-#include "m2_tc.cuh"
+#include "m2_paged_dev.cuh"
 
 namespace m2 {
 
 namespace {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNone = -1e30f;  // a running maximum before any position
-
-__device__ __forceinline__ float ex2_approx(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float lg2_approx(float x) {
-    float r;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-// two e4m3 codes (the low byte first) as fp16, exactly
-__device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.e4m3x2 %0, %1;" : "=r"(r) : "h"((uint16_t)two));
-    return r;
-}
-__device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
-__device__ __forceinline__ float2 unpack_f16x2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
 __device__ __forceinline__ void ldsm_x4(uint32_t addr, uint32_t (&r)[4]) {
     asm volatile("ldmatrix.sync.aligned.m8n8.x4.shared.b16 {%0, %1, %2, %3}, [%4];"
                  : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3])
@@ -94,23 +63,6 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
-// 4 bytes global -> shared, completion counted by cp_async_arrive
-__device__ __forceinline__ void cp_async4(void* dst, const void* src) {
-    asm volatile("cp.async.ca.shared.global [%0], [%1], 4;" ::"r"(tc::smem_u32(dst)), "l"(src) : "memory");
-}
-// One of the barrier's expected arrivals, made when this thread's earlier
-// cp.async copies have landed.
-__device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
-    asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
-}
-
-// The power of two that takes a row's largest magnitude to [2^14, 2^15) (1
-// for a row of zeros; the exponent is kept below 2^126).
-__device__ __forceinline__ float row_power(float amax) {
-    const int ex = (int)(__float_as_uint(amax) >> 23) - 127;
-    return amax == 0.f ? 1.f : __uint_as_float((uint32_t)(min(14 - ex, 126) + 127) << 23);
-}
-
 constexpr int kRwWarps = 4;                              // warps that compute
 constexpr int kRwThreads = 32 * kRwWarps + 32;           // ... and the producer
 constexpr int kRwTc = 16 * kRwWarps;                     // positions per chunk
@@ -275,7 +227,7 @@ __global__ void __launch_bounds__(kRwThreads, 2)
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float pw = row_power(top), sg = a.scale < 0.f ? -pw : pw;
+            const float pw = row_power(top, 14), sg = a.scale < 0.f ? -pw : pw;
 #pragma unroll
             for (int u = 0; u < 8; ++u)
 #pragma unroll
@@ -493,20 +445,6 @@ __global__ void __launch_bounds__(kRwThreads, 2)
     }
 }
 
-// Pages as rows of 128 bytes; a box is a page, or 64 rows of a longer one.
-cudaError_t make_page_map(const uint8_t* pages, const KvCache& c, int box_rows, CUtensorMap* map) {
-    tc::EncodeTiledFn enc = tc::encode_tiled();
-    if (!enc) return cudaErrorNotSupported;
-    const cuuint64_t dims[2] = {(cuuint64_t)kKvD, (cuuint64_t)c.n_pages * c.Hkv * c.ps};
-    const cuuint64_t strides[1] = {(cuuint64_t)kKvD};
-    const cuuint32_t box[2] = {(cuuint32_t)kKvD, (cuuint32_t)(c.ps < box_rows ? c.ps : box_rows)};
-    const cuuint32_t estr[2] = {1, 1};
-    CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_UINT8, 2, const_cast<uint8_t*>(pages), dims, strides, box, estr,
-                     CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                     CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 // Per device, once: the kernel's shared-memory and cluster attributes, and
 // how many clusters of 2, 4, 8 and 16 walkers the device holds at once.
 struct RwSetup {
@@ -593,7 +531,9 @@ size_t attn_paged_workspace_bytes(const KvCache& c, int T, int Hq, bool bf16) {
 
 cudaError_t launch_attn_paged(const PagedAttnArgs& a, cudaStream_t st) {
     if (!a.bf16) return launch_rows<float, 1, 2>(a, st);
-    return a.T * (a.Hq / a.c.Hkv) <= 8 ? launch_rows<bf16_t, 1, 1>(a, st) : launch_rows<bf16_t, 2, 1>(a, st);
+    const long rows = (long)a.T * (a.Hq / a.c.Hkv);
+    if (rows > 16) return launch_attn_paged_tiles(a, st);
+    return rows <= 8 ? launch_rows<bf16_t, 1, 1>(a, st) : launch_rows<bf16_t, 2, 1>(a, st);
 }
 
 }  // namespace m2

@@ -1,0 +1,597 @@
+// Attention over the paged e4m3 cache for many rows (a prefill, sessions
+// catching up, cross attention of a whole sequence), bf16 activations, on the
+// tcgen05 tensor cores. The operator and its formulas are those of
+// m2_attn_paged.cu; a kv head's rows are its (query, head) pairs, row = t R + r.
+//
+// One CTA takes two tiles of 128 rows of one (session, kv head) and walks the
+// positions they see, 128 at a time. Per chunk and tile:
+//   S = q K^T       kind::f8f6f4 straight from the cache's codes. A query row,
+//                   scaled by a power of two to a largest element in
+//                   [2^7, 2^8), enters as two e4m3 terms, hi and lo: 8
+//                   significant bits, which is all of a bf16 (elements below
+//                   2^-8 of the largest are off by at most 2^-17 of it), at
+//                   the cost of one product in 16 bits and with no
+//                   conversion of the keys;
+//   softmax         one thread a row, S read out of tensor memory in fp32:
+//                   x = S (scale ks), p = 2^(x - m), l += p, and the weight
+//                   w = p vs 2^(m - mv + 7) to fp16 (2^-11) over S;
+//   O += w V        kind::f16, w from tensor memory, V converted to fp16
+//                   (exactly) by two warps.
+// m and mv (the reference of the weights, a maximum of x + log2 vs) move only
+// when a chunk exceeds them by more than 2^8, which p <= 2^8 in fp32 and
+// w <= 2^15 in fp16 allow; only then is O rescaled in tensor memory.
+//     out = 2^(mv - m - 7) O / l.
+//
+// Warps: 0 copies (pages by TMA through rings, scales by 4-byte asynchronous
+// copies), 1 issues the products, 2 and 3 convert V, 4-7 and 8-11 the
+// softmax of tile 0 and of tile 1. The products of one tile run under the
+// other's softmax. Where few CTAs would leave SMs idle, W CTAs of a cluster
+// share the positions of one pair of tiles and merge through distributed
+// shared memory, each the owner of 256 / W rows.
+#include <cuda_fp8.h>
+
+#include <mutex>
+
+#include "m2_paged_dev.cuh"
+
+namespace m2 {
+
+namespace {
+
+constexpr int kTlThreads = 384;
+constexpr int kTlRows = 128;                       // rows of a tile
+constexpr int kTlTc = 128;                         // positions per chunk
+constexpr int kTlBlocks = kTlTc / kKvBlock;        // scales of a chunk
+constexpr uint32_t kTlTile = kTlTc * kKvD;         // 16 KB of codes
+constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kScStages = 4;
+constexpr float kSlack = 8.f;                      // log2 by which a chunk may exceed the references
+constexpr float kLift = 7.f;                       // log2 of the weights' reference: 2^(7 + 8) at most
+constexpr uint32_t kColO = 0, kColS = 256;         // tensor memory: O of the two tiles, then S (and w over it)
+constexpr int kTlMaxW = 8;
+
+struct TlSmem {
+    static constexpr uint32_t kQ = 0;                                    // [tile][hi, lo] 16 KB, K-major, 128-byte swizzle
+    static constexpr uint32_t kK = kQ + 4 * kTlTile;                     // kKStages, the same layout
+    static constexpr uint32_t kV = kK + kKStages * kTlTile;              // kVStages
+    static constexpr uint32_t kH = kV + kVStages * kTlTile;              // V in fp16, kHStages x 32 KB, MN-major
+    static constexpr uint32_t kSc = kH + kHStages * 2 * kTlTile;         // float [stage][ks 8, vs 8]
+    static constexpr uint32_t kBar = kSc + kScStages * 2 * kTlBlocks * 4;
+    // kfull, kempty, vfull, vempty, hfull, hempty, scfull, scempty, sfull[2], pfull[2], qfull, ofull, end
+    static constexpr int kBars = 2 * (kKStages + kVStages + kHStages + kScStages) + 7;
+    static constexpr uint32_t kTmem = kBar + kBars * 8;
+    static constexpr uint32_t kFlag = kTmem + 4;
+    static constexpr uint32_t kBytes = kFlag + 4 + 1024;  // + slack to align to 1024
+    // after the walk, over the rings: 256 / W rows x W walkers x 128 floats, then their (l, m, mv)
+    static constexpr uint32_t kMl = 2 * kTlRows * kKvD * 4;
+    static_assert(kMl + 2 * kTlRows * 16 <= kSc, "the merge fits in the rings");
+    static_assert(kBytes <= 227 * 1024, "one CTA an SM");
+};
+
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N) {  // e4m3 x e4m3, both K-major, fp32 sums
+    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+__host__ __device__ constexpr uint32_t idesc_f16_bmn(int M, int N) {  // fp16 x fp16, B MN-major, fp32 sums
+    return (1u << 4) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+}
+
+__device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t bdesc, uint32_t idesc, uint32_t accumulate) {
+    asm volatile(
+        "{\n\t.reg .pred p;\n\t"
+        "setp.ne.b32 p, %4, 0;\n\t"
+        "tcgen05.mma.cta_group::1.kind::f8f6f4 [%0], %1, %2, %3, p;\n\t}" ::"r"(d_tmem),
+        "l"(adesc), "l"(bdesc), "r"(idesc), "r"(accumulate)
+        : "memory");
+}
+
+// 32 lanes x 32 consecutive columns: thread t of the warp gets lane base + t.
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    asm volatile(
+        "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
+        "%20,%21,%22,%23,%24,%25,%26,%27,%28,%29,%30,%31}, [%32];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(r[16]), "=r"(r[17]),
+          "=r"(r[18]), "=r"(r[19]), "=r"(r[20]), "=r"(r[21]), "=r"(r[22]), "=r"(r[23]), "=r"(r[24]), "=r"(r[25]), "=r"(r[26]),
+          "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
+        : "r"(taddr));
+}
+__device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
+    asm volatile(
+        "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
+        "r"(r[0]), "r"(r[1]), "r"(r[2]), "r"(r[3]), "r"(r[4]), "r"(r[5]), "r"(r[6]), "r"(r[7]), "r"(r[8]), "r"(r[9]), "r"(r[10]),
+        "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
+        : "memory");
+}
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t caddr, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(caddr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
+// grid (W x Hkv x row pairs, S), a cluster of W CTAs when W > 1
+__global__ void __launch_bounds__(kTlThreads, 1)
+    attn_paged_tile_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                           int W) {
+    using L = TlSmem;
+    extern __shared__ uint8_t tl_raw[];
+    uint8_t* sm = tl_raw + ((1024u - (tc::smem_u32(tl_raw) & 1023u)) & 1023u);
+    float* scales = reinterpret_cast<float*>(sm + L::kSc);
+    uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + L::kBar);
+    uint64_t *kempty = kfull + kKStages, *vfull = kempty + kKStages, *vempty = vfull + kVStages, *hfull = vempty + kVStages,
+             *hempty = hfull + kHStages, *scfull = hempty + kHStages, *scempty = scfull + kScStages,
+             *sfull = scempty + kScStages, *pfull = sfull + 2, *qfull = pfull + 2, *ofull = qfull + 1, *endbar = ofull + 1;
+    uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + L::kTmem);
+    volatile uint32_t* flag = reinterpret_cast<uint32_t*>(sm + L::kFlag);
+    const KvCache& c = a.c;
+    const int wk = (int)blockIdx.x % W, s = blockIdx.y;
+    // the row pairs from the last on: under a causal limit they take longest
+    const int pair = (int)(gridDim.x - 1 - blockIdx.x) / W;
+    const int g = pair % c.Hkv, row0 = pair / c.Hkv * (2 * kTlRows);
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
+    const int R = a.Hq / c.Hkv;
+
+    if (W > 1) tc::cluster_arrive_relaxed();  // waited on before the first remote store: every CTA has started
+    pdl_wait();  // the queries and the cache may come from the previous kernel
+    pdl_trigger();
+    int before, n;
+    const bool ok = kv_extent(c, s, a.T, a.lens, a.n_new, a.causal ? c.capacity() : c.capacity() + a.T, &before, &n) &&
+                    before <= c.capacity();
+    if (!ok && blockIdx.x == 0 && tid == 0) atomicOr(c.err, ERR_ATTN_LENGTH);
+    const int rows = min(n * R - row0, 2 * kTlRows);
+    if (rows <= 0) return;  // the whole cluster
+    // positions that the tiles' last rows see, and this CTA's run of chunks
+    auto seen_by = [&](int last) { return !ok ? 0 : a.causal ? before + (row0 + last) / R + 1 : before; };
+    const int total = seen_by(rows - 1);
+    const int nch = (total + kTlTc - 1) / kTlTc, cpw = (nch + W - 1) / W;
+    const int cb = min(wk * cpw, nch), nc = min(cpw, nch - cb);  // chunks cb .. cb + nc - 1
+    const int total0 = seen_by(min(rows, kTlRows) - 1);
+    const int nc0 = min(max((total0 + kTlTc - 1) / kTlTc - cb, 0), nc);  // of which tile 0 takes so many
+    const int nc1 = rows > kTlRows ? nc : 0;
+
+    if (tid == 0) {
+        for (int i = 0; i < kKStages; ++i) tc::mbar_init(kfull + i, 1), tc::mbar_init(kempty + i, 1);
+        for (int i = 0; i < kVStages; ++i) tc::mbar_init(vfull + i, 1), tc::mbar_init(vempty + i, 2);
+        for (int i = 0; i < kHStages; ++i) tc::mbar_init(hfull + i, 64), tc::mbar_init(hempty + i, 1);
+        for (int i = 0; i < kScStages; ++i) tc::mbar_init(scfull + i, 32), tc::mbar_init(scempty + i, 8);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(sfull + i, 1), tc::mbar_init(pfull + i, kTlRows);
+        tc::mbar_init(qfull, 2 * kTlRows);
+        tc::mbar_init(ofull, 1);
+        tc::mbar_init(endbar, 1);
+        tc::fence_mbar_init();
+        *flag = 0;
+    }
+    if (warp == 1) {
+        tc::tmem_alloc(sTmem, 512);
+        tc::tmem_relinquish();
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tm = *sTmem;
+
+    // A bounded wait; the first that runs out stops the CTA's work.
+    auto wait_ok = [&](uint64_t* bar, uint32_t parity) -> bool {
+        if (*flag) return false;
+        if (tc::mbar_wait(bar, parity)) return true;
+        atomicOr(c.err, ERR_MBAR_TIMEOUT_MMA);
+        *flag = 1;
+        return false;
+    };
+    // the same for a converged warp
+    auto warp_ok = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait_ok(bar, parity)); };
+
+    float m = kNone, mv = kNone, l = 0.f;  // of a softmax thread's row
+    if (warp == 0) {
+        // ------------------------------------------------------------ copies
+        const int* table = c.table + (size_t)s * c.max_pages;
+        const int pieces = kTlTc >> c.ps_shift;  // pages a chunk (a page holds at most a chunk)
+        const uint32_t page_bytes = (uint32_t)c.ps * kKvD;
+        const int last_page = (total - 1) >> c.ps_shift;
+        int held = -32, page_ids = 0;  // this lane's entry of table[held .. held + 31]
+        for (int j = 0; j < nc; ++j) {
+            const int p0 = (cb + j) * kTlTc, first = p0 >> c.ps_shift;
+            if (held < 0 || first + pieces > held + 32) {
+                held = first;
+                page_ids = first + lane <= last_page ? table[first + lane] : 0;
+                if (page_ids < 0 || page_ids >= c.n_pages) {
+                    atomicOr(c.err, ERR_KV_PAGE);
+                    page_ids = 0;  // some page of the pool: what is read is undefined
+                }
+                __syncwarp();
+            }
+            const int live = min(pieces, last_page - first + 1);
+            const int ks = j % kKStages, vs = j % kVStages, ss = j % kScStages;
+            // lane i < live copies page first + i
+            const int y = (__shfl_sync(0xffffffffu, page_ids, first - held + min(lane, pieces - 1)) * c.Hkv + g) * c.ps;
+            if (j >= kKStages && !warp_ok(kempty + ks, (uint32_t)(j / kKStages - 1) & 1)) break;
+            if (lane == 0) tc::mbar_arrive_expect_tx(kfull + ks, live * page_bytes);
+            __syncwarp();
+            if (lane < live) tc::tma_load_2d(sm + L::kK + ks * kTlTile + lane * page_bytes, &tmk, 0, y, kfull + ks);
+            __syncwarp();
+            if (j >= kScStages && !warp_ok(scempty + ss, (uint32_t)(j / kScStages - 1) & 1)) break;
+            {
+                const int b = lane & (kTlBlocks - 1), p = p0 + b * kKvBlock;  // lanes 0 .. 7 the keys' scales, 8 .. 15 the values'
+                const int page = __shfl_sync(0xffffffffu, page_ids, min((p >> c.ps_shift) - held, 31));
+                if (lane < 2 * kTlBlocks && p < total) {
+                    const size_t at = (((size_t)page * c.Hkv + g) << (c.ps_shift - 4)) + ((p & (c.ps - 1)) >> 4);
+                    cp_async4(scales + ss * 2 * kTlBlocks + lane, (lane < kTlBlocks ? c.ks : c.vs) + at);
+                }
+                cp_async_arrive(scfull + ss);
+            }
+            if (j >= kVStages && !warp_ok(vempty + vs, (uint32_t)(j / kVStages - 1) & 1)) break;
+            if (lane == 0) tc::mbar_arrive_expect_tx(vfull + vs, live * page_bytes);
+            __syncwarp();
+            if (lane < live) tc::tma_load_2d(sm + L::kV + vs * kTlTile + lane * page_bytes, &tmv, 0, y, vfull + vs);
+            __syncwarp();
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else if (warp == 1) {
+        // ---------------------------------------------------------- products
+        const bool leader = tc::elect_one();
+        const uint32_t sbase = tc::smem_u32(sm);
+        const uint32_t id8 = idesc_f8(kTlRows, kTlTc), id16 = idesc_f16_bmn(kTlRows, kKvD);
+        bool good = nc == 0 || warp_ok(qfull, 0);
+        for (int j = 0; j <= nc && good; ++j) {
+#pragma unroll
+            for (int i = 0; i < 2; ++i) {
+                const int nci = i ? nc1 : nc0;
+                if (j > 0 && j - 1 < nci) {  // O_i += w V of chunk j - 1
+                    const int h = (j - 1) % kHStages;
+                    good = good && warp_ok(hfull + h, (uint32_t)((j - 1) / kHStages) & 1) && warp_ok(pfull + i, (uint32_t)(j - 1) & 1);
+                    if (!good) break;
+                    tc::tc_fence_after();
+                    if (leader) {
+                        const uint64_t bd = tc::sdesc(sbase + L::kH + h * 2 * kTlTile, 2048, 128, 0);
+#pragma unroll
+                        for (int k = 0; k < 8; ++k)
+                            tc::mma_bf16_tmem_a(tm + kColO + 128 * i, tm + kColS + 128 * i + 8 * k, bd + (uint64_t)(k * 4096 >> 4),
+                                                id16, (j > 1 || k > 0) ? 1u : 0u);
+                        // the last tile that reads this V releases it (tile 1 takes every chunk, where there is one)
+                        if (i == 1 || nc1 == 0) tc::mma_commit(hempty + h);
+                    }
+                    __syncwarp();
+                }
+                if (j < nci) {  // S_i = q_i K^T of chunk j
+                    const int k8 = j % kKStages;
+                    good = good && warp_ok(kfull + k8, (uint32_t)(j / kKStages) & 1);
+                    if (!good) break;
+                    tc::tc_fence_after();
+                    if (leader) {
+                        const uint64_t bd = tc::sdesc(sbase + L::kK + k8 * kTlTile, 0, 1024, 2);
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            const uint64_t ad = tc::sdesc(sbase + L::kQ + (2 * i + part) * kTlTile, 0, 1024, 2);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_f8(tm + kColS + 128 * i, ad + 2 * k, bd + 2 * k, id8, (part > 0 || k > 0) ? 1u : 0u);
+                        }
+                        tc::mma_commit(sfull + i);
+                        if (i == 1 || nc1 == 0) tc::mma_commit(kempty + k8);
+                    }
+                    __syncwarp();
+                }
+            }
+        }
+        if (leader && good) tc::mma_commit(ofull);
+        __syncwarp();
+    } else if (warp < 4) {
+        // -------------------------------------------- V to fp16, 64 threads
+        const int ct = tid - 64, k7 = ct & 7, sub = ct >> 3;  // position within 8; one of 8 (position group, unit) pairs
+        for (int j = 0; j < nc; ++j) {
+            const int vs = j % kVStages, h = j % kHStages;
+            if (!warp_ok(vfull + vs, (uint32_t)(j / kVStages) & 1)) break;
+            if (j >= kHStages && !warp_ok(hempty + h, (uint32_t)(j / kHStages - 1) & 1)) break;
+            const uint8_t* src = sm + L::kV + vs * kTlTile;
+            uint8_t* dst = sm + L::kH + h * 2 * kTlTile;
+            const int left = total - (cb + j) * kTlTc;  // positions behind the last count as zero values
+            // thread: position 8 pg + k7, dims 16 sub .. + 15 (16 codes, swizzled) -> two 16-byte
+            // pieces of the 8 x 8 blocks of the product's MN-major operand
+#pragma unroll 4
+            for (int pg = 0; pg < kTlTc / 8; ++pg) {
+                const int p = 8 * pg + k7;
+                uint4 w = *reinterpret_cast<const uint4*>(src + p * kKvD + ((sub ^ k7) << 4));
+                if (p >= left) w = make_uint4(0u, 0u, 0u, 0u);
+                uint4 lo, hi;
+                lo.x = e4m3x2_to_f16x2(w.x & 0xFFFFu), lo.y = e4m3x2_to_f16x2(w.x >> 16);
+                lo.z = e4m3x2_to_f16x2(w.y & 0xFFFFu), lo.w = e4m3x2_to_f16x2(w.y >> 16);
+                hi.x = e4m3x2_to_f16x2(w.z & 0xFFFFu), hi.y = e4m3x2_to_f16x2(w.z >> 16);
+                hi.z = e4m3x2_to_f16x2(w.w & 0xFFFFu), hi.w = e4m3x2_to_f16x2(w.w >> 16);
+                uint8_t* o = dst + pg * 2048 + sub * 256 + k7 * 16;
+                *reinterpret_cast<uint4*>(o) = lo;
+                *reinterpret_cast<uint4*>(o + 128) = hi;
+            }
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(hfull + h);
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(vempty + vs);
+        }
+    } else {
+        // ------------------------------------------ softmax, one row a thread
+        const int i = (warp - 4) >> 2, r = tid - 128 - 128 * i, row = 128 * i + r;  // tile, row of it, row of the pair
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tm + lanes + kColS + 128 * i, tO = tm + lanes + kColO + 128 * i;
+        const bool live = row < rows;
+        // the row of q, scaled, as e4m3 hi + lo
+        float cs;
+        {
+            uint4 x[16];
+            const int rr = row0 + (live ? row : 0);
+            const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
+                                                              ((size_t)s * a.T + rr / R) * a.q_stride + (size_t)(g * R + rr % R) * kKvD);
+            float top = 0.f;
+#pragma unroll
+            for (int u = 0; u < 16; ++u) x[u] = __ldg(src + u);
+#pragma unroll
+            for (int u = 0; u < 16; ++u) {
+                const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+#pragma unroll
+                for (int e = 0; e < 4; ++e)
+                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+            }
+            const float pw = row_power(top, 7), sg = a.scale < 0.f ? -pw : pw;
+            cs = top < INFINITY ? fabsf(a.scale) * kLog2e / pw : NAN;  // e4m3 has no infinity: such a row reads NaN
+            uint8_t* q8 = sm + L::kQ + 2 * i * kTlTile + r * kKvD;
+#pragma unroll
+            for (int u = 0; u < 8; ++u) {
+                uint32_t hi[4], lo[4];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint4& y = x[2 * u + (e >> 1)];
+                    const uint32_t w0 = (e & 1) ? y.z : y.x, w1 = (e & 1) ? y.w : y.y;
+                    const float f[4] = {__uint_as_float(w0 << 16) * sg, __uint_as_float(w0 & 0xFFFF0000u) * sg,
+                                        __uint_as_float(w1 << 16) * sg, __uint_as_float(w1 & 0xFFFF0000u) * sg};
+                    hi[e] = lo[e] = 0u;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * b], f[2 * b + 1]), __NV_SATFINITE, __NV_E4M3);
+                        const float2 back = unpack_f16x2(e4m3x2_to_f16x2(h2));
+                        const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * b] - back.x, f[2 * b + 1] - back.y),
+                                                                     __NV_SATFINITE, __NV_E4M3);
+                        hi[e] |= h2 << (16 * b);
+                        lo[e] |= l2 << (16 * b);
+                    }
+                }
+                const uint32_t off = (uint32_t)(u ^ (r & 7)) << 4;
+                *reinterpret_cast<uint4*>(q8 + off) = live ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(0u, 0u, 0u, 0u);
+                *reinterpret_cast<uint4*>(q8 + kTlTile + off) =
+                    live ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(0u, 0u, 0u, 0u);
+            }
+            tc::fence_proxy_async_smem();
+            tc::mbar_arrive(qfull);
+        }
+        const int lim = !live || !ok ? -1 : a.causal ? before + (row0 + row) / R : before - 1;  // the last position seen
+        const int nci = i ? nc1 : nc0;
+        for (int j = 0; j < nc; ++j) {
+            const int ss = j % kScStages;
+            if (!warp_ok(scfull + ss, (uint32_t)(j / kScStages) & 1)) break;
+            if (j < nci) {
+                if (!warp_ok(sfull + i, (uint32_t)j & 1)) break;
+                tc::tc_fence_after();
+                const float* sk = scales + ss * 2 * kTlBlocks;
+                const int see = lim - (cb + j) * kTlTc;  // columns 0 .. see are seen
+                const bool cut = __any_sync(0xffffffffu, see < kTlTc - 1);
+                float v[32];
+                // the chunk's maxima: of x, and of x + log2 vs
+                float mx = -INFINITY, mvx = -INFINITY;
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    tmem_ld32(tS + 32 * q, v);
+                    tc::tmem_wait_ld();
+                    if (cut)
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) v[k] = 32 * q + k <= see ? v[k] : -INFINITY;
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        float t = v[16 * b];
+#pragma unroll
+                        for (int k = 1; k < 16; ++k) t = fmaxf(t, v[16 * b + k]);
+                        const float x = 32 * q + 16 * b <= see ? t * (cs * sk[2 * q + b]) : -INFINITY;
+                        mx = fmaxf(mx, x);
+                        mvx = fmaxf(mvx, x + lg2_approx(sk[kTlBlocks + 2 * q + b]));
+                    }
+                }
+                if (mx > m + kSlack) {
+                    l *= ex2_approx(m - mx);
+                    m = mx;
+                }
+                const bool grow = mvx > mv + kSlack;
+                const float f = grow ? ex2_approx(mv - mvx) : 1.f;
+                if (grow) mv = mvx;
+                if (j > 0 && __any_sync(0xffffffffu, grow)) {  // O is idle: its products came before S
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        tmem_ld32(tO + 32 * q, v);
+                        tc::tmem_wait_ld();
+                        uint32_t y[2][16];
+#pragma unroll
+                        for (int k = 0; k < 32; ++k) y[k >> 4][k & 15] = __float_as_uint(v[k] * f);
+                        tmem_st16(tO + 32 * q, y[0]);
+                        tmem_st16(tO + 32 * q + 16, y[1]);
+                    }
+                }
+                const float lift = ex2_approx(m - mv + kLift);
+#pragma unroll
+                for (int q = 0; q < 4; ++q) {
+                    tmem_ld32(tS + 32 * q, v);
+                    tc::tmem_wait_ld();
+                    uint32_t y[16];
+#pragma unroll
+                    for (int b = 0; b < 2; ++b) {
+                        const bool any = 32 * q + 16 * b <= see;
+                        const float cx = any ? cs * sk[2 * q + b] : 1.f;
+                        const float vsb = sk[kTlBlocks + 2 * q + b];
+                        const float to = !any || vsb == 0.f ? 0.f : vsb * lift;
+                        float sum = 0.f;
+#pragma unroll
+                        for (int k = 0; k < 16; ++k) v[16 * b + k] = fmaf(v[16 * b + k], cx, -m);
+                        if (cut)
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) v[16 * b + k] = 32 * q + 16 * b + k <= see ? v[16 * b + k] : -INFINITY;
+#pragma unroll
+                        for (int k = 0; k < 16; k += 2) {
+                            const float p0 = ex2_approx(v[16 * b + k]), p1 = ex2_approx(v[16 * b + k + 1]);
+                            sum += p0 + p1;
+                            y[8 * b + (k >> 1)] = pack_f16x2(p0 * to, p1 * to);
+                        }
+                        l += sum;
+                    }
+                    tmem_st16(tS + 16 * q, y);  // over columns of S that are read already
+                }
+                tc::tmem_wait_st();
+                tc::tc_fence_before();
+                tc::mbar_arrive(pfull + i);
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(scempty + ss);
+        }
+    }
+    // ------------------------------------------------------------- the merge
+    __syncwarp();
+    const bool walked = warp < 4 || (warp < 8 ? nc0 : nc1) == 0 || warp_ok(ofull, 0);
+    tc::tc_fence_after();
+    __syncthreads();
+    const bool gave_up = *flag != 0;
+    if (gave_up && warp == 1 && tc::elect_one()) {
+        // every product issued must be done and the copies in flight must land
+        // before the tensor memory is freed and the CTA exits (all bounded)
+        tc::mma_commit(endbar);
+        tc::mbar_wait(endbar, 0, 100000000ull);
+        for (int i = 0; i < kKStages; ++i)
+            tc::mbar_wait(kfull + i, 0, 100000000ull), tc::mbar_wait(kfull + i, 1, 100000000ull);
+        for (int i = 0; i < kVStages; ++i)
+            tc::mbar_wait(vfull + i, 0, 100000000ull), tc::mbar_wait(vfull + i, 1, 100000000ull);
+    }
+    __syncthreads();
+    const int own = 2 * kTlRows / W;  // rows that a CTA of the cluster owns
+    if (W > 1) {
+        tc::cluster_wait();    // every CTA has started ...
+        tc::cluster_arrive();  // ... and is done with its rings
+        tc::cluster_wait();
+    }
+    if (warp >= 4) {
+        const int i = (warp - 4) >> 2, row = tid - 128;
+        const uint32_t tO = tm + ((uint32_t)((warp & 3) * 32) << 16) + kColO + 128 * i;
+        const bool some = walked && !gave_up && (i ? nc1 : nc0) > 0;  // (the same in the whole warp)
+        const bool live = row < rows;
+        if (!some) m = mv = kNone, l = 0.f;
+        const int rr = row0 + (live ? row : 0);
+        uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + ((size_t)s * a.T + rr / R) * a.out_stride +
+                        (size_t)(g * R + rr % R) * kKvD;
+        const float f = l == 0.f ? 0.f : ex2_approx(mv - m - kLift) / l;
+        const uint32_t slot = tc::smem_u32(sm) + (uint32_t)((wk * own + row % own) * kKvD * 4);
+        const uint32_t owner = (uint32_t)(row / own);
+#pragma unroll
+        for (int q = 0; q < 4; ++q) {
+            float v[32];
+            if (some) {
+                tmem_ld32(tO + 32 * q, v);
+                tc::tmem_wait_ld();
+            } else {
+#pragma unroll
+                for (int k = 0; k < 32; ++k) v[k] = 0.f;
+            }
+            if (live && W == 1) {
+#pragma unroll
+                for (int k = 0; k < 32; k += 8) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int e = 0; e < 4; ++e)
+                        w[e] = (uint32_t)float_to_bf16_bits(l == 0.f ? 0.f : v[k + 2 * e] * f) |
+                               ((uint32_t)float_to_bf16_bits(l == 0.f ? 0.f : v[k + 2 * e + 1] * f) << 16);
+                    *reinterpret_cast<uint4*>(out + 32 * q + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                }
+            } else if (live) {
+                // 16-byte pieces rotated by the row, so that a warp's rows do not meet in one bank
+#pragma unroll
+                for (int k = 0; k < 8; ++k)
+                    st_cluster_f32x4(tc::cluster_map(slot + (uint32_t)(((8 * q + k + row) & 31) << 4), owner),
+                                     make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+            }
+            __syncwarp();
+        }
+        if (W > 1 && live)
+            st_cluster_f32x4(tc::cluster_map(tc::smem_u32(sm + L::kMl) + (uint32_t)((wk * own + row % own) * 16), owner),
+                             make_float4(m, l, mv, 0.f));
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    if (warp == 1) tc::tmem_dealloc(tm, 512);
+    if (W == 1) return;
+    tc::cluster_arrive();  // the stores into the owners' memory are visible ...
+    tc::cluster_wait();    // ... once every CTA has made them
+    // this CTA's rows, a warp a row, four dims a lane:
+    // out = 2^(V - M - 7) sum_w 2^(mv_w - V) O_w / sum_w 2^(m_w - M) l_w
+    const float4* ml = reinterpret_cast<const float4*>(sm + L::kMl);
+    for (int r = warp; r < own; r += kTlThreads / 32) {
+        const int row = wk * own + r;
+        if (row >= rows) break;
+        float M = kNone, V = kNone;
+        for (int w = 0; w < W; ++w) {
+            M = fmaxf(M, ml[w * own + r].x);
+            V = fmaxf(V, ml[w * own + r].z);
+        }
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+        float sum = 0.f;
+        for (int w = 0; w < W; ++w) {
+            const float4 x = ml[w * own + r];
+            const float f = ex2_approx(x.z - V);
+            const float4 y = *reinterpret_cast<const float4*>(sm + (uint32_t)((w * own + r) * kKvD * 4) + (((lane + row) & 31) << 4));
+            o.x = fmaf(f, y.x, o.x), o.y = fmaf(f, y.y, o.y), o.z = fmaf(f, y.z, o.z), o.w = fmaf(f, y.w, o.w);
+            sum = fmaf(ex2_approx(x.x - M), x.y, sum);
+        }
+        const float f = ex2_approx(V - M - kLift) / sum;
+        const bool none = sum == 0.f;  // a row that sees nothing: zeros
+        const int rr = row0 + row;
+        uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + ((size_t)s * a.T + rr / R) * a.out_stride +
+                        (size_t)(g * R + rr % R) * kKvD + 4 * lane;
+        const uint32_t w0 = (uint32_t)float_to_bf16_bits(none ? 0.f : o.x * f) | ((uint32_t)float_to_bf16_bits(none ? 0.f : o.y * f) << 16);
+        const uint32_t w1 = (uint32_t)float_to_bf16_bits(none ? 0.f : o.z * f) | ((uint32_t)float_to_bf16_bits(none ? 0.f : o.w * f) << 16);
+        *reinterpret_cast<uint2*>(out) = make_uint2(w0, w1);
+    }
+}
+
+cudaError_t tile_setup() {
+    static std::mutex mutex;
+    static bool done[64];
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    std::lock_guard<std::mutex> lock(mutex);
+    if (!done[dev & 63]) {
+        e = cudaFuncSetAttribute(attn_paged_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TlSmem::kBytes);
+        if (e != cudaSuccess) return e;
+        done[dev & 63] = true;
+    }
+    return cudaSuccess;
+}
+
+}  // namespace
+
+cudaError_t launch_attn_paged_tiles(const PagedAttnArgs& a, cudaStream_t st) {
+    cudaError_t e = tile_setup();
+    if (e != cudaSuccess) return e;
+    CUtensorMap tmk, tmv;
+    e = make_page_map(a.c.kp, a.c, kTlTc, &tmk);
+    if (e == cudaSuccess) e = make_page_map(a.c.vp, a.c, kTlTc, &tmv);
+    if (e != cudaSuccess) return e;
+    const long groups = ((long)a.T * (a.Hq / a.c.Hkv) + 2 * kTlRows - 1) / (2 * kTlRows);
+    const long pairs = (long)a.c.S * a.c.Hkv * groups, chunks = (a.c.capacity() + kTlTc - 1) / kTlTc;
+    int W = 1;
+    while (2 * W <= kTlMaxW && pairs * 2 * W <= 152 && 4 * W <= chunks) W *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(W * groups * a.c.Hkv), a.c.S);
+    cfg.blockDim = dim3(kTlThreads);
+    cfg.dynamicSmemBytes = TlSmem::kBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = W;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = W > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, attn_paged_tile_kernel, a, tmk, tmv, W);
+}
+
+}  // namespace m2

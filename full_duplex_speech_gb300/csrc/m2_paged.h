@@ -53,6 +53,8 @@ struct PagedAttnArgs {
 };
 size_t attn_paged_workspace_bytes(const KvCache& c, int T, int Hq, bool bf16);
 cudaError_t launch_attn_paged(const PagedAttnArgs& a, cudaStream_t st);
+// the form for many rows, bf16 (m2_attn_paged_tile.cu)
+cudaError_t launch_attn_paged_tiles(const PagedAttnArgs& a, cudaStream_t st);
 
 #ifdef __CUDACC__
 // A session's positions before the call and its new ones (n_new clamped to
