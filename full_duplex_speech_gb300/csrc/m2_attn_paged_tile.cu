@@ -84,7 +84,7 @@ __device__ __forceinline__ void mma_f8(uint32_t d_tmem, uint64_t adesc, uint64_t
 }
 
 // 32 lanes x 32 consecutive columns: thread t of the warp gets lane base + t.
-__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
+__device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
     uint32_t* r = reinterpret_cast<uint32_t*>(v);
     asm volatile(
         "tcgen05.ld.sync.aligned.32x32b.x32.b32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16,%17,%18,%19,"
@@ -95,6 +95,45 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float (&v)[32]) {
           "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
+__device__ __forceinline__ float max3(float a, float b, float c) {
+    float r;
+    asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
+    return r;
+}
+// pairs of fp32, each rounded as by itself
+__device__ __forceinline__ float2 fma2(float2 a, float2 b, float2 c) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, z, w;\n\t"
+        "mov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\tmov.b64 z, {%6, %7};\n\t"
+        "fma.rn.f32x2 w, x, y, z;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y), "f"(c.x), "f"(c.y));
+    return r;
+}
+__device__ __forceinline__ float2 mul2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "mul.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+__device__ __forceinline__ float2 add2(float2 a, float2 b) {
+    float2 r;
+    asm("{\n\t.reg .b64 x, y, w;\n\tmov.b64 x, {%2, %3};\n\tmov.b64 y, {%4, %5};\n\t"
+        "add.rn.f32x2 w, x, y;\n\tmov.b64 {%0, %1}, w;\n\t}"
+        : "=f"(r.x), "=f"(r.y)
+        : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
+    return r;
+}
+// The warpgroup's registers a thread (multiples of 8): the launch's 168 are
+// split into 72 for the copy, product and conversion warps and 216 for the
+// softmax warps, and even again before they meet.
+template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
+template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+constexpr int kRegsLaunch = 168, kRegsFew = 72, kRegsMany = 216;
+static_assert(128 * kRegsFew + 256 * kRegsMany <= kTlThreads * kRegsLaunch, "the split is covered by the launch's registers");
+
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
         "tcgen05.st.sync.aligned.32x32b.x16.b32 [%0], {%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15,%16};" ::"r"(taddr),
@@ -180,132 +219,137 @@ __global__ void __launch_bounds__(kTlThreads, 1)
     auto warp_ok = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait_ok(bar, parity)); };
 
     float m = kNone, mv = kNone, l = 0.f;  // of a softmax thread's row
-    if (warp == 0) {
-        // ------------------------------------------------------------ copies
-        const int* table = c.table + (size_t)s * c.max_pages;
-        const int pieces = kTlTc >> c.ps_shift;  // pages a chunk (a page holds at most a chunk)
-        const uint32_t page_bytes = (uint32_t)c.ps * kKvD;
-        const int last_page = (total - 1) >> c.ps_shift;
-        int held = -32, page_ids = 0;  // this lane's entry of table[held .. held + 31]
-        for (int j = 0; j < nc; ++j) {
-            const int p0 = (cb + j) * kTlTc, first = p0 >> c.ps_shift;
-            if (held < 0 || first + pieces > held + 32) {
-                held = first;
-                page_ids = first + lane <= last_page ? table[first + lane] : 0;
-                if (page_ids < 0 || page_ids >= c.n_pages) {
-                    atomicOr(c.err, ERR_KV_PAGE);
-                    page_ids = 0;  // some page of the pool: what is read is undefined
+    if (warp < 4) {
+        regs_down<kRegsFew>();
+        if (warp == 0) {
+            // ------------------------------------------------------------ copies
+            const int* table = c.table + (size_t)s * c.max_pages;
+            const int pieces = kTlTc >> c.ps_shift;  // pages a chunk (a page holds at most a chunk)
+            const uint32_t page_bytes = (uint32_t)c.ps * kKvD;
+            const int last_page = (total - 1) >> c.ps_shift;
+            int held = -32, page_ids = 0;  // this lane's entry of table[held .. held + 31]
+            for (int j = 0; j < nc; ++j) {
+                const int p0 = (cb + j) * kTlTc, first = p0 >> c.ps_shift;
+                if (held < 0 || first + pieces > held + 32) {
+                    held = first;
+                    page_ids = first + lane <= last_page ? table[first + lane] : 0;
+                    if (page_ids < 0 || page_ids >= c.n_pages) {
+                        atomicOr(c.err, ERR_KV_PAGE);
+                        page_ids = 0;  // some page of the pool: what is read is undefined
+                    }
+                    __syncwarp();
                 }
+                const int live = min(pieces, last_page - first + 1);
+                const int ks = j % kKStages, vs = j % kVStages, ss = j % kScStages;
+                // lane i < live copies page first + i
+                const int y = (__shfl_sync(0xffffffffu, page_ids, first - held + min(lane, pieces - 1)) * c.Hkv + g) * c.ps;
+                if (j >= kKStages && !warp_ok(kempty + ks, (uint32_t)(j / kKStages - 1) & 1)) break;
+                if (lane == 0) tc::mbar_arrive_expect_tx(kfull + ks, live * page_bytes);
+                __syncwarp();
+                if (lane < live) tc::tma_load_2d(sm + L::kK + ks * kTlTile + lane * page_bytes, &tmk, 0, y, kfull + ks);
+                __syncwarp();
+                if (j >= kScStages && !warp_ok(scempty + ss, (uint32_t)(j / kScStages - 1) & 1)) break;
+                {
+                    const int b = lane & (kTlBlocks - 1), p = p0 + b * kKvBlock;  // lanes 0 .. 7 the keys' scales, 8 .. 15 the values'
+                    const int page = __shfl_sync(0xffffffffu, page_ids, min((p >> c.ps_shift) - held, 31));
+                    if (lane < 2 * kTlBlocks && p < total) {
+                        const size_t at = (((size_t)page * c.Hkv + g) << (c.ps_shift - 4)) + ((p & (c.ps - 1)) >> 4);
+                        cp_async4(scales + ss * 2 * kTlBlocks + lane, (lane < kTlBlocks ? c.ks : c.vs) + at);
+                    }
+                    cp_async_arrive(scfull + ss);
+                }
+                if (j >= kVStages && !warp_ok(vempty + vs, (uint32_t)(j / kVStages - 1) & 1)) break;
+                if (lane == 0) tc::mbar_arrive_expect_tx(vfull + vs, live * page_bytes);
+                __syncwarp();
+                if (lane < live) tc::tma_load_2d(sm + L::kV + vs * kTlTile + lane * page_bytes, &tmv, 0, y, vfull + vs);
                 __syncwarp();
             }
-            const int live = min(pieces, last_page - first + 1);
-            const int ks = j % kKStages, vs = j % kVStages, ss = j % kScStages;
-            // lane i < live copies page first + i
-            const int y = (__shfl_sync(0xffffffffu, page_ids, first - held + min(lane, pieces - 1)) * c.Hkv + g) * c.ps;
-            if (j >= kKStages && !warp_ok(kempty + ks, (uint32_t)(j / kKStages - 1) & 1)) break;
-            if (lane == 0) tc::mbar_arrive_expect_tx(kfull + ks, live * page_bytes);
-            __syncwarp();
-            if (lane < live) tc::tma_load_2d(sm + L::kK + ks * kTlTile + lane * page_bytes, &tmk, 0, y, kfull + ks);
-            __syncwarp();
-            if (j >= kScStages && !warp_ok(scempty + ss, (uint32_t)(j / kScStages - 1) & 1)) break;
-            {
-                const int b = lane & (kTlBlocks - 1), p = p0 + b * kKvBlock;  // lanes 0 .. 7 the keys' scales, 8 .. 15 the values'
-                const int page = __shfl_sync(0xffffffffu, page_ids, min((p >> c.ps_shift) - held, 31));
-                if (lane < 2 * kTlBlocks && p < total) {
-                    const size_t at = (((size_t)page * c.Hkv + g) << (c.ps_shift - 4)) + ((p & (c.ps - 1)) >> 4);
-                    cp_async4(scales + ss * 2 * kTlBlocks + lane, (lane < kTlBlocks ? c.ks : c.vs) + at);
-                }
-                cp_async_arrive(scfull + ss);
-            }
-            if (j >= kVStages && !warp_ok(vempty + vs, (uint32_t)(j / kVStages - 1) & 1)) break;
-            if (lane == 0) tc::mbar_arrive_expect_tx(vfull + vs, live * page_bytes);
-            __syncwarp();
-            if (lane < live) tc::tma_load_2d(sm + L::kV + vs * kTlTile + lane * page_bytes, &tmv, 0, y, vfull + vs);
-            __syncwarp();
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp == 1) {
-        // ---------------------------------------------------------- products
-        const bool leader = tc::elect_one();
-        const uint32_t sbase = tc::smem_u32(sm);
-        const uint32_t id8 = idesc_f8(kTlRows, kTlTc), id16 = idesc_f16_bmn(kTlRows, kKvD);
-        bool good = nc == 0 || warp_ok(qfull, 0);
-        for (int j = 0; j <= nc && good; ++j) {
+            asm volatile("cp.async.wait_all;" ::: "memory");
+        } else if (warp == 1) {
+            // ---------------------------------------------------------- products
+            const bool leader = tc::elect_one();
+            const uint32_t sbase = tc::smem_u32(sm);
+            const uint32_t id8 = idesc_f8(kTlRows, kTlTc), id16 = idesc_f16_bmn(kTlRows, kKvD);
+            bool good = nc == 0 || warp_ok(qfull, 0);
+            for (int j = 0; j <= nc && good; ++j) {
 #pragma unroll
-            for (int i = 0; i < 2; ++i) {
-                const int nci = i ? nc1 : nc0;
-                if (j > 0 && j - 1 < nci) {  // O_i += w V of chunk j - 1
-                    const int h = (j - 1) % kHStages;
-                    good = good && warp_ok(hfull + h, (uint32_t)((j - 1) / kHStages) & 1) && warp_ok(pfull + i, (uint32_t)(j - 1) & 1);
-                    if (!good) break;
-                    tc::tc_fence_after();
-                    if (leader) {
-                        const uint64_t bd = tc::sdesc(sbase + L::kH + h * 2 * kTlTile, 2048, 128, 0);
+                for (int i = 0; i < 2; ++i) {
+                    const int nci = i ? nc1 : nc0;
+                    if (j > 0 && j - 1 < nci) {  // O_i += w V of chunk j - 1
+                        const int h = (j - 1) % kHStages;
+                        good = good && warp_ok(hfull + h, (uint32_t)((j - 1) / kHStages) & 1) && warp_ok(pfull + i, (uint32_t)(j - 1) & 1);
+                        if (!good) break;
+                        tc::tc_fence_after();
+                        if (leader) {
+                            const uint64_t bd = tc::sdesc(sbase + L::kH + h * 2 * kTlTile, 2048, 128, 0);
 #pragma unroll
-                        for (int k = 0; k < 8; ++k)
-                            tc::mma_bf16_tmem_a(tm + kColO + 128 * i, tm + kColS + 128 * i + 8 * k, bd + (uint64_t)(k * 4096 >> 4),
-                                                id16, (j > 1 || k > 0) ? 1u : 0u);
-                        // the last tile that reads this V releases it (tile 1 takes every chunk, where there is one)
-                        if (i == 1 || nc1 == 0) tc::mma_commit(hempty + h);
-                    }
-                    __syncwarp();
-                }
-                if (j < nci) {  // S_i = q_i K^T of chunk j
-                    const int k8 = j % kKStages;
-                    good = good && warp_ok(kfull + k8, (uint32_t)(j / kKStages) & 1);
-                    if (!good) break;
-                    tc::tc_fence_after();
-                    if (leader) {
-                        const uint64_t bd = tc::sdesc(sbase + L::kK + k8 * kTlTile, 0, 1024, 2);
-#pragma unroll
-                        for (int part = 0; part < 2; ++part) {
-                            const uint64_t ad = tc::sdesc(sbase + L::kQ + (2 * i + part) * kTlTile, 0, 1024, 2);
-#pragma unroll
-                            for (int k = 0; k < 4; ++k)
-                                mma_f8(tm + kColS + 128 * i, ad + 2 * k, bd + 2 * k, id8, (part > 0 || k > 0) ? 1u : 0u);
+                            for (int k = 0; k < 8; ++k)
+                                tc::mma_bf16_tmem_a(tm + kColO + 128 * i, tm + kColS + 128 * i + 8 * k, bd + (uint64_t)(k * 4096 >> 4),
+                                                    id16, (j > 1 || k > 0) ? 1u : 0u);
+                            // the last tile that reads this V releases it (tile 1 takes every chunk, where there is one)
+                            if (i == 1 || nc1 == 0) tc::mma_commit(hempty + h);
                         }
-                        tc::mma_commit(sfull + i);
-                        if (i == 1 || nc1 == 0) tc::mma_commit(kempty + k8);
+                        __syncwarp();
                     }
-                    __syncwarp();
+                    if (j < nci) {  // S_i = q_i K^T of chunk j
+                        const int k8 = j % kKStages;
+                        good = good && warp_ok(kfull + k8, (uint32_t)(j / kKStages) & 1);
+                        if (!good) break;
+                        tc::tc_fence_after();
+                        if (leader) {
+                            const uint64_t bd = tc::sdesc(sbase + L::kK + k8 * kTlTile, 0, 1024, 2);
+#pragma unroll
+                            for (int part = 0; part < 2; ++part) {
+                                const uint64_t ad = tc::sdesc(sbase + L::kQ + (2 * i + part) * kTlTile, 0, 1024, 2);
+#pragma unroll
+                                for (int k = 0; k < 4; ++k)
+                                    mma_f8(tm + kColS + 128 * i, ad + 2 * k, bd + 2 * k, id8, (part > 0 || k > 0) ? 1u : 0u);
+                            }
+                            tc::mma_commit(sfull + i);
+                            if (i == 1 || nc1 == 0) tc::mma_commit(kempty + k8);
+                        }
+                        __syncwarp();
+                    }
                 }
             }
-        }
-        if (leader && good) tc::mma_commit(ofull);
-        __syncwarp();
-    } else if (warp < 4) {
-        // -------------------------------------------- V to fp16, 64 threads
-        const int ct = tid - 64, k7 = ct & 7, sub = ct >> 3;  // position within 8; one of 8 (position group, unit) pairs
-        for (int j = 0; j < nc; ++j) {
-            const int vs = j % kVStages, h = j % kHStages;
-            if (!warp_ok(vfull + vs, (uint32_t)(j / kVStages) & 1)) break;
-            if (j >= kHStages && !warp_ok(hempty + h, (uint32_t)(j / kHStages - 1) & 1)) break;
-            const uint8_t* src = sm + L::kV + vs * kTlTile;
-            uint8_t* dst = sm + L::kH + h * 2 * kTlTile;
-            const int left = total - (cb + j) * kTlTc;  // positions behind the last count as zero values
-            // thread: position 8 pg + k7, dims 16 sub .. + 15 (16 codes, swizzled) -> two 16-byte
-            // pieces of the 8 x 8 blocks of the product's MN-major operand
+            if (leader && good) tc::mma_commit(ofull);
+        } else {
+            // -------------------------------------------- V to fp16, 64 threads
+            const int ct = tid - 64, k7 = ct & 7, sub = ct >> 3;  // position within 8; one of 8 (position group, unit) pairs
+            for (int j = 0; j < nc; ++j) {
+                const int vs = j % kVStages, h = j % kHStages;
+                if (!warp_ok(vfull + vs, (uint32_t)(j / kVStages) & 1)) break;
+                if (j >= kHStages && !warp_ok(hempty + h, (uint32_t)(j / kHStages - 1) & 1)) break;
+                const uint8_t* src = sm + L::kV + vs * kTlTile;
+                uint8_t* dst = sm + L::kH + h * 2 * kTlTile;
+                const int left = total - (cb + j) * kTlTc;  // positions behind the last count as zero values
+                // thread: position 8 pg + k7, dims 16 sub .. + 15 (16 codes, swizzled) -> two 16-byte
+                // pieces of the 8 x 8 blocks of the product's MN-major operand
 #pragma unroll 4
-            for (int pg = 0; pg < kTlTc / 8; ++pg) {
-                const int p = 8 * pg + k7;
-                uint4 w = *reinterpret_cast<const uint4*>(src + p * kKvD + ((sub ^ k7) << 4));
-                if (p >= left) w = make_uint4(0u, 0u, 0u, 0u);
-                uint4 lo, hi;
-                lo.x = e4m3x2_to_f16x2(w.x & 0xFFFFu), lo.y = e4m3x2_to_f16x2(w.x >> 16);
-                lo.z = e4m3x2_to_f16x2(w.y & 0xFFFFu), lo.w = e4m3x2_to_f16x2(w.y >> 16);
-                hi.x = e4m3x2_to_f16x2(w.z & 0xFFFFu), hi.y = e4m3x2_to_f16x2(w.z >> 16);
-                hi.z = e4m3x2_to_f16x2(w.w & 0xFFFFu), hi.w = e4m3x2_to_f16x2(w.w >> 16);
-                uint8_t* o = dst + pg * 2048 + sub * 256 + k7 * 16;
-                *reinterpret_cast<uint4*>(o) = lo;
-                *reinterpret_cast<uint4*>(o + 128) = hi;
+                for (int pg = 0; pg < kTlTc / 8; ++pg) {
+                    const int p = 8 * pg + k7;
+                    uint4 w = *reinterpret_cast<const uint4*>(src + p * kKvD + ((sub ^ k7) << 4));
+                    if (p >= left) w = make_uint4(0u, 0u, 0u, 0u);
+                    uint4 lo, hi;
+                    lo.x = e4m3x2_to_f16x2(w.x & 0xFFFFu), lo.y = e4m3x2_to_f16x2(w.x >> 16);
+                    lo.z = e4m3x2_to_f16x2(w.y & 0xFFFFu), lo.w = e4m3x2_to_f16x2(w.y >> 16);
+                    hi.x = e4m3x2_to_f16x2(w.z & 0xFFFFu), hi.y = e4m3x2_to_f16x2(w.z >> 16);
+                    hi.z = e4m3x2_to_f16x2(w.w & 0xFFFFu), hi.w = e4m3x2_to_f16x2(w.w >> 16);
+                    uint8_t* o = dst + pg * 2048 + sub * 256 + k7 * 16;
+                    *reinterpret_cast<uint4*>(o) = lo;
+                    *reinterpret_cast<uint4*>(o + 128) = hi;
+                }
+                tc::fence_proxy_async_smem();
+                tc::mbar_arrive(hfull + h);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(vempty + vs);
             }
-            tc::fence_proxy_async_smem();
-            tc::mbar_arrive(hfull + h);
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(vempty + vs);
         }
+        __syncwarp();
+        regs_up<kRegsLaunch>();
     } else {
         // ------------------------------------------ softmax, one row a thread
+        regs_up<kRegsMany>();
         const int i = (warp - 4) >> 2, r = tid - 128 - 128 * i, row = 128 * i + r;  // tile, row of it, row of the pair
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tm + lanes + kColS + 128 * i, tO = tm + lanes + kColO + 128 * i;
@@ -358,6 +402,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
             tc::fence_proxy_async_smem();
             tc::mbar_arrive(qfull);
         }
+        float2 l0 = make_float2(0.f, 0.f), l1 = l0;  // the row's sum, in four parts
         const int lim = !live || !ok ? -1 : a.causal ? before + (row0 + row) / R : before - 1;  // the last position seen
         const int nci = i ? nc1 : nc0;
         for (int j = 0; j < nc; ++j) {
@@ -369,72 +414,74 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                 const float* sk = scales + ss * 2 * kTlBlocks;
                 const int see = lim - (cb + j) * kTlTc;  // columns 0 .. see are seen
                 const bool cut = __any_sync(0xffffffffu, see < kTlTc - 1);
-                float v[32];
+                float v[kTlTc];
+#pragma unroll
+                for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, v + 32 * q);
+                tc::tmem_wait_ld();
+                if (cut) {
+#pragma unroll
+                    for (int k = 0; k < kTlTc; ++k) v[k] = k <= see ? v[k] : -INFINITY;
+                }
                 // the chunk's maxima: of x, and of x + log2 vs
                 float mx = -INFINITY, mvx = -INFINITY;
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    tmem_ld32(tS + 32 * q, v);
-                    tc::tmem_wait_ld();
-                    if (cut)
-#pragma unroll
-                        for (int k = 0; k < 32; ++k) v[k] = 32 * q + k <= see ? v[k] : -INFINITY;
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        float t = v[16 * b];
-#pragma unroll
-                        for (int k = 1; k < 16; ++k) t = fmaxf(t, v[16 * b + k]);
-                        const float x = 32 * q + 16 * b <= see ? t * (cs * sk[2 * q + b]) : -INFINITY;
-                        mx = fmaxf(mx, x);
-                        mvx = fmaxf(mvx, x + lg2_approx(sk[kTlBlocks + 2 * q + b]));
-                    }
+                for (int b = 0; b < kTlBlocks; ++b) {
+                    const float* w = v + 16 * b;
+                    const float t = max3(max3(max3(w[0], w[1], w[2]), max3(w[3], w[4], w[5]), max3(w[6], w[7], w[8])),
+                                         max3(w[9], w[10], w[11]), max3(fmaxf(w[12], w[13]), w[14], w[15]));
+                    const float x = 16 * b <= see ? t * (cs * sk[b]) : -INFINITY;
+                    mx = fmaxf(mx, x);
+                    mvx = fmaxf(mvx, x + lg2_approx(sk[kTlBlocks + b]));
                 }
                 if (mx > m + kSlack) {
-                    l *= ex2_approx(m - mx);
+                    const float f = ex2_approx(m - mx);
+                    l0.x *= f, l0.y *= f, l1.x *= f, l1.y *= f;
                     m = mx;
                 }
                 const bool grow = mvx > mv + kSlack;
                 const float f = grow ? ex2_approx(mv - mvx) : 1.f;
                 if (grow) mv = mvx;
                 if (j > 0 && __any_sync(0xffffffffu, grow)) {  // O is idle: its products came before S
-#pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        tmem_ld32(tO + 32 * q, v);
+#pragma unroll 1
+                    for (int q = 0; q < 8; ++q) {
+                        float o[16];
+                        tc::tmem_ld16(tO + 16 * q, o);
                         tc::tmem_wait_ld();
-                        uint32_t y[2][16];
+                        uint32_t y[16];
 #pragma unroll
-                        for (int k = 0; k < 32; ++k) y[k >> 4][k & 15] = __float_as_uint(v[k] * f);
-                        tmem_st16(tO + 32 * q, y[0]);
-                        tmem_st16(tO + 32 * q + 16, y[1]);
+                        for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(o[k] * f);
+                        tmem_st16(tO + 16 * q, y);
                     }
                 }
                 const float lift = ex2_approx(m - mv + kLift);
+                const float2 nm = make_float2(-m, -m);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    tmem_ld32(tS + 32 * q, v);
-                    tc::tmem_wait_ld();
                     uint32_t y[16];
 #pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const bool any = 32 * q + 16 * b <= see;
-                        const float cx = any ? cs * sk[2 * q + b] : 1.f;
-                        const float vsb = sk[kTlBlocks + 2 * q + b];
+                    for (int h = 0; h < 2; ++h) {
+                        const int b = 2 * q + h;
+                        const bool any = 16 * b <= see;
+                        const float cx = any ? cs * sk[b] : 1.f, vsb = sk[kTlBlocks + b];
                         const float to = !any || vsb == 0.f ? 0.f : vsb * lift;
-                        float sum = 0.f;
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) v[16 * b + k] = fmaf(v[16 * b + k], cx, -m);
-                        if (cut)
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) v[16 * b + k] = 32 * q + 16 * b + k <= see ? v[16 * b + k] : -INFINITY;
-#pragma unroll
-                        for (int k = 0; k < 16; k += 2) {
-                            const float p0 = ex2_approx(v[16 * b + k]), p1 = ex2_approx(v[16 * b + k + 1]);
-                            sum += p0 + p1;
-                            y[8 * b + (k >> 1)] = pack_f16x2(p0 * to, p1 * to);
+                        for (int k = 0; k < 8; ++k) {
+                            const int at = 16 * b + 2 * k;
+                            float2 x = fma2(make_float2(v[at], v[at + 1]), make_float2(cx, cx), nm);
+                            if (cut) {
+                                x.x = at <= see ? x.x : -INFINITY;
+                                x.y = at + 1 <= see ? x.y : -INFINITY;
+                            }
+                            const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                            if (k & 1)
+                                l1 = add2(l1, p);
+                            else
+                                l0 = add2(l0, p);
+                            const float2 w = mul2(p, make_float2(to, to));
+                            y[8 * h + k] = pack_f16x2(w.x, w.y);
                         }
-                        l += sum;
                     }
-                    tmem_st16(tS + 16 * q, y);  // over columns of S that are read already
+                    tmem_st16(tS + 16 * q, y);  // over S, which is read
                 }
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
@@ -443,6 +490,9 @@ __global__ void __launch_bounds__(kTlThreads, 1)
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(scempty + ss);
         }
+        l = (l0.x + l0.y) + (l1.x + l1.y);
+        __syncwarp();
+        regs_down<kRegsLaunch>();
     }
     // ------------------------------------------------------------- the merge
     __syncwarp();
@@ -557,6 +607,11 @@ cudaError_t tile_setup() {
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mutex);
     if (!done[dev & 63]) {
+        // the warps' register split draws on what the launch gives
+        cudaFuncAttributes fa;
+        e = cudaFuncGetAttributes(&fa, attn_paged_tile_kernel);
+        if (e != cudaSuccess) return e;
+        if (fa.numRegs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
         e = cudaFuncSetAttribute(attn_paged_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TlSmem::kBytes);
         if (e != cudaSuccess) return e;
         done[dev & 63] = true;
