@@ -29,6 +29,7 @@
 // share the positions of one pair of tiles and merge through distributed
 // shared memory, each the owner of 256 / W rows.
 #include <cuda_fp8.h>
+#include <float.h>
 
 #include <mutex>
 
@@ -209,6 +210,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
 
     // A bounded wait; the first that runs out stops the CTA's work.
     auto wait_ok = [&](uint64_t* bar, uint32_t parity) -> bool {
+        if (tc::mbar_try_wait(bar, parity)) return true;
         if (*flag) return false;
         if (tc::mbar_wait(bar, parity)) return true;
         atomicOr(c.err, ERR_MBAR_TIMEOUT_MMA);
@@ -267,36 +269,32 @@ __global__ void __launch_bounds__(kTlThreads, 1)
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (warp == 1) {
             // ---------------------------------------------------------- products
-            const bool leader = tc::elect_one();
-            const uint32_t sbase = tc::smem_u32(sm);
-            const uint32_t id8 = idesc_f8(kTlRows, kTlTc), id16 = idesc_f16_bmn(kTlRows, kKvD);
-            bool good = nc == 0 || warp_ok(qfull, 0);
-            for (int j = 0; j <= nc && good; ++j) {
+            if (tc::elect_one()) {
+                const uint32_t sbase = tc::smem_u32(sm);
+                const uint32_t id8 = idesc_f8(kTlRows, kTlTc), id16 = idesc_f16_bmn(kTlRows, kKvD);
+                bool good = nc == 0 || wait_ok(qfull, 0);
+                for (int j = 0; j <= nc && good; ++j) {
+                    // the operands from memory first: what the loop then waits for is the softmax alone
+                    const int h = (j + kHStages - 1) % kHStages, k8 = j % kKStages;
+                    if (j < nc) good = good && wait_ok(kfull + k8, (uint32_t)(j / kKStages) & 1);
+                    if (j > 0) good = good && wait_ok(hfull + h, (uint32_t)((j - 1) / kHStages) & 1);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int nci = i ? nc1 : nc0;
-                    if (j > 0 && j - 1 < nci) {  // O_i += w V of chunk j - 1
-                        const int h = (j - 1) % kHStages;
-                        good = good && warp_ok(hfull + h, (uint32_t)((j - 1) / kHStages) & 1) && warp_ok(pfull + i, (uint32_t)(j - 1) & 1);
-                        if (!good) break;
-                        tc::tc_fence_after();
-                        if (leader) {
+                    for (int i = 0; i < 2; ++i) {
+                        const int nci = i ? nc1 : nc0;
+                        if (j > 0 && j - 1 < nci) {  // O_i += w V of chunk j - 1
+                            good = good && wait_ok(pfull + i, (uint32_t)(j - 1) & 1);
+                            if (!good) break;
+                            tc::tc_fence_after();
                             const uint64_t bd = tc::sdesc(sbase + L::kH + h * 2 * kTlTile, 2048, 128, 0);
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
-                                tc::mma_bf16_tmem_a(tm + kColO + 128 * i, tm + kColS + 128 * i + 8 * k, bd + (uint64_t)(k * 4096 >> 4),
-                                                    id16, (j > 1 || k > 0) ? 1u : 0u);
+                                tc::mma_bf16_tmem_a(tm + kColO + 128 * i, tm + kColS + 128 * i + 8 * k,
+                                                    bd + (uint64_t)(k * 4096 >> 4), id16, (j > 1 || k > 0) ? 1u : 0u);
                             // the last tile that reads this V releases it (tile 1 takes every chunk, where there is one)
                             if (i == 1 || nc1 == 0) tc::mma_commit(hempty + h);
                         }
-                        __syncwarp();
-                    }
-                    if (j < nci) {  // S_i = q_i K^T of chunk j
-                        const int k8 = j % kKStages;
-                        good = good && warp_ok(kfull + k8, (uint32_t)(j / kKStages) & 1);
-                        if (!good) break;
-                        tc::tc_fence_after();
-                        if (leader) {
+                        if (j < nci) {  // S_i = q_i K^T of chunk j
+                            tc::tc_fence_after();
                             const uint64_t bd = tc::sdesc(sbase + L::kK + k8 * kTlTile, 0, 1024, 2);
 #pragma unroll
                             for (int part = 0; part < 2; ++part) {
@@ -308,11 +306,10 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                             tc::mma_commit(sfull + i);
                             if (i == 1 || nc1 == 0) tc::mma_commit(kempty + k8);
                         }
-                        __syncwarp();
                     }
                 }
+                if (good) tc::mma_commit(ofull);
             }
-            if (leader && good) tc::mma_commit(ofull);
         } else {
             // -------------------------------------------- V to fp16, 64 threads
             const int ct = tid - 64, k7 = ct & 7, sub = ct >> 3;  // position within 8; one of 8 (position group, unit) pairs
@@ -409,18 +406,36 @@ __global__ void __launch_bounds__(kTlThreads, 1)
             const int ss = j % kScStages;
             if (!warp_ok(scfull + ss, (uint32_t)(j / kScStages) & 1)) break;
             if (j < nci) {
+                // the chunk's scales: of the scores (with the softmax factor), and of the values
+                float cxs[kTlBlocks], vss[kTlBlocks], lvs[kTlBlocks];
+                {
+                    const float4* sk = reinterpret_cast<const float4*>(scales + ss * 2 * kTlBlocks);
+#pragma unroll
+                    for (int b = 0; b < kTlBlocks / 4; ++b) {
+                        const float4 x = sk[b], y = sk[kTlBlocks / 4 + b];
+                        cxs[4 * b] = cs * x.x, cxs[4 * b + 1] = cs * x.y, cxs[4 * b + 2] = cs * x.z, cxs[4 * b + 3] = cs * x.w;
+                        vss[4 * b] = y.x, vss[4 * b + 1] = y.y, vss[4 * b + 2] = y.z, vss[4 * b + 3] = y.w;
+                    }
+#pragma unroll
+                    for (int b = 0; b < kTlBlocks; ++b) {
+                        lvs[b] = lg2_approx(vss[b]);
+                        cxs[b] = cxs[b] < FLT_MIN ? FLT_MIN : cxs[b];  // not 0: hidden scores are -inf
+                    }
+                }
                 if (!warp_ok(sfull + i, (uint32_t)j & 1)) break;
                 tc::tc_fence_after();
-                const float* sk = scales + ss * 2 * kTlBlocks;
                 const int see = lim - (cb + j) * kTlTc;  // columns 0 .. see are seen
                 const bool cut = __any_sync(0xffffffffu, see < kTlTc - 1);
                 float v[kTlTc];
 #pragma unroll
                 for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, v + 32 * q);
                 tc::tmem_wait_ld();
-                if (cut) {
+                if (cut) {  // the factors of a block that the row does not see may be anything
 #pragma unroll
                     for (int k = 0; k < kTlTc; ++k) v[k] = k <= see ? v[k] : -INFINITY;
+#pragma unroll
+                    for (int b = 0; b < kTlBlocks; ++b)
+                        if (16 * b > see) cxs[b] = 1.f, vss[b] = 0.f, lvs[b] = -INFINITY;
                 }
                 // the chunk's maxima: of x, and of x + log2 vs
                 float mx = -INFINITY, mvx = -INFINITY;
@@ -429,9 +444,9 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                     const float* w = v + 16 * b;
                     const float t = max3(max3(max3(w[0], w[1], w[2]), max3(w[3], w[4], w[5]), max3(w[6], w[7], w[8])),
                                          max3(w[9], w[10], w[11]), max3(fmaxf(w[12], w[13]), w[14], w[15]));
-                    const float x = 16 * b <= see ? t * (cs * sk[b]) : -INFINITY;
+                    const float x = t * cxs[b];
                     mx = fmaxf(mx, x);
-                    mvx = fmaxf(mvx, x + lg2_approx(sk[kTlBlocks + b]));
+                    mvx = fmaxf(mvx, x + lvs[b]);
                 }
                 if (mx > m + kSlack) {
                     const float f = ex2_approx(m - mx);
@@ -453,7 +468,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                         tmem_st16(tO + 16 * q, y);
                     }
                 }
-                const float lift = ex2_approx(m - mv + kLift);
+                const float lift = fminf(ex2_approx(m - mv + kLift), FLT_MAX);  // (finite: a block of scale 0 weighs 0)
                 const float2 nm = make_float2(-m, -m);
 #pragma unroll
                 for (int q = 0; q < 4; ++q) {
@@ -461,17 +476,11 @@ __global__ void __launch_bounds__(kTlThreads, 1)
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
                         const int b = 2 * q + h;
-                        const bool any = 16 * b <= see;
-                        const float cx = any ? cs * sk[b] : 1.f, vsb = sk[kTlBlocks + b];
-                        const float to = !any || vsb == 0.f ? 0.f : vsb * lift;
+                        const float cx = cxs[b], to = vss[b] * lift;
 #pragma unroll
                         for (int k = 0; k < 8; ++k) {
                             const int at = 16 * b + 2 * k;
-                            float2 x = fma2(make_float2(v[at], v[at + 1]), make_float2(cx, cx), nm);
-                            if (cut) {
-                                x.x = at <= see ? x.x : -INFINITY;
-                                x.y = at + 1 <= see ? x.y : -INFINITY;
-                            }
+                            const float2 x = fma2(make_float2(v[at], v[at + 1]), make_float2(cx, cx), nm);
                             const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
                             if (k & 1)
                                 l1 = add2(l1, p);
