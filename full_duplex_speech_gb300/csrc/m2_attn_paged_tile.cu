@@ -14,13 +14,13 @@
 //                   conversion of the keys;
 //   softmax         one thread a row, S read out of tensor memory in fp32:
 //                   x = S (scale ks), p = 2^(x - m), l += p, and the weight
-//                   w = p vs 2^(m - mv + 7) to fp16 (2^-11) over S;
+//                   w = p vs 2^(m - mv + 3) to fp16 (2^-11) over S;
 //   O += w V        kind::f16, w from tensor memory, V converted to fp16
 //                   (exactly) by two warps.
 // m and mv (the reference of the weights, a maximum of x + log2 vs) move only
-// when a chunk exceeds them by more than 2^8, which p <= 2^8 in fp32 and
+// when a chunk exceeds them by more than 2^12, which p <= 2^12 in fp32 and
 // w <= 2^15 in fp16 allow; only then is O rescaled in tensor memory.
-//     out = 2^(mv - m - 7) O / l.
+//     out = 2^(mv - m - 3) O / l.
 //
 // Warps: 0 copies (pages by TMA through rings, scales by 4-byte asynchronous
 // copies), 1 issues the products, 2 and 3 convert V, 4-7 and 8-11 the
@@ -45,8 +45,8 @@ constexpr int kTlTc = 128;                         // positions per chunk
 constexpr int kTlBlocks = kTlTc / kKvBlock;        // scales of a chunk
 constexpr uint32_t kTlTile = kTlTc * kKvD;         // 16 KB of codes
 constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kScStages = 4;
-constexpr float kSlack = 8.f;                      // log2 by which a chunk may exceed the references
-constexpr float kLift = 7.f;                       // log2 of the weights' reference: 2^(7 + 8) at most
+constexpr float kSlack = 12.f;                     // log2 by which a chunk may exceed the references
+constexpr float kLift = 3.f;                       // log2 of the weights' reference: 2^(3 + 12) at most
 constexpr uint32_t kColO = 0, kColS = 256;         // tensor memory: O of the two tiles, then S (and w over it)
 constexpr int kTlMaxW = 8;
 
@@ -132,6 +132,9 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // softmax warps, and even again before they meet.
 template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+// The softmax warps give back before anyone takes: a warp that is done early
+// must not take what they still wait for.
+__device__ __forceinline__ void all_done() { asm volatile("barrier.sync 1, %0;" ::"n"(kTlThreads) : "memory"); }
 constexpr int kRegsLaunch = 168, kRegsFew = 72, kRegsMany = 216;
 static_assert(128 * kRegsFew + 256 * kRegsMany <= kTlThreads * kRegsLaunch, "the split is covered by the launch's registers");
 
@@ -190,9 +193,9 @@ __global__ void __launch_bounds__(kTlThreads, 1)
     if (tid == 0) {
         for (int i = 0; i < kKStages; ++i) tc::mbar_init(kfull + i, 1), tc::mbar_init(kempty + i, 1);
         for (int i = 0; i < kVStages; ++i) tc::mbar_init(vfull + i, 1), tc::mbar_init(vempty + i, 2);
-        for (int i = 0; i < kHStages; ++i) tc::mbar_init(hfull + i, 64), tc::mbar_init(hempty + i, 1);
+        for (int i = 0; i < kHStages; ++i) tc::mbar_init(hfull + i, 2), tc::mbar_init(hempty + i, 1);
         for (int i = 0; i < kScStages; ++i) tc::mbar_init(scfull + i, 32), tc::mbar_init(scempty + i, 8);
-        for (int i = 0; i < 2; ++i) tc::mbar_init(sfull + i, 1), tc::mbar_init(pfull + i, kTlRows);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(sfull + i, 1), tc::mbar_init(pfull + i, 4);
         tc::mbar_init(qfull, 2 * kTlRows);
         tc::mbar_init(ofull, 1);
         tc::mbar_init(endbar, 1);
@@ -312,7 +315,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
             }
         } else {
             // -------------------------------------------- V to fp16, 64 threads
-            const int ct = tid - 64, k7 = ct & 7, sub = ct >> 3;  // position within 8; one of 8 (position group, unit) pairs
+            const int ct = tid - 64, k7 = ct & 7, sub = ct >> 3;
             for (int j = 0; j < nc; ++j) {
                 const int vs = j % kVStages, h = j % kHStages;
                 if (!warp_ok(vfull + vs, (uint32_t)(j / kVStages) & 1)) break;
@@ -320,7 +323,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                 const uint8_t* src = sm + L::kV + vs * kTlTile;
                 uint8_t* dst = sm + L::kH + h * 2 * kTlTile;
                 const int left = total - (cb + j) * kTlTc;  // positions behind the last count as zero values
-                // thread: position 8 pg + k7, dims 16 sub .. + 15 (16 codes, swizzled) -> two 16-byte
+                // thread: positions 8 pg + k7, dims 16 sub .. + 15 (16 codes, swizzled) -> two 16-byte
                 // pieces of the 8 x 8 blocks of the product's MN-major operand
 #pragma unroll 4
                 for (int pg = 0; pg < kTlTc / 8; ++pg) {
@@ -337,12 +340,12 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                     *reinterpret_cast<uint4*>(o + 128) = hi;
                 }
                 tc::fence_proxy_async_smem();
-                tc::mbar_arrive(hfull + h);
                 __syncwarp();
-                if (lane == 0) tc::mbar_arrive(vempty + vs);
+                if (lane == 0) tc::mbar_arrive(hfull + h), tc::mbar_arrive(vempty + vs);
             }
         }
         __syncwarp();
+        all_done();
         regs_up<kRegsLaunch>();
     } else {
         // ------------------------------------------ softmax, one row a thread
@@ -458,14 +461,18 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                 if (grow) mv = mvx;
                 if (j > 0 && __any_sync(0xffffffffu, grow)) {  // O is idle: its products came before S
 #pragma unroll 1
-                    for (int q = 0; q < 8; ++q) {
-                        float o[16];
-                        tc::tmem_ld16(tO + 16 * q, o);
+                    for (int q = 0; q < 4; ++q) {
+                        float o[2][16];
+                        tc::tmem_ld16(tO + 32 * q, o[0]);
+                        tc::tmem_ld16(tO + 32 * q + 16, o[1]);
                         tc::tmem_wait_ld();
-                        uint32_t y[16];
 #pragma unroll
-                        for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(o[k] * f);
-                        tmem_st16(tO + 16 * q, y);
+                        for (int h = 0; h < 2; ++h) {
+                            uint32_t y[16];
+#pragma unroll
+                            for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(o[h][k] * f);
+                            tmem_st16(tO + 32 * q + 16 * h, y);
+                        }
                     }
                 }
                 const float lift = fminf(ex2_approx(m - mv + kLift), FLT_MAX);  // (finite: a block of scale 0 weighs 0)
@@ -494,7 +501,8 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                 }
                 tc::tmem_wait_st();
                 tc::tc_fence_before();
-                tc::mbar_arrive(pfull + i);
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(pfull + i);
             }
             __syncwarp();
             if (lane == 0) tc::mbar_arrive(scempty + ss);
@@ -502,6 +510,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
         l = (l0.x + l0.y) + (l1.x + l1.y);
         __syncwarp();
         regs_down<kRegsLaunch>();
+        all_done();
     }
     // ------------------------------------------------------------- the merge
     __syncwarp();
@@ -578,7 +587,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
     tc::cluster_arrive();  // the stores into the owners' memory are visible ...
     tc::cluster_wait();    // ... once every CTA has made them
     // this CTA's rows, a warp a row, four dims a lane:
-    // out = 2^(V - M - 7) sum_w 2^(mv_w - V) O_w / sum_w 2^(m_w - M) l_w
+    // out = 2^(V - M - 3) sum_w 2^(mv_w - V) O_w / sum_w 2^(m_w - M) l_w
     const float4* ml = reinterpret_cast<const float4*>(sm + L::kMl);
     for (int r = warp; r < own; r += kTlThreads / 32) {
         const int row = wk * own + r;
