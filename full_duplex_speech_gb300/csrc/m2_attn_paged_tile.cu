@@ -16,16 +16,18 @@
 //                   x = S (scale ks), p = 2^(x - m), l += p, and the weight
 //                   w = p vs 2^(m - mv + 3) to fp16 (2^-11) over S;
 //   O += w V        kind::f16, w from tensor memory, V converted to fp16
-//                   (exactly) by two warps.
+//                   (exactly) by four warps.
 // m and mv (the reference of the weights, a maximum of x + log2 vs) move only
 // when a chunk exceeds them by more than 2^12, which p <= 2^12 in fp32 and
 // w <= 2^15 in fp16 allow; only then is O rescaled in tensor memory.
 //     out = 2^(mv - m - 3) O / l.
 //
 // Warps: 0 copies (pages by TMA through rings, scales by 4-byte asynchronous
-// copies), 1 issues the products, 2 and 3 convert V, 4-7 and 8-11 the
-// softmax of tile 0 and of tile 1. The products of one tile run under the
-// other's softmax. Where few CTAs would leave SMs idle, W CTAs of a cluster
+// copies), 1 issues the products, 2 waits for their operands, 4-7 convert V,
+// 8-11 and 12-15 the softmax of the tiles. One warp issues for both tiles, in
+// turn: two of their own let the tiles fall into step, both in the softmax
+// and then both in the products (716 us against 665 at 4 x 4096 positions).
+// The products of one tile run under the other's softmax. Where few CTAs would leave SMs idle, W CTAs of a cluster
 // share the positions of one pair of tiles and merge through distributed
 // shared memory, each the owner of 256 / W rows.
 #include <cuda_fp8.h>
@@ -39,12 +41,12 @@ namespace m2 {
 
 namespace {
 
-constexpr int kTlThreads = 384;
+constexpr int kTlThreads = 512;
 constexpr int kTlRows = 128;                       // rows of a tile
 constexpr int kTlTc = 128;                         // positions per chunk
 constexpr int kTlBlocks = kTlTc / kKvBlock;        // scales of a chunk
 constexpr uint32_t kTlTile = kTlTc * kKvD;         // 16 KB of codes
-constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kScStages = 4;
+constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kScStages = kKStages + 1;
 constexpr float kSlack = 12.f;                     // log2 by which a chunk may exceed the references
 constexpr float kLift = 3.f;                       // log2 of the weights' reference: 2^(3 + 12) at most
 constexpr uint32_t kColO = 0, kColS = 256;         // tensor memory: O of the two tiles, then S (and w over it)
@@ -57,8 +59,8 @@ struct TlSmem {
     static constexpr uint32_t kH = kV + kVStages * kTlTile;              // V in fp16, kHStages x 32 KB, MN-major
     static constexpr uint32_t kSc = kH + kHStages * 2 * kTlTile;         // float [stage][ks 8, vs 8]
     static constexpr uint32_t kBar = kSc + kScStages * 2 * kTlBlocks * 4;
-    // kfull, kempty, vfull, vempty, hfull, hempty, scfull, scempty, sfull[2], pfull[2], qfull, ofull, end
-    static constexpr int kBars = 2 * (kKStages + kVStages + kHStages + kScStages) + 7;
+    // kfull, kempty, vfull, vempty, hfull, hempty, scfull, sfull[2], ofull[2], end
+    static constexpr int kBars = 2 * (kKStages + kVStages + kHStages) + kScStages + 5;
     static constexpr uint32_t kTmem = kBar + kBars * 8;
     static constexpr uint32_t kFlag = kTmem + 4;
     static constexpr uint32_t kBytes = kFlag + 4 + 1024;  // + slack to align to 1024
@@ -127,16 +129,24 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
         : "f"(a.x), "f"(a.y), "f"(b.x), "f"(b.y));
     return r;
 }
-// The warpgroup's registers a thread (multiples of 8): the launch's 168 are
-// split into 72 for the copy, product and conversion warps and 216 for the
+// The warpgroup's registers a thread (multiples of 8): the launch's 128 are
+// split into 56 for the copy, product and conversion warps and 200 for the
 // softmax warps, and even again before they meet.
 template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
+// A tile's four softmax warps, and the warp that has seen the operands from
+// memory, hand over to the warp that issues the products: a hardware barrier,
+// since a look at one in shared memory takes some 200 cycles beside the
+// products' own traffic. Every warp makes every meeting, also after a wait
+// that gave up (what the products then read is there, if not what it should
+// be, and the CTA's results are dropped).
+__device__ __forceinline__ void tile_arrive(int i) { asm volatile("barrier.arrive %0, 192;" ::"r"(2 + i) : "memory"); }
+__device__ __forceinline__ void tile_sync(int i) { asm volatile("barrier.sync %0, 192;" ::"r"(2 + i) : "memory"); }
 // The softmax warps give back before anyone takes: a warp that is done early
 // must not take what they still wait for.
 __device__ __forceinline__ void all_done() { asm volatile("barrier.sync 1, %0;" ::"n"(kTlThreads) : "memory"); }
-constexpr int kRegsLaunch = 168, kRegsFew = 72, kRegsMany = 216;
-static_assert(128 * kRegsFew + 256 * kRegsMany <= kTlThreads * kRegsLaunch, "the split is covered by the launch's registers");
+constexpr int kRegsLaunch = 128, kRegsFew = 56, kRegsMany = 200;
+static_assert(256 * kRegsFew + 256 * kRegsMany <= kTlThreads * kRegsLaunch, "the split is covered by the launch's registers");
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
     asm volatile(
@@ -160,8 +170,8 @@ __global__ void __launch_bounds__(kTlThreads, 1)
     float* scales = reinterpret_cast<float*>(sm + L::kSc);
     uint64_t* kfull = reinterpret_cast<uint64_t*>(sm + L::kBar);
     uint64_t *kempty = kfull + kKStages, *vfull = kempty + kKStages, *vempty = vfull + kVStages, *hfull = vempty + kVStages,
-             *hempty = hfull + kHStages, *scfull = hempty + kHStages, *scempty = scfull + kScStages,
-             *sfull = scempty + kScStages, *pfull = sfull + 2, *qfull = pfull + 2, *ofull = qfull + 1, *endbar = ofull + 1;
+             *hempty = hfull + kHStages, *scfull = hempty + kHStages,
+             *sfull = scfull + kScStages, *ofull = sfull + 2, *endbar = ofull + 2;
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + L::kTmem);
     volatile uint32_t* flag = reinterpret_cast<uint32_t*>(sm + L::kFlag);
     const KvCache& c = a.c;
@@ -192,12 +202,10 @@ __global__ void __launch_bounds__(kTlThreads, 1)
 
     if (tid == 0) {
         for (int i = 0; i < kKStages; ++i) tc::mbar_init(kfull + i, 1), tc::mbar_init(kempty + i, 1);
-        for (int i = 0; i < kVStages; ++i) tc::mbar_init(vfull + i, 1), tc::mbar_init(vempty + i, 2);
-        for (int i = 0; i < kHStages; ++i) tc::mbar_init(hfull + i, 2), tc::mbar_init(hempty + i, 1);
-        for (int i = 0; i < kScStages; ++i) tc::mbar_init(scfull + i, 32), tc::mbar_init(scempty + i, 8);
-        for (int i = 0; i < 2; ++i) tc::mbar_init(sfull + i, 1), tc::mbar_init(pfull + i, 4);
-        tc::mbar_init(qfull, 2 * kTlRows);
-        tc::mbar_init(ofull, 1);
+        for (int i = 0; i < kVStages; ++i) tc::mbar_init(vfull + i, 1), tc::mbar_init(vempty + i, 4);
+        for (int i = 0; i < kHStages; ++i) tc::mbar_init(hfull + i, 4), tc::mbar_init(hempty + i, 1);
+        for (int i = 0; i < kScStages; ++i) tc::mbar_init(scfull + i, 32);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(sfull + i, 1), tc::mbar_init(ofull + i, 1);
         tc::mbar_init(endbar, 1);
         tc::fence_mbar_init();
         *flag = 0;
@@ -224,7 +232,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
     auto warp_ok = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait_ok(bar, parity)); };
 
     float m = kNone, mv = kNone, l = 0.f;  // of a softmax thread's row
-    if (warp < 4) {
+    if (warp < 8) {
         regs_down<kRegsFew>();
         if (warp == 0) {
             // ------------------------------------------------------------ copies
@@ -253,7 +261,9 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                 __syncwarp();
                 if (lane < live) tc::tma_load_2d(sm + L::kK + ks * kTlTile + lane * page_bytes, &tmk, 0, y, kfull + ks);
                 __syncwarp();
-                if (j >= kScStages && !warp_ok(scempty + ss, (uint32_t)(j / kScStages - 1) & 1)) break;
+                // The scales' ring has one stage more than the keys': the keys of chunk j waited for
+                // the scores of chunk j - 3, which are issued when both tiles are done with the
+                // scales of chunk j - 4.
                 {
                     const int b = lane & (kTlBlocks - 1), p = p0 + b * kKvBlock;  // lanes 0 .. 7 the keys' scales, 8 .. 15 the values'
                     const int page = __shfl_sync(0xffffffffu, page_ids, min((p >> c.ps_shift) - held, 31));
@@ -272,50 +282,60 @@ __global__ void __launch_bounds__(kTlThreads, 1)
             asm volatile("cp.async.wait_all;" ::: "memory");
         } else if (warp == 1) {
             // ---------------------------------------------------------- products
-            if (tc::elect_one()) {
-                const uint32_t sbase = tc::smem_u32(sm);
-                const uint32_t id8 = idesc_f8(kTlRows, kTlTc), id16 = idesc_f16_bmn(kTlRows, kKvD);
-                bool good = nc == 0 || wait_ok(qfull, 0);
-                for (int j = 0; j <= nc && good; ++j) {
-                    // the operands from memory first: what the loop then waits for is the softmax alone
-                    const int h = (j + kHStages - 1) % kHStages, k8 = j % kKStages;
-                    if (j < nc) good = good && wait_ok(kfull + k8, (uint32_t)(j / kKStages) & 1);
-                    if (j > 0) good = good && wait_ok(hfull + h, (uint32_t)((j - 1) / kHStages) & 1);
+            const bool leader = tc::elect_one();
+            const uint32_t sbase = tc::smem_u32(sm);
+            for (int j = 0; j <= nc; ++j) {
+                const int h = (j + kHStages - 1) % kHStages, k8 = j % kKStages;
 #pragma unroll
-                    for (int i = 0; i < 2; ++i) {
-                        const int nci = i ? nc1 : nc0;
-                        if (j > 0 && j - 1 < nci) {  // O_i += w V of chunk j - 1
-                            good = good && wait_ok(pfull + i, (uint32_t)(j - 1) & 1);
-                            if (!good) break;
-                            tc::tc_fence_after();
+                for (int i = 0; i < 2; ++i) {
+                    const int nci = i ? nc1 : nc0;
+                    if (nci == 0 || j > nci) continue;
+                    tile_sync(i);  // the tile's weights of chunk j - 1 (its q) are whole, and so are the operands
+                    tc::tc_fence_after();
+                    if (leader) {
+                        if (j > 0) {  // O += w V of chunk j - 1
                             const uint64_t bd = tc::sdesc(sbase + L::kH + h * 2 * kTlTile, 2048, 128, 0);
 #pragma unroll
                             for (int k = 0; k < 8; ++k)
                                 tc::mma_bf16_tmem_a(tm + kColO + 128 * i, tm + kColS + 128 * i + 8 * k,
-                                                    bd + (uint64_t)(k * 4096 >> 4), id16, (j > 1 || k > 0) ? 1u : 0u);
+                                                    bd + (uint64_t)(k * 4096 >> 4), idesc_f16_bmn(kTlRows, kKvD),
+                                                    (j > 1 || k > 0) ? 1u : 0u);
                             // the last tile that reads this V releases it (tile 1 takes every chunk, where there is one)
                             if (i == 1 || nc1 == 0) tc::mma_commit(hempty + h);
                         }
-                        if (j < nci) {  // S_i = q_i K^T of chunk j
-                            tc::tc_fence_after();
+                        if (j < nci) {  // S = q K^T of chunk j, over the weights
                             const uint64_t bd = tc::sdesc(sbase + L::kK + k8 * kTlTile, 0, 1024, 2);
 #pragma unroll
                             for (int part = 0; part < 2; ++part) {
                                 const uint64_t ad = tc::sdesc(sbase + L::kQ + (2 * i + part) * kTlTile, 0, 1024, 2);
 #pragma unroll
                                 for (int k = 0; k < 4; ++k)
-                                    mma_f8(tm + kColS + 128 * i, ad + 2 * k, bd + 2 * k, id8, (part > 0 || k > 0) ? 1u : 0u);
+                                    mma_f8(tm + kColS + 128 * i, ad + 2 * k, bd + 2 * k, idesc_f8(kTlRows, kTlTc),
+                                           (part > 0 || k > 0) ? 1u : 0u);
                             }
                             tc::mma_commit(sfull + i);
                             if (i == 1 || nc1 == 0) tc::mma_commit(kempty + k8);
+                        } else {
+                            tc::mma_commit(ofull + i);
                         }
                     }
+                    __syncwarp();
                 }
-                if (good) tc::mma_commit(ofull);
             }
-        } else {
-            // -------------------------------------------- V to fp16, 64 threads
-            const int ct = tid - 64, k7 = ct & 7, sub = ct >> 3;
+        } else if (warp == 2) {
+            // ------- waits for the operands from memory on behalf of the products
+            bool good = true;
+            for (int j = 0; j <= nc; ++j) {
+                if (j < nc) good = good && warp_ok(kfull + j % kKStages, (uint32_t)(j / kKStages) & 1);
+                if (j > 0) good = good && warp_ok(hfull + (j - 1) % kHStages, (uint32_t)((j - 1) / kHStages) & 1);
+                for (int i = 0; i < 2; ++i) {
+                    const int nci = i ? nc1 : nc0;
+                    if (nci > 0 && j <= nci) tile_sync(i);
+                }
+            }
+        } else if (warp >= 4) {
+            // --------------------------------------------- V to fp16, four warps
+            const int k7 = lane & 7;
             for (int j = 0; j < nc; ++j) {
                 const int vs = j % kVStages, h = j % kHStages;
                 if (!warp_ok(vfull + vs, (uint32_t)(j / kVStages) & 1)) break;
@@ -323,18 +343,25 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                 const uint8_t* src = sm + L::kV + vs * kTlTile;
                 uint8_t* dst = sm + L::kH + h * 2 * kTlTile;
                 const int left = total - (cb + j) * kTlTc;  // positions behind the last count as zero values
-                // thread: positions 8 pg + k7, dims 16 sub .. + 15 (16 codes, swizzled) -> two 16-byte
-                // pieces of the 8 x 8 blocks of the product's MN-major operand
-#pragma unroll 4
-                for (int pg = 0; pg < kTlTc / 8; ++pg) {
-                    const int p = 8 * pg + k7;
-                    uint4 w = *reinterpret_cast<const uint4*>(src + p * kKvD + ((sub ^ k7) << 4));
-                    if (p >= left) w = make_uint4(0u, 0u, 0u, 0u);
+                // a warp's item: 8 positions (8 pg + k7) x 4 pieces of 16 dims, a piece a lane (16
+                // codes, swizzled) -> two 16-byte pieces of the product's 8 x 8 blocks (MN-major);
+                // all of a chunk's reads are in flight together
+                constexpr int kItems = kTlTc / 16;
+                uint4 w[kItems];
+#pragma unroll
+                for (int n = 0; n < kItems; ++n) {
+                    const int it = warp - 4 + 4 * n, sub = 4 * (it & 1) + (lane >> 3);
+                    w[n] = *reinterpret_cast<const uint4*>(src + (8 * (it >> 1) + k7) * kKvD + ((sub ^ k7) << 4));
+                }
+#pragma unroll
+                for (int n = 0; n < kItems; ++n) {
+                    const int it = warp - 4 + 4 * n, pg = it >> 1, sub = 4 * (it & 1) + (lane >> 3);
+                    if (8 * pg + k7 >= left) w[n] = make_uint4(0u, 0u, 0u, 0u);
                     uint4 lo, hi;
-                    lo.x = e4m3x2_to_f16x2(w.x & 0xFFFFu), lo.y = e4m3x2_to_f16x2(w.x >> 16);
-                    lo.z = e4m3x2_to_f16x2(w.y & 0xFFFFu), lo.w = e4m3x2_to_f16x2(w.y >> 16);
-                    hi.x = e4m3x2_to_f16x2(w.z & 0xFFFFu), hi.y = e4m3x2_to_f16x2(w.z >> 16);
-                    hi.z = e4m3x2_to_f16x2(w.w & 0xFFFFu), hi.w = e4m3x2_to_f16x2(w.w >> 16);
+                    lo.x = e4m3x2_to_f16x2(w[n].x & 0xFFFFu), lo.y = e4m3x2_to_f16x2(w[n].x >> 16);
+                    lo.z = e4m3x2_to_f16x2(w[n].y & 0xFFFFu), lo.w = e4m3x2_to_f16x2(w[n].y >> 16);
+                    hi.x = e4m3x2_to_f16x2(w[n].z & 0xFFFFu), hi.y = e4m3x2_to_f16x2(w[n].z >> 16);
+                    hi.z = e4m3x2_to_f16x2(w[n].w & 0xFFFFu), hi.w = e4m3x2_to_f16x2(w[n].w >> 16);
                     uint8_t* o = dst + pg * 2048 + sub * 256 + k7 * 16;
                     *reinterpret_cast<uint4*>(o) = lo;
                     *reinterpret_cast<uint4*>(o + 128) = hi;
@@ -350,7 +377,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
     } else {
         // ------------------------------------------ softmax, one row a thread
         regs_up<kRegsMany>();
-        const int i = (warp - 4) >> 2, r = tid - 128 - 128 * i, row = 128 * i + r;  // tile, row of it, row of the pair
+        const int i = (warp - 8) >> 2, r = tid - 256 - 128 * i, row = 128 * i + r;  // tile, row of it, row of the pair
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tm + lanes + kColS + 128 * i, tO = tm + lanes + kColO + 128 * i;
         const bool live = row < rows;
@@ -400,112 +427,113 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                     live ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(0u, 0u, 0u, 0u);
             }
             tc::fence_proxy_async_smem();
-            tc::mbar_arrive(qfull);
         }
         float2 l0 = make_float2(0.f, 0.f), l1 = l0;  // the row's sum, in four parts
         const int lim = !live || !ok ? -1 : a.causal ? before + (row0 + row) / R : before - 1;  // the last position seen
         const int nci = i ? nc1 : nc0;
-        for (int j = 0; j < nc; ++j) {
-            const int ss = j % kScStages;
-            if (!warp_ok(scfull + ss, (uint32_t)(j / kScStages) & 1)) break;
-            if (j < nci) {
-                // the chunk's scales: of the scores (with the softmax factor), and of the values
-                float cxs[kTlBlocks], vss[kTlBlocks], lvs[kTlBlocks];
-                {
-                    const float4* sk = reinterpret_cast<const float4*>(scales + ss * 2 * kTlBlocks);
+        // the weights of chunk j from its scores
+        auto softmax_chunk = [&](int j) -> bool {
+            if (!warp_ok(scfull + j % kScStages, (uint32_t)(j / kScStages) & 1)) return false;
+            // the chunk's scales: of the scores (with the softmax factor), and of the values
+            float cxs[kTlBlocks], vss[kTlBlocks], lvs[kTlBlocks];
+            {
+                const float4* sk = reinterpret_cast<const float4*>(scales + j % kScStages * 2 * kTlBlocks);
 #pragma unroll
-                    for (int b = 0; b < kTlBlocks / 4; ++b) {
-                        const float4 x = sk[b], y = sk[kTlBlocks / 4 + b];
-                        cxs[4 * b] = cs * x.x, cxs[4 * b + 1] = cs * x.y, cxs[4 * b + 2] = cs * x.z, cxs[4 * b + 3] = cs * x.w;
-                        vss[4 * b] = y.x, vss[4 * b + 1] = y.y, vss[4 * b + 2] = y.z, vss[4 * b + 3] = y.w;
-                    }
-#pragma unroll
-                    for (int b = 0; b < kTlBlocks; ++b) {
-                        lvs[b] = lg2_approx(vss[b]);
-                        cxs[b] = cxs[b] < FLT_MIN ? FLT_MIN : cxs[b];  // not 0: hidden scores are -inf
-                    }
+                for (int b = 0; b < kTlBlocks / 4; ++b) {
+                    const float4 x = sk[b], y = sk[kTlBlocks / 4 + b];
+                    cxs[4 * b] = cs * x.x, cxs[4 * b + 1] = cs * x.y, cxs[4 * b + 2] = cs * x.z, cxs[4 * b + 3] = cs * x.w;
+                    vss[4 * b] = y.x, vss[4 * b + 1] = y.y, vss[4 * b + 2] = y.z, vss[4 * b + 3] = y.w;
                 }
-                if (!warp_ok(sfull + i, (uint32_t)j & 1)) break;
-                tc::tc_fence_after();
-                const int see = lim - (cb + j) * kTlTc;  // columns 0 .. see are seen
-                const bool cut = __any_sync(0xffffffffu, see < kTlTc - 1);
-                float v[kTlTc];
-#pragma unroll
-                for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, v + 32 * q);
-                tc::tmem_wait_ld();
-                if (cut) {  // the factors of a block that the row does not see may be anything
-#pragma unroll
-                    for (int k = 0; k < kTlTc; ++k) v[k] = k <= see ? v[k] : -INFINITY;
-#pragma unroll
-                    for (int b = 0; b < kTlBlocks; ++b)
-                        if (16 * b > see) cxs[b] = 1.f, vss[b] = 0.f, lvs[b] = -INFINITY;
-                }
-                // the chunk's maxima: of x, and of x + log2 vs
-                float mx = -INFINITY, mvx = -INFINITY;
 #pragma unroll
                 for (int b = 0; b < kTlBlocks; ++b) {
-                    const float* w = v + 16 * b;
-                    const float t = max3(max3(max3(w[0], w[1], w[2]), max3(w[3], w[4], w[5]), max3(w[6], w[7], w[8])),
-                                         max3(w[9], w[10], w[11]), max3(fmaxf(w[12], w[13]), w[14], w[15]));
-                    const float x = t * cxs[b];
-                    mx = fmaxf(mx, x);
-                    mvx = fmaxf(mvx, x + lvs[b]);
+                    lvs[b] = lg2_approx(vss[b]);
+                    cxs[b] = cxs[b] < FLT_MIN ? FLT_MIN : cxs[b];  // not 0: hidden scores are -inf
                 }
-                if (mx > m + kSlack) {
-                    const float f = ex2_approx(m - mx);
-                    l0.x *= f, l0.y *= f, l1.x *= f, l1.y *= f;
-                    m = mx;
-                }
-                const bool grow = mvx > mv + kSlack;
-                const float f = grow ? ex2_approx(mv - mvx) : 1.f;
-                if (grow) mv = mvx;
-                if (j > 0 && __any_sync(0xffffffffu, grow)) {  // O is idle: its products came before S
+            }
+            if (!warp_ok(sfull + i, (uint32_t)j & 1)) return false;
+            tc::tc_fence_after();
+            const int see = lim - (cb + j) * kTlTc;  // columns 0 .. see are seen
+            const bool cut = __any_sync(0xffffffffu, see < kTlTc - 1);
+            float v[kTlTc];
+#pragma unroll
+            for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, v + 32 * q);
+            tc::tmem_wait_ld();
+            if (cut) {  // the factors of a block that the row does not see may be anything
+#pragma unroll
+                for (int k = 0; k < kTlTc; ++k) v[k] = k <= see ? v[k] : -INFINITY;
+#pragma unroll
+                for (int b = 0; b < kTlBlocks; ++b)
+                    if (16 * b > see) cxs[b] = 1.f, vss[b] = 0.f, lvs[b] = -INFINITY;
+            }
+            // the chunk's maxima: of x, and of x + log2 vs
+            float mx = -INFINITY, mvx = -INFINITY;
+#pragma unroll
+            for (int b = 0; b < kTlBlocks; ++b) {
+                const float* w = v + 16 * b;
+                const float t = max3(max3(max3(w[0], w[1], w[2]), max3(w[3], w[4], w[5]), max3(w[6], w[7], w[8])),
+                                     max3(w[9], w[10], w[11]), max3(fmaxf(w[12], w[13]), w[14], w[15]));
+                const float x = t * cxs[b];
+                mx = fmaxf(mx, x);
+                mvx = fmaxf(mvx, x + lvs[b]);
+            }
+            if (mx > m + kSlack) {
+                const float f = ex2_approx(m - mx);
+                l0.x *= f, l0.y *= f, l1.x *= f, l1.y *= f;
+                m = mx;
+            }
+            const bool grow = mvx > mv + kSlack;
+            const float f = grow ? ex2_approx(mv - mvx) : 1.f;
+            if (grow) mv = mvx;
+            if (j > 0 && __any_sync(0xffffffffu, grow)) {  // O is idle: its products came before S
 #pragma unroll 1
-                    for (int q = 0; q < 4; ++q) {
-                        float o[2][16];
-                        tc::tmem_ld16(tO + 32 * q, o[0]);
-                        tc::tmem_ld16(tO + 32 * q + 16, o[1]);
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int h = 0; h < 2; ++h) {
-                            uint32_t y[16];
-#pragma unroll
-                            for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(o[h][k] * f);
-                            tmem_st16(tO + 32 * q + 16 * h, y);
-                        }
-                    }
-                }
-                const float lift = fminf(ex2_approx(m - mv + kLift), FLT_MAX);  // (finite: a block of scale 0 weighs 0)
-                const float2 nm = make_float2(-m, -m);
-#pragma unroll
                 for (int q = 0; q < 4; ++q) {
-                    uint32_t y[16];
+                    float o[2][16];
+                    tc::tmem_ld16(tO + 32 * q, o[0]);
+                    tc::tmem_ld16(tO + 32 * q + 16, o[1]);
+                    tc::tmem_wait_ld();
 #pragma unroll
                     for (int h = 0; h < 2; ++h) {
-                        const int b = 2 * q + h;
-                        const float cx = cxs[b], to = vss[b] * lift;
+                        uint32_t y[16];
 #pragma unroll
-                        for (int k = 0; k < 8; ++k) {
-                            const int at = 16 * b + 2 * k;
-                            const float2 x = fma2(make_float2(v[at], v[at + 1]), make_float2(cx, cx), nm);
-                            const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
-                            if (k & 1)
-                                l1 = add2(l1, p);
-                            else
-                                l0 = add2(l0, p);
-                            const float2 w = mul2(p, make_float2(to, to));
-                            y[8 * h + k] = pack_f16x2(w.x, w.y);
-                        }
+                        for (int k = 0; k < 16; ++k) y[k] = __float_as_uint(o[h][k] * f);
+                        tmem_st16(tO + 32 * q + 16 * h, y);
                     }
-                    tmem_st16(tS + 16 * q, y);  // over S, which is read
                 }
-                tc::tmem_wait_st();
-                tc::tc_fence_before();
-                __syncwarp();
-                if (lane == 0) tc::mbar_arrive(pfull + i);
             }
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(scempty + ss);
+            const float lift = fminf(ex2_approx(m - mv + kLift), FLT_MAX);  // (finite: a block of scale 0 weighs 0)
+            const float2 nm = make_float2(-m, -m);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t y[16];
+#pragma unroll
+                for (int h = 0; h < 2; ++h) {
+                    const int b = 2 * q + h;
+                    const float cx = cxs[b], to = vss[b] * lift;
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        const int at = 16 * b + 2 * k;
+                        const float2 x = fma2(make_float2(v[at], v[at + 1]), make_float2(cx, cx), nm);
+                        const float2 p = make_float2(ex2_approx(x.x), ex2_approx(x.y));
+                        if (k & 1)
+                            l1 = add2(l1, p);
+                        else
+                            l0 = add2(l0, p);
+                        const float2 w = mul2(p, make_float2(to, to));
+                        y[8 * h + k] = pack_f16x2(w.x, w.y);
+                    }
+                }
+                tmem_st16(tS + 16 * q, y);  // over S, which is read
+            }
+            tc::tmem_wait_st();
+            return true;
+        };
+        bool good = true;
+        tc::tc_fence_before();
+        if (nci > 0) tile_arrive(i);  // the tile of q is whole
+        for (int j = 0; j < nci; ++j) {
+            good = good && softmax_chunk(j);
+            tc::tc_fence_before();
+            tile_arrive(i);  // the chunk's weights are whole
         }
         l = (l0.x + l0.y) + (l1.x + l1.y);
         __syncwarp();
@@ -514,19 +542,22 @@ __global__ void __launch_bounds__(kTlThreads, 1)
     }
     // ------------------------------------------------------------- the merge
     __syncwarp();
-    const bool walked = warp < 4 || (warp < 8 ? nc0 : nc1) == 0 || warp_ok(ofull, 0);
+    const bool walked = warp < 8 || (warp < 12 ? nc0 : nc1) == 0 || warp_ok(ofull + (warp < 12 ? 0 : 1), 0);
     tc::tc_fence_after();
     __syncthreads();
     const bool gave_up = *flag != 0;
-    if (gave_up && warp == 1 && tc::elect_one()) {
-        // every product issued must be done and the copies in flight must land
+    if (gave_up && warp < 2 && tc::elect_one()) {
+        // the copies in flight must land and every product issued must be done
         // before the tensor memory is freed and the CTA exits (all bounded)
-        tc::mma_commit(endbar);
-        tc::mbar_wait(endbar, 0, 100000000ull);
-        for (int i = 0; i < kKStages; ++i)
-            tc::mbar_wait(kfull + i, 0, 100000000ull), tc::mbar_wait(kfull + i, 1, 100000000ull);
-        for (int i = 0; i < kVStages; ++i)
-            tc::mbar_wait(vfull + i, 0, 100000000ull), tc::mbar_wait(vfull + i, 1, 100000000ull);
+        if (warp == 0) {
+            for (int i = 0; i < kKStages; ++i)
+                tc::mbar_wait(kfull + i, 0, 100000000ull), tc::mbar_wait(kfull + i, 1, 100000000ull);
+            for (int i = 0; i < kVStages; ++i)
+                tc::mbar_wait(vfull + i, 0, 100000000ull), tc::mbar_wait(vfull + i, 1, 100000000ull);
+        } else {
+            tc::mma_commit(endbar);
+            tc::mbar_wait(endbar, 0, 100000000ull);
+        }
     }
     __syncthreads();
     const int own = 2 * kTlRows / W;  // rows that a CTA of the cluster owns
@@ -535,8 +566,8 @@ __global__ void __launch_bounds__(kTlThreads, 1)
         tc::cluster_arrive();  // ... and is done with its rings
         tc::cluster_wait();
     }
-    if (warp >= 4) {
-        const int i = (warp - 4) >> 2, row = tid - 128;
+    if (warp >= 8) {
+        const int i = (warp - 8) >> 2, row = tid - 256;
         const uint32_t tO = tm + ((uint32_t)((warp & 3) * 32) << 16) + kColO + 128 * i;
         const bool some = walked && !gave_up && (i ? nc1 : nc0) > 0;  // (the same in the whole warp)
         const bool live = row < rows;
