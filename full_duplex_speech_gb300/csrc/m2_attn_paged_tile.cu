@@ -14,13 +14,13 @@
 //                   conversion of the keys;
 //   softmax         one thread a row, S read out of tensor memory in fp32:
 //                   x = S (scale ks), p = 2^(x - m), l += p, and the weight
-//                   w = p vs 2^(m - mv + 3) to fp16 (2^-11) over S;
+//                   w = p vs 2^(m - mv) to fp16 (2^-11) over S;
 //   O += w V        kind::f16, w from tensor memory, V converted to fp16
 //                   (exactly) by four warps.
 // m and mv (the reference of the weights, a maximum of x + log2 vs) move only
-// when a chunk exceeds them by more than 2^12, which p <= 2^12 in fp32 and
+// when a chunk exceeds them by more than 2^15, which p <= 2^15 in fp32 and
 // w <= 2^15 in fp16 allow; only then is O rescaled in tensor memory.
-//     out = 2^(mv - m - 3) O / l.
+//     out = 2^(mv - m) O / l.
 //
 // Warps: 0 copies (pages by TMA through rings, scales by 4-byte asynchronous
 // copies), 1 issues the products, 2 waits for their operands, 4-7 convert V,
@@ -47,8 +47,7 @@ constexpr int kTlTc = 128;                         // positions per chunk
 constexpr int kTlBlocks = kTlTc / kKvBlock;        // scales of a chunk
 constexpr uint32_t kTlTile = kTlTc * kKvD;         // 16 KB of codes
 constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kScStages = kKStages + 1;
-constexpr float kSlack = 12.f;                     // log2 by which a chunk may exceed the references
-constexpr float kLift = 3.f;                       // log2 of the weights' reference: 2^(3 + 12) at most
+constexpr float kSlack = 15.f;                     // log2 by which a chunk may exceed the references
 constexpr uint32_t kColO = 0, kColS = 256;         // tensor memory: O of the two tiles, then S (and w over it)
 constexpr int kTlMaxW = 8;
 
@@ -381,50 +380,68 @@ __global__ void __launch_bounds__(kTlThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tm + lanes + kColS + 128 * i, tO = tm + lanes + kColO + 128 * i;
         const bool live = row < rows;
-        // the row of q, scaled, as e4m3 hi + lo
-        float cs;
+        // The warp's 32 rows of q, scaled, as e4m3 hi + lo: two rows at a time, 16 lanes a
+        // row (a lane a row would touch 32 cache lines with every load), all loads in flight
+        // together; the row's factor goes to the lane that owns the row.
+        float cs = 0.f;
         {
-            uint4 x[16];
             const int rr = row0 + (live ? row : 0);
-            const uint4* src = reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) +
-                                                              ((size_t)s * a.T + rr / R) * a.q_stride + (size_t)(g * R + rr % R) * kKvD);
-            float top = 0.f;
+            const long at = ((long)s * a.T + rr / R) * a.q_stride + (long)(g * R + rr % R) * kKvD;
+            const int piece = lane & 15;
+            uint4 x[16];
 #pragma unroll
-            for (int u = 0; u < 16; ++u) x[u] = __ldg(src + u);
+            for (int t = 0; t < 16; ++t) {
+                const long from = __shfl_sync(0xffffffffu, at, 2 * t + (lane >> 4));
+                const bool in = row - lane + 2 * t + (lane >> 4) < rows;
+                x[t] = in ? __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) + from) + piece)
+                          : make_uint4(0u, 0u, 0u, 0u);
+            }
+            // every row's largest magnitude, then every row's terms: 16 rows' latencies side by side
+            float top[16];
 #pragma unroll
-            for (int u = 0; u < 16; ++u) {
-                const uint32_t w[4] = {x[u].x, x[u].y, x[u].z, x[u].w};
+            for (int t = 0; t < 16; ++t) {
+                const uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
+                top[t] = 0.f;
 #pragma unroll
                 for (int e = 0; e < 4; ++e)
-                    top = fmaxf(top, fmaxf(fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u))));
+                    top[t] = max3(top[t], fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u)));
             }
-            const float pw = row_power(top, 7), sg = a.scale < 0.f ? -pw : pw;
-            cs = top < INFINITY ? fabsf(a.scale) * kLog2e / pw : NAN;  // e4m3 has no infinity: such a row reads NaN
-            uint8_t* q8 = sm + L::kQ + 2 * i * kTlTile + r * kKvD;
 #pragma unroll
-            for (int u = 0; u < 8; ++u) {
-                uint32_t hi[4], lo[4];
+            for (int off = 1; off < 16; off <<= 1)
+#pragma unroll
+                for (int t = 0; t < 16; ++t) top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], off));
+            float mine = 0.f;  // of the row that this lane owns
+#pragma unroll
+            for (int t = 0; t < 16; ++t) {
+                const float y = __shfl_sync(0xffffffffu, top[t], (lane & 1) << 4);
+                if ((lane >> 1) == t) mine = y;
+            }
+            // e4m3 has no infinity: such a row reads NaN
+            cs = mine < INFINITY ? fabsf(a.scale) * kLog2e / row_power(mine, 7) : NAN;
+#pragma unroll
+            for (int t = 0; t < 16; ++t) {
+                const uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
+                const float pw = row_power(top[t], 7), sg = a.scale < 0.f ? -pw : pw;
+                float f[8];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint4& y = x[2 * u + (e >> 1)];
-                    const uint32_t w0 = (e & 1) ? y.z : y.x, w1 = (e & 1) ? y.w : y.y;
-                    const float f[4] = {__uint_as_float(w0 << 16) * sg, __uint_as_float(w0 & 0xFFFF0000u) * sg,
-                                        __uint_as_float(w1 << 16) * sg, __uint_as_float(w1 & 0xFFFF0000u) * sg};
-                    hi[e] = lo[e] = 0u;
-#pragma unroll
-                    for (int b = 0; b < 2; ++b) {
-                        const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * b], f[2 * b + 1]), __NV_SATFINITE, __NV_E4M3);
-                        const float2 back = unpack_f16x2(e4m3x2_to_f16x2(h2));
-                        const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(f[2 * b] - back.x, f[2 * b + 1] - back.y),
-                                                                     __NV_SATFINITE, __NV_E4M3);
-                        hi[e] |= h2 << (16 * b);
-                        lo[e] |= l2 << (16 * b);
-                    }
+                    f[2 * e] = __uint_as_float(w[e] << 16);
+                    f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
                 }
-                const uint32_t off = (uint32_t)(u ^ (r & 7)) << 4;
-                *reinterpret_cast<uint4*>(q8 + off) = live ? make_uint4(hi[0], hi[1], hi[2], hi[3]) : make_uint4(0u, 0u, 0u, 0u);
-                *reinterpret_cast<uint4*>(q8 + kTlTile + off) =
-                    live ? make_uint4(lo[0], lo[1], lo[2], lo[3]) : make_uint4(0u, 0u, 0u, 0u);
+                uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const float y0 = f[2 * e] * sg, y1 = f[2 * e + 1] * sg;
+                    const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
+                    const float2 back = unpack_f16x2(e4m3x2_to_f16x2(h2));
+                    const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(y0 - back.x, y1 - back.y), __NV_SATFINITE, __NV_E4M3);
+                    hi[e >> 1] |= h2 << (16 * (e & 1));
+                    lo[e >> 1] |= l2 << (16 * (e & 1));
+                }
+                const int qr = (r & ~31) + 2 * t + (lane >> 4);  // row of the tile
+                uint8_t* q8 = sm + L::kQ + 2 * i * kTlTile + qr * kKvD + (((piece >> 1) ^ (qr & 7)) << 4) + 8 * (piece & 1);
+                *reinterpret_cast<uint2*>(q8) = make_uint2(hi[0], hi[1]);
+                *reinterpret_cast<uint2*>(q8 + kTlTile) = make_uint2(lo[0], lo[1]);
             }
             tc::fence_proxy_async_smem();
         }
@@ -500,7 +517,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                     }
                 }
             }
-            const float lift = fminf(ex2_approx(m - mv + kLift), FLT_MAX);  // (finite: a block of scale 0 weighs 0)
+            const float lift = fminf(ex2_approx(m - mv), FLT_MAX);  // (finite: a block of scale 0 weighs 0)
             const float2 nm = make_float2(-m, -m);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -575,7 +592,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
         const int rr = row0 + (live ? row : 0);
         uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + ((size_t)s * a.T + rr / R) * a.out_stride +
                         (size_t)(g * R + rr % R) * kKvD;
-        const float f = l == 0.f ? 0.f : ex2_approx(mv - m - kLift) / l;
+        const float f = l == 0.f ? 0.f : ex2_approx(mv - m) / l;
         const uint32_t slot = tc::smem_u32(sm) + (uint32_t)((wk * own + row % own) * kKvD * 4);
         const uint32_t owner = (uint32_t)(row / own);
 #pragma unroll
@@ -618,7 +635,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
     tc::cluster_arrive();  // the stores into the owners' memory are visible ...
     tc::cluster_wait();    // ... once every CTA has made them
     // this CTA's rows, a warp a row, four dims a lane:
-    // out = 2^(V - M - 3) sum_w 2^(mv_w - V) O_w / sum_w 2^(m_w - M) l_w
+    // out = 2^(V - M) sum_w 2^(mv_w - V) O_w / sum_w 2^(m_w - M) l_w
     const float4* ml = reinterpret_cast<const float4*>(sm + L::kMl);
     for (int r = warp; r < own; r += kTlThreads / 32) {
         const int row = wk * own + r;
@@ -637,7 +654,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
             o.x = fmaf(f, y.x, o.x), o.y = fmaf(f, y.y, o.y), o.z = fmaf(f, y.z, o.z), o.w = fmaf(f, y.w, o.w);
             sum = fmaf(ex2_approx(x.x - M), x.y, sum);
         }
-        const float f = ex2_approx(V - M - kLift) / sum;
+        const float f = ex2_approx(V - M) / sum;
         const bool none = sum == 0.f;  // a row that sees nothing: zeros
         const int rr = row0 + row;
         uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + ((size_t)s * a.T + rr / R) * a.out_stride +
