@@ -380,69 +380,69 @@ __global__ void __launch_bounds__(kTlThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tm + lanes + kColS + 128 * i, tO = tm + lanes + kColO + 128 * i;
         const bool live = row < rows;
-        // The warp's 32 rows of q, scaled, as e4m3 hi + lo: two rows at a time, 16 lanes a
-        // row (a lane a row would touch 32 cache lines with every load), all loads in flight
-        // together; the row's factor goes to the lane that owns the row.
+        // The warp's 32 rows of q, scaled, as e4m3 hi + lo, two rows at a time, 16 lanes a row
+        // (a lane a row would touch 32 cache lines with every load). A row's 256 bytes come by
+        // asynchronous copies to where its hi and lo will be, so that all are in flight
+        // together and the loops stay short (straight-line code for all the rows cost 3 us
+        // more: it runs once, as fast as instructions can be fetched). The row's factor goes
+        // to the lane that owns the row.
         float cs = 0.f;
         {
-            const int rr = row0 + (live ? row : 0);
+            const int rr = row0 + (live ? row : 0), piece = lane & 15, up = lane >> 4;
             const long at = ((long)s * a.T + rr / R) * a.q_stride + (long)(g * R + rr % R) * kKvD;
-            const int piece = lane & 15;
-            uint4 x[16];
-#pragma unroll
+            uint8_t* q8 = sm + L::kQ + 2 * i * kTlTile + (r & ~31) * kKvD;  // the warp's first row
+#pragma unroll 4
             for (int t = 0; t < 16; ++t) {
-                const long from = __shfl_sync(0xffffffffu, at, 2 * t + (lane >> 4));
-                const bool in = row - lane + 2 * t + (lane >> 4) < rows;
-                x[t] = in ? __ldg(reinterpret_cast<const uint4*>(reinterpret_cast<const uint16_t*>(a.q) + from) + piece)
-                          : make_uint4(0u, 0u, 0u, 0u);
+                const long from = __shfl_sync(0xffffffffu, at, 2 * t + up);
+                cp_async16(q8 + (piece >> 3) * kTlTile + (2 * t + up) * kKvD + (piece & 7) * 16,
+                           reinterpret_cast<const uint16_t*>(a.q) + from + 8 * piece);
             }
-            // every row's largest magnitude, then every row's terms: 16 rows' latencies side by side
-            float top[16];
+            asm volatile("cp.async.wait_all;" ::: "memory");
+            __syncwarp();
+            float mine = 0.f;  // the largest magnitude of the row that this lane owns
+#pragma unroll 1
+            for (int t4 = 0; t4 < 16; t4 += 4) {  // eight rows side by side
+                float f[4][8], top[4];
 #pragma unroll
-            for (int t = 0; t < 16; ++t) {
-                const uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
-                top[t] = 0.f;
+                for (int t = 0; t < 4; ++t) {
+                    const uint4 x = *reinterpret_cast<const uint4*>(q8 + (piece >> 3) * kTlTile + (2 * (t4 + t) + up) * kKvD +
+                                                                    (piece & 7) * 16);
+                    const uint32_t w[4] = {x.x, x.y, x.z, x.w};
+                    top[t] = 0.f;
 #pragma unroll
-                for (int e = 0; e < 4; ++e)
-                    top[t] = max3(top[t], fabsf(__uint_as_float(w[e] << 16)), fabsf(__uint_as_float(w[e] & 0xFFFF0000u)));
-            }
+                    for (int e = 0; e < 4; ++e) {
+                        f[t][2 * e] = __uint_as_float(w[e] << 16);
+                        f[t][2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
+                        top[t] = max3(top[t], fabsf(f[t][2 * e]), fabsf(f[t][2 * e + 1]));
+                    }
+                }
 #pragma unroll
-            for (int off = 1; off < 16; off <<= 1)
+                for (int off = 1; off < 16; off <<= 1)
 #pragma unroll
-                for (int t = 0; t < 16; ++t) top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], off));
-            float mine = 0.f;  // of the row that this lane owns
+                    for (int t = 0; t < 4; ++t) top[t] = fmaxf(top[t], __shfl_xor_sync(0xffffffffu, top[t], off));
 #pragma unroll
-            for (int t = 0; t < 16; ++t) {
-                const float y = __shfl_sync(0xffffffffu, top[t], (lane & 1) << 4);
-                if ((lane >> 1) == t) mine = y;
+                for (int t = 0; t < 4; ++t) {  // (the 16 lanes have read their rows: they have exchanged the maxima)
+                    const float own = __shfl_sync(0xffffffffu, top[t], (lane & 1) << 4);
+                    if ((lane >> 1) == t4 + t) mine = own;
+                    const float pw = row_power(top[t], 7), sg = a.scale < 0.f ? -pw : pw;
+                    uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
+#pragma unroll
+                    for (int e = 0; e < 4; ++e) {
+                        const float y0 = f[t][2 * e] * sg, y1 = f[t][2 * e + 1] * sg;
+                        const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
+                        const float2 back = unpack_f16x2(e4m3x2_to_f16x2(h2));
+                        const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(y0 - back.x, y1 - back.y), __NV_SATFINITE, __NV_E4M3);
+                        hi[e >> 1] |= h2 << (16 * (e & 1));
+                        lo[e >> 1] |= l2 << (16 * (e & 1));
+                    }
+                    const int qr = 2 * (t4 + t) + up;
+                    uint8_t* o = q8 + qr * kKvD + (((piece >> 1) ^ (qr & 7)) << 4) + 8 * (piece & 1);
+                    *reinterpret_cast<uint2*>(o) = make_uint2(hi[0], hi[1]);
+                    *reinterpret_cast<uint2*>(o + kTlTile) = make_uint2(lo[0], lo[1]);
+                }
             }
             // e4m3 has no infinity: such a row reads NaN
             cs = mine < INFINITY ? fabsf(a.scale) * kLog2e / row_power(mine, 7) : NAN;
-#pragma unroll
-            for (int t = 0; t < 16; ++t) {
-                const uint32_t w[4] = {x[t].x, x[t].y, x[t].z, x[t].w};
-                const float pw = row_power(top[t], 7), sg = a.scale < 0.f ? -pw : pw;
-                float f[8];
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    f[2 * e] = __uint_as_float(w[e] << 16);
-                    f[2 * e + 1] = __uint_as_float(w[e] & 0xFFFF0000u);
-                }
-                uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
-#pragma unroll
-                for (int e = 0; e < 4; ++e) {
-                    const float y0 = f[2 * e] * sg, y1 = f[2 * e + 1] * sg;
-                    const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
-                    const float2 back = unpack_f16x2(e4m3x2_to_f16x2(h2));
-                    const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(y0 - back.x, y1 - back.y), __NV_SATFINITE, __NV_E4M3);
-                    hi[e >> 1] |= h2 << (16 * (e & 1));
-                    lo[e >> 1] |= l2 << (16 * (e & 1));
-                }
-                const int qr = (r & ~31) + 2 * t + (lane >> 4);  // row of the tile
-                uint8_t* q8 = sm + L::kQ + 2 * i * kTlTile + qr * kKvD + (((piece >> 1) ^ (qr & 7)) << 4) + 8 * (piece & 1);
-                *reinterpret_cast<uint2*>(q8) = make_uint2(hi[0], hi[1]);
-                *reinterpret_cast<uint2*>(q8 + kTlTile) = make_uint2(lo[0], lo[1]);
-            }
             tc::fence_proxy_async_smem();
         }
         float2 l0 = make_float2(0.f, 0.f), l1 = l0;  // the row's sum, in four parts
