@@ -128,6 +128,8 @@ def load():
     """Load libmamba2.so (built by full_duplex_speech_gb300.build). Raises
     if it is missing: there is no other implementation to fall back to."""
     global _lib
+    if _lib is not None:
+        return _lib
     with _lock:
         if _lib is not None:
             return _lib
@@ -204,7 +206,8 @@ def _p(t):
 def _stream(stream):
     if stream is None:
         import torch
-        return torch.cuda.current_stream().cuda_stream
+        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of the time of the Stream object
+        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
