@@ -22,7 +22,12 @@
 // and of the values, so that every global access is 8 or 16 bytes wide and
 // the pair (d, d + rot / 2) of the half layout sits in another lane of the
 // same half-warp. The maximum goes through shuffles and shared memory. The
-// queries' rows go to CTAs of their own, 16 rows of 128 dims at a time.
+// queries go to CTAs of their own, 16 (position, heads) rows at a time.
+// 4 x 4096 positions with 40 query heads, bf16, 446 MB: 88 us, 5.1 TB/s (76%
+// of the measured copy rate; 34 us without the queries, where a CTA's chain
+// of length, rows, maximum and stores shows: four heads in turn with the next
+// one's rows in flight took 44). One frame: 2.4 us, of 64 sessions 3.8 us,
+// mostly the launch and the chain.
 #include <cuda_fp8.h>
 
 #include "m2_common.cuh"
@@ -54,42 +59,54 @@ __device__ __forceinline__ void store8_f32(float* p, const float (&f)[8]) {
     *reinterpret_cast<float4*>(p + 4) = make_float4(f[4], f[5], f[6], f[7]);
 }
 
-// Dims [8 piece, 8 piece + 8) of a row at position pos, rotated in place.
-// Every lane of the warp calls it (the half layout exchanges dims between
-// lanes); `turn` false leaves the lane's values.
-__device__ __forceinline__ void rotate8(const KvAppendArgs& a, int piece, int lane, int pos, bool turn, float (&f)[8]) {
-    if (a.rot == 0) return;
-    const int half = a.rot >> 1;
-    if (a.interleaved) {
-        if (!turn || 8 * piece >= a.rot) return;
-        const float4 c = __ldg(reinterpret_cast<const float4*>(a.cos + (size_t)pos * half + 4 * piece));
-        const float4 s = __ldg(reinterpret_cast<const float4*>(a.sin + (size_t)pos * half + 4 * piece));
-        const float cv[4] = {c.x, c.y, c.z, c.w}, sv[4] = {s.x, s.y, s.z, s.w};
-#pragma unroll
-        for (int j = 0; j < 4; ++j) {
-            const float x = f[2 * j], y = f[2 * j + 1];
-            f[2 * j] = __fsub_rn(__fmul_rn(x, cv[j]), __fmul_rn(y, sv[j]));
-            f[2 * j + 1] = __fadd_rn(__fmul_rn(x, sv[j]), __fmul_rn(y, cv[j]));
-        }
-        return;
-    }
-    const int hp = half >> 3;  // pieces of one half
-    const bool first = piece < hp, in = piece < 2 * hp;
-    const int mate = !in ? lane : first ? lane + hp : lane - hp;
-    float g[8];
-#pragma unroll
-    for (int j = 0; j < 8; ++j) g[j] = __shfl_sync(0xffffffffu, f[j], mate);
-    if (!turn || !in) return;
-    const size_t at = (size_t)pos * half + 8 * (first ? piece : piece - hp);
+// The rotation of dims [8 piece, 8 piece + 8) at one position: the table's
+// factors, and in the half layout the lane with the pairs' other dims.
+struct Turn {
     float c[8], s[8];
-    load8_f32(a.cos + at, c);
-    load8_f32(a.sin + at, s);
-#pragma unroll
-    for (int j = 0; j < 8; ++j) {
-        const float u = __fmul_rn(f[j], c[j]), w = __fmul_rn(g[j], s[j]);
-        f[j] = first ? __fsub_rn(u, w) : __fadd_rn(w, u);
+    int mate;
+    bool on, second;  // turned at all; the pairs' second dims (half layout)
+
+    __device__ __forceinline__ void load(const KvAppendArgs& a, int piece, int lane, int pos, bool live) {
+        on = live && a.rot > 0 && 8 * piece < a.rot;
+        const int half = a.rot >> 1, hp = half >> 3;  // hp: pieces of one half
+        second = !a.interleaved && piece >= hp;
+        mate = a.interleaved || 8 * piece >= a.rot ? lane : second ? lane - hp : lane + hp;
+        if (!on) return;
+        if (a.interleaved) {
+            const float4 x = __ldg(reinterpret_cast<const float4*>(a.cos + (size_t)pos * half + 4 * piece));
+            const float4 y = __ldg(reinterpret_cast<const float4*>(a.sin + (size_t)pos * half + 4 * piece));
+            c[0] = x.x, c[1] = x.y, c[2] = x.z, c[3] = x.w;
+            s[0] = y.x, s[1] = y.y, s[2] = y.z, s[3] = y.w;
+        } else {
+            const size_t at = (size_t)pos * half + 8 * (second ? piece - hp : piece);
+            load8_f32(a.cos + at, c);
+            load8_f32(a.sin + at, s);
+        }
     }
-}
+    // Every lane of the warp calls it (the half layout exchanges dims).
+    __device__ __forceinline__ void apply(const KvAppendArgs& a, float (&f)[8]) const {
+        if (a.rot == 0) return;
+        if (a.interleaved) {
+            if (!on) return;
+#pragma unroll
+            for (int j = 0; j < 4; ++j) {
+                const float x = f[2 * j], y = f[2 * j + 1];
+                f[2 * j] = __fsub_rn(__fmul_rn(x, c[j]), __fmul_rn(y, s[j]));
+                f[2 * j + 1] = __fadd_rn(__fmul_rn(x, s[j]), __fmul_rn(y, c[j]));
+            }
+            return;
+        }
+        float g[8];
+#pragma unroll
+        for (int j = 0; j < 8; ++j) g[j] = __shfl_sync(0xffffffffu, f[j], mate);
+        if (!on) return;
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float u = __fmul_rn(f[j], c[j]), w = __fmul_rn(g[j], s[j]);
+            f[j] = second ? __fadd_rn(w, u) : __fsub_rn(u, w);
+        }
+    }
+};
 
 __device__ __forceinline__ uint2 pack_e4m3(const float (&f)[8], float inv) {
     uint32_t h[4];
@@ -101,8 +118,10 @@ __device__ __forceinline__ uint2 pack_e4m3(const float (&f)[8], float inv) {
 }
 
 // grid (blocks of a session x kv heads + CTAs of its queries, sessions)
-template <typename TA>
-__global__ void __launch_bounds__(kApThreads) kv_append_kernel(KvAppendArgs a, int blocks) {
+// QH: heads of the queries that a thread rotates. (bf16: five CTAs an SM, 48
+// registers, 88 us above against 92 with four.)
+template <typename TA, int QH>
+__global__ void __launch_bounds__(kApThreads, sizeof(TA) == 2 ? 5 : 4) kv_append_kernel(KvAppendArgs a, int blocks) {
     __shared__ uint32_t smax[2][kApThreads / 32];
     const KvCache& c = a.c;
     const int s = blockIdx.y;
@@ -118,23 +137,37 @@ __global__ void __launch_bounds__(kApThreads) kv_append_kernel(KvAppendArgs a, i
         return;
     }
     if ((int)blockIdx.x >= blocks * c.Hkv) {
-        // the queries: 16 (position, head) rows
-        const int r = ((int)blockIdx.x - blocks * c.Hkv) * (kApThreads / kPieces) + row;
-        const int t = r / a.Hq, h = r % a.Hq;
+        // the queries: 16 (position, QH heads) rows; the factors are read once for the heads
+        const int r = ((int)blockIdx.x - blocks * c.Hkv) * (kApThreads / kPieces) + row, parts = (a.Hq + QH - 1) / QH;
+        const int t = r / parts, h0 = r % parts * QH;
         const bool live = t < n;
-        float f[8] = {};
-        if (live) load8<TA>(a.q, ((size_t)s * a.T + t) * a.q_stride + (size_t)h * kKvD + 8 * piece, f);
-        rotate8(a, piece, lane, L + t, live, f);
-        if (live) {
-            const size_t o = ((size_t)s * a.T + t) * a.qo_stride + (size_t)h * kKvD + 8 * piece;
-            if constexpr (sizeof(TA) == 2) {
-                uint32_t w[4];
+        Turn turn;
+        turn.load(a, piece, lane, L + t, live);
+        const size_t in = ((size_t)s * a.T + t) * a.q_stride + 8 * piece, to = ((size_t)s * a.T + t) * a.qo_stride + 8 * piece;
+        Act8<TA> x[QH];
 #pragma unroll
-                for (int j = 0; j < 4; ++j)
-                    w[j] = (uint32_t)float_to_bf16_bits(f[2 * j]) | ((uint32_t)float_to_bf16_bits(f[2 * j + 1]) << 16);
-                *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.q_out) + o) = make_uint4(w[0], w[1], w[2], w[3]);
-            } else {
-                store8_f32(reinterpret_cast<float*>(a.q_out) + o, f);
+        for (int h = 0; h < QH; ++h)
+            if (live && h0 + h < a.Hq) x[h].load_rw(a.q, in + (size_t)(h0 + h) * kKvD);
+#pragma unroll
+        for (int h = 0; h < QH; ++h) {
+            float f[8] = {};
+            const bool here = live && h0 + h < a.Hq;
+            if (here) {
+#pragma unroll
+                for (int j = 0; j < 8; ++j) f[j] = x[h].get(j);
+            }
+            turn.apply(a, f);
+            if (here) {
+                const size_t o = to + (size_t)(h0 + h) * kKvD;
+                if constexpr (sizeof(TA) == 2) {
+                    uint32_t w[4];
+#pragma unroll
+                    for (int j = 0; j < 4; ++j)
+                        w[j] = (uint32_t)float_to_bf16_bits(f[2 * j]) | ((uint32_t)float_to_bf16_bits(f[2 * j + 1]) << 16);
+                    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.q_out) + o) = make_uint4(w[0], w[1], w[2], w[3]);
+                } else {
+                    store8_f32(reinterpret_cast<float*>(a.q_out) + o, f);
+                }
             }
         }
         return;
@@ -152,8 +185,12 @@ __global__ void __launch_bounds__(kApThreads) kv_append_kernel(KvAppendArgs a, i
             load8<TA>(a.k, e, k);
             load8<TA>(a.v, e, v);
         }
-        rotate8(a, piece, lane, pos, live, k);
+        Turn turn;
+        turn.load(a, piece, lane, pos, live);
+        turn.apply(a, k);
     };
+    // (n == 0 writes no block, and base may lie behind the table)
+    const int page = n > 0 ? c.table[(size_t)s * c.max_pages + (base >> c.ps_shift)] : -1;
     const int pos = base + row;
     const bool old = pos < L, live = pos < end;
     float k[8] = {}, v[8] = {};
@@ -161,17 +198,7 @@ __global__ void __launch_bounds__(kApThreads) kv_append_kernel(KvAppendArgs a, i
         load8_f32(c.kt + tail, k);
         load8_f32(c.vt + tail, v);
     }
-    {
-        float kn[8] = {}, vn[8] = {};
-        fresh(pos, live && !old, kn, vn);
-        if (live && !old) {
-#pragma unroll
-            for (int j = 0; j < 8; ++j) {
-                k[j] = kn[j];
-                v[j] = vn[j];
-            }
-        }
-    }
+    fresh(pos, live && !old, k, v);  // (a row of the tail stays as it is)
     // the block's maxima, as the bits of |x|: their order is that of the
     // numbers, and a NaN is above them all
     uint32_t mk = 0, mv = 0;
@@ -195,7 +222,6 @@ __global__ void __launch_bounds__(kApThreads) kv_append_kernel(KvAppendArgs a, i
     mk = max(mk, __float_as_uint(kKvTiny));
     mv = max(mv, __float_as_uint(kKvTiny));
     if (n > 0) {
-        const int page = c.table[(size_t)s * c.max_pages + (base >> c.ps_shift)];
         if (page < 0 || page >= c.n_pages) {
             if (tid == 0) atomicOr(c.err, ERR_KV_PAGE);
         } else {
@@ -224,14 +250,27 @@ __global__ void __launch_bounds__(kApThreads) kv_append_kernel(KvAppendArgs a, i
     }
 }
 
+// QH: heads of the queries that a thread rotates.
+template <typename TA, int QH>
+cudaError_t launch_append(const KvAppendArgs& a, long blocks, cudaStream_t st) {
+    const long rows = (long)a.T * ((a.Hq + QH - 1) / QH);
+    const long qctas = (rows + kApThreads / kPieces - 1) / (kApThreads / kPieces);
+    const dim3 grid((unsigned)(blocks * a.c.Hkv + qctas), (unsigned)a.c.S);
+    return launch_pdl(kv_append_kernel<TA, QH>, grid, dim3(kApThreads), 0, st, a, (int)blocks);
+}
+
 }  // namespace
 
 cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t st) {
     const long blocks = ((long)kKvBlock - 1 + a.T + kKvBlock - 1) / kKvBlock;  // the most a session touches
-    const long qctas = ((long)a.T * a.Hq + kApThreads / kPieces - 1) / (kApThreads / kPieces);
-    const dim3 grid((unsigned)(blocks * a.c.Hkv + qctas), (unsigned)a.c.S);
-    return a.bf16 ? launch_pdl(kv_append_kernel<bf16_t>, grid, dim3(kApThreads), 0, st, a, (int)blocks)
-                  : launch_pdl(kv_append_kernel<float>, grid, dim3(kApThreads), 0, st, a, (int)blocks);
+    // One head a thread spreads few queries over the GPU; from two CTAs an SM
+    // on, several heads a thread read the factors once and have their loads in
+    // flight together (16,384 positions x 40 heads in bf16: 157 us with one,
+    // 97 with two, 88 with four, 98 with eight; 1,505 x 40 in fp32, whose loads
+    // are twice as wide: 13.5 with one, 11.4 with two, 11.8 with four).
+    const bool many = (long)a.c.S * a.T * a.Hq / 4 >= (long)2 * 152 * (kApThreads / kPieces);
+    if (a.bf16) return many ? launch_append<bf16_t, 4>(a, blocks, st) : launch_append<bf16_t, 1>(a, blocks, st);
+    return many ? launch_append<float, 2>(a, blocks, st) : launch_append<float, 1>(a, blocks, st);
 }
 
 }  // namespace m2
