@@ -9,8 +9,8 @@
 // attn_paged_rows_kernel: few rows (single frames). A kv head's rows are its
 // (query, head) pairs, row = t R + r, taken 8 or 16 at a time. Bound by HBM:
 // every cached key and value is read once for 8 or 16 rows, 256 bytes and
-// 32 scale-bits a position and kv head. One CTA ("walker") takes a run of
-// 64-position chunks of one (session, kv head, row group): a producer warp
+// 32 scale-bits a position and kv head. One CTA ("walker") takes every W-th
+// 64-position chunk of one (session, kv head, row group): a producer warp
 // keeps a ring of TMA copies in flight (a page, or the part of one that lies
 // in the chunk, is one box of 128-byte rows; the scales come by 4-byte
 // asynchronous copies on the same barrier), and each of four warps takes 16
@@ -81,11 +81,35 @@ struct RwSmem {
     static constexpr uint32_t kRecv = kScales + kStages * 2 * kRwWarps * 4;
     static constexpr uint32_t kBar = kRecv + kSlots * kRwSlotF * 4;          // full, empty [kStages]
     static constexpr uint32_t kFlag = kBar + 2 * kStages * 8;
-    static constexpr uint32_t kBytes = kFlag + 16 + 1024;                    // + slack to align to 1024
+    static constexpr uint32_t kKeys = kFlag + 16;                            // int [kRwThreads + 1]: the sessions' ranking
+    static constexpr uint32_t kBytes = kKeys + (kRwThreads + 1) * 4 + 1024;  // + slack to align to 1024
     // the warps' merge, over the ring: acc [warp][row][128], then (m, l, mv)
     static constexpr uint32_t kMl = kRwWarps * kRows * kKvD * 4;
     static_assert(kMl + kRwWarps * kRows * 4 * 4 <= kScales, "the merge fits in the ring");
     static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two CTAs an SM");
+};
+
+// A lane's 32 dims of a query row: 4t .. 4t + 3 of each 16, as loaded.
+template <typename TA>
+struct QueryRow {
+    using Four = typename std::conditional<sizeof(TA) == 2, uint2, float4>::type;
+    Four w[8];
+    __device__ __forceinline__ void load(const PagedAttnArgs& a, int s, int g, int R, int row, int t) {
+        const size_t at = ((size_t)s * a.T + row / R) * a.q_stride + (size_t)(g * R + row % R) * kKvD + 4 * t;
+        const char* p = reinterpret_cast<const char*>(a.q) + at * sizeof(TA);
+#pragma unroll
+        for (int u = 0; u < 8; ++u) w[u] = __ldg(reinterpret_cast<const Four*>(p + 16 * u * sizeof(TA)));
+    }
+    __device__ __forceinline__ void get(int u, float (&x)[4]) const {
+        if constexpr (sizeof(TA) == 2) {
+            x[0] = __uint_as_float(w[u].x << 16);
+            x[1] = __uint_as_float(w[u].x & 0xFFFF0000u);
+            x[2] = __uint_as_float(w[u].y << 16);
+            x[3] = __uint_as_float(w[u].y & 0xFFFF0000u);
+        } else {
+            x[0] = w[u].x, x[1] = w[u].y, x[2] = w[u].z, x[3] = w[u].w;
+        }
+    }
 };
 
 // grid (W x Hkv x row groups, S), a cluster of W walkers when W > 1.
@@ -93,7 +117,7 @@ struct RwSmem {
 template <typename TA, int NT, int TERMS>
 __global__ void __launch_bounds__(kRwThreads, 2)
     attn_paged_rows_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap tmk,
-                           const __grid_constant__ CUtensorMap tmv, int W) {
+                           const __grid_constant__ CUtensorMap tmv, int W, bool ranked) {
     using L = RwSmem<NT>;
     constexpr int ST = L::kStages;
     extern __shared__ uint8_t rw_raw[];
@@ -104,7 +128,8 @@ __global__ void __launch_bounds__(kRwThreads, 2)
     uint64_t* empty = full + ST;
     volatile uint32_t* flag = reinterpret_cast<uint32_t*>(sm + L::kFlag);
     const KvCache& c = a.c;
-    const int wk = (int)blockIdx.x % W, pair = (int)blockIdx.x / W, s = blockIdx.y;
+    const int wk = (int)blockIdx.x % W, pair = (int)blockIdx.x / W;
+    int s = blockIdx.y;
     const int g = pair % c.Hkv, row0 = pair / c.Hkv * L::kRows;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int R = a.Hq / c.Hkv;
@@ -120,28 +145,57 @@ __global__ void __launch_bounds__(kRwThreads, 2)
     if (W > 1) tc::cluster_arrive_relaxed();  // waited on before the first remote store: every walker has started
     pdl_wait();  // the queries and the cache may come from the previous kernel
     pdl_trigger();
+    if (ranked) {
+        // More CTAs than the GPU holds at once, in the order of blockIdx: the
+        // sessions by their lengths, the longest first, so that none of them is
+        // still at work alone at the end. (At most a session a thread.)
+        int* key = reinterpret_cast<int*>(sm + L::kKeys);
+        const int mine = tid >= c.S ? 0 : a.n_new && a.n_new[tid] <= 0 ? -1 : a.lens[tid];
+        key[tid] = mine;
+        __syncthreads();
+        if (tid < c.S) {
+            int rank = 0;
+#pragma unroll 8
+            for (int u = 0; u < c.S; ++u) rank += key[u] > mine || (key[u] == mine && u < tid);
+            if (rank == (int)blockIdx.y) key[kRwThreads] = tid;
+        }
+        __syncthreads();
+        s = key[kRwThreads];
+    }
+    // what does not need the session's length is on its way beside it: the
+    // page numbers of the first chunks (a lane an entry, ppc a chunk) ...
+    const int ppc = c.ps < kRwTc ? kRwTc >> c.ps_shift : 1;
+    auto entry = [&](int k) -> int {
+        const long i = ((long)(wk + (k + lane / ppc) * W) * kRwTc >> c.ps_shift) + lane % ppc;
+        return i < c.max_pages ? c.table[(size_t)s * c.max_pages + i] : 0;
+    };
+    int page_ids = warp == kRwWarps ? entry(0) : 0;
+    // ... and the queries (rows past the session's new ones are read, not used)
+    QueryRow<TA> q[NT];
+    if (warp < kRwWarps) {
+#pragma unroll
+        for (int f = 0; f < NT; ++f) q[f].load(a, s, g, R, min(row0 + 8 * f + (lane >> 2), a.T * R - 1), lane & 3);
+    }
     int before, n;
     const bool ok = kv_extent(c, s, a.T, a.lens, a.n_new, a.causal ? c.capacity() : c.capacity() + a.T, &before, &n) &&
                     before <= c.capacity();
     if (!ok && blockIdx.x == 0 && tid == 0) atomicOr(c.err, ERR_ATTN_LENGTH);
     const int rows = min(n * R - row0, (int)L::kRows);
     if (rows <= 0) return;  // the whole cluster
-    // positions that this group's last row sees, in chunks, and this walker's run of them
+    // positions that this group's last row sees, and this walker's chunks of
+    // them: wk, wk + W, ...
     const int total = !ok ? 0 : a.causal ? before + (row0 + rows - 1) / R + 1 : before;
-    const int nch = (total + kRwTc - 1) / kRwTc, cpw = (nch + W - 1) / W;
-    const int cb = wk * cpw, ce = min(cb + cpw, nch);
+    const int nch = (total + kRwTc - 1) / kRwTc, nc = nch > wk ? (nch - wk + W - 1) / W : 0;
     __syncthreads();  // the barriers are initialised
 
     if (warp == kRwWarps) {
         // ---------------------------------------------------------- producer
-        const int* table = c.table + (size_t)s * c.max_pages;
         const int box = min(c.ps, kRwTc), pieces = kRwTc / box;  // rows a copy, copies a chunk
-        const int last_page = (total - 1) >> c.ps_shift;
-        int held = -32, page_ids = 0;  // this lane's entry of table[held .. held + 31]
+        int held = 0;  // the first chunk whose pages the lanes hold
         bool good = true;
-        for (int ch = cb; ch < ce && good; ++ch) {
-            const int st = (ch - cb) % ST;
-            const uint32_t round = (uint32_t)((ch - cb) / ST);
+        for (int k = 0; k < nc && good; ++k) {
+            const int st = k % ST;
+            const uint32_t round = (uint32_t)(k / ST);
             if (round > 0 && !tc::mbar_wait(empty + st, (round - 1) & 1)) {
                 if (lane == 0) atomicOr(c.err, ERR_MBAR_TIMEOUT_LOAD);
                 *flag = 1;
@@ -149,23 +203,24 @@ __global__ void __launch_bounds__(kRwThreads, 2)
             }
             good = __all_sync(0xffffffffu, good);
             if (!good) break;
-            const int p0 = ch * kRwTc, left = min(kRwTc, total - p0);  // positions to load
-            const int first = p0 >> c.ps_shift;
-            if (first + 4 > held + 32 || held < 0) {  // a chunk lies in at most four pages
-                held = first;
-                page_ids = first + lane <= last_page ? table[first + lane] : 0;
-                if (page_ids < 0 || page_ids >= c.n_pages) {
-                    atomicOr(c.err, ERR_KV_PAGE);
-                    page_ids = 0;  // some page of the pool: what is read is unused or undefined
-                }
-                __syncwarp();
+            const int p0 = (wk + k * W) * kRwTc, left = min(kRwTc, total - p0);  // positions to load
+            if (k - held == 32 / ppc) {
+                held = k;
+                page_ids = entry(k);
             }
+            const int at0 = (k - held) * ppc;  // lane of the chunk's first page
+            if (lane >= at0 && lane < at0 + ppc && p0 + ((lane - at0) << c.ps_shift) < total &&
+                (page_ids < 0 || page_ids >= c.n_pages)) {
+                atomicOr(c.err, ERR_KV_PAGE);
+                page_ids = 0;  // some page of the pool: what is read is undefined
+            }
+            __syncwarp();
             uint8_t* dst = sm + st * 2 * kRwTile;
             const int live = (left + box - 1) / box;
             if (lane == 0) tc::mbar_arrive_expect_tx(full + st, (uint32_t)(live * box * kKvD * 2));
             __syncwarp();
             for (int i = 0; i < pieces; ++i) {
-                const int page = __shfl_sync(0xffffffffu, page_ids, first + i - held);
+                const int page = __shfl_sync(0xffffffffu, page_ids, at0 + i);
                 if (i < live && lane == 0) {
                     const int y = (page * c.Hkv + g) * c.ps + (p0 & (c.ps - 1));  // (0 for pages of at most a chunk)
                     tc::tma_load_2d(dst + i * box * kKvD, &tmk, 0, y, full + st);
@@ -175,7 +230,7 @@ __global__ void __launch_bounds__(kRwThreads, 2)
             // the chunk's scales: lanes 0 .. 3 the keys' four blocks, 4 .. 7 the values'
             {
                 const int b = lane & (kRwWarps - 1), p = p0 + b * kKvBlock;
-                const int page = __shfl_sync(0xffffffffu, page_ids, min((p >> c.ps_shift) - held, 31));
+                const int page = __shfl_sync(0xffffffffu, page_ids, at0 + (b * kKvBlock >> c.ps_shift));
                 if (lane < 2 * kRwWarps && p < total) {
                     const size_t at = (((size_t)page * c.Hkv + g) << (c.ps_shift - 4)) + ((p & (c.ps - 1)) >> 4);
                     cp_async4(scales + st * 2 * kRwWarps + lane, (lane < kRwWarps ? c.ks : c.vs) + at);
@@ -207,21 +262,10 @@ __global__ void __launch_bounds__(kRwThreads, 2)
         int lim[NT][2];
 #pragma unroll
         for (int f = 0; f < NT; ++f) {
-            const int row = row0 + min(8 * f + gq, rows - 1);  // (rows past the last read it again)
-            const size_t at = ((size_t)s * a.T + row / R) * a.q_stride + (size_t)(g * R + row % R) * kKvD + 4 * t;
             float x[8][4], top = 0.f;
 #pragma unroll
             for (int u = 0; u < 8; ++u) {
-                if constexpr (sizeof(TA) == 2) {
-                    const uint2 w = __ldg(reinterpret_cast<const uint2*>(reinterpret_cast<const uint16_t*>(a.q) + at + 16 * u));
-                    x[u][0] = __uint_as_float(w.x << 16);
-                    x[u][1] = __uint_as_float(w.x & 0xFFFF0000u);
-                    x[u][2] = __uint_as_float(w.y << 16);
-                    x[u][3] = __uint_as_float(w.y & 0xFFFF0000u);
-                } else {
-                    const float4 w = __ldg(reinterpret_cast<const float4*>(reinterpret_cast<const float*>(a.q) + at + 16 * u));
-                    x[u][0] = w.x, x[u][1] = w.y, x[u][2] = w.z, x[u][3] = w.w;
-                }
+                q[f].get(u, x[u]);
 #pragma unroll
                 for (int e = 0; e < 4; ++e) top = fmaxf(top, fabsf(x[u][e]));
             }
@@ -248,16 +292,16 @@ __global__ void __launch_bounds__(kRwThreads, 2)
             }
         }
         bool good = true;
-        for (int ch = cb; ch < ce; ++ch) {
-            const int st = (ch - cb) % ST;
-            if (!tc::mbar_wait(full + st, (uint32_t)((ch - cb) / ST) & 1)) {
+        for (int k = 0; k < nc; ++k) {
+            const int st = k % ST;
+            if (!tc::mbar_wait(full + st, (uint32_t)(k / ST) & 1)) {
                 atomicOr(c.err, ERR_MBAR_TIMEOUT_LOAD);
                 *flag = 1;
                 good = false;
             }
             good = __all_sync(0xffffffffu, good);
             if (!good) break;
-            const int p0 = ch * kRwTc + 16 * warp;  // this warp's block
+            const int p0 = (wk + k * W) * kRwTc + 16 * warp;  // this warp's block
             if (p0 < total) {
                 uint8_t* sV = sm + st * 2 * kRwTile + kRwTile + warp * 16 * kKvD;
                 const uint32_t kb = tc::smem_u32(sV - kRwTile), vb = tc::smem_u32(sV);
@@ -389,59 +433,76 @@ __global__ void __launch_bounds__(kRwThreads, 2)
     }
     __syncthreads();
     if (W > 1) tc::cluster_wait();  // every walker of the cluster has started: its shared memory is there
-    auto write = [&](int r, float o, float lsum, float from) {  // row r of the group, dim tid
+    // A warp takes a row and a lane four of its dims. This walker's (acc, m, l,
+    // mv) of row r, each relative to the walker's own references, go to the
+    // row's owner: slot (r / W) W + wk of walker r % W.
+    auto write = [&](int r, const float (&o)[4], float sum, float from) {
         const int row = row0 + r;
-        const size_t at = ((size_t)s * a.T + row / R) * a.out_stride + (size_t)(g * R + row % R) * kKvD + tid;
-        store_act<TA>(a.out, at, lsum == 0.f ? 0.f : o / lsum * from);  // a row that sees nothing: zeros
+        const size_t at = ((size_t)s * a.T + row / R) * a.out_stride + (size_t)(g * R + row % R) * kKvD + 4 * lane;
+        const float f = sum == 0.f ? 0.f : 1.f / sum;
+        float y[4];
+#pragma unroll
+        for (int e = 0; e < 4; ++e) y[e] = sum == 0.f ? 0.f : o[e] * f * from;  // a row that sees nothing: zeros
+        if constexpr (sizeof(TA) == 2) {
+            const uint32_t w0 = (uint32_t)float_to_bf16_bits(y[0]) | ((uint32_t)float_to_bf16_bits(y[1]) << 16);
+            const uint32_t w1 = (uint32_t)float_to_bf16_bits(y[2]) | ((uint32_t)float_to_bf16_bits(y[3]) << 16);
+            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) = make_uint2(w0, w1);
+        } else {
+            *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
+        }
     };
-    // this walker's (acc, m, l, mv) of each row, to the row's owner: slot
-    // (r / W) W + wk of walker r % W
-    if (tid < kKvD) {
-        for (int r = 0; r < rows; ++r) {
-            float M = kNone, V = kNone;
+    for (int r = warp; r < rows; r += kRwThreads / 32) {
+        float4 x[kRwWarps], y[kRwWarps];
+        float M = kNone, V = kNone, sum = 0.f, o[4] = {0.f, 0.f, 0.f, 0.f};
 #pragma unroll
-            for (int w = 0; w < kRwWarps; ++w) {
-                const float4 x = sml[w * L::kRows + r];
-                M = fmaxf(M, x.x);
-                V = fmaxf(V, x.z);
-            }
-            float o = 0.f, sum = 0.f;
+        for (int w = 0; w < kRwWarps; ++w) {
+            x[w] = sml[w * L::kRows + r];
+            y[w] = *reinterpret_cast<const float4*>(sacc + (w * L::kRows + r) * kKvD + 4 * lane);
+            M = fmaxf(M, x[w].x);
+            V = fmaxf(V, x[w].z);
+        }
 #pragma unroll
-            for (int w = 0; w < kRwWarps; ++w) {
-                const float4 x = sml[w * L::kRows + r];
-                o = fmaf(ex2_approx(x.z - V), sacc[(w * L::kRows + r) * kKvD + tid], o);
-                sum = fmaf(ex2_approx(x.x - M), x.y, sum);
-            }
-            if (W == 1) {
-                write(r, o, sum, ex2_approx(V - M - 15.f));
-            } else {
-                const uint32_t slot = tc::smem_u32(recv + ((r / W) * W + wk) * kRwSlotF), owner = (uint32_t)(r % W);
-                tc::st_cluster_f32(tc::cluster_map(slot + 4u * tid, owner), o);
-                if (tid == 0) {
-                    tc::st_cluster_f32x2(tc::cluster_map(slot + 4u * kKvD, owner), make_float2(M, sum));
-                    tc::st_cluster_f32(tc::cluster_map(slot + 4u * (kKvD + 2), owner), V);
-                }
-            }
+        for (int w = 0; w < kRwWarps; ++w) {
+            const float f = ex2_approx(x[w].z - V);
+            o[0] = fmaf(f, y[w].x, o[0]), o[1] = fmaf(f, y[w].y, o[1]);
+            o[2] = fmaf(f, y[w].z, o[2]), o[3] = fmaf(f, y[w].w, o[3]);
+            sum = fmaf(ex2_approx(x[w].x - M), x[w].y, sum);
+        }
+        if (W == 1) {
+            write(r, o, sum, ex2_approx(V - M - 15.f));
+        } else {
+            const uint32_t slot = tc::cluster_map(tc::smem_u32(recv + ((r / W) * W + wk) * kRwSlotF), (uint32_t)(r % W));
+            st_cluster_f32x4(slot + 16u * lane, make_float4(o[0], o[1], o[2], o[3]));
+            if (lane == 0) st_cluster_f32x4(slot + 4u * kKvD, make_float4(M, sum, V, 0.f));
         }
     }
     if (W == 1) return;
     tc::cluster_arrive();  // the stores into the owners' slots are visible ...
     tc::cluster_wait();    // ... once every walker has made them
-    if (tid < kKvD) {
-        for (int r = wk; r < rows; r += W) {
-            const float* sl = recv + (r / W) * W * kRwSlotF;
-            float M = kNone, V = kNone;
-            for (int w = 0; w < W; ++w) {
-                M = fmaxf(M, sl[w * kRwSlotF + kKvD]);
-                V = fmaxf(V, sl[w * kRwSlotF + kKvD + 2]);
-            }
-            float o = 0.f, sum = 0.f;
-            for (int w = 0; w < W; ++w) {
-                o = fmaf(ex2_approx(sl[w * kRwSlotF + kKvD + 2] - V), sl[w * kRwSlotF + tid], o);
-                sum = fmaf(ex2_approx(sl[w * kRwSlotF + kKvD] - M), sl[w * kRwSlotF + kKvD + 1], sum);
-            }
-            write(r, o, sum, ex2_approx(V - M - 15.f));
+    for (int r = wk + W * warp; r < rows; r += W * (kRwThreads / 32)) {
+        const float* sl = recv + (r / W) * W * kRwSlotF;
+        // lane w: walker w's references and sum
+        const float4 x = lane < W ? *reinterpret_cast<const float4*>(sl + lane * kRwSlotF + kKvD) : make_float4(kNone, 0.f, kNone, 0.f);
+        float M = x.x, V = x.z;
+#pragma unroll
+        for (int off = 1; off < kRwMaxW; off <<= 1) {
+            M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+            V = fmaxf(V, __shfl_xor_sync(0xffffffffu, V, off));
         }
+        M = __shfl_sync(0xffffffffu, M, 0), V = __shfl_sync(0xffffffffu, V, 0);
+        float sum = ex2_approx(x.x - M) * x.y;
+#pragma unroll
+        for (int off = 1; off < kRwMaxW; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+        sum = __shfl_sync(0xffffffffu, sum, 0);
+        const float fw = ex2_approx(x.z - V);
+        float o[4] = {0.f, 0.f, 0.f, 0.f};
+#pragma unroll 4
+        for (int w = 0; w < W; ++w) {
+            const float f = __shfl_sync(0xffffffffu, fw, w);
+            const float4 y = *reinterpret_cast<const float4*>(sl + w * kRwSlotF + 4 * lane);
+            o[0] = fmaf(f, y.x, o[0]), o[1] = fmaf(f, y.y, o[1]), o[2] = fmaf(f, y.z, o[2]), o[3] = fmaf(f, y.w, o[3]);
+        }
+        write(r, o, sum, ex2_approx(V - M - 15.f));
     }
 }
 
@@ -519,7 +580,8 @@ cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = W > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, attn_paged_rows_kernel<TA, NT, TERMS>, a, tmk, tmv, W);
+    const bool ranked = a.c.S > 1 && a.c.S <= kRwThreads && pairs * W > 2 * 152;
+    return cudaLaunchKernelEx(&cfg, attn_paged_rows_kernel<TA, NT, TERMS>, a, tmk, tmv, W, ranked);
 }
 
 }  // namespace

@@ -50,6 +50,12 @@ __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
 }
 
+// 16 bytes into a cluster's shared window
+__device__ __forceinline__ void st_cluster_f32x4(uint32_t caddr, float4 v) {
+    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(caddr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
+                 : "memory");
+}
+
 // The power of two that takes a row's largest magnitude to [2^to, 2^(to + 1))
 // (1 for a row of zeros; the power is kept at 2^126 at most).
 __device__ __forceinline__ float row_power(float amax, int to) {

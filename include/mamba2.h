@@ -505,8 +505,8 @@ m2_status mamba2_lm_prefill(const m2_lm* m, int n_sessions, int T, void* hidden,
  * k_pages, v_pages [n_pages, n_kv_heads, page_size, head_dim] bytes; k_scales,
  * v_scales [n_pages, n_kv_heads, page_size / 16] fp32; tails
  * [n_sessions, n_kv_heads, 16, head_dim] fp32; page_table
- * [n_sessions, max_pages] int32 (entries past a session's positions are not
- * read). The tails are used by mamba2_kv_append only; k_tail_out and
+ * [n_sessions, max_pages] int32 (entries past a session's positions may be
+ * anything). The tails are used by mamba2_kv_append only; k_tail_out and
  * v_tail_out may be k_tail and v_tail (the tail updated in place), otherwise
  * they must not overlap them. `act` is the dtype of the rows that go in and
  * out (keys, values, queries, outputs).

@@ -339,6 +339,22 @@ def test_long_cache_split_over_the_gpu(m2, act, T):
     _check(cache, q, got, [L], [T], True, D ** -0.5, act)
 
 
+@pytest.mark.parametrize("S", [80, 200])
+def test_more_sessions_than_the_gpu_holds(m2, S):
+    """Single frames of many sessions of all lengths, some equal, some empty,
+    some without a new position: the order in which they run is not theirs."""
+    rng = np.random.default_rng(S)
+    lengths = [int(x) for x in rng.choice([0, 1, 17, 60, 64, 65, 130], S)]
+    new = [int(x) for x in rng.choice([1, 1, 1, 0], S)]
+    Hkv = 4 if S == 80 else 2
+    cache = _fill(m2, 91, S, Hkv, 16, "bf16", [L + n for L, n in zip(lengths, new)])
+    q, _ = _rows(92, S, 1, 3 * Hkv, "bf16")
+    got = cache.attend(q, True, _int(new), lengths=_int(lengths))
+    _check(cache, q, got, lengths, new, True, D ** -0.5, "bf16")
+    got = cache.attend(q, False, _int(new), lengths=_int(lengths))
+    _check(cache, q, got, lengths, new, False, D ** -0.5, "bf16")
+
+
 @pytest.mark.parametrize("T", [2, 40])
 def test_uneven_scales_and_large_scores(m2, T):
     """Values of some blocks a million times smaller or all zero, queries that
