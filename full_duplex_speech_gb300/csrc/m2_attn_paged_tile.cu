@@ -32,6 +32,7 @@
 // shared memory, each the owner of 256 / W rows.
 #include <cuda_fp8.h>
 #include <float.h>
+#include <math.h>
 
 #include <mutex>
 
@@ -49,7 +50,7 @@ constexpr uint32_t kTlTile = kTlTc * kKvD;         // 16 KB of codes
 constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kScStages = kKStages + 1;
 constexpr float kSlack = 15.f;                     // log2 by which a chunk may exceed the references
 constexpr uint32_t kColO = 0, kColS = 256;         // tensor memory: O of the two tiles, then S (and w over it)
-constexpr int kTlMaxW = 8;
+constexpr int kTlMaxW = 8;                         // (16, not portable: 39 us for 26, 65 rows over 7,500 positions)
 
 struct TlSmem {
     static constexpr uint32_t kQ = 0;                                    // [tile][hi, lo] 16 KB, K-major, 128-byte swizzle
@@ -63,7 +64,7 @@ struct TlSmem {
     static constexpr uint32_t kTmem = kBar + kBars * 8;
     static constexpr uint32_t kFlag = kTmem + 4;
     static constexpr uint32_t kBytes = kFlag + 4 + 1024;  // + slack to align to 1024
-    // after the walk, over the rings: 256 / W rows x W walkers x 128 floats, then their (l, m, mv)
+    // after the walk, over the rings: 256 rows x 128 floats, then their (m, l, mv)
     static constexpr uint32_t kMl = 2 * kTlRows * kKvD * 4;
     static_assert(kMl + 2 * kTlRows * 16 <= kSc, "the merge fits in the rings");
     static_assert(kBytes <= 227 * 1024, "one CTA an SM");
@@ -572,12 +573,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
         }
     }
     __syncthreads();
-    const int own = 2 * kTlRows / W;  // rows that a CTA of the cluster owns
-    if (W > 1) {
-        tc::cluster_wait();    // every CTA has started ...
-        tc::cluster_arrive();  // ... and is done with its rings
-        tc::cluster_wait();
-    }
+    if (W > 1) tc::cluster_wait();  // (pairs with the arrival at the start)
     if (warp >= 8) {
         const int i = (warp - 8) >> 2, row = tid - 256;
         const uint32_t tO = tm + ((uint32_t)((warp & 3) * 32) << 16) + kColO + 128 * i;
@@ -588,8 +584,6 @@ __global__ void __launch_bounds__(kTlThreads, 1)
         uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + ((size_t)s * a.T + rr / R) * a.out_stride +
                         (size_t)(g * R + rr % R) * kKvD;
         const float f = l == 0.f ? 0.f : ex2_approx(mv - m) / l;
-        const uint32_t slot = tc::smem_u32(sm) + (uint32_t)((wk * own + row % own) * kKvD * 4);
-        const uint32_t owner = (uint32_t)(row / own);
 #pragma unroll
         for (int q = 0; q < 4; ++q) {
             float v[32];
@@ -614,40 +608,46 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                 // 16-byte pieces rotated by the row, so that a warp's rows do not meet in one bank
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
-                    st_cluster_f32x4(tc::cluster_map(slot + (uint32_t)(((8 * q + k + row) & 31) << 4), owner),
-                                     make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]));
+                    *reinterpret_cast<float4*>(sm + row * kKvD * 4 + (((8 * q + k + row) & 31) << 4)) =
+                        make_float4(v[4 * k], v[4 * k + 1], v[4 * k + 2], v[4 * k + 3]);
             }
             __syncwarp();
         }
-        if (W > 1 && live)
-            st_cluster_f32x4(tc::cluster_map(tc::smem_u32(sm + L::kMl) + (uint32_t)((wk * own + row % own) * 16), owner),
-                             make_float4(m, l, mv, 0.f));
+        if (W > 1 && live) *reinterpret_cast<float4*>(sm + L::kMl + row * 16) = make_float4(m, l, mv, 0.f);
     }
     tc::tc_fence_before();
     __syncthreads();
     if (warp == 1) tc::tmem_dealloc(tm, 512);
     if (W == 1) return;
-    tc::cluster_arrive();  // the stores into the owners' memory are visible ...
-    tc::cluster_wait();    // ... once every CTA has made them
-    // this CTA's rows, a warp a row, four dims a lane:
+    tc::cluster_arrive();  // every CTA's rows are in its shared memory ...
+    tc::cluster_wait();
+    // ... and each reads the rows that it owns, a warp a row, four dims a lane
+    // (a row's 512 bytes in one go; sent by the threads that hold them, 16 bytes
+    // here and there, they took 1 to 3 us more):
     // out = 2^(V - M) sum_w 2^(mv_w - V) O_w / sum_w 2^(m_w - M) l_w
-    const float4* ml = reinterpret_cast<const float4*>(sm + L::kMl);
-    for (int r = warp; r < own; r += kTlThreads / 32) {
-        const int row = wk * own + r;
-        if (row >= rows) break;
-        float M = kNone, V = kNone;
-        for (int w = 0; w < W; ++w) {
-            M = fmaxf(M, ml[w * own + r].x);
-            V = fmaxf(V, ml[w * own + r].z);
+    const int own = 2 * kTlRows / W;
+    const uint32_t base = tc::smem_u32(sm);
+    for (int row = wk * own + warp; row < min((wk + 1) * own, rows); row += kTlThreads / 32) {
+        float4 x[kTlMaxW], y[kTlMaxW];
+#pragma unroll
+        for (int w = 0; w < kTlMaxW; ++w) {
+            if (w < W) {
+                x[w] = ld_cluster_f32x4(tc::cluster_map(base + L::kMl + row * 16, w));
+                y[w] = ld_cluster_f32x4(tc::cluster_map(base + row * kKvD * 4 + (((lane + row) & 31) << 4), w));
+            }
         }
+        float M = kNone, V = kNone, sum = 0.f;
         float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        float sum = 0.f;
-        for (int w = 0; w < W; ++w) {
-            const float4 x = ml[w * own + r];
-            const float f = ex2_approx(x.z - V);
-            const float4 y = *reinterpret_cast<const float4*>(sm + (uint32_t)((w * own + r) * kKvD * 4) + (((lane + row) & 31) << 4));
-            o.x = fmaf(f, y.x, o.x), o.y = fmaf(f, y.y, o.y), o.z = fmaf(f, y.z, o.z), o.w = fmaf(f, y.w, o.w);
-            sum = fmaf(ex2_approx(x.x - M), x.y, sum);
+#pragma unroll
+        for (int w = 0; w < kTlMaxW; ++w)
+            if (w < W) M = fmaxf(M, x[w].x), V = fmaxf(V, x[w].z);
+#pragma unroll
+        for (int w = 0; w < kTlMaxW; ++w) {
+            if (w < W) {
+                const float f = ex2_approx(x[w].z - V);
+                o.x = fmaf(f, y[w].x, o.x), o.y = fmaf(f, y[w].y, o.y), o.z = fmaf(f, y[w].z, o.z), o.w = fmaf(f, y[w].w, o.w);
+                sum = fmaf(ex2_approx(x[w].x - M), x[w].y, sum);
+            }
         }
         const float f = ex2_approx(V - M) / sum;
         const bool none = sum == 0.f;  // a row that sees nothing: zeros
@@ -658,16 +658,26 @@ __global__ void __launch_bounds__(kTlThreads, 1)
         const uint32_t w1 = (uint32_t)float_to_bf16_bits(none ? 0.f : o.z * f) | ((uint32_t)float_to_bf16_bits(none ? 0.f : o.w * f) << 16);
         *reinterpret_cast<uint2*>(out) = make_uint2(w0, w1);
     }
+    tc::cluster_arrive();  // nobody leaves while its memory is read
+    tc::cluster_wait();
 }
 
-cudaError_t tile_setup() {
+// Per device, once: the kernel's attributes, and how many clusters of 1, 2, 4
+// and 8 CTAs the device holds at once.
+struct TlSetup {
+    bool done;
+    int held[4];
+};
+
+cudaError_t tile_setup(const TlSetup** out) {
     static std::mutex mutex;
-    static bool done[64];
+    static TlSetup per_device[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     std::lock_guard<std::mutex> lock(mutex);
-    if (!done[dev & 63]) {
+    TlSetup& u = per_device[dev & 63];
+    if (!u.done) {
         // the warps' register split draws on what the launch gives
         cudaFuncAttributes fa;
         e = cudaFuncGetAttributes(&fa, attn_paged_tile_kernel);
@@ -675,15 +685,35 @@ cudaError_t tile_setup() {
         if (fa.numRegs < kRegsLaunch) return cudaErrorLaunchOutOfResources;
         e = cudaFuncSetAttribute(attn_paged_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)TlSmem::kBytes);
         if (e != cudaSuccess) return e;
-        done[dev & 63] = true;
+        u.held[0] = 152;
+        for (int k = 1; k < 4; ++k) {
+            cudaLaunchConfig_t cfg = {};
+            cfg.gridDim = dim3(1u << k);
+            cfg.blockDim = dim3(kTlThreads);
+            cfg.dynamicSmemBytes = TlSmem::kBytes;
+            cudaLaunchAttribute attr[1];
+            attr[0].id = cudaLaunchAttributeClusterDimension;
+            attr[0].val.clusterDim.x = 1u << k;
+            attr[0].val.clusterDim.y = 1;
+            attr[0].val.clusterDim.z = 1;
+            cfg.attrs = attr;
+            cfg.numAttrs = 1;
+            int held = 0;
+            if (cudaOccupancyMaxActiveClusters(&held, attn_paged_tile_kernel, &cfg) != cudaSuccess) held = 0;
+            u.held[k] = held;
+        }
+        (void)cudaGetLastError();  // a refused query leaves no sticky error
+        u.done = true;
     }
+    *out = &u;
     return cudaSuccess;
 }
 
 }  // namespace
 
 cudaError_t launch_attn_paged_tiles(const PagedAttnArgs& a, cudaStream_t st) {
-    cudaError_t e = tile_setup();
+    const TlSetup* setup = nullptr;
+    cudaError_t e = tile_setup(&setup);
     if (e != cudaSuccess) return e;
     CUtensorMap tmk, tmv;
     e = make_page_map(a.c.kp, a.c, kTlTc, &tmk);
@@ -691,8 +721,21 @@ cudaError_t launch_attn_paged_tiles(const PagedAttnArgs& a, cudaStream_t st) {
     if (e != cudaSuccess) return e;
     const long groups = ((long)a.T * (a.Hq / a.c.Hkv) + 2 * kTlRows - 1) / (2 * kTlRows);
     const long pairs = (long)a.c.S * a.c.Hkv * groups, chunks = (a.c.capacity() + kTlTc - 1) / kTlTc;
+    // CTAs that share a pair's positions: the least of rounds x (chunks each
+    // walks + 5 for a CTA's start and end, + 2 for the merge), in chunks.
+    // Several sessions are mostly shorter than the table's reach, so that a
+    // last round counts by its part; one session's CTAs are all alike. (Six
+    // sessions catching up by at most 75 positions over at most 3,076, 96
+    // pairs: 47 us with one CTA a pair, 34 with two, 43 with four; 2 x 300 rows
+    // across to 1,500 positions: 31, 25 and 43.)
     int W = 1;
-    while (2 * W <= kTlMaxW && pairs * 2 * W <= 152 && 4 * W <= chunks) W *= 2;
+    float least = 0.f;
+    for (int k = 0, w = 1; k < 4 && (w == 1 || w <= chunks) && setup->held[k] > 0; ++k, w *= 2) {
+        const float part = (float)pairs / (float)setup->held[k];
+        const float rounds = a.c.S == 1 ? ceilf(part) : fmaxf(1.f, part);
+        const float cost = rounds * (float)((chunks + w - 1) / w + 5 + (w > 1 ? 2 : 0));
+        if (w == 1 || cost < least) W = w, least = cost;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(W * groups * a.c.Hkv), a.c.S);
     cfg.blockDim = dim3(kTlThreads);

@@ -56,6 +56,16 @@ __device__ __forceinline__ void st_cluster_f32x4(uint32_t caddr, float4 v) {
                  : "memory");
 }
 
+// ... and out of it
+__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t caddr) {
+    float4 v;
+    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
+                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
+                 : "r"(caddr)
+                 : "memory");
+    return v;
+}
+
 // The power of two that takes a row's largest magnitude to [2^to, 2^(to + 1))
 // (1 for a row of zeros; the power is kept at 2^126 at most).
 __device__ __forceinline__ float row_power(float amax, int to) {
