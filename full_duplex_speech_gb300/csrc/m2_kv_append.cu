@@ -2,15 +2,15 @@
 // position rotation of keys (and queries) applied on the way.
 //
 // A block of 16 positions of one kv head shares one fp32 scale:
-//     m = max(max |block|, 2^-100), scale = m / 448, code = e4m3(x * (448 / m)),
-// e4m3 by rounding to nearest even, the one rounding that a cached value
-// gets. The positions of the block that is still open are kept in fp32 (the
+//     m = max(max |block|, 2^-100), scale = m / 448, code = e4m3(448 x / m),
+// the quotient rounded once, to nearest even: the one rounding that a cached
+// value gets. The positions of the block that is still open are kept in fp32 (the
 // tail, rows [0, length mod 16)), so a block is always quantised from its
 // exact values by its own maximum, and the cache does not depend on how the
 // positions were split over calls: a prefill and single frames leave the same
 // bits. The rotation of dims (a, b) of a pair at position t by the table's
 // cos and sin, each product and sum rounded to fp32 by itself (no fused
-// multiply-add, so that the codes are those of the formula as written):
+// multiply-add, so that the results are those of the formula as written):
 //     a' = a cos_t - b sin_t,  b' = a sin_t + b cos_t.
 //
 // Memory-bound: per new position and kv head 2 x 128 activations in and
@@ -23,11 +23,11 @@
 // the pair (d, d + rot / 2) of the half layout sits in another lane of the
 // same half-warp. The maximum goes through shuffles and shared memory. The
 // queries go to CTAs of their own, 16 (position, heads) rows at a time.
-// 4 x 4096 positions with 40 query heads, bf16, 446 MB: 88 us, 5.1 TB/s (76%
-// of the measured copy rate; 34 us without the queries, where a CTA's chain
-// of length, rows, maximum and stores shows: four heads in turn with the next
-// one's rows in flight took 44). One frame: 2.4 us, of 64 sessions 3.8 us,
-// mostly the launch and the chain.
+// 4 x 4096 positions with 40 query heads, bf16, 446 MB: 95 us, 4.7 TB/s (70%
+// of the measured copy rate; 88 us with quotients rounded twice; 34 us of that
+// without the queries, where a CTA's chain of length, rows, maximum and stores
+// shows: four heads in turn with the next one's rows in flight took 44). One
+// frame: 2.6 us, of 64 sessions 4.0 us, mostly the launch and the chain.
 #include <cuda_fp8.h>
 
 #include "m2_common.cuh"
@@ -108,18 +108,56 @@ struct Turn {
     }
 };
 
-__device__ __forceinline__ uint2 pack_e4m3(const float (&f)[8], float inv) {
+// y, which is 448 x / m but for two units in its last place at most, is next
+// to a value halfway between two codes: that value M, or its neighbour on the
+// side of the exact quotient. 448 |x| = p + r exactly (r a fused
+// multiply-add's), and p - M m is exact too, the two being so near.
+__device__ __forceinline__ float settle(float x, float y, float m) {
+    const float down = m > 1e18f ? 0x1p-20f : 1.f;  // (448 |x| stays finite)
+    const float a = fabsf(x) * down, mm = m * down, t = fabsf(y) < 0x1p-6f ? fabsf(y) + 0x1p-6f : fabsf(y);
+    float M = __uint_as_float(((__float_as_uint(t) + 2u - 0x80000u) & ~0xFFFFFu) + 0x80000u);
+    if (fabsf(y) < 0x1p-6f) M -= 0x1p-6f;
+    const float p = __fmul_rn(a, 448.f), r = __fmaf_rn(a, 448.f, -p);
+    const float over = __fadd_rn(__fmaf_rn(-M, mm, p), r);
+    const uint32_t bits = __float_as_uint(M) + (over > 0.f ? 1u : over < 0.f ? ~0u : 0u);
+    return copysignf(__uint_as_float(bits), y);
+}
+
+// The codes e4m3(448 x / m) of 8 values, to nearest even. x (448 / m) in fp32
+// is off by less than two units in its last place, which matters only next to
+// a value halfway between two codes: there the exact quotient decides (bf16
+// values meet such ties in one block of seven or so, where m is a multiple of
+// 7; fp32 values almost never).
+__device__ __forceinline__ uint2 pack_e4m3(const float (&x)[8], float m) {
+    const float inv = __fdiv_rn(kE4m3Max, m);
+    // e4m3 keeps three bits behind the first, so that next to halfway the other
+    // 20 are next to 0x80000; below 2^-6 its step is that of [2^-6, 2^-5)
+    auto off = [](float v) { return (__float_as_uint(v) + 2u - 0x80000u) & 0xFFFFFu; };
+    float y[8], least = 1.f;
+    uint32_t nearest = ~0u;
+#pragma unroll
+    for (int j = 0; j < 8; ++j) {
+        y[j] = __fmul_rn(x[j], inv);
+        nearest = min(nearest, off(y[j]));
+        least = fminf(least, fabsf(y[j]));
+    }
+    if ((nearest <= 4u || least < 0x1p-6f) && m < INFINITY) {
+#pragma unroll
+        for (int j = 0; j < 8; ++j) {
+            const float a = fabsf(y[j]);
+            if (off(a < 0x1p-6f ? a + 0x1p-6f : a) <= 4u) y[j] = settle(x[j], y[j], m);
+        }
+    }
     uint32_t h[4];
 #pragma unroll
     for (int j = 0; j < 4; ++j)
-        h[j] = __nv_cvt_float2_to_fp8x2(make_float2(__fmul_rn(f[2 * j], inv), __fmul_rn(f[2 * j + 1], inv)), __NV_SATFINITE,
-                                        __NV_E4M3);
+        h[j] = __nv_cvt_float2_to_fp8x2(make_float2(y[2 * j], y[2 * j + 1]), __NV_SATFINITE, __NV_E4M3);
     return make_uint2(h[0] | (h[1] << 16), h[2] | (h[3] << 16));
 }
 
 // grid (blocks of a session x kv heads + CTAs of its queries, sessions)
 // QH: heads of the queries that a thread rotates. (bf16: five CTAs an SM, 48
-// registers, 88 us above against 92 with four.)
+// registers, 95 us above against 98 with four.)
 template <typename TA, int QH>
 __global__ void __launch_bounds__(kApThreads, sizeof(TA) == 2 ? 5 : 4) kv_append_kernel(KvAppendArgs a, int blocks) {
     __shared__ uint32_t smax[2][kApThreads / 32];
@@ -228,8 +266,8 @@ __global__ void __launch_bounds__(kApThreads, sizeof(TA) == 2 ? 5 : 4) kv_append
             const size_t at = ((size_t)page * c.Hkv + g) * c.ps + (base & (c.ps - 1));  // row of the block's first position
             if (live) {
                 const size_t o = (at + row) * kKvD + 8 * piece;
-                *reinterpret_cast<uint2*>(c.kp + o) = pack_e4m3(k, __fdiv_rn(kE4m3Max, __uint_as_float(mk)));
-                *reinterpret_cast<uint2*>(c.vp + o) = pack_e4m3(v, __fdiv_rn(kE4m3Max, __uint_as_float(mv)));
+                *reinterpret_cast<uint2*>(c.kp + o) = pack_e4m3(k, __uint_as_float(mk));
+                *reinterpret_cast<uint2*>(c.vp + o) = pack_e4m3(v, __uint_as_float(mv));
             }
             if (tid == 0) {
                 c.ks[at / kKvBlock] = __fdiv_rn(__uint_as_float(mk), kE4m3Max);
@@ -265,9 +303,10 @@ cudaError_t launch_kv_append(const KvAppendArgs& a, cudaStream_t st) {
     const long blocks = ((long)kKvBlock - 1 + a.T + kKvBlock - 1) / kKvBlock;  // the most a session touches
     // One head a thread spreads few queries over the GPU; from two CTAs an SM
     // on, several heads a thread read the factors once and have their loads in
-    // flight together (16,384 positions x 40 heads in bf16: 157 us with one,
-    // 97 with two, 88 with four, 98 with eight; 1,505 x 40 in fp32, whose loads
-    // are twice as wide: 13.5 with one, 11.4 with two, 11.8 with four).
+    // flight together (before the quotients' exact rounding, 16,384 positions
+    // x 40 heads in bf16: 157 us with one, 97 with two, 88 with four, 98 with
+    // eight; 1,505 x 40 in fp32, whose loads are twice as wide: 13.5 with one,
+    // 11.4 with two, 11.8 with four).
     const bool many = (long)a.c.S * a.T * a.Hq / 4 >= (long)2 * 152 * (kApThreads / kPieces);
     if (a.bf16) return many ? launch_append<bf16_t, 4>(a, blocks, st) : launch_append<bf16_t, 1>(a, blocks, st);
     return many ? launch_append<float, 2>(a, blocks, st) : launch_append<float, 1>(a, blocks, st);

@@ -495,7 +495,8 @@ m2_status mamba2_lm_prefill(const m2_lm* m, int n_sessions, int T, void* hidden,
  * p % page_size. Keys and values are e4m3 with one fp32 scale for each block
  * of 16 positions (slots 16 i .. 16 i + 15 of a page) and kv head:
  *     m = max(max |block|, 2^-100), scale = m / 448,
- *     code = e4m3(x * (448 / m))    to nearest even,  value = scale * code
+ *     code = e4m3(448 x / m), rounded once to nearest even,
+ *     value = scale * code
  * The positions of the block that is still open are kept in fp32 as well
  * (the tail: rows [0, length % 16)), so that a block is always quantised from
  * its exact values: the cache holds the same bits however the positions were

@@ -2,10 +2,10 @@
 mamba2_kv_append leaves in the pages, and mamba2_attn_paged's outputs in fp64.
 
 A block of 16 positions of one kv head shares one fp32 scale,
-m = max(max |block|, 2^-100), scale = m / 448, code = e4m3(x * (448 / m)) to
-nearest even, each operation rounded to fp32 as the library's header states
-it, so that codes and scales are compared bit for bit; `rotate64` is the
-rotation in fp64, for the bound against the exact values."""
+m = max(max |block|, 2^-100), scale = m / 448 (in fp32), code =
+e4m3(448 x / m) to nearest even, and the rotation in fp32 operations as the
+library's header states them, so that codes and scales are compared bit for
+bit (`rotate` in fp64 gives the exact values for a bound)."""
 from __future__ import annotations
 
 import numpy as np
@@ -66,7 +66,9 @@ def quantise(rows):
         block = rows[i * BLOCK:(i + 1) * BLOCK]
         m = np.maximum(np.abs(block).max((0, 2)), TINY).astype(np.float32)
         scales[i] = m / np.float32(448)
-        codes[i * BLOCK:(i + 1) * BLOCK] = to_e4m3(block * (np.float32(448) / m)[:, None])
+        # 448 x is exact in fp64, and a quotient of fp32 numbers is no nearer than
+        # 2^-50 of itself to a value halfway between two codes unless it is one
+        codes[i * BLOCK:(i + 1) * BLOCK] = to_e4m3(block.astype(np.float64) * 448 / m.astype(np.float64)[:, None])
     return codes, scales
 
 

@@ -223,6 +223,31 @@ def test_append_against_64_bits_and_extreme_blocks(m2):
     assert np.all(vd[0:16, 0] == 0)
 
 
+@pytest.mark.parametrize("power", [-95, 0, 70, 110])
+def test_quotients_halfway_between_two_codes(m2, power):
+    """448 x / m exactly halfway between two codes where 448 / m is not an fp32
+    number (m = 21 x 2^power), and its fp32 neighbours on either side; codes
+    subnormal and normal, blocks small and huge."""
+    import torch
+    mids = (kv.E4M3[:126] + kv.E4M3[1:127]) / 2
+    x = (mids * 3 / 64).astype(np.float32)
+    assert np.all(x.astype(np.float64) * 448 / 21 == mids)
+    x = np.concatenate((x, np.nextafter(x, np.float32(0)), np.nextafter(x, np.float32(30))))
+    rows = np.zeros((16, 1, D), np.float32)
+    rows.reshape(-1)[:2 * len(x)] = np.concatenate((x, -x))
+    rows[15, 0, 127] = 21
+    rows = np.ldexp(rows, power)
+    cache = Cache(m2, 1, 1, 16, 16, "f32")
+    t = torch.from_numpy(rows[None]).cuda()
+    cache.append(t, t)
+    codes, scales = kv.quantise(rows)
+    kp, vp, ks, vs = cache.host()
+    page = cache.table[0, 0]
+    for p, sc in ((kp, ks), (vp, vs)):
+        _same(p[page, 0], codes[:, 0])
+        _same(sc[page, 0], scales[0])
+
+
 def test_cache_does_not_depend_on_the_split(m2):
     """One call, single frames, and odd pieces leave the same pool and tails."""
     S, Hkv, T, ps = 2, 2, 83, 16

@@ -30,7 +30,7 @@ def test_quantised_values_are_within_half_a_step():
     value = kv.E4M3[codes] * np.repeat(scales.astype(np.float64), kv.BLOCK, 0)[:37, :, None]
     step = np.repeat(scales.astype(np.float64), kv.BLOCK, 0)[:37, :, None]
     # half a step of e4m3, 2^-4 of the value, or 2^-10 of the scale below the
-    # normals; 2^-22: the fp32 roundings of 448 / m and of the product
+    # normals; 2^-22: the fp32 rounding of the scale
     assert np.all(np.abs(value - rows) <= (2.0 ** -4 + 2.0 ** -22) * np.abs(rows) + 2.0 ** -10 * step)
     assert np.all(codes[16:32, 1] == 0) and np.all(scales[1, 1] == kv.TINY / np.float32(448))
 
