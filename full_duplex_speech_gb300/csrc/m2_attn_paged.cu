@@ -305,12 +305,16 @@ __global__ void __launch_bounds__(kRwThreads, 2)
             if (p0 < total) {
                 uint8_t* sV = sm + st * 2 * kRwTile + kRwTile + warp * 16 * kKvD;
                 const uint32_t kb = tc::smem_u32(sV - kRwTile), vb = tc::smem_u32(sV);
-                if (p0 + 16 > total) {  // whatever lies behind the last position counts as zero values
-                    for (int e = lane; e < (p0 + 16 - total) * 8; e += 32)
-                        *reinterpret_cast<uint4*>(sV + (total - p0) * kKvD + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+                const float ks = scales[st * 2 * kRwWarps + warp], vs = scales[st * 2 * kRwWarps + kRwWarps + warp];
+                // whatever lies behind the last position counts as zero values, and so do
+                // those of a block with a scale that is not finite: the rows that see it get
+                // their NaN by the weights, and the others none
+                const int from = fabsf(vs) < INFINITY ? min(total - p0, 16) : 0;
+                if (from < 16) {
+                    for (int e = lane; e < (16 - from) * 8; e += 32)
+                        *reinterpret_cast<uint4*>(sV + from * kKvD + e * 16) = make_uint4(0u, 0u, 0u, 0u);
                     __syncwarp();
                 }
-                const float ks = scales[st * 2 * kRwWarps + warp], vs = scales[st * 2 * kRwWarps + kRwWarps + warp];
                 // S^T (16 positions x 8 rows): lanes 8j .. 8j + 7 address the
                 // 8 x 16-byte piece j: positions + 8 (j & 1), 16-byte unit + (j >> 1)
                 const int fr = (lane & 7) + 8 * ((lane >> 3) & 1), fu = lane >> 4;
@@ -353,7 +357,7 @@ __global__ void __launch_bounds__(kRwThreads, 2)
                         mv[f][e] = vn;
                         const float pa = ex2_approx(x[e] - mn), pc = ex2_approx(x[e + 2] - mn);  // 0 for -inf
                         l[f][e] = fmaf(l[f][e], cl, pa + pc);
-                        const float to = vs == 0.f ? 0.f : vs * ex2_approx(mn - vn + 15.f);
+                        const float to = vs == 0.f || p0 > lim[f][e] ? 0.f : vs * ex2_approx(mn - vn + 15.f);
                         w[e] = pa * to;
                         w[e + 2] = pc * to;
 #pragma unroll
@@ -587,11 +591,6 @@ cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t st) {
 }
 
 }  // namespace
-
-size_t attn_paged_workspace_bytes(const KvCache& c, int T, int Hq, bool bf16) {
-    (void)c, (void)T, (void)Hq, (void)bf16;
-    return 0;
-}
 
 cudaError_t launch_attn_paged(const PagedAttnArgs& a, cudaStream_t st) {
     if (!a.bf16) return launch_rows<float, 1, 2>(a, st);

@@ -337,7 +337,17 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                 if (j >= kHStages && !warp_ok(hempty + h, (uint32_t)(j / kHStages - 1) & 1)) break;
                 const uint8_t* src = sm + L::kV + vs * kTlTile;
                 uint8_t* dst = sm + L::kH + h * 2 * kTlTile;
-                const int left = total - (cb + j) * kTlTc;  // positions behind the last count as zero values
+                // positions behind the last count as zero values, and so do those of a block with a
+                // scale that is not finite: the rows that see it get their NaN by the weights, and
+                // the others none
+                const int left = total - (cb + j) * kTlTc;
+                if (!warp_ok(scfull + j % kScStages, (uint32_t)(j / kScStages) & 1)) break;
+                uint32_t none = 0;  // a bit a block
+                {
+                    const float* sv = scales + j % kScStages * 2 * kTlBlocks + kTlBlocks;
+                    const bool bad = lane < kTlBlocks && !(fabsf(sv[lane & (kTlBlocks - 1)]) < INFINITY);
+                    none = __ballot_sync(0xffffffffu, bad);
+                }
                 // a warp's item: 8 positions (8 pg + k7) x 4 pieces of 16 dims, a piece a lane (16
                 // codes, swizzled) -> two 16-byte pieces of the product's 8 x 8 blocks (MN-major);
                 // all of a chunk's reads are in flight together
@@ -351,7 +361,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
 #pragma unroll
                 for (int n = 0; n < kItems; ++n) {
                     const int it = warp - 4 + 4 * n, pg = it >> 1, sub = 4 * (it & 1) + (lane >> 3);
-                    if (8 * pg + k7 >= left) w[n] = make_uint4(0u, 0u, 0u, 0u);
+                    if (8 * pg + k7 >= left || (none >> (pg >> 1) & 1u)) w[n] = make_uint4(0u, 0u, 0u, 0u);
                     uint4 lo, hi;
                     lo.x = e4m3x2_to_f16x2(w[n].x & 0xFFFFu), lo.y = e4m3x2_to_f16x2(w[n].x >> 16);
                     lo.z = e4m3x2_to_f16x2(w[n].y & 0xFFFFu), lo.w = e4m3x2_to_f16x2(w[n].y >> 16);

@@ -49,9 +49,7 @@ struct PagedAttnArgs {
     void* out;
     long q_stride, out_stride;
     float scale;
-    float* ws;
 };
-size_t attn_paged_workspace_bytes(const KvCache& c, int T, int Hq, bool bf16);
 cudaError_t launch_attn_paged(const PagedAttnArgs& a, cudaStream_t st);
 // the form for many rows, bf16 (m2_attn_paged_tile.cu)
 cudaError_t launch_attn_paged_tiles(const PagedAttnArgs& a, cudaStream_t st);

@@ -602,10 +602,18 @@ m2_status mamba2_kv_append(const m2_kv_cache* c, int T, const int32_t* lengths, 
  *   strides times the element size a multiple of 16 bytes, at least
  *   n_heads * 128. out must not overlap q.
  * Scores, softmax and sums in fp32, out rounded once.
- * Scratch: workspace of at least mamba2_attn_paged_workspace_bytes(...) (NULL
- *   where that is 0), which calls that may overlap on the GPU must not share.
+ * Scratch: workspace of at least mamba2_attn_paged_workspace_bytes(...), which
+ *   is 0 for every size (NULL with 0 bytes is fine): the CTAs that share a
+ *   session's positions merge in shared memory.
+ * Forms: bf16 of up to 48 rows a kv head (T x n_heads / n_kv_heads), and fp32
+ *   of any number, 8 or 16 rows at a time on the warps' matrix instructions;
+ *   bf16 of more rows on the tcgen05 tensor cores, 256 at a time. Both give the
+ *   same sums in a different order (the results agree within rounding).
+ * A block whose scale is infinite or a NaN makes the rows that see it NaN, and
+ *   no others.
  * Errors: M2_EINVAL (also a scale that is not finite), M2_ESHAPE, M2_EALIGN,
- *   M2_EWORKSPACE, M2_EUNSUPPORTED, M2_ECUDA. Seen only on the device, in the
+ *   M2_EUNSUPPORTED, M2_ECUDA. A bounded wait that runs out records 0x101 or
+ *   0x102 (mamba2_device_error). Seen only on the device, in the
  *   error word: 0x104, a negative length or positions past max_pages *
  *   page_size: that session's rows of out are zeros; 0x105, a page number
  *   outside the pool: what the rows that would read it hold is undefined.
@@ -615,8 +623,7 @@ m2_status mamba2_attn_paged(const m2_kv_cache* c, int T, int n_heads, int causal
                             const int32_t* n_new, const void* q, long q_stride, float scale, void* out, long out_stride,
                             void* workspace, size_t workspace_bytes, void* stream);
 
-/* Bytes of device scratch that mamba2_attn_paged needs (0: none, or the sizes
- * are invalid). Only the sizes in `c` are read. */
+/* Bytes of device scratch that mamba2_attn_paged needs: 0 for every size. */
 size_t mamba2_attn_paged_workspace_bytes(const m2_kv_cache* c, int T, int n_heads);
 
 /* Static description of a status code. */

@@ -63,11 +63,8 @@ def test_kv_paged_validation_without_gpu(m2):
     assert att(H=0) == 1 and att(H=44) == 2 and att(scale=float("nan")) == 1 and att(scale=float("inf")) == 1
     assert att(q=None) == 1 and att(o=None) == 1 and att(q=q + 2) == 3 and att(o=out + 8) == 3
     assert att(qs=5119) == 1 and att(os_=5119) == 1 and att(qs=5124) == 3
-    need = m2.mamba2_attn_paged_workspace_bytes(cache(), 4, 40)
-    if need:
-        assert att(wsb=need - 1) == 6 and att(ws=None) == 6 and att(ws=(1 << 30) + 8) == 3
-    assert m2.mamba2_attn_paged_workspace_bytes(cache(D=64), 4, 40) == 0
-    assert m2.mamba2_attn_paged_workspace_bytes(cache(), 4, 41) == 0
+    assert m2.mamba2_attn_paged_workspace_bytes(cache(), 4, 40) == 0  # merges in shared memory
+    assert att(ws=(1 << 30) + 8) == 3 and _past_host_checks(att(cache(S=0), ws=None, wsb=0))
     for S in (0, 2) if NO_GPU else (0,):
         c = cache(S=S)
         assert _past_host_checks(app(c)) and _past_host_checks(app(c, **full, rope=rope())) and _past_host_checks(att(c))

@@ -402,6 +402,30 @@ def test_uneven_scales_and_large_scores(m2, T):
         _check(cache, q, got, [L], [T], True, scale, act)
 
 
+@pytest.mark.parametrize("T,bad", [(9, math.nan), (9, math.inf), (80, math.nan), (80, math.inf)])
+def test_a_block_that_is_not_finite_reaches_only_who_sees_it(m2, T, bad):
+    """NaN or infinite values (and keys) in a block of the new positions: the
+    queries before it are right, those that see it are NaN; its session alone."""
+    import torch
+    act, S, Hkv, L, ps = "bf16", 2, 1, 43, 16
+    first = (L + T - 1) // BLOCK * BLOCK  # the last block's first position
+    for where in "kv":
+        cache = Cache(m2, S, Hkv, ps, L + T, act)
+        rows = {n: _rows(95, S, L + T, Hkv, act)[0] for n in "kv"}
+        rows[where][1, L + T - 1, 0, 5] = bad
+        cache.append(rows["k"], rows["v"])
+        q, _ = _rows(96, S, T, 5, act)
+        got = cache.attend(q, True, None, lengths=_int([L, L]))
+        good = first - L  # queries of session 1 that end before the block
+        assert 0 < good < T
+        new = [T, good]
+        part = got.clone()
+        part[1, good:] = -7.0
+        _check(cache, q, part, [L, L], new, True, D ** -0.5, act)
+        assert bool(torch.isnan(got[1, good:]).any(-1).all())
+        assert m2.mamba2_device_error() == 0
+
+
 @pytest.mark.parametrize("T", [1, 30])
 def test_refused_sessions(m2, T):
     """A negative length, positions past the page table, a page outside the
