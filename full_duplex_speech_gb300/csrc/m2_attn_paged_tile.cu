@@ -12,7 +12,8 @@
 //                   2^-8 of the largest are off by at most 2^-17 of it), at
 //                   the cost of one product in 16 bits and with no
 //                   conversion of the keys;
-//   softmax         one thread a row, S read out of tensor memory in fp32:
+//   softmax         one thread a row, S read out of tensor memory in fp32 with
+//                   each block's maximum (tcgen05.ld.red):
 //                   x = S (scale ks), p = 2^(x - m), l += p, and the weight
 //                   w = p vs 2^(m - mv) to fp16 (2^-11) over S;
 //   O += w V        kind::f16, w from tensor memory, V converted to fp16
@@ -98,6 +99,17 @@ __device__ __forceinline__ void tmem_ld32(uint32_t taddr, float* v) {
           "=r"(r[27]), "=r"(r[28]), "=r"(r[29]), "=r"(r[30]), "=r"(r[31])
         : "r"(taddr));
 }
+// 32 lanes x 16 consecutive columns, and the largest of each lane's 16.
+__device__ __forceinline__ void tmem_ld16_max(uint32_t taddr, float* v, float& top) {
+    uint32_t* r = reinterpret_cast<uint32_t*>(v);
+    uint32_t t;
+    asm volatile(
+        "tcgen05.ld.red.sync.aligned.32x32b.x16.max.f32 {%0,%1,%2,%3,%4,%5,%6,%7,%8,%9,%10,%11,%12,%13,%14,%15}, %16, [%17];"
+        : "=r"(r[0]), "=r"(r[1]), "=r"(r[2]), "=r"(r[3]), "=r"(r[4]), "=r"(r[5]), "=r"(r[6]), "=r"(r[7]), "=r"(r[8]),
+          "=r"(r[9]), "=r"(r[10]), "=r"(r[11]), "=r"(r[12]), "=r"(r[13]), "=r"(r[14]), "=r"(r[15]), "=r"(t)
+        : "r"(taddr));
+    top = __uint_as_float(t);
+}
 __device__ __forceinline__ float max3(float a, float b, float c) {
     float r;
     asm("max.f32 %0, %1, %2, %3;" : "=f"(r) : "f"(a), "f"(b), "f"(c));
@@ -130,7 +142,7 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
     return r;
 }
 // The warpgroup's registers a thread (multiples of 8): the launch's 128 are
-// split into 56 for the copy, product and conversion warps and 200 for the
+// split into 48 for the copy, product and conversion warps and 208 for the
 // softmax warps, and even again before they meet.
 template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
@@ -145,7 +157,7 @@ __device__ __forceinline__ void tile_sync(int i) { asm volatile("barrier.sync %0
 // The softmax warps give back before anyone takes: a warp that is done early
 // must not take what they still wait for.
 __device__ __forceinline__ void all_done() { asm volatile("barrier.sync 1, %0;" ::"n"(kTlThreads) : "memory"); }
-constexpr int kRegsLaunch = 128, kRegsFew = 56, kRegsMany = 200;
+constexpr int kRegsLaunch = 128, kRegsFew = 48, kRegsMany = 208;
 static_assert(256 * kRegsFew + 256 * kRegsMany <= kTlThreads * kRegsLaunch, "the split is covered by the launch's registers");
 
 __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16]) {
@@ -350,26 +362,28 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                 }
                 // a warp's item: 8 positions (8 pg + k7) x 4 pieces of 16 dims, a piece a lane (16
                 // codes, swizzled) -> two 16-byte pieces of the product's 8 x 8 blocks (MN-major);
-                // all of a chunk's reads are in flight together
-                constexpr int kItems = kTlTc / 16;
-                uint4 w[kItems];
+                // the reads of four items are in flight together
+#pragma unroll 1
+                for (int it0 = warp - 4; it0 < kTlTc / 4; it0 += 16) {
+                    uint4 w[4];
 #pragma unroll
-                for (int n = 0; n < kItems; ++n) {
-                    const int it = warp - 4 + 4 * n, sub = 4 * (it & 1) + (lane >> 3);
-                    w[n] = *reinterpret_cast<const uint4*>(src + (8 * (it >> 1) + k7) * kKvD + ((sub ^ k7) << 4));
-                }
+                    for (int n = 0; n < 4; ++n) {
+                        const int it = it0 + 4 * n, sub = 4 * (it & 1) + (lane >> 3);
+                        w[n] = *reinterpret_cast<const uint4*>(src + (8 * (it >> 1) + k7) * kKvD + ((sub ^ k7) << 4));
+                    }
 #pragma unroll
-                for (int n = 0; n < kItems; ++n) {
-                    const int it = warp - 4 + 4 * n, pg = it >> 1, sub = 4 * (it & 1) + (lane >> 3);
-                    if (8 * pg + k7 >= left || (none >> (pg >> 1) & 1u)) w[n] = make_uint4(0u, 0u, 0u, 0u);
-                    uint4 lo, hi;
-                    lo.x = e4m3x2_to_f16x2(w[n].x & 0xFFFFu), lo.y = e4m3x2_to_f16x2(w[n].x >> 16);
-                    lo.z = e4m3x2_to_f16x2(w[n].y & 0xFFFFu), lo.w = e4m3x2_to_f16x2(w[n].y >> 16);
-                    hi.x = e4m3x2_to_f16x2(w[n].z & 0xFFFFu), hi.y = e4m3x2_to_f16x2(w[n].z >> 16);
-                    hi.z = e4m3x2_to_f16x2(w[n].w & 0xFFFFu), hi.w = e4m3x2_to_f16x2(w[n].w >> 16);
-                    uint8_t* o = dst + pg * 2048 + sub * 256 + k7 * 16;
-                    *reinterpret_cast<uint4*>(o) = lo;
-                    *reinterpret_cast<uint4*>(o + 128) = hi;
+                    for (int n = 0; n < 4; ++n) {
+                        const int it = it0 + 4 * n, pg = it >> 1, sub = 4 * (it & 1) + (lane >> 3);
+                        if (8 * pg + k7 >= left || (none >> (pg >> 1) & 1u)) w[n] = make_uint4(0u, 0u, 0u, 0u);
+                        uint4 lo, hi;
+                        lo.x = e4m3x2_to_f16x2(w[n].x & 0xFFFFu), lo.y = e4m3x2_to_f16x2(w[n].x >> 16);
+                        lo.z = e4m3x2_to_f16x2(w[n].y & 0xFFFFu), lo.w = e4m3x2_to_f16x2(w[n].y >> 16);
+                        hi.x = e4m3x2_to_f16x2(w[n].z & 0xFFFFu), hi.y = e4m3x2_to_f16x2(w[n].z >> 16);
+                        hi.z = e4m3x2_to_f16x2(w[n].w & 0xFFFFu), hi.w = e4m3x2_to_f16x2(w[n].w >> 16);
+                        uint8_t* o = dst + pg * 2048 + sub * 256 + k7 * 16;
+                        *reinterpret_cast<uint4*>(o) = lo;
+                        *reinterpret_cast<uint4*>(o + 128) = hi;
+                    }
                 }
                 tc::fence_proxy_async_smem();
                 __syncwarp();
@@ -477,25 +491,26 @@ __global__ void __launch_bounds__(kTlThreads, 1)
             tc::tc_fence_after();
             const int see = lim - (cb + j) * kTlTc;  // columns 0 .. see are seen
             const bool cut = __any_sync(0xffffffffu, see < kTlTc - 1);
-            float v[kTlTc];
+            float v[kTlTc], tops[kTlBlocks];  // the scores, and each block's largest
 #pragma unroll
-            for (int q = 0; q < 4; ++q) tmem_ld32(tS + 32 * q, v + 32 * q);
+            for (int b = 0; b < kTlBlocks; ++b) tmem_ld16_max(tS + 16 * b, v + 16 * b, tops[b]);
             tc::tmem_wait_ld();
             if (cut) {  // the factors of a block that the row does not see may be anything
 #pragma unroll
                 for (int k = 0; k < kTlTc; ++k) v[k] = k <= see ? v[k] : -INFINITY;
 #pragma unroll
-                for (int b = 0; b < kTlBlocks; ++b)
+                for (int b = 0; b < kTlBlocks; ++b) {
+                    const float* w = v + 16 * b;
+                    tops[b] = max3(max3(max3(w[0], w[1], w[2]), max3(w[3], w[4], w[5]), max3(w[6], w[7], w[8])),
+                                   max3(w[9], w[10], w[11]), max3(fmaxf(w[12], w[13]), w[14], w[15]));
                     if (16 * b > see) cxs[b] = 1.f, vss[b] = 0.f, lvs[b] = -INFINITY;
+                }
             }
             // the chunk's maxima: of x, and of x + log2 vs
             float mx = -INFINITY, mvx = -INFINITY;
 #pragma unroll
             for (int b = 0; b < kTlBlocks; ++b) {
-                const float* w = v + 16 * b;
-                const float t = max3(max3(max3(w[0], w[1], w[2]), max3(w[3], w[4], w[5]), max3(w[6], w[7], w[8])),
-                                     max3(w[9], w[10], w[11]), max3(fmaxf(w[12], w[13]), w[14], w[15]));
-                const float x = t * cxs[b];
+                const float x = tops[b] * cxs[b];
                 mx = fmaxf(mx, x);
                 mvx = fmaxf(mvx, x + lvs[b]);
             }
