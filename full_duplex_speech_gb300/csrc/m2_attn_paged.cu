@@ -18,6 +18,10 @@
 // scales are constants of the warp. The walkers of one (session, kv head, row
 // group) form a thread-block cluster and merge through distributed shared
 // memory, so that one launch does it all.
+//   Measured, 40 query and 8 kv heads, bf16: 64 sessions of 40 to 7,500
+// positions 89 us (5.8 TB/s of cache, 87% of a copy's rate); one session over
+// 7,500 positions 9.4 us, over 300 4.4 us, where latency counts: a launch, two
+// rounds of loads, the merge.
 //
 // Codes become fp16 exactly (cvt from e4m3), so the products run on fp16
 // matrix instructions with fp32 sums:
@@ -30,6 +34,8 @@
 //          Blocks whose values are of very different size thus lose nothing
 //          to fp16's range; sums of p (l) stay fp32 and apart.
 //     out = 2^(mv - m - 15) acc / l.
+#include <math.h>
+
 #include <mutex>
 
 #include "m2_paged_dev.cuh"
@@ -531,7 +537,7 @@ cudaError_t rows_setup(const RwSetup** out) {
         e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)RwSmem<NT>::kBytes);
         if (e != cudaSuccess) return e;
         const bool wide = cudaFuncSetAttribute(kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) == cudaSuccess;
-        u.clusters[0] = 1 << 30;
+        u.clusters[0] = 2 * 152;
         for (int k = 1; k < 5; ++k) {
             cudaLaunchConfig_t cfg = {};
             cfg.gridDim = dim3(1u << k);
@@ -565,13 +571,26 @@ cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t st) {
     if (e == cudaSuccess) e = make_page_map(a.c.vp, a.c, kRwTc, &tmv);
     if (e != cudaSuccess) return e;
     const int groups = (a.T * (a.Hq / a.c.Hkv) + 8 * NT - 1) / (8 * NT);
-    // The walkers of a group double while all CTAs stay resident at once (two
-    // an SM of the 152) and while a walker may have more than one chunk (one
-    // session over 300 positions, 40 heads: 4.4 us with 8 walkers of one chunk,
-    // 4.9 with 4).
+    // Walkers: the least time in chunks (of about half a microsecond), with 10
+    // for a CTA's start and end and 2 (4 where many merge) for the merge. The
+    // lengths are on the device; the table's reach stands for them. One
+    // session's walkers are all alike: rounds x a walker's time. Several
+    // sessions are mostly shorter than the reach, say by half: the longest
+    // walker's time, or all of them over the CTAs held at once. (40
+    // query and 8 kv heads, sessions of up to 7,500 positions: 4 sessions 14 us
+    // with 8 walkers, 21 with 4; 12: 25 with 4, 31 with 8, 43 with 2; 24: 42
+    // with 4, 45 with 2; 40: 53 with 2, 66 with 4, 82 with 1; 64: 89 with 1, 93
+    // with 2. One session over 300: 4.4 us with 8, 4.9 with 4.)
     const long pairs = (long)a.c.S * a.c.Hkv * groups, chunks = (a.c.capacity() + kRwTc - 1) / kRwTc;
     int W = 1;
-    for (int k = 1; k < 5 && pairs * 2 * W <= 2 * 152 && W < chunks && pairs <= setup->clusters[k]; ++k) W *= 2;
+    float least = 0.f;
+    for (int k = 0, w = 1; k < 5 && (w == 1 || w < 2 * chunks) && setup->clusters[k] > 0; ++k, w *= 2) {
+        const float part = (float)pairs / (float)setup->clusters[k], walk = (float)((chunks + w - 1) / w);
+        const float cost = a.c.S == 1 ? ceilf(part) * (walk + (w > 1 ? 12.f : 10.f))
+                                      : fmaxf(walk + (w > 1 ? 14.f : 10.f),
+                                              part * ((float)chunks / (float)(2 * w) + (w > 1 ? 14.f : 10.f)));
+        if (w == 1 || cost < least) W = w, least = cost;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(W * groups * a.c.Hkv, a.c.S);
     cfg.blockDim = dim3(kRwThreads);
