@@ -198,7 +198,6 @@ __global__ void __launch_bounds__(kTlThreads, 1)
 
     if (W > 1) tc::cluster_arrive_relaxed();  // waited on before the first remote store: every CTA has started
     pdl_wait();  // the queries and the cache may come from the previous kernel
-    pdl_trigger();
     int before, n;
     const bool ok = kv_extent(c, s, a.T, a.lens, a.n_new, a.causal ? c.capacity() : c.capacity() + a.T, &before, &n) &&
                     before <= c.capacity();
@@ -232,6 +231,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
     __syncthreads();
     tc::tc_fence_after();
     const uint32_t tm = *sTmem;
+    pdl_trigger();  // not before the tensor memory is held: the next kernel may take some before it waits for this one
 
     // A bounded wait; the first that runs out stops the CTA's work.
     auto wait_ok = [&](uint64_t* bar, uint32_t parity) -> bool {
