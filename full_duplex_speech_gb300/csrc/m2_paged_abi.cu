@@ -113,6 +113,7 @@ m2_status mamba2_kv_append(const m2_kv_cache* c, int T, const int32_t* lengths, 
     if (st == M2_OK && (q || q_out)) {
         st = check_rows(c, q, q_stride, (long)n_heads * c->head_dim);
         if (st == M2_OK) st = check_rows(c, q_out, q_out_stride, (long)n_heads * c->head_dim);
+        if (st == M2_OK && q == q_out && q_stride != q_out_stride) return M2_EINVAL;
     }
     if (st != M2_OK) return st;
     if (((long long)T / m2::kKvBlock + 2) * c->n_kv_heads > (1LL << 30)) return M2_ESHAPE;
@@ -160,6 +161,7 @@ m2_status mamba2_attn_paged(const m2_kv_cache* c, int T, int n_heads, int causal
     if (!aligned(lengths, 4) || !aligned(n_new, 4)) return M2_EALIGN;
     st = check_rows(c, q, q_stride, (long)n_heads * c->head_dim);
     if (st == M2_OK) st = check_rows(c, out, out_stride, (long)n_heads * c->head_dim);
+    if (st == M2_OK && out == q) return M2_EINVAL;
     if (st != M2_OK) return st;
     m2::PagedAttnArgs a;
     a.c = cache_of(c);

@@ -562,7 +562,8 @@ typedef struct {
  *   bytes, at least n_kv_heads * 128.
  * q, q_out (both NULL: none): the new positions' queries, rows of
  *   n_heads * 128 activations at q_stride and q_out_stride as above, rotated
- *   like the keys and rounded once; q_out may be q (with the same stride).
+ *   like the keys and rounded once; q_out may be q (with the same stride;
+ *   another one is M2_EINVAL).
  *   Rows t >= n_new[s] of q_out are left as they were.
  * lengths, n_new: int32 [S] in device memory, 4-byte aligned.
  * Written: the codes of the new positions, and of the older ones of the block
@@ -600,7 +601,7 @@ m2_status mamba2_kv_append(const m2_kv_cache* c, int T, const int32_t* lengths, 
  * q, out: rows of n_heads * 128 activations, row s * T + t starting q_stride
  *   (out_stride) * (s * T + t) elements past the pointer; 16-byte aligned,
  *   strides times the element size a multiple of 16 bytes, at least
- *   n_heads * 128. out must not overlap q.
+ *   n_heads * 128. out must not overlap q (M2_EINVAL where it is q).
  * Scores, softmax and sums in fp32, out rounded once.
  * Scratch: workspace of at least mamba2_attn_paged_workspace_bytes(...), which
  *   is 0 for every size (NULL with 0 bytes is fine): the CTAs that share a
@@ -610,7 +611,8 @@ m2_status mamba2_kv_append(const m2_kv_cache* c, int T, const int32_t* lengths, 
  *   bf16 of more rows on the tcgen05 tensor cores, 256 at a time. Both give the
  *   same sums in a different order (the results agree within rounding).
  * A block whose scale is infinite or a NaN makes the rows that see it NaN, and
- *   no others.
+ *   no others. A query row that holds an infinity or a NaN gives NaN where it
+ *   sees any position.
  * Errors: M2_EINVAL (also a scale that is not finite), M2_ESHAPE, M2_EALIGN,
  *   M2_EUNSUPPORTED, M2_ECUDA. A bounded wait that runs out records 0x101 or
  *   0x102 (mamba2_device_error). Seen only on the device, in the

@@ -57,6 +57,7 @@ def test_kv_paged_validation_without_gpu(m2):
     assert app(**full | dict(q=None)) == 1 and app(**full | dict(o=None)) == 1
     assert app(**full | dict(H=41)) == 2 and app(**full | dict(H=0)) == 1 and app(H=-1) == 1
     assert app(**full | dict(qs=5119)) == 1 and app(**full | dict(os_=5124)) == 3 and app(**full | dict(o=qo + 4)) == 3
+    assert app(**full | dict(o=q, os_=5248)) == 1 and att(o=q) == 1  # rotated in place at two strides; out over q
     rope = lambda rot=64, n=10, c=cos, s=sin: m2.rope(rot, n, c, s)  # noqa: E731
     assert app(rope=rope(rot=-16)) == 1 and app(rope=rope(n=0)) == 1 and app(rope=rope(c=None)) == 1
     assert app(rope=rope(rot=24)) == 2 and app(rope=rope(rot=144)) == 2 and app(rope=rope(s=sin + 4)) == 3
