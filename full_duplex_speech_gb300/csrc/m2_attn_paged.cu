@@ -277,7 +277,8 @@ __global__ void __launch_bounds__(kRwThreads, 2)
             }
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 1));
             top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, 2));
-            const float pw = row_power(top, 14), sg = a.scale < 0.f ? -pw : pw;
+            // (a row that holds an infinity reads NaN)
+            const float pw = top < INFINITY ? row_power(top, 14) : NAN, sg = a.scale < 0.f ? -pw : pw;
 #pragma unroll
             for (int u = 0; u < 8; ++u)
 #pragma unroll
@@ -319,6 +320,7 @@ __global__ void __launch_bounds__(kRwThreads, 2)
                 if (from < 16) {
                     for (int e = lane; e < (16 - from) * 8; e += 32)
                         *reinterpret_cast<uint4*>(sV + from * kKvD + e * 16) = make_uint4(0u, 0u, 0u, 0u);
+                    tc::fence_proxy_async_smem();  // ahead of the next copy into the stage
                     __syncwarp();
                 }
                 // S^T (16 positions x 8 rows): lanes 8j .. 8j + 7 address the

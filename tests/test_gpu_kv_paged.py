@@ -426,6 +426,27 @@ def test_a_block_that_is_not_finite_reaches_only_who_sees_it(m2, T, bad):
         assert m2.mamba2_device_error() == 0
 
 
+@pytest.mark.parametrize("act,T", [("bf16", 1), ("bf16", 8), ("bf16", 60), ("f32", 6)])
+@pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
+def test_a_query_that_is_not_finite_reaches_only_its_row(m2, act, T, bad):
+    """An infinity or a NaN in one head of one query gives that row NaN (its
+    softmax has no value), and leaves every other row of the call right; where
+    the row sees nothing it is zeros."""
+    import torch
+    Hkv, R, L = 2, 5, 77
+    cache = _fill(m2, 97, 2, Hkv, 32, act, [L + T] * 2)
+    q, _ = _rows(98, 2, T, Hkv * R, act)
+    clean = cache.attend(q, True, None, lengths=_int([L, L])).clone()
+    dirty = q.clone()
+    dirty[1, T - 1, 3, 17] = bad
+    got = cache.attend(dirty, True, None, lengths=_int([L, L]))
+    assert bool(torch.isnan(got[1, T - 1, 3]).all())
+    got[1, T - 1, 3] = clean[1, T - 1, 3]
+    assert torch.equal(got, clean)
+    assert not bool(cache.attend(dirty, False, None, lengths=_int([0, 0])).any())
+    assert m2.mamba2_device_error() == 0
+
+
 @pytest.mark.parametrize("T", [1, 30])
 def test_refused_sessions(m2, T):
     """A negative length, positions past the page table, a page outside the
