@@ -456,9 +456,8 @@ __global__ void __launch_bounds__(kRwThreads, 2)
 #pragma unroll
         for (int e = 0; e < 4; ++e) y[e] = sum == 0.f ? 0.f : o[e] * f * from;  // a row that sees nothing: zeros
         if constexpr (sizeof(TA) == 2) {
-            const uint32_t w0 = (uint32_t)float_to_bf16_bits(y[0]) | ((uint32_t)float_to_bf16_bits(y[1]) << 16);
-            const uint32_t w1 = (uint32_t)float_to_bf16_bits(y[2]) | ((uint32_t)float_to_bf16_bits(y[3]) << 16);
-            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) = make_uint2(w0, w1);
+            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + at) =
+                make_uint2(pack_bf16x2(y[0], y[1]), pack_bf16x2(y[2], y[3]));
         } else {
             *reinterpret_cast<float4*>(reinterpret_cast<float*>(a.out) + at) = make_float4(y[0], y[1], y[2], y[3]);
         }

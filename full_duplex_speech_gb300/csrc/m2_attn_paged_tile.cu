@@ -58,7 +58,6 @@ constexpr uint32_t kTlTile = kTlTc * kKvD;         // 16 KB of codes
 constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kScStages = kKStages + 1;
 constexpr float kSlack = 15.f;                     // log2 by which a chunk may exceed the references
 constexpr uint32_t kColO = 0, kColS = 256;         // tensor memory: O of the two tiles, then S (and w over it)
-constexpr int kTlMaxW = 8;                         // (16, not portable: 39 us for 26, 65 rows over 7,500 positions)
 
 struct TlSmem {
     static constexpr uint32_t kQ = 0;                                    // [tile][hi, lo] 16 KB, K-major, 128-byte swizzle
@@ -174,6 +173,61 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
         "r"(r[11]), "r"(r[12]), "r"(r[13]), "r"(r[14]), "r"(r[15])
         : "memory");
 }
+// The merge of a cluster's W parts of the rows that CTA wk owns, a warp a row,
+// four dims a lane:
+//     out = 2^(V - M) sum_w 2^(mv_w - V) O_w / sum_w 2^(m_w - M) l_w
+// A warp has 16 / W rows, and all of their parts are on their way together
+// (a row after the other took 12,000 cycles more of a CTA's 45,000 with W = 2);
+// lane i < 16 holds the references of a part of row i / W. A row's parts are
+// taken from the CTA's own on, which needs no other's shared memory.
+template <int W>
+__device__ __forceinline__ void merge_rows(const PagedAttnArgs& a, uint8_t* sm, int wk, int rows, int row0, int s, int g) {
+    constexpr int kWarps = kTlThreads / 32, kParts = 2 * kTlRows / kWarps;  // parts a warp
+    const int lane = threadIdx.x & 31, R = a.Hq / a.c.Hkv;
+    const int first = wk * (2 * kTlRows / W) + (int)(threadIdx.x >> 5);  // the warp's rows: first, first + kWarps, ...
+    if (first >= rows) return;
+    uint32_t from[W];
+#pragma unroll
+    for (int w = 1; w < W; ++w) from[w] = tc::cluster_map(tc::smem_u32(sm), (wk + w) % W);
+    const int mine = min(first + kWarps * ((lane & (kParts - 1)) / W), rows - 1);
+    const float4 x = ld_cluster_f32x4(tc::cluster_map(tc::smem_u32(sm), (wk + lane) % W) + TlSmem::kMl + mine * 16);
+    float4 y[kParts];
+#pragma unroll
+    for (int k = 0; k < kParts; ++k) {
+        const int row = min(first + kWarps * (k / W), rows - 1);
+        const uint32_t at = row * kKvD * 4 + (((lane + row) & 31) << 4);
+        y[k] = k % W ? ld_cluster_f32x4(from[k % W] + at) : *reinterpret_cast<const float4*>(sm + at);
+    }
+    float M = x.x, V = x.z;
+#pragma unroll
+    for (int off = 1; off < W; off <<= 1) {
+        M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+        V = fmaxf(V, __shfl_xor_sync(0xffffffffu, V, off));
+    }
+    const float f = ex2_approx(x.z - V);
+    float sum = ex2_approx(x.x - M) * x.y;
+#pragma unroll
+    for (int off = 1; off < W; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
+    const float whole = sum == 0.f ? 0.f : ex2_approx(V - M) / sum;  // a row that sees nothing: zeros
+    const int rr = row0 + mine;
+    const long at = ((long)s * a.T + rr / R) * a.out_stride + (long)(g * R + rr % R) * kKvD;
+#pragma unroll
+    for (int n = 0; n < kParts / W; ++n) {
+        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+        for (int w = 0; w < W; ++w) {
+            const float fw = __shfl_sync(0xffffffffu, f, n * W + w);
+            const float4 v = y[n * W + w];
+            o.x = fmaf(fw, v.x, o.x), o.y = fmaf(fw, v.y, o.y), o.z = fmaf(fw, v.z, o.z), o.w = fmaf(fw, v.w, o.w);
+        }
+        const float by = __shfl_sync(0xffffffffu, whole, n * W);
+        const long to = __shfl_sync(0xffffffffu, at, n * W);
+        if (first + kWarps * n < rows)
+            *reinterpret_cast<uint2*>(reinterpret_cast<uint16_t*>(a.out) + to + 4 * lane) =
+                make_uint2(pack_bf16x2(o.x * by, o.y * by), pack_bf16x2(o.z * by, o.w * by));
+    }
+}
+
 // grid (W x Hkv x row pairs, S), a cluster of W CTAs when W > 1
 __global__ void __launch_bounds__(kTlThreads, 1)
     attn_paged_tile_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
@@ -613,10 +667,11 @@ __global__ void __launch_bounds__(kTlThreads, 1)
         const bool live = row < rows;
         if (!some) m = mv = kNone, l = 0.f;
         const int rr = row0 + (live ? row : 0);
-        uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + ((size_t)s * a.T + rr / R) * a.out_stride +
-                        (size_t)(g * R + rr % R) * kKvD;
+        const long at = ((long)s * a.T + rr / R) * a.out_stride + (long)(g * R + rr % R) * kKvD;
         const float f = l == 0.f ? 0.f : ex2_approx(mv - m) / l;
-#pragma unroll
+        uint8_t* own = sm + (row & ~31) * 256;  // W == 1: the warp's rows in bf16
+        // (rolled up, here and in the merge: code that runs once goes as fast as it is fetched)
+#pragma unroll 1
         for (int q = 0; q < 4; ++q) {
             float v[32];
             if (some) {
@@ -626,15 +681,14 @@ __global__ void __launch_bounds__(kTlThreads, 1)
 #pragma unroll
                 for (int k = 0; k < 32; ++k) v[k] = 0.f;
             }
-            if (live && W == 1) {
+            if (W == 1) {
 #pragma unroll
                 for (int k = 0; k < 32; k += 8) {
                     uint32_t w[4];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e)
-                        w[e] = (uint32_t)float_to_bf16_bits(l == 0.f ? 0.f : v[k + 2 * e] * f) |
-                               ((uint32_t)float_to_bf16_bits(l == 0.f ? 0.f : v[k + 2 * e + 1] * f) << 16);
-                    *reinterpret_cast<uint4*>(out + 32 * q + k) = make_uint4(w[0], w[1], w[2], w[3]);
+                    for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(v[k + 2 * e] * f, v[k + 2 * e + 1] * f);
+                    *reinterpret_cast<uint4*>(own + lane * 256 + (((4 * q + k / 8) ^ (lane & 15)) << 4)) =
+                        make_uint4(w[0], w[1], w[2], w[3]);
                 }
             } else if (live) {
                 // 16-byte pieces rotated by the row, so that a warp's rows do not meet in one bank
@@ -645,6 +699,18 @@ __global__ void __launch_bounds__(kTlThreads, 1)
             }
             __syncwarp();
         }
+        if (W == 1) {
+            // two rows at a time, 16 lanes a row: whole lines go out (a lane a row took 6,000
+            // cycles a CTA)
+#pragma unroll 4
+            for (int t = 0; t < 16; ++t) {
+                const int r = 2 * t + (lane >> 4), piece = lane & 15;
+                const long to = __shfl_sync(0xffffffffu, at, r);
+                if ((row & ~31) + r < rows)
+                    *reinterpret_cast<uint4*>(reinterpret_cast<uint16_t*>(a.out) + to + 8 * piece) =
+                        *reinterpret_cast<const uint4*>(own + r * 256 + ((piece ^ (r & 15)) << 4));
+            }
+        }
         if (W > 1 && live) *reinterpret_cast<float4*>(sm + L::kMl + row * 16) = make_float4(m, l, mv, 0.f);
     }
     tc::tc_fence_before();
@@ -653,43 +719,13 @@ __global__ void __launch_bounds__(kTlThreads, 1)
     if (W == 1) return;
     tc::cluster_arrive();  // every CTA's rows are in its shared memory ...
     tc::cluster_wait();
-    // ... and each reads the rows that it owns, a warp a row, four dims a lane
-    // (a row's 512 bytes in one go; sent by the threads that hold them, 16 bytes
-    // here and there, they took 1 to 3 us more):
-    // out = 2^(V - M) sum_w 2^(mv_w - V) O_w / sum_w 2^(m_w - M) l_w
-    const int own = 2 * kTlRows / W;
-    const uint32_t base = tc::smem_u32(sm);
-    for (int row = wk * own + warp; row < min((wk + 1) * own, rows); row += kTlThreads / 32) {
-        float4 x[kTlMaxW], y[kTlMaxW];
-#pragma unroll
-        for (int w = 0; w < kTlMaxW; ++w) {
-            if (w < W) {
-                x[w] = ld_cluster_f32x4(tc::cluster_map(base + L::kMl + row * 16, w));
-                y[w] = ld_cluster_f32x4(tc::cluster_map(base + row * kKvD * 4 + (((lane + row) & 31) << 4), w));
-            }
-        }
-        float M = kNone, V = kNone, sum = 0.f;
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-#pragma unroll
-        for (int w = 0; w < kTlMaxW; ++w)
-            if (w < W) M = fmaxf(M, x[w].x), V = fmaxf(V, x[w].z);
-#pragma unroll
-        for (int w = 0; w < kTlMaxW; ++w) {
-            if (w < W) {
-                const float f = ex2_approx(x[w].z - V);
-                o.x = fmaf(f, y[w].x, o.x), o.y = fmaf(f, y[w].y, o.y), o.z = fmaf(f, y[w].z, o.z), o.w = fmaf(f, y[w].w, o.w);
-                sum = fmaf(ex2_approx(x[w].x - M), x[w].y, sum);
-            }
-        }
-        const float f = ex2_approx(V - M) / sum;
-        const bool none = sum == 0.f;  // a row that sees nothing: zeros
-        const int rr = row0 + row;
-        uint16_t* out = reinterpret_cast<uint16_t*>(a.out) + ((size_t)s * a.T + rr / R) * a.out_stride +
-                        (size_t)(g * R + rr % R) * kKvD + 4 * lane;
-        const uint32_t w0 = (uint32_t)float_to_bf16_bits(none ? 0.f : o.x * f) | ((uint32_t)float_to_bf16_bits(none ? 0.f : o.y * f) << 16);
-        const uint32_t w1 = (uint32_t)float_to_bf16_bits(none ? 0.f : o.z * f) | ((uint32_t)float_to_bf16_bits(none ? 0.f : o.w * f) << 16);
-        *reinterpret_cast<uint2*>(out) = make_uint2(w0, w1);
-    }
+    // ... and each reads the rows that it owns
+    if (W == 2)
+        merge_rows<2>(a, sm, wk, rows, row0, s, g);
+    else if (W == 4)
+        merge_rows<4>(a, sm, wk, rows, row0, s, g);
+    else
+        merge_rows<8>(a, sm, wk, rows, row0, s, g);
     tc::cluster_arrive();  // nobody leaves while its memory is read
     tc::cluster_wait();
 }
