@@ -616,8 +616,8 @@ cudaError_t launch_attn_paged(const PagedAttnArgs& a, cudaStream_t st) {
     if (!a.bf16) return launch_rows<float, 1, 2>(a, st);
     // Up to 48 rows (8 or 16 at a time, each time reading the cache again)
     // against a tile that computes 128: 20 rows of one session over 7,500
-    // positions 18 us (tile: 25), of 64 sessions 153 (270); 40 rows 20 (26) and
-    // 194 (230); 65 rows 32 (26) and 287 (250).
+    // positions 18 us (tile: 25), of 64 sessions 146 (262); 40 rows 19 (24) and
+    // 185 (222); 65 rows 31 (24) and 274 (241).
     const long rows = (long)a.T * (a.Hq / a.c.Hkv);
     if (rows > 48) return launch_attn_paged_tiles(a, st);
     return rows <= 8 ? launch_rows<bf16_t, 1, 1>(a, st) : launch_rows<bf16_t, 2, 1>(a, st);

@@ -33,11 +33,14 @@
 // of one pair of tiles and merge through distributed shared memory, each the
 // owner of 256 / W rows.
 //   Measured: 4 sessions of 4096 positions, 40 query and 8 kv heads, causal,
-// 687 GFLOP: 563 us, 1.22 PFLOP/s (65% of a bf16 library product's measured
-// rate). The tensor pipe is active 53% of the time and the issue slots 51%: a
-// chunk of a pair costs its softmax (128 exponentials, and as many scalings
-// and conversions, a thread) and the hand-overs, which the other tile's
-// products hide only in part.
+// 687 GFLOP: 533 us, 1.29 PFLOP/s (69% of a bf16 library product's measured
+// rate). A chunk of a pair takes 2,880 cycles. The warp that issues is held
+// by the products for 2,400 of them; a tile's own round, its softmax (1,130),
+// the hand-overs and the scales (1,200), and 1,020 of products, is as long as
+// that, so that neither alone makes it shorter: an eighth of the products
+// leaves 483 us, no exponentials 527. The scores of the next chunk during the
+// softmax (one S for both tiles, the weights in columns of their own) took
+// 567: the products then wait for one another.
 #include <cuda_fp8.h>
 #include <float.h>
 #include <math.h>
@@ -177,7 +180,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 // four dims a lane:
 //     out = 2^(V - M) sum_w 2^(mv_w - V) O_w / sum_w 2^(m_w - M) l_w
 // A warp has 16 / W rows, and all of their parts are on their way together
-// (a row after the other took 12,000 cycles more of a CTA's 45,000 with W = 2);
+// (a row after the other took 2 us more of a CTA's 24 with W = 2);
 // lane i < 16 holds the references of a part of row i / W. A row's parts are
 // taken from the CTA's own on, which needs no other's shared memory.
 template <int W>
@@ -794,8 +797,8 @@ cudaError_t launch_attn_paged_tiles(const PagedAttnArgs& a, cudaStream_t st) {
     // Several sessions are mostly shorter than the table's reach, so that a
     // last round counts by its part; one session's CTAs are all alike. (Six
     // sessions catching up by at most 75 positions over at most 3,076, 96
-    // pairs: 47 us with one CTA a pair, 34 with two, 43 with four; 2 x 300 rows
-    // across to 1,500 positions: 31, 25 and 43.)
+    // pairs: 46 us with one CTA a pair, 30 with two, 39 with four; 2 x 300 rows
+    // across to 1,500 positions: 29, 22 and 37.)
     int W = 1;
     float least = 0.f;
     for (int k = 0, w = 1; k < 4 && (w == 1 || w <= chunks) && setup->held[k] > 0; ++k, w *= 2) {
