@@ -19,8 +19,8 @@
 // group) form a thread-block cluster and merge through distributed shared
 // memory, so that one launch does it all.
 //   Measured, 40 query and 8 kv heads, bf16: 64 sessions of 40 to 7,500
-// positions 89 us (5.8 TB/s of cache, 87% of a copy's rate); one session over
-// 7,500 positions 9.4 us, over 300 4.4 us, where latency counts: a launch, two
+// positions 86 us (5.9 TB/s of cache, 89% of a copy's rate); one session over
+// 7,500 positions 9.1 us, over 300 4.3 us, where latency counts: a launch, two
 // rounds of loads, the merge.
 //
 // Codes become fp16 exactly (cvt from e4m3), so the products run on fp16
@@ -95,6 +95,10 @@ struct RwSmem {
     static_assert(2 * (kBytes + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 
+struct RwMaps {
+    CUtensorMap kv[2];  // the keys' pages, the values'
+};
+
 // A lane's 32 dims of a query row: 4t .. 4t + 3 of each 16, as loaded.
 template <typename TA>
 struct QueryRow {
@@ -122,8 +126,7 @@ struct QueryRow {
 // TERMS: fp16 terms of a query and of a weight (2 for fp32 activations).
 template <typename TA, int NT, int TERMS>
 __global__ void __launch_bounds__(kRwThreads, 2)
-    attn_paged_rows_kernel(PagedAttnArgs a, const __grid_constant__ CUtensorMap tmk,
-                           const __grid_constant__ CUtensorMap tmv, int W, bool ranked) {
+    attn_paged_rows_kernel(PagedAttnArgs a, const __grid_constant__ RwMaps maps, int W, bool ranked) {
     using L = RwSmem<NT>;
     constexpr int ST = L::kStages;
     extern __shared__ uint8_t rw_raw[];
@@ -148,6 +151,7 @@ __global__ void __launch_bounds__(kRwThreads, 2)
         tc::fence_mbar_init();
         *flag = 0;
     }
+    if (tid == 32) prefetch_map(maps.kv), prefetch_map(maps.kv + 1);
     if (W > 1) tc::cluster_arrive_relaxed();  // waited on before the first remote store: every walker has started
     pdl_wait();  // the queries and the cache may come from the previous kernel
     pdl_trigger();
@@ -225,12 +229,21 @@ __global__ void __launch_bounds__(kRwThreads, 2)
             const int live = (left + box - 1) / box;
             if (lane == 0) tc::mbar_arrive_expect_tx(full + st, (uint32_t)(live * box * kKvD * 2));
             __syncwarp();
-            for (int i = 0; i < pieces; ++i) {
-                const int page = __shfl_sync(0xffffffffu, page_ids, at0 + i);
-                if (i < live && lane == 0) {
+            {
+                // lane i: keys of page i of the chunk, lane 16 + i its values (one lane for all
+                // of them took 1 us more with pages of 16). In one instruction, 64 sessions'
+                // frames take 86 us against 89 in two; with 16 rows, two save the registers
+                // that it spills (187 us against 189 for 40 rows of 64 sessions).
+                const int i = lane & 15;
+                const int page = __shfl_sync(0xffffffffu, page_ids, at0 + min(i, pieces - 1));
+                if (i < live) {
                     const int y = (page * c.Hkv + g) * c.ps + (p0 & (c.ps - 1));  // (0 for pages of at most a chunk)
-                    tc::tma_load_2d(dst + i * box * kKvD, &tmk, 0, y, full + st);
-                    tc::tma_load_2d(dst + kRwTile + i * box * kKvD, &tmv, 0, y, full + st);
+                    if constexpr (NT == 1)
+                        tc::tma_load_2d(dst + (lane >> 4) * kRwTile + i * box * kKvD, maps.kv + (lane >> 4), 0, y, full + st);
+                    else if (lane < 16)
+                        tc::tma_load_2d(dst + i * box * kKvD, maps.kv, 0, y, full + st);
+                    else
+                        tc::tma_load_2d(dst + kRwTile + i * box * kKvD, maps.kv + 1, 0, y, full + st);
                 }
             }
             // the chunk's scales: lanes 0 .. 3 the keys' four blocks, 4 .. 7 the values'
@@ -567,9 +580,9 @@ cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t st) {
     const RwSetup* setup = nullptr;
     cudaError_t e = rows_setup<TA, NT, TERMS>(&setup);
     if (e != cudaSuccess) return e;
-    CUtensorMap tmk, tmv;
-    e = make_page_map(a.c.kp, a.c, kRwTc, &tmk);
-    if (e == cudaSuccess) e = make_page_map(a.c.vp, a.c, kRwTc, &tmv);
+    RwMaps maps;
+    e = make_page_map(a.c.kp, a.c, kRwTc, &maps.kv[0]);
+    if (e == cudaSuccess) e = make_page_map(a.c.vp, a.c, kRwTc, &maps.kv[1]);
     if (e != cudaSuccess) return e;
     const int groups = (a.T * (a.Hq / a.c.Hkv) + 8 * NT - 1) / (8 * NT);
     // Walkers: the least time in chunks (of about half a microsecond), with 10
@@ -607,7 +620,7 @@ cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = W > 1 ? 2 : 1;
     const bool ranked = a.c.S > 1 && a.c.S <= kRwThreads && pairs * W > 2 * 152;
-    return cudaLaunchKernelEx(&cfg, attn_paged_rows_kernel<TA, NT, TERMS>, a, tmk, tmv, W, ranked);
+    return cudaLaunchKernelEx(&cfg, attn_paged_rows_kernel<TA, NT, TERMS>, a, maps, W, ranked);
 }
 
 }  // namespace

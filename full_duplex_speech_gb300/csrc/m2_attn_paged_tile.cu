@@ -253,6 +253,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int R = a.Hq / c.Hkv;
 
+    if (tid == 32) prefetch_map(&tmk), prefetch_map(&tmv);
     if (W > 1) tc::cluster_arrive_relaxed();  // waited on before the first remote store: every CTA has started
     pdl_wait();  // the queries and the cache may come from the previous kernel
     int before, n;

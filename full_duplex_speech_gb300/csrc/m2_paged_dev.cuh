@@ -71,6 +71,11 @@ __device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t caddr) {
     return v;
 }
 
+// The descriptor of the copies to come, fetched ahead of the first.
+__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
+    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
+}
+
 // The power of two that takes a row's largest magnitude to [2^to, 2^(to + 1))
 // (1 for a row of zeros; the power is kept at 2^126 at most).
 __device__ __forceinline__ float row_power(float amax, int to) {
