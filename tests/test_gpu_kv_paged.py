@@ -592,3 +592,58 @@ def test_the_same_call_gives_the_same_bits(m2):
         a = cache.attend(q, True, None, lengths=_int([L])).clone()
         b = cache.attend(q, True, None, lengths=_int([L]))
         assert torch.equal(a, b)
+
+
+@pytest.mark.parametrize("act,S,T,Hq,Hkv,longest", [
+    ("bf16", 30, 1, 24, 8, 2000),   # frames, two CTAs and more to a session, more than the GPU holds
+    ("bf16", 5, 3, 40, 8, 4000),    # 15 rows, eight and more CTAs
+    ("f32", 9, 2, 12, 2, 2047),
+    ("bf16", 6, 75, 40, 8, 1500),   # tiles, shared by two CTAs
+    ("bf16", 2, 75, 40, 8, 2500),   # ... by four
+    ("bf16", 2, 300, 10, 2, 700),   # long runs of rows whose tiles see different numbers of positions
+])
+def test_sessions_of_very_different_ages(m2, act, S, T, Hq, Hkv, longest):
+    """Work along the cache shared by clusters where the sessions' lengths
+    differ: some of a cluster's CTAs have nothing, or see nothing."""
+    rng = np.random.default_rng(S * 1000 + T)
+    lengths = [longest, 0] + [int(x) for x in rng.integers(0, longest, S - 2)]
+    new = [T, T] + [int(x) for x in rng.integers(0, T + 1, S - 2)]
+    cache = _fill(m2, 201, S, Hkv, 32, act, [L + n for L, n in zip(lengths, new)])
+    q, _ = _rows(202, S, T, Hq, act)
+    for causal in (True, False):
+        got = cache.attend(q, causal, _int(new), lengths=_int(lengths))
+        _check(cache, q, got, lengths, new, causal, D ** -0.5, act)
+    assert m2.mamba2_device_error() == 0
+
+
+def test_calls_from_two_threads(m2):
+    """Two host threads, each with its own cache and stream, at once."""
+    import threading
+
+    import torch
+    act, Hkv, ps = "bf16", 2, 64
+    work = []
+    for i, (T, L) in enumerate(((1, 500), (40, 300))):
+        cache = _fill(m2, 211 + i, 1, Hkv, ps, act, [L + T])
+        work.append((cache, _rows(213 + i, 1, T, 8, act)[0], L, T, torch.cuda.Stream()))
+    torch.cuda.synchronize()
+    got, failed = [None, None], []
+
+    def run(i):
+        cache, q, L, T, stream = work[i]
+        try:
+            with torch.cuda.stream(stream):
+                for _ in range(30):
+                    got[i] = cache.attend(q, True, None, lengths=_int([L]))
+                stream.synchronize()
+        except Exception as e:  # noqa: BLE001 (reported by the main thread)
+            failed.append(e)
+
+    threads = [threading.Thread(target=run, args=(i,)) for i in range(2)]
+    for t in threads:
+        t.start()
+    for t in threads:
+        t.join()
+    assert not failed
+    for i, (cache, q, L, T, _) in enumerate(work):
+        _check(cache, q, got[i], [L], [T], True, D ** -0.5, act)
