@@ -203,11 +203,24 @@ def _p(t):
     return t.data_ptr()
 
 
+_current = None
+
+
+def _current_stream():
+    """The current stream's handle, by torch's own functions behind
+    current_device() and current_stream() (a tenth of their time)."""
+    global _current
+    if _current is None:
+        import torch
+        torch.cuda.current_device()  # initialises CUDA
+        raw, device = (getattr(torch._C, n, None) for n in ("_cuda_getCurrentRawStream", "_cuda_getDevice"))
+        _current = (lambda: raw(device())) if raw and device else (lambda: torch.cuda.current_stream().cuda_stream)
+    return _current()
+
+
 def _stream(stream):
     if stream is None:
-        import torch
-        raw = getattr(torch._C, "_cuda_getCurrentRawStream", None)  # a tenth of the time of the Stream object
-        return raw(torch.cuda.current_device()) if raw else torch.cuda.current_stream().cuda_stream
+        return _current_stream()
     if isinstance(stream, int):
         return stream
     return stream.cuda_stream
