@@ -576,13 +576,9 @@ cudaError_t rows_setup(const RwSetup** out) {
 }
 
 template <typename TA, int NT, int TERMS>
-cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t st) {
+cudaError_t plan_rows(const PagedAttnArgs& a, PagedAttnPlan* plan) {
     const RwSetup* setup = nullptr;
     cudaError_t e = rows_setup<TA, NT, TERMS>(&setup);
-    if (e != cudaSuccess) return e;
-    RwMaps maps;
-    e = make_page_map(a.c.kp, a.c, kRwTc, &maps.kv[0]);
-    if (e == cudaSuccess) e = make_page_map(a.c.vp, a.c, kRwTc, &maps.kv[1]);
     if (e != cudaSuccess) return e;
     const int groups = (a.T * (a.Hq / a.c.Hkv) + 8 * NT - 1) / (8 * NT);
     // Walkers: the least time in chunks (of about half a microsecond), with 10
@@ -596,15 +592,29 @@ cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t st) {
     // with 4, 45 with 2; 40: 53 with 2, 66 with 4, 82 with 1; 64: 89 with 1, 93
     // with 2. One session over 300: 4.4 us with 8, 4.9 with 4.)
     const long pairs = (long)a.c.S * a.c.Hkv * groups, chunks = (a.c.capacity() + kRwTc - 1) / kRwTc;
-    int W = 1;
     float least = 0.f;
     for (int k = 0, w = 1; k < 5 && (w == 1 || w < 2 * chunks) && setup->clusters[k] > 0; ++k, w *= 2) {
         const float part = (float)pairs / (float)setup->clusters[k], walk = (float)((chunks + w - 1) / w);
         const float cost = a.c.S == 1 ? ceilf(part) * (walk + (w > 1 ? 12.f : 10.f))
                                       : fmaxf(walk + (w > 1 ? 14.f : 10.f),
                                               part * ((float)chunks / (float)(2 * w) + (w > 1 ? 14.f : 10.f)));
-        if (w == 1 || cost < least) W = w, least = cost;
+        if (w > 1 && cost >= least) continue;
+        least = cost;
+        plan->W = w;
+        // (fitted to 16 rows a walker, bf16)
+        const float start = w > 1 ? 5.5f : 4.5f;
+        plan->us = a.c.S == 1 ? ceilf(part) * (start + 0.7f * walk) : fmaxf(start + 0.6f * walk, part * (start + 0.46f * walk));
     }
+    return cudaSuccess;
+}
+
+template <typename TA, int NT, int TERMS>
+cudaError_t launch_rows(const PagedAttnArgs& a, int W, cudaStream_t st) {
+    RwMaps maps;
+    cudaError_t e = make_page_map(a.c.kp, a.c, kRwTc, &maps.kv[0]);
+    if (e == cudaSuccess) e = make_page_map(a.c.vp, a.c, kRwTc, &maps.kv[1]);
+    if (e != cudaSuccess) return e;
+    const int groups = (a.T * (a.Hq / a.c.Hkv) + 8 * NT - 1) / (8 * NT);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(W * groups * a.c.Hkv, a.c.S);
     cfg.blockDim = dim3(kRwThreads);
@@ -619,21 +629,37 @@ cudaError_t launch_rows(const PagedAttnArgs& a, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = W > 1 ? 2 : 1;
-    const bool ranked = a.c.S > 1 && a.c.S <= kRwThreads && pairs * W > 2 * 152;
+    const bool ranked = a.c.S > 1 && a.c.S <= kRwThreads && (long)a.c.S * a.c.Hkv * groups * W > 2 * 152;
     return cudaLaunchKernelEx(&cfg, attn_paged_rows_kernel<TA, NT, TERMS>, a, maps, W, ranked);
+}
+
+template <typename TA, int NT, int TERMS>
+cudaError_t run_rows(const PagedAttnArgs& a, cudaStream_t st) {
+    PagedAttnPlan plan;
+    const cudaError_t e = plan_rows<TA, NT, TERMS>(a, &plan);
+    return e == cudaSuccess ? launch_rows<TA, NT, TERMS>(a, plan.W, st) : e;
 }
 
 }  // namespace
 
 cudaError_t launch_attn_paged(const PagedAttnArgs& a, cudaStream_t st) {
-    if (!a.bf16) return launch_rows<float, 1, 2>(a, st);
-    // Up to 48 rows (8 or 16 at a time, each time reading the cache again)
-    // against a tile that computes 128: 20 rows of one session over 7,500
-    // positions 18 us (tile: 25), of 64 sessions 146 (262); 40 rows 19 (24) and
-    // 185 (222); 65 rows 31 (24) and 274 (241).
+    if (!a.bf16) return run_rows<float, 1, 2>(a, st);
     const long rows = (long)a.T * (a.Hq / a.c.Hkv);
-    if (rows > 48) return launch_attn_paged_tiles(a, st);
-    return rows <= 8 ? launch_rows<bf16_t, 1, 1>(a, st) : launch_rows<bf16_t, 2, 1>(a, st);
+    if (rows <= 8) return run_rows<bf16_t, 1, 1>(a, st);
+    // Sixteen rows at a time, each time reading the cache again, against tiles
+    // that compute 256 and take 8 us to start and end: by a guess of both times,
+    // whose constants are fitted to 150 calls (one session, several alike or
+    // ragged, 10 to 2,000 rows over 12 to 7,500 positions; the tiles' with a
+    // margin, since where the two are near, long lengths cost the rows more).
+    // One session, 8 kv heads: 60 rows over 12 positions 5.2 us (tiles: 8.4), over
+    // 2,000 9.7 (14.5), over 6,000 16.8 (21.0); 240 rows over 148 6.5 (10.6), over
+    // 2,048 21 (17), over 6,048 48 (25). 64 sessions of up to 7,500: 20 rows 148
+    // (210), 80 rows 278 (189).
+    PagedAttnPlan few, many;
+    cudaError_t e = plan_rows<bf16_t, 2, 1>(a, &few);
+    if (e == cudaSuccess) e = plan_attn_paged_tiles(a, &many);
+    if (e != cudaSuccess) return e;
+    return few.us < 0.85f * many.us ? launch_rows<bf16_t, 2, 1>(a, few.W, st) : launch_attn_paged_tiles(a, many.W, st);
 }
 
 }  // namespace m2

@@ -33,14 +33,14 @@
 // of one pair of tiles and merge through distributed shared memory, each the
 // owner of 256 / W rows.
 //   Measured: 4 sessions of 4096 positions, 40 query and 8 kv heads, causal,
-// 687 GFLOP: 533 us, 1.29 PFLOP/s (69% of a bf16 library product's measured
+// 687 GFLOP: 535 us, 1.28 PFLOP/s (69% of a bf16 library product's measured
 // rate). A chunk of a pair takes 2,880 cycles. The warp that issues is held
 // by the products for 2,400 of them; a tile's own round, its softmax (1,130),
 // the hand-overs and the scales (1,200), and 1,020 of products, is as long as
 // that, so that neither alone makes it shorter: an eighth of the products
 // leaves 483 us, no exponentials 527. The scores of the next chunk during the
 // softmax (one S for both tiles, the weights in columns of their own) took
-// 567: the products then wait for one another.
+// 567 where this took 533: the products then wait for one another.
 #include <cuda_fp8.h>
 #include <float.h>
 #include <math.h>
@@ -805,13 +805,9 @@ cudaError_t tile_setup(const TlSetup** out) {
 
 }  // namespace
 
-cudaError_t launch_attn_paged_tiles(const PagedAttnArgs& a, cudaStream_t st) {
+cudaError_t plan_attn_paged_tiles(const PagedAttnArgs& a, PagedAttnPlan* plan) {
     const TlSetup* setup = nullptr;
-    cudaError_t e = tile_setup(&setup);
-    if (e != cudaSuccess) return e;
-    CUtensorMap tmk, tmv;
-    e = make_page_map(a.c.kp, a.c, kTlTc, &tmk);
-    if (e == cudaSuccess) e = make_page_map(a.c.vp, a.c, kTlTc, &tmv);
+    const cudaError_t e = tile_setup(&setup);
     if (e != cudaSuccess) return e;
     const long groups = ((long)a.T * (a.Hq / a.c.Hkv) + 2 * kTlRows - 1) / (2 * kTlRows);
     const long pairs = (long)a.c.S * a.c.Hkv * groups, chunks = (a.c.capacity() + kTlTc - 1) / kTlTc;
@@ -822,14 +818,25 @@ cudaError_t launch_attn_paged_tiles(const PagedAttnArgs& a, cudaStream_t st) {
     // sessions catching up by at most 75 positions over at most 3,076, 96
     // pairs: 46 us with one CTA a pair, 30 with two, 39 with four; 2 x 300 rows
     // across to 1,500 positions: 29, 22 and 37.)
-    int W = 1;
     float least = 0.f;
     for (int k = 0, w = 1; k < 4 && (w == 1 || w <= chunks) && setup->held[k] > 0; ++k, w *= 2) {
-        const float part = (float)pairs / (float)setup->held[k];
+        const float part = (float)pairs / (float)setup->held[k], walk = (float)((chunks + w - 1) / w);
         const float rounds = a.c.S == 1 ? ceilf(part) : fmaxf(1.f, part);
-        const float cost = rounds * (float)((chunks + w - 1) / w + 5 + (w > 1 ? 2 : 0));
-        if (w == 1 || cost < least) W = w, least = cost;
+        const float cost = rounds * (walk + 5.f + (w > 1 ? 2.f : 0.f));
+        if (w > 1 && cost >= least) continue;
+        least = cost;
+        plan->W = w;
+        plan->us = rounds * ((w > 1 ? 11.f : 8.f) + (a.c.S == 1 ? 1.45f : 1.1f) * walk);
     }
+    return cudaSuccess;
+}
+
+cudaError_t launch_attn_paged_tiles(const PagedAttnArgs& a, int W, cudaStream_t st) {
+    CUtensorMap tmk, tmv;
+    cudaError_t e = make_page_map(a.c.kp, a.c, kTlTc, &tmk);
+    if (e == cudaSuccess) e = make_page_map(a.c.vp, a.c, kTlTc, &tmv);
+    if (e != cudaSuccess) return e;
+    const long groups = ((long)a.T * (a.Hq / a.c.Hkv) + 2 * kTlRows - 1) / (2 * kTlRows);
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(W * groups * a.c.Hkv), a.c.S);
     cfg.blockDim = dim3(kTlThreads);

@@ -606,10 +606,11 @@ m2_status mamba2_kv_append(const m2_kv_cache* c, int T, const int32_t* lengths, 
  * Scratch: workspace of at least mamba2_attn_paged_workspace_bytes(...), which
  *   is 0 for every size (NULL with 0 bytes is fine): the CTAs that share a
  *   session's positions merge in shared memory.
- * Forms: bf16 of up to 48 rows a kv head (T x n_heads / n_kv_heads), and fp32
- *   of any number, 8 or 16 rows at a time on the warps' matrix instructions;
- *   bf16 of more rows on the tcgen05 tensor cores, 256 at a time. Both give the
- *   same sums in a different order (the results agree within rounding).
+ * Forms: fp32, and bf16 of few rows a kv head (T x n_heads / n_kv_heads; how
+ *   many goes by the number of sessions and heads and by max_pages), 8 or 16
+ *   rows at a time on the warps' matrix instructions; bf16 of more rows on the
+ *   tcgen05 tensor cores, 256 at a time. Both give the same sums in a different
+ *   order (the results agree within rounding).
  * A block whose scale is infinite or a NaN makes the rows that see it NaN, and
  *   no others. A query row that holds an infinity or a NaN gives NaN where it
  *   sees any position.

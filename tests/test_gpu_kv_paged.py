@@ -334,6 +334,13 @@ ATTN_CASES = [
     ("bf16", False, 64, 10, 2, [0, 1, 65, 300], [3, 1, 2, 0]),
     ("bf16", False, 16, 40, 8, [251, 0, 16], [33, 40, 7]),
     ("bf16", False, 128, 8, 4, [500, 129], [1, 1]),
+    # many kv heads: the form for many rows
+    ("bf16", True, 32, 160, 32, [77, 0, 5, 128], [9, 23, 0, 16]),
+    ("bf16", True, 16, 160, 32, [0, 40], [130, 77]),
+    ("bf16", True, 128, 32, 32, [3, 300], [200, 257]),
+    ("bf16", True, 64, 96, 8, [1500], [40]),
+    ("bf16", True, 64, 4160, 32, [90], [2]),
+    ("bf16", False, 16, 160, 32, [251, 0, 16], [33, 40, 7]),
     ("f32", True, 64, 12, 2, [0, 1, 63, 64, 500], [1] * 5),
     ("f32", True, 16, 5, 1, [0, 40, 17], [35, 17, 0]),
     ("f32", False, 32, 16, 2, [77, 0, 300], [9, 4, 1]),
@@ -352,7 +359,7 @@ def test_attention(m2, case):
     assert m2.mamba2_device_error() == 0
 
 
-@pytest.mark.parametrize("T", [1, 24])
+@pytest.mark.parametrize("T", [1, 24, 200])
 @pytest.mark.parametrize("act", ["bf16", "f32"])
 def test_long_cache_split_over_the_gpu(m2, act, T):
     """One session, thousands of positions: the work along the cache is split
@@ -380,11 +387,11 @@ def test_more_sessions_than_the_gpu_holds(m2, S):
     _check(cache, q, got, lengths, new, False, D ** -0.5, "bf16")
 
 
-@pytest.mark.parametrize("T", [2, 40])
-def test_uneven_scales_and_large_scores(m2, T):
+@pytest.mark.parametrize("T,Hkv", [(2, 1), (40, 1), (40, 64)])
+def test_uneven_scales_and_large_scores(m2, T, Hkv):
     """Values of some blocks a million times smaller or all zero, queries that
     make one position nearly everything, a negative scale, zero queries."""
-    act, S, Hkv, L, ps = "bf16", 1, 1, 150, 32
+    act, S, L, ps = "bf16", 1, 150, 32
     cache = Cache(m2, S, Hkv, ps, L + T, act)
     (k, _), (v, _) = _rows(21, S, L + T, Hkv, act), _rows(22, S, L + T, Hkv, act)
     v[0, 0:16] *= 2.0 ** -20
@@ -393,7 +400,7 @@ def test_uneven_scales_and_large_scores(m2, T):
     v[0, 80:96] = 0
     k[0, 96:112] *= 2.0 ** -30
     cache.append(k, v)
-    q, _ = _rows(23, S, T, 4, act)
+    q, _ = _rows(23, S, T, 4 * Hkv, act)
     q[0, :, 0] = k[0, 3, 0] * 4   # position 3 (tiny values) nearly alone
     q[0, :, 1] = k[0, 20, 0] * 4  # position 20 (zero values) nearly alone
     q[0, :, 2] = 0
@@ -402,31 +409,33 @@ def test_uneven_scales_and_large_scores(m2, T):
         _check(cache, q, got, [L], [T], True, scale, act)
 
 
-@pytest.mark.parametrize("T,bad", [(9, math.nan), (9, math.inf), (80, math.nan), (80, math.inf)])
-def test_a_block_that_is_not_finite_reaches_only_who_sees_it(m2, T, bad):
+@pytest.mark.parametrize("bad", [math.nan, math.inf])
+@pytest.mark.parametrize("T,Hkv", [(9, 1), (80, 1), (80, 32)])
+def test_a_block_that_is_not_finite_reaches_only_who_sees_it(m2, T, Hkv, bad):
     """NaN or infinite values (and keys) in a block of the new positions: the
     queries before it are right, those that see it are NaN; its session alone."""
     import torch
-    act, S, Hkv, L, ps = "bf16", 2, 1, 43, 16
+    act, S, L, ps = "bf16", 2, 43, 16
     first = (L + T - 1) // BLOCK * BLOCK  # the last block's first position
     for where in "kv":
         cache = Cache(m2, S, Hkv, ps, L + T, act)
         rows = {n: _rows(95, S, L + T, Hkv, act)[0] for n in "kv"}
         rows[where][1, L + T - 1, 0, 5] = bad
         cache.append(rows["k"], rows["v"])
-        q, _ = _rows(96, S, T, 5, act)
+        q, _ = _rows(96, S, T, 5 * Hkv, act)
         got = cache.attend(q, True, None, lengths=_int([L, L]))
         good = first - L  # queries of session 1 that end before the block
         assert 0 < good < T
         new = [T, good]
+        assert not bool(torch.isnan(got[:, :, 5:]).any())  # the other kv heads
         part = got.clone()
         part[1, good:] = -7.0
         _check(cache, q, part, [L, L], new, True, D ** -0.5, act)
-        assert bool(torch.isnan(got[1, good:]).any(-1).all())
+        assert bool(torch.isnan(got[1, good:, :5]).any(-1).all())
         assert m2.mamba2_device_error() == 0
 
 
-@pytest.mark.parametrize("act,T", [("bf16", 1), ("bf16", 8), ("bf16", 60), ("f32", 6)])
+@pytest.mark.parametrize("act,T", [("bf16", 1), ("bf16", 8), ("bf16", 60), ("bf16", 500), ("f32", 6)])
 @pytest.mark.parametrize("bad", [math.inf, -math.inf, math.nan])
 def test_a_query_that_is_not_finite_reaches_only_its_row(m2, act, T, bad):
     """An infinity or a NaN in one head of one query gives that row NaN (its
@@ -447,7 +456,7 @@ def test_a_query_that_is_not_finite_reaches_only_its_row(m2, act, T, bad):
     assert m2.mamba2_device_error() == 0
 
 
-@pytest.mark.parametrize("T", [1, 30])
+@pytest.mark.parametrize("T", [1, 30, 700])
 def test_refused_sessions(m2, T):
     """A negative length, positions past the page table, a page outside the
     pool: the error word tells, the other sessions are right, and a refused
@@ -560,7 +569,7 @@ def test_pool_past_32_bit_offsets(m2):
     far = cache.kp[n_pages - 4:].cpu().numpy()
     np.testing.assert_array_equal(far[np.where(p < ps, 3, 1), :, p % ps], codes)
     assert int(cache.kp[:n_pages - 4].max()) == 0 and m2.mamba2_device_error() == 0
-    for n in (1, 40):
+    for n in (1, 40, T):
         q, _ = _rows(63, 1, n, 40, act)
         got = cache.attend(q, True, None, lengths=_int([T - n]))
         small = Cache(m2, 1, Hkv, ps, T, act)
@@ -568,9 +577,10 @@ def test_pool_past_32_bit_offsets(m2):
         _check(small, q, got, [T - n], [n], True, D ** -0.5, act)
 
 
-def test_two_streams_with_their_own_workspaces(m2):
+@pytest.mark.parametrize("T", [20, 400])
+def test_two_streams_with_their_own_workspaces(m2, T):
     import torch
-    act, Hkv, ps, T = "bf16", 2, 64, 20
+    act, Hkv, ps = "bf16", 2, 64
     caches = [_fill(m2, 70 + i, 1, Hkv, ps, act, [900 + T]) for i in range(2)]
     qs = [_rows(72 + i, 1, T, 8, act)[0] for i in range(2)]
     streams = [torch.cuda.Stream() for _ in range(2)]
@@ -586,7 +596,7 @@ def test_two_streams_with_their_own_workspaces(m2):
 
 def test_the_same_call_gives_the_same_bits(m2):
     import torch
-    for T, L in ((1, 3000), (33, 2000), (300, 0)):
+    for T, L in ((1, 3000), (33, 2000), (300, 0), (1000, 2000)):
         cache = _fill(m2, 80, 1, 1, 32, "bf16", [L + T])
         q, _ = _rows(81, 1, T, 5, "bf16")
         a = cache.attend(q, True, None, lengths=_int([L])).clone()
@@ -623,7 +633,7 @@ def test_calls_from_two_threads(m2):
     import torch
     act, Hkv, ps = "bf16", 2, 64
     work = []
-    for i, (T, L) in enumerate(((1, 500), (40, 300))):
+    for i, (T, L) in enumerate(((1, 500), (400, 900))):
         cache = _fill(m2, 211 + i, 1, Hkv, ps, act, [L + T])
         work.append((cache, _rows(213 + i, 1, T, 8, act)[0], L, T, torch.cuda.Stream()))
     torch.cuda.synchronize()
