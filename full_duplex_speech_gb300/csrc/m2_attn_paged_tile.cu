@@ -811,18 +811,21 @@ cudaError_t plan_attn_paged_tiles(const PagedAttnArgs& a, PagedAttnPlan* plan) {
     if (e != cudaSuccess) return e;
     const long groups = ((long)a.T * (a.Hq / a.c.Hkv) + 2 * kTlRows - 1) / (2 * kTlRows);
     const long pairs = (long)a.c.S * a.c.Hkv * groups, chunks = (a.c.capacity() + kTlTc - 1) / kTlTc;
-    // CTAs that share a pair's positions: the least of rounds x (chunks each
-    // walks + 5 for a CTA's start and end, + 2 for the merge), in chunks.
-    // Several sessions are mostly shorter than the table's reach, so that a
-    // last round counts by its part; one session's CTAs are all alike. (Six
-    // sessions catching up by at most 75 positions over at most 3,076, 96
-    // pairs: 46 us with one CTA a pair, 30 with two, 39 with four; 2 x 300 rows
-    // across to 1,500 positions: 29, 22 and 37.)
+    // CTAs that share a pair's positions: the least time, in chunks (of 1.45 us),
+    // with 5 for a CTA's start and end and 1 for the merge. One session's CTAs
+    // are all alike: rounds x a CTA's time. Several sessions are mostly shorter
+    // than the table's reach: the longest, and where not all CTAs are held at
+    // once, what the others take. (Over 75 calls within 2.2% of the best W on
+    // average. Six sessions catching up by at most 75 positions over at most
+    // 3,076, 96 pairs: 46 us with one CTA a pair, 30 with two, 39 with four; by
+    // 200 over 6,200: 99, 58 and 86; 2 x 300 rows across to 1,500 positions: 29,
+    // 22 and 37.)
     float least = 0.f;
     for (int k = 0, w = 1; k < 4 && (w == 1 || w <= chunks) && setup->held[k] > 0; ++k, w *= 2) {
         const float part = (float)pairs / (float)setup->held[k], walk = (float)((chunks + w - 1) / w);
-        const float rounds = a.c.S == 1 ? ceilf(part) : fmaxf(1.f, part);
-        const float cost = rounds * (walk + 5.f + (w > 1 ? 2.f : 0.f));
+        const float rounds = a.c.S == 1 ? ceilf(part) : fmaxf(1.f, part), ends = w > 1 ? 6.f : 5.f;
+        const float cost = a.c.S == 1 ? rounds * (walk + ends)
+                                      : walk + ends + (part > 1.f ? (part - 0.7f) * (0.3f * walk + ends) : 0.f);
         if (w > 1 && cost >= least) continue;
         least = cost;
         plan->W = w;
