@@ -48,6 +48,7 @@
 #include <mutex>
 
 #include "m2_paged_dev.cuh"
+#include "m2_tile_meet.h"
 
 namespace m2 {
 
@@ -155,14 +156,11 @@ __device__ __forceinline__ float2 add2(float2 a, float2 b) {
 // softmax warps, and even again before they meet.
 template <int N> __device__ __forceinline__ void regs_down() { asm volatile("setmaxnreg.dec.sync.aligned.u32 %0;" ::"n"(N)); }
 template <int N> __device__ __forceinline__ void regs_up() { asm volatile("setmaxnreg.inc.sync.aligned.u32 %0;" ::"n"(N)); }
-// A tile's four softmax warps, and the warp that has seen the operands from
-// memory, hand over to the warp that issues the products: a hardware barrier,
-// since a look at one in shared memory takes some 200 cycles beside the
-// products' own traffic. Every warp makes every meeting, also after a wait
-// that gave up (what the products then read is there, if not what it should
-// be, and the CTA's results are dropped).
-__device__ __forceinline__ void tile_arrive(int i) { asm volatile("barrier.arrive %0, 192;" ::"r"(2 + i) : "memory"); }
-__device__ __forceinline__ void tile_sync(int i) { asm volatile("barrier.sync %0, 192;" ::"r"(2 + i) : "memory"); }
+// The meetings of m2_tile_meet.h on hardware barriers, since a look at one in
+// shared memory takes some 200 cycles beside the products' own traffic.
+struct TileBarriers {
+    __device__ __forceinline__ void sync(int i) const { asm volatile("barrier.sync %0, 192;" ::"r"(2 + i) : "memory"); }
+};
 // The softmax warps give back before anyone takes: a warp that is done early
 // must not take what they still wait for.
 __device__ __forceinline__ void all_done() { asm volatile("barrier.sync 1, %0;" ::"n"(kTlThreads) : "memory"); }
@@ -378,55 +376,47 @@ __global__ void __launch_bounds__(kTlThreads, 1)
             // ---------------------------------------------------------- products
             const bool leader = tc::elect_one();
             const uint32_t sbase = tc::smem_u32(sm);
-            for (int j = 0; j <= nc; ++j) {
-                const int h = (j + kHStages - 1) % kHStages, k8 = j % kKStages;
+            tile_turns_meet(TileBarriers(), nc, nc0, nc1, [](int) {}, [&](int i, int j) {
+                const int nci = i ? nc1 : nc0, h = (j + kHStages - 1) % kHStages, k8 = j % kKStages;
+                tc::tc_fence_after();
+                if (leader) {
+                    if (j > 0) {  // O += w V of chunk j - 1
+                        const uint64_t bd = tc::sdesc(sbase + L::kH + h * 2 * kTlTile, 2048, 128, 0);
 #pragma unroll
-                for (int i = 0; i < 2; ++i) {
-                    const int nci = i ? nc1 : nc0;
-                    if (nci == 0 || j > nci) continue;
-                    tile_sync(i);  // the tile's weights of chunk j - 1 (its q) are whole, and so are the operands
-                    tc::tc_fence_after();
-                    if (leader) {
-                        if (j > 0) {  // O += w V of chunk j - 1
-                            const uint64_t bd = tc::sdesc(sbase + L::kH + h * 2 * kTlTile, 2048, 128, 0);
-#pragma unroll
-                            for (int k = 0; k < 8; ++k)
-                                tc::mma_bf16_tmem_a(tm + kColO + 128 * i, tm + kColS + 128 * i + 8 * k,
-                                                    bd + (uint64_t)(k * 4096 >> 4), idesc_f16_bmn(kTlRows, kKvD),
-                                                    (j > 1 || k > 0) ? 1u : 0u);
-                            // the last tile that reads this V releases it (tile 1 takes every chunk, where there is one)
-                            if (i == 1 || nc1 == 0) tc::mma_commit(hempty + h);
-                        }
-                        if (j < nci) {  // S = q K^T of chunk j, over the weights
-                            const uint64_t bd = tc::sdesc(sbase + L::kK + k8 * kTlTile, 0, 1024, 2);
-#pragma unroll
-                            for (int part = 0; part < 2; ++part) {
-                                const uint64_t ad = tc::sdesc(sbase + L::kQ + (2 * i + part) * kTlTile, 0, 1024, 2);
-#pragma unroll
-                                for (int k = 0; k < 4; ++k)
-                                    mma_f8(tm + kColS + 128 * i, ad + 2 * k, bd + 2 * k, idesc_f8(kTlRows, kTlTc),
-                                           (part > 0 || k > 0) ? 1u : 0u);
-                            }
-                            tc::mma_commit(sfull + i);
-                            if (i == 1 || nc1 == 0) tc::mma_commit(kempty + k8);
-                        } else {
-                            tc::mma_commit(ofull + i);
-                        }
+                        for (int k = 0; k < 8; ++k)
+                            tc::mma_bf16_tmem_a(tm + kColO + 128 * i, tm + kColS + 128 * i + 8 * k,
+                                                bd + (uint64_t)(k * 4096 >> 4), idesc_f16_bmn(kTlRows, kKvD),
+                                                (j > 1 || k > 0) ? 1u : 0u);
+                        // the last tile that reads this V releases it (tile 1 takes every chunk, where there is one)
+                        if (i == 1 || nc1 == 0) tc::mma_commit(hempty + h);
                     }
-                    __syncwarp();
+                    if (j < nci) {  // S = q K^T of chunk j, over the weights
+                        const uint64_t bd = tc::sdesc(sbase + L::kK + k8 * kTlTile, 0, 1024, 2);
+#pragma unroll
+                        for (int part = 0; part < 2; ++part) {
+                            const uint64_t ad = tc::sdesc(sbase + L::kQ + (2 * i + part) * kTlTile, 0, 1024, 2);
+#pragma unroll
+                            for (int k = 0; k < 4; ++k)
+                                mma_f8(tm + kColS + 128 * i, ad + 2 * k, bd + 2 * k, idesc_f8(kTlRows, kTlTc),
+                                       (part > 0 || k > 0) ? 1u : 0u);
+                        }
+                        tc::mma_commit(sfull + i);
+                        if (i == 1 || nc1 == 0) tc::mma_commit(kempty + k8);
+                    } else {
+                        tc::mma_commit(ofull + i);
+                    }
                 }
-            }
+                __syncwarp();
+            });
         } else if (warp == 2) {
             // ------- waits for the operands from memory on behalf of the products
+            // (after one that gave up, what the products read is there, if not what it should be,
+            // and the CTA's results are dropped)
             bool good = true;
-            for (int j = 0; j <= nc; ++j) {
+            tile_turns_meet(TileBarriers(), nc, nc0, nc1, [&](int j) {
                 if (j < nc) good = good && warp_ok(kfull + j % kKStages, (uint32_t)(j / kKStages) & 1);
                 if (j > 0) good = good && warp_ok(hfull + (j - 1) % kHStages, (uint32_t)((j - 1) / kHStages) & 1);
-                for (int i = 0; i < 2; ++i) {
-                    const int nci = i ? nc1 : nc0;
-                    if (nci > 0 && j <= nci) tile_sync(i);
-                }
-            }
+            }, [](int, int) {});
         } else if (warp >= 4) {
             // --------------------------------------------- V to fp16, four warps
             const int k7 = lane & 7;
@@ -654,12 +644,10 @@ __global__ void __launch_bounds__(kTlThreads, 1)
         };
         bool good = true;
         tc::tc_fence_before();
-        if (nci > 0) tile_arrive(i);  // the tile of q is whole
-        for (int j = 0; j < nci; ++j) {
+        tile_rows_meet(TileBarriers(), i, nci, [&](int j) {
             good = good && softmax_chunk(j);
             tc::tc_fence_before();
-            tile_arrive(i);  // the chunk's weights are whole
-        }
+        });
         l = (l0.x + l0.y) + (l1.x + l1.y);
         __syncwarp();
         regs_down<kRegsLaunch>();
