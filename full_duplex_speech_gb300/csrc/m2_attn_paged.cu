@@ -592,6 +592,7 @@ cudaError_t plan_rows(const PagedAttnArgs& a, PagedAttnPlan* plan) {
     // with 4, 45 with 2; 40: 53 with 2, 66 with 4, 82 with 1; 64: 89 with 1, 93
     // with 2. One session over 300: 4.4 us with 8, 4.9 with 4.)
     const long pairs = (long)a.c.S * a.c.Hkv * groups, chunks = (a.c.capacity() + kRwTc - 1) / kRwTc;
+    plan->tiles = false;
     float least = 0.f;
     for (int k = 0, w = 1; k < 5 && (w == 1 || w < 2 * chunks) && setup->clusters[k] > 0; ++k, w *= 2) {
         const float part = (float)pairs / (float)setup->clusters[k], walk = (float)((chunks + w - 1) / w);
@@ -633,22 +634,17 @@ cudaError_t launch_rows(const PagedAttnArgs& a, int W, cudaStream_t st) {
     return cudaLaunchKernelEx(&cfg, attn_paged_rows_kernel<TA, NT, TERMS>, a, maps, W, ranked);
 }
 
-template <typename TA, int NT, int TERMS>
-cudaError_t run_rows(const PagedAttnArgs& a, cudaStream_t st) {
-    PagedAttnPlan plan;
-    const cudaError_t e = plan_rows<TA, NT, TERMS>(a, &plan);
-    return e == cudaSuccess ? launch_rows<TA, NT, TERMS>(a, plan.W, st) : e;
-}
+// bf16 rows that go 8 at a time
+bool few_rows(const PagedAttnArgs& a) { return (long)a.T * (a.Hq / a.c.Hkv) <= 8; }
 
 }  // namespace
 
-cudaError_t launch_attn_paged(const PagedAttnArgs& a, cudaStream_t st) {
+cudaError_t plan_attn_paged(const PagedAttnArgs& a, PagedAttnPlan* plan) {
     // fp32 takes 8 rows at a time: 16 hold 255 registers and one CTA an SM (six
     // sessions catching up 111 us against 109, 20 rows of 64 sessions 240 against
     // 207).
-    if (!a.bf16) return run_rows<float, 1, 2>(a, st);
-    const long rows = (long)a.T * (a.Hq / a.c.Hkv);
-    if (rows <= 8) return run_rows<bf16_t, 1, 1>(a, st);
+    if (!a.bf16) return plan_rows<float, 1, 2>(a, plan);
+    if (few_rows(a)) return plan_rows<bf16_t, 1, 1>(a, plan);
     // Sixteen rows at a time, each time reading the cache again, against tiles
     // that compute 256 and take 8 us to start and end: by a guess of both times,
     // whose constants are fitted to 150 calls (one session, several alike or
@@ -662,7 +658,17 @@ cudaError_t launch_attn_paged(const PagedAttnArgs& a, cudaStream_t st) {
     cudaError_t e = plan_rows<bf16_t, 2, 1>(a, &few);
     if (e == cudaSuccess) e = plan_attn_paged_tiles(a, &many);
     if (e != cudaSuccess) return e;
-    return few.us < 0.85f * many.us ? launch_rows<bf16_t, 2, 1>(a, few.W, st) : launch_attn_paged_tiles(a, many.W, st);
+    *plan = few.us < 0.85f * many.us ? few : many;
+    return cudaSuccess;
+}
+
+cudaError_t launch_attn_paged(const PagedAttnArgs& a, cudaStream_t st) {
+    PagedAttnPlan plan;
+    const cudaError_t e = plan_attn_paged(a, &plan);
+    if (e != cudaSuccess) return e;
+    if (plan.tiles) return launch_attn_paged_tiles(a, plan.W, st);
+    if (!a.bf16) return launch_rows<float, 1, 2>(a, plan.W, st);
+    return few_rows(a) ? launch_rows<bf16_t, 1, 1>(a, plan.W, st) : launch_rows<bf16_t, 2, 1>(a, plan.W, st);
 }
 
 }  // namespace m2

@@ -808,6 +808,7 @@ cudaError_t plan_attn_paged_tiles(const PagedAttnArgs& a, PagedAttnPlan* plan) {
     // 3,076, 96 pairs: 46 us with one CTA a pair, 30 with two, 39 with four; by
     // 200 over 6,200: 99, 58 and 86; 2 x 300 rows across to 1,500 positions: 29,
     // 22 and 37.)
+    plan->tiles = true;
     float least = 0.f;
     for (int k = 0, w = 1; k < 4 && (w == 1 || w <= chunks) && setup->held[k] > 0; ++k, w *= 2) {
         const float part = (float)pairs / (float)setup->held[k], walk = (float)((chunks + w - 1) / w);

@@ -51,12 +51,14 @@ struct PagedAttnArgs {
     float scale;
 };
 cudaError_t launch_attn_paged(const PagedAttnArgs& a, cudaStream_t st);
-// How a form would run a call: the CTAs that share a set of rows' positions,
-// and a guess of its time in microseconds, from the sizes that the host knows.
+// How a call is run: the CTAs that share a set of rows' positions, and a guess
+// of a form's time in microseconds, from the sizes that the host knows.
 struct PagedAttnPlan {
     int W;
     float us;
+    bool tiles;  // the form for many rows
 };
+cudaError_t plan_attn_paged(const PagedAttnArgs& a, PagedAttnPlan* plan);
 // the form for many rows, bf16 (m2_attn_paged_tile.cu)
 cudaError_t plan_attn_paged_tiles(const PagedAttnArgs& a, PagedAttnPlan* plan);
 cudaError_t launch_attn_paged_tiles(const PagedAttnArgs& a, int W, cudaStream_t st);

@@ -185,4 +185,23 @@ m2_status mamba2_attn_paged(const m2_kv_cache* c, int T, int n_heads, int causal
     return launched(m2::launch_attn_paged(a, static_cast<cudaStream_t>(stream)));
 }
 
+// How mamba2_attn_paged would run a call of these sizes, for the tests that are
+// written for one form (not in the public header): the CTAs that share a set of
+// rows' positions, + 256 for the form for many rows; the negative status where
+// the sizes or the device are refused.
+int m2_attn_paged_plan(const m2_kv_cache* c, int T, int n_heads) {
+    m2_status st = check_sizes(c, T);
+    if (st == M2_OK) st = check_heads(c, T, n_heads);
+    if (st == M2_OK) st = m2::check_device();
+    if (st != M2_OK) return -(int)st;
+    m2::PagedAttnArgs a = {};
+    a.c = cache_of(c);
+    a.bf16 = c->act == M2_BF16;
+    a.T = T;
+    a.Hq = n_heads;
+    m2::PagedAttnPlan plan;
+    st = launched(m2::plan_attn_paged(a, &plan));
+    return st == M2_OK ? plan.W + (plan.tiles ? 256 : 0) : -(int)st;
+}
+
 }  // extern "C"
