@@ -15,13 +15,13 @@
 //   softmax         one thread a row, S read out of tensor memory in fp32 with
 //                   each block's maximum (tcgen05.ld.red):
 //                   x = S (scale ks), p = 2^(x - m), l += p, and the weight
-//                   w = p vs 2^(m - mv) to fp16 (2^-11) over S;
+//                   w = p vs 2^(m - mv + 7) to fp16 (2^-11) over S;
 //   O += w V        kind::f16, w from tensor memory, V converted to fp16
 //                   (exactly) by four warps.
 // m and mv (the reference of the weights, a maximum of x + log2 vs) move only
-// when a chunk exceeds them by more than 2^15, which p <= 2^15 in fp32 and
+// when a chunk exceeds them by more than 2^8, which p <= 2^8 in fp32 and
 // w <= 2^15 in fp16 allow; only then is O rescaled in tensor memory.
-//     out = 2^(mv - m) O / l.
+//     out = 2^(mv - m - 7) O / l.
 //
 // Warps: 0 copies (pages by TMA through rings, scales by 4-byte asynchronous
 // copies), 1 issues the products, 2 waits for their operands, 4-7 convert V,
@@ -60,7 +60,14 @@ constexpr int kTlTc = 128;                         // positions per chunk
 constexpr int kTlBlocks = kTlTc / kKvBlock;        // scales of a chunk
 constexpr uint32_t kTlTile = kTlTc * kKvD;         // 16 KB of codes
 constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kScStages = kKStages + 1;
-constexpr float kSlack = 15.f;                     // log2 by which a chunk may exceed the references
+// log2 by which a chunk may exceed m and mv, and log2 of the weight of a position
+// at mv: fp16 reaches from 2^15 down to 2^-24, so that a weight is off by 2^-32 of
+// the one at mv at most, and is dropped below that (a long flat rest behind one
+// dominant position is many of them: with 15 and 0, which took 541 us where this
+// takes 561, 2^20 positions of 2^-25 each lost an eighth of themselves; 5 and 10
+// took 573). 2^(m - mv + 7) and its inverse stay normal for values up to the
+// largest (log2 vs from -109 to 119).
+constexpr float kSlackM = 8.f, kSlackV = 8.f, kLift = 7.f;
 constexpr uint32_t kColO = 0, kColS = 256;         // tensor memory: O of the two tiles, then S (and w over it)
 
 struct TlSmem {
@@ -176,7 +183,7 @@ __device__ __forceinline__ void tmem_st16(uint32_t taddr, const uint32_t (&r)[16
 }
 // The merge of a cluster's W parts of the rows that CTA wk owns, a warp a row,
 // four dims a lane:
-//     out = 2^(V - M) sum_w 2^(mv_w - V) O_w / sum_w 2^(m_w - M) l_w
+//     out = 2^(V - M - 7) sum_w 2^(mv_w - V) O_w / sum_w 2^(m_w - M) l_w
 // A warp has 16 / W rows, and all of their parts are on their way together
 // (a row after the other took 2 us more of a CTA's 24 with W = 2);
 // lane i < 16 holds the references of a part of row i / W. A row's parts are
@@ -209,7 +216,7 @@ __device__ __forceinline__ void merge_rows(const PagedAttnArgs& a, uint8_t* sm, 
     float sum = ex2_approx(x.x - M) * x.y;
 #pragma unroll
     for (int off = 1; off < W; off <<= 1) sum += __shfl_xor_sync(0xffffffffu, sum, off);
-    const float whole = sum == 0.f ? 0.f : ex2_approx(V - M) / sum;  // a row that sees nothing: zeros
+    const float whole = sum == 0.f ? 0.f : ex2_approx(V - M - kLift) / sum;  // a row that sees nothing: zeros
     const int rr = row0 + mine;
     const long at = ((long)s * a.T + rr / R) * a.out_stride + (long)(g * R + rr % R) * kKvD;
 #pragma unroll
@@ -591,12 +598,12 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                 mx = fmaxf(mx, x);
                 mvx = fmaxf(mvx, x + lvs[b]);
             }
-            if (mx > m + kSlack) {
+            if (mx > m + kSlackM) {
                 const float f = ex2_approx(m - mx);
                 l0.x *= f, l0.y *= f, l1.x *= f, l1.y *= f;
                 m = mx;
             }
-            const bool grow = mvx > mv + kSlack;
+            const bool grow = mvx > mv + kSlackV;
             const float f = grow ? ex2_approx(mv - mvx) : 1.f;
             if (grow) mv = mvx;
             if (j > 0 && __any_sync(0xffffffffu, grow)) {  // O is idle: its products came before S
@@ -615,7 +622,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                     }
                 }
             }
-            const float lift = fminf(ex2_approx(m - mv), FLT_MAX);  // (finite: a block of scale 0 weighs 0)
+            const float lift = fminf(ex2_approx(m - mv + kLift), FLT_MAX);  // (finite: a block of scale 0 weighs 0)
             const float2 nm = make_float2(-m, -m);
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
@@ -682,7 +689,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
         if (!some) m = mv = kNone, l = 0.f;
         const int rr = row0 + (live ? row : 0);
         const long at = ((long)s * a.T + rr / R) * a.out_stride + (long)(g * R + rr % R) * kKvD;
-        const float f = l == 0.f ? 0.f : ex2_approx(mv - m) / l;
+        const float f = l == 0.f ? 0.f : ex2_approx(mv - m - kLift) / l;
         uint8_t* own = sm + (row & ~31) * 256;  // W == 1: the warp's rows in bf16
         // (rolled up, here and in the merge: code that runs once goes as fast as it is fetched)
 #pragma unroll 1
