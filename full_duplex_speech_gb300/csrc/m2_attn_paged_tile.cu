@@ -7,11 +7,14 @@
 // positions they see, 128 at a time. Per chunk and tile:
 //   S = q K^T       kind::f8f6f4 straight from the cache's codes. A query row,
 //                   scaled by a power of two to a largest element in
-//                   [2^7, 2^8), enters as two e4m3 terms, hi and lo: 8
-//                   significant bits, which is all of a bf16 (elements below
-//                   2^-8 of the largest are off by at most 2^-17 of it), at
-//                   the cost of one product in 16 bits and with no
-//                   conversion of the keys;
+//                   [2^11, 2^12), enters as two terms, hi in e5m2 and lo in
+//                   e4m3: 8 significant bits, which is all of a bf16, for
+//                   elements from 2^-13 of the largest on (hi leaves at most
+//                   16 steps of the last bit, which lo holds); below, off by
+//                   at most 2^-21 of the largest and 2^-3 of themselves. At
+//                   the cost of one product in 16 bits and with no conversion
+//                   of the keys. (Both in e4m3, the largest in [2^7, 2^8),
+//                   were off by 2^-17 of it, exact from 2^-9 on.)
 //   softmax         one thread a row, S read out of tensor memory in fp32 with
 //                   each block's maximum (tcgen05.ld.red):
 //                   x = S (scale ks), p = 2^(x - m), l += p, and the weight
@@ -60,6 +63,7 @@ constexpr int kTlTc = 128;                         // positions per chunk
 constexpr int kTlBlocks = kTlTc / kKvBlock;        // scales of a chunk
 constexpr uint32_t kTlTile = kTlTc * kKvD;         // 16 KB of codes
 constexpr int kKStages = 3, kVStages = 2, kHStages = 2, kScStages = kKStages + 1;
+constexpr int kQPower = 11;  // a row of q is scaled to a largest element in [2^11, 2^12)
 // log2 by which a chunk may exceed m and mv, and log2 of the weight of a position
 // at mv: fp16 reaches from 2^15 down to 2^-24, so that a weight is off by 2^-32 of
 // the one at mv at most, and is dropped below that (a long flat rest behind one
@@ -88,8 +92,8 @@ struct TlSmem {
     static_assert(kBytes <= 227 * 1024, "one CTA an SM");
 };
 
-__host__ __device__ constexpr uint32_t idesc_f8(int M, int N) {  // e4m3 x e4m3, both K-major, fp32 sums
-    return (1u << 4) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
+__host__ __device__ constexpr uint32_t idesc_f8(int M, int N, bool e5m2) {  // e5m2 or e4m3 x e4m3, both K-major, fp32 sums
+    return (1u << 4) | ((uint32_t)e5m2 << 7) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
 }
 __host__ __device__ constexpr uint32_t idesc_f16_bmn(int M, int N) {  // fp16 x fp16, B MN-major, fp32 sums
     return (1u << 4) | (1u << 16) | ((uint32_t)(N >> 3) << 17) | ((uint32_t)(M >> 4) << 24);
@@ -404,7 +408,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                             const uint64_t ad = tc::sdesc(sbase + L::kQ + (2 * i + part) * kTlTile, 0, 1024, 2);
 #pragma unroll
                             for (int k = 0; k < 4; ++k)
-                                mma_f8(tm + kColS + 128 * i, ad + 2 * k, bd + 2 * k, idesc_f8(kTlRows, kTlTc),
+                                mma_f8(tm + kColS + 128 * i, ad + 2 * k, bd + 2 * k, idesc_f8(kTlRows, kTlTc, part == 0),
                                        (part > 0 || k > 0) ? 1u : 0u);
                         }
                         tc::mma_commit(sfull + i);
@@ -484,7 +488,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tm + lanes + kColS + 128 * i, tO = tm + lanes + kColO + 128 * i;
         const bool live = row < rows;
-        // The warp's 32 rows of q, scaled, as e4m3 hi + lo, two rows at a time, 16 lanes a row
+        // The warp's 32 rows of q, scaled, as hi (e5m2) + lo (e4m3), two rows at a time, 16 lanes a row
         // (a lane a row would touch 32 cache lines with every load). A row's 256 bytes come by
         // asynchronous copies to where its hi and lo will be, so that all are in flight
         // together and the loops stay short (straight-line code for all the rows cost 3 us
@@ -528,13 +532,13 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                 for (int t = 0; t < 4; ++t) {  // (the 16 lanes have read their rows: they have exchanged the maxima)
                     const float own = __shfl_sync(0xffffffffu, top[t], (lane & 1) << 4);
                     if ((lane >> 1) == t4 + t) mine = own;
-                    const float pw = row_power(top[t], 7), sg = a.scale < 0.f ? -pw : pw;
+                    const float pw = row_power(top[t], kQPower), sg = a.scale < 0.f ? -pw : pw;
                     uint32_t hi[2] = {0u, 0u}, lo[2] = {0u, 0u};
 #pragma unroll
                     for (int e = 0; e < 4; ++e) {
                         const float y0 = f[t][2 * e] * sg, y1 = f[t][2 * e + 1] * sg;
-                        const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E4M3);
-                        const float2 back = unpack_f16x2(e4m3x2_to_f16x2(h2));
+                        const uint32_t h2 = __nv_cvt_float2_to_fp8x2(make_float2(y0, y1), __NV_SATFINITE, __NV_E5M2);
+                        const float2 back = unpack_f16x2(e5m2x2_to_f16x2(h2));
                         const uint32_t l2 = __nv_cvt_float2_to_fp8x2(make_float2(y0 - back.x, y1 - back.y), __NV_SATFINITE, __NV_E4M3);
                         hi[e >> 1] |= h2 << (16 * (e & 1));
                         lo[e >> 1] |= l2 << (16 * (e & 1));
@@ -545,8 +549,8 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                     *reinterpret_cast<uint2*>(o + kTlTile) = make_uint2(lo[0], lo[1]);
                 }
             }
-            // e4m3 has no infinity: such a row reads NaN
-            cs = mine < INFINITY ? fabsf(a.scale) * kLog2e / row_power(mine, 7) : NAN;
+            // a row that holds an infinity reads NaN
+            cs = mine < INFINITY ? fabsf(a.scale) * kLog2e / row_power(mine, kQPower) : NAN;
             tc::fence_proxy_async_smem();
         }
         float2 l0 = make_float2(0.f, 0.f), l1 = l0;  // the row's sum, in four parts

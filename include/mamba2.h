@@ -602,15 +602,22 @@ m2_status mamba2_kv_append(const m2_kv_cache* c, int T, const int32_t* lengths, 
  *   (out_stride) * (s * T + t) elements past the pointer; 16-byte aligned,
  *   strides times the element size a multiple of 16 bytes, at least
  *   n_heads * 128. out must not overlap q (M2_EINVAL where it is q).
- * Scores, softmax and sums in fp32, out rounded once.
+ * Scores, maxima and all sums are fp32, out is rounded once. What enters the
+ *   products with fewer bits: a softmax weight, as fp16 (2^-11 of itself; or
+ *   2^-32 of the largest product of a weight and its value's scale, below which
+ *   it is dropped) for bf16, as two fp16 terms (22 bits; 2^-40) for fp32; an
+ *   fp32 query, as two fp16 terms (22 bits). A bf16 query enters exactly where
+ *   an element is at least 2^-13 of its row's largest; one below that is off by
+ *   at most 2^-21 of that largest and 2^-3 of itself (in the form for few rows,
+ *   exactly down to 2^-31, off by 2^-39).
  * Scratch: workspace of at least mamba2_attn_paged_workspace_bytes(...), which
  *   is 0 for every size (NULL with 0 bytes is fine): the CTAs that share a
  *   session's positions merge in shared memory.
  * Forms: fp32, and bf16 of few rows a kv head (T x n_heads / n_kv_heads; how
  *   many goes by the number of sessions and heads and by max_pages), 8 or 16
  *   rows at a time on the warps' matrix instructions; bf16 of more rows on the
- *   tcgen05 tensor cores, 256 at a time. Both give the same sums in a different
- *   order (the results agree within rounding).
+ *   tcgen05 tensor cores, 256 at a time. They agree within the bounds above and
+ *   the order of fp32 sums; a wider page table may thus change the last bits.
  * A block whose scale is infinite or a NaN makes the rows that see it NaN, and
  *   no others. A query row that holds an infinity or a NaN gives NaN where it
  *   sees any position.

@@ -4,7 +4,8 @@ shared, runs of positions longer than the page numbers that are read at once,
 and page tables much wider than their sessions.
 
 References in fp64 on the GPU, from what the cache holds; the tolerances are
-those that stand at the head of test_gpu_kv_paged.py."""
+those that stand at the head of test_gpu_kv_paged.py, with queries that may be
+off by 2^-21 of a row's largest."""
 import ctypes
 
 import numpy as np
@@ -81,7 +82,7 @@ def check(cache, q, got, lengths, new, causal, scale, act):
         d = 128 * 2.0 ** -24 * A
         if act == "bf16":
             wide = k.abs().sum(-1).amax(0).repeat_interleave(R)[:, None]
-            d = d + 2.0 ** -17 * qd.abs().amax(-1, keepdim=True) * abs(scale) * wide
+            d = d + 2.0 ** -21 * qd.abs().amax(-1, keepdim=True) * abs(scale) * wide
             tol = 2.0 ** -8 * want.abs() + (2.0 ** -11 + 1e-5 + 2 * d) * S
         else:
             tol = 2.0 ** -24 * want.abs() + (2.0 ** -21 + 1e-5 + 2 * (d + 2.0 ** -21 * A)) * S

@@ -1,6 +1,6 @@
 """Attention over the paged cache where its arithmetic is stretched, in the form
 for a few rows and in the tiles: values near the type's largest, one dominant
-position before a long flat rest. The caches are written directly,
+position before a long flat rest, queries with one wide channel. The caches are written directly,
 as codes and scales, so that the exact outputs are known."""
 import math
 
@@ -91,3 +91,32 @@ def test_one_dominant_position_before_a_long_flat_rest(m2, form, log2_weight):
     lost = rest / 4 if log2_weight < -24 else 0.0
     want = rest / (1 + rest)
     assert (abs(got - want) <= (2.0 ** -8 + 2.0 ** -11 + 1e-5 + lost) * want).all(), (got[0], want)
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("wide", [1.0, 300.0, 5000.0, 1e4, 1e5, 3e6])
+def test_queries_with_one_wide_channel(m2, form, wide):
+    """One channel of the queries is much wider than the others, and the keys are
+    zero there, so that the scores are the other channels'. These may be off by
+    2^-21 of the widest and 2^-3 of themselves in the tiles, not at all where
+    they are 2^-13 of it or more, and not at all in the rows form."""
+    import torch
+    Hkv, n, small = FORMS[form][1], 400, 1.296875
+    cache = cache_of(m2, Hkv, n)
+    for p in range(0, n, 2):  # every other position scores 2 and is worth 1, the rest 0 and 0
+        page, slot, _ = at(cache, p)
+        cache.kp[page, :, slot, 1:] = ONE
+    for p in range(1, n, 2):
+        page, slot, _ = at(cache, p)
+        cache.vp[page, :, slot] = 0
+    q = torch.full((D,), small)
+    q[0] = wide
+    widest = float(q.to(torch.bfloat16)[0])
+    got = across(m2, cache, form, q, 2 / (127 * small), n)
+    off = 0.0
+    if form == "tiles" and small < 2.0 ** -13 * widest:
+        off = 2 * min(2.0 ** -21 * widest / small, 2.0 ** -3)
+    # a softmax share moves by a quarter of the score at most; scores are fp32 sums of 128 products
+    want = 1 / (1 + math.exp(-2))
+    tol = (2.0 ** -8 + 2.0 ** -11 + 1e-5) * want + (off + 128 * 2.0 ** -24 * 2) / 4
+    assert (abs(got - want) <= tol).all(), (got[0], want, tol)
