@@ -4,6 +4,7 @@
 #include <cuda.h>
 #include <cuda_fp16.h>
 #include <cuda_runtime.h>
+#include <float.h>
 
 #include "m2_common.cuh"
 #include "m2_paged.h"
@@ -12,7 +13,7 @@
 namespace m2 {
 
 constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNone = -1e30f;  // a running maximum before any position
+constexpr float kNone = -FLT_MAX;  // a running maximum before any position: below every finite score
 
 __device__ __forceinline__ float ex2_approx(float x) {
     float r;

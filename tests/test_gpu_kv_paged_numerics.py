@@ -1,6 +1,7 @@
 """Attention over the paged cache where its arithmetic is stretched, in the form
 for a few rows and in the tiles: values near the type's largest, one dominant
-position before a long flat rest, queries with one wide channel. The caches are written directly,
+position before a long flat rest, queries with one wide channel, scores of any
+finite size. The caches are written directly,
 as codes and scales, so that the exact outputs are known."""
 import math
 
@@ -120,3 +121,22 @@ def test_queries_with_one_wide_channel(m2, form, wide):
     want = 1 / (1 + math.exp(-2))
     tol = (2.0 ** -8 + 2.0 ** -11 + 1e-5) * want + (off + 128 * 2.0 ** -24 * 2) / 4
     assert (abs(got - want) <= tol).all(), (got[0], want, tol)
+
+
+@pytest.mark.parametrize("form", list(FORMS))
+@pytest.mark.parametrize("n", [40, 700])
+@pytest.mark.parametrize("power", [-112, -100, 112])
+def test_scores_of_any_finite_size(m2, form, n, power):
+    """Every score is +-2^112 or so; half of the positions, worth 1, score alike,
+    and the other half, worth 0, score twice as far below zero."""
+    import torch
+    cache = cache_of(m2, FORMS[form][1], n)
+    for p in range(n):
+        page, slot, block = at(cache, p)
+        low = (p // BLOCK) % 2 == 0
+        cache.kp[page, :, slot, 0] = ONE
+        cache.ks[page, :, block] = 2.0 ** (abs(power) // 2) * (2.0 if low == (power < 0) else 1.0)
+        cache.vp[page, :, slot] = 0 if low else ONE
+    q = torch.zeros(D)
+    q[0] = math.copysign(2.0 ** (abs(power) // 2), power)
+    assert (across(m2, cache, form, q, 1.0, n) == 1.0).all()
