@@ -172,6 +172,12 @@ __global__ void __launch_bounds__(kApThreads, sizeof(TA) == 2 ? 5 : 4) kv_append
     const long limit = a.rot ? min(c.capacity(), (long)a.n_pos) : c.capacity();
     if (!kv_extent(c, s, a.T, a.lens, a.n_new, limit, &L, &n)) {  // the whole session is refused
         if (blockIdx.x == 0 && tid == 0) atomicOr(c.err, ERR_ATTN_LENGTH);
+        if ((int)blockIdx.x < c.Hkv) {  // ... and keeps its tail, whichever rows of it are open
+            const size_t at = (((size_t)s * c.Hkv + blockIdx.x) * kKvBlock + row) * kKvD + 8 * piece;
+            float f[8];
+            if (c.kto != c.kt) load8_f32(c.kt + at, f), store8_f32(c.kto + at, f);
+            if (c.vto != c.vt) load8_f32(c.vt + at, f), store8_f32(c.vto + at, f);
+        }
         return;
     }
     if ((int)blockIdx.x >= blocks * c.Hkv) {

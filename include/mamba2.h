@@ -577,9 +577,10 @@ typedef struct {
  *   n_heads not a multiple of n_kv_heads), M2_EALIGN, M2_EUNSUPPORTED,
  *   M2_ECUDA. Seen only on the device, in the error word: 0x104, a negative
  *   length or positions past max_pages * page_size (or, with a rotation,
- *   n_pos): that session is left as it was; 0x105, a page number outside the
- *   pool: that block is not written. n_sessions == 0 is a no-op once the
- *   arguments check out. Asynchronous on `stream`. */
+ *   n_pos): that session is left as it was (its tails out become copies of its
+ *   tails, all 16 rows); 0x105, a page number outside the pool: that block is
+ *   not written. n_sessions == 0 is a no-op once the arguments check out.
+ *   Asynchronous on `stream`. */
 m2_status mamba2_kv_append(const m2_kv_cache* c, int T, const int32_t* lengths, const int32_t* n_new, const void* k,
                            const void* v, long kv_stride, const m2_rope* rope, int n_heads, const void* q, long q_stride,
                            void* q_out, long q_out_stride, void* stream);
