@@ -225,7 +225,7 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
     const float sl2 = a.scale * kLog2e;
     __syncthreads();
     if (ncached > 0 && !tc::mbar_wait(bar, 0)) {
-        atomicOr(a.err, ERR_MBAR_TIMEOUT_LOAD);
+        record_error(a.err, ERR_MBAR_TIMEOUT_LOAD);
         *sFlag = 1;
     }
     __syncthreads();
@@ -397,7 +397,7 @@ __global__ void __launch_bounds__(kAttnMaxR * 64) attn_combine_kernel(AttnArgs a
         v0 *= inv;
         v1 *= inv;
     } else if (threadIdx.x == 0) {
-        atomicOr(a.err, ERR_ATTN_LENGTH);
+        record_error(a.err, ERR_ATTN_LENGTH);
     }
     const size_t o = (size_t)s * a.out_ss + (size_t)(g * R + r) * kAttnD + 2 * dp;
     if constexpr (sizeof(TA) == 2) {
@@ -560,7 +560,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2)
         uint8_t* sK = sm + st * kWalkStage;
         uint8_t* sV = sK + 2 * kWalkBox;
         bool landed = tc::mbar_wait(bar + st, phase);
-        if (!landed) atomicOr(a.err, ERR_MBAR_TIMEOUT_LOAD);
+        if (!landed) record_error(a.err, ERR_MBAR_TIMEOUT_LOAD);
         if (c == nch - 1) {
             // the chunk holding position len: the new key and value go into
             // their rows here and into the caches; the value rows past len
@@ -717,7 +717,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2)
             if (tid == 0) tc::st_cluster_f32x2(tc::cluster_map(slot + 4u * kAttnD, owner), make_float2(M, L));
         }
     }
-    if (bad && wk == 0 && g == 0 && tid == 0) atomicOr(a.err, ERR_ATTN_LENGTH);
+    if (bad && wk == 0 && g == 0 && tid == 0) record_error(a.err, ERR_ATTN_LENGTH);
     if (W == 1) return;
     tc::cluster_arrive();  // the stores into the owners' slots are visible ...
     tc::cluster_wait();    // ... once every walker has made them

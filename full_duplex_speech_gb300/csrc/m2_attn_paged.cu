@@ -189,7 +189,7 @@ __global__ void __launch_bounds__(kRwThreads, 2)
     int before, n;
     const bool ok = kv_extent(c, s, a.T, a.lens, a.n_new, a.causal ? c.capacity() : c.capacity() + a.T, &before, &n) &&
                     before <= c.capacity();
-    if (!ok && blockIdx.x == 0 && tid == 0) atomicOr(c.err, ERR_ATTN_LENGTH);
+    if (!ok && blockIdx.x == 0 && tid == 0) record_error(c.err, ERR_ATTN_LENGTH);
     const int rows = min(n * R - row0, (int)L::kRows);
     if (rows <= 0) return;  // the whole cluster
     // positions that this group's last row sees, and this walker's chunks of
@@ -207,7 +207,7 @@ __global__ void __launch_bounds__(kRwThreads, 2)
             const int st = k % ST;
             const uint32_t round = (uint32_t)(k / ST);
             if (round > 0 && !tc::mbar_wait(empty + st, (round - 1) & 1)) {
-                if (lane == 0) atomicOr(c.err, ERR_MBAR_TIMEOUT_LOAD);
+                if (lane == 0) record_error(c.err, ERR_MBAR_TIMEOUT_LOAD);
                 *flag = 1;
                 good = false;
             }
@@ -221,7 +221,7 @@ __global__ void __launch_bounds__(kRwThreads, 2)
             const int at0 = (k - held) * ppc;  // lane of the chunk's first page
             if (lane >= at0 && lane < at0 + ppc && p0 + ((lane - at0) << c.ps_shift) < total &&
                 (page_ids < 0 || page_ids >= c.n_pages)) {
-                atomicOr(c.err, ERR_KV_PAGE);
+                record_error(c.err, ERR_KV_PAGE);
                 page_ids = 0;  // some page of the pool: what is read is undefined
             }
             __syncwarp();
@@ -315,7 +315,7 @@ __global__ void __launch_bounds__(kRwThreads, 2)
         for (int k = 0; k < nc; ++k) {
             const int st = k % ST;
             if (!tc::mbar_wait(full + st, (uint32_t)(k / ST) & 1)) {
-                atomicOr(c.err, ERR_MBAR_TIMEOUT_LOAD);
+                record_error(c.err, ERR_MBAR_TIMEOUT_LOAD);
                 *flag = 1;
                 good = false;
             }

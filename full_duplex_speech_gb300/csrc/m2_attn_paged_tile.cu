@@ -290,7 +290,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
     int before, n;
     const bool ok = kv_extent(c, s, a.T, a.lens, a.n_new, a.causal ? c.capacity() : c.capacity() + a.T, &before, &n) &&
                     before <= c.capacity();
-    if (!ok && blockIdx.x == 0 && tid == 0) atomicOr(c.err, ERR_ATTN_LENGTH);
+    if (!ok && blockIdx.x == 0 && tid == 0) record_error(c.err, ERR_ATTN_LENGTH);
     const int rows = min(n * R - row0, 2 * kTlRows);
     if (rows <= 0) return;  // the whole cluster
     // positions that the tiles' last rows see, and this CTA's run of chunks
@@ -327,7 +327,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
         if (tc::mbar_try_wait(bar, parity)) return true;
         if (*flag) return false;
         if (tc::mbar_wait(bar, parity)) return true;
-        atomicOr(c.err, ERR_MBAR_TIMEOUT_MMA);
+        record_error(c.err, ERR_MBAR_TIMEOUT_MMA);
         *flag = 1;
         return false;
     };
@@ -350,7 +350,7 @@ __global__ void __launch_bounds__(kTlThreads, 1)
                     held = first;
                     page_ids = first + lane <= last_page ? table[first + lane] : 0;
                     if (page_ids < 0 || page_ids >= c.n_pages) {
-                        atomicOr(c.err, ERR_KV_PAGE);
+                        record_error(c.err, ERR_KV_PAGE);
                         page_ids = 0;  // some page of the pool: what is read is undefined
                     }
                     __syncwarp();

@@ -178,4 +178,12 @@ enum : unsigned int {
     ERR_KV_PAGE = 0x105,      // a page number outside the pool
 };
 
+// The first condition since the word was cleared stays (the codes are not bits:
+// two of them in one word could read as a third).
+__device__ __forceinline__ void record_error(unsigned int* err, unsigned int code) { atomicCAS(err, 0u, code); }
+// The same for ERR_MBAR_TIMEOUT_LOAD, the least of the codes, by a maximum, which
+// returns nothing: the 4-bit GEMM's registers fall out differently with an
+// exchange in its cold path (300 rows 441 us, 320 with this).
+__device__ __forceinline__ void record_load_timeout(unsigned int* err) { atomicMax(err, (unsigned)ERR_MBAR_TIMEOUT_LOAD); }
+
 }  // namespace m2

@@ -171,7 +171,7 @@ __global__ void __launch_bounds__(kApThreads, sizeof(TA) == 2 ? 5 : 4) kv_append
     int L, n;
     const long limit = a.rot ? min(c.capacity(), (long)a.n_pos) : c.capacity();
     if (!kv_extent(c, s, a.T, a.lens, a.n_new, limit, &L, &n)) {  // the whole session is refused
-        if (blockIdx.x == 0 && tid == 0) atomicOr(c.err, ERR_ATTN_LENGTH);
+        if (blockIdx.x == 0 && tid == 0) record_error(c.err, ERR_ATTN_LENGTH);
         if ((int)blockIdx.x < c.Hkv) {  // ... and keeps its tail, whichever rows of it are open
             const size_t at = (((size_t)s * c.Hkv + blockIdx.x) * kKvBlock + row) * kKvD + 8 * piece;
             float f[8];
@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kApThreads, sizeof(TA) == 2 ? 5 : 4) kv_append
     mv = max(mv, __float_as_uint(kKvTiny));
     if (n > 0) {
         if (page < 0 || page >= c.n_pages) {
-            if (tid == 0) atomicOr(c.err, ERR_KV_PAGE);
+            if (tid == 0) record_error(c.err, ERR_KV_PAGE);
         } else {
             const size_t at = ((size_t)page * c.Hkv + g) * c.ps + (base & (c.ps - 1));  // row of the block's first position
             if (live) {

@@ -120,7 +120,7 @@ __global__ void __launch_bounds__(kGmThreads) qgemm_kernel(QLinearArgs a, const 
     auto wait_ok = [&](uint64_t* bar, uint32_t parity) -> bool {
         if (*sFlag) return false;
         if (tc::mbar_wait(bar, parity)) return true;
-        atomicOr(a.err, ERR_MBAR_TIMEOUT_LOAD);
+        record_load_timeout(a.err);
         *sFlag = 1;
         return false;
     };

@@ -435,7 +435,7 @@ __global__ void __launch_bounds__(kComputeWarps == 16 ? 640 : kSsdThreads, 1) sc
     auto wait_ok = [&](uint64_t* bar, uint32_t parity, unsigned code) -> bool {
         if (*sFlag) return false;
         if (tc::mbar_wait(bar, parity)) return true;
-        atomicOr(a.err, code);
+        record_error(a.err, code);
         *sFlag = 1;
         return false;
     };

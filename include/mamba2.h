@@ -644,8 +644,12 @@ const char* mamba2_status_string(m2_status s);
 int mamba2_last_cuda_error(void);
 
 /* Reads and clears the device-side error word of the current device
- * (0 = no error; otherwise the code of a bounded wait that ran out).
- * Synchronises `stream`. Returns M2_ECUDA if the read itself fails. */
+ * (0 = no error; otherwise the code of the first condition since the last read:
+ * 0x101 or 0x102, a bounded wait that ran out; 0x104, a length that does not fit
+ * its cache; 0x105, a page number outside the pool). Later conditions are not
+ * kept: a call that met several shows the others when it is made again with the
+ * first mended. Synchronises `stream`. Returns M2_ECUDA if the read itself
+ * fails. */
 m2_status mamba2_device_error(void* stream, unsigned int* code);
 
 #ifdef __cplusplus

@@ -1,5 +1,6 @@
 """Sessions that mamba2_kv_append refuses on the device are left as they were,
-also where the tails out are not the tails."""
+also where the tails out are not the tails; and the error word tells the first
+of several conditions."""
 import numpy as np
 import pytest
 
@@ -47,3 +48,31 @@ def test_a_refused_session_keeps_its_tail_when_the_tails_are_swapped(m2, act, T,
     left = (L + T) % BLOCK
     for tail, rows in ((cache.kto, kh), (cache.vto, vh)):
         _same(tail[:, :, :left].cpu().numpy(), np.ascontiguousarray(rows[:, L + T - left:].transpose(0, 2, 1, 3)))
+
+
+def test_the_error_word_keeps_the_first_condition(m2):
+    """A bad length and a bad page in either order, and in one call."""
+    cache = Cache(m2, 2, 1, 16, 40, "bf16")
+    k, _ = _rows(1, 2, 3, 1, "bf16")
+    q, _ = _rows(2, 2, 3, 4, "bf16")
+    cache.append(k, k)
+    table = cache.d_table.clone()
+
+    def bad_length():
+        cache.attend(q, True, lengths=_int([0, -1]))
+
+    def bad_page(call):
+        cache.d_table[0, 0] = cache.n_pages
+        call()
+        cache.d_table.copy_(table)
+
+    assert m2.mamba2_device_error() == 0
+    for first, second, code in ((bad_length, lambda: bad_page(lambda: cache.attend(q)), 0x104),
+                                (lambda: bad_page(lambda: cache.append(k, k)), bad_length, 0x105)):
+        first()
+        second()
+        assert m2.mamba2_device_error() == code
+        assert m2.mamba2_device_error() == 0
+    bad_page(bad_length)
+    assert m2.mamba2_device_error() in (0x104, 0x105)
+    assert m2.mamba2_device_error() == 0
