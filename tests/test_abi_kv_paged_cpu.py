@@ -71,3 +71,20 @@ def test_kv_paged_validation_without_gpu(m2):
         assert _past_host_checks(app(c)) and _past_host_checks(app(c, **full, rope=rope())) and _past_host_checks(att(c))
         assert _past_host_checks(app(c, new=None)) and _past_host_checks(att(c, new=None, causal=False))
     assert _past_host_checks(att(T=0))
+
+
+def test_the_plan_of_a_call_is_refused_like_the_call(m2):
+    """m2_attn_paged_plan, which the tests of each form ask, checks sizes as
+    mamba2_attn_paged does and returns the negative status."""
+    import ctypes
+    plan = m2.load().m2_attn_paged_plan
+
+    def ask(T=4, H=40, D=128, ps=64):
+        c = m2.kv_cache(2, 8, ps, 100, 10, *(None,) * 5, head_dim=D)
+        return plan(ctypes.byref(c), T, H)
+
+    assert plan(None, 1, 1) == -1
+    assert ask(T=-1) == -1 and ask(H=0) == -1
+    assert ask(H=41) == -2 and ask(D=64) == -2 and ask(ps=48) == -2
+    if NO_GPU:
+        assert ask() == -5
