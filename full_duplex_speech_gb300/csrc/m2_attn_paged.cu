@@ -647,9 +647,10 @@ cudaError_t plan_attn_paged(const PagedAttnArgs& a, PagedAttnPlan* plan) {
     if (few_rows(a)) return plan_rows<bf16_t, 1, 1>(a, plan);
     // Sixteen rows at a time, each time reading the cache again, against tiles
     // that compute 256 and take 8 us to start and end: by a guess of both times,
-    // whose constants are fitted to 150 calls (one session, several alike or
-    // ragged, 10 to 2,000 rows over 12 to 7,500 positions; the tiles' with a
-    // margin, since where the two are near, long lengths cost the rows more).
+    // whose constants are fitted to 150 calls (40 query and 8 kv heads; one session,
+    // several alike or ragged, 10 to 2,000 rows over 12 to 7,500 positions, tables
+    // that end with the longest session; the tiles' with a margin, since where the
+    // two are near, long lengths cost the rows more).
     // One session, 8 kv heads: 60 rows over 12 positions 5.2 us (tiles: 8.4), over
     // 2,000 9.7 (14.5), over 6,000 16.8 (21.0); 240 rows over 148 6.5 (10.6), over
     // 2,048 21 (17), over 6,048 48 (25). 64 sessions of up to 7,500: 20 rows 148

@@ -36,14 +36,16 @@
 // of one pair of tiles and merge through distributed shared memory, each the
 // owner of 256 / W rows.
 //   Measured: 4 sessions of 4096 positions, 40 query and 8 kv heads, causal,
-// 687 GFLOP: 535 us, 1.28 PFLOP/s (69% of a bf16 library product's measured
-// rate). A chunk of a pair takes 2,880 cycles. The warp that issues is held
-// by the products for 2,400 of them; a tile's own round, its softmax (1,130),
-// the hand-overs and the scales (1,200), and 1,020 of products, is as long as
-// that, so that neither alone makes it shorter: an eighth of the products
-// leaves 483 us, no exponentials 527. The scores of the next chunk during the
-// softmax (one S for both tiles, the weights in columns of their own) took
-// 567 where this took 533: the products then wait for one another.
+// 687 GFLOP: 559 us, 1.23 PFLOP/s (66% of a bf16 library product's measured
+// rate). With references that lagged by 2^15 and softmax warps that did not wait
+// in the meetings it took 535, and these cycles: a chunk of a pair 2,880; the
+// warp that issues is held by the products for 2,400 of them (about 272 KB pass
+// through shared memory, 2,180 cycles of it); a tile's own round, its softmax
+// (1,130), the hand-overs and the scales (1,200), and 1,020 of products, is as
+// long as that, so that neither alone makes it shorter: an eighth of the products
+// left 483 us, no exponentials 527. The scores of the next chunk during the
+// softmax (one S for both tiles, the weights in columns of their own) took 567
+// where this took 533: the products then wait for one another.
 #include <cuda_fp8.h>
 #include <float.h>
 #include <math.h>
@@ -814,11 +816,11 @@ cudaError_t plan_attn_paged_tiles(const PagedAttnArgs& a, PagedAttnPlan* plan) {
     // with 5 for a CTA's start and end and 1 for the merge. One session's CTAs
     // are all alike: rounds x a CTA's time. Several sessions are mostly shorter
     // than the table's reach: the longest, and where not all CTAs are held at
-    // once, what the others take. (Over 75 calls within 2.2% of the best W on
-    // average. Six sessions catching up by at most 75 positions over at most
-    // 3,076, 96 pairs: 46 us with one CTA a pair, 30 with two, 39 with four; by
-    // 200 over 6,200: 99, 58 and 86; 2 x 300 rows across to 1,500 positions: 29,
-    // 22 and 37.)
+    // once, what the others take. (Over 75 calls, whose tables end with their
+    // longest session, within 2.2% of the best W on average. Six sessions catching
+    // up by at most 75 positions over at most 3,076, 96 pairs: 46 us with one CTA a
+    // pair, 30 with two, 39 with four; by 200 over 6,200: 99, 58 and 86; 2 x 300
+    // rows across to 1,500 positions: 29, 22 and 37.)
     plan->tiles = true;
     float least = 0.f;
     for (int k = 0, w = 1; k < 4 && (w == 1 || w <= chunks) && setup->held[k] > 0; ++k, w *= 2) {
