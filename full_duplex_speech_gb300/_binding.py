@@ -185,6 +185,17 @@ def load():
         lib.mamba2_attn_paged.restype = ip
         lib.mamba2_attn_paged_workspace_bytes.argtypes = [cp, ip, ip]
         lib.mamba2_attn_paged_workspace_bytes.restype = sz
+        fp = ctypes.c_float
+        lib.mamba2_attn_prompt.argtypes = [ip] * 7 + [vp] * 3 + [lp, vp, vp, lp, vp, vp, fp, vp, lp, vp, vp]
+        lib.mamba2_attn_prompt.restype = ip
+        lib.mamba2_attn_prompt_weights.argtypes = [ip] * 7 + [vp] * 3 + [lp, vp, fp, vp, ip, vp, vp, vp]
+        lib.mamba2_attn_prompt_weights.restype = ip
+        lib.mamba2_attn_decode_weights.argtypes = [ip] * 6 + [vp] * 6 + [fp] + [vp] * 4 + [sz, vp]
+        lib.mamba2_attn_decode_weights.restype = ip
+        lib.mamba2_attn_decode_weights_workspace_bytes.argtypes = [ip] * 6
+        lib.mamba2_attn_decode_weights_workspace_bytes.restype = sz
+        lib.mamba2_kv_evict.argtypes = [ip] * 5 + [vp] * 4 + [ip] * 3 + [vp] * 5
+        lib.mamba2_kv_evict.restype = ip
         lib.mamba2_status_string.argtypes = [ip]
         lib.mamba2_status_string.restype = ctypes.c_char_p
         lib.mamba2_last_cuda_error.argtypes = []
@@ -489,6 +500,64 @@ def mamba2_attn_paged(c: M2KvCache, T, n_heads, causal, lengths, n_new, q, q_str
         float(scale), _p(out), int(out_stride), _p(workspace), _ws_bytes(workspace, workspace_bytes), _stream(stream))
     if check and rc:
         raise M2Error(rc, "mamba2_attn_paged")
+    return rc
+
+
+def mamba2_attn_prompt(n_sessions, n_rows, n_heads, n_kv_heads, head_dim, max_len, act, row_start, lengths, q, q_stride,
+                       k_new, v_new, kv_stride, k_cache, v_cache, scale, out, out_stride, lse=None, stream=None,
+                       check=True) -> int:
+    """Attention of packed whole prompts with their append to the dense caches
+    (see mamba2_attn_prompt in include/mamba2.h)."""
+    rc = load().mamba2_attn_prompt(
+        int(n_sessions), int(n_rows), int(n_heads), int(n_kv_heads), int(head_dim), int(max_len), _act_code(act),
+        _p(row_start), _p(lengths), _p(q), int(q_stride), _p(k_new), _p(v_new), int(kv_stride), _p(k_cache), _p(v_cache),
+        float(scale), _p(out), int(out_stride), _p(lse), _stream(stream))
+    if check and rc:
+        raise M2Error(rc, "mamba2_attn_prompt")
+    return rc
+
+
+def mamba2_attn_prompt_weights(n_sessions, n_rows, n_heads, n_kv_heads, head_dim, max_len, act, row_start, lengths, q,
+                               q_stride, k_cache, scale, lse, window, acc, acc_out, stream=None, check=True) -> int:
+    """The weight that cached positions receive from the last `window` rows of
+    each packed session, added up (see include/mamba2.h)."""
+    rc = load().mamba2_attn_prompt_weights(
+        int(n_sessions), int(n_rows), int(n_heads), int(n_kv_heads), int(head_dim), int(max_len), _act_code(act),
+        _p(row_start), _p(lengths), _p(q), int(q_stride), _p(k_cache), float(scale), _p(lse), int(window), _p(acc),
+        _p(acc_out), _stream(stream))
+    if check and rc:
+        raise M2Error(rc, "mamba2_attn_prompt_weights")
+    return rc
+
+
+def mamba2_attn_decode_weights_workspace_bytes(n_sessions, n_heads, n_kv_heads, head_dim, max_len, act="bf16") -> int:
+    return load().mamba2_attn_decode_weights_workspace_bytes(int(n_sessions), int(n_heads), int(n_kv_heads),
+                                                             int(head_dim), int(max_len), _act_code(act))
+
+
+def mamba2_attn_decode_weights(n_sessions, n_heads, n_kv_heads, head_dim, max_len, act, lengths, q, k_new, v_new, k_cache,
+                               v_cache, scale, out, acc, acc_out, workspace, workspace_bytes=None, stream=None,
+                               check=True) -> int:
+    """mamba2_attn_decode that adds up the weight each cached position receives
+    (see include/mamba2.h)."""
+    rc = load().mamba2_attn_decode_weights(
+        int(n_sessions), int(n_heads), int(n_kv_heads), int(head_dim), int(max_len), _act_code(act), _p(lengths), _p(q),
+        _p(k_new), _p(v_new), _p(k_cache), _p(v_cache), float(scale), _p(out), _p(acc), _p(acc_out), _p(workspace),
+        _ws_bytes(workspace, workspace_bytes), _stream(stream))
+    if check and rc:
+        raise M2Error(rc, "mamba2_attn_decode_weights")
+    return rc
+
+
+def mamba2_kv_evict(n_sessions, n_kv_heads, head_dim, max_len, act, lengths, k_cache, v_cache, acc, keep, recent,
+                    out_max_len, k_out, v_out, acc_out, kept=None, stream=None, check=True) -> int:
+    """Eviction from the dense caches by accumulated weight (see include/mamba2.h)."""
+    rc = load().mamba2_kv_evict(
+        int(n_sessions), int(n_kv_heads), int(head_dim), int(max_len), _act_code(act), _p(lengths), _p(k_cache),
+        _p(v_cache), _p(acc), int(keep), int(recent), int(out_max_len), _p(k_out), _p(v_out), _p(acc_out), _p(kept),
+        _stream(stream))
+    if check and rc:
+        raise M2Error(rc, "mamba2_kv_evict")
     return rc
 
 

@@ -77,6 +77,12 @@ bool attn_use_walk(int S, int Hkv, int Tmax, bool bf16) {
     return bf16 && (long long)S * Hkv * Tmax < (1LL << 31) - 64;
 }
 
+// Where weights are added up, a position's scores (log2 domain, scaled) are kept
+// until the heads' statistics are known: [S, Hkv, Tmax up to whole chunks, heads
+// up to an even number] fp32; behind them the fp32 form's statistics [S, Hq, 2].
+__host__ __device__ inline int sums_pitch(int R) { return (R + 1) & ~1; }
+__host__ __device__ inline size_t sums_head(int Tmax, int R) { return (size_t)((Tmax + 63) / 64 * 64) * sums_pitch(R); }
+
 // Positions per chunk of the split kernel: the most a CTA holds, halved (down
 // to 32) while the grid would have fewer than two CTAs per SM of the 152-SM
 // GB300, so that a short cache of few sessions still spreads over the GPU. A
@@ -275,6 +281,10 @@ __global__ void __launch_bounds__(kAttnThreads) attn_split_kernel(AttnArgs a) {
             if (r == i8 && r < R && t < tc) sS[r * TCM + t] = t < n ? d[r] * sl2 : -INFINITY;
     }
     __syncthreads();
+    if (a.kept) {
+        float* kept = a.kept + ((size_t)s * a.Hkv + g) * sums_head(a.Tmax, R) + (size_t)t0 * sums_pitch(R);
+        for (int i = tid; i < n * R; i += kAttnThreads) kept[(i / R) * sums_pitch(R) + i % R] = sS[(i % R) * TCM + i / R];
+    }
 
     // softmax statistics per head (warp w takes heads w and w + 4); the
     // weights go out position-major for the value pass
@@ -396,6 +406,9 @@ __global__ void __launch_bounds__(kAttnMaxR * 64) attn_combine_kernel(AttnArgs a
         const float inv = 1.f / den;
         v0 *= inv;
         v1 *= inv;
+        if (a.kept && dp == 0)
+            *reinterpret_cast<float2*>(a.kept + (size_t)a.S * a.Hkv * sums_head(a.Tmax, R) +
+                                       2 * ((size_t)s * a.Hq + g * R + r)) = make_float2(M, inv);
     } else if (threadIdx.x == 0) {
         record_error(a.err, ERR_ATTN_LENGTH);
     }
@@ -406,6 +419,28 @@ __global__ void __launch_bounds__(kAttnMaxR * 64) attn_combine_kernel(AttnArgs a
     } else {
         *reinterpret_cast<float2*>(reinterpret_cast<float*>(a.out) + o) = make_float2(v0, v1);
     }
+}
+
+// acc_out[p] = acc[p] (0 for the new position) + sum over the heads of their
+// weights of position p, from the kept scores and statistics.
+constexpr int kSumThreads = 256;
+__global__ void __launch_bounds__(kSumThreads) attn_sums_kernel(AttnArgs a) {
+    __shared__ float2 stat[kAttnMaxR];
+    const int g = blockIdx.y, s = blockIdx.z, R = a.Hq / a.Hkv, p = blockIdx.x * kSumThreads + threadIdx.x;
+    pdl_wait();
+    pdl_trigger();
+    const int len = a.lens[s] + a.len_add;
+    if (len < 0 || len >= a.Tmax) return;  // refused; the combine kernel reports it
+    const size_t head = (size_t)s * a.Hkv + g;
+    if (threadIdx.x < R)
+        stat[threadIdx.x] = *reinterpret_cast<const float2*>(a.kept + (size_t)a.S * a.Hkv * sums_head(a.Tmax, R) +
+                                                             2 * ((size_t)s * a.Hq + g * R + threadIdx.x));
+    __syncthreads();
+    if (p > len) return;
+    const float* kept = a.kept + head * sums_head(a.Tmax, R) + (size_t)p * sums_pitch(R);
+    float sum = 0.f;
+    for (int r = 0; r < R; ++r) sum = fmaf(ex2_approx(kept[r] - stat[r].x), stat[r].y, sum);
+    a.acc_out[head * a.Tmax + p] = (p < len ? a.acc[head * a.Tmax + p] : 0.f) + sum;
 }
 
 // ---------------------------------------------------------------------------
@@ -441,7 +476,10 @@ constexpr int kWalkSlots = kAttnMaxR + kWalkMaxW - 1;  // ceil(R / W) W, at most
 constexpr uint32_t kWalkSlotF = kAttnD + 2;
 constexpr uint32_t kWalkRecv = kWalkStages * kWalkStage;
 constexpr uint32_t kWalkBar = kWalkRecv + kWalkSlots * kWalkSlotF * 4;
-constexpr uint32_t kWalkSmem = kWalkBar + kWalkStages * 8 + 1024;  // + barriers, + slack to align to 1024
+// Where weights are added up: every walker's (max, sum) of every head, and the
+// heads' (max, 1 / sum) of all of them.
+constexpr uint32_t kWalkStat = kWalkBar + (kWalkStages * 8 + 15) / 16 * 16;
+constexpr uint32_t kWalkSmem = kWalkStat + (kWalkMaxW + 1) * kAttnMaxR * 8 + 1024;  // + slack to align to 1024
 static_assert(2 * (kWalkSmem + 1024) <= 228 * 1024, "two CTAs an SM");
 // The four warps' merge, over the first stage (no longer read): their
 // (m, l) and acc.
@@ -490,7 +528,8 @@ __device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
 
 // grid (W, Hkv, S), a cluster of W walkers per (session, kv head) when W > 1;
 // walker w takes chunks [w cpw, (w + 1) cpw) of those holding positions
-// 0 .. len. Two CTAs an SM.
+// 0 .. len. Two CTAs an SM. kSums: the weights of each position are added up.
+template <bool kSums>
 __global__ void __launch_bounds__(kWalkThreads, 2)
     attn_walk_kernel(AttnArgs a, const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
                      int cpw) {
@@ -606,6 +645,13 @@ __global__ void __launch_bounds__(kWalkThreads, 2)
         const float v01 = (p0ok && h1ok) ? (sa[1] + sb[1]) * sl2 : -INFINITY;
         const float v10 = (p1ok && h0ok) ? (sa[2] + sb[2]) * sl2 : -INFINITY;
         const float v11 = (p1ok && h1ok) ? (sa[3] + sb[3]) * sl2 : -INFINITY;
+        if constexpr (kSums) {
+            if (h0ok) {
+                float* kept = a.kept + ((size_t)s * a.Hkv + g) * sums_head(a.Tmax, R) + (size_t)pos * sums_pitch(R) + 2 * t;
+                *reinterpret_cast<float2*>(kept) = make_float2(v00, v01);
+                *reinterpret_cast<float2*>(kept + 8 * sums_pitch(R)) = make_float2(v10, v11);
+            }
+        }
         float mx0 = fmaxf(v00, v10), mx1 = fmaxf(v01, v11);
 #pragma unroll
         for (int off = 4; off < 32; off <<= 1) {
@@ -716,11 +762,41 @@ __global__ void __launch_bounds__(kWalkThreads, 2)
             tc::st_cluster_f32(tc::cluster_map(slot + 4u * tid, owner), o);
             if (tid == 0) tc::st_cluster_f32x2(tc::cluster_map(slot + 4u * kAttnD, owner), make_float2(M, L));
         }
+        if constexpr (kSums) {
+            if (tid < W)
+                tc::st_cluster_f32x2(tc::cluster_map(tc::smem_u32(sm + kWalkStat) + 8u * (wk * kAttnMaxR + r), (uint32_t)tid),
+                                     make_float2(M, L));
+        }
     }
     if (bad && wk == 0 && g == 0 && tid == 0) record_error(a.err, ERR_ATTN_LENGTH);
-    if (W == 1) return;
+    if (!kSums && W == 1) return;
     tc::cluster_arrive();  // the stores into the owners' slots are visible ...
     tc::cluster_wait();    // ... once every walker has made them
+    if constexpr (kSums) {
+        // every walker adds up the weights of its own positions, whose scores it kept
+        float2* stat = reinterpret_cast<float2*>(sm + kWalkStat);
+        float2* whole = stat + kWalkMaxW * kAttnMaxR;
+        if (tid < R) {
+            float M = -1e30f, L = 0.f;
+            for (int w = 0; w < W; ++w) M = fmaxf(M, stat[w * kAttnMaxR + tid].x);
+            for (int w = 0; w < W; ++w) L = fmaf(ex2_approx(stat[w * kAttnMaxR + tid].x - M), stat[w * kAttnMaxR + tid].y, L);
+            whole[tid] = make_float2(M, 1.f / L);
+        }
+        __syncthreads();
+        const float* kept = a.kept + ((size_t)s * a.Hkv + g) * sums_head(a.Tmax, R);
+        const int end = ok ? min(ce * kWalkTc, len + 1) : 0;
+        for (int p = cb * kWalkTc + tid; p < end; p += kWalkThreads) {
+            const float2* sc = reinterpret_cast<const float2*>(kept + (size_t)p * sums_pitch(R));
+            float sum = 0.f;
+            for (int r = 0; r < R; r += 2) {
+                const float2 x = sc[r >> 1];
+                sum = fmaf(ex2_approx(x.x - whole[r].x), whole[r].y, sum);
+                if (r + 1 < R) sum = fmaf(ex2_approx(x.y - whole[r + 1].x), whole[r + 1].y, sum);
+            }
+            a.acc_out[row0 + p] = (p < len ? a.acc[row0 + p] : 0.f) + sum;
+        }
+        if (W == 1) return;
+    }
     // out for the heads this walker owns: M = max_w m_w,
     // out = sum_w 2^(m_w - M) acc_w / sum_w 2^(m_w - M) l_w
     for (int r = wk; r < R; r += W) {
@@ -773,6 +849,7 @@ cudaError_t make_cache_map(const void* cache, const AttnArgs& a, CUtensorMap* ma
 
 // Per device, once: the kernel's shared-memory and cluster-size attributes,
 // and how many clusters of 2, 4, 8 and 16 walkers the device holds at once.
+template <bool kSums>
 cudaError_t walk_setup(const int (**clusters)[5]) {
     static int configured_device = -1;
     static int cached[5];
@@ -780,9 +857,9 @@ cudaError_t walk_setup(const int (**clusters)[5]) {
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
     if (configured_device != dev) {
-        e = cudaFuncSetAttribute(attn_walk_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWalkSmem);
+        e = cudaFuncSetAttribute(attn_walk_kernel<kSums>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWalkSmem);
         if (e != cudaSuccess) return e;
-        const bool wide = cudaFuncSetAttribute(attn_walk_kernel, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
+        const bool wide = cudaFuncSetAttribute(attn_walk_kernel<kSums>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
                           cudaSuccess;
         cached[0] = 1 << 30;
         for (int k = 1; k < 5; ++k) {
@@ -798,7 +875,7 @@ cudaError_t walk_setup(const int (**clusters)[5]) {
             cfg.attrs = attr;
             cfg.numAttrs = 1;
             int n = 0;
-            if ((k == 4 && !wide) || cudaOccupancyMaxActiveClusters(&n, attn_walk_kernel, &cfg) != cudaSuccess) n = 0;
+            if ((k == 4 && !wide) || cudaOccupancyMaxActiveClusters(&n, attn_walk_kernel<kSums>, &cfg) != cudaSuccess) n = 0;
             cached[k] = n;
         }
         (void)cudaGetLastError();  // a refused query leaves no sticky error
@@ -808,9 +885,10 @@ cudaError_t walk_setup(const int (**clusters)[5]) {
     return cudaSuccess;
 }
 
+template <bool kSums>
 cudaError_t launch_walk(const AttnArgs& a, cudaStream_t st) {
     const int (*clusters)[5] = nullptr;
-    cudaError_t e = walk_setup(&clusters);
+    cudaError_t e = walk_setup<kSums>(&clusters);
     if (e != cudaSuccess) return e;
     CUtensorMap tmk, tmv;
     e = make_cache_map(a.k_cache, a, &tmk);
@@ -832,7 +910,7 @@ cudaError_t launch_walk(const AttnArgs& a, cudaStream_t st) {
     cfg.attrs = attr;
     cfg.numAttrs = p.W > 1 ? 2 : 1;
     const int cpw = p.cpw;
-    return cudaLaunchKernelEx(&cfg, attn_walk_kernel, a, tmk, tmv, cpw);
+    return cudaLaunchKernelEx(&cfg, attn_walk_kernel<kSums>, a, tmk, tmv, cpw);
 }
 
 template <typename TA, int RM>
@@ -861,7 +939,9 @@ cudaError_t launch_split_combine(const AttnArgs& a, cudaStream_t st) {
                     : R <= 5 ? launch_split<TA, 5>(a, st)
                              : launch_split<TA, 8>(a, st);
     if (e != cudaSuccess) return e;
-    return launch_pdl(attn_combine_kernel<TA>, dim3(a.Hkv, a.S), dim3(R * (kAttnD / 2)), 0, st, a);
+    e = launch_pdl(attn_combine_kernel<TA>, dim3(a.Hkv, a.S), dim3(R * (kAttnD / 2)), 0, st, a);
+    if (e != cudaSuccess || !a.kept) return e;
+    return launch_pdl(attn_sums_kernel, dim3((a.Tmax + kSumThreads - 1) / kSumThreads, a.Hkv, a.S), dim3(kSumThreads), 0, st, a);
 }
 
 }  // namespace
@@ -874,9 +954,14 @@ size_t attn_workspace_bytes(int S, int Hq, int Hkv, int Tmax, bool bf16) {
     return parts * (kAttnD + 2) * sizeof(float);
 }
 
+size_t attn_sums_workspace_bytes(int S, int Hq, int Hkv, int Tmax) {
+    if (S <= 0 || Hq <= 0 || Hkv <= 0 || Tmax <= 0 || Hq % Hkv) return 0;
+    return ((size_t)S * Hkv * sums_head(Tmax, Hq / Hkv) + 2 * (size_t)S * Hq) * sizeof(float);
+}
+
 cudaError_t launch_attn_decode(const AttnArgs& a0, cudaStream_t st) {
     if (a0.S == 0) return cudaSuccess;
-    if (attn_use_walk(a0.S, a0.Hkv, a0.Tmax, a0.bf16)) return launch_walk(a0, st);
+    if (attn_use_walk(a0.S, a0.Hkv, a0.Tmax, a0.bf16)) return a0.kept ? launch_walk<true>(a0, st) : launch_walk<false>(a0, st);
     AttnArgs a = a0;
     a.tc = attn_chunk_len(a.S, a.Hkv, a.Tmax, a.bf16);
     return a.bf16 ? launch_split_combine<bf16_t>(a, st) : launch_split_combine<float>(a, st);

@@ -1,0 +1,138 @@
+// The weight that cached positions receive from the last `window` rows of each
+// session of a packed prompt (m2_attn_prompt.cu), given the rows' lse:
+//     acc_out[g][p] = acc[g][p] (p < before, else 0)
+//                     + sum over rows t of the window with p <= before + t, and
+//                       heads h of kv head g, of e^(scale q_t,h . k_p - lse_t,h)
+// Every position of a kv head belongs to one CTA, which sums its weights in a
+// fixed order: no atomics, and the same sums from call to call.
+#include <math.h>
+
+#include "m2_dense_dev.cuh"
+
+namespace m2 {
+
+namespace {
+
+// ------------------------------------------------- fp32 products of fp32 units
+// A CTA takes 64 positions of one (session, kv head) and walks the window's
+// rows that see any of them, whole packed rows of R heads, up to 64 at a time.
+constexpr int kWfThreads = 256, kWfRows = 64, kWfPos = 64;
+constexpr int kWfPitch = kAttnD + 4;
+struct WfSmem {
+    static constexpr int kQ = 0, kK = kQ + kWfRows * kWfPitch, kL = kK + kWfPos * kWfPitch, kSum = kL + kWfRows,
+                         kFloats = kSum + 16 * kWfPos;
+};
+
+template <typename TA> __device__ __forceinline__ float4 load4(const void* p, size_t elem) {
+    if constexpr (sizeof(TA) == 2) {
+        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + elem);
+        return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
+                           __uint_as_float(w.y & 0xFFFF0000u));
+    } else {
+        return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + elem);
+    }
+}
+
+// grid (position tiles, Hkv, S)
+template <typename TA>
+__global__ void __launch_bounds__(kWfThreads) weights_fp32_kernel(PromptArgs a, PromptSums w) {
+    extern __shared__ __align__(16) float wf[];
+    float *sQ = wf + WfSmem::kQ, *sK = wf + WfSmem::kK, *sL = wf + WfSmem::kL, *sSum = wf + WfSmem::kSum;
+    const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
+    const int R = a.Hq / a.Hkv, per = kWfRows / R;
+    const int g = blockIdx.y, s = blockIdx.z, p0 = blockIdx.x * kWfPos;
+    pdl_wait();
+    pdl_trigger();
+    Session x;
+    if (!session_of(a, s, &x)) {
+        if (tid == 0) record_error(a.err, ERR_ROW_START);
+        return;
+    }
+    if (!x.ok) {
+        if (tid == 0) record_error(a.err, ERR_ATTN_LENGTH);
+        return;
+    }
+    const int total = x.before + x.n;
+    if (p0 >= total) return;
+    const size_t head = ((size_t)s * a.Hkv + g) * a.Tmax;
+    const int first = max(max(0, x.n - w.window), p0 - x.before);  // the first row of the window that sees a position here
+    if (first < x.n)
+        for (int i = tid; i < kWfPos * kAttnD / 4; i += kWfThreads) {
+            const int p = i / (kAttnD / 4), d = i % (kAttnD / 4) * 4;
+            float4 k = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (p0 + p < total) k = load4<TA>(a.k_cache, (head + p0 + p) * kAttnD + d);
+            *reinterpret_cast<float4*>(sK + p * kWfPitch + d) = k;
+        }
+    const float sl2 = a.scale * kDenseLog2e;
+    float sum[4] = {0.f, 0.f, 0.f, 0.f};
+    for (int t0 = first; t0 < x.n; t0 += per) {
+        const int rows = min(per, x.n - t0) * R;
+        __syncthreads();
+        for (int i = tid; i < kWfRows * kAttnD / 4; i += kWfThreads) {
+            const int row = i / (kAttnD / 4), d = i % (kAttnD / 4) * 4;
+            float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
+            if (row < rows)
+                v = load4<TA>(a.q, (size_t)(x.row0 + t0 + row / R) * a.q_stride + (size_t)(g * R + row % R) * kAttnD + d);
+            *reinterpret_cast<float4*>(sQ + row * kWfPitch + d) = v;
+        }
+        if (tid < rows) sL[tid] = a.lse[(size_t)(x.row0 + t0 + tid / R) * a.Hq + g * R + tid % R] * kDenseLog2e;
+        __syncthreads();
+        float d4[4][4];
+#pragma unroll
+        for (int i = 0; i < 4; ++i)
+#pragma unroll
+            for (int j = 0; j < 4; ++j) d4[i][j] = 0.f;
+#pragma unroll 4
+        for (int d = 0; d < kAttnD; d += 4) {
+            float4 qv[4], kv[4];
+#pragma unroll
+            for (int i = 0; i < 4; ++i) qv[i] = *reinterpret_cast<const float4*>(sQ + (4 * ty + i) * kWfPitch + d);
+#pragma unroll
+            for (int j = 0; j < 4; ++j) kv[j] = *reinterpret_cast<const float4*>(sK + (tx + 16 * j) * kWfPitch + d);
+#pragma unroll
+            for (int i = 0; i < 4; ++i)
+#pragma unroll
+                for (int j = 0; j < 4; ++j) {
+                    d4[i][j] = fmaf(qv[i].x, kv[j].x, d4[i][j]);
+                    d4[i][j] = fmaf(qv[i].y, kv[j].y, d4[i][j]);
+                    d4[i][j] = fmaf(qv[i].z, kv[j].z, d4[i][j]);
+                    d4[i][j] = fmaf(qv[i].w, kv[j].w, d4[i][j]);
+                }
+        }
+#pragma unroll
+        for (int i = 0; i < 4; ++i) {
+            const int row = 4 * ty + i, see = row < rows ? x.before + t0 + row / R - p0 : -1;
+#pragma unroll
+            for (int j = 0; j < 4; ++j)
+                if (tx + 16 * j <= see) sum[j] += dense_ex2(fmaf(d4[i][j], sl2, -sL[row]));
+        }
+    }
+    __syncthreads();
+#pragma unroll
+    for (int j = 0; j < 4; ++j) sSum[ty * kWfPos + tx + 16 * j] = sum[j];
+    __syncthreads();
+    if (tid < kWfPos && p0 + tid < total) {
+        float t = 0.f;
+#pragma unroll
+        for (int i = 0; i < 16; ++i) t += sSum[i * kWfPos + tid];
+        const float old = p0 + tid < x.before ? w.acc[head + p0 + tid] : 0.f;
+        w.acc_out[head + p0 + tid] = old + t;
+    }
+}
+
+template <typename TA>
+cudaError_t launch_fp32(const PromptArgs& a, const PromptSums& w, cudaStream_t st) {
+    constexpr int bytes = WfSmem::kFloats * 4;
+    cudaError_t e = cudaFuncSetAttribute(weights_fp32_kernel<TA>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e != cudaSuccess) return e;
+    return launch_pdl(weights_fp32_kernel<TA>, dim3((a.Tmax + kWfPos - 1) / kWfPos, a.Hkv, a.S), dim3(kWfThreads), bytes, st,
+                      a, w);
+}
+
+}  // namespace
+
+cudaError_t launch_attn_prompt_weights(const PromptArgs& a, const PromptSums& w, cudaStream_t st) {
+    return a.bf16 ? launch_fp32<bf16_t>(a, w, st) : launch_fp32<float>(a, w, st);
+}
+
+}  // namespace m2

@@ -176,6 +176,7 @@ enum : unsigned int {
     ERR_TMEM_ALLOC = 0x103,
     ERR_ATTN_LENGTH = 0x104,  // a cached length outside [0, max_len), or positions past a page table's reach
     ERR_KV_PAGE = 0x105,      // a page number outside the pool
+    ERR_ROW_START = 0x106,    // packed rows of a session outside the call's
 };
 
 // The first condition since the word was cleared stays (the codes are not bits:

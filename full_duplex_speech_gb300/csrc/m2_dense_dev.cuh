@@ -1,0 +1,75 @@
+// Device helpers shared by the kernels over packed prompts and dense caches.
+#pragma once
+
+#include <float.h>
+
+#include "m2_common.cuh"
+#include "m2_dense.h"
+#include "m2_launch.h"
+
+namespace m2 {
+
+// The tile `x` of all the sessions' tiles of `per` rows each, found by the
+// whole block: session and tile of it, the last tile of a session first (it
+// sees the most positions). `scratch`: blockDim / 32 + 3 ints of shared memory.
+// False past the last tile. A session whose rows do not lie within the call's
+// has no tiles, and is recorded in the error word.
+__device__ __forceinline__ bool find_tile(const PromptArgs& a, int per, int x, int* scratch, int* session, int* tile) {
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = (int)blockDim.x >> 5;
+    int* found = scratch + warps;  // session, tile, one more than the last tile so far
+    if (tid == 0) found[0] = -1;
+    int base = 0;
+    for (int s0 = 0; s0 < a.S; s0 += (int)blockDim.x) {
+        const int s = s0 + tid;
+        int mine = 0;
+        if (s < a.S) {
+            const int b = a.start[s], e = a.start[s + 1];
+            if (b < 0 || e < b || e > a.rows)
+                record_error(a.err, ERR_ROW_START);
+            else
+                mine = (e - b + per - 1) / per;
+        }
+        int upto = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int below = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += below;
+        }
+        __syncthreads();  // (the scratch of the block before is read)
+        if (lane == 31) scratch[warp] = upto;
+        __syncthreads();
+        int ahead = base, all = base;
+        for (int w = 0; w < warps; ++w) {
+            const int t = scratch[w];
+            if (w < warp) ahead += t;
+            all += t;
+        }
+        const int first = ahead + upto - mine;
+        if (x >= first && x < first + mine) {
+            found[0] = s;
+            found[1] = mine - 1 - (x - first);
+        }
+        base = all;
+        if (x < base) break;  // the same in the whole block
+    }
+    __syncthreads();
+    *session = found[0];
+    *tile = found[1];
+    return found[0] >= 0;
+}
+
+// Tiles of `per` rows that the sessions have at most, from what the host knows.
+inline long most_tiles(int S, int rows, int per) {
+    const long n = (long)rows / per + S;
+    return n < rows ? n : rows;
+}
+
+// 2^x, lg2 x
+__device__ __forceinline__ float dense_ex2(float x) {
+    float r;
+    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
+    return r;
+}
+constexpr float kDenseLog2e = 1.4426950408889634f, kDenseLn2 = 0.6931471805599453f;
+
+}  // namespace m2

@@ -148,7 +148,14 @@ struct AttnArgs {
     // positions of a prefill after the first)
     long q_ss, kv_ss, out_ss;
     int len_add;
+    // Weights that the positions receive, added up (NULL: not wanted): [S, Hkv,
+    // Tmax], and the scores and statistics kept meanwhile
+    const float* acc = nullptr;
+    float* acc_out = nullptr;   // (may be acc)
+    float* kept = nullptr;      // attn_sums_workspace_bytes
 };
+// Scratch for the scores when weights are added up, beside attn_workspace_bytes.
+size_t attn_sums_workspace_bytes(int S, int Hq, int Hkv, int Tmax);
 size_t attn_workspace_bytes(int S, int Hq, int Hkv, int Tmax, bool bf16);
 cudaError_t launch_attn_decode(const AttnArgs& a, cudaStream_t st);
 

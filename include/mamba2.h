@@ -21,8 +21,9 @@
  *   mamba2_step      — one frame for a batch of sessions from cached state.
  * Around it: the gated output norm and the 4-bit projections of the Mamba
  * layer, the cached decode of the model's attention layers
- * (mamba2_gated_norm, mamba2_qlinear, mamba2_attn_decode), and a paged 8-bit
- * cache for them (mamba2_kv_append, mamba2_attn_paged).
+ * (mamba2_gated_norm, mamba2_qlinear, mamba2_attn_decode), a paged 8-bit
+ * cache for them (mamba2_kv_append, mamba2_attn_paged), and whole prompts and
+ * eviction for their dense caches (mamba2_attn_prompt, mamba2_kv_evict).
  *
  * Conventions shared by every entry point
  * ---------------------------------------
@@ -637,6 +638,121 @@ m2_status mamba2_attn_paged(const m2_kv_cache* c, int T, int n_heads, int causal
 /* Bytes of device scratch that mamba2_attn_paged needs: 0 for every size. */
 size_t mamba2_attn_paged_workspace_bytes(const m2_kv_cache* c, int T, int n_heads);
 
+/* ------------------------------------------------------------------------
+ * Dense caches that stay bounded over a long session: whole prompts into the
+ * caches of mamba2_attn_decode, the attention weight that every cached position
+ * has received, and the eviction of the positions that received least (the
+ * attention KV caches of "docs/nemotron-voicechat.md", section Online session,
+ * which otherwise grow by a position a frame for as long as a session lasts).
+ * The model's attention layers rotate nothing, so a position may move to
+ * another slot.
+ *
+ * k_cache, v_cache [n_sessions, n_kv_heads, max_len, 128] in `act`; acc
+ * [n_sessions, n_kv_heads, max_len] fp32, the weight that each cached position
+ * has received, summed over the query heads of its kv head and over the queries
+ * so far. Slots at and past a session's length are not read in any of them.
+ * Where acc_out is not acc, it must not overlap it.
+ * Sizes, all four calls: head_dim 128; n_heads a multiple of n_kv_heads, at most
+ * 8 query heads per kv head; n_sessions and n_kv_heads at most 65535; max_len
+ * at most 2^30. Pointers 16-byte aligned (row_start, lengths, lse and kept:
+ * 4-byte). n_sessions == 0 is a no-op once the arguments check out.
+ * Asynchronous on `stream`. Nothing is added up by atomics: a call gives the
+ * same bits each time. */
+
+/* Attention of whole prompts, packed, with their append to the dense caches:
+ * grouped query heads, causal, sequences of different lengths, each from an
+ * empty cache or behind what its session has cached. Session s has the packed
+ * rows row_start[s] .. row_start[s + 1] - 1 (none: allowed), and with lengths[s]
+ * positions cached (lengths NULL: none) its row t goes to position lengths[s] + t:
+ *     k_cache[s][g][lengths[s] + t] = k_new[row],  v_cache likewise
+ *     a_p = scale * q[row][h] . k_cache[s][g][p]    for p = 0 .. lengths[s] + t
+ *     out[row][h] = sum_p softmax(a)_p v_cache[s][g][p]
+ *     lse[row][h] = ln sum_p exp(a_p)
+ * where query head h reads kv head g = h / (n_heads / n_kv_heads). The caller
+ * advances lengths.
+ *
+ * row_start: int32 [n_sessions + 1] in DEVICE memory, not decreasing, within
+ *   [0, n_rows]; rows outside every session's are left as they were in out, lse.
+ * q, out: n_rows rows of n_heads * 128 activations, q_stride (out_stride)
+ *   elements apart; k_new, v_new: n_rows rows of n_kv_heads * 128, kv_stride
+ *   apart, so that they may be columns of the projection's rows q | k | v.
+ *   Strides times the element size a multiple of 16 bytes. out must not overlap
+ *   an input (M2_EINVAL where it is q, k_new or v_new).
+ * lse: [n_rows, n_heads] fp32, for mamba2_attn_prompt_weights (NULL: not wanted).
+ * n_rows * n_kv_heads at most 2^30.
+ * Scores, maxima and sums are fp32, out is rounded once; in bf16 a softmax
+ *   weight enters its product with the values rounded to bf16 (2^-8 of itself).
+ * A value that is not finite makes the outputs of the rows that see it not
+ *   finite (in its dim, or NaN in all dims), and no others.
+ * Errors: M2_EINVAL, M2_ESHAPE, M2_EALIGN, M2_EUNSUPPORTED, M2_ECUDA. A bounded
+ *   wait that runs out records 0x101 or 0x102 (mamba2_device_error). Seen only on
+ *   the device, in the error word: 0x104, a negative length or positions past
+ *   max_len: that session's rows of out are zeros, of lse -infinity, and its
+ *   caches are as they were; 0x106, a row_start that decreases or lies outside
+ *   [0, n_rows]: the sessions on both sides of it are left out. */
+m2_status mamba2_attn_prompt(int n_sessions, int n_rows, int n_heads, int n_kv_heads, int head_dim, int max_len,
+                             m2_dtype act, const int32_t* row_start, const int32_t* lengths, const void* q, long q_stride,
+                             const void* k_new, const void* v_new, long kv_stride, void* k_cache, void* v_cache,
+                             float scale, void* out, long out_stride, float* lse, void* stream);
+
+/* The weight that cached positions receive from the last `window` rows of each
+ * session of a packed prompt (window >= n_rows: from all of them; 0: from none),
+ * with the rows' lse as mamba2_attn_prompt left it, for p < lengths[s] + n with
+ * n the session's rows:
+ *     acc_out[s][g][p] = (p < lengths[s] ? acc[s][g][p] : 0)
+ *         + sum over rows t >= n - window with p <= lengths[s] + t, and heads h of
+ *           kv head g, of exp(scale * q[row][h] . k_cache[s][g][p] - lse[row][h])
+ * To be called behind mamba2_attn_prompt with the same arguments, before the
+ * caller advances lengths. Other slots of acc_out are left as they were; acc_out
+ * may be acc. Sums in fp32.
+ * Errors as mamba2_attn_prompt; a session with 0x104 or 0x106 is left out. */
+m2_status mamba2_attn_prompt_weights(int n_sessions, int n_rows, int n_heads, int n_kv_heads, int head_dim, int max_len,
+                                     m2_dtype act, const int32_t* row_start, const int32_t* lengths, const void* q,
+                                     long q_stride, const void* k_cache, float scale, const float* lse, int window,
+                                     const float* acc, float* acc_out, void* stream);
+
+/* mamba2_attn_decode (one cached position a session, its arguments and results)
+ * that also adds up the weight each position receives: for p <= lengths[s] = L
+ *     acc_out[s][g][p] = (p < L ? acc[s][g][p] : 0) + sum over the heads of kv
+ *                        head g of their softmax weight of p
+ * in fp32; acc_out may be acc, its slots past L are left as they were. out and
+ * the caches hold the same bits as after mamba2_attn_decode.
+ * Scratch: workspace of at least mamba2_attn_decode_weights_workspace_bytes(...)
+ *   (the scores, until their softmax's sum is known): 4 bytes for every position
+ *   and head of the caches, about.
+ * Errors as mamba2_attn_decode; a session with a length outside [0, max_len) has
+ *   its acc_out left as it was. */
+m2_status mamba2_attn_decode_weights(int n_sessions, int n_heads, int n_kv_heads, int head_dim, int max_len, m2_dtype act,
+                                     const int32_t* lengths, const void* q, const void* k_new, const void* v_new,
+                                     void* k_cache, void* v_cache, float scale, void* out, const float* acc,
+                                     float* acc_out, void* workspace, size_t workspace_bytes, void* stream);
+size_t mamba2_attn_decode_weights_workspace_bytes(int n_sessions, int n_heads, int n_kv_heads, int head_dim, int max_len,
+                                                  m2_dtype act);
+
+/* Eviction by accumulated weight. A session with lengths[s] = L > keep positions
+ * keeps, in each kv head, its last `recent` positions and of the older ones the
+ * keep - recent with the largest acc (of equal ones the lowest positions; a NaN
+ * counts as the largest); one with L <= keep keeps all. With kept_0 < kept_1 < ...
+ * the positions that stay, n = min(L, keep) of them,
+ *     k_out[s][g][j] = k_cache[s][g][kept_j],  v_out and acc_out likewise,
+ *     kept[s][g][j] = kept_j                              for j < n,
+ * bit for bit; what lies past n is left as it was. The caller sets lengths to
+ * min(lengths, keep).
+ *
+ * k_out, v_out [n_sessions, n_kv_heads, out_max_len, 128], acc_out [n_sessions,
+ *   n_kv_heads, out_max_len]: either the caches themselves (in place: k_out is
+ *   k_cache and v_out is v_cache, out_max_len is max_len; acc_out may be acc
+ *   whenever out_max_len is max_len) or memory that overlaps none of the inputs
+ *   (M2_EINVAL otherwise), for instance smaller caches.
+ * kept: int32 [n_sessions, n_kv_heads, keep] (NULL: not wanted).
+ * 1 <= keep <= out_max_len (M2_EINVAL, M2_ESHAPE), 0 <= recent <= keep
+ *   (M2_EINVAL).
+ * Errors: M2_EINVAL, M2_ESHAPE, M2_EALIGN, M2_EUNSUPPORTED, M2_ECUDA; in the
+ *   error word: 0x104, a length outside [0, max_len]: that session is left out. */
+m2_status mamba2_kv_evict(int n_sessions, int n_kv_heads, int head_dim, int max_len, m2_dtype act, const int32_t* lengths,
+                          const void* k_cache, const void* v_cache, const float* acc, int keep, int recent,
+                          int out_max_len, void* k_out, void* v_out, float* acc_out, int32_t* kept, void* stream);
+
 /* Static description of a status code. */
 const char* mamba2_status_string(m2_status s);
 
@@ -646,8 +762,8 @@ int mamba2_last_cuda_error(void);
 /* Reads and clears the device-side error word of the current device
  * (0 = no error; otherwise the code of the first condition since the last read:
  * 0x101 or 0x102, a bounded wait that ran out; 0x104, a length that does not fit
- * its cache; 0x105, a page number outside the pool). Later conditions are not
- * kept: a call that met several shows the others when it is made again with the
+ * its cache; 0x105, a page number outside the pool; 0x106, packed rows of a
+ * session outside the call's). Later conditions are not kept: a call that met several shows the others when it is made again with the
  * first mended. Synchronises `stream`. Returns M2_ECUDA if the read itself
  * fails. */
 m2_status mamba2_device_error(void* stream, unsigned int* code);
