@@ -107,7 +107,7 @@ __global__ void __launch_bounds__(kPfThreads) prompt_fp32_kernel(PromptArgs a) {
         *reinterpret_cast<float4*>(sQ + row * kPfPitch + d) = v;
     }
     const size_t cache0 = ((size_t)s * a.Hkv + g) * a.Tmax * kAttnD;
-    const float sl2 = a.scale * kDenseLog2e;
+    const float sl2 = a.scale * kLog2e;
     int lim[4];  // the last position that this thread's rows see
     float m[4], l[4], o[4][8];
     bool bad[4];
@@ -176,14 +176,14 @@ __global__ void __launch_bounds__(kPfThreads) prompt_fp32_kernel(PromptArgs a) {
             }
 #pragma unroll
             for (int off = 1; off < 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
-            const float now = fmaxf(m[i], top), f = dense_ex2(m[i] - now);
+            const float now = fmaxf(m[i], top), f = ex2_approx(m[i] - now);
             m[i] = now;
             l[i] *= f;
 #pragma unroll
             for (int e = 0; e < 8; ++e) o[i][e] *= f;
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float p = dense_ex2(w[i][j] - now);
+                const float p = ex2_approx(w[i][j] - now);
                 l[i] += p;
                 sP[(4 * ty + i) * (kPfPos + 4) + tx + 16 * j] = p;
             }
@@ -228,7 +228,7 @@ __global__ void __launch_bounds__(kPfThreads) prompt_fp32_kernel(PromptArgs a) {
             store_act<TA>(a.out, at + 4 * tx + e, o[i][e] * inv);
             store_act<TA>(a.out, at + 64 + 4 * tx + e, o[i][4 + e] * inv);
         }
-        if (a.lse && tx == 0) a.lse[packed * a.Hq + g * R + row % R] = m[i] * kDenseLn2 + logf(l[i]);
+        if (a.lse && tx == 0) a.lse[packed * a.Hq + g * R + row % R] = m[i] * kLn2 + logf(l[i]);
     }
 }
 
@@ -246,7 +246,7 @@ cudaError_t launch_fp32(const PromptArgs& a, cudaStream_t st) {
 cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t st) {
     cudaError_t e = launch_append(a, st);
     if (e != cudaSuccess) return e;
-    return a.bf16 ? launch_fp32<bf16_t>(a, st) : launch_fp32<float>(a, st);
+    return a.bf16 ? launch_attn_prompt_tiles(a, st) : launch_fp32<float>(a, st);
 }
 
 }  // namespace m2

@@ -63,7 +63,7 @@ __global__ void __launch_bounds__(kWfThreads) weights_fp32_kernel(PromptArgs a, 
             if (p0 + p < total) k = load4<TA>(a.k_cache, (head + p0 + p) * kAttnD + d);
             *reinterpret_cast<float4*>(sK + p * kWfPitch + d) = k;
         }
-    const float sl2 = a.scale * kDenseLog2e;
+    const float sl2 = a.scale * kLog2e;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
     for (int t0 = first; t0 < x.n; t0 += per) {
         const int rows = min(per, x.n - t0) * R;
@@ -75,7 +75,7 @@ __global__ void __launch_bounds__(kWfThreads) weights_fp32_kernel(PromptArgs a, 
                 v = load4<TA>(a.q, (size_t)(x.row0 + t0 + row / R) * a.q_stride + (size_t)(g * R + row % R) * kAttnD + d);
             *reinterpret_cast<float4*>(sQ + row * kWfPitch + d) = v;
         }
-        if (tid < rows) sL[tid] = a.lse[(size_t)(x.row0 + t0 + tid / R) * a.Hq + g * R + tid % R] * kDenseLog2e;
+        if (tid < rows) sL[tid] = a.lse[(size_t)(x.row0 + t0 + tid / R) * a.Hq + g * R + tid % R] * kLog2e;
         __syncthreads();
         float d4[4][4];
 #pragma unroll
@@ -104,7 +104,7 @@ __global__ void __launch_bounds__(kWfThreads) weights_fp32_kernel(PromptArgs a, 
             const int row = 4 * ty + i, see = row < rows ? x.before + t0 + row / R - p0 : -1;
 #pragma unroll
             for (int j = 0; j < 4; ++j)
-                if (tx + 16 * j <= see) sum[j] += dense_ex2(fmaf(d4[i][j], sl2, -sL[row]));
+                if (tx + 16 * j <= see) sum[j] += ex2_approx(fmaf(d4[i][j], sl2, -sL[row]));
         }
     }
     __syncthreads();

@@ -29,6 +29,8 @@ struct PromptArgs {
 };
 // (the append into the caches, then the attention over them)
 cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t st);
+// the attention in bf16, behind the append (m2_attn_prompt_tile.cu)
+cudaError_t launch_attn_prompt_tiles(const PromptArgs& a, cudaStream_t st);
 
 // Weights that cached positions receive from the last `window` rows of each
 // session: PromptArgs' q, lse (read) and k_cache, and

@@ -1,11 +1,10 @@
 // Device helpers shared by the kernels over packed prompts and dense caches.
 #pragma once
 
-#include <float.h>
-
 #include "m2_common.cuh"
 #include "m2_dense.h"
 #include "m2_launch.h"
+#include "m2_tile_dev.cuh"
 
 namespace m2 {
 
@@ -64,12 +63,6 @@ inline long most_tiles(int S, int rows, int per) {
     return n < rows ? n : rows;
 }
 
-// 2^x, lg2 x
-__device__ __forceinline__ float dense_ex2(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-constexpr float kDenseLog2e = 1.4426950408889634f, kDenseLn2 = 0.6931471805599453f;
+constexpr float kLn2 = 0.6931471805599453f;
 
 }  // namespace m2

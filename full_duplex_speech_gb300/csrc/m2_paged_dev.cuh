@@ -9,22 +9,10 @@
 #include "m2_common.cuh"
 #include "m2_paged.h"
 #include "m2_tc.cuh"
+#include "m2_tile_dev.cuh"
 
 namespace m2 {
 
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNone = -FLT_MAX;  // a running maximum before any position: below every finite score
-
-__device__ __forceinline__ float ex2_approx(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
-__device__ __forceinline__ float lg2_approx(float x) {
-    float r;
-    asm("lg2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
-}
 // two e4m3 codes (the low byte first) as fp16, exactly
 __device__ __forceinline__ uint32_t e4m3x2_to_f16x2(uint32_t two) {
     uint32_t r;
@@ -42,11 +30,6 @@ __device__ __forceinline__ uint32_t pack_f16x2(float lo, float hi) {
     asm("cvt.rn.f16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
     return r;
 }
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 __device__ __forceinline__ float2 unpack_f16x2(uint32_t v) { return __half22float2(*reinterpret_cast<const __half2*>(&v)); }
 // 16 bytes global -> shared
 __device__ __forceinline__ void cp_async16(void* dst, const void* src) {
@@ -60,27 +43,6 @@ __device__ __forceinline__ void cp_async4(void* dst, const void* src) {
 // cp.async copies have landed.
 __device__ __forceinline__ void cp_async_arrive(uint64_t* bar) {
     asm volatile("cp.async.mbarrier.arrive.noinc.shared.b64 [%0];" ::"r"(tc::smem_u32(bar)) : "memory");
-}
-
-// 16 bytes into a cluster's shared window
-__device__ __forceinline__ void st_cluster_f32x4(uint32_t caddr, float4 v) {
-    asm volatile("st.shared::cluster.v4.f32 [%0], {%1, %2, %3, %4};" ::"r"(caddr), "f"(v.x), "f"(v.y), "f"(v.z), "f"(v.w)
-                 : "memory");
-}
-
-// ... and out of it
-__device__ __forceinline__ float4 ld_cluster_f32x4(uint32_t caddr) {
-    float4 v;
-    asm volatile("ld.shared::cluster.v4.f32 {%0, %1, %2, %3}, [%4];"
-                 : "=f"(v.x), "=f"(v.y), "=f"(v.z), "=f"(v.w)
-                 : "r"(caddr)
-                 : "memory");
-    return v;
-}
-
-// The descriptor of the copies to come, fetched ahead of the first.
-__device__ __forceinline__ void prefetch_map(const CUtensorMap* map) {
-    asm volatile("prefetch.tensormap [%0];" ::"l"(map) : "memory");
 }
 
 // The power of two that takes a row's largest magnitude to [2^to, 2^(to + 1))
