@@ -56,8 +56,8 @@ struct PtSmem {
     static constexpr uint32_t kBad = kBar + kBars * 8;               // values that are not finite: a bit a position
     static constexpr uint32_t kTmem = kBad + kPtCut * 16;
     static constexpr uint32_t kFlag = kTmem + 4;
-    static constexpr uint32_t kFind = kFlag + 4;
-    static constexpr uint32_t kBytes = kFind + (kPtThreads / 32 + 4) * 4 + 1024;  // + slack to align to 1024
+    static constexpr uint32_t kWork = kFlag + 4;                     // session, its first packed row, rows, positions before, pair
+    static constexpr uint32_t kBytes = kWork + 5 * 4 + 1024;         // + slack to align to 1024
     // after the walk, over the ring: 256 rows x 128 floats, then their (m, l)
     static constexpr uint32_t kMl = kRing + 2 * kPtRows * kAttnD * 4;
     static_assert(kMl + 2 * kPtRows * 8 <= kBar, "the merge fits in the ring");
@@ -66,7 +66,71 @@ struct PtSmem {
 
 constexpr int kRegsLaunch = 168, kRegsFew = 72, kRegsMany = 216;
 static_assert(128 * kRegsFew + 256 * kRegsMany <= kPtThreads * kRegsLaunch, "the split is covered by the launch's registers");
-__device__ __forceinline__ void all_done() { asm volatile("barrier.sync 1, %0;" ::"n"(kPtThreads) : "memory"); }
+// the threads of a tile's softmax; of both tiles'
+__device__ __forceinline__ void tile_sync(int i) { asm volatile("barrier.sync %0, 128;" ::"r"(4 + i) : "memory"); }
+__device__ __forceinline__ void tiles_sync() { asm volatile("barrier.sync 6, 256;" ::: "memory"); }
+
+// A box of shared memory out to a tensor map's coordinates.
+__device__ __forceinline__ void tma_store_3d(const void* tmap, int x, int y, int z, const void* src) {
+    asm volatile("cp.async.bulk.tensor.3d.global.shared::cta.tile.bulk_group [%0, {%1, %2, %3}], [%4];" ::"l"(tmap), "r"(x),
+                 "r"(y), "r"(z), "r"(tc::smem_u32(src))
+                 : "memory");
+}
+
+// The pair of tiles `at` of all the sessions' pairs of `per` packed rows each,
+// found by a warp, eight sessions a lane at a time (a session's last pair first:
+// it sees the most positions). A session whose rows do not lie within the call's
+// has none, and is recorded.
+__device__ __forceinline__ bool find_pair(const PromptArgs& a, int per, int at, Session* x, int* session, int* pair) {
+    constexpr int kEach = 8;
+    const int lane = threadIdx.x & 31;
+    int base = 0;
+    for (int s0 = 0; s0 < a.S; s0 += 32 * kEach) {
+        int b[kEach + 1], before[kEach], n[kEach], mine = 0;
+        const int first = s0 + lane * kEach;
+#pragma unroll
+        for (int i = 0; i <= kEach; ++i) b[i] = first + i <= a.S ? a.start[first + i] : 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) before[i] = a.lens && first + i < a.S ? a.lens[first + i] : 0;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            n[i] = 0;
+            if (first + i < a.S) {
+                if (b[i] < 0 || b[i + 1] < b[i] || b[i + 1] > a.rows)
+                    record_error(a.err, ERR_ROW_START);
+                else
+                    n[i] = (b[i + 1] - b[i] + per - 1) / per;
+            }
+            mine += n[i];
+        }
+        int upto = mine;
+#pragma unroll
+        for (int off = 1; off < 32; off <<= 1) {
+            const int below = __shfl_up_sync(0xffffffffu, upto, off);
+            if (lane >= off) upto += below;
+        }
+        int ahead = base + upto - mine;
+        int v[5] = {-1, 0, 0, 0, 0};
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) {
+            if (at >= ahead && at < ahead + n[i])
+                v[0] = first + i, v[1] = b[i], v[2] = b[i + 1] - b[i], v[3] = before[i], v[4] = n[i] - 1 - (at - ahead);
+            ahead += n[i];
+        }
+        const unsigned who = __ballot_sync(0xffffffffu, v[0] >= 0);
+        if (who) {
+            const int from = __ffs(who) - 1;
+            *session = __shfl_sync(0xffffffffu, v[0], from);
+            x->row0 = __shfl_sync(0xffffffffu, v[1], from);
+            x->n = __shfl_sync(0xffffffffu, v[2], from);
+            x->before = __shfl_sync(0xffffffffu, v[3], from);
+            *pair = __shfl_sync(0xffffffffu, v[4], from);
+            return true;
+        }
+        base += __shfl_sync(0xffffffffu, upto, 31);
+    }
+    return false;
+}
 
 // The merge of a cluster's W parts of the rows that CTA wk owns, a warp a row,
 // four dims a lane:
@@ -110,7 +174,7 @@ __device__ __forceinline__ void merge_rows(const PromptArgs& a, uint8_t* sm, int
 // grid (W x Hkv x pairs of tiles), a cluster of W CTAs when W > 1
 __global__ void __launch_bounds__(kPtThreads, 1)
     attn_prompt_tile_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                            const __grid_constant__ CUtensorMap tmv, int W) {
+                            const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo, int W) {
     using L = PtSmem;
     extern __shared__ uint8_t pt_raw[];
     uint8_t* sm = pt_raw + ((1024u - (tc::smem_u32(pt_raw) & 1023u)) & 1023u);
@@ -120,21 +184,51 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     uint32_t* sBad = reinterpret_cast<uint32_t*>(sm + L::kBad);
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + L::kTmem);
     volatile uint32_t* flag = reinterpret_cast<uint32_t*>(sm + L::kFlag);
-    const int wk = (int)blockIdx.x % W, pair = (int)blockIdx.x / W, g = pair % a.Hkv;
+    int* work = reinterpret_cast<int*>(sm + L::kWork);
+    const int wk = (int)blockIdx.x % W, g = (int)blockIdx.x / W % a.Hkv;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int R = a.Hq / a.Hkv, per = kPtRows / R;  // packed rows a tile
 
-    if (tid == 32) prefetch_map(&tmq), prefetch_map(&tmk), prefetch_map(&tmv);
     if (W > 1) tc::cluster_arrive_relaxed();  // waited on before the first remote access: every CTA has started
-    pdl_wait();  // the rows and the caches come from the previous kernels
-    int s, tile2;
-    if (!find_tile(a, 2 * per, pair / a.Hkv, reinterpret_cast<int*>(sm + L::kFind), &s, &tile2)) return;  // the whole cluster
+    // Which rows: warp 0, which then sets the first copies going, while warp 1 takes the tensor
+    // memory. (The kernel before this one is this call's append, which has waited for what
+    // came before: only the caches are its own.)
+    if (warp == 0) {
+        if (lane == 0) {
+            prefetch_map(&tmq), prefetch_map(&tmk), prefetch_map(&tmv);
+            for (int i = 0; i < kPtStages; ++i) tc::mbar_init(full + i, 1), tc::mbar_init(empty + i, 1);
+            tc::mbar_init(qbar, 1);
+            for (int i = 0; i < kPtCut; ++i) tc::mbar_init(cutfull + i, 1), tc::mbar_init(mended + i, 1);
+            for (int i = 0; i < 2; ++i) tc::mbar_init(sfull + i, 1), tc::mbar_init(ofull + i, 1);
+            tc::mbar_init(endbar, 1);
+            tc::fence_mbar_init();
+            *flag = 0;
+        }
+        Session y;
+        int s = -1, pair = 0;
+        if (!find_pair(a, 2 * per, (int)blockIdx.x / W / a.Hkv, &y, &s, &pair)) s = -1;
+        if (lane == 0) work[0] = s, work[1] = y.row0, work[2] = y.n, work[3] = y.before, work[4] = pair;
+    } else if (warp == 1) {
+        tc::tmem_alloc(sTmem, 512);
+        tc::tmem_relinquish();
+    } else if (tid - 64 < kPtCut * 4) {
+        sBad[tid - 64] = 0u;
+    }
+    tc::tc_fence_before();
+    __syncthreads();
+    tc::tc_fence_after();
+    const uint32_t tm = *sTmem;
+    const int s = work[0];
     Session x;
-    session_of(a, s, &x);
-    const int t0 = tile2 * 2 * per, row_end = min(t0 + 2 * per, x.n);  // the pair's packed rows of the session
-    if (!x.ok) {
+    x.row0 = work[1], x.n = work[2], x.before = work[3];
+    x.ok = s >= 0 && x.before >= 0 && (long)x.before + x.n <= a.Tmax;
+    const int t0 = work[4] * 2 * per, row_end = min(t0 + 2 * per, x.n);  // the pair's packed rows of the session
+    pdl_wait();     // the append, and with it what it waited for
+    pdl_trigger();  // not before the tensor memory is held: the next kernel may take some before it waits for this one
+    if (!x.ok) {  // the whole cluster
+        if (warp == 1) tc::tmem_dealloc(tm, 512);
+        if (s < 0 || wk) return;  // (past the last pair: nothing to do)
         if (tid == 0) record_error(a.err, ERR_ATTN_LENGTH);
-        if (wk) return;
         const int rows = (row_end - t0) * R;
         for (int i = tid; i < rows * (kAttnD / 8); i += kPtThreads) {
             const int row = i / (kAttnD / 8);
@@ -155,26 +249,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const int nc0 = min(max((total0 + kPtPos - 1) / kPtPos - cb, 0), nc);
     const int nc1 = row_end > t0 + per ? nc : 0;
     const int cut = max(all / kPtPos, cb);      // the first of the run's chunks that is not whole for every row
-
-    if (tid == 0) {
-        for (int i = 0; i < kPtStages; ++i) tc::mbar_init(full + i, 1), tc::mbar_init(empty + i, 1);
-        tc::mbar_init(qbar, 1);
-        for (int i = 0; i < kPtCut; ++i) tc::mbar_init(cutfull + i, 1), tc::mbar_init(mended + i, 1);
-        for (int i = 0; i < 2; ++i) tc::mbar_init(sfull + i, 1), tc::mbar_init(ofull + i, 1);
-        tc::mbar_init(endbar, 1);
-        tc::fence_mbar_init();
-        *flag = 0;
-    }
-    if (tid < kPtCut * 4) sBad[tid] = 0u;
-    if (warp == 1) {
-        tc::tmem_alloc(sTmem, 512);
-        tc::tmem_relinquish();
-    }
-    tc::tc_fence_before();
-    __syncthreads();
-    tc::tc_fence_after();
-    const uint32_t tm = *sTmem;
-    pdl_trigger();  // not before the tensor memory is held: the next kernel may take some before it waits for this one
 
     // A bounded wait; the first that runs out stops the CTA's work.
     auto wait_ok = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -278,30 +352,36 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 const int piece = 2 * j + 1;
                 if (!warp_ok(cutfull + (cb + j - cut), 0)) break;
                 uint8_t* v = sm + L::kRing + stage(piece) * kPtTile;
-                const int left = total - (cb + j) * kPtPos;  // positions behind it hold anything
+                // positions of the chunk from `from` on are not seen by every row, and there is nothing from
+                // `left` on; lanes 0 .. 15 have the 16 pieces of a position, 16 .. 31 of the next
+                const int from = max(all - (cb + j) * kPtPos, 0), left = min(total - (cb + j) * kPtPos, kPtPos);
                 uint32_t* bad = sBad + 4 * (cb + j - cut);
-#pragma unroll 4
-                for (int i = lane; i < (int)(kPtTile / 16); i += 32) {
-                    uint4* at = reinterpret_cast<uint4*>(v) + i;
-                    const int p = (i >> 3) & 127;  // (whichever its piece, swizzled: all of a row's bytes count)
-                    const uint4 w = *at;
-                    const uint32_t u[4] = {w.x, w.y, w.z, w.w};
-                    bool off = false;
+                uint8_t* mine = v + (lane & 7) * 16 + ((lane >> 3) & 1) * kPtPanel;
+                for (int p0 = from + (lane >> 4); p0 < left; p0 += 16) {
+                    uint4 w[8];
 #pragma unroll
-                    for (int e = 0; e < 4; ++e) off |= (u[e] & 0x7F80u) == 0x7F80u || (u[e] & 0x7F800000u) == 0x7F800000u;
-                    if (p >= left || off) {
-                        *at = make_uint4(0u, 0u, 0u, 0u);
-                        if (p < left) atomicOr(bad + (p >> 5), 1u << (p & 31));
+                    for (int k = 0; k < 8; ++k)
+                        if (p0 + 2 * k < left) w[k] = *reinterpret_cast<const uint4*>(mine + (p0 + 2 * k) * 128);
+#pragma unroll
+                    for (int k = 0; k < 8; ++k) {
+                        if (p0 + 2 * k >= left) break;
+                        const uint32_t u[4] = {w[k].x, w[k].y, w[k].z, w[k].w};
+                        bool off = false;
+#pragma unroll
+                        for (int e = 0; e < 4; ++e) off |= (u[e] & 0x7F80u) == 0x7F80u || (u[e] & 0x7F800000u) == 0x7F800000u;
+                        if (off) {
+                            *reinterpret_cast<uint4*>(mine + (p0 + 2 * k) * 128) = make_uint4(0u, 0u, 0u, 0u);
+                            atomicOr(bad + ((p0 + 2 * k) >> 5), 1u << ((p0 + 2 * k) & 31));
+                        }
                     }
                 }
+                for (int p = left + (lane >> 4); p < kPtPos; p += 2)
+                    *reinterpret_cast<uint4*>(mine + p * 128) = make_uint4(0u, 0u, 0u, 0u);
                 tc::fence_proxy_async_smem();
                 __syncwarp();
                 if (lane == 0) tc::mbar_arrive(mended + (cb + j - cut));
             }
         }
-        __syncwarp();
-        all_done();
-        regs_up<kRegsLaunch>();
     } else {
         // ------------------------------------------ softmax, one row a thread
         regs_up<kRegsMany>();
@@ -309,7 +389,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
         const uint32_t tS = tm + lanes + kColS + 128 * i, tO = tm + lanes + kColO + 128 * i;
         const int t = t0 + i * per + r / R;
-        const int lim = r < per * R && t < row_end ? x.before + t : -1;  // the last position seen
+        // The last position seen. (A row behind the tile's last goes with what the last one sees:
+        // hiding all from it took its warp 700 cycles more a chunk, and 80 us of the size below.)
+        const int lim = min(x.before + t, total - 1);
         const int nci = i ? nc1 : nc0;
         const float cs = fmaxf(fabsf(a.scale) * kLog2e, FLT_MIN);  // not 0: hidden scores are -inf
         bool good = true;
@@ -393,97 +475,105 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             tc::tc_fence_before();
         });
         l = (l0.x + l0.y) + (l1.x + l1.y);
-        __syncwarp();
-        regs_down<kRegsLaunch>();
-        all_done();
-    }
-    // ------------------------------------------------------------- the merge
-    __syncwarp();
-    const bool walked = warp < 4 || (warp < 8 ? nc0 : nc1) == 0 || warp_ok(ofull + (warp < 8 ? 0 : 1), 0);
-    tc::tc_fence_after();
-    __syncthreads();
-    const bool gave_up = *flag != 0;
-    if (gave_up && warp < 2 && tc::elect_one()) {
-        // the copies in flight must land and every product issued must be done
-        // before the tensor memory is freed and the CTA exits (all bounded)
-        if (warp == 0) {
-            tc::mbar_wait(qbar, 0, 100000000ull);
-            for (int i = 0; i < kPtStages; ++i)
-                tc::mbar_wait(full + i, 0, 100000000ull), tc::mbar_wait(full + i, 1, 100000000ull);
-            for (int i = 0; i < kPtCut; ++i) tc::mbar_wait(cutfull + i, 0, 100000000ull);
-        } else {
-            tc::mma_commit(endbar);
-            tc::mbar_wait(endbar, 0, 100000000ull);
-        }
-    }
-    __syncthreads();
-    if (W > 1) tc::cluster_wait();  // (pairs with the arrival at the start)
-    if (warp >= 4) {
-        const int i = (warp - 4) >> 2, row = tid - 128, r = row & 127;
-        const uint32_t tO = tm + ((uint32_t)((warp & 3) * 32) << 16) + kColO + 128 * i;
-        const bool some = walked && !gave_up && (i ? nc1 : nc0) > 0;  // (the same in the whole warp)
-        const int t = t0 + i * per + r / R;
+        good = good && (nci == 0 || warp_ok(ofull + i, 0));
+        tc::tc_fence_after();
+        // ------------------------------------------------------------ O out
+        const bool some = good && nci > 0;  // (the same in the whole warp)
         const bool live = r < per * R && t < row_end;
         if (!some) m = kNone, l = 0.f;
         float poison = 0.f;  // NaN where the row sees a value that was not finite
-        if (live && some) {
-            for (int c = cut; c < cb + nc; ++c)
-                for (int w = 0; w < 4; ++w) {
-                    const int see = x.before + t - c * kPtPos - 32 * w;
-                    if (see >= 0 && (sBad[4 * (c - cut) + w] & (see >= 31 ? ~0u : (2u << see) - 1u))) poison = NAN;
-                }
-        }
+        for (int c = cut; c < cb + nc; ++c)
+            for (int w = 0; w < 4; ++w) {
+                const int see = lim - c * kPtPos - 32 * w;
+                const uint32_t off = sBad[4 * (c - cut) + w];
+                if (off && see >= 0 && (off & (see >= 31 ? ~0u : (2u << see) - 1u))) poison = NAN;
+            }
         const size_t packed = (size_t)x.row0 + t;
-        const size_t at = packed * a.out_stride + (size_t)(g * R + r % R) * kAttnD;
-        const float f = 1.f / l + poison;
-        uint8_t* own = sm + (row & ~31) * 256;  // W == 1: the warp's rows in bf16, over its tile's queries
-#pragma unroll 1
-        for (int q = 0; q < 4; ++q) {
-            float v[32];
-            if (some) {
+        if (W == 1) {
+            // in bf16 over the tile's queries, laid out as they were; a whole tile leaves by two copies
+            // of a thread, the last of a session two rows at a time (16 lanes a row)
+            const float f = 1.f / l + poison;
+            uint8_t* own = sm + L::kQ + i * kPtTile + r * 128;
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                float v[32];
                 tmem_ld32(tO + 32 * q, v);
                 tc::tmem_wait_ld();
-            } else {
-#pragma unroll
-                for (int k = 0; k < 32; ++k) v[k] = 0.f;
-            }
-            if (W == 1) {
 #pragma unroll
                 for (int k = 0; k < 32; k += 8) {
                     uint32_t w[4];
 #pragma unroll
                     for (int e = 0; e < 4; ++e) w[e] = pack_bf16x2(v[k + 2 * e] * f, v[k + 2 * e + 1] * f);
-                    *reinterpret_cast<uint4*>(own + lane * 256 + (((4 * q + k / 8) ^ (lane & 15)) << 4)) =
+                    *reinterpret_cast<uint4*>(own + (q >> 1) * kPtPanel + (((4 * (q & 1) + k / 8) ^ (r & 7)) << 4)) =
                         make_uint4(w[0], w[1], w[2], w[3]);
                 }
-            } else if (live) {
+            }
+            if (live && a.lse) a.lse[packed * a.Hq + g * R + r % R] = fmaf(m, kLn2, logf(l));
+            if (t0 + (i + 1) * per <= row_end) {
+                tc::fence_proxy_async_smem();
+                tile_sync(i);
+                if ((tid & 127) == 0) {
+                    for (int h = 0; h < 2; ++h)
+                        tma_store_3d(&tmo, 64 * h, g * R, x.row0 + t0 + i * per, sm + L::kQ + i * kPtTile + h * kPtPanel);
+                    asm volatile("cp.async.bulk.commit_group;" ::: "memory");
+                    asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+                }
+            } else {
+                __syncwarp();
+                const size_t at = packed * a.out_stride + (size_t)(g * R + r % R) * kAttnD;
+                const unsigned lives = __ballot_sync(0xffffffffu, live);
+#pragma unroll 4
+                for (int e = 0; e < 16; ++e) {
+                    const int rr = 2 * e + (lane >> 4), piece = lane & 15;
+                    const size_t to = __shfl_sync(0xffffffffu, at, rr);
+                    if (lives >> rr & 1u)
+                        *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + to + 8 * piece) =
+                            *reinterpret_cast<const uint4*>(sm + L::kQ + i * kPtTile + (piece >> 3) * kPtPanel +
+                                                            ((r & ~31) + rr) * 128 + (((piece & 7) ^ (rr & 7)) << 4));
+                }
+            }
+        } else {
+            tiles_sync();  // the ring is read: the tiles' products are done
+            const int row = 128 * i + r;
+#pragma unroll 1
+            for (int q = 0; q < 4; ++q) {
+                float v[32];
+                if (some) {
+                    tmem_ld32(tO + 32 * q, v);
+                    tc::tmem_wait_ld();
+                } else {
+#pragma unroll
+                    for (int k = 0; k < 32; ++k) v[k] = 0.f;
+                }
                 // 16-byte pieces rotated by the row, so that a warp's rows do not meet in one bank
 #pragma unroll
                 for (int k = 0; k < 8; ++k)
                     *reinterpret_cast<float4*>(sm + L::kRing + row * kAttnD * 4 + (((8 * q + k + row) & 31) << 4)) =
                         make_float4(v[4 * k] + poison, v[4 * k + 1] + poison, v[4 * k + 2] + poison, v[4 * k + 3] + poison);
             }
-            __syncwarp();
+            *reinterpret_cast<float2*>(sm + L::kMl + row * 8) = make_float2(m, l);
         }
-        if (W == 1) {
-            // two rows at a time, 16 lanes a row: whole lines go out
-            const unsigned lives = __ballot_sync(0xffffffffu, live);
-#pragma unroll 4
-            for (int e = 0; e < 16; ++e) {
-                const int rr = 2 * e + (lane >> 4), piece = lane & 15;
-                const size_t to = __shfl_sync(0xffffffffu, at, rr);
-                if (lives >> rr & 1u)
-                    *reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + to + 8 * piece) =
-                        *reinterpret_cast<const uint4*>(own + rr * 256 + ((piece ^ (rr & 15)) << 4));
-            }
-            if (live && a.lse) a.lse[packed * a.Hq + g * R + r % R] = fmaf(m, kLn2, logf(l));
-        }
-        if (W > 1 && live) *reinterpret_cast<float2*>(sm + L::kMl + row * 8) = make_float2(m, l);
     }
+    __syncwarp();
     tc::tc_fence_before();
     __syncthreads();
+    if (*flag) {  // (the same in the whole CTA)
+        // the copies in flight must land and every product issued must be done
+        // before the tensor memory is freed and the CTA exits (all bounded)
+        if (warp == 0 && tc::elect_one()) {
+            tc::mbar_wait(qbar, 0, 100000000ull);
+            for (int i = 0; i < kPtStages; ++i)
+                tc::mbar_wait(full + i, 0, 100000000ull), tc::mbar_wait(full + i, 1, 100000000ull);
+            for (int i = 0; i < kPtCut; ++i) tc::mbar_wait(cutfull + i, 0, 100000000ull);
+        } else if (warp == 1 && tc::elect_one()) {
+            tc::mma_commit(endbar);
+            tc::mbar_wait(endbar, 0, 100000000ull);
+        }
+        __syncthreads();
+    }
     if (warp == 1) tc::tmem_dealloc(tm, 512);
     if (W == 1) return;
+    tc::cluster_wait();    // (pairs with the arrival at the start)
     tc::cluster_arrive();  // every CTA's rows are in its shared memory ...
     tc::cluster_wait();
     merge_rows(a, sm, W, wk, row_end, x, t0, per, g);  // ... and each reads the rows that it owns
@@ -560,11 +650,12 @@ cudaError_t launch_attn_prompt_tiles(const PromptArgs& a, cudaStream_t st) {
     cudaError_t e = prompt_setup(&setup);
     if (e != cudaSuccess) return e;
     const int R = a.Hq / a.Hkv, per = kPtRows / R;
-    CUtensorMap tmq, tmk, tmv;
+    CUtensorMap tmq, tmk, tmv, tmo;
     const cuuint64_t row = kAttnD * 2;
     e = make_map(a.q, a.Hq, a.rows, row, (cuuint64_t)a.q_stride * 2, R, per, &tmq);
     if (e == cudaSuccess) e = make_map(a.k_cache, a.Tmax, (cuuint64_t)a.S * a.Hkv, row, row * a.Tmax, kPtPos, 1, &tmk);
     if (e == cudaSuccess) e = make_map(a.v_cache, a.Tmax, (cuuint64_t)a.S * a.Hkv, row, row * a.Tmax, kPtPos, 1, &tmv);
+    if (e == cudaSuccess) e = make_map(a.out, a.Hq, a.rows, row, (cuuint64_t)a.out_stride * 2, R, per, &tmo);
     if (e != cudaSuccess) return e;
     const long pairs = most_tiles(a.S, a.rows, 2 * per) * a.Hkv;
     int W = 1;
@@ -582,7 +673,7 @@ cudaError_t launch_attn_prompt_tiles(const PromptArgs& a, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = W > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, attn_prompt_tile_kernel, a, tmq, tmk, tmv, W);
+    return cudaLaunchKernelEx(&cfg, attn_prompt_tile_kernel, a, tmq, tmk, tmv, tmo, W);
 }
 
 }  // namespace m2
