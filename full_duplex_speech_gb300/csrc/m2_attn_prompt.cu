@@ -23,6 +23,19 @@ __global__ void __launch_bounds__(kApThreads) prompt_append_kernel(PromptArgs a,
     const int lane = threadIdx.x & 31;
     const int row = (int)((blockIdx.x * (long)kApThreads + threadIdx.x) >> 5);
     if (row >= a.rows) return;
+    const int pieces = a.Hkv * row_bytes / 16, per = row_bytes / 16;  // of keys, of a head
+    const size_t from = (size_t)row * a.kv_stride * (row_bytes / kAttnD);
+    const uint4* ks = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.k_new) + from);
+    const uint4* vs = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.v_new) + from);
+    // (the first of them are under way while the session is looked up)
+    constexpr int kFlight = 4;
+    uint4 k[kFlight], v[kFlight];
+    auto load = [&](int i0) {
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f)
+            if (i0 + 32 * f + lane < pieces) k[f] = __ldg(ks + i0 + 32 * f + lane), v[f] = __ldg(vs + i0 + 32 * f + lane);
+    };
+    load(0);
     // the last session whose first row is at or before this one
     int lo = 0, size = a.S;
     while (size > 1) {
@@ -34,17 +47,17 @@ __global__ void __launch_bounds__(kApThreads) prompt_append_kernel(PromptArgs a,
     }
     Session x;
     if (!session_of(a, lo, &x) || !x.ok || row < x.row0 || row >= x.row0 + x.n) return;
-    const int pieces = a.Hkv * row_bytes / 16, per = row_bytes / 16;  // of keys, of a head
-    const size_t esize = (size_t)row_bytes / kAttnD;
-    const size_t from = (size_t)row * a.kv_stride * esize;
     const size_t to = ((size_t)lo * a.Hkv * a.Tmax + x.before + (row - x.row0)) * row_bytes;
-    const uint4* ks = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.k_new) + from);
-    const uint4* vs = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.v_new) + from);
-#pragma unroll 4
-    for (int i = lane; i < pieces; i += 32) {
-        const size_t at = to + (size_t)(i / per) * a.Tmax * row_bytes + (size_t)(i % per) * 16;
-        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.k_cache) + at) = __ldg(ks + i);
-        *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.v_cache) + at) = __ldg(vs + i);
+    for (int i0 = 0; i0 < pieces; i0 += 32 * kFlight) {
+        if (i0 > 0) load(i0);
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) {
+            const int i = i0 + 32 * f + lane;
+            if (i >= pieces) continue;
+            const size_t at = to + (size_t)(i / per) * a.Tmax * row_bytes + (size_t)(i % per) * 16;
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.k_cache) + at) = k[f];
+            *reinterpret_cast<uint4*>(static_cast<uint8_t*>(a.v_cache) + at) = v[f];
+        }
     }
 }
 

@@ -326,8 +326,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         if (y.s >= 0) {
             const PtRun run(a, y, per, W, wk);
             copy_q(y, run, 0);
-            pdl_wait();
-            copy_pieces(y, run, 0, 0, min(kAhead, run.pieces));
         }
     } else if (warp == 1) {
         tc::tmem_alloc(sTmem, 512);
@@ -366,7 +364,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     ask_next(sm + L::kNext, next);
                 }
                 __syncwarp();
-                copy_pieces(y, run, first, min(kAhead, run.pieces), run.pieces);
+                // (first what need not wait for this pair's products, then the next pair, then the rest)
+                const int had = k > 0 ? min(kAhead, run.pieces) : 0, soon = min(kPtStages, run.pieces);
+                if (k == 0) pdl_wait();
+                copy_pieces(y, run, first, had, soon);
                 PtWork z = {-1, 0, 0, 0, 0, 0};
                 if (W == 1) {
                     good = good && warp_ok(next, (uint32_t)k & 1u);
@@ -375,6 +376,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     __syncwarp();
                     if (x >= 0) z = find_pair(a, 2 * per, x);
                 }
+                copy_pieces(y, run, first, soon, run.pieces);
                 if (lane == 0) *work(k + 1) = z;
                 if (z.s >= 0) {
                     const PtRun then(a, z, per, W, wk);
@@ -471,6 +473,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     } else {
         regs_up<kRegsMany>();
         int chunks = 0, walks = 0;  // of the tile so far
+        uint64_t* leaving = nullptr;  // thread 0 of the tile: the piece whose rows are still being copied out
+        auto left = [&] {
+            if (!leaving) return;
+            asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
+            tc::mbar_arrive(leaving);
+            leaving = nullptr;
+        };
         every_pair([&](const PtWork& y, const PtRun& run, int k, int before, int first) {
             // -------------------------------------- softmax, one row a thread
             const int i = (warp - 4) >> 2, r = tid - 128 - 128 * i;  // tile, row of it
@@ -561,6 +570,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 tc::tmem_wait_st();
                 return true;
             };
+            left();
             tc::tc_fence_before();
             tile_rows_meet(TileBarriers(), i, nci, [&](int j) {
                 here = here && softmax_chunk(j);
@@ -592,7 +602,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 uint8_t* mine = sm + L::kRing + at * kPtTile;
                 const size_t packed = (size_t)y.row0 + t;
                 const float f = run.ok ? 1.f / l + poison : 0.f;
-#pragma unroll
+#pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     float v[32];
                     tmem_ld32(tO + 32 * q, v);
@@ -614,8 +624,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         for (int h = 0; h < 2; ++h)
                             tma_store_3d(&tmo, 64 * h, y.g * R, y.row0 + run.t0 + i * per, mine + h * kPtPanel);
                         asm volatile("cp.async.bulk.commit_group;" ::: "memory");
-                        asm volatile("cp.async.bulk.wait_group.read 0;" ::: "memory");
-                        tc::mbar_arrive(empty + at);
+                        leaving = empty + at;
                     }
                 } else {
                     __syncwarp();
@@ -659,6 +668,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
             if (!run.ok && tid == 128) record_error(a.err, ERR_ATTN_LENGTH);
         });
+        left();
     }
     const PtWork y = *work(0);
     const bool none = y.s < 0;  // (W > 1: the whole cluster)
