@@ -53,16 +53,17 @@ constexpr uint32_t kPtTile = 2 * kPtPanel;
 constexpr int kPtStages = 5;                       // of a chunk's K or V, in turn
 constexpr float kPtSlack = 8.f;                    // log2 by which a chunk may exceed m
 constexpr int kPtCut = 3;                          // chunks that the tiles' at most 256 packed rows see partly, at most
+constexpr int kPtBad = 4 * kPtCut + 1;
 constexpr uint32_t kColO = 0, kColS = 256;         // tensor memory: O of the two tiles, then S (and p over it)
 
 struct PtSmem {
     static constexpr uint32_t kQ = 0;                                // [tile][panel] K-major
     static constexpr uint32_t kRing = kQ + 2 * kPtTile;              // K: K-major, V: MN-major; two panels each
     static constexpr uint32_t kBar = kRing + kPtStages * kPtTile;
-    // full[stages], empty[stages], ready[stages], qfull, qempty, s[2], o[2], next, end
-    static constexpr int kBars = 3 * kPtStages + 8;
-    static constexpr uint32_t kBad = kBar + kBars * 8;               // values that are not finite: a bit a position
-    static constexpr uint32_t kNext = (kBad + kPtCut * 16 + 15) / 16 * 16;  // the answer of clusterlaunchcontrol
+    // full[stages], empty[stages], ready[stages], qfull, qempty, s[2], o[2], next, passed, end
+    static constexpr int kBars = 3 * kPtStages + 9;
+    static constexpr uint32_t kBad = kBar + kBars * 8;               // values that are not finite: a bit a position, and whether any; in turn
+    static constexpr uint32_t kNext = (kBad + 2 * kPtBad * 4 + 15) / 16 * 16;  // the answer of clusterlaunchcontrol
     static constexpr uint32_t kWork = kNext + 16;                    // PtWork, in turn
     static constexpr uint32_t kTmem = kWork + 2 * 32;
     static constexpr uint32_t kFlag = kTmem + 4;
@@ -85,8 +86,14 @@ static_assert(128 * kRegsFew + 256 * kRegsMany <= kPtThreads * kRegsLaunch, "the
 __device__ __forceinline__ void tile_sync(int i) { asm volatile("barrier.sync %0, 128;" ::"r"(4 + i) : "memory"); }
 __device__ __forceinline__ void tiles_sync() { asm volatile("barrier.sync 6, 256;" ::: "memory"); }
 
-// all the CTA's warps, where a pair of tiles ends
-__device__ __forceinline__ void pairs_meet() { asm volatile("barrier.sync 1, %0;" ::"n"(kPtThreads) : "memory"); }
+// The next pair of tiles is known: warp 0 says so without waiting, and the softmax
+// of tile 0, that of tile 1 and the warps 1 to 3 wait for it, each for themselves.
+__device__ __forceinline__ void pair_known() {
+    asm volatile("barrier.arrive 7, 160;\n\tbarrier.arrive 8, 160;\n\tbarrier.arrive 9, 128;" ::: "memory");
+}
+__device__ __forceinline__ void pair_wait(int warp) {
+    asm volatile("barrier.sync %0, %1;" ::"r"(warp < 4 ? 9 : warp < 8 ? 7 : 8), "r"(warp < 4 ? 128 : 160) : "memory");
+}
 
 // Asks for the block index of a CTA that has not started, to run in its place;
 // the answer comes to `to`, counted on `bar`. Not to be asked again after a refusal.
@@ -191,7 +198,7 @@ struct PtRun {
         all = y.before + t0 + 1;
         total = y.before + row_end;
         const int total0 = y.before + min(t0 + per, row_end);
-        const int nch = ok ? (total + kPtPos - 1) / kPtPos : 0, cpw = (nch + W - 1) / W;
+        const int nch = ok ? (total + kPtPos - 1) / kPtPos : 0, cpw = W == 1 ? nch : (nch + W - 1) / W;
         cb = min(wk * cpw, nch);
         nc = min(cpw, nch - cb);
         nc0 = ok ? min(max((total0 + kPtPos - 1) / kPtPos - cb, 0), nc) : 0;
@@ -249,10 +256,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     uint8_t* sm = pt_raw + ((1024u - (tc::smem_u32(pt_raw) & 1023u)) & 1023u);
     uint64_t* full = reinterpret_cast<uint64_t*>(sm + L::kBar);
     uint64_t *empty = full + kPtStages, *ready = empty + kPtStages, *qfull = ready + kPtStages, *qempty = qfull + 1,
-             *sfull = qempty + 1, *ofull = sfull + 2, *next = ofull + 2, *endbar = next + 1;
-    uint32_t* sBad = reinterpret_cast<uint32_t*>(sm + L::kBad);
+             *sfull = qempty + 1, *ofull = sfull + 2, *next = ofull + 2, *passed = next + 1, *endbar = passed + 1;
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + L::kTmem);
     volatile uint32_t* flag = reinterpret_cast<uint32_t*>(sm + L::kFlag);
+    auto bad_of = [&](int k) { return reinterpret_cast<uint32_t*>(sm + L::kBad) + (k & 1) * kPtBad; };
     auto work = [&](int k) { return reinterpret_cast<PtWork*>(sm + L::kWork + (k & 1) * 32); };  // of the CTA's k-th pair
     const int wk = (int)blockIdx.x % W;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -314,6 +321,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             prefetch_map(&tmq), prefetch_map(&tmk), prefetch_map(&tmv), prefetch_map(&tmo);
             for (int i = 0; i < kPtStages; ++i) tc::mbar_init(full + i, 1), tc::mbar_init(empty + i, 1), tc::mbar_init(ready + i, 1);
             tc::mbar_init(qfull, 1), tc::mbar_init(qempty, 1), tc::mbar_init(next, 1), tc::mbar_init(endbar, 1);
+            tc::mbar_init(passed, kPtThreads / 32 - 1);
             for (int i = 0; i < 2; ++i) tc::mbar_init(sfull + i, 1), tc::mbar_init(ofull + i, 1);
             tc::fence_mbar_init();
             *flag = 0;
@@ -337,8 +345,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     const uint32_t tm = *sTmem;
     pdl_trigger();  // not before the tensor memory is held: the next kernel may take some before it waits for this one
 
-    // Each warp's loop over the CTA's pairs: role(y, run, k, q pairs with chunks before, first piece),
-    // and the meeting of all.
+    // Each warp's loop over the CTA's pairs: role(y, run, k, q pairs with chunks before, first piece).
+    // A tile's softmax goes on to the next pair by itself; warp 0 lets no warp fall two pairs behind.
     auto every_pair = [&](auto role) {
         PtWork y = *work(0);
         for (int k = 0, q = 0, first = 0; y.s >= 0; ++k) {
@@ -347,11 +355,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             first += run.pieces;
             q += run.nc > 0;
             __syncwarp();
-            tc::tc_fence_before();
-            pairs_meet();
-            tc::tc_fence_after();
             if (W > 1) break;
+            if (warp > 0) pair_wait(warp);
             y = *work(k + 1);
+            __syncwarp();
+            if (warp > 0 && lane == 0) tc::mbar_arrive(passed);
         }
     };
     if (warp < 4) {
@@ -375,9 +383,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     tc::fence_proxy_async_smem();  // (the answer is read before another may come)
                     __syncwarp();
                     if (x >= 0) z = find_pair(a, 2 * per, x);
+                    // (where the wait runs out, the others' waits end as soon as that is known: a second
+                    // one sees them pass)
+                    if (k > 0 && !warp_ok(passed, (uint32_t)(k - 1) & 1u)) good = false, tc::mbar_wait(passed, (uint32_t)(k - 1) & 1u);
+                    if (lane == 0) *work(k + 1) = z;
+                    __syncwarp();
+                    pair_known();
                 }
                 copy_pieces(y, run, first, soon, run.pieces);
-                if (lane == 0) *work(k + 1) = z;
                 if (z.s >= 0) {
                     const PtRun then(a, z, per, W, wk);
                     copy_q(z, then, before + (run.nc > 0));
@@ -432,7 +445,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 }, [](int, int) {});
             } else {
                 // ---------------------------- what has landed, looked over in turn
-                if (lane < kPtCut * 4) sBad[lane] = 0u;
+                uint32_t* bads = bad_of(k);
+                if (lane < kPtBad) bads[lane] = 0u;
                 __syncwarp();
                 for (int p = 0; p < run.pieces; ++p) {
                     const int at = stage(first + p), c = run.cb + (p >> 1);
@@ -441,7 +455,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         // positions of the chunk from `from` on are not seen by every row, and there is nothing from
                         // `left` on; lanes 0 .. 15 have the 16 pieces of a position, 16 .. 31 of the next
                         const int from = max(run.all - c * kPtPos, 0), left = min(run.total - c * kPtPos, kPtPos);
-                        uint32_t* bad = sBad + 4 * (c - run.cut);
+                        uint32_t* bad = bads + 4 * (c - run.cut);
                         uint8_t* mine = sm + L::kRing + at * kPtTile + (lane & 7) * 16 + ((lane >> 3) & 1) * kPtPanel;
                         for (int p0 = from + (lane >> 4); p0 < left; p0 += 16) {
                             uint4 w[8];
@@ -458,6 +472,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                                 if (off) {
                                     *reinterpret_cast<uint4*>(mine + (p0 + 2 * q) * 128) = make_uint4(0u, 0u, 0u, 0u);
                                     atomicOr(bad + ((p0 + 2 * q) >> 5), 1u << ((p0 + 2 * q) & 31));
+                                    bads[kPtBad - 1] = 1u;
                                 }
                             }
                         }
@@ -473,6 +488,11 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     } else {
         regs_up<kRegsMany>();
         int chunks = 0, walks = 0;  // of the tile so far
+        const int i = (warp - 4) >> 2, r = tid - 128 - 128 * i;  // tile, row of it
+        const int rt = i * per + r / R, rt0 = i * per + (r & ~31) / R;  // its packed row of the pair's, and the warp's first
+        const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
+        const uint32_t tS = tm + lanes + kColS + 128 * i, tO = tm + lanes + kColO + 128 * i;
+        const int head = r % R;
         uint64_t* leaving = nullptr;  // thread 0 of the tile: the piece whose rows are still being copied out
         auto left = [&] {
             if (!leaving) return;
@@ -482,15 +502,12 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         };
         every_pair([&](const PtWork& y, const PtRun& run, int k, int before, int first) {
             // -------------------------------------- softmax, one row a thread
-            const int i = (warp - 4) >> 2, r = tid - 128 - 128 * i;  // tile, row of it
-            const uint32_t lanes = (uint32_t)((warp & 3) * 32) << 16;
-            const uint32_t tS = tm + lanes + kColS + 128 * i, tO = tm + lanes + kColO + 128 * i;
-            const int t = run.t0 + i * per + r / R;
+            const int t = run.t0 + rt;
             // The last position seen. (A row behind the tile's last goes with what the last one sees:
             // hiding all from it took its warp 700 cycles more a chunk, and 80 us of the size below.)
             const int lim = min(y.before + t, run.total - 1);
             // ... and the fewest that a row of the warp sees
-            const int least = min(y.before + run.t0 + i * per + (r & ~31) / R, run.total - 1);
+            const int least = min(y.before + run.t0 + rt0, run.total - 1);
             const int nci = i ? run.nc1 : run.nc0;
             const float cs = fmaxf(fabsf(a.scale) * kLog2e, FLT_MIN);  // not 0: hidden scores are -inf
             bool here = true;
@@ -585,12 +602,14 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             // -------------------------------------------------------- O out
             const bool live = r < per * R && t < run.row_end;
             float poison = 0.f;  // NaN where the row sees a value that was not finite
-            for (int c = run.cut; c < run.cb + run.nc; ++c)
-                for (int w = 0; w < 4; ++w) {
-                    const int see = lim - c * kPtPos - 32 * w;
-                    const uint32_t off = sBad[4 * (c - run.cut) + w];
-                    if (off && see >= 0 && (off & (see >= 31 ? ~0u : (2u << see) - 1u))) poison = NAN;
+            const uint32_t* bads = bad_of(k);
+            if (nci > 0 && bads[kPtBad - 1]) {
+                for (int e = 0; e < 4 * (run.cb + run.nc - run.cut); ++e) {
+                    const int see = lim - run.cut * kPtPos - 32 * e;
+                    const uint32_t off = bads[e];
+                    if (see >= 0 && (off & (see >= 31 ? ~0u : (2u << see) - 1u))) poison = NAN;
                 }
+            }
             if (W == 1) {
                 if (run.t0 + i * per >= run.row_end) return;  // the tile has no rows
                 // in bf16 to a piece of the ring, laid out as the queries were; a whole tile leaves by two
@@ -616,7 +635,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         *reinterpret_cast<uint4*>(mine + (q >> 1) * kPtPanel + r * 128 + (((4 * (q & 1) + e / 8) ^ (r & 7)) << 4)) = x;
                     }
                 }
-                if (live && a.lse) a.lse[packed * a.Hq + y.g * R + r % R] = fmaf(m, kLn2, logf(l));
+                if (live && a.lse) a.lse[packed * a.Hq + y.g * R + head] = fmaf(m, kLn2, logf(l));
                 if (run.t0 + (i + 1) * per <= run.row_end) {
                     tc::fence_proxy_async_smem();
                     tile_sync(i);
@@ -628,7 +647,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     }
                 } else {
                     __syncwarp();
-                    const size_t to_row = packed * a.out_stride + (size_t)(y.g * R + r % R) * kAttnD;
+                    const size_t to_row = packed * a.out_stride + (size_t)(y.g * R + head) * kAttnD;
                     const unsigned lives = __ballot_sync(0xffffffffu, live);
 #pragma unroll 4
                     for (int e = 0; e < 16; ++e) {
@@ -670,8 +689,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         });
         left();
     }
-    const PtWork y = *work(0);
-    const bool none = y.s < 0;  // (W > 1: the whole cluster)
+    __syncthreads();
+    const PtWork y = *work(0);  // W > 1: the only one
+    const bool none = y.s < 0;  // ... of the whole cluster
     if (*flag) {                // (the same in the whole CTA: nobody waits any more)
         // the copies in flight must land and every product issued must be done
         // before the tensor memory is freed and the CTA exits (all bounded)
