@@ -211,46 +211,64 @@ struct PtRun {
 // The merge of a cluster's W parts of the rows that CTA wk owns, a warp a row,
 // four dims a lane:
 //     out = sum_w 2^(m_w - M) O_w / sum_w 2^(m_w - M) l_w
-__device__ __forceinline__ void merge_rows(const PromptArgs& a, uint8_t* sm, int W, int wk, const PtWork& y, const PtRun& run,
-                                           int per) {
-    const int lane = threadIdx.x & 31, R = a.Hq / a.Hkv, share = 2 * kPtRows / W;
+// Lane i holds the (m, l) of part i % W of the warp's row i / W; eight pieces of
+// a row's parts are on their way together (a row after the other, a part after the
+// other, took 8 us more of 35 with W = 2).
+template <int W>
+__device__ __forceinline__ void merge_rows(const PromptArgs& a, uint8_t* sm, int wk, const PtWork& y, const PtRun& run, int per) {
+    constexpr int kWarps = kPtThreads / 32, kShare = 2 * kPtRows / W, kRows = (kShare + kWarps - 1) / kWarps, kBatch = 8 / W;
+    static_assert(kRows * W <= 32, "a warp's parts, a lane each");
+    const int lane = threadIdx.x & 31, R = a.Hq / a.Hkv, first = wk * kShare + (int)(threadIdx.x >> 5);
     const uint32_t here = tc::smem_u32(sm);
-    for (int i = (int)(threadIdx.x >> 5); i < share; i += kPtThreads / 32) {
-        const int row = wk * share + i, tile = row >> 7, r = row & 127, t = run.t0 + tile * per + r / R;
-        if (r >= per * R || t >= run.row_end) continue;  // (the same in the whole warp)
-        float m = kNone, l = 0.f;
-        if (lane < W) {
-            const float2 ml = ld_cluster_f32x2(tc::cluster_map(here, (uint32_t)lane) + PtSmem::kMl + row * 8);
-            m = ml.x, l = ml.y;
-        }
-        float M = m;
+    auto row_of = [&](int n) { return min(first + kWarps * n, 2 * kPtRows - 1); };  // the warp's n-th row
+    const float2 ml = ld_cluster_f32x2(tc::cluster_map(here, (uint32_t)(lane % W)) + PtSmem::kMl + row_of(lane / W) * 8);
+    float M = ml.x;
 #pragma unroll
-        for (int off = 4; off > 0; off >>= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
-        M = __shfl_sync(0xffffffffu, M, 0);
-        const float f = lane < W ? ex2_approx(m - M) : 0.f;
-        float L = f * l;
+    for (int off = 1; off < W; off <<= 1) M = fmaxf(M, __shfl_xor_sync(0xffffffffu, M, off));
+    const float f = ex2_approx(ml.x - M);
+    float L = f * ml.y;
 #pragma unroll
-        for (int off = 4; off > 0; off >>= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
-        L = __shfl_sync(0xffffffffu, L, 0);
-        float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
-        for (int w = 0; w < W; ++w) {
-            const float fw = __shfl_sync(0xffffffffu, f, w);
-            const float4 v = ld_cluster_f32x4(tc::cluster_map(here, (uint32_t)w) + PtSmem::kRing + row * kAttnD * 4 +
-                                              (((lane + row) & 31) << 4));
-            o.x = fmaf(fw, v.x, o.x), o.y = fmaf(fw, v.y, o.y), o.z = fmaf(fw, v.z, o.z), o.w = fmaf(fw, v.w, o.w);
+    for (int off = 1; off < W; off <<= 1) L += __shfl_xor_sync(0xffffffffu, L, off);
+#pragma unroll 1
+    for (int n0 = 0; n0 < kRows; n0 += kBatch) {
+        float4 v[kBatch][W];
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b)
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const int row = row_of(n0 + b);
+                v[b][w] = ld_cluster_f32x4(tc::cluster_map(here, (uint32_t)w) + PtSmem::kRing + row * kAttnD * 4 +
+                                           (((lane + row) & 31) << 4));
+            }
+#pragma unroll
+        for (int b = 0; b < kBatch; ++b) {
+            const int n = n0 + b, row = row_of(n), from = min(n * W, 31);
+            float4 o = make_float4(0.f, 0.f, 0.f, 0.f);
+#pragma unroll
+            for (int w = 0; w < W; ++w) {
+                const float fw = __shfl_sync(0xffffffffu, f, min(from + w, 31));
+                const float4 x = v[b][w];
+                o.x = fmaf(fw, x.x, o.x), o.y = fmaf(fw, x.y, o.y), o.z = fmaf(fw, x.z, o.z), o.w = fmaf(fw, x.w, o.w);
+            }
+            const float Lr = __shfl_sync(0xffffffffu, L, from), Mr = __shfl_sync(0xffffffffu, M, from);
+            const int r = row & 127, t = run.t0 + (row >> 7) * per + r / R;
+            if (n >= kRows || first + kWarps * n >= (wk + 1) * kShare || r >= per * R || t >= run.row_end)
+                continue;  // (the same in the whole warp)
+            const float inv = run.ok ? 1.f / Lr : 0.f;  // (a refused session: zeros)
+            const size_t packed = (size_t)y.row0 + t;
+            *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + packed * a.out_stride + (size_t)(y.g * R + r % R) * kAttnD +
+                                      4 * lane) =
+                run.ok ? make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv)) : make_uint2(0u, 0u);
+            if (a.lse && lane == 0) a.lse[packed * a.Hq + y.g * R + r % R] = fmaf(Mr, kLn2, logf(Lr));
         }
-        const float inv = run.ok ? 1.f / L : 0.f;  // (a refused session: zeros)
-        const size_t packed = (size_t)y.row0 + t;
-        *reinterpret_cast<uint2*>(static_cast<uint16_t*>(a.out) + packed * a.out_stride + (size_t)(y.g * R + r % R) * kAttnD +
-                                  4 * lane) = make_uint2(pack_bf16x2(o.x * inv, o.y * inv), pack_bf16x2(o.z * inv, o.w * inv));
-        if (a.lse && lane == 0) a.lse[packed * a.Hq + y.g * R + r % R] = fmaf(M, kLn2, logf(L));
     }
 }
 
 // grid (W x Hkv x pairs of tiles), a cluster of W CTAs when W > 1
 __global__ void __launch_bounds__(kPtThreads, 1)
-    attn_prompt_tile_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmk,
-                            const __grid_constant__ CUtensorMap tmv, const __grid_constant__ CUtensorMap tmo, int W) {
+    attn_prompt_tile_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmo,
+                            const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
+                            const __grid_constant__ CUtensorMap tmkn, const __grid_constant__ CUtensorMap tmvn, int W) {
     using L = PtSmem;
     extern __shared__ uint8_t pt_raw[];
     uint8_t* sm = pt_raw + ((1024u - (tc::smem_u32(pt_raw) & 1023u)) & 1023u);
@@ -282,6 +300,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 
     if (W > 1) tc::cluster_arrive_relaxed();  // waited on before the first remote access: every CTA has started
     bool good = true;                         // warp 0: no wait has run out, and copies may go on
+    bool appended = false;                    // warp 0: the append has been waited for
     // warp 0: a pair's queries, behind those of q pairs before; and its pieces p .. end - 1 of the ring,
     // where `first` is the first of them
     auto copy_q = [&](const PtWork& y, const PtRun& run, int q) {
@@ -297,6 +316,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         __syncwarp();
     };
     auto copy_pieces = [&](const PtWork& y, const PtRun& run, int first, int p, int end) {
+        if (y.before > 0 && !appended) pdl_wait(), appended = true;
         for (; p < end; ++p) {
             const int piece = first + p, at = stage(piece);
             if (piece >= kPtStages) good = good && warp_ok(empty + at, phase(piece - kPtStages));
@@ -306,9 +326,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     tc::mbar_arrive(full + at);
                 } else {
                     tc::mbar_arrive_expect_tx(full + at, kPtTile);
+                    uint8_t* to = sm + L::kRing + at * kPtTile;
+                    const int p0 = (run.cb + (p >> 1)) * kPtPos;
                     for (int h = 0; h < 2; ++h)
-                        tc::tma_load_3d(sm + L::kRing + at * kPtTile + h * kPtPanel, p & 1 ? &tmv : &tmk, 64 * h,
-                                        (run.cb + (p >> 1)) * kPtPos, y.s * a.Hkv + y.g, full + at);
+                        if (y.before > 0)  // from the caches
+                            tc::tma_load_3d(to + h * kPtPanel, p & 1 ? &tmv : &tmk, 64 * h, p0, y.s * a.Hkv + y.g, full + at);
+                        else  // from the rows themselves
+                            tc::tma_load_3d(to + h * kPtPanel, p & 1 ? &tmvn : &tmkn, 64 * h, y.g, y.row0 + p0, full + at);
                 }
             }
             __syncwarp();
@@ -318,7 +342,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 
     if (warp == 0) {
         if (lane == 0) {
-            prefetch_map(&tmq), prefetch_map(&tmk), prefetch_map(&tmv), prefetch_map(&tmo);
+            prefetch_map(&tmq), prefetch_map(&tmo);
+            prefetch_map(&tmk), prefetch_map(&tmv), prefetch_map(&tmkn), prefetch_map(&tmvn);
             for (int i = 0; i < kPtStages; ++i) tc::mbar_init(full + i, 1), tc::mbar_init(empty + i, 1), tc::mbar_init(ready + i, 1);
             tc::mbar_init(qfull, 1), tc::mbar_init(qempty, 1), tc::mbar_init(next, 1), tc::mbar_init(endbar, 1);
             tc::mbar_init(passed, kPtThreads / 32 - 1);
@@ -328,7 +353,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         }
         __syncwarp();
         // (The kernel before this one is this call's append, which has waited for what came before
-        // it: only the caches are its own.)
+        // it: only the caches are its own. They are waited for where they are read, and at the end,
+        // so that whoever waits for this kernel has waited for the append too.)
         const PtWork y = find_pair(a, 2 * per, (int)blockIdx.x / W);
         if (lane == 0) *work(0) = y;
         if (y.s >= 0) {
@@ -374,7 +400,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 __syncwarp();
                 // (first what need not wait for this pair's products, then the next pair, then the rest)
                 const int had = k > 0 ? min(kAhead, run.pieces) : 0, soon = min(kPtStages, run.pieces);
-                if (k == 0) pdl_wait();
                 copy_pieces(y, run, first, had, soon);
                 PtWork z = {-1, 0, 0, 0, 0, 0};
                 if (W == 1) {
@@ -439,7 +464,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 // and the CTA's results are dropped)
                 bool here = true;
                 tile_turns_meet(TileBarriers(), run.nc, run.nc0, run.nc1, [&](int j) {
-                    if (j == 0) here = here && warp_ok(qfull, (uint32_t)before & 1u);
+                    if (j == 0 && run.nc > 0) here = here && warp_ok(qfull, (uint32_t)before & 1u);
                     if (j < run.nc) here = here && warp_ok(ready + stage(first + 2 * j), phase(first + 2 * j));
                     if (j > 0) here = here && warp_ok(ready + stage(first + 2 * j - 1), phase(first + 2 * j - 1));
                 }, [](int, int) {});
@@ -689,6 +714,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         });
         left();
     }
+    if (warp == 0 && !appended) pdl_wait();
     __syncthreads();
     const PtWork y = *work(0);  // W > 1: the only one
     const bool none = y.s < 0;  // ... of the whole cluster
@@ -712,7 +738,13 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     tc::cluster_wait();    // (pairs with the arrival at the start)
     tc::cluster_arrive();  // every CTA's rows are in its shared memory ...
     tc::cluster_wait();
-    merge_rows(a, sm, W, wk, y, run, per);  // ... and each reads the rows that it owns
+    // ... and each reads the rows that it owns
+    if (W == 2)
+        merge_rows<2>(a, sm, wk, y, run, per);
+    else if (W == 4)
+        merge_rows<4>(a, sm, wk, y, run, per);
+    else
+        merge_rows<8>(a, sm, wk, y, run, per);
     tc::cluster_arrive();  // nobody leaves while its memory is read
     tc::cluster_wait();
 }
@@ -786,15 +818,33 @@ cudaError_t launch_attn_prompt_tiles(const PromptArgs& a, cudaStream_t st) {
     cudaError_t e = prompt_setup(&setup);
     if (e != cudaSuccess) return e;
     const int R = a.Hq / a.Hkv, per = kPtRows / R;
-    CUtensorMap tmq, tmk, tmv, tmo;
+    CUtensorMap tmq, tmo, tmk, tmv, tmkn, tmvn;
     const cuuint64_t row = kAttnD * 2;
     e = make_map(a.q, a.Hq, a.rows, row, (cuuint64_t)a.q_stride * 2, R, per, &tmq);
     if (e == cudaSuccess) e = make_map(a.k_cache, a.Tmax, (cuuint64_t)a.S * a.Hkv, row, row * a.Tmax, kPtPos, 1, &tmk);
     if (e == cudaSuccess) e = make_map(a.v_cache, a.Tmax, (cuuint64_t)a.S * a.Hkv, row, row * a.Tmax, kPtPos, 1, &tmv);
+    if (e == cudaSuccess) e = make_map(a.k_new, a.Hkv, a.rows, row, (cuuint64_t)a.kv_stride * 2, 1, kPtPos, &tmkn);
+    if (e == cudaSuccess) e = make_map(a.v_new, a.Hkv, a.rows, row, (cuuint64_t)a.kv_stride * 2, 1, kPtPos, &tmvn);
     if (e == cudaSuccess) e = make_map(a.out, a.Hq, a.rows, row, (cuuint64_t)a.out_stride * 2, R, per, &tmo);
     if (e != cudaSuccess) return e;
     const long pairs = most_tiles(a.S, a.rows, 2 * per) * a.Hkv;
+    // CTAs that share a pair's positions: the least time, in chunks (of 1.4 us), with
+    // 4 for a CTA's start and end and 2 more for the merge. One session's CTAs are all
+    // alike: rounds x a CTA's time. Several sessions are mostly shorter than the caches:
+    // the longest, and where not all CTAs are held at once, what the others take. (Six
+    // sessions adding up to 75 rows behind up to 3001: 41 us with one CTA a pair, 30 with
+    // two, 37 with four; one adding 75 behind 7400: 87, 54, 33 and 45 with eight, of which
+    // the device holds less than the 16 clusters at once; 300 behind 3000: 43, 31, 42, 68;
+    // one of 1500: 37, 66, 102, 224.)
+    const long reach = a.lens || a.rows > a.Tmax ? a.Tmax : a.rows, chunks = (reach + kPtPos - 1) / kPtPos;
     int W = 1;
+    float best = 0.f;
+    for (int k = 0, w = 1; k < 4 && (w == 1 || w <= chunks) && setup->held[k] > 0; ++k, w *= 2) {
+        const float part = (float)pairs / (float)setup->held[k], walk = (float)((chunks + w - 1) / w), ends = w > 1 ? 6.f : 4.f;
+        const float cost = a.S == 1 ? fmaxf(1.f, ceilf(part)) * (walk + ends)
+                                    : walk + ends + (part > 1.f ? (part - 0.7f) * (0.3f * walk + ends) : 0.f);
+        if (w == 1 || cost < best) best = cost, W = w;
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(W * pairs));
     cfg.blockDim = dim3(kPtThreads);
@@ -809,7 +859,7 @@ cudaError_t launch_attn_prompt_tiles(const PromptArgs& a, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = W > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, attn_prompt_tile_kernel, a, tmq, tmk, tmv, tmo, W);
+    return cudaLaunchKernelEx(&cfg, attn_prompt_tile_kernel, a, tmq, tmo, tmk, tmv, tmkn, tmvn, W);
 }
 
 }  // namespace m2
