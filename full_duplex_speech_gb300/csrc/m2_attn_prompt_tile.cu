@@ -796,21 +796,6 @@ cudaError_t prompt_setup(const PtSetup** out) {
     return cudaSuccess;
 }
 
-// bf16 rows of 128 dims as [outer][middle][128], boxes of 64 dims x mid x out.
-cudaError_t make_map(const void* p, cuuint64_t mid, cuuint64_t out, cuuint64_t mid_bytes, cuuint64_t out_bytes, int box_mid,
-                     int box_out, CUtensorMap* map) {
-    tc::EncodeTiledFn enc = tc::encode_tiled();
-    if (!enc) return cudaErrorNotSupported;
-    const cuuint64_t dims[3] = {(cuuint64_t)kAttnD, mid, out};
-    const cuuint64_t strides[2] = {mid_bytes, out_bytes};
-    const cuuint32_t box[3] = {64, (cuuint32_t)box_mid, (cuuint32_t)box_out};
-    const cuuint32_t estr[3] = {1, 1, 1};
-    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr,
-                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
-                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
-    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
-}
-
 }  // namespace
 
 cudaError_t launch_attn_prompt_tiles(const PromptArgs& a, cudaStream_t st) {
@@ -820,12 +805,12 @@ cudaError_t launch_attn_prompt_tiles(const PromptArgs& a, cudaStream_t st) {
     const int R = a.Hq / a.Hkv, per = kPtRows / R;
     CUtensorMap tmq, tmo, tmk, tmv, tmkn, tmvn;
     const cuuint64_t row = kAttnD * 2;
-    e = make_map(a.q, a.Hq, a.rows, row, (cuuint64_t)a.q_stride * 2, R, per, &tmq);
-    if (e == cudaSuccess) e = make_map(a.k_cache, a.Tmax, (cuuint64_t)a.S * a.Hkv, row, row * a.Tmax, kPtPos, 1, &tmk);
-    if (e == cudaSuccess) e = make_map(a.v_cache, a.Tmax, (cuuint64_t)a.S * a.Hkv, row, row * a.Tmax, kPtPos, 1, &tmv);
-    if (e == cudaSuccess) e = make_map(a.k_new, a.Hkv, a.rows, row, (cuuint64_t)a.kv_stride * 2, 1, kPtPos, &tmkn);
-    if (e == cudaSuccess) e = make_map(a.v_new, a.Hkv, a.rows, row, (cuuint64_t)a.kv_stride * 2, 1, kPtPos, &tmvn);
-    if (e == cudaSuccess) e = make_map(a.out, a.Hq, a.rows, row, (cuuint64_t)a.out_stride * 2, R, per, &tmo);
+    e = make_rows_map(a.q, a.Hq, a.rows, row, (cuuint64_t)a.q_stride * 2, R, per, &tmq);
+    if (e == cudaSuccess) e = make_rows_map(a.k_cache, a.Tmax, (cuuint64_t)a.S * a.Hkv, row, row * a.Tmax, kPtPos, 1, &tmk);
+    if (e == cudaSuccess) e = make_rows_map(a.v_cache, a.Tmax, (cuuint64_t)a.S * a.Hkv, row, row * a.Tmax, kPtPos, 1, &tmv);
+    if (e == cudaSuccess) e = make_rows_map(a.k_new, a.Hkv, a.rows, row, (cuuint64_t)a.kv_stride * 2, 1, kPtPos, &tmkn);
+    if (e == cudaSuccess) e = make_rows_map(a.v_new, a.Hkv, a.rows, row, (cuuint64_t)a.kv_stride * 2, 1, kPtPos, &tmvn);
+    if (e == cudaSuccess) e = make_rows_map(a.out, a.Hq, a.rows, row, (cuuint64_t)a.out_stride * 2, R, per, &tmo);
     if (e != cudaSuccess) return e;
     const long pairs = most_tiles(a.S, a.rows, 2 * per) * a.Hkv;
     // CTAs that share a pair's positions: the least time, in chunks (of 1.4 us), with

@@ -132,7 +132,7 @@ cudaError_t launch_fp32(const PromptArgs& a, const PromptSums& w, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_attn_prompt_weights(const PromptArgs& a, const PromptSums& w, cudaStream_t st) {
-    return a.bf16 ? launch_fp32<bf16_t>(a, w, st) : launch_fp32<float>(a, w, st);
+    return a.bf16 ? launch_attn_weights_tiles(a, w, st) : launch_fp32<float>(a, w, st);
 }
 
 }  // namespace m2

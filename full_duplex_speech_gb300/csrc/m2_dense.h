@@ -40,6 +40,8 @@ struct PromptSums {
     float* acc_out;             // ... (may be acc)
 };
 cudaError_t launch_attn_prompt_weights(const PromptArgs& a, const PromptSums& w, cudaStream_t st);
+// ... in bf16 (m2_attn_weights_tile.cu)
+cudaError_t launch_attn_weights_tiles(const PromptArgs& a, const PromptSums& w, cudaStream_t st);
 
 struct EvictArgs {
     int S, Hkv, Tmax, out_max;

@@ -63,6 +63,22 @@ inline long most_tiles(int S, int rows, int per) {
     return n < rows ? n : rows;
 }
 
+// bf16 rows of 128 dims as [outer][middle][128]; a box is 64 dims x box_mid x
+// box_out, 128-byte swizzled.
+inline cudaError_t make_rows_map(const void* p, unsigned long long mid, unsigned long long out, unsigned long long mid_bytes,
+                                 unsigned long long out_bytes, int box_mid, int box_out, CUtensorMap* map) {
+    tc::EncodeTiledFn enc = tc::encode_tiled();
+    if (!enc) return cudaErrorNotSupported;
+    const cuuint64_t dims[3] = {(cuuint64_t)kAttnD, mid, out};
+    const cuuint64_t strides[2] = {mid_bytes, out_bytes};
+    const cuuint32_t box[3] = {64, (cuuint32_t)box_mid, (cuuint32_t)box_out};
+    const cuuint32_t estr[3] = {1, 1, 1};
+    const CUresult r = enc(map, CU_TENSOR_MAP_DATA_TYPE_BFLOAT16, 3, const_cast<void*>(p), dims, strides, box, estr,
+                           CU_TENSOR_MAP_INTERLEAVE_NONE, CU_TENSOR_MAP_SWIZZLE_128B, CU_TENSOR_MAP_L2_PROMOTION_L2_256B,
+                           CU_TENSOR_MAP_FLOAT_OOB_FILL_NONE);
+    return r == CUDA_SUCCESS ? cudaSuccess : cudaErrorInvalidValue;
+}
+
 constexpr float kLn2 = 0.6931471805599453f;
 
 }  // namespace m2
