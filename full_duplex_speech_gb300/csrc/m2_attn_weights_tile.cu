@@ -9,14 +9,16 @@
 //   S^T = K Q^T     kind::f16, M 128 positions x N 256 pairs, so that an operand
 //                   is read from shared memory at 96 bytes a cycle of the 128
 //                   that it gives (two products of N 128 need all of them);
-//   sum += e^(S scale - lse)    one thread a position: a pair's lse is the same
-//                   for all threads (read by broadcast), and the sum over the
-//                   pairs stays in the thread, added up step by step in a fixed
-//                   order.
+//   sum += e^(S scale - lse)    one thread a position and tile of pairs: a pair's
+//                   lse is the same for all threads (read by broadcast), and the
+//                   sum over the pairs stays in the thread, added up step by step
+//                   in a fixed order. The exponent is S (scale log2 e) -
+//                   (lse log2 e), the second product rounded once for all.
 // The products of one tile run under the other's exponentials.
 //
 // Warps: 0 copies keys once and queries through a ring, 1 issues the products, 2
-// fetches the rows' lse, 4-7 and 8-11 the sums of the tiles of positions.
+// fetches the rows' lse, 4-7 and 8-11 the sums of the first tile of positions, over
+// one tile of pairs each, 12-15 and 16-19 those of the second.
 #include <math.h>
 
 #include "m2_dense_dev.cuh"
@@ -26,18 +28,21 @@ namespace m2 {
 
 namespace {
 
-constexpr int kWtThreads = 384;
+constexpr int kWtThreads = 640;
 constexpr int kWtPos = 128;                        // positions a tile
 constexpr uint32_t kWtPanel = 128 * 128;           // 128 rows x 64 dims of bf16
 constexpr uint32_t kWtKeys = 2 * kWtPanel;
 constexpr uint32_t kWtStage = 4 * kWtPanel;        // 256 rows of queries
 constexpr int kWtStages = 2;
+constexpr int kWtRaw = 4;                          // steps whose lse is on its way
 
 struct WtSmem {
     static constexpr uint32_t kK = 0;                                 // [tile][panel] K-major, 128-byte swizzle
     static constexpr uint32_t kQ = kK + 2 * kWtKeys;                  // [stage][panel][256 rows], likewise
-    static constexpr uint32_t kL = kQ + kWtStages * kWtStage;         // float [stage][256]: the pairs' lse
-    static constexpr uint32_t kBar = kL + kWtStages * 256 * 4;
+    static constexpr uint32_t kL = kQ + kWtStages * kWtStage;         // float [stage][256]: the pairs' -lse log2 e
+    static constexpr uint32_t kSum = kL + kWtStages * 256 * 4;        // float [256]: sums over the second tile of pairs
+    static constexpr uint32_t kRaw = kSum + 256 * 4;                  // float [kWtRaw][256]: lse on its way
+    static constexpr uint32_t kBar = kRaw + kWtRaw * 256 * 4;
     // k, qfull[stages], qempty[stages], lfull[stages], lempty[stages], d[2], dempty[2], end
     static constexpr int kBars = 4 * kWtStages + 6;
     static constexpr uint32_t kTmem = kBar + kBars * 8;
@@ -84,9 +89,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         tc::mbar_init(kbar, 1);
         for (int i = 0; i < kWtStages; ++i) {
             tc::mbar_init(qfull + i, 1), tc::mbar_init(qempty + i, 1);
-            tc::mbar_init(lfull + i, 32), tc::mbar_init(lempty + i, 4 * tiles);
+            tc::mbar_init(lfull + i, 1), tc::mbar_init(lempty + i, 8 * tiles);
         }
-        for (int i = 0; i < 2; ++i) tc::mbar_init(dfull + i, 1), tc::mbar_init(dempty + i, 4);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(dfull + i, 1), tc::mbar_init(dempty + i, 8);
         tc::mbar_init(endbar, 1);
         tc::fence_mbar_init();
         *flag = 0;
@@ -95,15 +100,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         tc::tmem_alloc(sTmem, 512);
         tc::tmem_relinquish();
     }
-    // Rows of a tile of pairs that no packed row fills: zeros, and an lse that gives them no weight.
+    // Rows of a tile of pairs that no packed row fills: zeros (and an lse that gives them no weight).
     if (warp >= 4) {
         const int dead = 128 - per * R, each = dead * 8;  // 16-byte pieces of a tile's panel
         for (int i = tid - 128; i < kWtStages * 4 * each; i += kWtThreads - 128) {
             const int panel = i / each, row = per * R + i % each / 8;  // (stage, panel, tile)
             *reinterpret_cast<uint4*>(sm + L::kQ + panel * kWtPanel + row * 128 + i % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
-        for (int i = tid - 128; i < kWtStages * 256; i += kWtThreads - 128)
-            if ((i & 127) >= per * R) sL[i] = INFINITY;
         tc::fence_proxy_async_smem();
     }
     tc::tc_fence_before();
@@ -128,6 +131,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     // tiles of pairs of step j that have rows
     auto filled = [&](int j) { return first + (2 * j + 1) * per < x.n ? 2 : 1; };
 
+    const int mine = (warp - 4) >> 3, half = (warp - 4) >> 2 & 1, p = p0 + 128 * mine + (tid & 127);  // (warps 4 on)
     float sum = 0.f;
     if (warp == 0) {
         // ---------------------------------------------------------------- copies
@@ -177,56 +181,71 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         }
     } else if (warp == 2) {
         // ------------------------------------------------------------- rows' lse
-        for (int j = 0; j < steps; ++j) {
-            if (j >= kWtStages && !warp_ok(lempty + stage(j), phase(j - kWtStages))) break;
+        // (a lane's own copies, kWtRaw steps ahead: loaded step by step they took 550 us of the size below)
+        float* raw = reinterpret_cast<float*>(sm + L::kRaw) + lane;
+        auto fetch = [&](int j) {
             const int t0 = first + 2 * j * per;
 #pragma unroll
             for (int e = 0; e < 8; ++e) {
                 const int c = 32 * e + lane, r = c & 127, t = t0 + (c >> 7) * per + r / R;
-                if (r < per * R && t < x.n)
-                    cp_async4(sL + stage(j) * 256 + c, a.lse + (size_t)(x.row0 + t) * a.Hq + g * R + r % R);
+                if (j < steps && r < per * R && t < x.n)
+                    cp_async4(raw + j % kWtRaw * 256 + 32 * e, a.lse + (size_t)(x.row0 + t) * a.Hq + g * R + r % R);
             }
-            cp_async_arrive(lfull + stage(j));
+            asm volatile("cp.async.commit_group;" ::: "memory");
+        };
+        for (int j = 0; j < kWtRaw - 1; ++j) fetch(j);
+        for (int j = 0; j < steps; ++j) {
+            fetch(j + kWtRaw - 1);
+            asm volatile("cp.async.wait_group %0;" ::"n"(kWtRaw - 1) : "memory");
+            if (j >= kWtStages && !warp_ok(lempty + stage(j), phase(j - kWtStages))) break;
+#pragma unroll
+            for (int e = 0; e < 8; ++e) {  // (a row that the tile does not have gets no weight)
+                const int c = 32 * e + lane;
+                sL[stage(j) * 256 + c] = (c & 127) < per * R ? -raw[j % kWtRaw * 256 + 32 * e] * kLog2e : -INFINITY;
+            }
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(lfull + stage(j));
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp >= 4 && (warp - 4) >> 2 < tiles) {
-        // ------------------------------------------ sums, one position a thread
-        const int i = (warp - 4) >> 2, p = p0 + tid - 128;
-        const uint32_t tD = tm + ((uint32_t)((warp & 3) * 32) << 16) + 256 * i;
-        const float2 scale = make_float2(a.scale, a.scale), log2e = make_float2(kLog2e, kLog2e);
+    } else if (warp >= 4 && (warp - 4) >> 3 < tiles) {
+        // ------------------ sums, one position and tile of pairs a thread
+        const uint32_t tD = tm + ((uint32_t)((warp & 3) * 32) << 16) + 256 * mine + 128 * half;
+        const float sl2 = a.scale * kLog2e;
+        const float2 c2 = make_float2(sl2, sl2);
         for (int j = 0; j < steps; ++j) {
-            if (!warp_ok(lfull + stage(j), phase(j)) || !warp_ok(dfull + i, (uint32_t)j & 1u)) break;
+            if (!warp_ok(lfull + stage(j), phase(j)) || !warp_ok(dfull + mine, (uint32_t)j & 1u)) break;
             tc::tc_fence_after();
-            const float* lse = sL + stage(j) * 256;
-            const int n = filled(j);
             float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-            for (int h = 0; h < n; ++h) {
+            if (half < filled(j)) {
+                const float* nl = sL + stage(j) * 256 + 128 * half;
                 // pairs lo .. hi - 1 of the tile see the position
-                const int t = first + (2 * j + h) * per, lo = (p - x.before - t) * R, hi = min(x.n - t, per) * R;
+                const int t = first + (2 * j + half) * per, lo = (p - x.before - t) * R, hi = min(x.n - t, per) * R;
                 const bool part = __any_sync(0xffffffffu, lo > 0) || hi < per * R;
+                // (two loops: with the question inside it, it is answered for every pair, at twice the instructions)
+                if (part) {
+#pragma unroll 1
+                    for (int q = 0; q < 8; ++q) {
+                        float v[16];
+                        tc::tmem_ld16(tD + 16 * q, v);
+                        tc::tmem_wait_ld();
 #pragma unroll
-                for (int q = 0; q < 4; ++q) {
-                    float v[32];
-                    tmem_ld32(tD + 128 * h + 32 * q, v);
-                    tc::tmem_wait_ld();
-                    if (part) {
-#pragma unroll
-                        for (int e = 0; e < 32; ++e) {
-                            const int c = 32 * q + e;
-                            v[e] = c >= lo && c < hi ? fmaf(v[e], a.scale, -lse[128 * h + c]) * kLog2e : -INFINITY;
+                        for (int e = 0; e < 16; ++e) {
+                            const int c = 16 * q + e;
+                            const float z = fmaf(v[e], sl2, nl[c]);
+                            s0.x += ex2_approx(c >= lo && c < hi ? z : -INFINITY);
                         }
+                    }
+                } else {
+#pragma unroll
+                    for (int q = 0; q < 4; ++q) {
+                        float v[32];
+                        tmem_ld32(tD + 32 * q, v);
+                        tc::tmem_wait_ld();
 #pragma unroll
                         for (int e = 0; e < 32; e += 4) {
-                            s0 = add2(s0, make_float2(ex2_approx(v[e]), ex2_approx(v[e + 1])));
-                            s1 = add2(s1, make_float2(ex2_approx(v[e + 2]), ex2_approx(v[e + 3])));
-                        }
-                    } else {
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 l4 = *reinterpret_cast<const float4*>(lse + 128 * h + 32 * q + e);
-                            float2 x0 = fma2(make_float2(v[e], v[e + 1]), scale, make_float2(-l4.x, -l4.y));
-                            float2 x1 = fma2(make_float2(v[e + 2], v[e + 3]), scale, make_float2(-l4.z, -l4.w));
-                            x0 = mul2(x0, log2e), x1 = mul2(x1, log2e);
+                            const float4 l4 = *reinterpret_cast<const float4*>(nl + 32 * q + e);
+                            const float2 x0 = fma2(make_float2(v[e], v[e + 1]), c2, make_float2(l4.x, l4.y));
+                            const float2 x1 = fma2(make_float2(v[e + 2], v[e + 3]), c2, make_float2(l4.z, l4.w));
                             s0 = add2(s0, make_float2(ex2_approx(x0.x), ex2_approx(x0.y)));
                             s1 = add2(s1, make_float2(ex2_approx(x1.x), ex2_approx(x1.y)));
                         }
@@ -235,10 +254,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             }
             tc::tc_fence_before();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(dempty + i), tc::mbar_arrive(lempty + stage(j));
+            if (lane == 0) tc::mbar_arrive(dempty + mine), tc::mbar_arrive(lempty + stage(j));
             sum += (s0.x + s0.y) + (s1.x + s1.y);  // (a step's terms first, then the steps: no long chain of roundings)
         }
-        if (p < total) w.acc_out[head + p] = (p < x.before ? w.acc[head + p] : 0.f) + sum;
+        if (half == 1) reinterpret_cast<float*>(sm + L::kSum)[128 * mine + (tid & 127)] = sum;
     }
     __syncwarp();
     tc::tc_fence_before();
@@ -257,6 +276,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         __syncthreads();
     }
     if (warp == 1) tc::tmem_dealloc(tm, 512);
+    if (warp >= 4 && mine < tiles && half == 0 && p < total)
+        w.acc_out[head + p] = (p < x.before ? w.acc[head + p] : 0.f) + (sum + reinterpret_cast<const float*>(sm + L::kSum)[128 * mine + (tid & 127)]);
 }
 
 }  // namespace
