@@ -9,16 +9,18 @@
 //   S^T = K Q^T     kind::f16, M 128 positions x N 256 pairs, so that an operand
 //                   is read from shared memory at 96 bytes a cycle of the 128
 //                   that it gives (two products of N 128 need all of them);
-//   sum += e^(S scale - lse)    one thread a position and tile of pairs: a pair's
-//                   lse is the same for all threads (read by broadcast), and the
-//                   sum over the pairs stays in the thread, added up step by step
-//                   in a fixed order. The exponent is S (scale log2 e) -
+//   sum += e^(S scale - lse)    one thread a position: a pair's lse is the same for
+//                   all threads (read by broadcast), and the sum over the pairs
+//                   stays in the thread, added up step by step in a fixed order.
+//                   The exponent is S (scale log2 e) -
 //                   (lse log2 e), the second product rounded once for all.
 // The products of one tile run under the other's exponentials.
 //
 // Warps: 0 copies keys once and queries through a ring, 1 issues the products, 2
-// fetches the rows' lse, 4-7 and 8-11 the sums of the first tile of positions, over
-// one tile of pairs each, 12-15 and 16-19 those of the second.
+// fetches the rows' lse, 4-7 and 8-11 the sums of the tiles of positions: 32 pairs
+// at a time, while the next 32 products and lse are on their way. (Shared memory
+// answers late beside the products' own reads of it: four warps more a tile that
+// waited for each other's 32 took 313 us where this takes XXX.)
 #include <math.h>
 
 #include "m2_dense_dev.cuh"
@@ -28,7 +30,7 @@ namespace m2 {
 
 namespace {
 
-constexpr int kWtThreads = 640;
+constexpr int kWtThreads = 384;
 constexpr int kWtPos = 128;                        // positions a tile
 constexpr uint32_t kWtPanel = 128 * 128;           // 128 rows x 64 dims of bf16
 constexpr uint32_t kWtKeys = 2 * kWtPanel;
@@ -40,8 +42,7 @@ struct WtSmem {
     static constexpr uint32_t kK = 0;                                 // [tile][panel] K-major, 128-byte swizzle
     static constexpr uint32_t kQ = kK + 2 * kWtKeys;                  // [stage][panel][256 rows], likewise
     static constexpr uint32_t kL = kQ + kWtStages * kWtStage;         // float [stage][256]: the pairs' -lse log2 e
-    static constexpr uint32_t kSum = kL + kWtStages * 256 * 4;        // float [256]: sums over the second tile of pairs
-    static constexpr uint32_t kRaw = kSum + 256 * 4;                  // float [kWtRaw][256]: lse on its way
+    static constexpr uint32_t kRaw = kL + kWtStages * 256 * 4;                // float [kWtRaw][256]: lse on its way
     static constexpr uint32_t kBar = kRaw + kWtRaw * 256 * 4;
     // k, qfull[stages], qempty[stages], lfull[stages], lempty[stages], d[2], dempty[2], end
     static constexpr int kBars = 4 * kWtStages + 6;
@@ -89,9 +90,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         tc::mbar_init(kbar, 1);
         for (int i = 0; i < kWtStages; ++i) {
             tc::mbar_init(qfull + i, 1), tc::mbar_init(qempty + i, 1);
-            tc::mbar_init(lfull + i, 1), tc::mbar_init(lempty + i, 8 * tiles);
+            tc::mbar_init(lfull + i, 1), tc::mbar_init(lempty + i, 4 * tiles);
         }
-        for (int i = 0; i < 2; ++i) tc::mbar_init(dfull + i, 1), tc::mbar_init(dempty + i, 8);
+        for (int i = 0; i < 2; ++i) tc::mbar_init(dfull + i, 1), tc::mbar_init(dempty + i, 4);
         tc::mbar_init(endbar, 1);
         tc::fence_mbar_init();
         *flag = 0;
@@ -131,7 +132,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     // tiles of pairs of step j that have rows
     auto filled = [&](int j) { return first + (2 * j + 1) * per < x.n ? 2 : 1; };
 
-    const int mine = (warp - 4) >> 3, half = (warp - 4) >> 2 & 1, p = p0 + 128 * mine + (tid & 127);  // (warps 4 on)
     float sum = 0.f;
     if (warp == 0) {
         // ---------------------------------------------------------------- copies
@@ -207,57 +207,64 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             if (lane == 0) tc::mbar_arrive(lfull + stage(j));
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp >= 4 && (warp - 4) >> 3 < tiles) {
-        // ------------------ sums, one position and tile of pairs a thread
-        const uint32_t tD = tm + ((uint32_t)((warp & 3) * 32) << 16) + 256 * mine + 128 * half;
+    } else if (warp >= 4 && (warp - 4) >> 2 < tiles) {
+        // ------------------------------------------ sums, one position a thread
+        const int i = (warp - 4) >> 2, p = p0 + tid - 128;
+        const uint32_t tD = tm + ((uint32_t)((warp & 3) * 32) << 16) + 256 * i;
         const float sl2 = a.scale * kLog2e;
         const float2 c2 = make_float2(sl2, sl2);
         for (int j = 0; j < steps; ++j) {
-            if (!warp_ok(lfull + stage(j), phase(j)) || !warp_ok(dfull + mine, (uint32_t)j & 1u)) break;
-            tc::tc_fence_after();
+            if (!warp_ok(lfull + stage(j), phase(j))) break;
+            const float* nl = sL + stage(j) * 256;
+            // pairs lo .. hi - 1 of the step's (of a tile, with those of the other behind them) see the position
+            const int t = first + 2 * j * per;
+            const bool part = __any_sync(0xffffffffu, p - x.before > t) || x.n < t + 2 * per;
             float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-            if (half < filled(j)) {
-                const float* nl = sL + stage(j) * 256 + 128 * half;
-                // pairs lo .. hi - 1 of the tile see the position
-                const int t = first + (2 * j + half) * per, lo = (p - x.before - t) * R, hi = min(x.n - t, per) * R;
-                const bool part = __any_sync(0xffffffffu, lo > 0) || hi < per * R;
-                // (two loops: with the question inside it, it is answered for every pair, at twice the instructions)
-                if (part) {
-#pragma unroll 1
-                    for (int q = 0; q < 8; ++q) {
-                        float v[16];
-                        tc::tmem_ld16(tD + 16 * q, v);
-                        tc::tmem_wait_ld();
+            // the step's sum; kPart: some pairs do not see the position (in code of its own: with the
+            // question asked for every pair, the others took twice the instructions)
+            auto add_step = [&](auto kPart) -> bool {
+                float v[2][32];
+                float4 l4[2][8];
 #pragma unroll
-                        for (int e = 0; e < 16; ++e) {
-                            const int c = 16 * q + e;
-                            const float z = fmaf(v[e], sl2, nl[c]);
-                            s0.x += ex2_approx(c >= lo && c < hi ? z : -INFINITY);
-                        }
+                for (int e = 0; e < 8; ++e) l4[0][e] = reinterpret_cast<const float4*>(nl)[e];
+                if (!warp_ok(dfull + i, (uint32_t)j & 1u)) return false;
+                tc::tc_fence_after();
+                tmem_ld32(tD, v[0]);
+#pragma unroll
+                for (int q = 0; q < 8; ++q) {
+                    const int at = q & 1, to = at ^ 1;
+                    tc::tmem_wait_ld();
+                    if (q < 7) {
+                        tmem_ld32(tD + 32 * (q + 1), v[to]);
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) l4[to][e] = reinterpret_cast<const float4*>(nl + 32 * (q + 1))[e];
+                    } else {
+                        tc::tc_fence_before();
+                        __syncwarp();
+                        if (lane == 0) tc::mbar_arrive(dempty + i), tc::mbar_arrive(lempty + stage(j));
                     }
-                } else {
+                    const int tq = t + (q >> 2) * per, lo = (p - x.before - tq) * R - 32 * (q & 3),
+                              hi = min(x.n - tq, per) * R - 32 * (q & 3);
 #pragma unroll
-                    for (int q = 0; q < 4; ++q) {
-                        float v[32];
-                        tmem_ld32(tD + 32 * q, v);
-                        tc::tmem_wait_ld();
-#pragma unroll
-                        for (int e = 0; e < 32; e += 4) {
-                            const float4 l4 = *reinterpret_cast<const float4*>(nl + 32 * q + e);
-                            const float2 x0 = fma2(make_float2(v[e], v[e + 1]), c2, make_float2(l4.x, l4.y));
-                            const float2 x1 = fma2(make_float2(v[e + 2], v[e + 3]), c2, make_float2(l4.z, l4.w));
-                            s0 = add2(s0, make_float2(ex2_approx(x0.x), ex2_approx(x0.y)));
-                            s1 = add2(s1, make_float2(ex2_approx(x1.x), ex2_approx(x1.y)));
+                    for (int e = 0; e < 8; ++e) {
+                        const float4 l = l4[at][e];
+                        float2 x0 = fma2(make_float2(v[at][4 * e], v[at][4 * e + 1]), c2, make_float2(l.x, l.y));
+                        float2 x1 = fma2(make_float2(v[at][4 * e + 2], v[at][4 * e + 3]), c2, make_float2(l.z, l.w));
+                        if constexpr (decltype(kPart)::value) {
+                            const int c = 4 * e;
+                            x0.x = c >= lo && c < hi ? x0.x : -INFINITY, x0.y = c + 1 >= lo && c + 1 < hi ? x0.y : -INFINITY;
+                            x1.x = c + 2 >= lo && c + 2 < hi ? x1.x : -INFINITY, x1.y = c + 3 >= lo && c + 3 < hi ? x1.y : -INFINITY;
                         }
+                        s0 = add2(s0, make_float2(ex2_approx(x0.x), ex2_approx(x0.y)));
+                        s1 = add2(s1, make_float2(ex2_approx(x1.x), ex2_approx(x1.y)));
                     }
                 }
-            }
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(dempty + mine), tc::mbar_arrive(lempty + stage(j));
+                return true;
+            };
+            if (!(part ? add_step(std::true_type()) : add_step(std::false_type()))) break;
             sum += (s0.x + s0.y) + (s1.x + s1.y);  // (a step's terms first, then the steps: no long chain of roundings)
         }
-        if (half == 1) reinterpret_cast<float*>(sm + L::kSum)[128 * mine + (tid & 127)] = sum;
+        if (p < total) w.acc_out[head + p] = (p < x.before ? w.acc[head + p] : 0.f) + sum;
     }
     __syncwarp();
     tc::tc_fence_before();
@@ -276,8 +283,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         __syncthreads();
     }
     if (warp == 1) tc::tmem_dealloc(tm, 512);
-    if (warp >= 4 && mine < tiles && half == 0 && p < total)
-        w.acc_out[head + p] = (p < x.before ? w.acc[head + p] : 0.f) + (sum + reinterpret_cast<const float*>(sm + L::kSum)[128 * mine + (tid & 127)]);
 }
 
 }  // namespace
