@@ -132,7 +132,10 @@ cudaError_t launch_fp32(const PromptArgs& a, const PromptSums& w, cudaStream_t s
 }  // namespace
 
 cudaError_t launch_attn_prompt_weights(const PromptArgs& a, const PromptSums& w, cudaStream_t st) {
-    return a.bf16 ? launch_attn_weights_tiles(a, w, st) : launch_fp32<float>(a, w, st);
+    if (!a.bf16) return launch_fp32<float>(a, w, st);
+    // (the tiles divide by the scale: lse / scale stays a normal number for every lse in earnest)
+    const float size = fabsf(a.scale);
+    return size >= 0x1p-40f && size <= 0x1p40f ? launch_attn_weights_tiles(a, w, st) : launch_fp32<bf16_t>(a, w, st);
 }
 
 }  // namespace m2

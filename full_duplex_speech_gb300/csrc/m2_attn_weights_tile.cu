@@ -5,22 +5,26 @@
 // One CTA takes 256 positions of one (session, kv head), two tiles of 128, and
 // walks the window's rows that see any of them, up to 256 (row, head) pairs at a
 // time: two tiles of floor(128 / R) packed rows, each a box of a tensor map. Per
-// step and tile of positions:
-//   S^T = K Q^T     kind::f16, M 128 positions x N 256 pairs, so that an operand
-//                   is read from shared memory at 96 bytes a cycle of the 128
-//                   that it gives (two products of N 128 need all of them);
-//   sum += e^(S scale - lse)    one thread a position: a pair's lse is the same for
-//                   all threads (read by broadcast), and the sum over the pairs
-//                   stays in the thread, added up step by step in a fixed order.
-//                   The exponent is S (scale log2 e) -
-//                   (lse log2 e), the second product rounded once for all.
-// The products of one tile run under the other's exponentials.
+// step, tile of positions and tile of pairs:
+//   S^T = [K 1] [Q e]^T    kind::f16, M 128 positions x N 128 pairs, K from tensor
+//                   memory, where it stays (from shared memory, read anew with
+//                   every product, a product took 1,000 cycles for its 580, and the
+//                   whole 361 us where this takes XXX); 16 more of the products'
+//                   inner dim bring a pair's e = -lse / scale, as three bf16 terms
+//                   (24 bits) times ones, so that
+//   sum += 2^(S^T scale log2 e)    needs nothing but S^T: one thread a position, whose
+//                   sum over the pairs stays in it, added up step by step in a fixed
+//                   order. (With the lse read from shared memory, the same for
+//                   all threads, its 512 bytes a warp and read cost as much of
+//                   shared memory's time as the products: 314 us where this takes XXX.)
+// The products go to three buffers of tensor memory in turn; two are added up while
+// the third is filled.
 //
-// Warps: 0 copies keys once and queries through a ring, 1 issues the products, 2
-// fetches the rows' lse, 4-7 and 8-11 the sums of the tiles of positions: 32 pairs
-// at a time, while the next 32 products and lse are on their way. (Shared memory
-// answers late beside the products' own reads of it: four warps more a tile that
-// waited for each other's 32 took 313 us where this takes XXX.)
+// Warps: 0 copies queries through a ring, 1 issues the products, 2 and 3 make the
+// pairs' e, 4-7 and 8-11 the sums of the tiles of positions, whose keys they bring;
+// 12 waits for what the next products need while these are issued (an issue lasts as
+// long as the products, and a look at a barrier in shared memory some 200 cycles
+// more: 331 us where this takes XXX).
 #include <math.h>
 
 #include "m2_dense_dev.cuh"
@@ -30,39 +34,43 @@ namespace m2 {
 
 namespace {
 
-constexpr int kWtThreads = 384;
+constexpr int kWtThreads = 416;
 constexpr int kWtPos = 128;                        // positions a tile
 constexpr uint32_t kWtPanel = 128 * 128;           // 128 rows x 64 dims of bf16
-constexpr uint32_t kWtKeys = 2 * kWtPanel;
 constexpr uint32_t kWtStage = 4 * kWtPanel;        // 256 rows of queries
-constexpr int kWtStages = 2;
+constexpr int kWtStages = 3;
+constexpr int kWtBuffers = 3;                      // of 128 columns of tensor memory
+constexpr uint32_t kWtColK = 128 * kWtBuffers;     // behind them the keys, 64 columns a tile
 constexpr int kWtRaw = 4;                          // steps whose lse is on its way
 
+constexpr uint32_t kWtExtra = 128 * 32;            // 128 rows x 16 of bf16, 8 x 8 blocks: rows by 128 bytes, the second 8 2 KB on
 struct WtSmem {
-    static constexpr uint32_t kK = 0;                                 // [tile][panel] K-major, 128-byte swizzle
-    static constexpr uint32_t kQ = kK + 2 * kWtKeys;                  // [stage][panel][256 rows], likewise
-    static constexpr uint32_t kL = kQ + kWtStages * kWtStage;         // float [stage][256]: the pairs' -lse log2 e
-    static constexpr uint32_t kRaw = kL + kWtStages * 256 * 4;                // float [kWtRaw][256]: lse on its way
+    static constexpr uint32_t kQ = 0;                                 // [stage][panel][256 rows] K-major, 128-byte swizzle
+    static constexpr uint32_t kE = kQ + kWtStages * kWtStage;         // [stage][tile of pairs]: e, K-major, no swizzle
+    static constexpr uint32_t kOne = kE + kWtStages * 2 * kWtExtra;   // the ones they are multiplied by, likewise
+    static constexpr uint32_t kRaw = kOne + kWtExtra;                 // float [kWtRaw][256]: lse on its way
     static constexpr uint32_t kBar = kRaw + kWtRaw * 256 * 4;
-    // k, qfull[stages], qempty[stages], lfull[stages], lempty[stages], d[2], dempty[2], end
-    static constexpr int kBars = 4 * kWtStages + 6;
+    // k, qfull[stages], qempty[stages], efull[stages], d[buffers], dempty[buffers], end
+    static constexpr int kBars = 3 * kWtStages + 2 * kWtBuffers + 2;
     static constexpr uint32_t kTmem = kBar + kBars * 8;
     static constexpr uint32_t kFlag = kTmem + 4;
     static constexpr uint32_t kBytes = kFlag + 4 + 1024;              // + slack to align to 1024
     static_assert(kBytes <= 227 * 1024, "one CTA an SM");
 };
 
+// The warp that issues the products and the one that waits for their operands, once
+// a product.
+__device__ __forceinline__ void products_meet() { asm volatile("barrier.sync 1, 64;" ::: "memory"); }
+
 // grid: (position tiles of 256) x Hkv x S, the first tiles, which most rows see, first
 __global__ void __launch_bounds__(kWtThreads, 1)
-    attn_weights_tile_kernel(PromptArgs a, PromptSums w, const __grid_constant__ CUtensorMap tmq,
-                             const __grid_constant__ CUtensorMap tmk) {
+    attn_weights_tile_kernel(PromptArgs a, PromptSums w, const __grid_constant__ CUtensorMap tmq) {
     using L = WtSmem;
     extern __shared__ uint8_t wt_raw[];
     uint8_t* sm = wt_raw + ((1024u - (tc::smem_u32(wt_raw) & 1023u)) & 1023u);
-    float* sL = reinterpret_cast<float*>(sm + L::kL);
     uint64_t* kbar = reinterpret_cast<uint64_t*>(sm + L::kBar);
-    uint64_t *qfull = kbar + 1, *qempty = qfull + kWtStages, *lfull = qempty + kWtStages, *lempty = lfull + kWtStages,
-             *dfull = lempty + kWtStages, *dempty = dfull + 2, *endbar = dempty + 2;
+    uint64_t *qfull = kbar + 1, *qempty = qfull + kWtStages, *efull = qempty + kWtStages,
+             *dfull = efull + kWtStages, *dempty = dfull + kWtBuffers, *endbar = dempty + kWtBuffers;
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + L::kTmem);
     volatile uint32_t* flag = reinterpret_cast<uint32_t*>(sm + L::kFlag);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
@@ -70,7 +78,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const int heads = a.Hkv * a.S, p0 = (int)(blockIdx.x / heads) * 2 * kWtPos;
     const int g = blockIdx.x % heads % a.Hkv, s = blockIdx.x % heads / a.Hkv;
 
-    if (tid == 0) prefetch_map(&tmq), prefetch_map(&tmk);
+    if (tid == 0) prefetch_map(&tmq);
     pdl_wait();
     Session x;
     const bool rows_ok = session_of(a, s, &x);
@@ -87,12 +95,11 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const size_t head = ((size_t)s * a.Hkv + g) * a.Tmax;
 
     if (tid == 0) {
-        tc::mbar_init(kbar, 1);
+        tc::mbar_init(kbar, 4 * tiles);
         for (int i = 0; i < kWtStages; ++i) {
-            tc::mbar_init(qfull + i, 1), tc::mbar_init(qempty + i, 1);
-            tc::mbar_init(lfull + i, 1), tc::mbar_init(lempty + i, 4 * tiles);
+            tc::mbar_init(qfull + i, 1), tc::mbar_init(qempty + i, 1), tc::mbar_init(efull + i, 2);
         }
-        for (int i = 0; i < 2; ++i) tc::mbar_init(dfull + i, 1), tc::mbar_init(dempty + i, 4);
+        for (int i = 0; i < kWtBuffers; ++i) tc::mbar_init(dfull + i, 1), tc::mbar_init(dempty + i, 4);
         tc::mbar_init(endbar, 1);
         tc::fence_mbar_init();
         *flag = 0;
@@ -101,8 +108,13 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         tc::tmem_alloc(sTmem, 512);
         tc::tmem_relinquish();
     }
-    // Rows of a tile of pairs that no packed row fills: zeros (and an lse that gives them no weight).
+    // Rows of a tile of pairs that no packed row fills: zeros (and an e of -infinity). The ones: three
+    // of 16; what e's last 13 are is zeros.
     if (warp >= 4) {
+        for (int i = tid - 128; i < (int)((2 * kWtStages + 1) * kWtExtra / 16); i += kWtThreads - 128) {
+            const bool ones = i >= (int)(2 * kWtStages * kWtExtra / 16) && i % (int)(kWtExtra / 16) < 128;
+            *reinterpret_cast<uint4*>(sm + L::kE + i * 16) = ones ? make_uint4(0x3F803F80u, 0x3F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
+        }
         const int dead = 128 - per * R, each = dead * 8;  // 16-byte pieces of a tile's panel
         for (int i = tid - 128; i < kWtStages * 4 * each; i += kWtThreads - 128) {
             const int panel = i / each, row = per * R + i % each / 8;  // (stage, panel, tile)
@@ -135,13 +147,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     float sum = 0.f;
     if (warp == 0) {
         // ---------------------------------------------------------------- copies
-        if (steps > 0 && tc::elect_one()) {
-            tc::mbar_arrive_expect_tx(kbar, (uint32_t)tiles * kWtKeys);
-            for (int i = 0; i < tiles; ++i)
-                for (int h = 0; h < 2; ++h)
-                    tc::tma_load_3d(sm + L::kK + i * kWtKeys + h * kWtPanel, &tmk, 64 * h, p0 + i * kWtPos, s * a.Hkv + g, kbar);
-        }
-        __syncwarp();
         for (int j = 0; j < steps; ++j) {
             if (j >= kWtStages && !warp_ok(qempty + stage(j), phase(j - kWtStages))) break;
             if (tc::elect_one()) {
@@ -158,109 +163,159 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         // -------------------------------------------------------------- products
         const bool leader = tc::elect_one();
         const uint32_t sbase = tc::smem_u32(sm);
-        bool good = steps > 0 && warp_ok(kbar, 0);
-        for (int j = 0; good && j < steps; ++j) {
-            good = warp_ok(qfull + stage(j), phase(j));
-            for (int i = 0; good && i < tiles; ++i) {
-                if (j > 0) good = warp_ok(dempty + i, (uint32_t)(j - 1) & 1u);
-                if (!good) break;
+        for (int j = 0, m = 0; j < steps; ++j) {  // m: products so far
+            const int n = filled(j);
+            for (int d = 0; d < n * tiles; ++d, ++m) {
+                const int i = tiles == 2 ? d & 1 : 0, h = tiles == 2 ? d >> 1 : d, b = m % kWtBuffers;
+                products_meet();
                 tc::tc_fence_after();
                 if (leader) {
-                    const uint64_t ad = tc::sdesc(sbase + L::kK + i * kWtKeys, 0, 1024, 2);
-                    const uint64_t bd = tc::sdesc(sbase + L::kQ + stage(j) * kWtStage, 0, 1024, 2);
-                    const uint32_t id = filled(j) == 2 ? tc::idesc_bf16(128, 256, 0, 0) : tc::idesc_bf16(128, 128, 0, 0);
+                    const uint64_t bd = tc::sdesc(sbase + L::kQ + stage(j) * kWtStage + h * kWtPanel, 0, 1024, 2);
+                    const uint32_t to = tm + 128 * b, id = tc::idesc_bf16(128, 128, 0, 0);
+                    tc::mma_bf16(to, tc::sdesc(sbase + L::kOne, kWtExtra / 2, 128, 0),
+                                 tc::sdesc(sbase + L::kE + (2 * stage(j) + h) * kWtExtra, kWtExtra / 2, 128, 0), id, 0u);
 #pragma unroll
                     for (int q = 0; q < 8; ++q)
-                        tc::mma_bf16(tm + 256 * i, ad + (uint64_t)(((q >> 2) * kWtPanel + (q & 3) * 32) >> 4),
-                                     bd + (uint64_t)(((q >> 2) * 2 * kWtPanel + (q & 3) * 32) >> 4), id, q > 0 ? 1u : 0u);
-                    tc::mma_commit(dfull + i);
-                    if (i == tiles - 1) tc::mma_commit(qempty + stage(j));
+                        tc::mma_bf16_tmem_a(to, tm + kWtColK + 64 * i + 8 * q,
+                                            bd + (uint64_t)(((q >> 2) * 2 * kWtPanel + (q & 3) * 32) >> 4), id, 1u);
+                    tc::mma_commit(dfull + b);
+                    if (d == n * tiles - 1) tc::mma_commit(qempty + stage(j));
                 }
                 __syncwarp();
             }
         }
-    } else if (warp == 2) {
-        // ------------------------------------------------------------- rows' lse
-        // (a lane's own copies, kWtRaw steps ahead: loaded step by step they took 550 us of the size below)
-        float* raw = reinterpret_cast<float*>(sm + L::kRaw) + lane;
-        auto fetch = [&](int j) {
-            const int t0 = first + 2 * j * per;
+    } else if (warp == 12) {
+        // -------------------------------------- waits on behalf of the products
+        // (after one that gave up, what the products read is there, if not what it should be, and the
+        // error is recorded; every meeting takes place)
+        bool good = steps > 0 && warp_ok(kbar, 0);
+        for (int j = 0, m = 0; j < steps; ++j) {
+            good = good && warp_ok(qfull + stage(j), phase(j)) && warp_ok(efull + stage(j), phase(j));
+            const int n = filled(j);
+            for (int d = 0; d < n * tiles; ++d, ++m) {
+                if (m >= kWtBuffers) good = good && warp_ok(dempty + m % kWtBuffers, (uint32_t)(m / kWtBuffers - 1) & 1u);
+                tc::tc_fence_before();
+                products_meet();
+            }
+        }
+    } else if (warp < 4) {
+        // ------------------------------------- the pairs' e, a tile of pairs a warp
+        // (a lane's own copies of lse, kWtRaw steps ahead: loaded step by step they took 550 us of the
+        // size below, and with one warp, which has a step's time for 256 of them, 357)
+        const int h = warp - 2;
+        float* raw = reinterpret_cast<float*>(sm + L::kRaw) + 128 * h + lane;
+        const float* from[4];  // a lane's pairs 32 e + lane, step by step
+        int t[4];
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {
-                const int c = 32 * e + lane, r = c & 127, t = t0 + (c >> 7) * per + r / R;
-                if (j < steps && r < per * R && t < x.n)
-                    cp_async4(raw + j % kWtRaw * 256 + 32 * e, a.lse + (size_t)(x.row0 + t) * a.Hq + g * R + r % R);
+        for (int e = 0; e < 4; ++e) {
+            const int r = 32 * e + lane;
+            t[e] = r < per * R ? first + h * per + r / R : x.n;  // (a row that the tile does not have: never)
+            from[e] = a.lse + (size_t)(x.row0 + first + h * per + r / R) * a.Hq + g * R + r % R;
+        }
+        auto fetch = [&](int j) {
+#pragma unroll
+            for (int e = 0; e < 4; ++e) {
+                if (t[e] < x.n) cp_async4(raw + j % kWtRaw * 256 + 32 * e, from[e]);
+                t[e] += 2 * per, from[e] += (size_t)2 * per * a.Hq;
             }
             asm volatile("cp.async.commit_group;" ::: "memory");
         };
+        const float by = -1.f / a.scale, none = a.scale > 0.f ? -INFINITY : INFINITY;
         for (int j = 0; j < kWtRaw - 1; ++j) fetch(j);
         for (int j = 0; j < steps; ++j) {
             fetch(j + kWtRaw - 1);
             asm volatile("cp.async.wait_group %0;" ::"n"(kWtRaw - 1) : "memory");
-            if (j >= kWtStages && !warp_ok(lempty + stage(j), phase(j - kWtStages))) break;
+            if (j >= kWtStages && !warp_ok(qempty + stage(j), phase(j - kWtStages))) break;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) {  // (a row that the tile does not have gets no weight)
-                const int c = 32 * e + lane;
-                sL[stage(j) * 256 + c] = (c & 127) < per * R ? -raw[j % kWtRaw * 256 + 32 * e] * kLog2e : -INFINITY;
+            for (int e = 0; e < 4; ++e) {
+                const int r = 32 * e + lane;
+                const float z = r < per * R ? raw[j % kWtRaw * 256 + 32 * e] * by : none;  // (no weight)
+                // hi + mid + lo, each what the ones before it leave, rounded; of an infinity hi alone
+                const uint32_t hi = float_to_bf16_bits(z);
+                const float top = bf16_bits_to_float(hi), rest = fabsf(top) < INFINITY ? z - top : 0.f;
+                const uint32_t mid = float_to_bf16_bits(rest), lo = float_to_bf16_bits(rest - bf16_bits_to_float(mid));
+                *reinterpret_cast<uint2*>(sm + L::kE + (2 * stage(j) + h) * kWtExtra + (r >> 3) * 128 + (r & 7) * 16) =
+                    make_uint2(hi | mid << 16, lo);
             }
+            tc::fence_proxy_async_smem();
             __syncwarp();
-            if (lane == 0) tc::mbar_arrive(lfull + stage(j));
+            if (lane == 0) tc::mbar_arrive(efull + stage(j));
         }
         asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp >= 4 && (warp - 4) >> 2 < tiles) {
+    } else if (warp < 12 && (warp - 4) >> 2 < tiles) {
         // ------------------------------------------ sums, one position a thread
         const int i = (warp - 4) >> 2, p = p0 + tid - 128;
-        const uint32_t tD = tm + ((uint32_t)((warp & 3) * 32) << 16) + 256 * i;
+        const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
+        if (steps > 0) {  // its key, two dims a column
+            const uint4* key = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k_cache) + (head + p) * kAttnD);
+#pragma unroll
+            for (int q = 0; q < 4; ++q) {
+                uint32_t v[16];
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const uint4 u = p < total ? key[4 * q + e] : make_uint4(0u, 0u, 0u, 0u);
+                    v[4 * e] = u.x, v[4 * e + 1] = u.y, v[4 * e + 2] = u.z, v[4 * e + 3] = u.w;
+                }
+                tmem_st16(lanes + kWtColK + 64 * i + 16 * q, v);
+            }
+            tc::tmem_wait_st();
+            tc::tc_fence_before();
+            __syncwarp();
+            if (lane == 0) tc::mbar_arrive(kbar);
+        }
         const float sl2 = a.scale * kLog2e;
         const float2 c2 = make_float2(sl2, sl2);
+        int done = 0;  // products before the step's
         for (int j = 0; j < steps; ++j) {
-            if (!warp_ok(lfull + stage(j), phase(j))) break;
-            const float* nl = sL + stage(j) * 256;
-            // pairs lo .. hi - 1 of the step's (of a tile, with those of the other behind them) see the position
-            const int t = first + 2 * j * per;
-            const bool part = __any_sync(0xffffffffu, p - x.before > t) || x.n < t + 2 * per;
+            const int t0 = first + 2 * j * per, p_last = p - lane + 31;
             float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-            // the step's sum; kPart: some pairs do not see the position (in code of its own: with the
-            // question asked for every pair, the others took twice the instructions)
+            // The step's sum; kPart: some of its pairs do not see some of the warp's positions. (Code of its
+            // own: asked for every pair, or between the 32s, of every step, that cost them all a quarter.)
             auto add_step = [&](auto kPart) -> bool {
-                float v[2][32];
-                float4 l4[2][8];
+                constexpr bool kAsk = decltype(kPart)::value;
+                const int n = kAsk ? filled(j) : 2;
 #pragma unroll
-                for (int e = 0; e < 8; ++e) l4[0][e] = reinterpret_cast<const float4*>(nl)[e];
-                if (!warp_ok(dfull + i, (uint32_t)j & 1u)) return false;
-                tc::tc_fence_after();
-                tmem_ld32(tD, v[0]);
+                for (int h = 0; h < 2; ++h) {
+                    if (kAsk && h == n) break;
+                    const int m = done + h * tiles + i, b = m % kWtBuffers;  // the product
+                    const uint32_t tD = lanes + 128 * b;
+                    if (!warp_ok(dfull + b, (uint32_t)(m / kWtBuffers) & 1u)) return false;
+                    tc::tc_fence_after();
+                    float v[2][32];
+                    tmem_ld32(tD, v[0]);
 #pragma unroll
-                for (int q = 0; q < 8; ++q) {
-                    const int at = q & 1, to = at ^ 1;
-                    tc::tmem_wait_ld();
-                    if (q < 7) {
-                        tmem_ld32(tD + 32 * (q + 1), v[to]);
-#pragma unroll
-                        for (int e = 0; e < 8; ++e) l4[to][e] = reinterpret_cast<const float4*>(nl + 32 * (q + 1))[e];
-                    } else {
-                        tc::tc_fence_before();
-                        __syncwarp();
-                        if (lane == 0) tc::mbar_arrive(dempty + i), tc::mbar_arrive(lempty + stage(j));
-                    }
-                    const int tq = t + (q >> 2) * per, lo = (p - x.before - tq) * R - 32 * (q & 3),
-                              hi = min(x.n - tq, per) * R - 32 * (q & 3);
-#pragma unroll
-                    for (int e = 0; e < 8; ++e) {
-                        const float4 l = l4[at][e];
-                        float2 x0 = fma2(make_float2(v[at][4 * e], v[at][4 * e + 1]), c2, make_float2(l.x, l.y));
-                        float2 x1 = fma2(make_float2(v[at][4 * e + 2], v[at][4 * e + 3]), c2, make_float2(l.z, l.w));
-                        if constexpr (decltype(kPart)::value) {
-                            const int c = 4 * e;
-                            x0.x = c >= lo && c < hi ? x0.x : -INFINITY, x0.y = c + 1 >= lo && c + 1 < hi ? x0.y : -INFINITY;
-                            x1.x = c + 2 >= lo && c + 2 < hi ? x1.x : -INFINITY, x1.y = c + 3 >= lo && c + 3 < hi ? x1.y : -INFINITY;
+                    for (int q = 0; q < 4; ++q) {
+                        const int at = q & 1;
+                        tc::tmem_wait_ld();
+                        if (q < 3) {
+                            tmem_ld32(tD + 32 * (q + 1), v[at ^ 1]);
+                        } else {  // the buffer is read
+                            tc::tc_fence_before();
+                            __syncwarp();
+                            if (lane == 0) tc::mbar_arrive(dempty + b);
                         }
-                        s0 = add2(s0, make_float2(ex2_approx(x0.x), ex2_approx(x0.y)));
-                        s1 = add2(s1, make_float2(ex2_approx(x1.x), ex2_approx(x1.y)));
+                        // pairs lo .. hi - 1 of these 32 see the position
+                        const int t = t0 + h * per, hi = min(x.n - t, per) * R - 32 * q;
+                        const int lo = (p - x.before - t) * R - 32 * q, lo0 = lo - lane * R;
+                        if (kAsk && (hi <= 0 || lo0 >= 32)) continue;  // none of the warp's
+#pragma unroll
+                        for (int e = 0; e < 8; ++e) {
+                            float2 x0 = mul2(make_float2(v[at][4 * e], v[at][4 * e + 1]), c2);
+                            float2 x1 = mul2(make_float2(v[at][4 * e + 2], v[at][4 * e + 3]), c2);
+                            if (kAsk) {
+                                const int c = 4 * e;
+                                x0.x = c >= lo && c < hi ? x0.x : -INFINITY, x0.y = c + 1 >= lo && c + 1 < hi ? x0.y : -INFINITY;
+                                x1.x = c + 2 >= lo && c + 2 < hi ? x1.x : -INFINITY, x1.y = c + 3 >= lo && c + 3 < hi ? x1.y : -INFINITY;
+                            }
+                            s0 = add2(s0, make_float2(ex2_approx(x0.x), ex2_approx(x0.y)));
+                            s1 = add2(s1, make_float2(ex2_approx(x1.x), ex2_approx(x1.y)));
+                        }
                     }
                 }
+                done += n * tiles;
                 return true;
             };
+            const bool part = p_last - x.before > t0 || x.n < t0 + 2 * per;  // (the same in the whole warp)
             if (!(part ? add_step(std::true_type()) : add_step(std::false_type()))) break;
             sum += (s0.x + s0.y) + (s1.x + s1.y);  // (a step's terms first, then the steps: no long chain of roundings)
         }
@@ -273,7 +328,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         // the copies in flight must land and every product issued must be done
         // before the tensor memory is freed and the CTA exits (all bounded)
         if (warp == 0 && tc::elect_one()) {
-            tc::mbar_wait(kbar, 0, 100000000ull);
             for (int i = 0; i < kWtStages; ++i)
                 tc::mbar_wait(qfull + i, 0, 100000000ull), tc::mbar_wait(qfull + i, 1, 100000000ull);
         } else if (warp == 1 && tc::elect_one()) {
@@ -291,14 +345,13 @@ cudaError_t launch_attn_weights_tiles(const PromptArgs& a, const PromptSums& w, 
     cudaError_t e = cudaFuncSetAttribute(attn_weights_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)WtSmem::kBytes);
     if (e != cudaSuccess) return e;
     const int R = a.Hq / a.Hkv, per = 128 / R;
-    CUtensorMap tmq, tmk;
+    CUtensorMap tmq;
     const unsigned long long row = kAttnD * 2;
     // (a call without rows has no queries to copy: any map will do)
     e = make_rows_map(a.q, a.Hq, a.rows > 0 ? a.rows : 1, row, (unsigned long long)a.q_stride * 2, R, per, &tmq);
-    if (e == cudaSuccess) e = make_rows_map(a.k_cache, a.Tmax, (unsigned long long)a.S * a.Hkv, row, row * a.Tmax, kWtPos, 1, &tmk);
     if (e != cudaSuccess) return e;
     const long blocks = (long)((a.Tmax + 2 * kWtPos - 1) / (2 * kWtPos)) * a.Hkv * a.S;
-    return launch_pdl(attn_weights_tile_kernel, dim3((unsigned)blocks), dim3(kWtThreads), WtSmem::kBytes, st, a, w, tmq, tmk);
+    return launch_pdl(attn_weights_tile_kernel, dim3((unsigned)blocks), dim3(kWtThreads), WtSmem::kBytes, st, a, w, tmq);
 }
 
 }  // namespace m2

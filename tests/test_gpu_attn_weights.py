@@ -245,3 +245,17 @@ def test_two_graphs_share_a_workspace(m2, act):
     _done(m2)
     for i in range(2):
         assert torch.equal(f[i]["out"], want[i][0]) and torch.equal(out[i], want[i][1])
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("scale", [0.0, -0.05, 3.0, 2.0 ** -50])
+def test_prompt_scales(m2, act, scale):
+    import torch
+    c = Caches(m2, [20, 0], 10, 2, act, 200, seed=23, spread=0.5)
+    p = Packed(c, [150, 60])
+    p.attend(scale=scale)
+    acc = _acc(c)
+    out = torch.full_like(acc, -7.0)
+    p.weigh(acc, out, 1000)
+    _done(m2)
+    _check_prompt(c, p, acc, out, 1000)
