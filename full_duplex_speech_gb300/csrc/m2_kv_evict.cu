@@ -6,13 +6,16 @@
 //     k_out[j] = k[kept_j],  v_out[j] = v[kept_j],  acc_out[j] = acc[kept_j].
 // Bound by HBM: the kept rows are read and written once.
 //
-// A (session, kv head) is a cluster of W CTAs, and CTA w moves 1 / W of every
-// row's bytes, of keys and values alike. So each CTA moves its columns in
-// order by itself: a batch of rows is read before any of it is written, and
-// a row never moves up, so that in place nothing is written that a later batch
-// still reads, with no word between the CTAs. (Rows dealt to CTAs would have
-// to wait for one another.) Each CTA finds the least weight that stays by
-// itself: a radix selection, three passes over the weights.
+// W CTAs share a (session, kv head). Each finds by itself the least weight that
+// stays: a radix selection, three passes over the weights, which it keeps in shared
+// memory as whole numbers in the weights' order.
+//   Out of place a CTA then moves the rows of a run of positions.
+//   In place the W are a cluster, and each moves 1 / W of every row's bytes, of keys
+// and values alike. So it moves its columns in order by itself: a batch of rows
+// is read before any of it is written, and a row never moves up, so that nothing
+// is written that a later batch still reads, with no word between the CTAs. (Rows
+// dealt to CTAs would have to wait for one another.) The weights move last, when
+// no CTA reads them any more.
 #include <math.h>
 
 #include "m2_dense_dev.cuh"
@@ -22,11 +25,11 @@ namespace m2 {
 
 namespace {
 
-constexpr int kEvThreads = 512, kEvWarps = kEvThreads / 32;
-constexpr int kEvBlock = 1024;        // positions that are looked through at a time
+constexpr int kEvThreads = 512, kEvWarps = kEvThreads / 32;  // a position a thread is looked at at a time: a block
 constexpr int kEvBins = 2048;         // 11 bits of a key
-constexpr int kEvMaxW = 8;
-constexpr int kEvFlight = 8;          // 16-byte pieces a thread has in flight
+constexpr int kEvMaxW = 8;            // in place
+constexpr int kEvFlight = 8;          // 16-byte pieces, or keys, a thread has in flight
+constexpr int kEvStaged = 24576;      // positions whose keys fit in shared memory; longer caches read the weights again
 
 // Weights in order as whole numbers: NaN above all, +0 and -0 alike.
 __device__ __forceinline__ uint32_t weight_key(float f) {
@@ -37,8 +40,8 @@ __device__ __forceinline__ uint32_t weight_key(float f) {
 
 struct EvSmem {
     int bins[kEvBins];
-    int list[kEvBlock];               // positions of the block that stay
-    int warp[kEvWarps + 1];
+    int list[kEvThreads];             // positions of the block that stay
+    int warp[2][kEvWarps];
     int pick[2];
 };
 
@@ -65,47 +68,72 @@ __device__ __forceinline__ int block_sum(int v, int* warp, int* total) {
     return ahead + upto - v;
 }
 
-// grid (W, Hkv, S), a cluster of W
-__global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictArgs a, int W) {
+// grid (W, Hkv, S); in place a cluster of W
+__global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictArgs a, int W, bool in_place) {
     __shared__ EvSmem sm;
-    const int tid = threadIdx.x, w = blockIdx.x, g = blockIdx.y, s = blockIdx.z;
+    extern __shared__ uint32_t keys[];  // of the older positions, where they fit
+    const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, w = blockIdx.x, g = blockIdx.y, s = blockIdx.z;
     pdl_wait();
     pdl_trigger();
     const int L = a.lens[s];
-    if (L < 0 || L > a.Tmax) {  // the whole cluster
+    if (L < 0 || L > a.Tmax) {  // every CTA of them
         if (tid == 0 && w == 0) record_error(a.err, ERR_ATTN_LENGTH);
         return;
     }
-    const bool in_place = a.k == a.k_out;
+    const bool rows_stay = a.k == a.k_out;
     const size_t from = ((size_t)s * a.Hkv + g) * a.Tmax, to = ((size_t)s * a.Hkv + g) * a.out_max;
     const float* acc = a.acc + from;
     const bool cut = L > a.keep;
-    if (!cut && in_place && a.kept == nullptr && a.acc == a.acc_out) return;
+    if (!cut && rows_stay && a.kept == nullptr && a.acc == a.acc_out) return;
     const int old = cut ? L - a.recent : L;        // positions below it are weighed
     const int want = cut ? a.keep - a.recent : 0;  // of which so many stay
+    const bool weigh = cut && want > 0, staged = old <= kEvStaged;
+    for (int i = tid; i < kEvBins; i += kEvThreads) sm.bins[i] = 0;
+    __syncthreads();
     // the key of the last that stays, and how many of that key do
     uint32_t least = 0;
     int ties = 0;
-    if (cut && want > 0) {
+    if (weigh) {
         int left = want;
         uint32_t prefix = 0;
 #pragma unroll 1
         for (int pass = 0; pass < 3; ++pass) {
             const int shift = pass == 0 ? 21 : pass == 1 ? 10 : 0, bits = pass == 2 ? 10 : 11;
             const uint32_t above = pass == 0 ? 0u : ~0u << (pass == 1 ? 21 : 10);
-            for (int i = tid; i < kEvBins; i += kEvThreads) sm.bins[i] = 0;
-            __syncthreads();
-            for (int p = tid; p < old; p += kEvThreads) {
-                const uint32_t k = weight_key(acc[p]);
-                if ((k & above) == prefix) atomicAdd(sm.bins + ((k >> shift) & ((1u << bits) - 1u)), 1);
+            for (int p0 = tid; p0 < old; p0 += kEvFlight * kEvThreads) {
+                uint32_t k[kEvFlight];
+                if (pass > 0 && staged) {
+#pragma unroll
+                    for (int f = 0; f < kEvFlight; ++f)
+                        if (p0 + f * kEvThreads < old) k[f] = keys[p0 + f * kEvThreads];
+                } else {
+                    float x[kEvFlight];
+#pragma unroll
+                    for (int f = 0; f < kEvFlight; ++f)
+                        if (p0 + f * kEvThreads < old) x[f] = acc[p0 + f * kEvThreads];
+#pragma unroll
+                    for (int f = 0; f < kEvFlight; ++f)
+                        if (p0 + f * kEvThreads < old) {
+                            k[f] = weight_key(x[f]);
+                            if (staged) keys[p0 + f * kEvThreads] = k[f];
+                        }
+                }
+#pragma unroll
+                for (int f = 0; f < kEvFlight; ++f)
+                    if (p0 + f * kEvThreads < old && (k[f] & above) == prefix)
+                        atomicAdd(sm.bins + ((k[f] >> shift) & ((1u << bits) - 1u)), 1);
             }
             __syncthreads();
             // the bin that holds the left-th largest: thread i has bins from the top, 4 i .. 4 i + 3
             int c[4], mine = 0;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) mine += c[j] = sm.bins[kEvBins - 1 - (4 * tid + j)];
+            for (int j = 0; j < 4; ++j) {
+                int* bin = sm.bins + kEvBins - 1 - (4 * tid + j);
+                mine += c[j] = *bin;
+                *bin = 0;  // for the next pass
+            }
             int all;
-            int ahead = block_sum(mine, sm.warp, &all);
+            int ahead = block_sum(mine, sm.warp[0], &all);
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
                 if (ahead < left && left <= ahead + c[j]) sm.pick[0] = kEvBins - 1 - (4 * tid + j), sm.pick[1] = left - ahead;
@@ -114,52 +142,81 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictArgs a, int W
             __syncthreads();
             prefix |= (uint32_t)sm.pick[0] << shift;
             left = sm.pick[1];
-            __syncthreads();
         }
         least = prefix;
         ties = left;
     }
-    // Which positions of a block stay: ascending, into sm.list; returns how many.
+    auto key_at = [&](int p) { return staged ? keys[p] : weight_key(acc[p]); };
+    // Which positions of the block from p0 on stay: ascending, into sm.list; returns how many.
     // `seen` ties came before.
     auto block_list = [&](int p0, int* seen) -> int {
-        int n = 0;
-#pragma unroll
-        for (int h = 0; h < kEvBlock / kEvThreads; ++h) {
-            const int p = p0 + h * kEvThreads + tid;
-            bool keep = false, tie = false;
-            if (p < L) {
-                if (!cut || p >= old)
-                    keep = true;
-                else if (want > 0) {
-                    const uint32_t k = weight_key(acc[p]);
-                    keep = k > least;
-                    tie = k == least;
-                }
+        const int p = p0 + tid;
+        bool keep = false, tie = false;
+        if (p < L) {
+            if (!cut || p >= old) {
+                keep = true;
+            } else if (weigh) {
+                const uint32_t k = key_at(p);
+                keep = k > least;
+                tie = k == least;
             }
-            int all;
-            const int rank = block_sum(tie ? 1 : 0, sm.warp, &all) + *seen;
-            *seen += all;
-            keep = keep || (tie && rank < ties);
-            const int at = block_sum(keep ? 1 : 0, sm.warp, &all);
-            if (keep) sm.list[n + at] = p;
-            n += all;
         }
+        // both counts of a warp's ahead of its own, in one round
+        const unsigned below = (1u << lane) - 1u, kb = __ballot_sync(0xffffffffu, keep), tb = __ballot_sync(0xffffffffu, tie);
+        __syncthreads();
+        if (lane == 0) sm.warp[0][warp] = __popc(kb), sm.warp[1][warp] = __popc(tb);
+        __syncthreads();
+        int n = 0, ties_here = *seen, at = 0;
+#pragma unroll
+        for (int i = 0; i < kEvWarps; ++i) {
+            const int t = sm.warp[1][i], first = min(max(ties - ties_here, 0), t), stay = sm.warp[0][i] + first;
+            if (i == warp) {
+                // this warp's first `first` ties stay
+                const bool mine = keep || (tie && __popc(tb & below) < first);
+                const unsigned all = __ballot_sync(0xffffffffu, mine);
+                keep = mine;
+                at = n + __popc(all & below);
+            }
+            n += stay;
+            ties_here += t;
+        }
+        if (keep) sm.list[at] = p;
+        *seen = ties_here;
         __syncthreads();
         return n;
     };
-    const bool rows_move = cut || !in_place;
-    if (rows_move) {
+    // the run of blocks whose rows this CTA moves, and what stays of those ahead of it
+    const int blocks = (L + kEvThreads - 1) / kEvThreads;
+    const int b0 = in_place ? 0 : (int)((long)blocks * w / W), b1 = in_place ? blocks : (int)((long)blocks * (w + 1) / W);
+    int seen = 0, done = 0;
+    if (b0 > 0) {
+        int n = 0, t = 0;
+        for (int p = tid; p < b0 * kEvThreads; p += kEvThreads) {
+            if (!cut || p >= old) {
+                ++n;
+            } else if (weigh) {
+                const uint32_t k = key_at(p);
+                n += k > least;
+                t += k == least;
+            }
+        }
+        block_sum(n, sm.warp[0], &done);
+        block_sum(t, sm.warp[1], &seen);
+        done += min(seen, ties);
+    }
+    float* acc_out = a.acc_out + to;
+    int* kept = a.kept ? a.kept + ((size_t)s * a.Hkv + g) * a.keep : nullptr;
+    if (cut || !rows_stay) {
         // 16-byte pieces of this CTA: `per` of a row's keys, then as many of its values
-        const int per = a.row_bytes / 16 / W, both = 2 * per, at_once = kEvThreads / both;
+        const int share = in_place ? W : 1, per = a.row_bytes / 16 / share, both = 2 * per, at_once = kEvThreads / both;
         const int lane_row = tid / both, piece = tid % both;
         const bool value = piece >= per;
-        const size_t column = (size_t)(w * per + piece % per) * 16;
+        const size_t column = (size_t)((in_place ? w : 0) * per + piece % per) * 16;
         const uint8_t* src = static_cast<const uint8_t*>(value ? a.v : a.k) + from * a.row_bytes + column;
         uint8_t* dst = static_cast<uint8_t*>(value ? a.v_out : a.k_out) + to * a.row_bytes + column;
-        int seen = 0, done = 0;
-        for (int p0 = 0; p0 < L; p0 += kEvBlock) {
-            const int n = block_list(p0, &seen);
-            if (!(in_place && done == p0 && n == min(kEvBlock, L - p0))) {  // (nothing left before: already there)
+        for (int b = b0; b < b1; ++b) {
+            const int p0 = b * kEvThreads, n = block_list(p0, &seen);
+            if (!(rows_stay && done == p0 && n == min(kEvThreads, L - p0))) {  // (nothing left before: already there)
                 for (int i0 = 0; i0 < n; i0 += kEvFlight * at_once) {
                     uint4 v[kEvFlight];
 #pragma unroll
@@ -167,7 +224,7 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictArgs a, int W
                         const int i = i0 + f * at_once + lane_row;
                         if (i < n) v[f] = *reinterpret_cast<const uint4*>(src + (size_t)sm.list[i] * a.row_bytes);
                     }
-                    if (in_place) __syncthreads();  // the batch is read before any of it is written
+                    if (rows_stay) __syncthreads();  // the batch is read before any of it is written
 #pragma unroll
                     for (int f = 0; f < kEvFlight; ++f) {
                         const int i = i0 + f * at_once + lane_row;
@@ -175,32 +232,30 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictArgs a, int W
                     }
                 }
             }
+            if (!in_place && tid < n) {
+                acc_out[done + tid] = acc[sm.list[tid]];
+                if (kept) kept[done + tid] = sm.list[tid];
+            }
             done += n;
             __syncthreads();  // the list is read
         }
     }
+    if (!in_place) return;
     // The weights and the list, by the first CTA, when no other reads the weights any more.
     if (W > 1) {
         tc::cluster_arrive();
         tc::cluster_wait();
     }
     if (w != 0) return;
-    int seen = 0, done = 0;
-    float* acc_out = a.acc_out + to;
-    int* kept = a.kept ? a.kept + ((size_t)s * a.Hkv + g) * a.keep : nullptr;
-    for (int p0 = 0; p0 < L; p0 += kEvBlock) {
-        const int n = block_list(p0, &seen);
-        float v[kEvBlock / kEvThreads];
-#pragma unroll
-        for (int h = 0; h < kEvBlock / kEvThreads; ++h)
-            if (tid + h * kEvThreads < n) v[h] = acc[sm.list[tid + h * kEvThreads]];
+    seen = done = 0;
+    for (int b = 0; b < blocks; ++b) {
+        const int n = block_list(b * kEvThreads, &seen);
+        float v = 0.f;
+        if (tid < n) v = acc[sm.list[tid]];
         __syncthreads();
-#pragma unroll
-        for (int h = 0; h < kEvBlock / kEvThreads; ++h) {
-            const int j = tid + h * kEvThreads;
-            if (j >= n) continue;
-            acc_out[done + j] = v[h];
-            if (kept) kept[done + j] = sm.list[j];
+        if (tid < n) {
+            acc_out[done + tid] = v;
+            if (kept) kept[done + tid] = sm.list[tid];
         }
         done += n;
         __syncthreads();
@@ -210,12 +265,23 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictArgs a, int W
 }  // namespace
 
 cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t st) {
-    // CTAs a (session, kv head): while the GPU's 152 SMs hold them at once, four of 512 threads an SM
+    const bool in_place = a.k == a.k_out || a.acc == a.acc_out;
+    const int staged = a.Tmax < kEvStaged ? a.Tmax : kEvStaged;
+    const cudaError_t e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvStaged * 4);
+    if (e != cudaSuccess) return e;
+    // CTAs a (session, kv head): while the 152 SMs hold them at once, two an SM in place, four out of place
     int W = 1;
-    while (W < kEvMaxW && (long)a.S * a.Hkv * 2 * W <= 2 * 152) W *= 2;
+    const long pairs = (long)a.S * a.Hkv;
+    if (in_place) {
+        while (W < kEvMaxW && pairs * 2 * W <= 2 * 152) W *= 2;
+    } else {
+        const long blocks = (a.Tmax + kEvThreads - 1) / kEvThreads, most = 4 * 152 / pairs;
+        W = (int)(most < 1 ? 1 : most < blocks ? most : blocks);
+    }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(W, a.Hkv, a.S);
     cfg.blockDim = dim3(kEvThreads);
+    cfg.dynamicSmemBytes = (size_t)staged * 4;
     cfg.stream = st;
     cudaLaunchAttribute attr[2];
     attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
@@ -225,8 +291,8 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t st) {
     attr[1].val.clusterDim.y = 1;
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
-    cfg.numAttrs = W > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, kv_evict_kernel, a, W);
+    cfg.numAttrs = in_place && W > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, kv_evict_kernel, a, W, in_place);
 }
 
 }  // namespace m2
