@@ -28,6 +28,7 @@ namespace {
 constexpr int kEvThreads = 512, kEvWarps = kEvThreads / 32;  // a position a thread is looked at at a time: a block
 constexpr int kEvBins = 2048;         // 11 bits of a key
 constexpr int kEvMaxW = 8;            // in place
+constexpr int kEvRun = 128;           // positions a CTA is worth having for, out of place
 constexpr int kEvFlight = 8;          // 16-byte pieces, or keys, a thread has in flight
 constexpr int kEvStaged = 24576;      // positions whose keys fit in shared memory; longer caches read the weights again
 
@@ -147,12 +148,12 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictArgs a, int W
         ties = left;
     }
     auto key_at = [&](int p) { return staged ? keys[p] : weight_key(acc[p]); };
-    // Which positions of the block from p0 on stay: ascending, into sm.list; returns how many.
+    // Which positions of the block p0 .. end - 1 stay: ascending, into sm.list; returns how many.
     // `seen` ties came before.
-    auto block_list = [&](int p0, int* seen) -> int {
+    auto block_list = [&](int p0, int end, int* seen) -> int {
         const int p = p0 + tid;
         bool keep = false, tie = false;
-        if (p < L) {
+        if (p < end) {
             if (!cut || p >= old) {
                 keep = true;
             } else if (weigh) {
@@ -185,13 +186,12 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictArgs a, int W
         __syncthreads();
         return n;
     };
-    // the run of blocks whose rows this CTA moves, and what stays of those ahead of it
-    const int blocks = (L + kEvThreads - 1) / kEvThreads;
-    const int b0 = in_place ? 0 : (int)((long)blocks * w / W), b1 = in_place ? blocks : (int)((long)blocks * (w + 1) / W);
+    // the run of positions whose rows this CTA moves, and what stays of those ahead of it
+    const int q0 = in_place ? 0 : (int)((long)L * w / W), q1 = in_place ? L : (int)((long)L * (w + 1) / W);
     int seen = 0, done = 0;
-    if (b0 > 0) {
+    if (q0 > 0) {
         int n = 0, t = 0;
-        for (int p = tid; p < b0 * kEvThreads; p += kEvThreads) {
+        for (int p = tid; p < q0; p += kEvThreads) {
             if (!cut || p >= old) {
                 ++n;
             } else if (weigh) {
@@ -214,8 +214,8 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictArgs a, int W
         const size_t column = (size_t)((in_place ? w : 0) * per + piece % per) * 16;
         const uint8_t* src = static_cast<const uint8_t*>(value ? a.v : a.k) + from * a.row_bytes + column;
         uint8_t* dst = static_cast<uint8_t*>(value ? a.v_out : a.k_out) + to * a.row_bytes + column;
-        for (int b = b0; b < b1; ++b) {
-            const int p0 = b * kEvThreads, n = block_list(p0, &seen);
+        for (int p0 = q0; p0 < q1; p0 += kEvThreads) {
+            const int n = block_list(p0, q1, &seen);
             if (!(rows_stay && done == p0 && n == min(kEvThreads, L - p0))) {  // (nothing left before: already there)
                 for (int i0 = 0; i0 < n; i0 += kEvFlight * at_once) {
                     uint4 v[kEvFlight];
@@ -248,8 +248,8 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictArgs a, int W
     }
     if (w != 0) return;
     seen = done = 0;
-    for (int b = 0; b < blocks; ++b) {
-        const int n = block_list(b * kEvThreads, &seen);
+    for (int p0 = 0; p0 < L; p0 += kEvThreads) {
+        const int n = block_list(p0, L, &seen);
         float v = 0.f;
         if (tid < n) v = acc[sm.list[tid]];
         __syncthreads();
@@ -269,14 +269,18 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t st) {
     const int staged = a.Tmax < kEvStaged ? a.Tmax : kEvStaged;
     const cudaError_t e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvStaged * 4);
     if (e != cudaSuccess) return e;
-    // CTAs a (session, kv head): while the 152 SMs hold them at once, two an SM in place, four out of place
+    // CTAs a (session, kv head): in place while the 152 SMs hold them at once, two an SM. Out of place one
+    // an SM where there are few (each chooses by itself, which takes as long as moving 400 rows: one
+    // session of 7,500 positions 17.5 us with 19 a head, 19.1 with 38, 29.9 with 59), two a head where
+    // there are many (64 sessions: 161 us, 177 with one, 163 with three).
     int W = 1;
     const long pairs = (long)a.S * a.Hkv;
     if (in_place) {
         while (W < kEvMaxW && pairs * 2 * W <= 2 * 152) W *= 2;
     } else {
-        const long blocks = (a.Tmax + kEvThreads - 1) / kEvThreads, most = 4 * 152 / pairs;
-        W = (int)(most < 1 ? 1 : most < blocks ? most : blocks);
+        const long runs = (a.Tmax + kEvRun - 1) / kEvRun, most = 152 / pairs;
+        W = (int)(most < 2 ? 2 : most);
+        W = (int)(W < runs ? W : runs);
     }
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3(W, a.Hkv, a.S);
