@@ -785,15 +785,32 @@ __global__ void __launch_bounds__(kWalkThreads, 2)
         __syncthreads();
         const float* kept = a.kept + ((size_t)s * a.Hkv + g) * sums_head(a.Tmax, R);
         const int end = ok ? min(ce * kWalkTc, len + 1) : 0;
-        for (int p = cb * kWalkTc + tid; p < end; p += kWalkThreads) {
-            const float2* sc = reinterpret_cast<const float2*>(kept + (size_t)p * sums_pitch(R));
-            float sum = 0.f;
-            for (int r = 0; r < R; r += 2) {
-                const float2 x = sc[r >> 1];
-                sum = fmaf(ex2_approx(x.x - whole[r].x), whole[r].y, sum);
-                if (r + 1 < R) sum = fmaf(ex2_approx(x.y - whole[r + 1].x), whole[r + 1].y, sum);
+        // four positions a thread on their way together (one after the other, a walker of
+        // 3,700 positions spends 30 us here)
+        constexpr int kFlight = 4;
+        for (int p0 = cb * kWalkTc + tid; p0 < end; p0 += kFlight * kWalkThreads) {
+            float2 x[kFlight][kAttnMaxR / 2];
+            float old[kFlight];
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f) {
+                const int p = p0 + f * kWalkThreads;
+                const float2* sc = reinterpret_cast<const float2*>(kept + (size_t)p * sums_pitch(R));
+                old[f] = p < min(end, len) ? a.acc[row0 + p] : 0.f;
+#pragma unroll
+                for (int r = 0; r < kAttnMaxR; r += 2)
+                    if (r < R && p < end) x[f][r >> 1] = sc[r >> 1];
             }
-            a.acc_out[row0 + p] = (p < len ? a.acc[row0 + p] : 0.f) + sum;
+#pragma unroll
+            for (int f = 0; f < kFlight; ++f) {
+                const int p = p0 + f * kWalkThreads;
+                float sum = 0.f;
+#pragma unroll
+                for (int r = 0; r < kAttnMaxR; r += 2) {
+                    if (r < R) sum = fmaf(ex2_approx(x[f][r >> 1].x - whole[r].x), whole[r].y, sum);
+                    if (r + 1 < R) sum = fmaf(ex2_approx(x[f][r >> 1].y - whole[r + 1].x), whole[r + 1].y, sum);
+                }
+                if (p < end) a.acc_out[row0 + p] = old[f] + sum;
+            }
         }
         if (W == 1) return;
     }
