@@ -66,34 +66,33 @@ cudaError_t launch_append(const PromptArgs& a, cudaStream_t st) {
     return launch_pdl(prompt_append_kernel, dim3(blocks), dim3(kApThreads), 0, st, a, kAttnD * (a.bf16 ? 2 : 4));
 }
 
-// ------------------------------------------------- fp32 products of fp32 units
-// A CTA takes up to 64 rows of one (session, kv head), whole packed rows of R
-// heads, and walks the positions 64 at a time, with an online softmax.
-constexpr int kPfThreads = 256, kPfRows = 64, kPfPos = 64;
+// ------------------------------------------------------ fp32, on the CUDA cores
+// A CTA takes up to 32 rows of one (session, kv head), whole packed rows of R
+// heads, and walks the positions 64 at a time with an online softmax: a thread 4
+// rows x 4 positions of the scores, then 4 rows x 8 dims of the output, in paired
+// fp32 arithmetic. Bound by those products and their reads of shared memory; the
+// copies of a chunk's values run under its scores, those of the next keys under
+// its values. Two CTAs an SM, so that one's products cover the other's barriers
+// (five prompts of up to 301, 12 / 2 heads: 55 us; with 64 rows, 256 threads, one
+// CTA an SM and no copies ahead 70).
+constexpr int kPfThreads = 128, kPfRows = 32, kPfPos = 64;
 constexpr int kPfPitch = kAttnD + 4;  // floats: a column of 16-byte pieces meets all banks
 struct PfSmem {
     static constexpr int kQ = 0, kK = kQ + kPfRows * kPfPitch, kV = kK + kPfPos * kPfPitch, kP = kV + kPfPos * kAttnD,
                          kBad = kP + kPfRows * (kPfPos + 4), kFind = kBad + 4, kFloats = kFind + kPfThreads / 32 + 4;
+    static_assert(2 * (kFloats * 4 + 1024) <= 228 * 1024, "two CTAs an SM");
 };
 
-template <typename TA> __device__ __forceinline__ float4 load4(const void* p, size_t elem) {
-    if constexpr (sizeof(TA) == 2) {
-        const uint2 w = *reinterpret_cast<const uint2*>(static_cast<const uint16_t*>(p) + elem);
-        return make_float4(__uint_as_float(w.x << 16), __uint_as_float(w.x & 0xFFFF0000u), __uint_as_float(w.y << 16),
-                           __uint_as_float(w.y & 0xFFFF0000u));
-    } else {
-        return *reinterpret_cast<const float4*>(static_cast<const float*>(p) + elem);
-    }
-}
-
-template <typename TA>
-__global__ void __launch_bounds__(kPfThreads) prompt_fp32_kernel(PromptArgs a) {
+__global__ void __launch_bounds__(kPfThreads, 2) prompt_f32_kernel(PromptArgs a) {
     extern __shared__ __align__(16) float pf[];
     float *sQ = pf + PfSmem::kQ, *sK = pf + PfSmem::kK, *sV = pf + PfSmem::kV, *sP = pf + PfSmem::kP;
-    unsigned* sBad = reinterpret_cast<unsigned*>(pf + PfSmem::kBad);
+    // values that are not finite, a bit a position; for the chunks in turn (one's are still read when the next begins)
+    unsigned* sBads = reinterpret_cast<unsigned*>(pf + PfSmem::kBad);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int R = a.Hq / a.Hkv, per = kPfRows / R;
     const int g = blockIdx.x % a.Hkv;
+    const float* q = static_cast<const float*>(a.q);
+    float* out = static_cast<float*>(a.out);
     pdl_wait();
     pdl_trigger();
     int s, tile;
@@ -101,66 +100,58 @@ __global__ void __launch_bounds__(kPfThreads) prompt_fp32_kernel(PromptArgs a) {
     Session x;
     session_of(a, s, &x);
     const int t0 = tile * per, rows = min(per, x.n - t0) * R;
+    auto packed = [&](int row) { return (size_t)(x.row0 + t0 + row / R); };
+    auto column = [&](int row) { return (size_t)(g * R + row % R) * kAttnD; };
     if (!x.ok) {
         if (tid == 0) record_error(a.err, ERR_ATTN_LENGTH);
-        for (int i = tid; i < rows * kAttnD; i += kPfThreads) {
-            const int row = i / kAttnD;
-            store_act<TA>(a.out, (size_t)(x.row0 + t0 + row / R) * a.out_stride + (size_t)(g * R + row % R) * kAttnD + i % kAttnD, 0.f);
-        }
+        for (int i = tid; i < rows * kAttnD; i += kPfThreads)
+            out[packed(i / kAttnD) * a.out_stride + column(i / kAttnD) + i % kAttnD] = 0.f;
         if (a.lse)
-            for (int row = tid; row < rows; row += kPfThreads)
-                a.lse[(size_t)(x.row0 + t0 + row / R) * a.Hq + g * R + row % R] = -INFINITY;
+            for (int row = tid; row < rows; row += kPfThreads) a.lse[packed(row) * a.Hq + g * R + row % R] = -INFINITY;
         return;
     }
+    const int all = x.before + t0 + 1;           // positions that every row sees
+    const int total = x.before + t0 + rows / R;  // ... and that the last one does
+    const size_t cache0 = ((size_t)s * a.Hkv + g) * a.Tmax * kAttnD;
+    // a warp copies four positions at a time, a lane 16 bytes of each
+    auto copy = [&](const void* cache, int p0, float* to, int pitch) {
+        const float* from = static_cast<const float*>(cache) + cache0 + (size_t)p0 * kAttnD + (tid & 31) * 4;
+        for (int p = tid >> 5; p < kPfPos && p0 + p < total; p += kPfThreads / 32)
+            cp_async16(to + p * pitch + (tid & 31) * 4, from + (size_t)p * kAttnD);
+        asm volatile("cp.async.commit_group;" ::: "memory");
+    };
     for (int i = tid; i < kPfRows * kAttnD / 4; i += kPfThreads) {
         const int row = i / (kAttnD / 4), d = i % (kAttnD / 4) * 4;
         float4 v = make_float4(0.f, 0.f, 0.f, 0.f);
-        if (row < rows)
-            v = load4<TA>(a.q, (size_t)(x.row0 + t0 + row / R) * a.q_stride + (size_t)(g * R + row % R) * kAttnD + d);
+        if (row < rows) v = *reinterpret_cast<const float4*>(q + packed(row) * a.q_stride + column(row) + d);
         *reinterpret_cast<float4*>(sQ + row * kPfPitch + d) = v;
     }
-    const size_t cache0 = ((size_t)s * a.Hkv + g) * a.Tmax * kAttnD;
+    copy(a.k_cache, 0, sK, kPfPitch);
     const float sl2 = a.scale * kLog2e;
     int lim[4];  // the last position that this thread's rows see
-    float m[4], l[4], o[4][8];
+    float m[4], l[4];
+    float2 o[4][4];
     bool bad[4];
 #pragma unroll
     for (int i = 0; i < 4; ++i) {
         const int row = 4 * ty + i;
         lim[i] = row < rows ? x.before + t0 + row / R : -1;
-        m[i] = -FLT_MAX, l[i] = 0.f, bad[i] = false;
+        m[i] = kNone, l[i] = 0.f, bad[i] = false;
 #pragma unroll
-        for (int e = 0; e < 8; ++e) o[i][e] = 0.f;
+        for (int e = 0; e < 4; ++e) o[i][e] = make_float2(0.f, 0.f);
     }
-    const int all = x.before + t0 + 1;         // positions that every row sees
-    const int total = x.before + t0 + rows / R;  // ... and that the last one does
     for (int p0 = 0; p0 < total; p0 += kPfPos) {
         const bool cut = p0 + kPfPos > all;
-        __syncthreads();  // the tiles of the positions before are read
+        unsigned* sBad = sBads + 2 * (p0 / kPfPos & 1);
+        asm volatile("cp.async.wait_all;" ::: "memory");  // the keys
         if (tid < 2) sBad[tid] = 0u;
-        if (cut) __syncthreads();
-        for (int i = tid; i < kPfPos * kAttnD / 4; i += kPfThreads) {
-            const int p = i / (kAttnD / 4), d = i % (kAttnD / 4) * 4;
-            float4 k = make_float4(0.f, 0.f, 0.f, 0.f), v = k;
-            if (p0 + p < total) {
-                k = load4<TA>(a.k_cache, cache0 + (size_t)(p0 + p) * kAttnD + d);
-                v = load4<TA>(a.v_cache, cache0 + (size_t)(p0 + p) * kAttnD + d);
-                // a value that is not finite must not reach the rows that do not see it: it counts as 0
-                // here, and the rows that see it read NaN
-                if (cut && !(fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY && fabsf(v.z) < INFINITY && fabsf(v.w) < INFINITY)) {
-                    atomicOr(sBad + (p >> 5), 1u << (p & 31));
-                    v = make_float4(0.f, 0.f, 0.f, 0.f);
-                }
-            }
-            *reinterpret_cast<float4*>(sK + p * kPfPitch + d) = k;
-            *reinterpret_cast<float4*>(sV + p * kAttnD + d) = v;
-        }
-        __syncthreads();
-        float w[4][4];
+        __syncthreads();  // (and the values before are read)
+        copy(a.v_cache, p0, sV, kAttnD);
+        float2 z[4][4];
 #pragma unroll
         for (int i = 0; i < 4; ++i)
 #pragma unroll
-            for (int j = 0; j < 4; ++j) w[i][j] = 0.f;
+            for (int j = 0; j < 4; ++j) z[i][j] = make_float2(0.f, 0.f);
 #pragma unroll 4
         for (int d = 0; d < kAttnD; d += 4) {
             float4 qv[4], kv[4];
@@ -172,20 +163,18 @@ __global__ void __launch_bounds__(kPfThreads) prompt_fp32_kernel(PromptArgs a) {
             for (int i = 0; i < 4; ++i)
 #pragma unroll
                 for (int j = 0; j < 4; ++j) {
-                    w[i][j] = fmaf(qv[i].x, kv[j].x, w[i][j]);
-                    w[i][j] = fmaf(qv[i].y, kv[j].y, w[i][j]);
-                    w[i][j] = fmaf(qv[i].z, kv[j].z, w[i][j]);
-                    w[i][j] = fmaf(qv[i].w, kv[j].w, w[i][j]);
+                    z[i][j] = fma2(make_float2(qv[i].x, qv[i].y), make_float2(kv[j].x, kv[j].y), z[i][j]);
+                    z[i][j] = fma2(make_float2(qv[i].z, qv[i].w), make_float2(kv[j].z, kv[j].w), z[i][j]);
                 }
         }
 #pragma unroll
         for (int i = 0; i < 4; ++i) {
             const int see = lim[i] - p0;
-            float top = -INFINITY;
+            float w[4], top = -INFINITY;
 #pragma unroll
-            for (int j = 0; j < 4; ++j) {
-                w[i][j] = tx + 16 * j <= see ? w[i][j] * sl2 : -INFINITY;
-                top = fmaxf(top, w[i][j]);
+            for (int j = 0; j < 4; ++j) {  // (keys behind the last are whatever was there)
+                w[j] = tx + 16 * j <= see ? (z[i][j].x + z[i][j].y) * sl2 : -INFINITY;
+                top = fmaxf(top, w[j]);
             }
 #pragma unroll
             for (int off = 1; off < 16; off <<= 1) top = fmaxf(top, __shfl_xor_sync(0xffffffffu, top, off));
@@ -193,36 +182,56 @@ __global__ void __launch_bounds__(kPfThreads) prompt_fp32_kernel(PromptArgs a) {
             m[i] = now;
             l[i] *= f;
 #pragma unroll
-            for (int e = 0; e < 8; ++e) o[i][e] *= f;
+            for (int e = 0; e < 4; ++e) o[i][e] = mul2(o[i][e], make_float2(f, f));
 #pragma unroll
             for (int j = 0; j < 4; ++j) {
-                const float p = ex2_approx(w[i][j] - now);
+                const float p = ex2_approx(w[j] - now);
                 l[i] += p;
                 sP[(4 * ty + i) * (kPfPos + 4) + tx + 16 * j] = p;
             }
-            if (cut && see >= 0) {
-                const unsigned lo = sBad[0], hi = sBad[1];
-                bad[i] |= (lo & (see >= 31 ? ~0u : (2u << see) - 1u)) != 0u ||
-                          (see >= 32 && (hi & (see >= 63 ? ~0u : (2u << (see - 32)) - 1u)) != 0u);
+        }
+        asm volatile("cp.async.wait_all;" ::: "memory");  // the values
+        if (cut) {
+            // A value that is not finite must not reach the rows that do not see it: it counts as 0 here, and
+            // the rows that see it read NaN. Positions behind the last count as 0 too. (Each thread looks
+            // at what it copied.)
+            for (int p = tid >> 5; p < kPfPos; p += kPfThreads / 32) {
+                float4* at = reinterpret_cast<float4*>(sV + p * kAttnD + (tid & 31) * 4);
+                const float4 v = *at;
+                const bool there = p0 + p < total;
+                const bool off = !(fabsf(v.x) < INFINITY && fabsf(v.y) < INFINITY && fabsf(v.z) < INFINITY && fabsf(v.w) < INFINITY);
+                if (there && off) atomicOr(sBad + (p >> 5), 1u << (p & 31));
+                if (!there || off) *at = make_float4(0.f, 0.f, 0.f, 0.f);
             }
         }
-        __syncthreads();
+        __syncthreads();  // the values, the weights; the keys are read
+        if (p0 + kPfPos < total) copy(a.k_cache, p0 + kPfPos, sK, kPfPitch);
+        if (cut && (sBad[0] | sBad[1])) {
+#pragma unroll
+            for (int i = 0; i < 4; ++i) {
+                const int see = lim[i] - p0;
+                if (see >= 0)
+                    bad[i] |= (sBad[0] & (see >= 31 ? ~0u : (2u << see) - 1u)) != 0u ||
+                              (see >= 32 && (sBad[1] & (see >= 63 ? ~0u : (2u << (see - 32)) - 1u)) != 0u);
+            }
+        }
 #pragma unroll 2
         for (int p = 0; p < kPfPos; p += 4) {
             float4 pr[4];
 #pragma unroll
             for (int i = 0; i < 4; ++i) pr[i] = *reinterpret_cast<const float4*>(sP + (4 * ty + i) * (kPfPos + 4) + p);
 #pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                const float4 va = *reinterpret_cast<const float4*>(sV + (p + q) * kAttnD + 4 * tx);
-                const float4 vb = *reinterpret_cast<const float4*>(sV + (p + q) * kAttnD + 64 + 4 * tx);
+            for (int e = 0; e < 4; ++e) {
+                const float4 va = *reinterpret_cast<const float4*>(sV + (p + e) * kAttnD + 4 * tx);
+                const float4 vb = *reinterpret_cast<const float4*>(sV + (p + e) * kAttnD + 64 + 4 * tx);
 #pragma unroll
                 for (int i = 0; i < 4; ++i) {
-                    const float c = (&pr[i].x)[q];
-                    o[i][0] = fmaf(c, va.x, o[i][0]), o[i][1] = fmaf(c, va.y, o[i][1]);
-                    o[i][2] = fmaf(c, va.z, o[i][2]), o[i][3] = fmaf(c, va.w, o[i][3]);
-                    o[i][4] = fmaf(c, vb.x, o[i][4]), o[i][5] = fmaf(c, vb.y, o[i][5]);
-                    o[i][6] = fmaf(c, vb.z, o[i][6]), o[i][7] = fmaf(c, vb.w, o[i][7]);
+                    const float c = (&pr[i].x)[e];
+                    const float2 c2 = make_float2(c, c);
+                    o[i][0] = fma2(c2, make_float2(va.x, va.y), o[i][0]);
+                    o[i][1] = fma2(c2, make_float2(va.z, va.w), o[i][1]);
+                    o[i][2] = fma2(c2, make_float2(vb.x, vb.y), o[i][2]);
+                    o[i][3] = fma2(c2, make_float2(vb.z, vb.w), o[i][3]);
                 }
             }
         }
@@ -233,25 +242,20 @@ __global__ void __launch_bounds__(kPfThreads) prompt_fp32_kernel(PromptArgs a) {
         for (int off = 1; off < 16; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
         const int row = 4 * ty + i;
         if (row >= rows) continue;
-        const size_t packed = x.row0 + t0 + row / R;
-        const size_t at = packed * a.out_stride + (size_t)(g * R + row % R) * kAttnD;
+        float* to = out + packed(row) * a.out_stride + column(row) + 4 * tx;
         const float inv = bad[i] ? NAN : 1.f / l[i];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            store_act<TA>(a.out, at + 4 * tx + e, o[i][e] * inv);
-            store_act<TA>(a.out, at + 64 + 4 * tx + e, o[i][4 + e] * inv);
-        }
-        if (a.lse && tx == 0) a.lse[packed * a.Hq + g * R + row % R] = m[i] * kLn2 + logf(l[i]);
+        *reinterpret_cast<float4*>(to) = make_float4(o[i][0].x * inv, o[i][0].y * inv, o[i][1].x * inv, o[i][1].y * inv);
+        *reinterpret_cast<float4*>(to + 64) = make_float4(o[i][2].x * inv, o[i][2].y * inv, o[i][3].x * inv, o[i][3].y * inv);
+        if (a.lse && tx == 0) a.lse[packed(row) * a.Hq + g * R + row % R] = fmaf(m[i], kLn2, logf(l[i]));
     }
 }
 
-template <typename TA>
-cudaError_t launch_fp32(const PromptArgs& a, cudaStream_t st) {
+cudaError_t launch_f32(const PromptArgs& a, cudaStream_t st) {
     constexpr int bytes = PfSmem::kFloats * 4;
-    cudaError_t e = cudaFuncSetAttribute(prompt_fp32_kernel<TA>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = cudaFuncSetAttribute(prompt_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
     if (e != cudaSuccess) return e;
     const long tiles = most_tiles(a.S, a.rows, kPfRows / (a.Hq / a.Hkv));
-    return launch_pdl(prompt_fp32_kernel<TA>, dim3((unsigned)(tiles * a.Hkv)), dim3(kPfThreads), bytes, st, a);
+    return launch_pdl(prompt_f32_kernel, dim3((unsigned)(tiles * a.Hkv)), dim3(kPfThreads), bytes, st, a);
 }
 
 }  // namespace
@@ -259,7 +263,7 @@ cudaError_t launch_fp32(const PromptArgs& a, cudaStream_t st) {
 cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t st) {
     cudaError_t e = launch_append(a, st);
     if (e != cudaSuccess) return e;
-    return a.bf16 ? launch_attn_prompt_tiles(a, st) : launch_fp32<float>(a, st);
+    return a.bf16 ? launch_attn_prompt_tiles(a, st) : launch_f32(a, st);
 }
 
 }  // namespace m2
