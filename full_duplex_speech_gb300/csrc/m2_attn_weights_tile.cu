@@ -52,8 +52,8 @@ struct WtSmem {
     static constexpr uint32_t kOne = kE + kWtStages * 2 * kWtExtra;   // the ones they are multiplied by, likewise
     static constexpr uint32_t kRaw = kOne + kWtExtra;                 // float [kWtRaw][256]: lse on its way
     static constexpr uint32_t kBar = kRaw + kWtRaw * 256 * 4;
-    // k, qfull[stages], qempty[stages], efull[stages], d[buffers], dempty[buffers], end
-    static constexpr int kBars = 3 * kWtStages + 2 * kWtBuffers + 2;
+    // kload, k, qfull[stages], qempty[stages], efull[stages], d[buffers], dempty[buffers], end
+    static constexpr int kBars = 3 * kWtStages + 2 * kWtBuffers + 3;
     static constexpr uint32_t kTmem = kBar + kBars * 8;
     static constexpr uint32_t kFlag = kTmem + 4;
     static constexpr uint32_t kBytes = kFlag + 4 + 1024;              // + slack to align to 1024
@@ -66,12 +66,13 @@ __device__ __forceinline__ void products_meet() { asm volatile("barrier.sync 1, 
 
 // grid: (position tiles of 256) x Hkv x S, the first tiles, which most rows see, first
 __global__ void __launch_bounds__(kWtThreads, 1)
-    attn_weights_tile_kernel(PromptArgs a, PromptSums w, const __grid_constant__ CUtensorMap tmq) {
+    attn_weights_tile_kernel(PromptArgs a, PromptSums w, const __grid_constant__ CUtensorMap tmq,
+                             const __grid_constant__ CUtensorMap tmk) {
     using L = WtSmem;
     extern __shared__ uint8_t wt_raw[];
     uint8_t* sm = wt_raw + ((1024u - (tc::smem_u32(wt_raw) & 1023u)) & 1023u);
-    uint64_t* kbar = reinterpret_cast<uint64_t*>(sm + L::kBar);
-    uint64_t *qfull = kbar + 1, *qempty = qfull + kWtStages, *efull = qempty + kWtStages,
+    uint64_t* kload = reinterpret_cast<uint64_t*>(sm + L::kBar);
+    uint64_t *kbar = kload + 1, *qfull = kbar + 1, *qempty = qfull + kWtStages, *efull = qempty + kWtStages,
              *dfull = efull + kWtStages, *dempty = dfull + kWtBuffers, *endbar = dempty + kWtBuffers;
     uint32_t* sTmem = reinterpret_cast<uint32_t*>(sm + L::kTmem);
     volatile uint32_t* flag = reinterpret_cast<uint32_t*>(sm + L::kFlag);
@@ -80,7 +81,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const int heads = a.Hkv * a.S, p0 = (int)(blockIdx.x / heads) * 2 * kWtPos;
     const int g = blockIdx.x % heads % a.Hkv, s = blockIdx.x % heads / a.Hkv;
 
-    if (tid == 0) prefetch_map(&tmq);
+    if (tid == 0) prefetch_map(&tmq), prefetch_map(&tmk);
     pdl_wait();
     Session x;
     const bool rows_ok = session_of(a, s, &x);
@@ -97,7 +98,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     const size_t head = ((size_t)s * a.Hkv + g) * a.Tmax;
 
     if (tid == 0) {
-        tc::mbar_init(kbar, 4 * tiles);
+        tc::mbar_init(kload, 1), tc::mbar_init(kbar, 4 * tiles);
         for (int i = 0; i < kWtStages; ++i) {
             tc::mbar_init(qfull + i, 1), tc::mbar_init(qempty + i, 1), tc::mbar_init(efull + i, 2);
         }
@@ -118,7 +119,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             *reinterpret_cast<uint4*>(sm + L::kE + i * 16) = ones ? make_uint4(0x3F803F80u, 0x3F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
         }
         const int dead = 128 - per * R, each = dead * 8;  // 16-byte pieces of a tile's panel
-        for (int i = tid - 128; i < kWtStages * 4 * each; i += kWtThreads - 128) {
+        for (int i = tid - 128; i < (kWtStages - 1) * 4 * each; i += kWtThreads - 128) {
             const int panel = i / each, row = per * R + i % each / 8;  // (stage, panel, tile)
             *reinterpret_cast<uint4*>(sm + L::kQ + panel * kWtPanel + row * 128 + i % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
@@ -143,14 +144,37 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     auto warp_ok = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait_ok(bar, parity)); };
     auto stage = [](int j) { return j % kWtStages; };
     auto phase = [](int j) { return (uint32_t)(j / kWtStages) & 1u; };
+    // a warp: the rows of a stage that no packed row fills
+    auto zero_dead = [&](int st) {
+        for (int i = lane; i < 4 * (128 - per * R) * 8; i += 32) {
+            const int row = per * R + (i >> 5);
+            *reinterpret_cast<uint4*>(sm + L::kQ + st * kWtStage + (i >> 3 & 3) * kWtPanel + row * 128 + (i & 7) * 16) =
+                make_uint4(0u, 0u, 0u, 0u);
+        }
+        tc::fence_proxy_async_smem();
+        __syncwarp();
+    };
     // tiles of pairs of step j that have rows
     auto filled = [&](int j) { return first + (2 * j + 1) * per < x.n ? 2 : 1; };
 
     float sum = 0.f;
     if (warp == 0) {
         // ---------------------------------------------------------------- copies
+        // the keys go by way of the ring's last stage
+        if (steps > 0 && tc::elect_one()) {
+            tc::mbar_arrive_expect_tx(kload, (uint32_t)tiles * 2 * kWtPanel);
+            for (int i = 0; i < tiles; ++i)
+                for (int h = 0; h < 2; ++h)
+                    tc::tma_load_3d(sm + L::kQ + (kWtStages - 1) * kWtStage + (2 * i + h) * kWtPanel, &tmk, 64 * h, p0 + i * kWtPos,
+                                    s * a.Hkv + g, kload);
+        }
+        __syncwarp();
         for (int j = 0; j < steps; ++j) {
             if (j >= kWtStages && !warp_ok(qempty + stage(j), phase(j - kWtStages))) break;
+            if (j == kWtStages - 1) {  // the keys are read; the rows that no packed row fills are zeros again
+                if (!warp_ok(kbar, 0)) break;
+                zero_dead(j);
+            }
             if (tc::elect_one()) {
                 const int n = filled(j);
                 tc::mbar_arrive_expect_tx(qfull + stage(j), (uint32_t)(n * 2 * per * R * 128));
@@ -249,18 +273,22 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         // ------------------------------------------ sums, one position a thread
         const int i = (warp - 4) >> 2, p = p0 + tid - 128;
         const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
-        if (steps > 0) {  // its key, two dims a column
-            const uint4* key = reinterpret_cast<const uint4*>(static_cast<const uint16_t*>(a.k_cache) + (head + p) * kAttnD);
+        if (steps > 0) {
+            // its key, two dims a column (read from the cache, a row a thread, it took 2 us more)
+            warp_ok(kload, 0);
+            const uint8_t* key = sm + L::kQ + (kWtStages - 1) * kWtStage + 2 * i * kWtPanel + (tid & 127) * 128;
 #pragma unroll
             for (int q = 0; q < 4; ++q) {
                 uint32_t v[16];
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint4 u = p < total ? key[4 * q + e] : make_uint4(0u, 0u, 0u, 0u);
+                    const uint4 u = *reinterpret_cast<const uint4*>(key + (q >> 1) * kWtPanel +
+                                                                    (((4 * (q & 1) + e) ^ (tid & 7)) << 4));
                     v[4 * e] = u.x, v[4 * e + 1] = u.y, v[4 * e + 2] = u.z, v[4 * e + 3] = u.w;
                 }
                 tmem_st16(lanes + kWtColK + 64 * i + 16 * q, v);
             }
+            tc::fence_proxy_async_smem();  // (read before the stage's queries come)
             tc::tmem_wait_st();
             tc::tc_fence_before();
             __syncwarp();
@@ -331,6 +359,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         // the copies in flight must land and every product issued must be done
         // before the tensor memory is freed and the CTA exits (all bounded)
         if (warp == 0 && tc::elect_one()) {
+            if (steps > 0) tc::mbar_wait(kload, 0, 100000000ull);
             for (int i = 0; i < kWtStages; ++i)
                 tc::mbar_wait(qfull + i, 0, 100000000ull), tc::mbar_wait(qfull + i, 1, 100000000ull);
         } else if (warp == 1 && tc::elect_one()) {
@@ -348,13 +377,14 @@ cudaError_t launch_attn_weights_tiles(const PromptArgs& a, const PromptSums& w, 
     cudaError_t e = cudaFuncSetAttribute(attn_weights_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)WtSmem::kBytes);
     if (e != cudaSuccess) return e;
     const int R = a.Hq / a.Hkv, per = 128 / R;
-    CUtensorMap tmq;
+    CUtensorMap tmq, tmk;
     const unsigned long long row = kAttnD * 2;
     // (a call without rows has no queries to copy: any map will do)
     e = make_rows_map(a.q, a.Hq, a.rows > 0 ? a.rows : 1, row, (unsigned long long)a.q_stride * 2, R, per, &tmq);
+    if (e == cudaSuccess) e = make_rows_map(a.k_cache, a.Tmax, (unsigned long long)a.S * a.Hkv, row, row * a.Tmax, kWtPos, 1, &tmk);
     if (e != cudaSuccess) return e;
     const long blocks = (long)((a.Tmax + 2 * kWtPos - 1) / (2 * kWtPos)) * a.Hkv * a.S;
-    return launch_pdl(attn_weights_tile_kernel, dim3((unsigned)blocks), dim3(kWtThreads), WtSmem::kBytes, st, a, w, tmq);
+    return launch_pdl(attn_weights_tile_kernel, dim3((unsigned)blocks), dim3(kWtThreads), WtSmem::kBytes, st, a, w, tmq, tmk);
 }
 
 }  // namespace m2
