@@ -38,6 +38,8 @@
 // The run holding position len[s] takes the new key and value from the
 // inputs instead of the cache, and writes them into the cache there (no other
 // CTA reads that slot).
+#include <mutex>
+
 #include "m2_common.cuh"
 #include "m2_launch.h"
 #include "m2_tc.cuh"
@@ -868,12 +870,18 @@ cudaError_t make_cache_map(const void* cache, const AttnArgs& a, CUtensorMap* ma
 // and how many clusters of 2, 4, 8 and 16 walkers the device holds at once.
 template <bool kSums>
 cudaError_t walk_setup(const int (**clusters)[5]) {
-    static int configured_device = -1;
-    static int cached[5];
+    static std::mutex mutex;
+    static struct {
+        bool done;
+        int held[5];
+    } per_device[64];
     int dev = 0;
     cudaError_t e = cudaGetDevice(&dev);
     if (e != cudaSuccess) return e;
-    if (configured_device != dev) {
+    std::lock_guard<std::mutex> lock(mutex);
+    auto& u = per_device[dev & 63];
+    int(&cached)[5] = u.held;
+    if (!u.done) {
         e = cudaFuncSetAttribute(attn_walk_kernel<kSums>, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)kWalkSmem);
         if (e != cudaSuccess) return e;
         const bool wide = cudaFuncSetAttribute(attn_walk_kernel<kSums>, cudaFuncAttributeNonPortableClusterSizeAllowed, 1) ==
@@ -896,7 +904,7 @@ cudaError_t walk_setup(const int (**clusters)[5]) {
             cached[k] = n;
         }
         (void)cudaGetLastError();  // a refused query leaves no sticky error
-        configured_device = dev;
+        u.done = true;
     }
     *clusters = &cached;
     return cudaSuccess;

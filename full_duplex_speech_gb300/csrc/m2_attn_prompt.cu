@@ -252,7 +252,7 @@ __global__ void __launch_bounds__(kPfThreads, 2) prompt_f32_kernel(PromptArgs a)
 
 cudaError_t launch_f32(const PromptArgs& a, cudaStream_t st) {
     constexpr int bytes = PfSmem::kFloats * 4;
-    cudaError_t e = cudaFuncSetAttribute(prompt_f32_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = allow_shared<0>((const void*)prompt_f32_kernel, bytes);
     if (e != cudaSuccess) return e;
     const long tiles = most_tiles(a.S, a.rows, kPfRows / (a.Hq / a.Hkv));
     return launch_pdl(prompt_f32_kernel, dim3((unsigned)(tiles * a.Hkv)), dim3(kPfThreads), bytes, st, a);

@@ -129,14 +129,20 @@ __device__ __forceinline__ void tma_store_3d(const void* tmap, int x, int y, int
 // The pair of tiles `at` of all the sessions' pairs of `per` packed rows each,
 // found by a warp, four sessions a lane at a time (a session's last pair first:
 // it sees the most positions). A session whose rows do not lie within the call's
-// has none, and is recorded.
-__device__ __forceinline__ PtWork find_pair(const PromptArgs& a, int per, int at) {
+// has none, and is recorded. `from`: the sessions and pairs that lie before, for the
+// next time.
+struct PtFound {
+    int s0, base;
+};
+__device__ __forceinline__ PtWork find_pair(const PromptArgs& a, int per, int at, PtFound* from) {
     constexpr int kEach = 4;
     const int lane = threadIdx.x & 31;
     PtWork y = {-1, 0, 0, 0, 0, at % a.Hkv};
     at /= a.Hkv;
-    int base = 0;
-    for (int s0 = 0; s0 < a.S; s0 += 32 * kEach) {
+    if (at < from->base) *from = {0, 0};
+    int base = from->base;
+    for (int s0 = from->s0; s0 < a.S; s0 += 32 * kEach) {
+        *from = {s0, base};
         int b[kEach + 1], before[kEach], n[kEach], mine = 0;
         const int first = s0 + lane * kEach;
 #pragma unroll
@@ -169,12 +175,12 @@ __device__ __forceinline__ PtWork find_pair(const PromptArgs& a, int per, int at
         }
         const unsigned who = __ballot_sync(0xffffffffu, y.s >= 0);
         if (who) {
-            const int from = __ffs(who) - 1;
-            y.s = __shfl_sync(0xffffffffu, y.s, from);
-            y.row0 = __shfl_sync(0xffffffffu, y.row0, from);
-            y.n = __shfl_sync(0xffffffffu, y.n, from);
-            y.before = __shfl_sync(0xffffffffu, y.before, from);
-            y.pair = __shfl_sync(0xffffffffu, y.pair, from);
+            const int src = __ffs(who) - 1;
+            y.s = __shfl_sync(0xffffffffu, y.s, src);
+            y.row0 = __shfl_sync(0xffffffffu, y.row0, src);
+            y.n = __shfl_sync(0xffffffffu, y.n, src);
+            y.before = __shfl_sync(0xffffffffu, y.before, src);
+            y.pair = __shfl_sync(0xffffffffu, y.pair, src);
             return y;
         }
         base += __shfl_sync(0xffffffffu, upto, 31);
@@ -300,6 +306,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 
     if (W > 1) tc::cluster_arrive_relaxed();  // waited on before the first remote access: every CTA has started
     bool good = true;                         // warp 0: no wait has run out, and copies may go on
+    PtFound found = {0, 0};                   // warp 0: where it has looked for pairs
     bool appended = false;                    // warp 0: the append has been waited for
     // warp 0: a pair's queries, behind those of q pairs before; and its pieces p .. end - 1 of the ring,
     // where `first` is the first of them
@@ -355,7 +362,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         // (The kernel before this one is this call's append, which has waited for what came before
         // it: only the caches are its own. They are waited for where they are read, and at the end,
         // so that whoever waits for this kernel has waited for the append too.)
-        const PtWork y = find_pair(a, 2 * per, (int)blockIdx.x / W);
+        const PtWork y = find_pair(a, 2 * per, (int)blockIdx.x / W, &found);
         if (lane == 0) *work(0) = y;
         if (y.s >= 0) {
             const PtRun run(a, y, per, W, wk);
@@ -407,7 +414,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     const int x = good ? answer_next(sm + L::kNext) : -1;
                     tc::fence_proxy_async_smem();  // (the answer is read before another may come)
                     __syncwarp();
-                    if (x >= 0) z = find_pair(a, 2 * per, x);
+                    if (x >= 0) z = find_pair(a, 2 * per, x, &found);
                     // (where the wait runs out, the others' waits end as soon as that is known: a second
                     // one sees them pass)
                     if (k > 0 && !warp_ok(passed, (uint32_t)(k - 1) & 1u)) good = false, tc::mbar_wait(passed, (uint32_t)(k - 1) & 1u);

@@ -123,7 +123,7 @@ __global__ void __launch_bounds__(kWfThreads) weights_fp32_kernel(PromptArgs a, 
 template <typename TA>
 cudaError_t launch_fp32(const PromptArgs& a, const PromptSums& w, cudaStream_t st) {
     constexpr int bytes = WfSmem::kFloats * 4;
-    cudaError_t e = cudaFuncSetAttribute(weights_fp32_kernel<TA>, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    cudaError_t e = allow_shared<sizeof(TA)>((const void*)weights_fp32_kernel<TA>, bytes);
     if (e != cudaSuccess) return e;
     return launch_pdl(weights_fp32_kernel<TA>, dim3((a.Tmax + kWfPos - 1) / kWfPos, a.Hkv, a.S), dim3(kWfThreads), bytes, st,
                       a, w);

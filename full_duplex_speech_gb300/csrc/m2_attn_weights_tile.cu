@@ -64,7 +64,7 @@ struct WtSmem {
 // a product.
 __device__ __forceinline__ void products_meet() { asm volatile("barrier.sync 1, 64;" ::: "memory"); }
 
-// grid: (position tiles of 256) x Hkv x S, the first tiles, which most rows see, first
+// grid: n x Hkv x S, a CTA for every n-th tile of 256 positions; the first tiles, which most rows see, first
 __global__ void __launch_bounds__(kWtThreads, 1)
     attn_weights_tile_kernel(PromptArgs a, PromptSums w, const __grid_constant__ CUtensorMap tmq,
                              const __grid_constant__ CUtensorMap tmk) {
@@ -78,7 +78,8 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     volatile uint32_t* flag = reinterpret_cast<uint32_t*>(sm + L::kFlag);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int R = a.Hq / a.Hkv, per = 128 / R;  // packed rows a tile of pairs
-    const int heads = a.Hkv * a.S, p0 = (int)(blockIdx.x / heads) * 2 * kWtPos;
+    const int heads = a.Hkv * a.S, stride = gridDim.x / heads;  // tiles of 256 positions: this CTA's first, and from one to the next
+    const int tile0 = blockIdx.x / heads;
     const int g = blockIdx.x % heads % a.Hkv, s = blockIdx.x % heads / a.Hkv;
 
     if (tid == 0) prefetch_map(&tmq), prefetch_map(&tmk);
@@ -86,19 +87,15 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     Session x;
     const bool rows_ok = session_of(a, s, &x);
     if (!rows_ok || !x.ok) {
-        if (tid == 0 && p0 == 0) record_error(a.err, rows_ok ? ERR_ATTN_LENGTH : ERR_ROW_START);
+        if (tid == 0 && tile0 == 0) record_error(a.err, rows_ok ? ERR_ATTN_LENGTH : ERR_ROW_START);
         return;
     }
     const int total = x.before + x.n;
-    if (p0 >= total) return;
-    // the window's rows that see a position of the CTA: first .. n - 1, in steps of 2 per
-    const int first = max(max(0, x.n - w.window), p0 - x.before);
-    const int steps = first < x.n ? (x.n - first + 2 * per - 1) / (2 * per) : 0;
-    const int tiles = p0 + kWtPos < total ? 2 : 1;  // of positions
+    if (tile0 * 2 * kWtPos >= total) return;
     const size_t head = ((size_t)s * a.Hkv + g) * a.Tmax;
 
     if (tid == 0) {
-        tc::mbar_init(kload, 1), tc::mbar_init(kbar, 4 * tiles);
+        tc::mbar_init(kload, 1), tc::mbar_init(kbar, 8);
         for (int i = 0; i < kWtStages; ++i) {
             tc::mbar_init(qfull + i, 1), tc::mbar_init(qempty + i, 1), tc::mbar_init(efull + i, 2);
         }
@@ -154,203 +151,252 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         tc::fence_proxy_async_smem();
         __syncwarp();
     };
+    // A tile of 256 positions: the window's rows that see any of them, first .. n - 1, in steps of 2 per.
+    struct Item {
+        int p0, first, steps, tiles;  // tiles: of 128 positions
+    };
+    auto item = [&](int tile) {
+        Item it;
+        it.p0 = tile * 2 * kWtPos;
+        it.first = max(max(0, x.n - w.window), it.p0 - x.before);
+        it.steps = it.first < x.n ? (x.n - it.first + 2 * per - 1) / (2 * per) : 0;
+        it.tiles = it.p0 + kWtPos < total ? 2 : 1;
+        return it;
+    };
     // tiles of pairs of step j that have rows
-    auto filled = [&](int j) { return first + (2 * j + 1) * per < x.n ? 2 : 1; };
+    auto filled = [&](const Item& it, int j) { return it.first + (2 * j + 1) * per < x.n ? 2 : 1; };
+    // Each warp's loop over the CTA's tiles of positions that have steps: role(it, k of them and J steps before)
+    auto every_item = [&](auto role) {
+        for (int tile = tile0, k = 0, J = 0; tile * 2 * kWtPos < total; tile += stride) {
+            const Item it = item(tile);
+            role(it, k, J);
+            k += it.steps > 0;
+            J += it.steps;
+        }
+    };
 
-    float sum = 0.f;
     if (warp == 0) {
         // ---------------------------------------------------------------- copies
-        // the keys go by way of the ring's last stage
-        if (steps > 0 && tc::elect_one()) {
-            tc::mbar_arrive_expect_tx(kload, (uint32_t)tiles * 2 * kWtPanel);
-            for (int i = 0; i < tiles; ++i)
-                for (int h = 0; h < 2; ++h)
-                    tc::tma_load_3d(sm + L::kQ + (kWtStages - 1) * kWtStage + (2 * i + h) * kWtPanel, &tmk, 64 * h, p0 + i * kWtPos,
-                                    s * a.Hkv + g, kload);
-        }
-        __syncwarp();
-        for (int j = 0; j < steps; ++j) {
-            if (j >= kWtStages && !warp_ok(qempty + stage(j), phase(j - kWtStages))) break;
-            if (j == kWtStages - 1) {  // the keys are read; the rows that no packed row fills are zeros again
-                if (!warp_ok(kbar, 0)) break;
-                zero_dead(j);
-            }
-            if (tc::elect_one()) {
-                const int n = filled(j);
-                tc::mbar_arrive_expect_tx(qfull + stage(j), (uint32_t)(n * 2 * per * R * 128));
-                for (int i = 0; i < n; ++i)
+        bool good = true;
+        every_item([&](const Item& it, int k, int J) {
+            if (it.steps == 0 || !good) return;
+            // the keys go by way of the stage of the third step
+            const int ks = stage(J + kWtStages - 1);
+            if (J > 0) good = warp_ok(qempty + stage(J - 1), phase(J - 1));
+            if (good && tc::elect_one()) {
+                tc::mbar_arrive_expect_tx(kload, (uint32_t)it.tiles * 2 * kWtPanel);
+                for (int i = 0; i < it.tiles; ++i)
                     for (int h = 0; h < 2; ++h)
-                        tc::tma_load_3d(sm + L::kQ + stage(j) * kWtStage + (2 * h + i) * kWtPanel, &tmq, 64 * h, g * R,
-                                        x.row0 + first + (2 * j + i) * per, qfull + stage(j));
+                        tc::tma_load_3d(sm + L::kQ + ks * kWtStage + (2 * i + h) * kWtPanel, &tmk, 64 * h, it.p0 + i * kWtPos,
+                                        s * a.Hkv + g, kload);
             }
             __syncwarp();
-        }
+            for (int j = 0; j < it.steps || j < kWtStages; ++j) {
+                if (j == kWtStages - 1) {  // the keys are read; the rows that no packed row fills are zeros again
+                    good = good && warp_ok(kbar, (uint32_t)k & 1u);
+                    if (good) zero_dead(ks);
+                }
+                if (j >= it.steps) continue;
+                const int at = stage(J + j);
+                if (J + j >= kWtStages) good = good && warp_ok(qempty + at, phase(J + j - kWtStages));
+                if (good && tc::elect_one()) {
+                    const int n = filled(it, j);
+                    tc::mbar_arrive_expect_tx(qfull + at, (uint32_t)(n * 2 * per * R * 128));
+                    for (int i = 0; i < n; ++i)
+                        for (int h = 0; h < 2; ++h)
+                            tc::tma_load_3d(sm + L::kQ + at * kWtStage + (2 * h + i) * kWtPanel, &tmq, 64 * h, g * R,
+                                            x.row0 + it.first + (2 * j + i) * per, qfull + at);
+                }
+                __syncwarp();
+            }
+        });
     } else if (warp == 1) {
         // -------------------------------------------------------------- products
         const bool leader = tc::elect_one();
         const uint32_t sbase = tc::smem_u32(sm);
-        for (int j = 0, m = 0; j < steps; ++j) {  // m: products so far
-            const int n = filled(j);
-            for (int d = 0; d < n * tiles; ++d, ++m) {
-                const int i = tiles == 2 ? d & 1 : 0, h = tiles == 2 ? d >> 1 : d, b = m % kWtBuffers;
-                products_meet();
-                tc::tc_fence_after();
-                if (leader) {
-                    const uint64_t bd = tc::sdesc(sbase + L::kQ + stage(j) * kWtStage + h * kWtPanel, 0, 1024, 2);
-                    const uint32_t to = tm + 128 * b, id = tc::idesc_bf16(128, 128, 0, 0);
-#pragma unroll
-                    for (int q = 0; q < 8; ++q)
-                        tc::mma_bf16_tmem_a(to, tm + kWtColK + 64 * i + 8 * q,
-                                            bd + (uint64_t)(((q >> 2) * 2 * kWtPanel + (q & 3) * 32) >> 4), id, q > 0 ? 1u : 0u);
-                    // (e last: the sums are cut off at the size of what they have reached)
-                    tc::mma_bf16(to, tc::sdesc(sbase + L::kOne, kWtExtra / 2, 128, 0),
-                                 tc::sdesc(sbase + L::kE + (2 * stage(j) + h) * kWtExtra, kWtExtra / 2, 128, 0), id, 1u);
-                    tc::mma_commit(dfull + b);
-                    if (d == n * tiles - 1) tc::mma_commit(qempty + stage(j));
+        int m = 0;  // products so far
+        every_item([&](const Item& it, int, int J) {
+            for (int j = 0; j < it.steps; ++j) {
+                const int n = filled(it, j), at = stage(J + j);
+                for (int d = 0; d < n * it.tiles; ++d, ++m) {
+                    const int i = it.tiles == 2 ? d & 1 : 0, h = it.tiles == 2 ? d >> 1 : d, b = m % kWtBuffers;
+                    products_meet();
+                    tc::tc_fence_after();
+                    if (leader) {
+                        const uint64_t bd = tc::sdesc(sbase + L::kQ + at * kWtStage + h * kWtPanel, 0, 1024, 2);
+                        const uint32_t to = tm + 128 * b, id = tc::idesc_bf16(128, 128, 0, 0);
+    #pragma unroll
+                        for (int q = 0; q < 8; ++q)
+                            tc::mma_bf16_tmem_a(to, tm + kWtColK + 64 * i + 8 * q,
+                                                bd + (uint64_t)(((q >> 2) * 2 * kWtPanel + (q & 3) * 32) >> 4), id, q > 0 ? 1u : 0u);
+                        // (e last: the sums are cut off at the size of what they have reached)
+                        tc::mma_bf16(to, tc::sdesc(sbase + L::kOne, kWtExtra / 2, 128, 0),
+                                     tc::sdesc(sbase + L::kE + (2 * at + h) * kWtExtra, kWtExtra / 2, 128, 0), id, 1u);
+                        tc::mma_commit(dfull + b);
+                        if (d == n * it.tiles - 1) tc::mma_commit(qempty + at);
+                    }
+                    __syncwarp();
                 }
-                __syncwarp();
             }
-        }
+        });
     } else if (warp == 12) {
         // -------------------------------------- waits on behalf of the products
         // (after one that gave up, what the products read is there, if not what it should be, and the
         // error is recorded; every meeting takes place)
-        bool good = steps > 0 && warp_ok(kbar, 0);
-        for (int j = 0, m = 0; j < steps; ++j) {
-            good = good && warp_ok(qfull + stage(j), phase(j)) && warp_ok(efull + stage(j), phase(j));
-            const int n = filled(j);
-            for (int d = 0; d < n * tiles; ++d, ++m) {
-                if (m >= kWtBuffers) good = good && warp_ok(dempty + m % kWtBuffers, (uint32_t)(m / kWtBuffers - 1) & 1u);
-                tc::tc_fence_before();
-                products_meet();
+        bool good = true;
+        int m = 0;
+        every_item([&](const Item& it, int k, int J) {
+            if (it.steps > 0) good = good && warp_ok(kbar, (uint32_t)k & 1u);
+            for (int j = 0; j < it.steps; ++j) {
+                const int at = stage(J + j);
+                good = good && warp_ok(qfull + at, phase(J + j)) && warp_ok(efull + at, phase(J + j));
+                const int products = filled(it, j) * it.tiles;
+                for (int d = 0; d < products; ++d, ++m) {
+                    if (m >= kWtBuffers) good = good && warp_ok(dempty + m % kWtBuffers, (uint32_t)(m / kWtBuffers - 1) & 1u);
+                    tc::tc_fence_before();
+                    products_meet();
+                }
             }
-        }
+        });
     } else if (warp < 4) {
         // ------------------------------------- the pairs' e, a tile of pairs a warp
         // (a lane's own copies of lse, kWtRaw steps ahead: loaded step by step they took 550 us of the
         // size below, and with one warp, which has a step's time for 256 of them, 357)
         const int h = warp - 2;
         float* raw = reinterpret_cast<float*>(sm + L::kRaw) + 128 * h + lane;
-        const float* from[4];  // a lane's pairs 32 e + lane, step by step
-        int t[4];
-#pragma unroll
-        for (int e = 0; e < 4; ++e) {
-            const int r = 32 * e + lane;
-            t[e] = r < per * R ? first + h * per + r / R : x.n;  // (a row that the tile does not have: never)
-            from[e] = a.lse + (size_t)(x.row0 + first + h * per + r / R) * a.Hq + g * R + r % R;
-        }
-        auto fetch = [&](int j) {
-#pragma unroll
-            for (int e = 0; e < 4; ++e) {
-                if (t[e] < x.n) cp_async4(raw + j % kWtRaw * 256 + 32 * e, from[e]);
-                t[e] += 2 * per, from[e] += (size_t)2 * per * a.Hq;
-            }
-            asm volatile("cp.async.commit_group;" ::: "memory");
-        };
         const float by = -1.f / a.scale, none = a.scale > 0.f ? -INFINITY : INFINITY;
-        for (int j = 0; j < kWtRaw - 1; ++j) fetch(j);
-        for (int j = 0; j < steps; ++j) {
-            fetch(j + kWtRaw - 1);
-            asm volatile("cp.async.wait_group %0;" ::"n"(kWtRaw - 1) : "memory");
-            if (j >= kWtStages && !warp_ok(qempty + stage(j), phase(j - kWtStages))) break;
+        bool good = true;
+        every_item([&](const Item& it, int, int J) {
+            const float* from[4];  // a lane's pairs 32 e + lane, step by step
+            int t[4];
 #pragma unroll
             for (int e = 0; e < 4; ++e) {
                 const int r = 32 * e + lane;
-                const float z = r < per * R ? raw[j % kWtRaw * 256 + 32 * e] * by : none;  // (no weight)
-                // hi + mid + lo, each what the ones before it leave, rounded; of an infinity hi alone
-                const uint32_t hi = float_to_bf16_bits(z);
-                const float top = bf16_bits_to_float(hi), rest = fabsf(top) < INFINITY ? z - top : 0.f;
-                const uint32_t mid = float_to_bf16_bits(rest), lo = float_to_bf16_bits(rest - bf16_bits_to_float(mid));
-                *reinterpret_cast<uint2*>(sm + L::kE + (2 * stage(j) + h) * kWtExtra + (r >> 3) * 128 + (r & 7) * 16) =
-                    make_uint2(hi | mid << 16, lo);
+                t[e] = r < per * R ? it.first + h * per + r / R : x.n;  // (a row that the tile does not have: never)
+                from[e] = a.lse + (size_t)(x.row0 + it.first + h * per + r / R) * a.Hq + g * R + r % R;
             }
-            tc::fence_proxy_async_smem();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(efull + stage(j));
-        }
-        asm volatile("cp.async.wait_all;" ::: "memory");
-    } else if (warp < 12 && (warp - 4) >> 2 < tiles) {
-        // ------------------------------------------ sums, one position a thread
-        const int i = (warp - 4) >> 2, p = p0 + tid - 128;
-        const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
-        if (steps > 0) {
-            // its key, two dims a column (read from the cache, a row a thread, it took 2 us more)
-            warp_ok(kload, 0);
-            const uint8_t* key = sm + L::kQ + (kWtStages - 1) * kWtStage + 2 * i * kWtPanel + (tid & 127) * 128;
-#pragma unroll
-            for (int q = 0; q < 4; ++q) {
-                uint32_t v[16];
+            auto fetch = [&](int j) {
 #pragma unroll
                 for (int e = 0; e < 4; ++e) {
-                    const uint4 u = *reinterpret_cast<const uint4*>(key + (q >> 1) * kWtPanel +
-                                                                    (((4 * (q & 1) + e) ^ (tid & 7)) << 4));
-                    v[4 * e] = u.x, v[4 * e + 1] = u.y, v[4 * e + 2] = u.z, v[4 * e + 3] = u.w;
+                    if (t[e] < x.n) cp_async4(raw + (J + j) % kWtRaw * 256 + 32 * e, from[e]);
+                    t[e] += 2 * per, from[e] += (size_t)2 * per * a.Hq;
                 }
-                tmem_st16(lanes + kWtColK + 64 * i + 16 * q, v);
+                asm volatile("cp.async.commit_group;" ::: "memory");
+            };
+            if (it.steps == 0) return;
+            for (int j = 0; j < kWtRaw - 1; ++j) fetch(j);
+            for (int j = 0; j < it.steps; ++j) {
+                const int at = stage(J + j);
+                fetch(j + kWtRaw - 1);
+                asm volatile("cp.async.wait_group %0;" ::"n"(kWtRaw - 1) : "memory");
+                if (J + j >= kWtStages) good = good && warp_ok(qempty + at, phase(J + j - kWtStages));
+                if (!good) break;
+#pragma unroll
+                for (int e = 0; e < 4; ++e) {
+                    const int r = 32 * e + lane;
+                    const float z = r < per * R ? raw[(J + j) % kWtRaw * 256 + 32 * e] * by : none;  // (no weight)
+                    // hi + mid + lo, each what the ones before it leave, rounded; of an infinity hi alone
+                    const uint32_t hi = float_to_bf16_bits(z);
+                    const float top = bf16_bits_to_float(hi), rest = fabsf(top) < INFINITY ? z - top : 0.f;
+                    const uint32_t mid = float_to_bf16_bits(rest), lo = float_to_bf16_bits(rest - bf16_bits_to_float(mid));
+                    *reinterpret_cast<uint2*>(sm + L::kE + (2 * at + h) * kWtExtra + (r >> 3) * 128 + (r & 7) * 16) =
+                        make_uint2(hi | mid << 16, lo);
+                }
+                tc::fence_proxy_async_smem();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(efull + at);
             }
-            tc::fence_proxy_async_smem();  // (read before the stage's queries come)
-            tc::tmem_wait_st();
-            tc::tc_fence_before();
-            __syncwarp();
-            if (lane == 0) tc::mbar_arrive(kbar);
-        }
+        });
+        asm volatile("cp.async.wait_all;" ::: "memory");
+    } else {
+        // ------------------------------------------ sums, one position a thread
+        const int i = (warp - 4) >> 2;
+        const uint32_t lanes = tm + ((uint32_t)((warp & 3) * 32) << 16);
         const float sl2 = a.scale * kLog2e;
         const float2 c2 = make_float2(sl2, sl2);
         int done = 0;  // products before the step's
-        for (int j = 0; j < steps; ++j) {
-            const int t0 = first + 2 * j * per, p_last = p - lane + 31;
-            float2 s0 = make_float2(0.f, 0.f), s1 = s0;
-            // The step's sum; kPart: some of its pairs do not see some of the warp's positions. (Code of its
-            // own: asked for every pair, or between the 32s, of every step, that cost them all a quarter.)
-            auto add_step = [&](auto kPart) -> bool {
-                constexpr bool kAsk = decltype(kPart)::value;
-                const int n = kAsk ? filled(j) : 2;
-#pragma unroll
-                for (int h = 0; h < 2; ++h) {
-                    if (kAsk && h == n) break;
-                    const int m = done + h * tiles + i, b = m % kWtBuffers;  // the product
-                    const uint32_t tD = lanes + 128 * b;
-                    if (!warp_ok(dfull + b, (uint32_t)(m / kWtBuffers) & 1u)) return false;
-                    tc::tc_fence_after();
-                    float v[2][32];
-                    tmem_ld32(tD, v[0]);
+        every_item([&](const Item& it, int k, int J) {
+            const int p = it.p0 + tid - 128, tiles = it.tiles;
+            if (it.steps > 0) {
+                // its key, two dims a column (read from the cache, a row a thread, it took 2 us more); the
+                // products with the one before are done
+                warp_ok(kload, (uint32_t)k & 1u);
+                if (i < tiles) {
+                    const uint8_t* key = sm + L::kQ + stage(J + kWtStages - 1) * kWtStage + 2 * i * kWtPanel + (tid & 127) * 128;
 #pragma unroll
                     for (int q = 0; q < 4; ++q) {
-                        const int at = q & 1;
-                        tc::tmem_wait_ld();
-                        if (q < 3) {
-                            tmem_ld32(tD + 32 * (q + 1), v[at ^ 1]);
-                        } else {  // the buffer is read
-                            tc::tc_fence_before();
-                            __syncwarp();
-                            if (lane == 0) tc::mbar_arrive(dempty + b);
-                        }
-                        // pairs lo .. hi - 1 of these 32 see the position
-                        const int t = t0 + h * per, hi = min(x.n - t, per) * R - 32 * q;
-                        const int lo = (p - x.before - t) * R - 32 * q, lo0 = lo - lane * R;
-                        if (kAsk && (hi <= 0 || lo0 >= 32)) continue;  // none of the warp's
+                        uint32_t v[16];
 #pragma unroll
-                        for (int e = 0; e < 8; ++e) {
-                            float2 x0 = mul2(make_float2(v[at][4 * e], v[at][4 * e + 1]), c2);
-                            float2 x1 = mul2(make_float2(v[at][4 * e + 2], v[at][4 * e + 3]), c2);
-                            if (kAsk) {
-                                const int c = 4 * e;
-                                x0.x = c >= lo && c < hi ? x0.x : -INFINITY, x0.y = c + 1 >= lo && c + 1 < hi ? x0.y : -INFINITY;
-                                x1.x = c + 2 >= lo && c + 2 < hi ? x1.x : -INFINITY, x1.y = c + 3 >= lo && c + 3 < hi ? x1.y : -INFINITY;
+                        for (int e = 0; e < 4; ++e) {
+                            const uint4 u = *reinterpret_cast<const uint4*>(key + (q >> 1) * kWtPanel +
+                                                                            (((4 * (q & 1) + e) ^ (tid & 7)) << 4));
+                            v[4 * e] = u.x, v[4 * e + 1] = u.y, v[4 * e + 2] = u.z, v[4 * e + 3] = u.w;
+                        }
+                        tmem_st16(lanes + kWtColK + 64 * i + 16 * q, v);
+                    }
+                    tc::fence_proxy_async_smem();  // (read before the stage's queries come)
+                    tc::tmem_wait_st();
+                }
+                tc::tc_fence_before();
+                __syncwarp();
+                if (lane == 0) tc::mbar_arrive(kbar);
+            }
+            float sum = 0.f;
+            for (int j = 0; j < (i < tiles ? it.steps : 0); ++j) {
+                const int t0 = it.first + 2 * j * per, p_last = p - lane + 31;
+                float2 s0 = make_float2(0.f, 0.f), s1 = s0;
+                // The step's sum; kPart: some of its pairs do not see some of the warp's positions. (Code of its
+                // own: asked for every pair, or between the 32s, of every step, that cost them all a quarter.)
+                auto add_step = [&](auto kPart) -> bool {
+                    constexpr bool kAsk = decltype(kPart)::value;
+                    const int n = kAsk ? filled(it, j) : 2;
+#pragma unroll
+                    for (int h = 0; h < 2; ++h) {
+                        if (kAsk && h == n) break;
+                        const int m = done + h * tiles + i, b = m % kWtBuffers;  // the product
+                        const uint32_t tD = lanes + 128 * b;
+                        if (!warp_ok(dfull + b, (uint32_t)(m / kWtBuffers) & 1u)) return false;
+                        tc::tc_fence_after();
+                        float v[2][32];
+                        tmem_ld32(tD, v[0]);
+#pragma unroll
+                        for (int q = 0; q < 4; ++q) {
+                            const int at = q & 1;
+                            tc::tmem_wait_ld();
+                            if (q < 3) {
+                                tmem_ld32(tD + 32 * (q + 1), v[at ^ 1]);
+                            } else {  // the buffer is read
+                                tc::tc_fence_before();
+                                __syncwarp();
+                                if (lane == 0) tc::mbar_arrive(dempty + b);
                             }
-                            s0 = add2(s0, make_float2(ex2_approx(x0.x), ex2_approx(x0.y)));
-                            s1 = add2(s1, make_float2(ex2_approx(x1.x), ex2_approx(x1.y)));
+                            // pairs lo .. hi - 1 of these 32 see the position
+                            const int t = t0 + h * per, hi = min(x.n - t, per) * R - 32 * q;
+                            const int lo = (p - x.before - t) * R - 32 * q, lo0 = lo - lane * R;
+                            if (kAsk && (hi <= 0 || lo0 >= 32)) continue;  // none of the warp's
+#pragma unroll
+                            for (int e = 0; e < 8; ++e) {
+                                float2 x0 = mul2(make_float2(v[at][4 * e], v[at][4 * e + 1]), c2);
+                                float2 x1 = mul2(make_float2(v[at][4 * e + 2], v[at][4 * e + 3]), c2);
+                                if (kAsk) {
+                                    const int c = 4 * e;
+                                    x0.x = c >= lo && c < hi ? x0.x : -INFINITY, x0.y = c + 1 >= lo && c + 1 < hi ? x0.y : -INFINITY;
+                                    x1.x = c + 2 >= lo && c + 2 < hi ? x1.x : -INFINITY, x1.y = c + 3 >= lo && c + 3 < hi ? x1.y : -INFINITY;
+                                }
+                                s0 = add2(s0, make_float2(ex2_approx(x0.x), ex2_approx(x0.y)));
+                                s1 = add2(s1, make_float2(ex2_approx(x1.x), ex2_approx(x1.y)));
+                            }
                         }
                     }
-                }
-                done += n * tiles;
-                return true;
-            };
-            const bool part = p_last - x.before > t0 || x.n < t0 + 2 * per;  // (the same in the whole warp)
-            if (!(part ? add_step(std::true_type()) : add_step(std::false_type()))) break;
-            sum += (s0.x + s0.y) + (s1.x + s1.y);  // (a step's terms first, then the steps: no long chain of roundings)
-        }
-        if (p < total) w.acc_out[head + p] = (p < x.before ? w.acc[head + p] : 0.f) + sum;
+                    done += n * tiles;
+                    return true;
+                };
+                const bool part = p_last - x.before > t0 || x.n < t0 + 2 * per;  // (the same in the whole warp)
+                if (!(part ? add_step(std::true_type()) : add_step(std::false_type()))) break;
+                sum += (s0.x + s0.y) + (s1.x + s1.y);  // (a step's terms first, then the steps: no long chain of roundings)
+            }
+            if (p < total) w.acc_out[head + p] = (p < x.before ? w.acc[head + p] : 0.f) + sum;
+        });
     }
     __syncwarp();
     tc::tc_fence_before();
@@ -359,7 +405,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         // the copies in flight must land and every product issued must be done
         // before the tensor memory is freed and the CTA exits (all bounded)
         if (warp == 0 && tc::elect_one()) {
-            if (steps > 0) tc::mbar_wait(kload, 0, 100000000ull);
+            tc::mbar_wait(kload, 0, 100000000ull), tc::mbar_wait(kload, 1, 100000000ull);
             for (int i = 0; i < kWtStages; ++i)
                 tc::mbar_wait(qfull + i, 0, 100000000ull), tc::mbar_wait(qfull + i, 1, 100000000ull);
         } else if (warp == 1 && tc::elect_one()) {
@@ -374,7 +420,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 }  // namespace
 
 cudaError_t launch_attn_weights_tiles(const PromptArgs& a, const PromptSums& w, cudaStream_t st) {
-    cudaError_t e = cudaFuncSetAttribute(attn_weights_tile_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, (int)WtSmem::kBytes);
+    cudaError_t e = allow_shared<1>((const void*)attn_weights_tile_kernel, (int)WtSmem::kBytes);
     if (e != cudaSuccess) return e;
     const int R = a.Hq / a.Hkv, per = 128 / R;
     CUtensorMap tmq, tmk;
@@ -383,8 +429,10 @@ cudaError_t launch_attn_weights_tiles(const PromptArgs& a, const PromptSums& w, 
     e = make_rows_map(a.q, a.Hq, a.rows > 0 ? a.rows : 1, row, (unsigned long long)a.q_stride * 2, R, per, &tmq);
     if (e == cudaSuccess) e = make_rows_map(a.k_cache, a.Tmax, (unsigned long long)a.S * a.Hkv, row, row * a.Tmax, kWtPos, 1, &tmk);
     if (e != cudaSuccess) return e;
-    const long blocks = (long)((a.Tmax + 2 * kWtPos - 1) / (2 * kWtPos)) * a.Hkv * a.S;
-    return launch_pdl(attn_weights_tile_kernel, dim3((unsigned)blocks), dim3(kWtThreads), WtSmem::kBytes, st, a, w, tmq, tmk);
+    // A CTA a tile of positions while that is some four an SM; past that, where many tiles of many sessions
+    // may lie behind their last positions, a CTA takes every n-th of a (session, kv head).
+    const long heads = (long)a.Hkv * a.S, tiles = (a.Tmax + 2 * kWtPos - 1) / (2 * kWtPos), most = (4 * 152 + heads - 1) / heads;
+    return launch_pdl(attn_weights_tile_kernel, dim3((unsigned)(heads * (tiles < most ? tiles : most))), dim3(kWtThreads), WtSmem::kBytes, st, a, w, tmq, tmk);
 }
 
 }  // namespace m2

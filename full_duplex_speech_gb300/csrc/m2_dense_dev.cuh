@@ -1,6 +1,8 @@
 // Device helpers shared by the kernels over packed prompts and dense caches.
 #pragma once
 
+#include <atomic>
+
 #include "m2_common.cuh"
 #include "m2_dense.h"
 #include "m2_launch.h"
@@ -61,6 +63,21 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, int per, int x, i
 inline long most_tiles(int S, int rows, int per) {
     const long n = (long)rows / per + S;
     return n < rows ? n : rows;
+}
+
+// Lets a kernel have `bytes` of dynamic shared memory, once per device. (A key of
+// its own for each kernel: the function's type is not one.)
+template <int kKernel>
+inline cudaError_t allow_shared(const void* kernel, int bytes) {
+    static std::atomic<uint64_t> done{0};  // a bit a device
+    int dev = 0;
+    cudaError_t e = cudaGetDevice(&dev);
+    if (e != cudaSuccess) return e;
+    const uint64_t bit = 1ull << (dev & 63);
+    if (done.load(std::memory_order_acquire) & bit) return cudaSuccess;
+    e = cudaFuncSetAttribute(kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, bytes);
+    if (e == cudaSuccess) done.fetch_or(bit, std::memory_order_release);
+    return e;
 }
 
 // bf16 rows of 128 dims as [outer][middle][128]; a box is 64 dims x box_mid x

@@ -267,7 +267,7 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictArgs a, int W
 cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t st) {
     const bool in_place = a.k == a.k_out || a.acc == a.acc_out;
     const int staged = a.Tmax < kEvStaged ? a.Tmax : kEvStaged;
-    const cudaError_t e = cudaFuncSetAttribute(kv_evict_kernel, cudaFuncAttributeMaxDynamicSharedMemorySize, kEvStaged * 4);
+    const cudaError_t e = allow_shared<3>((const void*)kv_evict_kernel, kEvStaged * 4);
     if (e != cudaSuccess) return e;
     // CTAs a (session, kv head): in place while the 152 SMs hold them at once, two an SM. Out of place one
     // an SM where there are few (each chooses by itself, which takes as long as moving 400 rows: one

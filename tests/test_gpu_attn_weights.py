@@ -259,3 +259,24 @@ def test_prompt_scales(m2, act, scale):
     p.weigh(acc, out, 1000)
     _done(m2)
     _check_prompt(c, p, acc, out, 1000)
+
+
+@pytest.mark.parametrize("before,new,window", [(0, 700, 10000), (500, 40, 33), (0, 1, 1), (3, 530, 64)])
+def test_many_sessions_and_long_caches(m2, before, new, window):
+    """More (session, kv head)s than CTAs: a CTA takes several tiles of positions, of sessions that end anywhere."""
+    import torch
+    rng = np.random.default_rng(new)
+    S = 90
+    b = rng.integers(0, before + 1, S).tolist()
+    n = rng.integers(0, new + 1, S).tolist()
+    b[0], n[0], b[1], n[2] = before, new, 0, 0
+    c = Caches(m2, b, 8, 8, "bf16", 1300, seed=24)
+    p = Packed(c, n, lead=1)
+    p.attend()
+    acc = _acc(c)
+    out = torch.full_like(acc, -7.0)
+    p.weigh(acc, out, window)
+    _done(m2)
+    _check_prompt(c, p, acc, out, window, sessions=list(range(0, S, 7)) + [1, 2])
+    for s in range(S):
+        assert torch.all(out[s, :, b[s] + n[s]:] == -7)
