@@ -270,15 +270,17 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t st) {
     const cudaError_t e = allow_shared<3>((const void*)kv_evict_kernel, kEvStaged * 4);
     if (e != cudaSuccess) return e;
     // CTAs a (session, kv head): in place while the 152 SMs hold them at once, two an SM. Out of place one
-    // an SM where there are few (each chooses by itself, which takes as long as moving 400 rows: one
-    // session of 7,500 positions 17.5 us with 19 a head, 19.1 with 38, 29.9 with 59), two a head where
-    // there are many (64 sessions: 161 us, 177 with one, 163 with three).
+    // an SM for a single session (each CTA chooses by itself, which takes as long as moving 400 rows: 7,500
+    // positions 17.5 us with 19 a head, 19.1 with 38, 29.9 with 59); several sessions differ in length, and
+    // more CTAs even that out (16 sessions of up to 7,500 to 2048: 56 us with two a head, 47, 51 and 53 with
+    // three, four and six), up to two a head where there are many (64 sessions: 161 us, 177 with one, 163
+    // with three).
     int W = 1;
     const long pairs = (long)a.S * a.Hkv;
     if (in_place) {
         while (W < kEvMaxW && pairs * 2 * W <= 2 * 152) W *= 2;
     } else {
-        const long runs = (a.Tmax + kEvRun - 1) / kEvRun, most = 152 / pairs;
+        const long runs = (a.Tmax + kEvRun - 1) / kEvRun, most = (a.S == 1 ? 152 : 400) / pairs;
         W = (int)(most < 2 ? 2 : most);
         W = (int)(W < runs ? W : runs);
     }
