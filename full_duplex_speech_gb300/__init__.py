@@ -3,8 +3,9 @@ NemotronLabs VoiceChat: causal conv1d + SiLU over x|B|C, softplus dt, and the
 selective state-space recurrence, as a chunked (SSD) scan for full-history
 recompute / prefill and as a single-frame cached step for many sessions; and
 around it the gated output norm, the 4-bit projections, the cached decode of
-the model's grouped-query attention layers, and a paged 8-bit cache with the
-attention that reads it.
+the model's grouped-query attention layers, a paged 8-bit cache with the
+attention that reads it, and whole prompts, accumulated attention weights and
+eviction for the dense caches.
 
 Every step of the computation runs in the CUDA kernels of libmamba2.so
 (C ABI: include/mamba2.h). This package only marshals arguments: torch

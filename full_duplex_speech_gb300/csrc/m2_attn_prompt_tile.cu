@@ -29,16 +29,17 @@
 // its copies run ahead: the next rows' queries, keys and values are under way
 // while the softmax and the output of the last chunk still run. Outputs leave by way
 // of a piece of the ring a tile. A tile's softmax goes on to the next rows by itself.
-// (With a CTA started for each pair of tiles, 535 us of the size below, 487 so.)
+// (With a CTA started for each pair of tiles, 535 us of the size below, 490 so.)
 //
 // Where few pairs would leave SMs idle, W CTAs of a cluster share the positions
 // of one pair of tiles and merge through distributed shared memory; they take one
 // pair each.
-//   Measured: 4 sessions of 4096 rows, 40 query and 8 kv heads, causal, 687 GFLOP: 490
-// us with the append's 24, so 1.47 PFLOP/s (78 % of a bf16 library product's measured
-// rate). A chunk of a pair takes 2,600 cycles: 2 x 1,150 of products (2,050 at their
-// rate; what is left waits for shared memory, which they and the copies read and
-// write for 2,000 cycles), each tile's softmax 1,000 and its hand-overs some 450.
+//   Measured: 4 sessions of 4096 rows, 40 query and 8 kv heads, causal, 687 GFLOP: 492
+// us with the append (24 alone), 1.40 PFLOP/s, 74 % of a bf16 library product's measured
+// rate (524 us in a loop of eager calls of half a second). A chunk of a pair takes 2,600
+// cycles: 2 x 1,150 of products (2,050 at their rate; what is left waits for shared
+// memory, which they and the copies read and write for 2,000 cycles), each tile's
+// softmax 1,000 and its hand-overs some 450.
 #include <math.h>
 
 #include <mutex>

@@ -28,8 +28,8 @@
 // 12 waits for what the next products need while these are issued (an issue lasts as
 // long as the products, and a look at a barrier in shared memory some 200 cycles
 // more: 331 us without it, 287 with).
-//   Measured: 4 sessions of 4096 rows, 40 query and 8 kv heads, all rows, 344 GFLOP: 281
-// us, 1.22 PFLOP/s (65 % of a bf16 library product's measured rate). A step of 256
+//   Measured: 4 sessions of 4096 rows, 40 query and 8 kv heads, all rows, 344 GFLOP: 285
+// us, 1.21 PFLOP/s (64 % of a bf16 library product's measured rate). A step of 256
 // pairs takes 2,650 cycles: 2,300 of products (2,050 without e), and the
 // exponentials' unit is busy for 2,050 of them; a CTA's start and its first steps,
 // which some positions do not see, are another fifth.

@@ -683,7 +683,8 @@ size_t mamba2_attn_paged_workspace_bytes(const m2_kv_cache* c, int T, int n_head
  * Scores, maxima and sums are fp32, out is rounded once; in bf16 a softmax
  *   weight enters its product with the values rounded to bf16 (2^-8 of itself).
  * A value that is not finite makes the outputs of the rows that see it not
- *   finite (in its dim, or NaN in all dims), and no others.
+ *   finite (in its dim, or NaN in all dims), and no others; a key likewise, and
+ *   their lse; a query its own row and head.
  * Errors: M2_EINVAL, M2_ESHAPE, M2_EALIGN, M2_EUNSUPPORTED, M2_ECUDA. A bounded
  *   wait that runs out records 0x101 or 0x102 (mamba2_device_error). Seen only on
  *   the device, in the error word: 0x104, a negative length or positions past
@@ -704,7 +705,9 @@ m2_status mamba2_attn_prompt(int n_sessions, int n_rows, int n_heads, int n_kv_h
  *           kv head g, of exp(scale * q[row][h] . k_cache[s][g][p] - lse[row][h])
  * To be called behind mamba2_attn_prompt with the same arguments, before the
  * caller advances lengths. Other slots of acc_out are left as they were; acc_out
- * may be acc. Sums in fp32.
+ * may be acc. Sums in fp32; in bf16 the scores' sums are cut off, not rounded
+ * (a sum is within some 1e-6 of itself). A key that is not finite makes its own
+ * position's sum not finite, a query or lse those of the positions that it sees.
  * Errors as mamba2_attn_prompt; a session with 0x104 or 0x106 is left out. */
 m2_status mamba2_attn_prompt_weights(int n_sessions, int n_rows, int n_heads, int n_kv_heads, int head_dim, int max_len,
                                      m2_dtype act, const int32_t* row_start, const int32_t* lengths, const void* q,
@@ -763,9 +766,9 @@ int mamba2_last_cuda_error(void);
  * (0 = no error; otherwise the code of the first condition since the last read:
  * 0x101 or 0x102, a bounded wait that ran out; 0x104, a length that does not fit
  * its cache; 0x105, a page number outside the pool; 0x106, packed rows of a
- * session outside the call's). Later conditions are not kept: a call that met several shows the others when it is made again with the
- * first mended. Synchronises `stream`. Returns M2_ECUDA if the read itself
- * fails. */
+ * session outside the call's). Later conditions are not kept: a call that met
+ * several shows the others when it is made again with the first mended.
+ * Synchronises `stream`. Returns M2_ECUDA if the read itself fails. */
 m2_status mamba2_device_error(void* stream, unsigned int* code);
 
 #ifdef __cplusplus
