@@ -29,14 +29,18 @@
 // its copies run ahead: the next rows' queries, keys and values are under way
 // while the softmax and the output of the last chunk still run. Outputs leave by way
 // of a piece of the ring a tile. A tile's softmax goes on to the next rows by itself.
-// (With a CTA started for each pair of tiles, 535 us of the size below, 490 so.)
+// (With a CTA started for each pair of tiles, 535 us of the size below where it then took 490.)
 //
 // Where few pairs would leave SMs idle, W CTAs of a cluster share the positions
 // of one pair of tiles and merge through distributed shared memory; they take one
 // pair each.
-//   Measured: 4 sessions of 4096 rows, 40 query and 8 kv heads, causal, 687 GFLOP: 492
-// us with the append (24 alone), 1.40 PFLOP/s, 74 % of a bf16 library product's measured
-// rate (524 us in a loop of eager calls of half a second). A chunk of a pair takes 2,600
+// The roles' code together does not stay near the SM's instruction caches: what runs
+// every chunk is kept short, and the softmax comes first (with the others first, the
+// mending unrolled by eight and no way past it for most pieces: 490 us, 74 of nine
+// prompts of up to 750 where it now takes 70.5).
+//   Measured: 4 sessions of 4096 rows, 40 query and 8 kv heads, causal, 687 GFLOP: 467
+// us with the append (24 alone), 1.47 PFLOP/s, 78 % of a bf16 library product's measured
+// rate. A chunk of a pair takes 2,600
 // cycles: 2 x 1,150 of products (2,050 at their rate; what is left waits for shared
 // memory, which they and the copies read and write for 2,000 cycles), each tile's
 // softmax 1,000 and its hand-overs some 450.
@@ -404,130 +408,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (warp > 0 && lane == 0) tc::mbar_arrive(passed);
         }
     };
-    if (warp < 4) {
-        regs_down<kRegsFew>();
-        every_pair([&](const PtWork& y, const PtRun& run, int k, int before, int first) {
-            if (warp == 0) {
-                // -------------------------------------------------------- copies
-                if (W == 1 && lane == 0) {
-                    tc::mbar_arrive_expect_tx(next, 16);
-                    ask_next(sm + L::kNext, next);
-                }
-                __syncwarp();
-                // (first what need not wait for this pair's products, then the next pair, then the rest)
-                const int had = k > 0 ? min(kAhead, run.pieces) : 0, soon = min(kPtStages, run.pieces);
-                copy_pieces(y, run, first, had, soon);
-                PtWork z = {-1, 0, 0, 0, 0, 0};
-                if (W == 1) {
-                    good = good && warp_ok(next, (uint32_t)k & 1u);
-                    const int x = good ? answer_next(sm + L::kNext) : -1;
-                    tc::fence_proxy_async_smem();  // (the answer is read before another may come)
-                    __syncwarp();
-                    if (x >= 0) z = find_pair(a, 2 * per, x, &found);
-                    // (where the wait runs out, the others' waits end as soon as that is known: a second
-                    // one sees them pass)
-                    if (k > 0 && !warp_ok(passed, (uint32_t)(k - 1) & 1u)) good = false, tc::mbar_wait(passed, (uint32_t)(k - 1) & 1u);
-                    if (lane == 0) *work(k + 1) = z;
-                    __syncwarp();
-                    pair_known();
-                }
-                copy_pieces(y, run, first, soon, run.pieces);
-                if (z.s >= 0) {
-                    const PtRun then(a, z, per, W, wk);
-                    copy_q(z, then, before + (run.nc > 0));
-                    copy_pieces(z, then, first + run.pieces, 0, min(kAhead, then.pieces));
-                }
-            } else if (warp == 1) {
-                // ------------------------------------------------------ products
-                const bool leader = tc::elect_one();
-                const uint32_t sbase = tc::smem_u32(sm);
-                tile_turns_meet(TileBarriers(), run.nc, run.nc0, run.nc1, [](int) {}, [&](int i, int j) {
-                    const int nci = i ? run.nc1 : run.nc0;
-                    // the last of the tiles that read this chunk (tile 1 takes every one, where there is one)
-                    const bool last = i == 1 || run.nc1 == 0;
-                    tc::tc_fence_after();
-                    if (leader) {
-                        if (j > 0) {  // O += p V of chunk j - 1
-                            const int at = stage(first + 2 * j - 1);
-                            const uint64_t bd = tc::sdesc(sbase + L::kRing + at * kPtTile, kPtPanel, 1024, 2);
-    #pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                tc::mma_bf16_tmem_a(tm + kColO + 128 * i, tm + kColS + 128 * i + 8 * q, bd + (uint64_t)(q * 2048 >> 4),
-                                                    tc::idesc_bf16(kPtRows, kAttnD, 0, 1), (j > 1 || q > 0) ? 1u : 0u);
-                            if (last) tc::mma_commit(empty + at);
-                        }
-                        if (j < nci) {  // S = q K^T of chunk j, over the weights
-                            const int at = stage(first + 2 * j);
-                            const uint64_t ad = tc::sdesc(sbase + L::kQ + i * kPtTile, 0, 1024, 2);
-                            const uint64_t bd = tc::sdesc(sbase + L::kRing + at * kPtTile, 0, 1024, 2);
-    #pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                const uint64_t off = (uint64_t)(((q >> 2) * kPtPanel + (q & 3) * 32) >> 4);
-                                tc::mma_bf16(tm + kColS + 128 * i, ad + off, bd + off, tc::idesc_bf16(kPtRows, kPtPos, 0, 0),
-                                             q > 0 ? 1u : 0u);
-                            }
-                            tc::mma_commit(sfull + i);
-                            if (last) tc::mma_commit(empty + at);
-                            if (last && j == run.nc - 1) tc::mma_commit(qempty);
-                        } else {
-                            tc::mma_commit(ofull + i);
-                        }
-                    }
-                    __syncwarp();
-                });
-            } else if (warp == 2) {
-                // --- waits for the operands from memory on behalf of the products
-                // (after one that gave up, what the products read is there, if not what it should be,
-                // and the CTA's results are dropped)
-                bool here = true;
-                tile_turns_meet(TileBarriers(), run.nc, run.nc0, run.nc1, [&](int j) {
-                    if (j == 0 && run.nc > 0) here = here && warp_ok(qfull, (uint32_t)before & 1u);
-                    if (j < run.nc) here = here && warp_ok(ready + stage(first + 2 * j), phase(first + 2 * j));
-                    if (j > 0) here = here && warp_ok(ready + stage(first + 2 * j - 1), phase(first + 2 * j - 1));
-                }, [](int, int) {});
-            } else {
-                // ---------------------------- what has landed, looked over in turn
-                uint32_t* bads = bad_of(k);
-                if (lane < kPtBad) bads[lane] = 0u;
-                __syncwarp();
-                for (int p = 0; p < run.pieces; ++p) {
-                    const int at = stage(first + p), c = run.cb + (p >> 1);
-                    if (!warp_ok(full + at, phase(first + p))) break;
-                    if ((p & 1) && p < 2 * run.nc && c >= run.cut) {
-                        // positions of the chunk from `from` on are not seen by every row, and there is nothing from
-                        // `left` on; lanes 0 .. 15 have the 16 pieces of a position, 16 .. 31 of the next
-                        const int from = max(run.all - c * kPtPos, 0), left = min(run.total - c * kPtPos, kPtPos);
-                        uint32_t* bad = bads + 4 * (c - run.cut);
-                        uint8_t* mine = sm + L::kRing + at * kPtTile + (lane & 7) * 16 + ((lane >> 3) & 1) * kPtPanel;
-                        for (int p0 = from + (lane >> 4); p0 < left; p0 += 16) {
-                            uint4 w[8];
-    #pragma unroll
-                            for (int q = 0; q < 8; ++q)
-                                if (p0 + 2 * q < left) w[q] = *reinterpret_cast<const uint4*>(mine + (p0 + 2 * q) * 128);
-    #pragma unroll
-                            for (int q = 0; q < 8; ++q) {
-                                if (p0 + 2 * q >= left) break;
-                                const uint32_t u[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
-                                bool off = false;
-    #pragma unroll
-                                for (int e = 0; e < 4; ++e) off |= (u[e] & 0x7F80u) == 0x7F80u || (u[e] & 0x7F800000u) == 0x7F800000u;
-                                if (off) {
-                                    *reinterpret_cast<uint4*>(mine + (p0 + 2 * q) * 128) = make_uint4(0u, 0u, 0u, 0u);
-                                    atomicOr(bad + ((p0 + 2 * q) >> 5), 1u << ((p0 + 2 * q) & 31));
-                                    bads[kPtBad - 1] = 1u;
-                                }
-                            }
-                        }
-                        for (int q = left + (lane >> 4); q < kPtPos; q += 2)
-                            *reinterpret_cast<uint4*>(mine + q * 128) = make_uint4(0u, 0u, 0u, 0u);
-                        tc::fence_proxy_async_smem();
-                    }
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(ready + at);
-                }
-            }
-        });
-    } else {
+    if (warp >= 4) {
         regs_up<kRegsMany>();
         int chunks = 0, walks = 0;  // of the tile so far
         const int i = (warp - 4) >> 2, r = tid - 128 - 128 * i;  // tile, row of it
@@ -691,7 +572,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     __syncwarp();
                     const size_t to_row = packed * a.out_stride + (size_t)(y.g * R + head) * kAttnD;
                     const unsigned lives = __ballot_sync(0xffffffffu, live);
-#pragma unroll 4
+#pragma unroll 1
                     for (int e = 0; e < 16; ++e) {
                         const int rr = 2 * e + (lane >> 4), col = lane & 15;
                         const size_t to = __shfl_sync(0xffffffffu, to_row, rr);
@@ -730,6 +611,134 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             if (!run.ok && tid == 128) record_error(a.err, ERR_ATTN_LENGTH);
         });
         left();
+        } else {
+        regs_down<kRegsFew>();
+        every_pair([&](const PtWork& y, const PtRun& run, int k, int before, int first) {
+            if (warp == 0) {
+                // -------------------------------------------------------- copies
+                if (W == 1 && lane == 0) {
+                    tc::mbar_arrive_expect_tx(next, 16);
+                    ask_next(sm + L::kNext, next);
+                }
+                __syncwarp();
+                // (first what need not wait for this pair's products, then the next pair, then the rest)
+                const int had = k > 0 ? min(kAhead, run.pieces) : 0, soon = min(kPtStages, run.pieces);
+                copy_pieces(y, run, first, had, soon);
+                PtWork z = {-1, 0, 0, 0, 0, 0};
+                if (W == 1) {
+                    good = good && warp_ok(next, (uint32_t)k & 1u);
+                    const int x = good ? answer_next(sm + L::kNext) : -1;
+                    tc::fence_proxy_async_smem();  // (the answer is read before another may come)
+                    __syncwarp();
+                    if (x >= 0) z = find_pair(a, 2 * per, x, &found);
+                    // (where the wait runs out, the others' waits end as soon as that is known: a second
+                    // one sees them pass)
+                    if (k > 0 && !warp_ok(passed, (uint32_t)(k - 1) & 1u)) good = false, tc::mbar_wait(passed, (uint32_t)(k - 1) & 1u);
+                    if (lane == 0) *work(k + 1) = z;
+                    __syncwarp();
+                    pair_known();
+                }
+                copy_pieces(y, run, first, soon, run.pieces);
+                if (z.s >= 0) {
+                    const PtRun then(a, z, per, W, wk);
+                    copy_q(z, then, before + (run.nc > 0));
+                    copy_pieces(z, then, first + run.pieces, 0, min(kAhead, then.pieces));
+                }
+            } else if (warp == 1) {
+                // ------------------------------------------------------ products
+                const bool leader = tc::elect_one();
+                const uint32_t sbase = tc::smem_u32(sm);
+                tile_turns_meet(TileBarriers(), run.nc, run.nc0, run.nc1, [](int) {}, [&](int i, int j) {
+                    const int nci = i ? run.nc1 : run.nc0;
+                    // the last of the tiles that read this chunk (tile 1 takes every one, where there is one)
+                    const bool last = i == 1 || run.nc1 == 0;
+                    tc::tc_fence_after();
+                    if (leader) {
+                        if (j > 0) {  // O += p V of chunk j - 1
+                            const int at = stage(first + 2 * j - 1);
+                            const uint64_t bd = tc::sdesc(sbase + L::kRing + at * kPtTile, kPtPanel, 1024, 2);
+    #pragma unroll
+                            for (int q = 0; q < 8; ++q)
+                                tc::mma_bf16_tmem_a(tm + kColO + 128 * i, tm + kColS + 128 * i + 8 * q, bd + (uint64_t)(q * 2048 >> 4),
+                                                    tc::idesc_bf16(kPtRows, kAttnD, 0, 1), (j > 1 || q > 0) ? 1u : 0u);
+                            if (last) tc::mma_commit(empty + at);
+                        }
+                        if (j < nci) {  // S = q K^T of chunk j, over the weights
+                            const int at = stage(first + 2 * j);
+                            const uint64_t ad = tc::sdesc(sbase + L::kQ + i * kPtTile, 0, 1024, 2);
+                            const uint64_t bd = tc::sdesc(sbase + L::kRing + at * kPtTile, 0, 1024, 2);
+    #pragma unroll
+                            for (int q = 0; q < 8; ++q) {
+                                const uint64_t off = (uint64_t)(((q >> 2) * kPtPanel + (q & 3) * 32) >> 4);
+                                tc::mma_bf16(tm + kColS + 128 * i, ad + off, bd + off, tc::idesc_bf16(kPtRows, kPtPos, 0, 0),
+                                             q > 0 ? 1u : 0u);
+                            }
+                            tc::mma_commit(sfull + i);
+                            if (last) tc::mma_commit(empty + at);
+                            if (last && j == run.nc - 1) tc::mma_commit(qempty);
+                        } else {
+                            tc::mma_commit(ofull + i);
+                        }
+                    }
+                    __syncwarp();
+                });
+            } else if (warp == 2) {
+                // --- waits for the operands from memory on behalf of the products
+                // (after one that gave up, what the products read is there, if not what it should be,
+                // and the CTA's results are dropped)
+                bool here = true;
+                tile_turns_meet(TileBarriers(), run.nc, run.nc0, run.nc1, [&](int j) {
+                    if (j == 0 && run.nc > 0) here = here && warp_ok(qfull, (uint32_t)before & 1u);
+                    if (j < run.nc) here = here && warp_ok(ready + stage(first + 2 * j), phase(first + 2 * j));
+                    if (j > 0) here = here && warp_ok(ready + stage(first + 2 * j - 1), phase(first + 2 * j - 1));
+                }, [](int, int) {});
+            } else {
+                // ---------------------------- what has landed, looked over in turn
+                uint32_t* bads = bad_of(k);
+                if (lane < kPtBad) bads[lane] = 0u;
+                __syncwarp();
+                for (int p = 0; p < run.pieces; ++p) {
+                    const int at = stage(first + p), c = run.cb + (p >> 1);
+                    if (!warp_ok(full + at, phase(first + p))) break;
+                    if (c < run.cut) {  // most of them: nothing to do
+                        if (lane == 0) tc::mbar_arrive(ready + at);
+                        continue;
+                    }
+                    if ((p & 1) && p < 2 * run.nc) {
+                        // positions of the chunk from `from` on are not seen by every row, and there is nothing from
+                        // `left` on; lanes 0 .. 15 have the 16 pieces of a position, 16 .. 31 of the next
+                        const int from = max(run.all - c * kPtPos, 0), left = min(run.total - c * kPtPos, kPtPos);
+                        uint32_t* bad = bads + 4 * (c - run.cut);
+                        uint8_t* mine = sm + L::kRing + at * kPtTile + (lane & 7) * 16 + ((lane >> 3) & 1) * kPtPanel;
+                        for (int p0 = from + (lane >> 4); p0 < left; p0 += 4) {
+                            uint4 w[2];
+    #pragma unroll
+                            for (int q = 0; q < 2; ++q)
+                                if (p0 + 2 * q < left) w[q] = *reinterpret_cast<const uint4*>(mine + (p0 + 2 * q) * 128);
+    #pragma unroll
+                            for (int q = 0; q < 2; ++q) {
+                                if (p0 + 2 * q >= left) break;
+                                const uint32_t u[4] = {w[q].x, w[q].y, w[q].z, w[q].w};
+                                bool off = false;
+    #pragma unroll
+                                for (int e = 0; e < 4; ++e) off |= (u[e] & 0x7F80u) == 0x7F80u || (u[e] & 0x7F800000u) == 0x7F800000u;
+                                if (off) {
+                                    *reinterpret_cast<uint4*>(mine + (p0 + 2 * q) * 128) = make_uint4(0u, 0u, 0u, 0u);
+                                    atomicOr(bad + ((p0 + 2 * q) >> 5), 1u << ((p0 + 2 * q) & 31));
+                                    bads[kPtBad - 1] = 1u;
+                                }
+                            }
+                        }
+    #pragma unroll 1
+                        for (int q = left + (lane >> 4); q < kPtPos; q += 2)
+                            *reinterpret_cast<uint4*>(mine + q * 128) = make_uint4(0u, 0u, 0u, 0u);
+                        tc::fence_proxy_async_smem();
+                    }
+                    __syncwarp();
+                    if (lane == 0) tc::mbar_arrive(ready + at);
+                }
+            }
+        });
     }
     if (warp == 0 && !appended) pdl_wait();
     __syncthreads();

@@ -249,3 +249,22 @@ def test_offsets_past_32_bits(m2):
             # a weight may be rounded to 2^-8 of itself, and 1e-4 for fp32 scores and sums
             mag = (w[:, None] * v[:t + 1].view(-1, Hkv, D)[:, h // 5].abs()).sum(0) / total
             assert torch.all((got - want).abs() <= (2 ** -8 + 1e-4) * mag + 2 ** -8 * want.abs())
+
+
+@pytest.mark.parametrize("before", [0, 1, 127, 128, 129, 255, 256])
+@pytest.mark.parametrize("new", [1, 49, 50, 51, 127, 128, 129, 257])
+def test_appended_whatever_lies_around(m2, before, new):
+    """Every new row in the caches bit for bit, NaN and infinities among them, and no slot more: one to three
+    sessions, whose rows' chunks begin anywhere in a tile."""
+    import torch
+    c = Caches(m2, [before, 3, before], 10, 2, "bf16", before + new + 5, seed=70)
+    p = Packed(c, [new, 2, max(0, new - 40)], lead=1, tail=1)
+    p.k[2, 5], p.v[1 + new // 2, 200], p.v[new, 3] = math.nan, math.inf, -math.inf
+    p.attend()
+    _done(m2)
+    for s in range(3):
+        b, n = c.before[s], p.new[s]
+        for cache, rows in ((c.kc, p.k), (c.vc, p.v)):
+            want = rows[p.mine(s), :2 * D].reshape(n, 2, D).transpose(0, 1).contiguous()
+            assert torch.equal(cache[s, :, b:b + n].contiguous().view(torch.uint8), want.view(torch.uint8))
+            assert torch.isnan(cache[s, :, b + n:]).all()
