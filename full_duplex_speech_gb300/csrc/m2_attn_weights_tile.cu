@@ -28,9 +28,9 @@
 // 12 waits for what the next products need while these are issued (an issue lasts as
 // long as the products, and a look at a barrier in shared memory some 200 cycles
 // more: 331 us without it, 287 with).
-//   Measured: 4 sessions of 4096 rows, 40 query and 8 kv heads, all rows, 344 GFLOP: 285
-// us, 1.21 PFLOP/s (64 % of a bf16 library product's measured rate). A step of 256
-// pairs takes 2,650 cycles: 2,300 of products (2,050 without e), and the
+//   Measured: 4 sessions of 4096 rows, 40 query and 8 kv heads, all rows, 344 GFLOP: 263
+// us, 1.31 PFLOP/s (69 % of a bf16 library product's measured rate). A step of 256
+// pairs took 2,650 cycles when the whole took 284 us: 2,300 of products (2,050 without e), and the
 // exponentials' unit is busy for 2,050 of them; a CTA's start and its first steps,
 // which some positions do not see, are another fifth.
 #include <math.h>
@@ -149,6 +149,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     auto phase = [](int j) { return (uint32_t)(j / kWtStages) & 1u; };
     // a warp: the rows of a stage that no packed row fills
     auto zero_dead = [&](int st) {
+#pragma unroll 1
         for (int i = lane; i < 4 * (128 - per * R) * 8; i += 32) {
             const int row = per * R + (i >> 5);
             *reinterpret_cast<uint4*>(sm + L::kQ + st * kWtStage + (i >> 3 & 3) * kWtPanel + row * 128 + (i & 7) * 16) =
@@ -297,7 +298,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 asm volatile("cp.async.wait_group %0;" ::"n"(kWtRaw - 1) : "memory");
                 if (J + j >= kWtStages) good = good && warp_ok(qempty + at, phase(J + j - kWtStages));
                 if (!good) break;
-#pragma unroll
+#pragma unroll 1
                 for (int e = 0; e < 4; ++e) {
                     const int r = 32 * e + lane;
                     const float z = r < per * R ? raw[(J + j) % kWtRaw * 256 + 32 * e] * by : none;  // (no weight)
@@ -356,7 +357,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 auto add_step = [&](auto kPart) -> bool {
                     constexpr bool kAsk = decltype(kPart)::value;
                     const int n = kAsk ? filled(it, j) : 2;
-#pragma unroll
+#pragma unroll 1  // (twice the code: 284 us of the size above)
                     for (int h = 0; h < 2; ++h) {
                         if (kAsk && h == n) break;
                         const int m = done + h * tiles + i, b = m % kWtBuffers;  // the product
