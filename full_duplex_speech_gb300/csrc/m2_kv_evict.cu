@@ -216,6 +216,8 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictArgs a, int W
         uint8_t* dst = static_cast<uint8_t*>(value ? a.v_out : a.k_out) + to * a.row_bytes + column;
         for (int p0 = q0; p0 < q1; p0 += kEvThreads) {
             const int n = block_list(p0, q1, &seen);
+            float weight = 0.f;
+            if (!in_place && tid < n) weight = acc[sm.list[tid]];
             if (!(rows_stay && done == p0 && n == min(kEvThreads, L - p0))) {  // (nothing left before: already there)
                 for (int i0 = 0; i0 < n; i0 += kEvFlight * at_once) {
                     uint4 v[kEvFlight];
@@ -233,7 +235,7 @@ __global__ void __launch_bounds__(kEvThreads) kv_evict_kernel(EvictArgs a, int W
                 }
             }
             if (!in_place && tid < n) {
-                acc_out[done + tid] = acc[sm.list[tid]];
+                acc_out[done + tid] = weight;
                 if (kept) kept[done + tid] = sm.list[tid];
             }
             done += n;
