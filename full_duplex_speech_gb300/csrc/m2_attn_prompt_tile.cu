@@ -86,7 +86,8 @@ struct PtSmem {
     static_assert(kBytes <= 227 * 1024, "one CTA an SM");
 };
 
-// A pair of tiles: a session (-1: none is left) and its rows, the pair of it, the kv head.
+// A pair of tiles (or one tile, where there are few): a session (-1: none is left) and its rows,
+// the pair of it, the kv head.
 struct PtWork {
     int s, row0, n, before, pair, g;
 };
@@ -209,10 +210,10 @@ struct PtRun {
     int pieces;          // of the ring: K and V of each chunk in turn, and (W == 1) one for each tile's output
     int cut;             // the first of them that is not whole for every row
     bool ok;             // the session's positions fit the cache (otherwise no chunks)
-    __device__ __forceinline__ PtRun(const PromptArgs& a, const PtWork& y, int per, int W, int wk) {
+    __device__ __forceinline__ PtRun(const PromptArgs& a, const PtWork& y, int per, int span, int W, int wk) {
         ok = y.before >= 0 && (long)y.before + y.n <= a.Tmax;
-        t0 = y.pair * 2 * per;
-        row_end = min(t0 + 2 * per, y.n);
+        t0 = y.pair * span;
+        row_end = min(t0 + span, y.n);
         all = y.before + t0 + 1;
         total = y.before + row_end;
         const int total0 = y.before + min(t0 + per, row_end);
@@ -286,7 +287,7 @@ __device__ __forceinline__ void merge_rows(const PromptArgs& a, uint8_t* sm, int
 __global__ void __launch_bounds__(kPtThreads, 1)
     attn_prompt_tile_kernel(PromptArgs a, const __grid_constant__ CUtensorMap tmq, const __grid_constant__ CUtensorMap tmo,
                             const __grid_constant__ CUtensorMap tmk, const __grid_constant__ CUtensorMap tmv,
-                            const __grid_constant__ CUtensorMap tmkn, const __grid_constant__ CUtensorMap tmvn, int W) {
+                            const __grid_constant__ CUtensorMap tmkn, const __grid_constant__ CUtensorMap tmvn, int W, int tiles) {
     using L = PtSmem;
     extern __shared__ uint8_t pt_raw[];
     uint8_t* sm = pt_raw + ((1024u - (tc::smem_u32(pt_raw) & 1023u)) & 1023u);
@@ -299,7 +300,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     auto work = [&](int k) { return reinterpret_cast<PtWork*>(sm + L::kWork + (k & 1) * 32); };  // of the CTA's k-th pair
     const int wk = (int)blockIdx.x % W;
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
-    const int R = a.Hq / a.Hkv, per = kPtRows / R;  // packed rows a tile
+    const int R = a.Hq / a.Hkv, per = kPtRows / R, span = tiles * per;  // packed rows a tile, a pair of tiles
 
     // A bounded wait; the first that runs out stops the CTA's work.
     auto wait_ok = [&](uint64_t* bar, uint32_t parity) -> bool {
@@ -375,10 +376,10 @@ __global__ void __launch_bounds__(kPtThreads, 1)
         // (The kernel before this one is this call's append, which has waited for what came before
         // it: only the caches are its own. They are waited for where they are read, and at the end,
         // so that whoever waits for this kernel has waited for the append too.)
-        const PtWork y = find_pair(a, 2 * per, (int)blockIdx.x / W, &found);
+        const PtWork y = find_pair(a, span, (int)blockIdx.x / W, &found);
         if (lane == 0) *work(0) = y;
         if (y.s >= 0) {
-            const PtRun run(a, y, per, W, wk);
+            const PtRun run(a, y, per, span, W, wk);
             copy_q(y, run, 0);
         }
     } else if (warp == 1) {
@@ -396,7 +397,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     auto every_pair = [&](auto role) {
         PtWork y = *work(0);
         for (int k = 0, q = 0, first = 0; y.s >= 0; ++k) {
-            const PtRun run(a, y, per, W, wk);
+            const PtRun run(a, y, per, span, W, wk);
             role(y, run, k, q, first);
             first += run.pieces;
             q += run.nc > 0;
@@ -630,7 +631,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                     const int x = good ? answer_next(sm + L::kNext) : -1;
                     tc::fence_proxy_async_smem();  // (the answer is read before another may come)
                     __syncwarp();
-                    if (x >= 0) z = find_pair(a, 2 * per, x, &found);
+                    if (x >= 0) z = find_pair(a, span, x, &found);
                     // (where the wait runs out, the others' waits end as soon as that is known: a second
                     // one sees them pass)
                     if (k > 0 && !warp_ok(passed, (uint32_t)(k - 1) & 1u)) good = false, tc::mbar_wait(passed, (uint32_t)(k - 1) & 1u);
@@ -640,7 +641,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 }
                 copy_pieces(y, run, first, soon, run.pieces);
                 if (z.s >= 0) {
-                    const PtRun then(a, z, per, W, wk);
+                    const PtRun then(a, z, per, span, W, wk);
                     copy_q(z, then, before + (run.nc > 0));
                     copy_pieces(z, then, first + run.pieces, 0, min(kAhead, then.pieces));
                 }
@@ -760,7 +761,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     }
     if (warp == 1) tc::tmem_dealloc(tm, 512);
     if (W == 1 || none) return;
-    const PtRun run(a, y, per, W, wk);
+    const PtRun run(a, y, per, span, W, wk);
     tc::cluster_wait();    // (pairs with the arrival at the start)
     tc::cluster_arrive();  // every CTA's rows are in its shared memory ...
     tc::cluster_wait();
@@ -838,7 +839,7 @@ cudaError_t launch_attn_prompt_tiles(const PromptArgs& a, cudaStream_t st) {
     if (e == cudaSuccess) e = make_rows_map(a.v_new, a.Hkv, a.rows, row, (cuuint64_t)a.kv_stride * 2, 1, kPtPos, &tmvn);
     if (e == cudaSuccess) e = make_rows_map(a.out, a.Hq, a.rows, row, (cuuint64_t)a.out_stride * 2, R, per, &tmo);
     if (e != cudaSuccess) return e;
-    const long pairs = most_tiles(a.S, a.rows, 2 * per) * a.Hkv;
+    long pairs = most_tiles(a.S, a.rows, 2 * per) * a.Hkv;
     // CTAs that share a pair's positions: the least time, in chunks (of 1.4 us), with
     // 4 for a CTA's start and end and 2 more for the merge. One session's CTAs are all
     // alike: rounds x a CTA's time. Several sessions are mostly shorter than the caches:
@@ -848,14 +849,20 @@ cudaError_t launch_attn_prompt_tiles(const PromptArgs& a, cudaStream_t st) {
     // the device holds less than the 16 clusters at once; 300 behind 3000: 43, 31, 42, 68;
     // one of 1500: 37, 66, 102, 224.)
     const long reach = a.lens || a.rows > a.Tmax ? a.Tmax : a.rows, chunks = (reach + kPtPos - 1) / kPtPos;
-    int W = 1;
+    int W = 1, at = 0;
     float best = 0.f;
     for (int k = 0, w = 1; k < 4 && (w == 1 || w <= chunks) && setup->held[k] > 0; ++k, w *= 2) {
         const float part = (float)pairs / (float)setup->held[k], walk = (float)((chunks + w - 1) / w), ends = w > 1 ? 6.f : 4.f;
         const float cost = a.S == 1 ? fmaxf(1.f, ceilf(part)) * (walk + ends)
                                     : walk + ends + (part > 1.f ? (part - 0.7f) * (0.3f * walk + ends) : 0.f);
-        if (w == 1 || cost < best) best = cost, W = w;
+        if (w == 1 || cost < best) best = cost, W = w, at = k;
     }
+    // A tile a CTA, not a pair, while that leaves some SMs free: nothing of a chunk waits for the other tile.
+    // (One session of 100: 8.4 us, 10.3 in pairs; of 300 11.2 and 11.9; of 75 behind 7400 31.2 and 32.5; where
+    // they take almost every SM and the next kernel's CTAs wait for them, one of 450: 14.4 and 13.3.)
+    const long single = most_tiles(a.S, a.rows, per) * a.Hkv;
+    const int tiles = single * W <= 130 && single <= setup->held[at] ? 1 : 2;
+    if (tiles == 1) pairs = single;
     cudaLaunchConfig_t cfg = {};
     cfg.gridDim = dim3((unsigned)(W * pairs));
     cfg.blockDim = dim3(kPtThreads);
@@ -870,7 +877,7 @@ cudaError_t launch_attn_prompt_tiles(const PromptArgs& a, cudaStream_t st) {
     attr[1].val.clusterDim.z = 1;
     cfg.attrs = attr;
     cfg.numAttrs = W > 1 ? 2 : 1;
-    return cudaLaunchKernelEx(&cfg, attn_prompt_tile_kernel, a, tmq, tmo, tmk, tmv, tmkn, tmvn, W);
+    return cudaLaunchKernelEx(&cfg, attn_prompt_tile_kernel, a, tmq, tmo, tmk, tmv, tmkn, tmvn, W, tiles);
 }
 
 }  // namespace m2

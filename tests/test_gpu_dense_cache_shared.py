@@ -235,3 +235,47 @@ def test_evictions_from_caches_longer_than_the_staged_keys(m2, S, max_len, lens)
             assert torch.equal(kept[s, h], at.int())
             for now, was in ((ko, k), (vo, v), (ao, acc)):
                 assert torch.equal(now[s, h, :8191], was[s, h, at]) and torch.all(now[s, h, 8191:] == -7)
+
+
+LENGTHS = [1, 2, 25, 26, 49, 50, 51, 75, 76, 100, 101, 127, 128, 129, 130, 255, 256, 257, 300]
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("Hq,Hkv", [(40, 8), (8, 8), (64, 8), (16, 8), (24, 8)])
+@pytest.mark.parametrize("behind", [False, True])
+def test_lengths_of_many_sessions(m2, act, Hq, Hkv, behind):
+    """So many that a CTA takes a pair of tiles: the lengths around the edges of tiles, pairs and chunks."""
+    before = [(37 * i) % 260 if behind else 0 for i in range(len(LENGTHS))]
+    c = Caches(m2, before, Hq, Hkv, act, 600, seed=71)
+    p = Packed(c, LENGTHS, lead=3, tail=2)
+    p.attend()
+    _done(m2)
+    p.check()
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("place", [0, 0.5, 0.9])
+@pytest.mark.parametrize("what", [math.nan, math.inf])
+def test_values_that_are_not_finite_in_many_sessions(m2, act, place, what):
+    """One value of each session; the rows that do not see it keep their bits, and the caches have it."""
+    import torch
+    outs = []
+    for bad in (False, True):
+        c = Caches(m2, [(41 * i) % 200 for i in range(len(LENGTHS))], 40, 8, act, 600, seed=72)
+        p = Packed(c, LENGTHS)
+        at = [p.starts[s] + int(place * (n - 1)) for s, n in enumerate(LENGTHS)]
+        if bad:
+            for row in at:
+                p.v[row, 2 * D + 5] = what  # kv head 2
+        p.attend()
+        _done(m2)
+        outs.append((p.out.view(-1, 40, D).clone(), p.lse.clone()))
+    (clean, lse), (out, lse_bad) = outs
+    assert torch.equal(lse, lse_bad)
+    assert torch.equal(out[:, :10], clean[:, :10]) and torch.equal(out[:, 15:], clean[:, 15:])
+    for s, n in enumerate(LENGTHS):
+        b = c.before[s]
+        assert torch.equal(out[p.starts[s]:at[s], 10:15], clean[p.starts[s]:at[s], 10:15])
+        assert not torch.isfinite(out[at[s]:p.starts[s] + n, 10:15, 5]).any()
+        held = c.vc[s, 2, b + at[s] - p.starts[s], 5].item()
+        assert math.isnan(held) if math.isnan(what) else held == what
