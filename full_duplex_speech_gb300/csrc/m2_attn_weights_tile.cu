@@ -62,7 +62,8 @@ struct WtSmem {
     static constexpr int kBars = 3 * kWtStages + 2 * kWtBuffers + 3;
     static constexpr uint32_t kTmem = kBar + kBars * 8;
     static constexpr uint32_t kFlag = kTmem + 4;
-    static constexpr uint32_t kBytes = kFlag + 4 + 1024;              // + slack to align to 1024
+    static constexpr uint32_t kSum = (kFlag + 4 + 15) / 16 * 16;      // float [256]: the CTA's part of the positions' sums
+    static constexpr uint32_t kBytes = kSum + 2 * kWtPos * 4 + 1024;  // + slack to align to 1024
     static_assert(kBytes <= 227 * 1024, "one CTA an SM");
 };
 
@@ -70,10 +71,11 @@ struct WtSmem {
 // a product.
 __device__ __forceinline__ void products_meet() { asm volatile("barrier.sync 1, 64;" ::: "memory"); }
 
-// grid: n x Hkv x S, a CTA for every n-th tile of 256 positions; the first tiles, which most rows see, first
+// grid: n x Hkv x S x W, a CTA for every n-th tile of 256 positions; the first tiles, which most rows see, first.
+// W > 1: a cluster takes a tile, a CTA a run of its steps.
 __global__ void __launch_bounds__(kWtThreads, 1)
     attn_weights_tile_kernel(PromptArgs a, PromptSums w, const __grid_constant__ CUtensorMap tmq,
-                             const __grid_constant__ CUtensorMap tmk) {
+                             const __grid_constant__ CUtensorMap tmk, int W) {
     using L = WtSmem;
     extern __shared__ uint8_t wt_raw[];
     uint8_t* sm = wt_raw + ((1024u - (tc::smem_u32(wt_raw) & 1023u)) & 1023u);
@@ -84,9 +86,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     volatile uint32_t* flag = reinterpret_cast<uint32_t*>(sm + L::kFlag);
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5;
     const int R = a.Hq / a.Hkv, per = 128 / R;  // packed rows a tile of pairs
-    const int heads = a.Hkv * a.S, stride = gridDim.x / heads;  // tiles of 256 positions: this CTA's first, and from one to the next
-    const int tile0 = blockIdx.x / heads;
-    const int g = blockIdx.x % heads % a.Hkv, s = blockIdx.x % heads / a.Hkv;
+    const int heads = a.Hkv * a.S, stride = gridDim.x / W / heads;  // tiles of 256 positions: this CTA's first, and from one to the next
+    const int wk = blockIdx.x % W, block = blockIdx.x / W, tile0 = block / heads;
+    const int g = block % heads % a.Hkv, s = block % heads / a.Hkv;
 
     if (tid == 0) prefetch_map(&tmq), prefetch_map(&tmk);
     pdl_wait();
@@ -166,7 +168,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         Item it;
         it.p0 = tile * 2 * kWtPos;
         it.first = max(max(0, x.n - w.window), it.p0 - x.before);
-        it.steps = it.first < x.n ? (x.n - it.first + 2 * per - 1) / (2 * per) : 0;
+        const int steps = it.first < x.n ? (x.n - it.first + 2 * per - 1) / (2 * per) : 0, run = (steps + W - 1) / W;
+        it.first += wk * run * 2 * per;  // this CTA's run of them
+        it.steps = min(max(steps - wk * run, 0), run);
         it.tiles = it.p0 + kWtPos < total ? 2 : 1;
         return it;
     };
@@ -402,7 +406,10 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                 if (!(part ? add_step(std::true_type()) : add_step(std::false_type()))) break;
                 sum += (s0.x + s0.y) + (s1.x + s1.y);  // (a step's terms first, then the steps: no long chain of roundings)
             }
-            if (p < total) w.acc_out[head + p] = (p < x.before ? w.acc[head + p] : 0.f) + sum;
+            if (W > 1)
+                reinterpret_cast<float*>(sm + L::kSum)[tid - 128] = sum;
+            else if (p < total)
+                w.acc_out[head + p] = (p < x.before ? w.acc[head + p] : 0.f) + sum;
         });
     }
     __syncwarp();
@@ -422,6 +429,18 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         __syncthreads();
     }
     if (warp == 1) tc::tmem_dealloc(tm, 512);
+    if (W == 1) return;
+    tc::cluster_arrive();  // every CTA's sums are in its shared memory ...
+    tc::cluster_wait();
+    // ... and each adds up its share of the positions', in order
+    const int share = 2 * kWtPos / W, p = tile0 * 2 * kWtPos + wk * share + tid;
+    if (tid < share && p < total) {
+        float sum = 0.f;
+        for (int c = 0; c < W; ++c) sum += ld_cluster_f32(tc::cluster_map(tc::smem_u32(sm) + L::kSum + (wk * share + tid) * 4, c));
+        w.acc_out[head + p] = (p < x.before ? w.acc[head + p] : 0.f) + sum;
+    }
+    tc::cluster_arrive();  // nobody leaves while its memory is read
+    tc::cluster_wait();
 }
 
 }  // namespace
@@ -436,10 +455,32 @@ cudaError_t launch_attn_weights_tiles(const PromptArgs& a, const PromptSums& w, 
     e = make_rows_map(a.q, a.Hq, a.rows > 0 ? a.rows : 1, row, (unsigned long long)a.q_stride * 2, R, per, &tmq);
     if (e == cudaSuccess) e = make_rows_map(a.k_cache, a.Tmax, (unsigned long long)a.S * a.Hkv, row, row * a.Tmax, kWtPos, 1, &tmk);
     if (e != cudaSuccess) return e;
-    // A CTA a tile of positions while that is some four an SM; past that, where many tiles of many sessions
-    // may lie behind their last positions, a CTA takes every n-th of a (session, kv head).
-    const long heads = (long)a.Hkv * a.S, tiles = (a.Tmax + 2 * kWtPos - 1) / (2 * kWtPos), most = (4 * 152 + heads - 1) / heads;
-    return launch_pdl(attn_weights_tile_kernel, dim3((unsigned)(heads * (tiles < most ? tiles : most))), dim3(kWtThreads), WtSmem::kBytes, st, a, w, tmq, tmk);
+    // A CTA a tile of positions while that is some four an SM, or two where a tile has a step or two (six sessions
+    // of 75 rows behind up to 3,001, the last 32: 14.7 us, 17.0 with four; four sessions of 4096, all rows: 262
+    // with four, 289 with two); past that, where many tiles of many sessions may lie behind their last positions, a
+    // CTA takes every n-th of a (session, kv head).
+    const long window = w.window < a.rows ? w.window : a.rows, steps = (window + 2 * per - 1) / (2 * per);
+    const long heads = (long)a.Hkv * a.S, reach = a.lens ? a.Tmax : a.rows < a.Tmax ? a.rows : a.Tmax;
+    const long tiles = (reach + 2 * kWtPos - 1) / (2 * kWtPos), most = ((steps > 2 ? 4 : 2) * 152 + heads - 1) / heads;
+    // While the tiles leave most SMs idle, up to four CTAs share a tile's steps (one session of 300, all rows: 10.2
+    // us, 11.8 with two, 16.3 with one; of 600 12.4, 17.8, 25.3; eight were no faster).
+    int W = 1;
+    while (W < 4 && 2 * W <= steps && heads * tiles * 2 * W <= 152) W *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(W * heads * (tiles < 1 ? 1 : tiles < most ? tiles : most)));
+    cfg.blockDim = dim3(kWtThreads);
+    cfg.dynamicSmemBytes = WtSmem::kBytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = W;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = W > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, attn_weights_tile_kernel, a, w, tmq, tmk, W);
 }
 
 }  // namespace m2
