@@ -8,6 +8,7 @@
 #include <math.h>
 
 #include "m2_dense_dev.cuh"
+#include "m2_tc.cuh"
 
 namespace m2 {
 
@@ -81,28 +82,33 @@ struct PfSmem {
     static constexpr int kQ = 0, kK = kQ + kPfRows * kPfPitch, kV = kK + kPfPos * kPfPitch, kP = kV + kPfPos * kAttnD,
                          kBad = kP + kPfRows * (kPfPos + 4), kFind = kBad + 4, kFloats = kFind + kPfThreads / 32 + 4;
     static_assert(2 * (kFloats * 4 + 1024) <= 228 * 1024, "two CTAs an SM");
+    // W > 1, after the walk: the rows' sums over the keys, their (m, l) over the weights
+    static constexpr int kO = kK, kMl = kP;
 };
 
-__global__ void __launch_bounds__(kPfThreads, 2) prompt_f32_kernel(PromptArgs a) {
+// grid W x Hkv x tiles; W > 1: a cluster's CTAs share a tile's positions and merge through
+// distributed shared memory.
+__global__ void __launch_bounds__(kPfThreads, 2) prompt_f32_kernel(PromptArgs a, int W) {
     extern __shared__ __align__(16) float pf[];
     float *sQ = pf + PfSmem::kQ, *sK = pf + PfSmem::kK, *sV = pf + PfSmem::kV, *sP = pf + PfSmem::kP;
     // values that are not finite, a bit a position; for the chunks in turn (one's are still read when the next begins)
     unsigned* sBads = reinterpret_cast<unsigned*>(pf + PfSmem::kBad);
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int R = a.Hq / a.Hkv, per = kPfRows / R;
-    const int g = blockIdx.x % a.Hkv;
+    const int wk = blockIdx.x % W, block = blockIdx.x / W, g = block % a.Hkv;
     const float* q = static_cast<const float*>(a.q);
     float* out = static_cast<float*>(a.out);
     pdl_wait();
     pdl_trigger();
     int s, tile;
-    if (!find_tile(a, per, blockIdx.x / a.Hkv, reinterpret_cast<int*>(pf + PfSmem::kFind), &s, &tile)) return;
+    if (!find_tile(a, per, block / a.Hkv, reinterpret_cast<int*>(pf + PfSmem::kFind), &s, &tile)) return;
     Session x;
     session_of(a, s, &x);
     const int t0 = tile * per, rows = min(per, x.n - t0) * R;
     auto packed = [&](int row) { return (size_t)(x.row0 + t0 + row / R); };
     auto column = [&](int row) { return (size_t)(g * R + row % R) * kAttnD; };
-    if (!x.ok) {
+    if (!x.ok) {  // the whole cluster
+        if (wk > 0) return;
         if (tid == 0) record_error(a.err, ERR_ATTN_LENGTH);
         for (int i = tid; i < rows * kAttnD; i += kPfThreads)
             out[packed(i / kAttnD) * a.out_stride + column(i / kAttnD) + i % kAttnD] = 0.f;
@@ -112,6 +118,8 @@ __global__ void __launch_bounds__(kPfThreads, 2) prompt_f32_kernel(PromptArgs a)
     }
     const int all = x.before + t0 + 1;           // positions that every row sees
     const int total = x.before + t0 + rows / R;  // ... and that the last one does
+    // this CTA's run of positions
+    const int run = ((total + kPfPos - 1) / kPfPos + W - 1) / W * kPfPos, begin = wk * run, end = min(begin + run, total);
     const size_t cache0 = ((size_t)s * a.Hkv + g) * a.Tmax * kAttnD;
     // a warp copies four positions at a time, a lane 16 bytes of each
     auto copy = [&](const void* cache, int p0, float* to, int pitch) {
@@ -126,7 +134,7 @@ __global__ void __launch_bounds__(kPfThreads, 2) prompt_f32_kernel(PromptArgs a)
         if (row < rows) v = *reinterpret_cast<const float4*>(q + packed(row) * a.q_stride + column(row) + d);
         *reinterpret_cast<float4*>(sQ + row * kPfPitch + d) = v;
     }
-    copy(a.k_cache, 0, sK, kPfPitch);
+    if (begin < end) copy(a.k_cache, begin, sK, kPfPitch);
     const float sl2 = a.scale * kLog2e;
     int lim[4];  // the last position that this thread's rows see
     float m[4], l[4];
@@ -140,7 +148,7 @@ __global__ void __launch_bounds__(kPfThreads, 2) prompt_f32_kernel(PromptArgs a)
 #pragma unroll
         for (int e = 0; e < 4; ++e) o[i][e] = make_float2(0.f, 0.f);
     }
-    for (int p0 = 0; p0 < total; p0 += kPfPos) {
+    for (int p0 = begin; p0 < end; p0 += kPfPos) {
         const bool cut = p0 + kPfPos > all;
         unsigned* sBad = sBads + 2 * (p0 / kPfPos & 1);
         asm volatile("cp.async.wait_all;" ::: "memory");  // the keys
@@ -205,7 +213,7 @@ __global__ void __launch_bounds__(kPfThreads, 2) prompt_f32_kernel(PromptArgs a)
             }
         }
         __syncthreads();  // the values, the weights; the keys are read
-        if (p0 + kPfPos < total) copy(a.k_cache, p0 + kPfPos, sK, kPfPitch);
+        if (p0 + kPfPos < end) copy(a.k_cache, p0 + kPfPos, sK, kPfPitch);
         if (cut && (sBad[0] | sBad[1])) {
 #pragma unroll
             for (int i = 0; i < 4; ++i) {
@@ -241,21 +249,75 @@ __global__ void __launch_bounds__(kPfThreads, 2) prompt_f32_kernel(PromptArgs a)
 #pragma unroll
         for (int off = 1; off < 16; off <<= 1) l[i] += __shfl_xor_sync(0xffffffffu, l[i], off);
         const int row = 4 * ty + i;
-        if (row >= rows) continue;
+        if (row >= rows || W > 1) continue;
         float* to = out + packed(row) * a.out_stride + column(row) + 4 * tx;
         const float inv = bad[i] ? NAN : 1.f / l[i];
         *reinterpret_cast<float4*>(to) = make_float4(o[i][0].x * inv, o[i][0].y * inv, o[i][1].x * inv, o[i][1].y * inv);
         *reinterpret_cast<float4*>(to + 64) = make_float4(o[i][2].x * inv, o[i][2].y * inv, o[i][3].x * inv, o[i][3].y * inv);
         if (a.lse && tx == 0) a.lse[packed(row) * a.Hq + g * R + row % R] = fmaf(m[i], kLn2, logf(l[i]));
     }
+    if (W == 1) return;
+    __syncthreads();  // the keys and the weights are read
+#pragma unroll
+    for (int i = 0; i < 4; ++i) {
+        const int row = 4 * ty + i;
+        const float poison = bad[i] ? NAN : 0.f;
+        float* to = pf + PfSmem::kO + row * kAttnD + 4 * tx;
+        *reinterpret_cast<float4*>(to) = make_float4(o[i][0].x + poison, o[i][0].y + poison, o[i][1].x + poison, o[i][1].y + poison);
+        *reinterpret_cast<float4*>(to + 64) =
+            make_float4(o[i][2].x + poison, o[i][2].y + poison, o[i][3].x + poison, o[i][3].y + poison);
+        if (tx == 0) *reinterpret_cast<float2*>(pf + PfSmem::kMl + 2 * row) = make_float2(m[i], l[i]);
+    }
+    tc::cluster_arrive();  // every CTA's rows are in its shared memory ...
+    tc::cluster_wait();
+    // ... and each merges a share of them, a warp a row, four dims a lane
+    const int share = kPfRows / W, lane = tid & 31;
+    const uint32_t base = tc::smem_u32(pf);
+    for (int row = wk * share + (tid >> 5); row < min((wk + 1) * share, rows); row += kPfThreads / 32) {
+        float M = kNone, L = 0.f;
+        for (int w = 0; w < W; ++w)
+            M = fmaxf(M, ld_cluster_f32x2(tc::cluster_map(base + (PfSmem::kMl + 2 * row) * 4, w)).x);
+        float4 sum = make_float4(0.f, 0.f, 0.f, 0.f);
+        for (int w = 0; w < W; ++w) {
+            const float2 ml = ld_cluster_f32x2(tc::cluster_map(base + (PfSmem::kMl + 2 * row) * 4, w));
+            const float4 v = ld_cluster_f32x4(tc::cluster_map(base + (PfSmem::kO + row * kAttnD + 4 * lane) * 4, w));
+            const float f = ex2_approx(ml.x - M);
+            L = fmaf(f, ml.y, L);
+            sum.x = fmaf(f, v.x, sum.x), sum.y = fmaf(f, v.y, sum.y), sum.z = fmaf(f, v.z, sum.z), sum.w = fmaf(f, v.w, sum.w);
+        }
+        const float inv = 1.f / L;
+        *reinterpret_cast<float4*>(out + packed(row) * a.out_stride + column(row) + 4 * lane) =
+            make_float4(sum.x * inv, sum.y * inv, sum.z * inv, sum.w * inv);
+        if (a.lse && lane == 0) a.lse[packed(row) * a.Hq + g * R + row % R] = fmaf(M, kLn2, logf(L));
+    }
+    tc::cluster_arrive();  // nobody leaves while its memory is read
+    tc::cluster_wait();
 }
 
 cudaError_t launch_f32(const PromptArgs& a, cudaStream_t st) {
     constexpr int bytes = PfSmem::kFloats * 4;
     cudaError_t e = allow_shared<0>((const void*)prompt_f32_kernel, bytes);
     if (e != cudaSuccess) return e;
-    const long tiles = most_tiles(a.S, a.rows, kPfRows / (a.Hq / a.Hkv));
-    return launch_pdl(prompt_f32_kernel, dim3((unsigned)(tiles * a.Hkv)), dim3(kPfThreads), bytes, st, a);
+    const long blocks = most_tiles(a.S, a.rows, kPfRows / (a.Hq / a.Hkv)) * a.Hkv;
+    // CTAs that share a tile's positions, while they leave SMs idle (two an SM)
+    const long reach = a.lens || a.rows > a.Tmax ? a.Tmax : a.rows, chunks = (reach + kPfPos - 1) / kPfPos;
+    int W = 1;
+    while (W < 8 && 2 * W <= chunks && blocks * 2 * W <= 2 * 152) W *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(W * blocks));
+    cfg.blockDim = dim3(kPfThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = W;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = W > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, prompt_f32_kernel, a, W);
 }
 
 }  // namespace
