@@ -75,7 +75,9 @@ cudaError_t launch_append(const PromptArgs& a, cudaStream_t st) {
 // copies of a chunk's values run under its scores, those of the next keys under
 // its values. Two CTAs an SM, so that one's products cover the other's barriers
 // (five prompts of up to 301, 12 / 2 heads: 55 us; with 64 rows, 256 threads, one
-// CTA an SM and no copies ahead 70).
+// CTA an SM and no copies ahead 70). As mma.sync products of split operands, 64 rows
+// a CTA (tf32 in two terms, three products, or bf16 in three, six: the same time), four
+// prompts of 600 behind 1,000 took 1,223 us where this takes 1,696, but these 66.
 constexpr int kPfThreads = 128, kPfRows = 32, kPfPos = 64;
 constexpr int kPfPitch = kAttnD + 4;  // floats: a column of 16-byte pieces meets all banks
 struct PfSmem {
@@ -299,7 +301,8 @@ cudaError_t launch_f32(const PromptArgs& a, cudaStream_t st) {
     cudaError_t e = allow_shared<0>((const void*)prompt_f32_kernel, bytes);
     if (e != cudaSuccess) return e;
     const long blocks = most_tiles(a.S, a.rows, kPfRows / (a.Hq / a.Hkv)) * a.Hkv;
-    // CTAs that share a tile's positions, while they leave SMs idle (two an SM)
+    // CTAs that share a tile's positions, while they leave SMs idle (two an SM; 12 / 2 heads, 75 rows behind 7,400
+    // positions: 123 us with eight, 149, 285 and 553 with four, two and one; one row behind 600: 16, 21, 31 and 52)
     const long reach = a.lens || a.rows > a.Tmax ? a.Tmax : a.rows, chunks = (reach + kPfPos - 1) / kPfPos;
     int W = 1;
     while (W < 8 && 2 * W <= chunks && blocks * 2 * W <= 2 * 152) W *= 2;

@@ -8,6 +8,7 @@
 #include <math.h>
 
 #include "m2_dense_dev.cuh"
+#include "m2_tc.cuh"
 
 namespace m2 {
 
@@ -36,14 +37,14 @@ template <typename TA> __device__ __forceinline__ float4 load4(const void* p, si
     }
 }
 
-// grid (position tiles, Hkv, S)
+// grid (position tiles x W, Hkv, S); W > 1: a cluster takes a tile, a CTA a run of its rows.
 template <typename TA>
-__global__ void __launch_bounds__(kWfThreads) weights_fp32_kernel(PromptArgs a, PromptSums w) {
+__global__ void __launch_bounds__(kWfThreads) weights_fp32_kernel(PromptArgs a, PromptSums w, int W) {
     extern __shared__ __align__(16) float wf[];
     float *sQ = wf + WfSmem::kQ, *sK = wf + WfSmem::kK, *sL = wf + WfSmem::kL, *sSum = wf + WfSmem::kSum;
     const int tid = threadIdx.x, tx = tid & 15, ty = tid >> 4;
     const int R = a.Hq / a.Hkv, per = kWfRows / R;
-    const int g = blockIdx.y, s = blockIdx.z, p0 = blockIdx.x * kWfPos;
+    const int g = blockIdx.y, s = blockIdx.z, wk = blockIdx.x % W, p0 = blockIdx.x / W * kWfPos;
     pdl_wait();
     pdl_trigger();
     Session x;
@@ -58,8 +59,12 @@ __global__ void __launch_bounds__(kWfThreads) weights_fp32_kernel(PromptArgs a, 
     const int total = x.before + x.n;
     if (p0 >= total) return;
     const size_t head = ((size_t)s * a.Hkv + g) * a.Tmax;
-    const int first = max(max(0, x.n - w.window), p0 - x.before);  // the first row of the window that sees a position here
-    if (first < x.n)
+    int first = max(max(0, x.n - w.window), p0 - x.before);  // the first row of the window that sees a position here
+    // this CTA's run of the rows, in whole steps
+    const int run = ((max(x.n - first, 0) + per - 1) / per + W - 1) / W * per;
+    first += wk * run;
+    const int end = min(first + run, x.n);
+    if (first < end)
         for (int i = tid; i < kWfPos * kAttnD / 4; i += kWfThreads) {
             const int p = i / (kAttnD / 4), d = i % (kAttnD / 4) * 4;
             float4 k = make_float4(0.f, 0.f, 0.f, 0.f);
@@ -68,7 +73,7 @@ __global__ void __launch_bounds__(kWfThreads) weights_fp32_kernel(PromptArgs a, 
         }
     const float sl2 = a.scale * kLog2e;
     float sum[4] = {0.f, 0.f, 0.f, 0.f};
-    for (int t0 = first; t0 < x.n; t0 += per) {
+    for (int t0 = first; t0 < end; t0 += per) {
         const int rows = min(per, x.n - t0) * R;
         __syncthreads();
         for (int i = tid; i < kWfRows * kAttnD / 4; i += kWfThreads) {
@@ -118,9 +123,23 @@ __global__ void __launch_bounds__(kWfThreads) weights_fp32_kernel(PromptArgs a, 
         float t = 0.f;
 #pragma unroll
         for (int i = 0; i < 16; ++i) t += sSum[i * kWfPos + tid];
-        const float old = p0 + tid < x.before ? w.acc[head + p0 + tid] : 0.f;
-        w.acc_out[head + p0 + tid] = old + t;
+        if (W > 1)
+            sL[tid] = t;
+        else
+            w.acc_out[head + p0 + tid] = (p0 + tid < x.before ? w.acc[head + p0 + tid] : 0.f) + t;
     }
+    if (W == 1) return;
+    tc::cluster_arrive();  // every CTA's sums are in its shared memory ...
+    tc::cluster_wait();
+    // ... and each adds up its share of the positions', in order
+    const int p = wk * (kWfPos / W) + tid;
+    if (tid < kWfPos / W && p0 + p < total) {
+        float t = 0.f;
+        for (int c = 0; c < W; ++c) t += ld_cluster_f32(tc::cluster_map(tc::smem_u32(sL + p), c));
+        w.acc_out[head + p0 + p] = (p0 + p < x.before ? w.acc[head + p0 + p] : 0.f) + t;
+    }
+    tc::cluster_arrive();  // nobody leaves while its memory is read
+    tc::cluster_wait();
 }
 
 template <typename TA>
@@ -128,8 +147,28 @@ cudaError_t launch_fp32(const PromptArgs& a, const PromptSums& w, cudaStream_t s
     constexpr int bytes = WfSmem::kFloats * 4;
     cudaError_t e = allow_shared<sizeof(TA)>((const void*)weights_fp32_kernel<TA>, bytes);
     if (e != cudaSuccess) return e;
-    return launch_pdl(weights_fp32_kernel<TA>, dim3((a.Tmax + kWfPos - 1) / kWfPos, a.Hkv, a.S), dim3(kWfThreads), bytes, st,
-                      a, w);
+    const long reach = a.lens ? a.Tmax : a.rows < a.Tmax ? a.rows : a.Tmax, tiles = reach > 0 ? (reach + kWfPos - 1) / kWfPos : 1;
+    // CTAs that share a tile's rows, while the tiles leave SMs idle (three an SM; one session of 300, all rows, 12 / 2
+    // heads: 31 us with eight, 57, 103 and 200 with four, two and one; 40 / 8 heads 51 with eight, 67 where two an SM
+    // were the limit, 167 with one)
+    const long window = w.window < a.rows ? w.window : a.rows, steps = window * (a.Hq / a.Hkv) / kWfRows;
+    int W = 1;
+    while (W < 8 && 2 * W <= steps && tiles * a.Hkv * a.S * 2 * W <= 3 * 152) W *= 2;
+    cudaLaunchConfig_t cfg = {};
+    cfg.gridDim = dim3((unsigned)(W * tiles), a.Hkv, a.S);
+    cfg.blockDim = dim3(kWfThreads);
+    cfg.dynamicSmemBytes = bytes;
+    cfg.stream = st;
+    cudaLaunchAttribute attr[2];
+    attr[0].id = cudaLaunchAttributeProgrammaticStreamSerialization;
+    attr[0].val.programmaticStreamSerializationAllowed = 1;
+    attr[1].id = cudaLaunchAttributeClusterDimension;
+    attr[1].val.clusterDim.x = W;
+    attr[1].val.clusterDim.y = 1;
+    attr[1].val.clusterDim.z = 1;
+    cfg.attrs = attr;
+    cfg.numAttrs = W > 1 ? 2 : 1;
+    return cudaLaunchKernelEx(&cfg, weights_fp32_kernel<TA>, a, w, W);
 }
 
 }  // namespace
