@@ -34,16 +34,16 @@
 // Where few pairs would leave SMs idle, W CTAs of a cluster share the positions
 // of one pair of tiles and merge through distributed shared memory; they take one
 // pair each.
-// The roles' code together does not stay near the SM's instruction caches: what runs
-// every chunk is kept short, and the softmax comes first (with the others first, the
-// mending unrolled by eight and no way past it for most pieces: 490 us, 74 of nine
-// prompts of up to 750 where it now takes 70.5).
+// Code length alone costs time here, as where instructions do not stay in the nearest
+// caches: what runs every chunk is kept short, and the softmax comes first (with the
+// others first, the mending unrolled by eight and no way past it for most pieces 490 us of
+// the size below and 74 of nine prompts of up to 750, which now take 70.5).
 //   Measured: 4 sessions of 4096 rows, 40 query and 8 kv heads, causal, 687 GFLOP: 467
 // us with the append (24 alone), 1.47 PFLOP/s, 78 % of a bf16 library product's measured
-// rate. A chunk of a pair takes 2,600
-// cycles: 2 x 1,150 of products (2,050 at their rate; what is left waits for shared
-// memory, which they and the copies read and write for 2,000 cycles), each tile's
-// softmax 1,000 and its hand-overs some 450.
+// rate (508 us in a loop of eager calls of half a second). A chunk of a pair took 2,600
+// cycles when the whole took 490 us: 2 x 1,150 of products (2,050 at their rate; what is
+// left waits for shared memory, which they and the copies read and write for 2,000
+// cycles), each tile's softmax 1,000 and its hand-overs some 450.
 #include <math.h>
 
 #include <mutex>
