@@ -49,6 +49,7 @@
 #include <mutex>
 
 #include "m2_dense_dev.cuh"
+#include "m2_prompt_ring.h"
 #include "m2_tc.cuh"
 #include "m2_tile_meet.h"
 
@@ -61,7 +62,7 @@ constexpr int kPtRows = 128;                       // rows of a tile
 constexpr int kPtPos = 128;                        // positions a chunk
 constexpr uint32_t kPtPanel = 128 * 128;           // 128 rows x 64 dims of bf16
 constexpr uint32_t kPtTile = 2 * kPtPanel;
-constexpr int kPtStages = 5;                       // of a chunk's K or V, in turn
+constexpr int kPtStages = kRingStages;             // of a chunk's K or V, in turn
 constexpr float kPtSlack = 8.f;                    // log2 by which a chunk may exceed m
 constexpr int kPtCut = 3;                          // chunks that the tiles' at most 256 packed rows see partly, at most
 constexpr int kPtBad = 4 * kPtCut + 1;
@@ -207,7 +208,7 @@ struct PtRun {
     int all, total;      // positions that every row sees, and that the last one does
     int cb, nc;          // this CTA's run of chunks, cb .. cb + nc - 1
     int nc0, nc1;        // ... of which tile 0 and tile 1 take so many
-    int pieces;          // of the ring: K and V of each chunk in turn, and (W == 1) one for each tile's output
+    int pieces;          // of the ring: K and V of each chunk in turn, and (W == 1) room for each tile's output
     int cut;             // the first of them that is not whole for every row
     bool ok;             // the session's positions fit the cache (otherwise no chunks)
     __device__ __forceinline__ PtRun(const PromptArgs& a, const PtWork& y, int per, int span, int W, int wk) {
@@ -223,7 +224,22 @@ struct PtRun {
         nc0 = ok ? min(max((total0 + kPtPos - 1) / kPtPos - cb, 0), nc) : 0;
         nc1 = row_end > t0 + per ? nc : 0;
         cut = max(all / kPtPos, cb);
-        pieces = 2 * nc + (W > 1 ? 0 : row_end > t0 + per ? 2 : 1);
+        pieces = ring_pieces(nc, W > 1 ? 0 : row_end > t0 + per ? 2 : 1);
+    }
+};
+
+// The CTA's ring as m2_prompt_ring.h sees it; the calling warp is converged.
+template <typename WarpOk> struct PtRing {
+    uint64_t *full, *empty, *ready;
+    WarpOk ok;
+    static __device__ __forceinline__ int at(int piece) { return piece % kPtStages; }
+    static __device__ __forceinline__ uint32_t turn(int piece) { return (uint32_t)(piece / kPtStages) & 1u; }
+    __device__ __forceinline__ bool wait_full(int piece) { return ok(full + at(piece), turn(piece)); }
+    __device__ __forceinline__ bool wait_empty(int piece) { return ok(empty + at(piece), turn(piece)); }
+    __device__ __forceinline__ bool wait_ready(int piece) { return ok(ready + at(piece), turn(piece)); }
+    __device__ __forceinline__ void arrive_ready(int piece) {
+        __syncwarp();
+        if ((threadIdx.x & 31) == 0) tc::mbar_arrive(ready + at(piece));
     }
 };
 
@@ -314,8 +330,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     // the same for a converged warp
     auto warp_ok = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait_ok(bar, parity)); };
     // The ring's pieces, counted over all of the CTA's pairs.
+    PtRing<decltype(warp_ok)> ring{full, empty, ready, warp_ok};
     auto stage = [](int piece) { return piece % kPtStages; };
-    auto phase = [](int piece) { return (uint32_t)(piece / kPtStages) & 1u; };
 
     if (W > 1) tc::cluster_arrive_relaxed();  // waited on before the first remote access: every CTA has started
     bool good = true;                         // warp 0: no wait has run out, and copies may go on
@@ -337,10 +353,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     };
     auto copy_pieces = [&](const PtWork& y, const PtRun& run, int first, int p, int end) {
         if (y.before > 0 && !appended) pdl_wait(), appended = true;
-        for (; p < end; ++p) {
-            const int piece = first + p, at = stage(piece);
-            if (piece >= kPtStages) good = good && warp_ok(empty + at, phase(piece - kPtStages));
-            if (!good) break;
+        good = good && ring_fill(ring, first, p, end, [&](int p) {
+            const int at = stage(first + p);
             if (tc::elect_one()) {
                 if (p >= 2 * run.nc) {  // room for an output
                     tc::mbar_arrive(full + at);
@@ -356,7 +370,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 }
             }
             __syncwarp();
-        }
+        });
     };
     // pieces that are copied before the pair ahead of theirs ends (they wait for nothing of their own pair's)
     constexpr int kAhead = 3;
@@ -536,15 +550,25 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             }
             if (W == 1) {
                 if (run.t0 + i * per >= run.row_end) return;  // the tile has no rows
+                const size_t packed = (size_t)y.row0 + t;
+                if (!run.ok) {  // a refused session has no pieces of the ring: each row's zeros from its own thread
+                    if (tid == 128) record_error(a.err, ERR_ATTN_LENGTH);
+                    if (!live) return;
+                    uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + packed * a.out_stride +
+                                                         (size_t)(y.g * R + head) * kAttnD);
+#pragma unroll 1
+                    for (int e = 0; e < kAttnD / 8; ++e) to[e] = make_uint4(0u, 0u, 0u, 0u);
+                    if (a.lse) a.lse[packed * a.Hq + y.g * R + head] = -INFINITY;
+                    return;
+                }
                 // in bf16 to a piece of the ring, laid out as the queries were; a whole tile leaves by two
                 // copies of a thread, the last of a session two rows at a time (16 lanes a row)
-                // (A wait for a stage's phase needs the one before it to be over: that was a key or value of
-                // this pair that the tile's products have read, or of the pair before.)
+                // (The stage's turn before is over: that was a key or value of this pair that the tile's
+                // products have read, or a piece ahead of one.)
                 const int piece = first + 2 * run.nc + i, at = stage(piece);
-                here = warp_ok(full + at, phase(piece)) && here;
+                here = ring_room(ring, piece) && here;
                 uint8_t* mine = sm + L::kRing + at * kPtTile;
-                const size_t packed = (size_t)y.row0 + t;
-                const float f = run.ok ? 1.f / l + poison : 0.f;
+                const float f = 1.f / l + poison;
 #pragma unroll 1
                 for (int q = 0; q < 4; ++q) {
                     float v[32];
@@ -555,8 +579,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                         uint32_t w[4];
 #pragma unroll
                         for (int h = 0; h < 4; ++h) w[h] = pack_bf16x2(v[e + 2 * h] * f, v[e + 2 * h + 1] * f);
-                        const uint4 x = run.ok ? make_uint4(w[0], w[1], w[2], w[3]) : make_uint4(0u, 0u, 0u, 0u);
-                        *reinterpret_cast<uint4*>(mine + (q >> 1) * kPtPanel + r * 128 + (((4 * (q & 1) + e / 8) ^ (r & 7)) << 4)) = x;
+                        *reinterpret_cast<uint4*>(mine + (q >> 1) * kPtPanel + r * 128 + (((4 * (q & 1) + e / 8) ^ (r & 7)) << 4)) =
+                            make_uint4(w[0], w[1], w[2], w[3]);
                     }
                 }
                 if (live && a.lse) a.lse[packed * a.Hq + y.g * R + head] = fmaf(m, kLn2, logf(l));
@@ -608,8 +632,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                             make_float4(v[4 * e] + poison, v[4 * e + 1] + poison, v[4 * e + 2] + poison, v[4 * e + 3] + poison);
                 }
                 *reinterpret_cast<float2*>(sm + L::kMl + row * 8) = make_float2(m, l);
+                if (!run.ok && tid == 128) record_error(a.err, ERR_ATTN_LENGTH);
             }
-            if (!run.ok && tid == 128) record_error(a.err, ERR_ATTN_LENGTH);
         });
         left();
         } else {
@@ -690,21 +714,17 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 bool here = true;
                 tile_turns_meet(TileBarriers(), run.nc, run.nc0, run.nc1, [&](int j) {
                     if (j == 0 && run.nc > 0) here = here && warp_ok(qfull, (uint32_t)before & 1u);
-                    if (j < run.nc) here = here && warp_ok(ready + stage(first + 2 * j), phase(first + 2 * j));
-                    if (j > 0) here = here && warp_ok(ready + stage(first + 2 * j - 1), phase(first + 2 * j - 1));
+                    if (j < run.nc) here = here && ring.wait_ready(first + 2 * j);
+                    if (j > 0) here = here && ring.wait_ready(first + 2 * j - 1);
                 }, [](int, int) {});
             } else {
                 // ---------------------------- what has landed, looked over in turn
                 uint32_t* bads = bad_of(k);
                 if (lane < kPtBad) bads[lane] = 0u;
                 __syncwarp();
-                for (int p = 0; p < run.pieces; ++p) {
+                ring_look(ring, first, run.pieces, [&](int p) {
                     const int at = stage(first + p), c = run.cb + (p >> 1);
-                    if (!warp_ok(full + at, phase(first + p))) break;
-                    if (c < run.cut) {  // most of them: nothing to do
-                        if (lane == 0) tc::mbar_arrive(ready + at);
-                        continue;
-                    }
+                    if (c < run.cut) return;  // most of them: nothing to do
                     if ((p & 1) && p < 2 * run.nc) {
                         // positions of the chunk from `from` on are not seen by every row, and there is nothing from
                         // `left` on; lanes 0 .. 15 have the 16 pieces of a position, 16 .. 31 of the next
@@ -735,9 +755,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                             *reinterpret_cast<uint4*>(mine + q * 128) = make_uint4(0u, 0u, 0u, 0u);
                         tc::fence_proxy_async_smem();
                     }
-                    __syncwarp();
-                    if (lane == 0) tc::mbar_arrive(ready + at);
-                }
+                });
             }
         });
     }
