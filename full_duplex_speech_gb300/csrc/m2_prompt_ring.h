@@ -48,7 +48,9 @@ M2_RING_FN void ring_look(Ring& ring, int first, int pieces, Look look) {
     }
 }
 
-// A tile's wait for the room of its output, behind its products.
-template <typename Ring> M2_RING_FN bool ring_room(Ring& ring, int piece) { return ring.wait_full(piece); }
+// A tile's wait for the room of its output, behind its products. (For what looks at
+// the pieces to have come by: the tile empties the room by itself, and a look that
+// came after the stage's next piece had landed would wait for its own answer to that.)
+template <typename Ring> M2_RING_FN bool ring_room(Ring& ring, int piece) { return ring.wait_ready(piece); }
 
 }  // namespace m2

@@ -3,7 +3,8 @@
 // barriers that are waited on by parity, as the hardware's are, some of them slow.
 // A wait that passes before its piece's turn is over is a fault, and so is a run
 // that does not end. Prints "ok" and leaves 0 when there is none; `model pieces`
-// gives refused pairs pieces of the ring, as a check that the model sees it.
+// gives refused pairs pieces of the ring, and `model full` lets the tiles wait for no
+// more than their room to be empty, as checks that the model sees them.
 #include <chrono>
 #include <condition_variable>
 #include <cstdio>
@@ -33,7 +34,7 @@ struct Bar {
     int turns = 0;  // that are over
 };
 
-enum Slow { kNobody, kLanding, kLook, kTile0, kTile1, kOperands };
+enum Slow { kNobody, kLanding, kLook, kLookRoom, kTile0, kTile1, kOperands };
 
 struct Run {
     std::mutex mutex;
@@ -102,7 +103,7 @@ static void pause(bool yes) {
 }
 
 // 0: it ended; 1: a wait passed early; 2: it got stuck.
-static int run_of(const std::vector<Pair>& pairs, Slow slow, bool refused_pieces) {
+static int run_of(const std::vector<Pair>& pairs, Slow slow, bool refused_pieces, bool room_full) {
     std::shared_ptr<Run> run(new Run);
     const int count = (int)pairs.size();
     auto pieces_of = [=](const Pair& y) {
@@ -162,7 +163,7 @@ static int run_of(const std::vector<Pair>& pairs, Slow slow, bool refused_pieces
     warps.emplace_back([=] {  // what has landed, looked over
         every_pair([=](const Pair& y, int first) {
             Ring ring{run.get()};
-            m2::ring_look(ring, first, pieces_of(y), [&](int p) { pause(slow == kLook && p < 2 * y.chunks()); });
+            m2::ring_look(ring, first, pieces_of(y), [&](int p) { pause(slow == kLook || (slow == kLookRoom && p >= 2 * y.chunks() - 1)); });
         });
     });
     warps.emplace_back([=] {  // waits for the products' operands
@@ -208,7 +209,10 @@ static int run_of(const std::vector<Pair>& pairs, Slow slow, bool refused_pieces
                 pause(slow == (i ? kTile1 : kTile0));
                 if (pieces_of(y) == 0) return;
                 const int piece = first + 2 * y.chunks() + i;
-                m2::ring_room(ring, piece);
+                if (room_full)
+                    ring.wait_full(piece);
+                else
+                    m2::ring_room(ring, piece);
                 leaving = piece;
             });
             left();
@@ -225,7 +229,7 @@ static int run_of(const std::vector<Pair>& pairs, Slow slow, bool refused_pieces
 }
 
 int main(int argc, char** argv) {
-    const bool pieces = argc > 1 && !std::strcmp(argv[1], "pieces");
+    const bool pieces = argc > 1 && !std::strcmp(argv[1], "pieces"), full = argc > 1 && !std::strcmp(argv[1], "full");
     const Pair refused = {0, 0, true, true}, refused1 = {0, 0, true, false};
     auto pair = [](int n0, int n1) { return Pair{n0, n1, false, n1 > 0}; };
     const std::vector<std::vector<Pair>> runs = {
@@ -239,11 +243,11 @@ int main(int argc, char** argv) {
     int faults = 0;
     for (size_t r = 0; r < runs.size(); ++r)
         for (int slow = kNobody; slow <= kOperands; ++slow) {
-            const int what = run_of(runs[r], (Slow)slow, pieces);
+            const int what = run_of(runs[r], (Slow)slow, pieces, full);
             if (what == 0) continue;
             std::printf("%s: run %d, slow %d\n", what == 1 ? "early" : "stuck", (int)r, slow);
             ++faults;
-            if (pieces) return 2;
+            if (pieces || full) return 2;
         }
     if (!faults) std::printf("ok\n");
     return faults ? 1 : 0;

@@ -35,6 +35,12 @@ def test_the_model_sees_a_wait_that_passes_early(model):
     assert r.returncode == 2 and "early" in r.stdout, r.stdout + r.stderr
 
 
+def test_the_model_sees_a_run_that_gets_stuck(model):
+    """A warp that looks at an output's room only when the stage's next piece has landed waits for its own answer."""
+    r = subprocess.run([model, "full"], capture_output=True, text=True, timeout=200)
+    assert r.returncode == 2 and "stuck" in r.stdout, r.stdout + r.stderr
+
+
 def test_the_kernel_uses_its_ring_by_these_rules():
     src = open(os.path.join(ROOT, "full_duplex_speech_gb300", "csrc", "m2_attn_prompt_tile.cu")).read()
     for rule in ("ring_pieces(", "ring_fill(", "ring_look(", "ring_room("):
