@@ -449,17 +449,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const int nci = i ? run.nc1 : run.nc0;
             const float cs = fmaxf(fabsf(a.scale) * kLog2e, FLT_MIN);  // not 0: hidden scores are -inf
             bool here = true;
-            if (a.scale < 0.f && nci > 0) {  // the sign goes into the queries: the maxima are those of S
-                here = warp_ok(qfull, (uint32_t)before & 1u);
-#pragma unroll 1
-                for (int e = 0; e < 16; ++e) {
-                    uint4* q = reinterpret_cast<uint4*>(sm + L::kQ + i * kPtTile + (e >> 3) * kPtPanel + r * 128) + (e & 7);
-                    uint4 w = *q;
-                    w.x ^= 0x80008000u, w.y ^= 0x80008000u, w.z ^= 0x80008000u, w.w ^= 0x80008000u;
-                    *q = w;
-                }
-                tc::fence_proxy_async_smem();
-            }
             float m = kNone;
             float2 l0 = make_float2(0.f, 0.f), l1 = l0;  // the row's sum, in four parts
             // the weights of the run's chunk j from its scores
@@ -673,6 +662,8 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 // ------------------------------------------------------ products
                 const bool leader = tc::elect_one();
                 const uint32_t sbase = tc::smem_u32(sm);
+                // (a scale's sign goes into the products, so that the maxima are those of S)
+                const uint32_t scores = tc::idesc_bf16(kPtRows, kPtPos, 0, 0) | (a.scale < 0.f ? tc::kIdescNegateA : 0u);
                 tile_turns_meet(TileBarriers(), run.nc, run.nc0, run.nc1, [](int) {}, [&](int i, int j) {
                     const int nci = i ? run.nc1 : run.nc0;
                     // the last of the tiles that read this chunk (tile 1 takes every one, where there is one)
@@ -695,8 +686,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
     #pragma unroll
                             for (int q = 0; q < 8; ++q) {
                                 const uint64_t off = (uint64_t)(((q >> 2) * kPtPanel + (q & 3) * 32) >> 4);
-                                tc::mma_bf16(tm + kColS + 128 * i, ad + off, bd + off, tc::idesc_bf16(kPtRows, kPtPos, 0, 0),
-                                             q > 0 ? 1u : 0u);
+                                tc::mma_bf16(tm + kColS + 128 * i, ad + off, bd + off, scores, q > 0 ? 1u : 0u);
                             }
                             tc::mma_commit(sfull + i);
                             if (last) tc::mma_commit(empty + at);

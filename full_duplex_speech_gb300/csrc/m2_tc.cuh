@@ -200,6 +200,7 @@ __host__ __device__ constexpr uint32_t idesc_bf16(int M, int N, int a_mn, int b_
            | ((uint32_t)(N >> 3) << 17)   // N / 8
            | ((uint32_t)(M >> 4) << 24);  // M / 16
 }
+constexpr uint32_t kIdescNegateA = 1u << 13;  // D (+)= -A B
 
 // Shared-memory matrix descriptor. layout: 0 = no swizzle (core-matrix
 // interleave), 2 = 128-byte swizzle, 4 = 64-byte, 6 = 32-byte.

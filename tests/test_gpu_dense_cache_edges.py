@@ -61,3 +61,22 @@ def test_refused_sessions_among_many_pairs_of_tiles(m2, act):
         assert torch.equal(now[1::2].view(torch.uint8), was.view(torch.uint8))
     for now, want in ((c.kc, d.kc), (c.vc, d.vc)):
         assert torch.equal(now[::2].view(torch.uint8), want.view(torch.uint8))
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+def test_negative_scales_over_many_pairs_of_tiles(m2, act):
+    """Several pairs of tiles a CTA, some with one tile only: the scale's sign and the queries' are the same."""
+    import torch
+    b, n = [0, 300, 0, 500] * 40, [8, 40, 75, 16] * 40
+    c = Caches(m2, b, 32, 4, act, 600, seed=83)
+    p, q = Packed(c, n), Packed(c, n)
+    q.rows.copy_(p.rows)
+    q.q.neg_()
+    q.attend(scale=0.11)
+    _done(m2)
+    for _ in range(10):
+        p.out.fill_(-7.0), p.lse.fill_(-7.0)
+        p.attend(scale=-0.11)
+        _done(m2)
+        assert torch.equal(p.out, q.out) and torch.equal(p.lse, q.lse)
+    p.check(sessions=[0, 1, 2, 3, 157, 159])
