@@ -5,6 +5,7 @@
 //     lse_t,h = ln sum_p e^(a_p)
 // with kv head g = h / R, R = Hq / Hkv. A kv head's rows are its (row, head)
 // pairs, t R + r.
+#include <limits.h>
 #include <math.h>
 
 #include "m2_dense_dev.cuh"
@@ -16,7 +17,10 @@ namespace {
 
 // ---------------------------------------------------------------- the append
 // A warp a row: its keys and values, 16 bytes a lane at a time, to position
-// before + t of its session's caches. The session by a 32-way search.
+// before + t of its session's caches. The session is the one that ends at the first
+// entry of row_start past the row: those ahead of that are at or before the row, and
+// sessions behind it begin before it. It is left out where an entry ahead of its first
+// is larger. (Every entry up to it is looked at, 128 at a time.)
 constexpr int kApThreads = 256;
 __global__ void __launch_bounds__(kApThreads) prompt_append_kernel(PromptArgs a, int row_bytes) {
     pdl_wait();
@@ -37,18 +41,35 @@ __global__ void __launch_bounds__(kApThreads) prompt_append_kernel(PromptArgs a,
             if (i0 + 32 * f + lane < pieces) k[f] = __ldg(ks + i0 + 32 * f + lane), v[f] = __ldg(vs + i0 + 32 * f + lane);
     };
     load(0);
-    // the last session whose first row is at or before this one
-    int lo = 0, size = a.S;
-    while (size > 1) {
-        const int step = (size + 31) >> 5, at = lo + lane * step;
-        const int n = __popc(__ballot_sync(0xffffffffu, at < lo + size && a.start[min(at, a.S)] <= row));
-        if (n == 0) return;  // rows ahead of the first session's
-        lo += (n - 1) * step;
-        size = min(step, size - (n - 1) * step);
+    constexpr int kEach = 4;
+    int lo = -1, top = INT_MIN;  // the session; this lane's largest of the entries ahead of its first
+    int row0 = 0, end = 0, before = 0;
+    for (int s0 = 0; lo < 0 && s0 < a.S; s0 += 32 * kEach) {
+        int b[kEach], e[kEach], len[kEach];
+#pragma unroll
+        for (int f = 0; f < kEach; ++f) {
+            const int s = s0 + 32 * f + lane;
+            const bool there = s < a.S;
+            b[f] = there ? a.start[s] : INT_MIN, e[f] = there ? a.start[s + 1] : INT_MIN;
+            len[f] = there && a.lens ? a.lens[s] : 0;
+        }
+#pragma unroll
+        for (int f = 0; f < kEach; ++f) {
+            if (lo >= 0) continue;  // (the same in the whole warp)
+            const unsigned past = __ballot_sync(0xffffffffu, e[f] > row);
+            const int at = past ? __ffs(past) - 1 : 32;
+            if (lane < at) top = max(top, b[f]);
+            if (past) {
+                lo = s0 + 32 * f + at;
+                row0 = __shfl_sync(0xffffffffu, b[f], at), end = __shfl_sync(0xffffffffu, e[f], at);
+                before = __shfl_sync(0xffffffffu, len[f], at);
+            }
+        }
     }
-    Session x;
-    if (!session_of(a, lo, &x) || !x.ok || row < x.row0 || row >= x.row0 + x.n) return;
-    const size_t to = ((size_t)lo * a.Hkv * a.Tmax + x.before + (row - x.row0)) * row_bytes;
+    // (rows ahead of the first session's or behind the last's are nobody's)
+    if (lo < 0 || row < row0 || row0 < 0 || end > a.rows || row0 < __reduce_max_sync(0xffffffffu, top)) return;
+    if (before < 0 || (long)before + (end - row0) > a.Tmax) return;
+    const size_t to = ((size_t)lo * a.Hkv * a.Tmax + before + (row - row0)) * row_bytes;
     for (int i0 = 0; i0 < pieces; i0 += 32 * kFlight) {
         if (i0 > 0) load(i0);
 #pragma unroll

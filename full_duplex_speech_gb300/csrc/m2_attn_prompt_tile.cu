@@ -44,6 +44,7 @@
 // cycles when the whole took 490 us: 2 x 1,150 of products (2,050 at their rate; what is
 // left waits for shared memory, which they and the copies read and write for 2,000
 // cycles), each tile's softmax 1,000 and its hand-overs some 450.
+#include <limits.h>
 #include <math.h>
 
 #include <mutex>
@@ -142,32 +143,61 @@ __device__ __forceinline__ void tma_store_3d(const void* tmap, int x, int y, int
 
 // The pair of tiles `at` of all the sessions' pairs of `per` packed rows each,
 // found by a warp, four sessions a lane at a time (a session's last pair first:
-// it sees the most positions). A session whose rows do not lie within the call's
-// has none, and is recorded. `from`: the sessions and pairs that lie before, for the
-// next time.
+// it sees the most positions). A session whose rows do not lie within the call's, or
+// begin before an entry ahead of them, has none, and is recorded. `from`: the sessions
+// and pairs that lie before, and, once an entry is below the one ahead of it, the
+// largest of theirs, for the next time.
 struct PtFound {
     int s0, base;
+    bool fell;
+    int top;
 };
 __device__ __forceinline__ PtWork find_pair(const PromptArgs& a, int per, int at, PtFound* from) {
     constexpr int kEach = 4;
     const int lane = threadIdx.x & 31;
     PtWork y = {-1, 0, 0, 0, 0, at % a.Hkv};
     at /= a.Hkv;
-    if (at < from->base) *from = {0, 0};
-    int base = from->base;
+    if (at < from->base) *from = {0, 0, false, 0};
+    int base = from->base, top = from->top;
+    bool fell = from->fell;
     for (int s0 = from->s0; s0 < a.S; s0 += 32 * kEach) {
-        *from = {s0, base};
+        *from = {s0, base, fell, top};
         int b[kEach + 1], before[kEach], n[kEach], mine = 0;
         const int first = s0 + lane * kEach;
 #pragma unroll
         for (int i = 0; i <= kEach; ++i) b[i] = first + i <= a.S ? a.start[first + i] : 0;
 #pragma unroll
         for (int i = 0; i < kEach; ++i) before[i] = a.lens && first + i < a.S ? a.lens[first + i] : 0;
+        bool falls = false;
+#pragma unroll
+        for (int i = 0; i < kEach; ++i) falls = falls || (first + i < a.S && b[i + 1] < b[i]);
+        unsigned before_them = 0;  // a bit a session that begins before an entry ahead of its first
+        if (__builtin_expect(fell || __any_sync(0xffffffffu, falls), 0)) {
+            if (!fell) top = __shfl_sync(0xffffffffu, b[0], 0);
+            fell = true;
+            int largest = INT_MIN;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i)
+                if (first + i < a.S) largest = max(largest, b[i]);
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int below = __shfl_up_sync(0xffffffffu, largest, off);
+                if (lane >= off) largest = max(largest, below);
+            }
+            const int below = __shfl_up_sync(0xffffffffu, largest, 1);
+            int ahead = lane > 0 ? max(top, below) : top;
+#pragma unroll
+            for (int i = 0; i < kEach; ++i) {
+                if (b[i] < ahead) before_them |= 1u << i;
+                ahead = max(ahead, b[i]);
+            }
+            top = max(top, __shfl_sync(0xffffffffu, largest, 31));
+        }
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             n[i] = 0;
             if (first + i < a.S) {
-                if (b[i] < 0 || b[i + 1] < b[i] || b[i + 1] > a.rows)
+                if (b[i] < 0 || b[i + 1] < b[i] || b[i + 1] > a.rows || (before_them >> i & 1u))
                     record_error(a.err, ERR_ROW_START);
                 else
                     n[i] = (b[i + 1] - b[i] + per - 1) / per;
@@ -335,7 +365,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
 
     if (W > 1) tc::cluster_arrive_relaxed();  // waited on before the first remote access: every CTA has started
     bool good = true;                         // warp 0: no wait has run out, and copies may go on
-    PtFound found = {0, 0};                   // warp 0: where it has looked for pairs
+    PtFound found = {0, 0, false, 0};                   // warp 0: where it has looked for pairs
     bool appended = false;                    // warp 0: the append has been waited for
     // warp 0: a pair's queries, behind those of q pairs before; and its pieces p .. end - 1 of the ring,
     // where `first` is the first of them

@@ -48,7 +48,7 @@ __global__ void __launch_bounds__(kWfThreads) weights_fp32_kernel(PromptArgs a, 
     pdl_wait();
     pdl_trigger();
     Session x;
-    if (!session_of(a, s, &x)) {
+    if (!block_begins_behind(a, s, load_ahead(a, s)) || !session_of(a, s, &x)) {
         if (tid == 0) record_error(a.err, ERR_ROW_START);
         return;
     }

@@ -92,8 +92,9 @@ __global__ void __launch_bounds__(kWtThreads, 1)
 
     if (tid == 0) prefetch_map(&tmq), prefetch_map(&tmk);
     pdl_wait();
+    const int ahead = load_ahead(a, s);
     Session x;
-    const bool rows_ok = session_of(a, s, &x);
+    const bool within = session_of(a, s, &x), rows_ok = block_begins_behind(a, s, ahead) && within;
     if (!rows_ok || !x.ok) {
         if (tid == 0 && tile0 == 0) record_error(a.err, rows_ok ? ERR_ATTN_LENGTH : ERR_ROW_START);
         return;

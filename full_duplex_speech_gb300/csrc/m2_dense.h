@@ -7,6 +7,7 @@
 #pragma once
 
 #include <cuda_runtime.h>
+#include <limits.h>
 #include <stddef.h>
 #include <stdint.h>
 
@@ -62,7 +63,10 @@ struct Session {
     int row0, n, before;  // its first packed row, its rows, the positions cached before them
     bool ok;              // its positions fit the cache
 };
-// Session s of the call; false where its rows do not lie within the call's.
+// Session s of the call; false where its rows do not lie within the call's. A session
+// also has to begin at or behind every entry of row_start ahead of its first (they all
+// do where no entry is below the one ahead of it): only such sessions have rows of their
+// own, one behind the other. That is the caller's to see.
 __device__ __forceinline__ bool session_of(const PromptArgs& a, int s, Session* x) {
     const int b = a.start[s], e = a.start[s + 1];
     x->row0 = b;
@@ -70,6 +74,15 @@ __device__ __forceinline__ bool session_of(const PromptArgs& a, int s, Session* 
     x->before = a.lens ? a.lens[s] : 0;
     x->ok = x->before >= 0 && (long)x->before + x->n <= a.Tmax;
     return b >= 0 && e >= b && e <= a.rows;
+}
+// Whether session s begins behind the entries ahead, found by the whole block. `ahead`:
+// what load_ahead gave, so that it is on its way with the caller's other loads.
+__device__ __forceinline__ int load_ahead(const PromptArgs& a, int s) {
+    return (int)threadIdx.x < s ? a.start[threadIdx.x] : INT_MIN;
+}
+__device__ __forceinline__ bool block_begins_behind(const PromptArgs& a, int s, int ahead) {
+    for (int i = threadIdx.x + blockDim.x; i < s; i += blockDim.x) ahead = max(ahead, a.start[i]);
+    return __syncthreads_and(ahead <= a.start[s]);
 }
 #endif
 

@@ -1,6 +1,8 @@
 // Device helpers shared by the kernels over packed prompts and dense caches.
 #pragma once
 
+#include <limits.h>
+
 #include <atomic>
 
 #include "m2_common.cuh"
@@ -13,30 +15,51 @@ namespace m2 {
 // The tile `x` of all the sessions' tiles of `per` rows each, found by the
 // whole block: session and tile of it, the last tile of a session first (it
 // sees the most positions). `scratch`: blockDim / 32 + 3 ints of shared memory.
-// False past the last tile. A session whose rows do not lie within the call's
-// has no tiles, and is recorded in the error word.
+// False past the last tile. A session whose rows do not lie within the call's, or
+// begin before an entry ahead of them, has no tiles, and is recorded in the error word.
 __device__ __forceinline__ bool find_tile(const PromptArgs& a, int per, int x, int* scratch, int* session, int* tile) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = (int)blockDim.x >> 5;
     int* found = scratch + warps;  // session, tile, one more than the last tile so far
     if (tid == 0) found[0] = -1;
     int base = 0;
+    bool fell = false;  // an entry so far is below the one ahead of it;
+    int top = 0;        // then, the largest entry ahead of these
     for (int s0 = 0; s0 < a.S; s0 += (int)blockDim.x) {
-        const int s = s0 + tid;
-        int mine = 0;
-        if (s < a.S) {
-            const int b = a.start[s], e = a.start[s + 1];
-            if (b < 0 || e < b || e > a.rows)
-                record_error(a.err, ERR_ROW_START);
-            else
-                mine = (e - b + per - 1) / per;
+        const int s = s0 + tid, b = s < a.S ? a.start[s] : 0, e = s < a.S ? a.start[s + 1] : 0;
+        // (the barrier: the scratch of the block before is read)
+        const bool falls = __syncthreads_or(e < b);
+        bool behind = true;  // this session begins behind the entries ahead
+        if (fell || falls) {
+            if (!fell) top = a.start[s0];
+            fell = true;
+            int largest = s < a.S ? b : INT_MIN;
+#pragma unroll
+            for (int off = 1; off < 32; off <<= 1) {
+                const int below = __shfl_up_sync(0xffffffffu, largest, off);
+                if (lane >= off) largest = max(largest, below);
+            }
+            if (lane == 31) scratch[warp] = largest;
+            const int below = __shfl_up_sync(0xffffffffu, largest, 1);
+            __syncthreads();
+            int ahead = lane > 0 ? max(top, below) : top;
+            for (int w = 0; w < warps; ++w) {
+                if (w < warp) ahead = max(ahead, scratch[w]);
+                top = max(top, scratch[w]);
+            }
+            behind = s >= a.S || b >= ahead;
+            __syncthreads();  // (the scratch is read)
         }
+        int mine = 0;
+        if (b < 0 || e < b || e > a.rows || !behind)
+            record_error(a.err, ERR_ROW_START);
+        else
+            mine = (e - b + per - 1) / per;
         int upto = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {
             const int below = __shfl_up_sync(0xffffffffu, upto, off);
             if (lane >= off) upto += below;
         }
-        __syncthreads();  // (the scratch of the block before is read)
         if (lane == 31) scratch[warp] = upto;
         __syncthreads();
         int ahead = base, all = base;

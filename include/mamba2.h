@@ -690,7 +690,8 @@ size_t mamba2_attn_paged_workspace_bytes(const m2_kv_cache* c, int T, int n_head
  *   the device, in the error word: 0x104, a negative length or positions past
  *   max_len: that session's rows of out are zeros, of lse -infinity, and its
  *   caches are as they were; 0x106, a row_start that decreases or lies outside
- *   [0, n_rows]: the sessions on both sides of it are left out. */
+ *   [0, n_rows]: the sessions on both sides of it are left out, and every one that
+ *   begins before an entry ahead of it. */
 m2_status mamba2_attn_prompt(int n_sessions, int n_rows, int n_heads, int n_kv_heads, int head_dim, int max_len,
                              m2_dtype act, const int32_t* row_start, const int32_t* lengths, const void* q, long q_stride,
                              const void* k_new, const void* v_new, long kv_stride, void* k_cache, void* v_cache,

@@ -3,9 +3,10 @@ stand in tests/dense_cache_lib.py; where a test has one of its own, it is derive
 beside it."""
 import math
 
+import numpy as np
 import pytest
 
-from dense_cache_lib import Caches, Packed
+from dense_cache_lib import D, Caches, Packed, check_rows, check_sums
 
 pytestmark = pytest.mark.gpu
 
@@ -80,3 +81,65 @@ def test_negative_scales_over_many_pairs_of_tiles(m2, act):
         _done(m2)
         assert torch.equal(p.out, q.out) and torch.equal(p.lse, q.lse)
     p.check(sessions=[0, 1, 2, 3, 157, 159])
+
+
+def _own_rows(starts, n_rows):
+    """Sessions whose rows lie within the call's and behind every entry ahead of their first."""
+    return [s for s in range(len(starts) - 1)
+            if 0 <= starts[s] <= starts[s + 1] <= n_rows and starts[s] >= max(starts[:s], default=0)]
+
+
+def _long_row_starts(S, at, by):
+    """Sessions of up to three rows, with one entry raised."""
+    starts = np.concatenate([[0], np.cumsum(np.random.default_rng(S).integers(0, 4, S))])
+    starts[at] += by
+    return starts.tolist()
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("starts,n_rows", [
+    ([0, 100, 50, 150], 150), ([0, 40, 30, 70], 70), ([0, 100, 50, 60, 150, 170], 170), ([0, 30, -1, 60], 60),
+    ([10, 20, 500, 30, 60], 60), ([50, 0, 60, 80], 80), ([0, 0, 64, 63, 64, 128], 128),
+    (_long_row_starts(200, 20, 40), 300), (_long_row_starts(900, 127, 3000), 1400), (_long_row_starts(900, 600, 100), 1400),
+    (_long_row_starts(1100, 1024, 9), 1700),
+])
+def test_row_starts_that_decrease(m2, act, starts, n_rows):
+    """The sessions on both sides, and those that begin before an entry ahead of them, are left out: their caches and
+    sums, and rows that are nobody else's, stay as they were. The others come out as usual, theirs appended."""
+    import torch
+    S, Hq, Hkv, scale = len(starts) - 1, 10, 2, D ** -0.5
+    good = _own_rows(starts, n_rows)
+    assert good != list(range(S))
+    b = [(7 * s) % 40 for s in range(S)]
+    c = Caches(m2, b, Hq, Hkv, act, 160, seed=84)
+    p = Packed(c, [n_rows] + [0] * (S - 1))
+    row_start = torch.tensor(starts, dtype=torch.int32, device="cuda")
+    was = c.kc.clone(), c.vc.clone()
+    acc = torch.rand(S, Hkv, c.max_len, device="cuda")
+    sums = torch.full_like(acc, -7.0)
+    p.attend(row_start=row_start)
+    _done(m2, 0x106)
+    p.weigh(acc, sums, 5, row_start=row_start)
+    _done(m2, 0x106)
+    mine = torch.zeros(n_rows, dtype=torch.bool, device="cuda")
+    for s in range(S):
+        if s not in good:
+            for now, old in zip((c.kc, c.vc), was):
+                assert torch.equal(now[s].view(torch.uint8), old[s].view(torch.uint8))
+            assert torch.all(sums[s] == -7)
+            continue
+        at, n = starts[s], starts[s + 1] - starts[s]
+        mine[at:at + n] = True
+        for cache, rows in ((c.kc, p.k), (c.vc, p.v)):
+            want = rows[at:at + n, :Hkv * D].reshape(n, Hkv, D).transpose(0, 1).contiguous()
+            assert torch.equal(cache[s, :, b[s]:b[s] + n].contiguous().view(torch.uint8), want.view(torch.uint8))
+            assert torch.isnan(cache[s, :, b[s] + n:]).all()
+        if S < 100 or s % 25 == 0 or s > S - 10:
+            k, v = c.host(s, b[s] + n)
+            q = p.q[at:at + n].double().cpu().numpy().reshape(n, Hq, D)
+            lse = p.lse[at:at + n].double().cpu().numpy()
+            if n:
+                check_rows(p.out[at:at + n, :Hq * D].double().cpu().numpy().reshape(n, Hq, D), lse, q, k, v, scale, b[s], act)
+            check_sums(sums[s, :, :b[s] + n].double().cpu().numpy(), acc[s].double().cpu().numpy(), q, k, scale, b[s], lse, 5)
+            assert torch.all(sums[s, :, b[s] + n:] == -7)
+    assert torch.all(p.out[~mine] == -7) and torch.all(p.lse[~mine] == -7)
