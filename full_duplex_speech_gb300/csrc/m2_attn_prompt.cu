@@ -22,12 +22,7 @@ namespace {
 // sessions behind it begin before it. It is left out where an entry ahead of its first
 // is larger. (Every entry up to it is looked at, 128 at a time.)
 constexpr int kApThreads = 256;
-__global__ void __launch_bounds__(kApThreads) prompt_append_kernel(PromptArgs a, int row_bytes) {
-    pdl_wait();
-    pdl_trigger();
-    const int lane = threadIdx.x & 31;
-    const int row = (int)((blockIdx.x * (long)kApThreads + threadIdx.x) >> 5);
-    if (row >= a.rows) return;
+__device__ __forceinline__ void append_row(const PromptArgs& a, int row_bytes, int row, int lane) {
     const int pieces = a.Hkv * row_bytes / 16, per = row_bytes / 16;  // of keys, of a head
     const size_t from = (size_t)row * a.kv_stride * (row_bytes / kAttnD);
     const uint4* ks = reinterpret_cast<const uint4*>(static_cast<const uint8_t*>(a.k_new) + from);
@@ -83,8 +78,26 @@ __global__ void __launch_bounds__(kApThreads) prompt_append_kernel(PromptArgs a,
     }
 }
 
+__global__ void __launch_bounds__(kApThreads) prompt_append_kernel(PromptArgs a, int row_bytes) {
+    pdl_wait();
+    pdl_trigger();
+    const long thread = blockIdx.x * (long)kApThreads + threadIdx.x;
+    const int row = (int)(thread >> 5);
+    if (row < a.rows) append_row(a, row_bytes, row, threadIdx.x & 31);
+    // What is wrong with any session is recorded here, also where it has no rows or lies behind
+    // the last one that has. (A session that begins before an entry ahead of it lies behind one
+    // whose own entries decrease.)
+    for (long s = thread; s < a.S; s += (long)gridDim.x * kApThreads) {
+        Session x;
+        if (!session_of(a, (int)s, &x))
+            record_error(a.err, ERR_ROW_START);
+        else if (!x.ok)
+            record_error(a.err, ERR_ATTN_LENGTH);
+    }
+}
+
 cudaError_t launch_append(const PromptArgs& a, cudaStream_t st) {
-    const unsigned blocks = (unsigned)(((long)a.rows * 32 + kApThreads - 1) / kApThreads);
+    const unsigned blocks = a.rows > 0 ? (unsigned)(((long)a.rows * 32 + kApThreads - 1) / kApThreads) : 1u;
     return launch_pdl(prompt_append_kernel, dim3(blocks), dim3(kApThreads), 0, st, a, kAttnD * (a.bf16 ? 2 : 4));
 }
 
@@ -132,7 +145,6 @@ __global__ void __launch_bounds__(kPfThreads, 2) prompt_f32_kernel(PromptArgs a,
     auto column = [&](int row) { return (size_t)(g * R + row % R) * kAttnD; };
     if (!x.ok) {  // the whole cluster
         if (wk > 0) return;
-        if (tid == 0) record_error(a.err, ERR_ATTN_LENGTH);
         for (int i = tid; i < rows * kAttnD; i += kPfThreads)
             out[packed(i / kAttnD) * a.out_stride + column(i / kAttnD) + i % kAttnD] = 0.f;
         if (a.lse)
@@ -348,7 +360,7 @@ cudaError_t launch_f32(const PromptArgs& a, cudaStream_t st) {
 
 cudaError_t launch_attn_prompt(const PromptArgs& a, cudaStream_t st) {
     cudaError_t e = launch_append(a, st);
-    if (e != cudaSuccess) return e;
+    if (e != cudaSuccess || a.rows == 0) return e;
     return a.bf16 ? launch_attn_prompt_tiles(a, st) : launch_f32(a, st);
 }
 

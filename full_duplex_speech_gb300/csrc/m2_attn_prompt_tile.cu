@@ -144,7 +144,7 @@ __device__ __forceinline__ void tma_store_3d(const void* tmap, int x, int y, int
 // The pair of tiles `at` of all the sessions' pairs of `per` packed rows each,
 // found by a warp, four sessions a lane at a time (a session's last pair first:
 // it sees the most positions). A session whose rows do not lie within the call's, or
-// begin before an entry ahead of them, has none, and is recorded. `from`: the sessions
+// begin before an entry ahead of them, has none (the append records it). `from`: the sessions
 // and pairs that lie before, and, once an entry is below the one ahead of it, the
 // largest of theirs, for the next time.
 struct PtFound {
@@ -196,12 +196,8 @@ __device__ __forceinline__ PtWork find_pair(const PromptArgs& a, int per, int at
 #pragma unroll
         for (int i = 0; i < kEach; ++i) {
             n[i] = 0;
-            if (first + i < a.S) {
-                if (b[i] < 0 || b[i + 1] < b[i] || b[i + 1] > a.rows || (before_them >> i & 1u))
-                    record_error(a.err, ERR_ROW_START);
-                else
-                    n[i] = (b[i + 1] - b[i] + per - 1) / per;
-            }
+            if (first + i < a.S && b[i] >= 0 && b[i + 1] >= b[i] && b[i + 1] <= a.rows && !(before_them >> i & 1u))
+                n[i] = (b[i + 1] - b[i] + per - 1) / per;
             mine += n[i];
         }
         int upto = mine;
@@ -571,7 +567,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                 if (run.t0 + i * per >= run.row_end) return;  // the tile has no rows
                 const size_t packed = (size_t)y.row0 + t;
                 if (!run.ok) {  // a refused session has no pieces of the ring: each row's zeros from its own thread
-                    if (tid == 128) record_error(a.err, ERR_ATTN_LENGTH);
                     if (!live) return;
                     uint4* to = reinterpret_cast<uint4*>(static_cast<uint16_t*>(a.out) + packed * a.out_stride +
                                                          (size_t)(y.g * R + head) * kAttnD);
@@ -651,7 +646,6 @@ __global__ void __launch_bounds__(kPtThreads, 1)
                             make_float4(v[4 * e] + poison, v[4 * e + 1] + poison, v[4 * e + 2] + poison, v[4 * e + 3] + poison);
                 }
                 *reinterpret_cast<float2*>(sm + L::kMl + row * 8) = make_float2(m, l);
-                if (!run.ok && tid == 128) record_error(a.err, ERR_ATTN_LENGTH);
             }
         });
         left();

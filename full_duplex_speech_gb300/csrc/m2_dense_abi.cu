@@ -91,7 +91,7 @@ m2_status mamba2_attn_prompt(int n_sessions, int n_rows, int n_heads, int n_kv_h
     if (!aligned(k_cache, 16) || !aligned(v_cache, 16) || !aligned(lse, 4)) return M2_EALIGN;
     st = m2::check_device();
     if (st != M2_OK) return st;
-    if (n_sessions == 0 || n_rows == 0) return M2_OK;
+    if (n_sessions == 0) return M2_OK;
     m2::PromptArgs a = packed(n_sessions, n_rows, n_heads, n_kv_heads, max_len, act, row_start, lengths, q, q_stride, scale);
     a.k_new = k_new;
     a.v_new = v_new;

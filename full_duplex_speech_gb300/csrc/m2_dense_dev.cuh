@@ -16,7 +16,7 @@ namespace m2 {
 // whole block: session and tile of it, the last tile of a session first (it
 // sees the most positions). `scratch`: blockDim / 32 + 3 ints of shared memory.
 // False past the last tile. A session whose rows do not lie within the call's, or
-// begin before an entry ahead of them, has no tiles, and is recorded in the error word.
+// begin before an entry ahead of them, has no tiles. (The append records it.)
 __device__ __forceinline__ bool find_tile(const PromptArgs& a, int per, int x, int* scratch, int* session, int* tile) {
     const int tid = threadIdx.x, lane = tid & 31, warp = tid >> 5, warps = (int)blockDim.x >> 5;
     int* found = scratch + warps;  // session, tile, one more than the last tile so far
@@ -49,11 +49,7 @@ __device__ __forceinline__ bool find_tile(const PromptArgs& a, int per, int x, i
             behind = s >= a.S || b >= ahead;
             __syncthreads();  // (the scratch is read)
         }
-        int mine = 0;
-        if (b < 0 || e < b || e > a.rows || !behind)
-            record_error(a.err, ERR_ROW_START);
-        else
-            mine = (e - b + per - 1) / per;
+        const int mine = b < 0 || e < b || e > a.rows || !behind ? 0 : (e - b + per - 1) / per;
         int upto = mine;
 #pragma unroll
         for (int off = 1; off < 32; off <<= 1) {

@@ -143,3 +143,26 @@ def test_row_starts_that_decrease(m2, act, starts, n_rows):
             check_sums(sums[s, :, :b[s] + n].double().cpu().numpy(), acc[s].double().cpu().numpy(), q, k, scale, b[s], lse, 5)
             assert torch.all(sums[s, :, b[s] + n:] == -7)
     assert torch.all(p.out[~mine] == -7) and torch.all(p.lse[~mine] == -7)
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("what", ["start", "length"])
+@pytest.mark.parametrize("one_row", [199, 0])
+def test_what_is_wrong_behind_the_last_rows_is_recorded(m2, act, what, one_row):
+    """Sessions without rows far behind those that have them (or none has): one whose rows would end past the call's, or
+    whose length is past its cache."""
+    import torch
+    S = 700
+    b = [3] * S
+    if what == "length":
+        b[650] = 13
+    c = Caches(m2, b, 5, 1, act, 12, seed=85)
+    p = Packed(c, [1] * one_row + [0] * (S - one_row))
+    starts = list(p.starts)
+    if what == "start":
+        starts[-1] = 500
+    held = c.kc[one_row:].clone()
+    p.attend(row_start=torch.tensor(starts, dtype=torch.int32, device="cuda"))
+    _done(m2, 0x106 if what == "start" else 0x104)
+    p.check(sessions=range(0, one_row, 20))
+    assert torch.equal(c.kc[one_row:].view(torch.uint8), held.view(torch.uint8))
