@@ -38,6 +38,8 @@
 // The run holding position len[s] takes the new key and value from the
 // inputs instead of the cache, and writes them into the cache there (no other
 // CTA reads that slot).
+#include <float.h>
+
 #include <mutex>
 
 #include "m2_common.cuh"
@@ -96,6 +98,7 @@ int attn_chunk_len(int S, int Hkv, int Tmax, bool bf16) {
 }
 
 constexpr float kLog2e = 1.4426950408889634f;
+constexpr float kNoMax = -FLT_MAX;  // a running maximum before any position: no finite score is below it
 
 __device__ __forceinline__ float ex2_approx(float x) {
     float r;
@@ -586,7 +589,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2)
     // per head 2t and 2t + 1: running max (finite: a fully masked head stays
     // harmless), this lane's part of the sum, and acc^T (dims 16 dt + gq and
     // + 8)
-    float m0 = -1e30f, m1 = -1e30f, l0 = 0.f, l1 = 0.f;
+    float m0 = kNoMax, m1 = kNoMax, l0 = 0.f, l1 = 0.f;
     float acc[8][4];
 #pragma unroll
     for (int dt = 0; dt < 8; ++dt)
@@ -705,7 +708,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2)
         if (tid == 0)
             for (int i = 0; i < kWalkStages; ++i)
                 tc::mbar_wait(bar + i, 0, 100000000ull), tc::mbar_wait(bar + i, 1, 100000000ull);
-        m0 = m1 = -1e30f;
+        m0 = m1 = kNoMax;
         l0 = l1 = 0.f;
 #pragma unroll
         for (int dt = 0; dt < 8; ++dt)
@@ -741,10 +744,10 @@ __global__ void __launch_bounds__(kWalkThreads, 2)
     __syncthreads();
     if (W > 1) tc::cluster_wait();  // every walker of the cluster has started: its shared memory is there
     // this walker's (max, sum, acc) per query head, acc relative to its max
-    // (a walker without positions: max -1e30, sum 0, acc 0), to the head's
+    // (a walker without positions: max kNoMax, sum 0, acc 0), to the head's
     // owner: slot (r / W) W + wk of walker r % W
     for (int r = 0; r < R; ++r) {
-        float M = -1e30f;
+        float M = kNoMax;
 #pragma unroll
         for (int w = 0; w < 4; ++w) M = fmaxf(M, sml[(w * 8 + r) * 2]);
         float o = 0.f, L = 0.f;
@@ -779,7 +782,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2)
         float2* stat = reinterpret_cast<float2*>(sm + kWalkStat);
         float2* whole = stat + kWalkMaxW * kAttnMaxR;
         if (tid < R) {
-            float M = -1e30f, L = 0.f;
+            float M = kNoMax, L = 0.f;
             for (int w = 0; w < W; ++w) M = fmaxf(M, stat[w * kAttnMaxR + tid].x);
             for (int w = 0; w < W; ++w) L = fmaf(ex2_approx(stat[w * kAttnMaxR + tid].x - M), stat[w * kAttnMaxR + tid].y, L);
             whole[tid] = make_float2(M, 1.f / L);
@@ -820,7 +823,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2)
     // out = sum_w 2^(m_w - M) acc_w / sum_w 2^(m_w - M) l_w
     for (int r = wk; r < R; r += W) {
         const float* sl = recv + (r / W) * W * kWalkSlotF;
-        float M = -1e30f;
+        float M = kNoMax;
         for (int w = 0; w < W; ++w) M = fmaxf(M, sl[w * kWalkSlotF + kAttnD]);
         float o = 0.f, L = 0.f;
         for (int w = 0; w < W; ++w) {

@@ -6,7 +6,7 @@ import math
 import numpy as np
 import pytest
 
-from dense_cache_lib import D, Caches, Packed, check_rows, check_sums
+from dense_cache_lib import D, Caches, Packed, check_rows, check_sums, dtype
 
 pytestmark = pytest.mark.gpu
 
@@ -166,3 +166,39 @@ def test_what_is_wrong_behind_the_last_rows_is_recorded(m2, act, what, one_row):
     _done(m2, 0x106 if what == "start" else 0x104)
     p.check(sessions=range(0, one_row, 20))
     assert torch.equal(c.kc[one_row:].view(torch.uint8), held.view(torch.uint8))
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("Hq,Hkv,max_len,before", [
+    (40, 8, 300, [0, 1, 63, 64, 200, 299]), (40, 8, 7500, [7499]), (10, 2, 7500, [700]), (9, 3, 160, [40, 130, 0]),
+])
+def test_frames_of_scores_far_below_zero(m2, act, Hq, Hkv, max_len, before):
+    """Keys all alike, so that a position's weight is 1 / positions whatever the scores, which here lie near
+    -4e33 (every position's score comes from the same products in the same order: equal bits)."""
+    import torch
+    c = Caches(m2, before, Hq, Hkv, act, max_len, seed=80)
+    key = (1 + torch.rand(D, generator=c.g)).to(dtype(act)).cuda() * 1e16
+    for s, b in enumerate(before):
+        c.kc[s, :, :b] = key
+    q = -(1 + torch.rand(c.S, Hq, D, generator=c.g)).to(dtype(act)).cuda() * 1e16
+    k, v = key.expand(c.S, Hkv, D).contiguous(), c.values(c.S, Hkv, D)
+    kc, vc = c.kc.clone(), c.vc.clone()
+    acc = torch.zeros(c.S, Hkv, max_len, device="cuda")
+    sums, out = torch.full_like(acc, -7.0), torch.full((c.S, Hq, D), -7.0, dtype=dtype(act), device="cuda")
+    need = m2.mamba2_attn_decode_weights_workspace_bytes(c.S, Hq, Hkv, D, max_len, act)
+    ws = torch.empty(need, dtype=torch.uint8, device="cuda")
+    m2.mamba2_attn_decode_weights(c.S, Hq, Hkv, D, max_len, act, c.lengths, q, k, v, c.kc, c.vc, D ** -0.5, out, acc, sums, ws)
+    plain = torch.empty_like(out)
+    ws = torch.empty(max(1, m2.mamba2_attn_decode_workspace_bytes(c.S, Hq, Hkv, D, max_len, act)), dtype=torch.uint8,
+                     device="cuda")
+    m2.mamba2_attn_decode(c.S, Hq, Hkv, D, max_len, act, c.lengths, q, k, v, kc, vc, D ** -0.5, plain, ws)
+    _done(m2)
+    assert torch.equal(out, plain)
+    for s, b in enumerate(before):
+        # a weight and a sum of them are within 1e-5 of themselves (the scores' own error is the same for all)
+        want = Hq // Hkv / (b + 1)
+        assert torch.all((sums[s, :, :b + 1] - want).abs() <= 1e-5 * want) and torch.all(sums[s, :, b + 1:] == -7)
+        values = c.vc[s, :, :b + 1].double()
+        mean, mag = (x.mean(1).repeat_interleave(Hq // Hkv, 0) for x in (values, values.abs()))
+        half = 2.0 ** -8 if act == "bf16" else 2.0 ** -24
+        assert torch.all((out[s].double() - mean).abs() <= (1e-5 + (half if act == "bf16" else 0)) * mag + half * mean.abs())
