@@ -473,7 +473,9 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             // ... and the fewest that a row of the warp sees
             const int least = min(y.before + run.t0 + rt0, run.total - 1);
             const int nci = i ? run.nc1 : run.nc0;
-            const float cs = fmaxf(fabsf(a.scale) * kLog2e, FLT_MIN);  // not 0: hidden scores are -inf
+            // (Not 0, since hidden scores are -infinity: a scale of 0 counts as the least number above it, which
+            // leaves any finite product below 1e-6.)
+            const float cs = fmaxf(fabsf(a.scale) * kLog2e, FLT_TRUE_MIN);
             bool here = true;
             float m = kNone;
             float2 l0 = make_float2(0.f, 0.f), l1 = l0;  // the row's sum, in four parts

@@ -202,3 +202,15 @@ def test_frames_of_scores_far_below_zero(m2, act, Hq, Hkv, max_len, before):
         mean, mag = (x.mean(1).repeat_interleave(Hq // Hkv, 0) for x in (values, values.abs()))
         half = 2.0 ** -8 if act == "bf16" else 2.0 ** -24
         assert torch.all((out[s].double() - mean).abs() <= (1e-5 + (half if act == "bf16" else 0)) * mag + half * mean.abs())
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("before,new", [([20, 0], [150, 60]), ([2000], [30]), ([0], [1])])
+def test_a_scale_of_zero_and_large_products(m2, act, before, new):
+    """A score is 0, however large its products are (here some 1e37)."""
+    c = Caches(m2, before, 8, 2, act, max(b + n for b, n in zip(before, new)), seed=81)
+    p = Packed(c, new, lead=1)
+    c.kc.mul_(1e18), p.q.mul_(1e18), p.k.mul_(1e18)
+    p.attend(scale=0.0)
+    _done(m2)
+    p.check()
