@@ -30,7 +30,7 @@ m2_status check_sizes(int S, int Hq, int Hkv, int D, int max_len, m2_dtype act) 
     if (S < 0 || Hq <= 0 || Hkv <= 0 || D <= 0 || max_len <= 0) return M2_EINVAL;
     if (act != M2_BF16 && act != M2_F32) return M2_EINVAL;
     if (D != m2::kAttnD || Hq % Hkv != 0 || Hq / Hkv > m2::kAttnMaxR) return M2_ESHAPE;
-    if (S > 65535 || Hkv > 65535) return M2_ESHAPE;
+    if (S > 65535 || Hkv > 65535 || max_len > (1 << 30)) return M2_ESHAPE;  // (positions are 32-bit numbers)
     return M2_OK;
 }
 
@@ -48,8 +48,7 @@ m2_status check_packed(int S, int rows, int Hq, int Hkv, int D, int max_len, m2_
     m2_status st = check_sizes(S, Hq, Hkv, D, max_len, act);
     if (st != M2_OK) return st;
     if (rows < 0 || !isfinite(scale)) return M2_EINVAL;
-    // blocks of one row of every kv head, in a grid; positions are 32-bit numbers
-    if ((long long)rows * Hkv > (1LL << 30) || max_len > (1 << 30)) return M2_ESHAPE;
+    if ((long long)rows * Hkv > (1LL << 30)) return M2_ESHAPE;  // blocks of one row of every kv head, in a grid
     if (!row_start) return M2_EINVAL;
     if (!aligned(row_start, 4) || !aligned(lengths, 4)) return M2_EALIGN;
     return check_rows(q, q_stride, (long)Hq * D, act);
@@ -190,7 +189,7 @@ m2_status mamba2_kv_evict(int n_sessions, int n_kv_heads, int head_dim, int max_
     m2_status st = check_sizes(n_sessions, n_kv_heads, n_kv_heads, head_dim, max_len, act);
     if (st != M2_OK) return st;
     if (keep <= 0 || recent < 0 || recent > keep || out_max_len <= 0 || !lengths) return M2_EINVAL;
-    if (keep > out_max_len || max_len > (1 << 30) || out_max_len > (1 << 30)) return M2_ESHAPE;
+    if (keep > out_max_len || out_max_len > (1 << 30)) return M2_ESHAPE;
     const void* ptrs[] = {k_cache, v_cache, acc, k_out, v_out, acc_out};
     for (const void* p : ptrs)
         if (!p) return M2_EINVAL;

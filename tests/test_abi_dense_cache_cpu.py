@@ -103,6 +103,26 @@ def test_attn_decode_weights_validation_without_gpu(m2):
         assert _past_host_checks(call()) and _past_host_checks(call(acc_out=good["acc"]))
 
 
+def test_caches_past_the_limit_are_refused_by_every_call(m2):
+    """max_len at most 2^30: by the frames and the query of their scratch too."""
+    assert m2.mamba2_attn_decode_weights_workspace_bytes(1, 1, 1, 128, 1 << 30) >= (1 << 30) * 4
+    for longest in ((1 << 30) + 1, (1 << 31) - 1):
+        for act in ("bf16", "f32"):
+            assert m2.mamba2_attn_decode_weights_workspace_bytes(1, 1, 1, 128, longest, act) == 0
+    good = dict(GOOD, S=1, Hq=8, Hkv=1, ws=PTR[11], wsb=1 << 62, keep=50, recent=10, out_max=60, ko=PTR[12], vo=PTR[13],
+                kept=PTR[14])
+    for f, order in ((m2.mamba2_attn_prompt, SIZES + ["row_start", "lengths", "q", "qs", "k", "v", "kvs", "kc", "vc", "scale",
+                                                      "out", "outs", "lse"]),
+                     (m2.mamba2_attn_prompt_weights, SIZES + ["row_start", "lengths", "q", "qs", "kc", "scale", "lse", "window",
+                                                              "acc", "acc_out"]),
+                     (m2.mamba2_attn_decode_weights, ["S", "Hq", "Hkv", "D", "max_len", "act", "lengths", "q", "k", "v", "kc",
+                                                      "vc", "scale", "out", "acc", "acc_out", "ws", "wsb"]),
+                     (m2.mamba2_kv_evict, ["S", "Hkv", "D", "max_len", "act", "lengths", "kc", "vc", "acc", "keep", "recent",
+                                           "out_max", "ko", "vo", "acc_out", "kept"])):
+        for longest in ((1 << 30) + 1, (1 << 31) - 1):
+            assert _caller(f, order, good)(max_len=longest, acc_out=GOOD["acc"]) == 2, f.__name__
+
+
 def test_kv_evict_validation_without_gpu(m2):
     good = dict(GOOD, keep=50, recent=10, out_max=60, ko=PTR[11], vo=PTR[12], kept=PTR[13])
     call = _caller(m2.mamba2_kv_evict, ["S", "Hkv", "D", "max_len", "act", "lengths", "kc", "vc", "acc", "keep", "recent",
