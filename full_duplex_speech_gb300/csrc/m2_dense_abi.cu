@@ -202,12 +202,24 @@ m2_status mamba2_kv_evict(int n_sessions, int n_kv_heads, int head_dim, int max_
     const bool in_place = k_out == k_cache;
     if (in_place != (v_out == v_cache)) return M2_EINVAL;
     if ((in_place || acc_out == acc) && out_max_len != max_len) return M2_EINVAL;
-    if (overlap(k_out, out * row, v_out, out * row) || overlap(k_out, out * row, v_cache, in * row) ||
-        overlap(v_out, out * row, k_cache, in * row))
-        return M2_EINVAL;
-    if (!in_place && (overlap(k_out, out * row, k_cache, in * row) || overlap(v_out, out * row, v_cache, in * row)))
-        return M2_EINVAL;
-    if (acc_out != acc && overlap(acc_out, out * 4, acc, in * 4)) return M2_EINVAL;
+    const struct {
+        const void* p;
+        size_t bytes;
+        const void* place;  // the input it may be
+    } outs[] = {{k_out, out * row, k_cache},
+                {v_out, out * row, v_cache},
+                {acc_out, out * 4, acc},
+                {kept, kept ? cache_rows(n_sessions, n_kv_heads, keep) * 4 : 0, nullptr}};
+    const struct {
+        const void* p;
+        size_t bytes;
+    } ins[] = {{k_cache, in * row}, {v_cache, in * row}, {acc, in * 4}, {lengths, (size_t)n_sessions * 4}};
+    for (int i = 0; i < 4; ++i) {
+        for (const auto& x : ins)
+            if (!(outs[i].p == x.p && x.p == outs[i].place) && overlap(outs[i].p, outs[i].bytes, x.p, x.bytes)) return M2_EINVAL;
+        for (int j = 0; j < i; ++j)
+            if (overlap(outs[i].p, outs[i].bytes, outs[j].p, outs[j].bytes)) return M2_EINVAL;
+    }
     st = m2::check_device();
     if (st != M2_OK) return st;
     if (n_sessions == 0) return M2_OK;

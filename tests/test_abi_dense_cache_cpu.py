@@ -148,3 +148,23 @@ def test_kv_evict_validation_without_gpu(m2):
         for ok in (dict(), place, dict(place, acc_out=good["acc_out"]), dict(kept=None), dict(acc_out=acc, out_max=100),
                    dict(keep=60, recent=60), dict(act="f32")):
             assert _past_host_checks(call(**ok)), ok
+
+
+def test_kv_evict_outputs_lie_over_nothing_else(m2):
+    """k_out, v_out, acc_out and kept over an input that is not theirs in place, or over one another."""
+    good = dict(GOOD, keep=50, recent=10, out_max=60, ko=PTR[11], vo=PTR[12], kept=PTR[13])
+    call = _caller(m2.mamba2_kv_evict, ["S", "Hkv", "D", "max_len", "act", "lengths", "kc", "vc", "acc", "keep", "recent",
+                                        "out_max", "ko", "vo", "acc_out", "kept"], good)
+    kc, vc, acc, lengths = good["kc"], good["vc"], good["acc"], good["lengths"]
+    place = dict(ko=kc, vo=vc, acc_out=acc, out_max=100)
+    cache, rows, sums = 2 * 8 * 100 * 256, 2 * 8 * 60 * 256, 2 * 8 * 60 * 4
+    for bad in [dict(ko=acc), dict(vo=acc + 16), dict(ko=lengths), dict(vo=lengths - rows + 16), dict(acc_out=kc),
+                dict(acc_out=vc + cache - 16), dict(acc_out=lengths), dict(acc_out=good["ko"]), dict(acc_out=good["vo"] - sums + 16),
+                dict(place, acc_out=kc), dict(place, acc_out=vc + 64)] + \
+               [dict(more, kept=at + 4) for more in (dict(), place)
+                for at in (kc, vc, acc, lengths, {**good, **more}["ko"], {**good, **more}["vo"], {**good, **more}["acc_out"])]:
+        assert call(**bad) == 1, bad
+    if NO_GPU:
+        for ok in (dict(kept=kc + cache), dict(kept=acc - 2 * 8 * 50 * 4), dict(ko=acc + 2 * 8 * 100 * 4), dict(acc_out=good["ko"] + rows),
+                   dict(place, kept=vc + cache), dict(S=0, ko=acc)):
+            assert _past_host_checks(call(**ok)), ok
