@@ -37,8 +37,10 @@ m2_status check_sizes(int S, int Hq, int Hkv, int D, int max_len, m2_dtype act) 
 size_t cache_rows(int S, int Hkv, int max_len) { return (size_t)S * Hkv * max_len; }
 
 m2_status check_rows(const void* p, long stride, long width, m2_dtype act) {
+    const long size = act == M2_BF16 ? 2 : 4;
     if (!p || stride < width) return M2_EINVAL;
-    if (!aligned(p, 16) || (stride * (act == M2_BF16 ? 2 : 4)) % 16 != 0) return M2_EALIGN;
+    if (stride >= (1L << 40) / size) return M2_ESHAPE;  // (the limit of a tensor map)
+    if (!aligned(p, 16) || stride * size % 16 != 0) return M2_EALIGN;
     return M2_OK;
 }
 

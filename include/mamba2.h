@@ -676,8 +676,8 @@ size_t mamba2_attn_paged_workspace_bytes(const m2_kv_cache* c, int T, int n_head
  * q, out: n_rows rows of n_heads * 128 activations, q_stride (out_stride)
  *   elements apart; k_new, v_new: n_rows rows of n_kv_heads * 128, kv_stride
  *   apart, so that they may be columns of the projection's rows q | k | v.
- *   Strides times the element size a multiple of 16 bytes. out must not overlap
- *   an input (M2_EINVAL where it is q, k_new or v_new).
+ *   Strides times the element size a multiple of 16 bytes, less than 2^40. out must
+ *   not overlap an input (M2_EINVAL where it is q, k_new or v_new).
  * lse: [n_rows, n_heads] fp32, for mamba2_attn_prompt_weights (NULL: not wanted).
  * n_rows * n_kv_heads at most 2^30.
  * Scores, maxima and sums are fp32, out is rounded once; in bf16 a softmax

@@ -168,3 +168,18 @@ def test_kv_evict_outputs_lie_over_nothing_else(m2):
         for ok in (dict(kept=kc + cache), dict(kept=acc - 2 * 8 * 50 * 4), dict(ko=acc + 2 * 8 * 100 * 4), dict(acc_out=good["ko"] + rows),
                    dict(place, kept=vc + cache), dict(S=0, ko=acc)):
             assert _past_host_checks(call(**ok)), ok
+
+
+def test_row_strides_past_the_limit_are_refused(m2):
+    """2^40 bytes, which the copies' descriptors have room for, and what would wrap when multiplied out."""
+    prompt = _caller(m2.mamba2_attn_prompt, SIZES + ["row_start", "lengths", "q", "qs", "k", "v", "kvs", "kc", "vc", "scale",
+                                                     "out", "outs", "lse"], GOOD)
+    weights = _caller(m2.mamba2_attn_prompt_weights, SIZES + ["row_start", "lengths", "q", "qs", "kc", "scale", "lse", "window",
+                                                              "acc", "acc_out"], GOOD)
+    for act, size in (("bf16", 2), ("f32", 4)):
+        for stride in ((1 << 40) // size, (1 << 62), (1 << 63) - 8):
+            for n in ("qs", "kvs", "outs"):
+                assert prompt(rows=1, act=act, **{n: stride}) == 2, (n, stride)
+            assert weights(rows=1, act=act, qs=stride) == 2
+        if NO_GPU:
+            assert _past_host_checks(prompt(rows=1, act=act, qs=(1 << 40) // size - 8))
