@@ -117,17 +117,12 @@ __global__ void __launch_bounds__(kWtThreads, 1)
         tc::tmem_alloc(sTmem, 512);
         tc::tmem_relinquish();
     }
-    // Rows of a tile of pairs that no packed row fills: zeros (and an e of -infinity). The ones: three
-    // of 16; what e's last 13 are is zeros.
+    // The ones: three of 16; what e's last 13 are is zeros. (Rows of a tile of pairs that no packed row
+    // fills hold anything: their columns of the products are not added up.)
     if (warp >= 4) {
         for (int i = tid - 128; i < (int)((2 * kWtStages + 1) * kWtExtra / 16); i += kWtThreads - 128) {
             const bool ones = i >= (int)(2 * kWtStages * kWtExtra / 16) && i % (int)(kWtExtra / 16) < 128;
             *reinterpret_cast<uint4*>(sm + L::kE + i * 16) = ones ? make_uint4(0x3F803F80u, 0x3F80u, 0u, 0u) : make_uint4(0u, 0u, 0u, 0u);
-        }
-        const int dead = 128 - per * R, each = dead * 8;  // 16-byte pieces of a tile's panel
-        for (int i = tid - 128; i < (kWtStages - 1) * 4 * each; i += kWtThreads - 128) {
-            const int panel = i / each, row = per * R + i % each / 8;  // (stage, panel, tile)
-            *reinterpret_cast<uint4*>(sm + L::kQ + panel * kWtPanel + row * 128 + i % 8 * 16) = make_uint4(0u, 0u, 0u, 0u);
         }
         tc::fence_proxy_async_smem();
     }
@@ -150,17 +145,6 @@ __global__ void __launch_bounds__(kWtThreads, 1)
     auto warp_ok = [&](uint64_t* bar, uint32_t parity) -> bool { return __all_sync(0xffffffffu, wait_ok(bar, parity)); };
     auto stage = [](int j) { return j % kWtStages; };
     auto phase = [](int j) { return (uint32_t)(j / kWtStages) & 1u; };
-    // a warp: the rows of a stage that no packed row fills
-    auto zero_dead = [&](int st) {
-#pragma unroll 1
-        for (int i = lane; i < 4 * (128 - per * R) * 8; i += 32) {
-            const int row = per * R + (i >> 5);
-            *reinterpret_cast<uint4*>(sm + L::kQ + st * kWtStage + (i >> 3 & 3) * kWtPanel + row * 128 + (i & 7) * 16) =
-                make_uint4(0u, 0u, 0u, 0u);
-        }
-        tc::fence_proxy_async_smem();
-        __syncwarp();
-    };
     // A tile of 256 positions: the window's rows that see any of them, first .. n - 1, in steps of 2 per.
     struct Item {
         int p0, first, steps, tiles;  // tiles: of 128 positions
@@ -204,10 +188,7 @@ __global__ void __launch_bounds__(kWtThreads, 1)
             }
             __syncwarp();
             for (int j = 0; j < it.steps || j < kWtStages; ++j) {
-                if (j == kWtStages - 1) {  // the keys are read; the rows that no packed row fills are zeros again
-                    good = good && warp_ok(kbar, (uint32_t)k & 1u);
-                    if (good) zero_dead(ks);
-                }
+                if (j == kWtStages - 1) good = good && warp_ok(kbar, (uint32_t)k & 1u);  // the keys are read
                 if (j >= it.steps) continue;
                 const int at = stage(J + j);
                 if (J + j >= kWtStages) good = good && warp_ok(qempty + at, phase(J + j - kWtStages));
@@ -390,6 +371,11 @@ __global__ void __launch_bounds__(kWtThreads, 1)
                             for (int e = 0; e < 8; ++e) {
                                 float2 x0 = mul2(make_float2(v[at][4 * e], v[at][4 * e + 1]), c2);
                                 float2 x1 = mul2(make_float2(v[at][4 * e + 2], v[at][4 * e + 3]), c2);
+                                // the columns that no packed row fills, three at most
+                                if (!kAsk && q == 3 && e == 7) {
+                                    x0.y = per * R > 125 ? x0.y : -INFINITY;
+                                    x1.x = per * R > 126 ? x1.x : -INFINITY, x1.y = per * R > 127 ? x1.y : -INFINITY;
+                                }
                                 if (kAsk) {
                                     const int c = 4 * e;
                                     x0.x = c >= lo && c < hi ? x0.x : -INFINITY, x0.y = c + 1 >= lo && c + 1 < hi ? x0.y : -INFINITY;

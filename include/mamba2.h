@@ -683,8 +683,10 @@ size_t mamba2_attn_paged_workspace_bytes(const m2_kv_cache* c, int T, int n_head
  * Scores, maxima and sums are fp32, out is rounded once; in bf16 a softmax
  *   weight enters its product with the values rounded to bf16 (2^-8 of itself).
  * A value that is not finite makes the outputs of the rows that see it not
- *   finite (in its dim, or NaN in all dims), and no others; a key likewise, and
- *   their lse; a query its own row and head.
+ *   finite (in its dim, or NaN in all dims), and no others; a key whose score is
+ *   NaN or +infinity makes all dims of that row and head NaN, and the lse not
+ *   finite (one whose score is -infinity has no weight); a query its own row and
+ *   head.
  * Errors: M2_EINVAL, M2_ESHAPE, M2_EALIGN, M2_EUNSUPPORTED, M2_ECUDA. A bounded
  *   wait that runs out records 0x101 or 0x102 (mamba2_device_error). Seen only on
  *   the device, in the error word: 0x104, a negative length or positions past
@@ -706,9 +708,11 @@ m2_status mamba2_attn_prompt(int n_sessions, int n_rows, int n_heads, int n_kv_h
  *           kv head g, of exp(scale * q[row][h] . k_cache[s][g][p] - lse[row][h])
  * To be called behind mamba2_attn_prompt with the same arguments, before the
  * caller advances lengths. Other slots of acc_out are left as they were; acc_out
- * may be acc. Sums in fp32; in bf16 the scores' sums are cut off, not rounded
- * (a sum is within some 1e-6 of itself). A key that is not finite makes its own
- * position's sum not finite, a query or lse those of the positions that it sees.
+ * may be acc. Sums in fp32; in bf16 the scores' sums are cut off, not rounded. A
+ * weight is within 136 u A + 4 u |lse| + 1e-5 of itself, with u = 2^-24 and A the
+ * row's largest |scale| sum |q| |k|, and so are their sums. A key that is not finite
+ * makes its own position's sum not finite (or 0, where its scores are -infinity),
+ * and no other's; a query or lse those of the positions that it sees likewise.
  * Errors as mamba2_attn_prompt; a session with 0x104 or 0x106 is left out. */
 m2_status mamba2_attn_prompt_weights(int n_sessions, int n_rows, int n_heads, int n_kv_heads, int head_dim, int max_len,
                                      m2_dtype act, const int32_t* row_start, const int32_t* lengths, const void* q,
@@ -722,8 +726,9 @@ m2_status mamba2_attn_prompt_weights(int n_sessions, int n_rows, int n_heads, in
  * in fp32; acc_out may be acc, its slots past L are left as they were. out and
  * the caches hold the same bits as after mamba2_attn_decode.
  * Scratch: workspace of at least mamba2_attn_decode_weights_workspace_bytes(...)
- *   (the scores, until their softmax's sum is known): 4 bytes for every position
- *   and head of the caches, about.
+ *   (the scores, until their softmax's sum is known): 4 bytes for every position of
+ *   the caches and query head, where a kv head's query heads count as an even number,
+ *   beside what mamba2_attn_decode needs.
  * Errors as mamba2_attn_decode; a session with a length outside [0, max_len) has
  *   its acc_out left as it was. */
 m2_status mamba2_attn_decode_weights(int n_sessions, int n_heads, int n_kv_heads, int head_dim, int max_len, m2_dtype act,

@@ -214,3 +214,32 @@ def test_a_scale_of_zero_and_large_products(m2, act, before, new):
     p.attend(scale=0.0)
     _done(m2)
     p.check()
+
+
+@pytest.mark.parametrize("act", ["f32", "bf16"])
+@pytest.mark.parametrize("before,new", [([20], [150]), ([2000], [40]), ([0], [300])])
+def test_keys_of_infinite_scores(m2, act, before, new):
+    """A key whose score is -infinity has no weight, as one of -1e30 has none; one of +infinity makes what sees it NaN."""
+    import torch
+    b, n = before[0], new[0]
+    at = n // 3  # the row that it comes with
+    found = []
+    for key in (1e30, math.inf):
+        c = Caches(m2, before, 10, 2, act, b + n, seed=86)
+        p = Packed(c, new)
+        p.q.view(n, -1)[:, 3::D] = -1.0                  # dim 3 of every head
+        p.q.view(n, -1)[:, 5 * D + 3::D] = 1.0           # of kv head 1's: the score is +infinity
+        p.k[at, 3] = key
+        p.k[at, D + 3] = 0.0 if key == 1e30 else math.inf
+        p.attend()
+        acc = torch.zeros(1, 2, b + n, device="cuda")
+        sums = torch.full_like(acc, -7.0)
+        p.weigh(acc, sums, n)
+        _done(m2)
+        found.append([p.out.float().view(n, 10, D), p.lse.clone(), sums])
+    (out, lse, sums), (out_inf, lse_inf, sums_inf) = found
+    assert torch.equal(out_inf[:, :5], out[:, :5]) and torch.equal(lse_inf[:, :5], lse[:, :5])
+    assert torch.equal(sums_inf[:, 0], sums[:, 0]) and torch.all(sums[0, 0, b + at] == 0)
+    assert torch.equal(out_inf[:at, 5:], out[:at, 5:]) and torch.equal(lse_inf[:at, 5:], lse[:at, 5:])
+    assert torch.isnan(out_inf[at:, 5:]).all() and not torch.isfinite(lse_inf[at:, 5:]).any()
+    assert not torch.isfinite(sums_inf[0, 1, b + at])
