@@ -271,18 +271,20 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t st) {
     const int staged = a.Tmax < kEvStaged ? a.Tmax : kEvStaged;
     const cudaError_t e = allow_shared<3>((const void*)kv_evict_kernel, kEvStaged * 4);
     if (e != cudaSuccess) return e;
-    // CTAs a (session, kv head): in place while the 152 SMs hold them at once, two an SM. Out of place one
-    // an SM for a single session (each CTA chooses by itself, which takes as long as moving 400 rows: 7,500
-    // positions 17.5 us with 19 a head, 19.1 with 38, 29.9 with 59); several sessions differ in length, and
-    // more CTAs even that out (16 sessions of up to 7,500 to 2048: 56 us with two a head, 47, 51 and 53 with
-    // three, four and six), up to two a head where there are many (64 sessions: 161 us, 177 with one, 163
-    // with three).
+    // CTAs a (session, kv head): in place while the 152 SMs hold them at once, two an SM (eight heads, one
+    // session of 7,500 to 4096: 46.9 us; 64 of up to 7,500 to 2048, a CTA a head: 152). Out of place one an SM
+    // for a single session, since each CTA chooses by itself, which takes as long as moving 400 rows (7,500 to
+    // 4096: 16.8 us with 19 a head, 20.3 with 12, 18.4 with 38); for several no more than are held at once, two
+    // an SM, but two a head at least. Eight heads, sessions of up to 7,500 to 2048, and in brackets all of 7,500:
+    // two 20.2 (20.3) with 19, 19.0 (19.0) with 9, 27.1 (27.6) with 25; four 24.1 (26.2) with 9, 25.3 (27.2) with 4,
+    // 22.3 (34.8) with 12; eight 31.9 (37.4) with 4, 38.1 (41.0) with 2, 32.6 (45.4) with 6; 16 54.3 (58.1) with 2,
+    // 59.8 (69.3) with 3; 64 156 (202) with 2, 168 (191) with one, 158 (200) with three.
     int W = 1;
     const long pairs = (long)a.S * a.Hkv;
     if (in_place) {
         while (W < kEvMaxW && pairs * 2 * W <= 2 * 152) W *= 2;
     } else {
-        const long runs = (a.Tmax + kEvRun - 1) / kEvRun, most = (a.S == 1 ? 152 : 400) / pairs;
+        const long runs = (a.Tmax + kEvRun - 1) / kEvRun, most = (a.S == 1 ? 152 : 304) / pairs;
         W = (int)(most < 2 ? 2 : most);
         W = (int)(W < runs ? W : runs);
     }
