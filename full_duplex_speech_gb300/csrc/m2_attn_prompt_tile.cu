@@ -475,7 +475,7 @@ __global__ void __launch_bounds__(kPtThreads, 1)
             const int nci = i ? run.nc1 : run.nc0;
             // (Not 0, since hidden scores are -infinity: a scale of 0 counts as the least number above it, which
             // leaves any finite product below 1e-6.)
-            const float cs = fmaxf(fabsf(a.scale) * kLog2e, FLT_TRUE_MIN);
+            const float cs = fmaxf(fabsf(a.scale) * kLog2e * kCutOff, FLT_TRUE_MIN);
             bool here = true;
             float m = kNone;
             float2 l0 = make_float2(0.f, 0.f), l1 = l0;  // the row's sum, in four parts
