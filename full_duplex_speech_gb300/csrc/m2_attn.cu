@@ -38,13 +38,12 @@
 // The run holding position len[s] takes the new key and value from the
 // inputs instead of the cache, and writes them into the cache there (no other
 // CTA reads that slot).
-#include <float.h>
-
 #include <mutex>
 
 #include "m2_common.cuh"
 #include "m2_launch.h"
 #include "m2_tc.cuh"
+#include "m2_tile_dev.cuh"
 
 namespace m2 {
 
@@ -95,15 +94,6 @@ int attn_chunk_len(int S, int Hkv, int Tmax, bool bf16) {
     int tc = bf16 ? AttnTile<bf16_t>::kTc : AttnTile<float>::kTc;
     while (tc > 32 && (long)S * Hkv * attn_chunks(Tmax, tc) < 2 * 152) tc /= 2;
     return tc;
-}
-
-constexpr float kLog2e = 1.4426950408889634f;
-constexpr float kNoMax = -FLT_MAX;  // a running maximum before any position: no finite score is below it
-
-__device__ __forceinline__ float ex2_approx(float x) {
-    float r;
-    asm("ex2.approx.ftz.f32 %0, %1;" : "=f"(r) : "f"(x));
-    return r;
 }
 
 // The 16 dims of q (or k) a lane holds: the 16-byte chunks i and i + 8 of a
@@ -525,11 +515,6 @@ __device__ __forceinline__ uint32_t movmatrix_t(uint32_t x) {
     asm volatile("movmatrix.sync.aligned.m8n8.trans.b16 %0, %1;" : "=r"(r) : "r"(x));
     return r;
 }
-__device__ __forceinline__ uint32_t pack_bf16x2(float lo, float hi) {
-    uint32_t r;
-    asm("cvt.rn.bf16x2.f32 %0, %1, %2;" : "=r"(r) : "f"(hi), "f"(lo));
-    return r;
-}
 
 // grid (W, Hkv, S), a cluster of W walkers per (session, kv head) when W > 1;
 // walker w takes chunks [w cpw, (w + 1) cpw) of those holding positions
@@ -589,7 +574,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2)
     // per head 2t and 2t + 1: running max (finite: a fully masked head stays
     // harmless), this lane's part of the sum, and acc^T (dims 16 dt + gq and
     // + 8)
-    float m0 = kNoMax, m1 = kNoMax, l0 = 0.f, l1 = 0.f;
+    float m0 = kNone, m1 = kNone, l0 = 0.f, l1 = 0.f;
     float acc[8][4];
 #pragma unroll
     for (int dt = 0; dt < 8; ++dt)
@@ -708,7 +693,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2)
         if (tid == 0)
             for (int i = 0; i < kWalkStages; ++i)
                 tc::mbar_wait(bar + i, 0, 100000000ull), tc::mbar_wait(bar + i, 1, 100000000ull);
-        m0 = m1 = kNoMax;
+        m0 = m1 = kNone;
         l0 = l1 = 0.f;
 #pragma unroll
         for (int dt = 0; dt < 8; ++dt)
@@ -744,10 +729,10 @@ __global__ void __launch_bounds__(kWalkThreads, 2)
     __syncthreads();
     if (W > 1) tc::cluster_wait();  // every walker of the cluster has started: its shared memory is there
     // this walker's (max, sum, acc) per query head, acc relative to its max
-    // (a walker without positions: max kNoMax, sum 0, acc 0), to the head's
+    // (a walker without positions: max kNone, sum 0, acc 0), to the head's
     // owner: slot (r / W) W + wk of walker r % W
     for (int r = 0; r < R; ++r) {
-        float M = kNoMax;
+        float M = kNone;
 #pragma unroll
         for (int w = 0; w < 4; ++w) M = fmaxf(M, sml[(w * 8 + r) * 2]);
         float o = 0.f, L = 0.f;
@@ -782,7 +767,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2)
         float2* stat = reinterpret_cast<float2*>(sm + kWalkStat);
         float2* whole = stat + kWalkMaxW * kAttnMaxR;
         if (tid < R) {
-            float M = kNoMax, L = 0.f;
+            float M = kNone, L = 0.f;
             for (int w = 0; w < W; ++w) M = fmaxf(M, stat[w * kAttnMaxR + tid].x);
             for (int w = 0; w < W; ++w) L = fmaf(ex2_approx(stat[w * kAttnMaxR + tid].x - M), stat[w * kAttnMaxR + tid].y, L);
             whole[tid] = make_float2(M, 1.f / L);
@@ -823,7 +808,7 @@ __global__ void __launch_bounds__(kWalkThreads, 2)
     // out = sum_w 2^(m_w - M) acc_w / sum_w 2^(m_w - M) l_w
     for (int r = wk; r < R; r += W) {
         const float* sl = recv + (r / W) * W * kWalkSlotF;
-        float M = kNoMax;
+        float M = kNone;
         for (int w = 0; w < W; ++w) M = fmaxf(M, sl[w * kWalkSlotF + kAttnD]);
         float o = 0.f, L = 0.f;
         for (int w = 0; w < W; ++w) {
