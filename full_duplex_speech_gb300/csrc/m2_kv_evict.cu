@@ -274,17 +274,21 @@ cudaError_t launch_kv_evict(const EvictArgs& a, cudaStream_t st) {
     // CTAs a (session, kv head): in place while the 152 SMs hold them at once, two an SM (eight heads, one
     // session of 7,500 to 4096: 46.9 us; 64 of up to 7,500 to 2048, a CTA a head: 152). Out of place one an SM
     // for a single session, since each CTA chooses by itself, which takes as long as moving 400 rows (7,500 to
-    // 4096: 16.8 us with 19 a head, 20.3 with 12, 18.4 with 38); for several no more than are held at once, two
-    // an SM, but two a head at least. Eight heads, sessions of up to 7,500 to 2048, and in brackets all of 7,500:
-    // two 20.2 (20.3) with 19, 19.0 (19.0) with 9, 27.1 (27.6) with 25; four 24.1 (26.2) with 9, 25.3 (27.2) with 4,
-    // 22.3 (34.8) with 12; eight 31.9 (37.4) with 4, 38.1 (41.0) with 2, 32.6 (45.4) with 6; 16 54.3 (58.1) with 2,
-    // 59.8 (69.3) with 3; 64 156 (202) with 2, 168 (191) with one, 158 (200) with three.
+    // 4096: 16.8 us with 19 a head, 20.3 with 12, 18.4 with 38). For several no more than are held at once, two
+    // an SM, as long as that is four a head or more; more sessions differ more in what they have to move, which
+    // more CTAs even out, up to two a head where there are many. Eight heads, to 2048, the mean of eight draws of
+    // lengths up to 7,500, and in brackets all of 7,500: two sessions 18.6 (20.4) with 19, 23.4 (27.6) with 25;
+    // four 24.7 (26.3) with 9, 28.1 (34.9) with 12; eight 34.4 (37.4) with 4, 36.3 (45.4) with 6; ten 38.8 (49.6)
+    // with 5, 39.7 (42.6) with 3; 16 51.8 (69.2) with 3, 52.7 (58.2) with 2, to 4096 74.3 and 80.1; 64 156 (202)
+    // with 2, 168 (191) with one, 158 (200) with 3.
     int W = 1;
     const long pairs = (long)a.S * a.Hkv;
     if (in_place) {
         while (W < kEvMaxW && pairs * 2 * W <= 2 * 152) W *= 2;
     } else {
-        const long runs = (a.Tmax + kEvRun - 1) / kEvRun, most = (a.S == 1 ? 152 : 304) / pairs;
+        const long runs = (a.Tmax + kEvRun - 1) / kEvRun;
+        long most = (a.S == 1 ? 152 : 304) / pairs;
+        if (a.S > 1 && most < 4) most = 400 / pairs;
         W = (int)(most < 2 ? 2 : most);
         W = (int)(W < runs ? W : runs);
     }
