@@ -38,9 +38,9 @@
 // caches: what runs every chunk is kept short, and the softmax comes first (with the
 // others first, the mending unrolled by eight and no way past it for most pieces 490 us of
 // the size below and 74 of nine prompts of up to 750, which now take 70.5).
-//   Measured: 4 sessions of 4096 rows, 40 query and 8 kv heads, causal, 687 GFLOP: 467
-// us with the append (24 alone), 1.47 PFLOP/s, 78 % of a bf16 library product's measured
-// rate (508 us in a loop of eager calls of half a second). A chunk of a pair took 2,600
+//   Measured: 4 sessions of 4096 rows, 40 query and 8 kv heads, causal, 687 GFLOP: 464
+// us with the append (24 alone) replayed from a graph, 1.48 PFLOP/s, 78 % of a bf16 library
+// product's measured rate; 505 in a loop of eager calls of half a second, 1.36. A chunk of a pair took 2,600
 // cycles when the whole took 490 us: 2 x 1,150 of products (2,050 at their rate; what is
 // left waits for shared memory, which they and the copies read and write for 2,000
 // cycles), each tile's softmax 1,000 and its hand-overs some 450.

@@ -30,8 +30,9 @@
 // 12 waits for what the next products need while these are issued (an issue lasts as
 // long as the products, and a look at a barrier in shared memory some 200 cycles
 // more: 331 us without it, 287 with).
-//   Measured: 4 sessions of 4096 rows, 40 query and 8 kv heads, all rows, 344 GFLOP: 263
-// us, 1.31 PFLOP/s (69 % of a bf16 library product's measured rate). A step of 256
+//   Measured: 4 sessions of 4096 rows, 40 query and 8 kv heads, all rows, 344 GFLOP: 262
+// us replayed from a graph, 1.31 PFLOP/s (69 % of a bf16 library product's measured rate);
+// 287 in a loop of eager calls of half a second, 1.20. A step of 256
 // pairs took 2,650 cycles when the whole took 284 us: 2,300 of products (2,050 without e), and the
 // exponentials' unit is busy for 2,050 of them; a CTA's start and its first steps,
 // which some positions do not see, are another fifth.
