@@ -220,7 +220,7 @@ static int run_of(const std::vector<Pair>& pairs, Slow slow, bool refused_pieces
     bool all;
     {
         std::unique_lock<std::mutex> lock(run->mutex);
-        all = run->changed.wait_until(lock, Clock::now() + std::chrono::seconds(3), [&] { return run->early || run->ended == 6; });
+        all = run->changed.wait_until(lock, Clock::now() + std::chrono::seconds(10), [&] { return run->early || run->ended == 6; });
         run->over = true;
         run->changed.notify_all();
     }
