@@ -20,7 +20,9 @@ namespace {
 // before + t of its session's caches. The session is the one that ends at the first
 // entry of row_start past the row: those ahead of that are at or before the row, and
 // sessions behind it begin before it. It is left out where an entry ahead of its first
-// is larger. (Every entry up to it is looked at, 128 at a time.)
+// is larger. (Every entry up to it is looked at: a search would take fewer looks, and
+// see nothing of that. 64 sessions: 25 us with the tiles either way; 65,535 of one row:
+// 2.7 ms, 1.8 with a search.)
 constexpr int kApThreads = 256;
 __device__ __forceinline__ void append_row(const PromptArgs& a, int row_bytes, int row, int lane) {
     const int pieces = a.Hkv * row_bytes / 16, per = row_bytes / 16;  // of keys, of a head
@@ -36,30 +38,42 @@ __device__ __forceinline__ void append_row(const PromptArgs& a, int row_bytes, i
             if (i0 + 32 * f + lane < pieces) k[f] = __ldg(ks + i0 + 32 * f + lane), v[f] = __ldg(vs + i0 + 32 * f + lane);
     };
     load(0);
-    constexpr int kEach = 4;
-    int lo = -1, top = INT_MIN;  // the session; this lane's largest of the entries ahead of its first
+    int lo = -1, top = INT_MIN;  // the session; this lane's largest of the entries ahead of its last
     int row0 = 0, end = 0, before = 0;
-    for (int s0 = 0; lo < 0 && s0 < a.S; s0 += 32 * kEach) {
-        int b[kEach], e[kEach], len[kEach];
+    {  // the first 32 with all there is of them, so that nothing follows where there are no more
+        const int b = lane < a.S ? a.start[lane] : INT_MIN, e = lane < a.S ? a.start[lane + 1] : INT_MIN;
+        const int len = lane < a.S && a.lens ? a.lens[lane] : 0;
+        const unsigned past = __ballot_sync(0xffffffffu, e > row);
+        const int at = past ? __ffs(past) - 1 : 32;
+        if (lane <= at) top = b;
+        if (lane < at) top = max(top, e);
+        if (past) {
+            lo = at, row0 = __shfl_sync(0xffffffffu, b, at), end = __shfl_sync(0xffffffffu, e, at);
+            before = __shfl_sync(0xffffffffu, len, at);
+        }
+    }
+    constexpr int kEach = 8;  // then their last entries alone
+    for (int s0 = 32; lo < 0 && s0 < a.S; s0 += 32 * kEach) {
+        int e[kEach], largest = INT_MIN;
 #pragma unroll
         for (int f = 0; f < kEach; ++f) {
             const int s = s0 + 32 * f + lane;
-            const bool there = s < a.S;
-            b[f] = there ? a.start[s] : INT_MIN, e[f] = there ? a.start[s + 1] : INT_MIN;
-            len[f] = there && a.lens ? a.lens[s] : 0;
+            e[f] = s < a.S ? a.start[s + 1] : INT_MIN;
+            largest = max(largest, e[f]);
+        }
+        if (!__any_sync(0xffffffffu, largest > row)) {
+            top = max(top, largest);
+            continue;
         }
 #pragma unroll
         for (int f = 0; f < kEach; ++f) {
             if (lo >= 0) continue;  // (the same in the whole warp)
             const unsigned past = __ballot_sync(0xffffffffu, e[f] > row);
             const int at = past ? __ffs(past) - 1 : 32;
-            if (lane < at) top = max(top, b[f]);
-            if (past) {
-                lo = s0 + 32 * f + at;
-                row0 = __shfl_sync(0xffffffffu, b[f], at), end = __shfl_sync(0xffffffffu, e[f], at);
-                before = __shfl_sync(0xffffffffu, len[f], at);
-            }
+            if (lane < at) top = max(top, e[f]);
+            if (past) lo = s0 + 32 * f + at;
         }
+        row0 = a.start[lo], end = a.start[lo + 1], before = a.lens ? a.lens[lo] : 0;
     }
     // (rows ahead of the first session's or behind the last's are nobody's)
     if (lo < 0 || row < row0 || row0 < 0 || end > a.rows || row0 < __reduce_max_sync(0xffffffffu, top)) return;

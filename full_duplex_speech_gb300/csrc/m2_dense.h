@@ -81,7 +81,14 @@ __device__ __forceinline__ int load_ahead(const PromptArgs& a, int s) {
     return (int)threadIdx.x < s ? a.start[threadIdx.x] : INT_MIN;
 }
 __device__ __forceinline__ bool block_begins_behind(const PromptArgs& a, int s, int ahead) {
-    for (int i = threadIdx.x + blockDim.x; i < s; i += blockDim.x) ahead = max(ahead, a.start[i]);
+    constexpr int kFlight = 8;  // of a thread's on their way together
+    for (int i0 = threadIdx.x + blockDim.x; i0 < s; i0 += kFlight * blockDim.x) {
+        int e[kFlight];
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) e[f] = i0 + f * (int)blockDim.x < s ? a.start[i0 + f * blockDim.x] : INT_MIN;
+#pragma unroll
+        for (int f = 0; f < kFlight; ++f) ahead = max(ahead, e[f]);
+    }
     return __syncthreads_and(ahead <= a.start[s]);
 }
 #endif
